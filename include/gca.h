@@ -28,6 +28,8 @@
  *  - dtype GCA_BF16: d in {32, 64, 128}, S in {64, 128} (tensor-core path)
  *  - dtype GCA_F32 : d in {16, 32, 64}, S in {16, 32, 64} (fp32 FFMA path)
  *  - 1 <= topk <= 32, landmark dimension <= 8192, chunks per row <= 16384.
+ *  - sliding-window entries: see gca_swa_params_t, gca_swa_sink_params_t and
+ *    gca_paged_params_t.
  */
 #ifndef GCA_H_
 #define GCA_H_
@@ -267,6 +269,131 @@ size_t gca_swa_bwd_workspace_size(const gca_swa_params_t* params);
 gca_status_t gca_swa_bwd(const gca_swa_params_t* params, const void* q, const void* k,
                          const void* v, const void* o, const float* lse, const void* dout, void* dq,
                          void* dk, void* dv, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Windowed self-attention with sinks: the sliding-window self-attention above,
+ * whose first `sinks` tokens stay visible to every later token.  Token t of a
+ * row attends to the keys
+ *   V(t) = { s <= t : s > t - window  or  s < sinks },
+ *   o_t = sum_{s in V(t)} softmax_s(attn_scale q_t . k_s) v_s per head,
+ * with H / Hkv consecutive query heads sharing a key head (query head h reads
+ * key head h / (H / Hkv)).  sinks = 0 is the plain window; window >= L is full
+ * causal attention.
+ */
+typedef struct {
+    int B, L;             /* rows, tokens per row (any L >= 1)                              */
+    int H, Hkv, d;        /* query heads, key heads (H a multiple, H / Hkv <= 128), 64 or 128 */
+    int window;           /* W >= 1                                                         */
+    int sinks;            /* first tokens that stay visible, >= 0                           */
+    gca_dtype_t dtype;    /* GCA_BF16                                                       */
+    float attn_scale;     /* 0 => 1/sqrt(d)                                                 */
+    int q_stride;         /* elements between consecutive tokens of q; 0 => H*d             */
+    int kv_stride;        /* the same of k and v; 0 => Hkv*d.  Both multiples of 8; rows of
+                             one batch entry are L * stride elements apart, heads are dense
+                             (a slice of a packed q/k/v projection has this form)           */
+} gca_swa_sink_params_t;
+
+/* Bytes of device workspace gca_swa_sink_fwd needs (0 for invalid parameters). */
+size_t gca_swa_sink_fwd_workspace_size(const gca_swa_sink_params_t* params);
+
+/*
+ * gca_swa_sink_fwd -- forward.
+ *   q [B, L, H, d], k, v [B, L, Hkv, d] (token strides as in params);
+ *   o [B, L, H, d] dense, fully written.
+ *   lse [B, L, H] fp32 or NULL: ln sum_{s in V(t)} exp(attn_scale q_t . k_s);
+ *   needed later by gca_swa_sink_bwd.  fp32 accumulation, bf16 output.
+ *   workspace: >= gca_swa_sink_fwd_workspace_size() bytes, 256-byte aligned,
+ *   contents need not be initialised; calls that may overlap need their own.
+ *   K and V must be finite wherever some token of the row sees them.
+ */
+gca_status_t gca_swa_sink_fwd(const gca_swa_sink_params_t* params, const void* q, const void* k,
+                              const void* v, void* o, float* lse, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/* Bytes of device workspace gca_swa_sink_bwd needs (0 for invalid parameters). */
+size_t gca_swa_sink_bwd_workspace_size(const gca_swa_sink_params_t* params);
+
+/*
+ * gca_swa_sink_bwd -- gradients: with p_ts the forward's probabilities,
+ * delta_t = dout_t . o_t and ds_ts = attn_scale p_ts (dout_t . v_s - delta_t):
+ *   dq_t = sum_s ds_ts k_s,  dk_s = sum_t ds_ts q_t,  dv_s = sum_t p_ts dout_t,
+ *   dk and dv summed over the query heads of the key head as well.
+ *   q, k, v as in the forward; o, lse from it; dout [B, L, H, d] dense.
+ *   dq [B, L, H, d]; dk, dv [B, L, Hkv, d]: dense, fully overwritten; fp32
+ *   accumulation in a fixed order, no atomics (bitwise reproducible).
+ *   workspace: >= gca_swa_sink_bwd_workspace_size() bytes, 256-byte aligned.
+ */
+gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q, const void* k,
+                              const void* v, const void* o, const float* lse, const void* dout,
+                              void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * Paged K/V cache of the window self-attention, for generation: the keys and
+ * values of B running sequences live in pages of `page` tokens,
+ *   k_cache, v_cache [n_pages, page, Hkv, d],
+ * and token s of sequence b is row s % page of page table[b][s / page].
+ * A call serves a batch of sequences with any number of new tokens each
+ * (none, one, a prompt chunk): the new tokens of sequence b are the rows
+ * cu_q[b] .. cu_q[b+1]-1 of the token tensors, and their positions are the last
+ * ones of its kv_len[b] tokens (the new ones included).  Rows behind
+ * cu_q[B] are neither read nor written.
+ *   table [B, table_width], cu_q [B + 1], kv_len [B]: int32, device.  They are
+ *   read on the device only, so a captured call follows their contents.
+ * A sequence whose entries contradict each other (cu_q decreasing or beyond
+ * total_q, more than max_q new tokens, kv_len below 0 or beyond
+ * table_width * page) is left out and GCA_ERR_DEVICE_INDEX recorded.
+ */
+typedef struct {
+    int B;                /* sequences, >= 1                                                */
+    int total_q;          /* rows of the token tensors, >= 0 (0: nothing is enqueued)       */
+    int max_q;            /* at least the new tokens of any one sequence; 0 => total_q      */
+    int H, Hkv, d;        /* as in gca_swa_sink_params_t (H is not used by the append)      */
+    int page;             /* tokens per page: 16, 32, 64 or 128                             */
+    int n_pages;          /* pages in the cache                                             */
+    int table_width;      /* table entries per sequence                                     */
+    int window;           /* 0: every earlier token is visible; else as above               */
+    int sinks;            /* first tokens that stay visible behind a window                 */
+    gca_dtype_t dtype;    /* GCA_BF16                                                       */
+    float attn_scale;     /* 0 => 1/sqrt(d)                                                 */
+    int q_stride;         /* elements between consecutive tokens of q; 0 => H*d             */
+    int kv_stride;        /* the same of k_new and v_new; 0 => Hkv*d; multiples of 8        */
+} gca_paged_params_t;
+
+/*
+ * gca_paged_append -- write new tokens into the cache.
+ *   k_new, v_new [total_q, Hkv, d]; token i of sequence b goes to its position
+ *   kv_len[b] - (cu_q[b+1] - cu_q[b]) + i.  Tokens at negative positions and
+ *   tokens whose page is not in [0, n_pages) are not written (the latter records
+ *   GCA_ERR_DEVICE_INDEX); no other row of the cache changes.  With a window,
+ *   tokens that no later token can see (neither sinks nor among the last
+ *   window + new tokens) are still written.
+ */
+gca_status_t gca_paged_append(const gca_paged_params_t* params, const void* k_new,
+                              const void* v_new, const int32_t* cu_q, const int32_t* kv_len,
+                              const int32_t* table, void* k_cache, void* v_cache, void* stream);
+
+/* Bytes of device workspace gca_paged_attn needs (0 for invalid parameters). */
+size_t gca_paged_attn_workspace_size(const gca_paged_params_t* params);
+
+/*
+ * gca_paged_attn -- attention of the new tokens over the cache, which already
+ * holds their own keys and values (gca_paged_append first): gca_swa_sink_fwd's
+ * formula at the tokens' positions.
+ *   q [total_q, H, d] -> o [total_q, H, d] dense; lse [total_q, H] fp32 or NULL.
+ *   A token at a negative position (kv_len below the number of new tokens)
+ *   sees nothing: its output is 0 and its lse -inf.
+ *   Only pages that hold a visible token are looked up, so the table entries of
+ *   pages that left the window may be anything.  Such a page outside
+ *   [0, n_pages) reads as zeros and records GCA_ERR_DEVICE_INDEX.  Cache rows at or
+ *   behind kv_len may hold anything (NaN included).
+ *   workspace: >= gca_paged_attn_workspace_size() bytes, 256-byte aligned,
+ *   contents need not be initialised; calls that may overlap need their own.
+ */
+gca_status_t gca_paged_attn(const gca_paged_params_t* params, const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* cu_q, const int32_t* kv_len,
+                            const int32_t* table, void* o, float* lse, void* workspace,
+                            size_t ws_bytes, void* stream);
 
 /*
  * gca_get_status -- synchronise `stream`, then return and clear the device

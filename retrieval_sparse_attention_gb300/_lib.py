@@ -26,7 +26,9 @@ EXPORTED = ("gca_score_topk", "gca_fwd", "gca_bwd_workspace_size", "gca_bwd",
             "gca_prof_enable", "gca_prof_read", "gca_decode_retrieve_noalloc",
             "gca_score_topk_noisy", "gca_landmark_bwd_workspace_size", "gca_landmark_bwd",
             "gca_gather_chunks", "gca_swa_fwd", "gca_swa_bwd_workspace_size", "gca_swa_bwd",
-            "gca_debug_stall_next_decode")
+            "gca_swa_sink_fwd_workspace_size", "gca_swa_sink_fwd",
+            "gca_swa_sink_bwd_workspace_size", "gca_swa_sink_bwd", "gca_paged_append",
+            "gca_paged_attn_workspace_size", "gca_paged_attn", "gca_debug_stall_next_decode")
 
 
 class GcaParams(ctypes.Structure):
@@ -43,6 +45,24 @@ class GcaSwaParams(ctypes.Structure):
     """Mirror of gca_swa_params_t."""
     _fields_ = [("B", ctypes.c_int), ("L", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
                 ("window", ctypes.c_int), ("dtype", ctypes.c_int), ("attn_scale", ctypes.c_float)]
+
+
+class GcaSwaSinkParams(ctypes.Structure):
+    """Mirror of gca_swa_sink_params_t."""
+    _fields_ = [("B", ctypes.c_int), ("L", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("window", ctypes.c_int),
+                ("sinks", ctypes.c_int), ("dtype", ctypes.c_int), ("attn_scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int), ("kv_stride", ctypes.c_int)]
+
+
+class GcaPagedParams(ctypes.Structure):
+    """Mirror of gca_paged_params_t."""
+    _fields_ = [("B", ctypes.c_int), ("total_q", ctypes.c_int), ("max_q", ctypes.c_int),
+                ("H", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("table_width", ctypes.c_int),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("attn_scale", ctypes.c_float), ("q_stride", ctypes.c_int),
+                ("kv_stride", ctypes.c_int)]
 
 
 class GcaError(RuntimeError):
@@ -80,6 +100,13 @@ def load() -> ctypes.CDLL:
             "gca_swa_fwd": ([ctypes.POINTER(GcaSwaParams), vp, vp, vp, vp, vp, vp], i32),
             "gca_swa_bwd_workspace_size": ([ctypes.POINTER(GcaSwaParams)], sz),
             "gca_swa_bwd": ([ctypes.POINTER(GcaSwaParams)] + [vp] * 10 + [sz, vp], i32),
+            "gca_swa_sink_fwd_workspace_size": ([ctypes.POINTER(GcaSwaSinkParams)], sz),
+            "gca_swa_sink_fwd": ([ctypes.POINTER(GcaSwaSinkParams)] + [vp] * 6 + [sz, vp], i32),
+            "gca_swa_sink_bwd_workspace_size": ([ctypes.POINTER(GcaSwaSinkParams)], sz),
+            "gca_swa_sink_bwd": ([ctypes.POINTER(GcaSwaSinkParams)] + [vp] * 10 + [sz, vp], i32),
+            "gca_paged_append": ([ctypes.POINTER(GcaPagedParams)] + [vp] * 8, i32),
+            "gca_paged_attn_workspace_size": ([ctypes.POINTER(GcaPagedParams)], sz),
+            "gca_paged_attn": ([ctypes.POINTER(GcaPagedParams)] + [vp] * 9 + [sz, vp], i32),
             "gca_get_status": ([vp], i32),
             "gca_status_string": ([i32], ctypes.c_char_p),
             "gca_last_launch_count": ([], i32),

@@ -17,7 +17,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import GCA_BF16, GCA_F32, GcaError, GcaParams, GcaSwaParams
+from ._lib import (GCA_BF16, GCA_F32, GcaError, GcaPagedParams, GcaParams, GcaSwaParams,
+                   GcaSwaSinkParams)
 
 _DT = {torch.bfloat16: GCA_BF16, torch.float32: GCA_F32}
 
@@ -174,6 +175,206 @@ def swa_bwd(q, k, v, o, lse, dout, *, window, attn_scale=0.0, workspace=None):
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     gca_swa_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, workspace)
     return dq, dk, dv
+
+
+# --- windowed attention with sinks, and its paged K/V cache ----------------------------
+def _token_stride(t):
+    """Elements between consecutive tokens of a [..., tokens, heads, d] tensor whose heads
+    are dense and whose batch rows follow each other (a dense tensor, or a slice of a
+    packed projection)."""
+    if not t.is_cuda:
+        raise ValueError("GCA entry points take CUDA tensors")
+    h, d = t.shape[-2], t.shape[-1]
+    st = t.stride()
+    step = st[-3] if t.shape[-3] > 1 else (st[-4] if t.dim() == 4 and t.shape[0] > 1 else h * d)
+    if (d > 1 and st[-1] != 1) or (h > 1 and st[-2] != d) or step < h * d or \
+            (t.dim() == 4 and t.shape[0] > 1 and st[0] != t.shape[1] * step):
+        raise ValueError("token tensors need dense heads and equally spaced tokens")
+    return step
+
+
+def _vp(t):
+    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+
+
+def _on_current_device(*ts):
+    """The entries launch on the current device's stream: tensors of another device (or of
+    none) would be read through a foreign address."""
+    dev = torch.cuda.current_device() if ts[0].is_cuda else -1
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError("tensors must be CUDA tensors on the current device")
+
+
+def _dense(t, shape, dtype, what):
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s" % (what, tuple(shape)))
+
+
+def make_swa_sink_params(*, B, L, H, d, window, Hkv=None, sinks=0, dtype=torch.bfloat16,
+                         attn_scale=0.0, q_stride=0, kv_stride=0) -> GcaSwaSinkParams:
+    return GcaSwaSinkParams(B=B, L=L, H=H, Hkv=H if Hkv is None else Hkv, d=d, window=window,
+                            sinks=sinks, dtype=dtype_code(dtype), attn_scale=attn_scale,
+                            q_stride=q_stride, kv_stride=kv_stride)
+
+
+def gca_swa_sink_fwd_workspace_size(params: GcaSwaSinkParams) -> int:
+    return int(_lib.load().gca_swa_sink_fwd_workspace_size(ctypes.byref(params)))
+
+
+def gca_swa_sink_fwd(params: GcaSwaSinkParams, q, k, v, o, lse, workspace, stream=None):
+    _check("gca_swa_sink_fwd", _lib.load().gca_swa_sink_fwd(
+        ctypes.byref(params), _vp(q), _vp(k), _vp(v), _vp(o), _vp(lse), _vp(workspace),
+        workspace.numel() if workspace is not None else 0, _stream(stream)))
+
+
+def gca_swa_sink_bwd_workspace_size(params: GcaSwaSinkParams) -> int:
+    return int(_lib.load().gca_swa_sink_bwd_workspace_size(ctypes.byref(params)))
+
+
+def gca_swa_sink_bwd(params: GcaSwaSinkParams, q, k, v, o, lse, dout, dq, dk, dv, workspace,
+                     stream=None):
+    _check("gca_swa_sink_bwd", _lib.load().gca_swa_sink_bwd(
+        ctypes.byref(params), _vp(q), _vp(k), _vp(v), _vp(o), _vp(lse), _vp(dout), _vp(dq),
+        _vp(dk), _vp(dv), _vp(workspace), workspace.numel(), _stream(stream)))
+
+
+def _swa_sink_args(q, k, v, window, sinks, attn_scale):
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.shape[:2] != q.shape[:2] or \
+            k.shape[3] != q.shape[3]:
+        raise ValueError("q must be [B, L, H, d] and k, v [B, L, Hkv, d]")
+    if q.dtype != k.dtype or q.dtype != v.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    _on_current_device(q, k, v)
+    kvs = _token_stride(k)
+    if kvs != _token_stride(v):
+        raise ValueError("k and v must have one token stride")
+    B, L, H, d = q.shape
+    return make_swa_sink_params(B=B, L=L, H=H, Hkv=k.shape[2], d=d, window=window, sinks=sinks,
+                                dtype=q.dtype, attn_scale=attn_scale, q_stride=_token_stride(q),
+                                kv_stride=kvs)
+
+
+def _workspace(given, need, dev):
+    if given is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _on_current_device(given)
+    if given.dtype != torch.uint8 or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return given
+
+
+def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, workspace=None):
+    """Windowed self-attention with sinks: q [B, L, H, d], k, v [B, L, Hkv, d] (token strides
+    may be those of a packed projection) -> (o [B, L, H, d], lse [B, L, H])."""
+    p = _swa_sink_args(q, k, v, window, sinks, attn_scale)
+    dev = q.device
+    ws = _workspace(workspace, gca_swa_sink_fwd_workspace_size(p), dev)
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if with_lse else None
+    gca_swa_sink_fwd(p, q, k, v, o, lse, ws)
+    return o, lse
+
+
+def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, workspace=None):
+    """Gradients of swa_sink_fwd: returns dense (dq, dk, dv)."""
+    p = _swa_sink_args(q, k, v, window, sinks, attn_scale)
+    _on_current_device(q, o, lse, dout)
+    _dense(o, q.shape, q.dtype, "o")
+    _dense(dout, q.shape, q.dtype, "dout")
+    _dense(lse, q.shape[:3], torch.float32, "lse")
+    dev = q.device
+    ws = _workspace(workspace, gca_swa_sink_bwd_workspace_size(p), dev)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    gca_swa_sink_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, ws)
+    return dq, dk, dv
+
+
+def make_paged_params(*, B, total_q, Hkv, d, page, n_pages, table_width, H=None, max_q=0, window=0,
+                      sinks=0, dtype=torch.bfloat16, attn_scale=0.0, q_stride=0,
+                      kv_stride=0) -> GcaPagedParams:
+    return GcaPagedParams(B=B, total_q=total_q, max_q=max_q, H=Hkv if H is None else H, Hkv=Hkv,
+                          d=d, page=page, n_pages=n_pages, table_width=table_width, window=window,
+                          sinks=sinks, dtype=dtype_code(dtype), attn_scale=attn_scale,
+                          q_stride=q_stride, kv_stride=kv_stride)
+
+
+def gca_paged_append(params: GcaPagedParams, k_new, v_new, cu_q, kv_len, table, k_cache, v_cache,
+                     stream=None):
+    _check("gca_paged_append", _lib.load().gca_paged_append(
+        ctypes.byref(params), _vp(k_new), _vp(v_new), _vp(cu_q), _vp(kv_len), _vp(table),
+        _vp(k_cache), _vp(v_cache), _stream(stream)))
+
+
+def gca_paged_attn_workspace_size(params: GcaPagedParams) -> int:
+    return int(_lib.load().gca_paged_attn_workspace_size(ctypes.byref(params)))
+
+
+def gca_paged_attn(params: GcaPagedParams, q, k_cache, v_cache, cu_q, kv_len, table, o, lse,
+                   workspace, stream=None):
+    _check("gca_paged_attn", _lib.load().gca_paged_attn(
+        ctypes.byref(params), _vp(q), _vp(k_cache), _vp(v_cache), _vp(cu_q), _vp(kv_len),
+        _vp(table), _vp(o), _vp(lse), _vp(workspace), workspace.numel(), _stream(stream)))
+
+
+def _paged_cache(tok, k_cache, v_cache, table, cu_q, kv_len):
+    """Checks what the paged entries address by: returns (n_pages, page, Hkv, d, B, width)."""
+    if k_cache.dim() != 4 or table.dim() != 2:
+        raise ValueError("caches must be [n_pages, page, Hkv, d] and table [B, table_width]")
+    _on_current_device(k_cache, v_cache, table, cu_q, kv_len, tok)
+    _dense(k_cache, k_cache.shape, tok.dtype, "k_cache")
+    _dense(v_cache, k_cache.shape, tok.dtype, "v_cache")
+    B, width = table.shape
+    _dense(table, (B, width), torch.int32, "table")
+    _dense(cu_q, (B + 1,), torch.int32, "cu_q")
+    _dense(kv_len, (B,), torch.int32, "kv_len")
+    return (*k_cache.shape, B, width)
+
+
+def paged_append(k_new, v_new, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0):
+    """Write new tokens into the paged cache, in place: k_new, v_new [T, Hkv, d]; caches
+    [n_pages, page, Hkv, d]; table [B, table_width], cu_q [B + 1], kv_len [B] int32 on the
+    device.  ``kv_len`` counts the new tokens."""
+    n_pages, page, Hkv, d, B, width = _paged_cache(k_new, k_cache, v_cache, table, cu_q, kv_len)
+    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != (Hkv, d) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [T, %d, %d]" % (Hkv, d))
+    if v_new.dtype != k_new.dtype:
+        raise TypeError("k_new and v_new must have one dtype")
+    _on_current_device(k_new, v_new)
+    kvs = _token_stride(k_new)
+    if kvs != _token_stride(v_new):
+        raise ValueError("k_new and v_new must have one token stride")
+    p = make_paged_params(B=B, total_q=k_new.shape[0], max_q=max_q, Hkv=Hkv, d=d, page=page,
+                          n_pages=n_pages, table_width=width, dtype=k_new.dtype, kv_stride=kvs)
+    gca_paged_append(p, k_new, v_new, cu_q, kv_len, table, k_cache, v_cache)
+
+
+def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, sinks=0,
+               attn_scale=0.0, with_lse=False, out=None, workspace=None):
+    """Attention of the new tokens q [T, H, d] over the paged cache -> (o [T, H, d], lse [T, H]
+    or None).  ``max_q`` bounds the new tokens of one sequence (0: T); a host that knows it
+    saves work.  Rows of o behind cu_q[B] are left as they were (``out`` supplies o)."""
+    n_pages, page, Hkv, d, B, width = _paged_cache(q, k_cache, v_cache, table, cu_q, kv_len)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [T, H, %d]" % d)
+    T, H = q.shape[0], q.shape[1]
+    p = make_paged_params(B=B, total_q=T, max_q=max_q, H=H, Hkv=Hkv, d=d, page=page,
+                          n_pages=n_pages, table_width=width, window=window, sinks=sinks,
+                          dtype=q.dtype, attn_scale=attn_scale, q_stride=_token_stride(q))
+    dev = q.device
+    ws = _workspace(workspace, gca_paged_attn_workspace_size(p), dev)
+    if out is None:
+        out = torch.empty(T, H, d, dtype=q.dtype, device=dev)
+    else:
+        _on_current_device(out)
+        _dense(out, q.shape, q.dtype, "out")
+    lse = torch.empty(T, H, dtype=torch.float32, device=dev) if with_lse else None
+    gca_paged_attn(p, q, k_cache, v_cache, cu_q, kv_len, table, out, lse, ws)
+    return out, lse
 
 
 def gather_chunks(cache_k, cache_v, idx):

@@ -290,6 +290,167 @@ gca_status_t gca_swa_bwd(const gca_swa_params_t* params, const void* q, const vo
     return r;
 }
 
+namespace {
+gca_status_t check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return GCA_OK;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || have < need) return GCA_ERR_WORKSPACE;
+    return GCA_OK;
+}
+
+// What the windowed attention with sinks and the paged entries share.
+gca_status_t sink_common(int H, int Hkv, int d, gca_dtype_t dtype, float attn_scale, int q_stride,
+                         int kv_stride, SinkShape* s) {
+    if (H < 1 || Hkv < 1 || d < 1 || H % Hkv != 0) return GCA_ERR_INVALID_ARG;
+    if (dtype != GCA_BF16 && dtype != GCA_F32) return GCA_ERR_INVALID_ARG;
+    if (!(attn_scale >= 0.f) || isinf(attn_scale) || q_stride < 0 || kv_stride < 0) return GCA_ERR_INVALID_ARG;
+    if (dtype != GCA_BF16 || (d != 64 && d != 128) || H / Hkv > 128 || H > 4096) return GCA_ERR_UNSUPPORTED;
+    s->H = H; s->Hkv = Hkv; s->d = d;
+    s->q_stride = q_stride ? q_stride : H * d;
+    s->kv_stride = kv_stride ? kv_stride : Hkv * d;
+    if (s->q_stride < H * d || s->kv_stride < Hkv * d || s->q_stride % 8 != 0 || s->kv_stride % 8 != 0)
+        return GCA_ERR_INVALID_ARG;
+    if (s->q_stride > (1 << 24) || s->kv_stride > (1 << 24)) return GCA_ERR_UNSUPPORTED;
+    s->scale = attn_scale > 0.f ? attn_scale : 1.0f / sqrtf((float)d);
+    return GCA_OK;
+}
+
+gca_status_t swa_sink_check(const gca_swa_sink_params_t* p, SinkShape* out) {
+    if (!p) return GCA_ERR_INVALID_ARG;
+    SinkShape s{};
+    if (p->B < 1 || p->L < 1 || p->window < 1 || p->sinks < 0) return GCA_ERR_INVALID_ARG;
+    gca_status_t r = sink_common(p->H, p->Hkv, p->d, p->dtype, p->attn_scale, p->q_stride, p->kv_stride, &s);
+    if (r != GCA_OK) return r;
+    if ((long long)p->B * p->L * p->H >= (1ll << 31)) return GCA_ERR_UNSUPPORTED;
+    s.B = p->B; s.L = p->L;
+    s.T = p->B * p->L; s.max_q = p->L;
+    // a window that covers the row hides nothing, and then sinks add nothing
+    s.W = p->window < p->L ? p->window : p->L;
+    s.ns = s.W < p->L ? (p->sinks < p->L ? p->sinks : p->L) : 0;
+    *out = s;
+    return GCA_OK;
+}
+
+gca_status_t paged_check(const gca_paged_params_t* p, SinkShape* out) {
+    if (!p) return GCA_ERR_INVALID_ARG;
+    SinkShape s{};
+    if (p->B < 1 || p->total_q < 0 || p->max_q < 0 || p->n_pages < 1 || p->table_width < 1 || p->page < 1 ||
+        p->window < 0 || p->sinks < 0)
+        return GCA_ERR_INVALID_ARG;
+    gca_status_t r = sink_common(p->H, p->Hkv, p->d, p->dtype, p->attn_scale, p->q_stride, p->kv_stride, &s);
+    if (r != GCA_OK) return r;
+    if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return GCA_ERR_UNSUPPORTED;
+    if ((long long)p->total_q * p->H >= (1ll << 31) || (long long)p->table_width * p->page > kNoWindow / 2 ||
+        (long long)p->B * p->table_width >= (1ll << 31) || p->B > 65535)
+        return GCA_ERR_UNSUPPORTED;
+    s.B = p->B; s.T = p->total_q;
+    s.max_q = p->max_q > 0 && p->max_q < p->total_q ? p->max_q : p->total_q;
+    s.page = p->page; s.n_pages = p->n_pages; s.width = p->table_width;
+    const int cap = p->table_width * p->page;
+    s.W = p->window > 0 && p->window < cap ? p->window : kNoWindow;
+    s.ns = s.W == kNoWindow ? 0 : (p->sinks < cap ? p->sinks : cap);
+    s.paged = 1;
+    *out = s;
+    return GCA_OK;
+}
+}  // namespace
+
+size_t gca_swa_sink_fwd_workspace_size(const gca_swa_sink_params_t* params) {
+    SinkShape s;
+    if (swa_sink_check(params, &s) != GCA_OK) return 0;
+    return sink_fwd_workspace_bytes(s);
+}
+
+gca_status_t gca_swa_sink_fwd(const gca_swa_sink_params_t* params, const void* q, const void* k,
+                              const void* v, void* o, float* lse, void* workspace, size_t ws_bytes,
+                              void* stream) {
+    SinkShape s;
+    gca_status_t r = swa_sink_check(params, &s);
+    if (r != GCA_OK) return r;
+    if ((r = check_ptrs({q, k, v, o})) != GCA_OK) return r;
+    if (lse && !aligned16(lse)) return GCA_ERR_INVALID_ARG;
+    if ((r = check_workspace(workspace, ws_bytes, sink_fwd_workspace_bytes(s))) != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    int n = 0;
+    r = from_cuda(launch_sink_fwd(s, q, k, v, nullptr, nullptr, nullptr, o, lse, workspace, st,
+                                  static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+size_t gca_swa_sink_bwd_workspace_size(const gca_swa_sink_params_t* params) {
+    SinkShape s;
+    if (swa_sink_check(params, &s) != GCA_OK) return 0;
+    return sink_bwd_workspace_bytes(s);
+}
+
+gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q, const void* k,
+                              const void* v, const void* o, const float* lse, const void* dout,
+                              void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes,
+                              void* stream) {
+    SinkShape s;
+    gca_status_t r = swa_sink_check(params, &s);
+    if (r != GCA_OK) return r;
+    if ((r = check_ptrs({q, k, v, o, lse, dout, dq, dk, dv})) != GCA_OK) return r;
+    if ((r = check_workspace(workspace, ws_bytes, sink_bwd_workspace_bytes(s))) != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    int n = 0;
+    r = from_cuda(launch_sink_bwd(s, q, k, v, o, lse, dout, dq, dk, dv, workspace, st,
+                                  static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+gca_status_t gca_paged_append(const gca_paged_params_t* params, const void* k_new,
+                              const void* v_new, const int32_t* cu_q, const int32_t* kv_len,
+                              const int32_t* table, void* k_cache, void* v_cache, void* stream) {
+    SinkShape s;
+    gca_status_t r = paged_check(params, &s);
+    if (r != GCA_OK) return r;
+    if (s.T == 0) {
+        t_launches = 0;
+        return GCA_OK;
+    }
+    if ((r = check_ptrs({k_new, v_new, cu_q, kv_len, table, k_cache, v_cache})) != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    int n = 0;
+    r = from_cuda(launch_paged_append(s, k_new, v_new, cu_q, kv_len, table, k_cache, v_cache, st,
+                                      static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+size_t gca_paged_attn_workspace_size(const gca_paged_params_t* params) {
+    SinkShape s;
+    if (paged_check(params, &s) != GCA_OK || s.T == 0) return 0;
+    return sink_fwd_workspace_bytes(s);
+}
+
+gca_status_t gca_paged_attn(const gca_paged_params_t* params, const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* cu_q, const int32_t* kv_len,
+                            const int32_t* table, void* o, float* lse, void* workspace,
+                            size_t ws_bytes, void* stream) {
+    SinkShape s;
+    gca_status_t r = paged_check(params, &s);
+    if (r != GCA_OK) return r;
+    if (s.T == 0) {
+        t_launches = 0;
+        return GCA_OK;
+    }
+    if ((r = check_ptrs({q, k_cache, v_cache, cu_q, kv_len, table, o})) != GCA_OK) return r;
+    if (lse && !aligned16(lse)) return GCA_ERR_INVALID_ARG;
+    if ((r = check_workspace(workspace, ws_bytes, sink_fwd_workspace_bytes(s))) != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    int n = 0;
+    r = from_cuda(launch_sink_fwd(s, q, k_cache, v_cache, cu_q, kv_len, table, o, lse, workspace, st,
+                                  static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
 size_t gca_bwd_workspace_size(const gca_params_t* params) {
     Shape s;
     if (make_shape(params, true, &s) != GCA_OK) return 0;

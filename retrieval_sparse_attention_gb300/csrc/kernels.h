@@ -128,6 +128,31 @@ cudaError_t launch_gather_chunks(const void* src_k, const void* src_v, int n_src
                                  const int32_t* idx, int topk, void* dst_k, void* dst_v,
                                  int32_t* dst_idx, int* status, cudaStream_t st, int* launches);
 
+// Windowed attention with sinks over dense sequences (paged = 0) or a paged cache.
+struct SinkShape {
+    int B, H, Hkv, d, W, ns;      // W >= 1 (a call without a window passes kNoWindow)
+    int L;                        // dense: tokens per row
+    int T, max_q;                 // paged: rows of the token tensors, bound on a sequence's new tokens
+    int page, n_pages, width;     // paged: the cache and its table
+    int q_stride, kv_stride;      // elements between consecutive tokens
+    float scale;
+    int paged;
+};
+constexpr int kNoWindow = 0x40000000;
+
+size_t sink_fwd_workspace_bytes(const SinkShape& s);
+cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, const void* v,
+                            const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, void* o,
+                            float* lse, void* ws, int* status, cudaStream_t st, int* launches);
+size_t sink_bwd_workspace_bytes(const SinkShape& s);
+cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, const void* v,
+                            const void* o, const float* lse, const void* dout, void* dq, void* dk,
+                            void* dv, void* ws, int* status, cudaStream_t st, int* launches);
+cudaError_t launch_paged_append(const SinkShape& s, const void* k_new, const void* v_new,
+                                const int32_t* cu_q, const int32_t* kv_len, const int32_t* table,
+                                void* k_cache, void* v_cache, int* status, cudaStream_t st,
+                                int* launches);
+
 cudaError_t launch_synth_fill(void* dst, size_t n, gca_dtype_t dt, uint64_t seed, uint64_t tid,
                               uint64_t first, cudaStream_t st);
 
