@@ -1,9 +1,7 @@
-// attn_sink.cu -- windowed self-attention with sinks, dense and over a paged K/V
-// cache, forward and backward, in fp32 arithmetic on the CUDA cores.
+// attn_sink.cu -- gradients of the windowed self-attention with sinks in fp32
+// arithmetic on the CUDA cores.
 //
-// Forward: one warp per (token, query head); a lane takes every 32nd visible key,
-// the 32 scores join a running maximum and sum, and each lane accumulates d / 32
-// columns of sum_s p_s v_s.  Backward: one warp per (token, query head) for dQ
+// One warp per (token, query head) for dQ
 // and one per (token, key head) for dK and dV, over the tokens that see the key.
 #include <math.h>
 
@@ -53,65 +51,6 @@ struct Keys {
     }
     __device__ int at(int i) const { return i < n_sink ? i : lo + i - n_sink; }
 };
-
-template <int D>
-__global__ void __launch_bounds__(128) sink_fwd_kernel(Args a) {
-    __shared__ float sq[4][D];
-    const int wp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 4 + wp;
-    const int h = static_cast<int>(w % a.H);
-    const long long bt = w / a.H;
-    const int per = a.paged ? a.p.max_q : a.L;
-    const int b = static_cast<int>(bt / per), i = static_cast<int>(bt % per);
-    if (b >= a.B) return;
-    SeqInfo s{b * a.L, a.L, 0};
-    if (a.paged) s = paged_seq(a.p, b, a.status);
-    if (i >= s.n) return;
-    const size_t tok = s.row0 + i;
-    const bf16* qr = a.q + tok * a.q_stride + h * D;
-    for (int c = lane; c < D; c += 32) sq[wp][c] = __bfloat162float(qr[c]);
-    __syncwarp();
-    const Keys ks(s.pos0 + i, a.W, a.ns);
-    const int hk = h / (a.H / a.Hkv);
-    auto row = [&](int key) -> long long {
-        if (!a.paged) return ((long long)b * a.L + key) * a.kv_stride + hk * D;
-        const int pg = a.p.table[(size_t)b * a.p.width + (key >> a.p.page_log2)];
-        if (pg < 0 || pg >= a.p.n_pages) {
-            set_status(a.status, GCA_ERR_DEVICE_INDEX);
-            return -1;
-        }
-        return (((long long)pg << a.p.page_log2) + (key & ((1 << a.p.page_log2) - 1))) * a.Hkv * D + hk * D;
-    };
-    float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-    for (int j0 = 0; j0 < ks.n; j0 += 32) {
-        const int j = j0 + lane;
-        long long r = -1;
-        float x = -INFINITY;
-        if (j < ks.n) {
-            r = row(ks.at(j));
-            x = r < 0 ? 0.f : dot<D>(sq[wp], a.k + r) * a.scale;
-        }
-        float mt = x;
-        for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, o));
-        const float mn = fmaxf(m, mt), al = __expf(m - mn);
-        const float p = __expf(x - mn);
-        l = l * al + warp_sum(p);
-        m = mn;
-        for (int c = 0; c < D / 32; ++c) acc[c] *= al;
-        const int cnt = min(32, ks.n - j0);
-        for (int u = 0; u < cnt; ++u) {
-            const float pu = __shfl_sync(~0u, p, u);
-            const long long ru = __shfl_sync(~0u, r, u);
-            if (ru < 0) continue;
-            for (int c = 0; c < D / 32; ++c)
-                acc[c] = fmaf(pu, __bfloat162float(a.v[ru + c * 32 + lane]), acc[c]);
-        }
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int c = 0; c < D / 32; ++c)
-        a.o[(tok * a.H + h) * D + c * 32 + lane] = __float2bfloat16_rn(acc[c] * inv);
-    if (a.lse && lane == 0) a.lse[tok * a.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
-}
 
 struct BwdArgs {
     Args f;
@@ -216,24 +155,6 @@ Args make_args(const SinkShape& s, const void* q, const void* k, const void* v, 
 }
 
 }  // namespace
-
-size_t sink_fwd_workspace_bytes(const SinkShape&) { return 256; }
-
-cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, const void* v,
-                            const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, void* o,
-                            float* lse, void*, int* status, cudaStream_t st, int* launches) {
-    Args a = make_args(s, q, k, v, status);
-    if (s.paged) a.p = PagedArgs{cu_q, kv_len, table, s.T, s.max_q, __builtin_ctz(s.page), s.n_pages, s.width};
-    a.o = static_cast<bf16*>(o);
-    a.lse = lse;
-    const long long blocks = ((long long)s.B * s.max_q * s.H + 3) / 4;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    GCA_LAUNCH("sink_fwd", st, (s.d == 64 ? sink_fwd_kernel<64><<<(unsigned)blocks, 128, 0, st>>>(a)
-                                          : sink_fwd_kernel<128><<<(unsigned)blocks, 128, 0, st>>>(a)));
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) *launches += 1;
-    return e;
-}
 
 size_t sink_bwd_workspace_bytes(const SinkShape&) { return 256; }
 

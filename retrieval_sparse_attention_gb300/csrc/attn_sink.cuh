@@ -37,4 +37,87 @@ __device__ __forceinline__ SeqInfo paged_seq(const PagedArgs& a, int b, int* sta
     return s;
 }
 
+// ---------------------------------------------------------------------------
+// Units of the forward and of the query-major gradients: the query rows of one
+// key head are packed into 128-row tiles, token-major (row r of a tile is token
+// r / G, query head r % G of the group), so a key tile is read once for the
+// whole group; keys come in tiles of 128.
+// ---------------------------------------------------------------------------
+struct SinkSched {
+    int B, L;            // sequences; dense: their length
+    int H, Hkv, G;       // G = H / Hkv
+    int W, ns;
+    int TM;              // tokens per query tile: min(128 / G, longest sequence)
+    int nMT;             // query tiles of the longest sequence
+    int paged;
+    PagedArgs p;
+};
+
+__device__ __forceinline__ SeqInfo sink_seq(const SinkSched& a, int b, int* status) {
+    if (!a.paged) return SeqInfo{b * a.L, a.L, 0};
+    return paged_seq(a.p, b, status);
+}
+
+// The key tiles that query tile mt of a sequence sees: nsk tiles of sinks from tile 0
+// on, then tiles k0 .. of the window.  nt = 0: no such query tile.  A query tile
+// that sees no key at all (negative positions) has one, fully masked.
+struct KeyTiles {
+    int p0, p1;          // positions of its first and last token
+    int k0, nsk, nt;
+    __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(const SinkSched& a, const SeqInfo& s, int mt) {
+    KeyTiles k;
+    const int t0 = mt * a.TM;
+    k.p0 = s.pos0 + t0;
+    k.p1 = s.pos0 + min(s.n, t0 + a.TM) - 1;
+    const int lo = max(0, k.p0 - a.W + 1);
+    k.k0 = lo >> 7;
+    k.nsk = min((a.ns + 127) >> 7, k.k0);
+    k.nt = t0 >= s.n ? 0 : k.nsk + (max(k.p1, 0) >> 7) - k.k0 + 1;
+    if (k.p1 < 0) { k.k0 = 0; k.nsk = 0; k.nt = t0 >= s.n ? 0 : 1; }
+    return k;
+}
+
+// Position in the stream of all (sequence, query tile, key head, key tile), in that
+// order: where a worker's share of the stream begins, and how long it is.
+struct StreamPos {
+    int b, mt, h, j;
+    int left;
+};
+
+// A worker's walk over its share, one key tile at a time.
+struct Walker {
+    SeqInfo s;
+    KeyTiles k;
+    int b, mt, h, j, left;
+    __device__ __forceinline__ void init(const SinkSched& a, const StreamPos& p) {
+        b = p.b; mt = p.mt; h = p.h; j = p.j; left = p.left;
+        s = SeqInfo{0, 0, 0};
+        k = KeyTiles{0, 0, 0, 0, 0};
+        if (left > 0) {
+            s = sink_seq(a, b, nullptr);
+            k = key_tiles(a, s, mt);
+        }
+    }
+    // Does the segment of this unit that the worker holds end with the current tile?
+    __device__ __forceinline__ bool last_tile() const { return j + 1 == k.nt || left == 1; }
+    __device__ __forceinline__ void next(const SinkSched& a) {
+        --left;
+        if (++j < k.nt || left <= 0) return;
+        j = 0;
+        if (++h < a.Hkv) return;
+        h = 0;
+        ++mt;
+        k = key_tiles(a, s, mt);
+        while (k.nt == 0 && b + 1 < a.B) {
+            ++b;
+            mt = 0;
+            s = sink_seq(a, b, nullptr);
+            k = key_tiles(a, s, 0);
+        }
+        if (k.nt == 0) left = 0;           // cannot happen: the share ends inside the stream
+    }
+};
+
 }  // namespace gca

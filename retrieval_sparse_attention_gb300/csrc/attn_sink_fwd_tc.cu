@@ -1,0 +1,788 @@
+// attn_sink_fwd_tc.cu -- forward of the windowed attention with sinks on the
+// Blackwell tensor cores (bf16, d = 64 or 128), over dense sequences and over a
+// paged K/V cache, from one new token to whole prompts.
+//
+//   o_t = sum_{s in V(t)} softmax_s(attn_scale q_t . k_s) v_s,
+//   V(t) = { s <= t : s > t - W or s < ns }.
+//
+// Work: units (sequence, 128-row query tile, key head) of a few to many key
+// tiles (attn_sink.cuh).  All key tiles of all units form one stream, which is cut
+// into equal shares, one per worker, wherever the cuts fall: a chunk of a
+// prompt, a batch of single tokens over uneven caches and one token over a long
+// cache all fill the machine.  Every CTA finds its cuts itself from a scan over
+// the sequences' lengths (on the device: a captured graph follows them).  A
+// unit cut by a share's end leaves unnormalised fp32 sums with their maxima in
+// the workspace, two slots a worker, and a second small kernel joins them in the
+// order of the stream (no atomics: bitwise reproducible).
+//
+// One CTA per SM (12 warps), two workers per CTA:
+//   warp 0     Q tiles and the K ring, by TMA (lanes issue one page each)
+//   warp 3     the V ring
+//   warp 1     S = Q K^T   (M = 128, N = 128) into the worker's S buffer
+//   warp 2     O += P V    (A = P from tensor memory)
+//   warps 4-11 one softmax warpgroup per worker; a thread owns a query row.
+// Producers and issuers walk the two workers' tiles in turn, so one worker's
+// softmax overlaps the other's products.  Tensor memory, d = 64: S 2 x 128
+// columns, O 2 x 64, P 2 x 64; d = 128: S 2 x 128, O 2 x 128, and P lies over the
+// first half of its own S (the next S product then waits for P V).
+// The online softmax keeps a stale maximum: sums are rescaled only when a tile's
+// maximum exceeds it by more than 2^8, so P <= 256 and its rounding to bf16
+// (relative 2^-8, the operand type of P V) is all that is lost.
+#include <math.h>
+
+#include "attn_sink.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.h"
+
+namespace gca {
+namespace {
+
+using namespace tc;
+using tcx::fast_exp2;
+using tcx::kLn2;
+using tcx::kLog2e;
+using tcx::Ring;
+
+constexpr int kThreads = 384;
+constexpr int kRegsLaunch = 168;
+constexpr int kRegsCtrl = 88;
+constexpr int kRegsSoftmax = 208;
+static_assert(128 * kRegsCtrl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch,
+              "register split exceeds the launch allocation");
+constexpr int kMaxCtas = 152;              // one per SM; the workspace is sized for them
+constexpr int kMaxWorkers = 2 * kMaxCtas;
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int kSmemMax = 232448;
+
+template <int D>
+struct Cfg {
+    static constexpr int SUB = D / 64;                    // 64-column sub-tiles of a tile
+    static constexpr int STILE = 128 * 128;               // bytes of a 128-row sub-tile
+    static constexpr int TILE = SUB * STILE;
+    static constexpr int QB = D == 64 ? 2 : 1;            // Q buffers a worker
+    static constexpr int KST = D == 64 ? 4 : 2;
+    static constexpr int VST = D == 64 ? 6 : 3;
+    static constexpr int STAGES = VST;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = 2 * QB * TILE;
+    static constexpr int OFF_V = OFF_K + KST * TILE;
+    static constexpr int SMEM = OFF_V + VST * TILE + 1024;
+    static constexpr uint32_t COL_S = 0;                  // + 128 w
+    static constexpr uint32_t COL_O = 256;                // + D w
+    static constexpr bool P_OVER_S = D == 128;
+    static constexpr uint32_t COL_P = P_OVER_S ? 0 : 384; // + 128 w (over S) or + 64 w
+    static constexpr uint32_t P_STEP = P_OVER_S ? 128 : 64;
+};
+
+struct FwdArgs {
+    SinkSched s;
+    __nv_bfloat16* o;
+    float* lse;
+    float* part_o;           // [2 * workers][R][D]
+    float2* part_ml;         // [2 * workers][R]: maximum (log2 units), sum
+    int4* tail;              // [workers]: unit (b, mt, h, 1) whose first part this worker holds, or .w = 0
+    int* head;               // [workers]: 0, 1 (holds the last part of an earlier worker's unit), 2 (a middle part)
+    int R;                   // rows of a query tile: TM * G
+    int snap;                // cut the stream only between units
+    int* status;
+    float scale_log2;
+};
+
+template <int STAGES>
+struct __align__(8) Bars {
+    uint64_t q_full[2][2], q_empty[2][2];
+    uint64_t k_full[STAGES], k_empty[STAGES];
+    uint64_t v_full[STAGES], v_empty[STAGES];
+    uint64_t s_full[2], s_empty[2];
+    uint64_t p_full[2], p_empty[2];
+    uint64_t o_full[2], o_empty[2];
+    uint64_t done, done2;
+    uint32_t tmem;
+    int abort;
+    StreamPos pos[2];
+    long long total;
+    long long wsum[12];
+};
+
+__device__ __forceinline__ uint32_t full_par(int k) { return static_cast<uint32_t>(k) & 1u; }
+__device__ __forceinline__ uint32_t empty_par(int k) { return (static_cast<uint32_t>(k) & 1u) ^ 1u; }
+
+// The CTA's two shares of the stream of key tiles (see StreamPos).  All threads take part.
+template <typename B>
+__device__ __forceinline__ void find_shares(const FwdArgs& a, B& sb) {
+    const SinkSched& s = a.s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = s.B * s.nMT;
+    const int per = (E + kThreads - 1) / kThreads;
+    const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
+    // entries e = b * nMT + mt; consecutive entries of a thread mostly share b
+    auto walk = [&](auto f) {
+        int b = e0 / s.nMT, mt = e0 - b * s.nMT;
+        SeqInfo q{0, 0, 0};
+        for (int e = e0; e < e1; ++e) {
+            if (e == e0 || mt == 0) q = sink_seq(s, b, a.status);
+            f(b, mt, key_tiles(s, q, mt).nt);
+            if (++mt == s.nMT) { mt = 0; ++b; }
+        }
+    };
+    long long mine = 0;
+    walk([&](int, int, int nt) { mine += nt; });
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) sb.wsum[warp] = inc;
+    if (tid < 2) sb.pos[tid] = StreamPos{0, 0, 0, 0, 0};
+    __syncthreads();
+    long long base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) base += sb.wsum[w];
+        total += sb.wsum[w];
+    }
+    base = (base + inc - mine) * s.Hkv;
+    total *= s.Hkv;
+    const long long top = base + mine * s.Hkv;
+    const int workers = 2 * gridDim.x;
+    const long long quota = (total + workers - 1) / workers;
+    // this thread's entries hold positions base .. top - 1 of the stream
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const long long wid = blockIdx.x + (long long)w * gridDim.x;
+        const long long from = wid * quota, to = min(total, from + quota);
+#pragma unroll
+        for (int end = 0; end < 2; ++end) {
+            // the share's first tile, and its end (one past the last tile)
+            const long long x = end ? to : from;
+            if (from >= total) continue;
+            if (x >= total) {
+                if (tid == 0 && end) atomicAdd(&sb.pos[w].left, static_cast<int>(total - from));
+                continue;
+            }
+            if (x < base || x >= top) continue;
+            long long at = base;
+            walk([&](int b, int mt, int nt) {
+                const long long n = (long long)nt * s.Hkv;
+                if (x >= at && x < at + n) {
+                    int h = static_cast<int>((x - at) / nt), j = static_cast<int>((x - at) % nt);
+                    const int skip = (a.snap && j > 0) ? nt - j : 0;      // up to the next unit
+                    if (end) {
+                        atomicAdd(&sb.pos[w].left, static_cast<int>(x - from) + skip);
+                    } else {
+                        atomicAdd(&sb.pos[w].left, -skip);
+                        if (skip) {
+                            j = 0;
+                            if (++h == s.Hkv) { h = 0; ++mt; }           // (the walker skips empty query tiles)
+                        }
+                        sb.pos[w].b = b; sb.pos[w].mt = mt; sb.pos[w].h = h; sb.pos[w].j = j;
+                    }
+                }
+                at += n;
+            });
+        }
+    }
+    __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const FwdArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+    __shared__ Bars<C::STAGES> sb;
+    static_assert(C::SMEM + sizeof(Bars<C::STAGES>) <= kSmemMax, "shared memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto wait = [&](uint64_t* bar, uint32_t par) { return tcx::wait_bar(&sb.abort, bar, par, a.status); };
+    // the accesses after a wait are warp-collective: a wait that gave up in one lane does in all
+    auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
+    const SinkSched& sc = a.s;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&sb.q_full[i][u], 1);
+                mbar_init(&sb.q_empty[i][u], 1);
+            }
+            mbar_init(&sb.s_full[i], 1);
+            mbar_init(&sb.s_empty[i], C::P_OVER_S ? 1 : 128);
+            mbar_init(&sb.p_full[i], 128);
+            mbar_init(&sb.p_empty[i], 1);
+            mbar_init(&sb.o_full[i], 1);
+            mbar_init(&sb.o_empty[i], 128);
+        }
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&sb.k_full[i], 1);
+            mbar_init(&sb.k_empty[i], 1);
+            mbar_init(&sb.v_full[i], 1);
+            mbar_init(&sb.v_empty[i], 1);
+        }
+        mbar_init(&sb.done, 1);
+        mbar_init(&sb.done2, 1);
+        sb.abort = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sb.tmem, TMEM_COLS);
+        tmem_relinquish();
+    }
+    find_shares(a, sb);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sb.tmem;
+
+    // Walkers start here; one whose snapped start fell behind its sequence's last query tile
+    // moves on to the next unit.
+    auto start = [&](Walker& w, int i) {
+        w.init(sc, sb.pos[i]);
+        while (w.left > 0 && w.k.nt == 0 && w.b + 1 < sc.B) {
+            ++w.b;
+            w.mt = 0;
+            w.s = sink_seq(sc, w.b, nullptr);
+            w.k = key_tiles(sc, w.s, 0);
+        }
+    };
+
+    if (warp < 4) {
+    setmaxnreg_dec<kRegsCtrl>();
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------ producers (whole warps)
+        const bool kl = warp == 0;
+        Walker wk[2];
+        start(wk[0], 0);
+        start(wk[1], 1);
+        Ring rg{0, 0};
+        int kq[2] = {0, 0};
+        uint64_t* full = kl ? sb.k_full : sb.v_full;
+        uint64_t* empty = kl ? sb.k_empty : sb.v_empty;
+        const CUtensorMap* map = kl ? &tk : &tv;
+        uint8_t* ring = sm + (kl ? C::OFF_K : C::OFF_V);
+        const int nst = kl ? C::KST : C::VST;
+        const int pages = sc.paged ? 128 >> sc.p.page_log2 : 1;       // boxes of a tile, one lane each
+        // page id of this lane's box of the walker's current tile; n_pages (outside the
+        // map: reads as zeros) where no row of the unit sees any of the page
+        auto lookup = [&](const Walker& w) {
+            if (!sc.paged || w.left <= 0 || lane >= pages) return 0;
+            const int c0 = w.k.tile(w.j) * 128 + (lane << sc.p.page_log2);
+            const int c1 = c0 + (1 << sc.p.page_log2) - 1;
+            if (c0 > w.k.p1 || (c1 <= w.k.p0 - sc.W && c0 >= sc.ns)) return sc.p.n_pages;
+            int pg = sc.p.table[(size_t)w.b * sc.p.width + (c0 >> sc.p.page_log2)];
+            if (pg < 0 || pg >= sc.p.n_pages) {
+                set_status(a.status, GCA_ERR_DEVICE_INDEX);
+                pg = sc.p.n_pages;
+            }
+            return pg;
+        };
+        int pg[2] = {lookup(wk[0]), lookup(wk[1])};
+        bool ok = true;
+        uint32_t used = 0;                                            // stages (bits) and Q buffers in flight at the end
+        while (ok && (wk[0].left > 0 || wk[1].left > 0)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                Walker& w = wk[i];
+                if (w.left <= 0 || !ok) continue;
+                if (kl && (kq[i] == 0 || w.j == 0)) {                 // first tile of a unit's segment: its Q
+                    const int qb = kq[i] % C::QB;
+                    if (!wwait(&sb.q_empty[i][qb], empty_par(kq[i] / C::QB))) { ok = false; break; }
+                    if (lane == 0) {
+                        uint8_t* dst = sm + C::OFF_Q + (i * C::QB + qb) * C::TILE;
+                        mbar_arrive_expect_tx(&sb.q_full[i][qb], C::SUB * a.R * 128);
+#pragma unroll
+                        for (int c = 0; c < C::SUB; ++c)
+                            tma_load_3d(dst + c * C::STILE, &tq, &sb.q_full[i][qb], c * 64, w.h * sc.G,
+                                        w.s.row0 + w.mt * sc.TM);
+                    }
+                    ++kq[i];
+                }
+                if (!wwait(&empty[rg.i], rg.ph ^ 1u)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(&full[rg.i], C::TILE);
+                __syncwarp();
+                if (lane < pages) {
+                    uint8_t* dst = ring + rg.i * C::TILE;
+                    const int col = w.h * D;
+                    if (sc.paged) {
+                        dst += (lane << sc.p.page_log2) * 128;
+#pragma unroll
+                        for (int c = 0; c < C::SUB; ++c)
+                            tma_load_3d(dst + c * C::STILE, map, &full[rg.i], col + c * 64, 0, pg[i]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C::SUB; ++c)
+                            tma_load_3d(dst + c * C::STILE, map, &full[rg.i], col + c * 64, w.k.tile(w.j) * 128, w.b);
+                    }
+                }
+                used |= 1u << rg.i;
+                rg.next(nst);
+                w.next(sc);
+                pg[i] = lookup(w);                                    // a turn ahead of its use
+            }
+        }
+        // no copy may still be writing shared memory when the CTA exits: the last load of
+        // each buffer has completed its current phase
+        if (lane == 0) {
+            for (int i = 0; i < nst; ++i)
+                if (used >> i & 1u) mbar_wait(&full[i], i < rg.i ? rg.ph : rg.ph ^ 1u, nullptr, 100000000ull);
+            if (kl)
+                for (int i = 0; i < 2; ++i)
+                    for (int u = 0; u < C::QB; ++u) {
+                        const int n = (kq[i] - u + C::QB - 1) / C::QB;   // loads into buffer u
+                        if (n > 0) mbar_wait(&sb.q_full[i][u], full_par(n - 1), nullptr, 100000000ull);
+                    }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ S issuer
+        if (lane == 0) {
+            Walker wk[2];
+            start(wk[0], 0);
+            start(wk[1], 1);
+            Ring kv{0, 0};
+            int kq[2] = {0, 0}, ts[2] = {0, 0};
+            bool fresh[2] = {true, true};
+            bool issued = false, ok = true;
+            const uint32_t id_s = idesc_bf16(128, 128, false, false);
+            while (ok && (wk[0].left > 0 || wk[1].left > 0)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    Walker& w = wk[i];
+                    if (w.left <= 0 || !ok) continue;
+                    const int qb = kq[i] % C::QB;
+                    if ((fresh[i] && !wait(&sb.q_full[i][qb], full_par(kq[i] / C::QB))) ||
+                        !wait(&sb.k_full[kv.i], kv.ph) || !wait(&sb.s_empty[i], empty_par(ts[i]))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t qaddr = smem_u32(sm + C::OFF_Q + (i * C::QB + qb) * C::TILE);
+                    const uint32_t kaddr = smem_u32(sm + C::OFF_K + kv.i * C::TILE);
+                    tcx::mma_kmajor_dh<D>(tmem + C::COL_S + i * 128, qaddr, 128, kaddr, 128, id_s, 0);
+                    mma_commit(&sb.s_full[i]);
+                    mma_commit(&sb.k_empty[kv.i]);
+                    issued = true;
+                    ++ts[i];
+                    fresh[i] = w.last_tile();
+                    if (fresh[i]) {
+                        mma_commit(&sb.q_empty[i][qb]);
+                        ++kq[i];
+                    }
+                    kv.next(C::KST);
+                    w.next(sc);
+                }
+            }
+            if (issued) {
+                mma_commit(&sb.done);
+                mbar_wait(&sb.done, 0, nullptr, 100000000ull);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ P V issuer (whole warp: it also
+        // clears the V rows behind a sequence's last token, whose cache rows may hold anything)
+        Walker wk[2];
+        start(wk[0], 0);
+        start(wk[1], 1);
+        Ring kv{0, 0};
+        int ko[2] = {0, 0}, tp[2] = {0, 0};
+        bool fresh[2] = {true, true};
+        bool issued = false, ok = true;
+        const uint32_t id_o = idesc_bf16(128, 64, false, true);
+        while (ok && (wk[0].left > 0 || wk[1].left > 0)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                Walker& w = wk[i];
+                if (w.left <= 0 || !ok) continue;
+                if (!wwait(&sb.v_full[kv.i], kv.ph)) { ok = false; break; }
+                uint8_t* vt = sm + C::OFF_V + kv.i * C::TILE;
+                const int behind = w.s.pos0 + w.s.n - w.k.tile(w.j) * 128;      // first row behind the last token
+                if (sc.paged && behind < 128) {
+                    for (int r = max(behind, 0) * 8 + lane; r < 128 * 8; r += 32)
+#pragma unroll
+                        for (int c = 0; c < C::SUB; ++c)
+                            reinterpret_cast<uint4*>(vt + c * C::STILE)[r] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if ((fresh[i] && !wwait(&sb.o_empty[i], empty_par(ko[i]))) ||
+                    !wwait(&sb.p_full[i], full_par(tp[i]))) { ok = false; break; }
+                if (lane == 0) {
+                    tc_fence_after();
+                    tcx::mma_ts_mn_dh<D, 8>(tmem + C::COL_O + i * D, tmem + C::COL_P + i * C::P_STEP, smem_u32(vt),
+                                            128, id_o, fresh[i] ? 0u : 1u);
+                    mma_commit(&sb.v_empty[kv.i]);
+                    mma_commit(&sb.p_empty[i]);
+                    if (C::P_OVER_S) mma_commit(&sb.s_empty[i]);
+                    if (w.last_tile()) mma_commit(&sb.o_full[i]);
+                }
+                issued = true;
+                ++tp[i];
+                fresh[i] = w.last_tile();
+                if (fresh[i]) ++ko[i];
+                kv.next(C::VST);
+                w.next(sc);
+            }
+        }
+        if (issued && lane == 0) {
+            mma_commit(&sb.done2);
+            mbar_wait(&sb.done2, 0, nullptr, 100000000ull);
+        }
+    }
+    } else {
+        // ------------------------------------------------------------ softmax + epilogue
+        setmaxnreg_inc<kRegsSoftmax>();
+        const int wg = (warp - 4) >> 2;
+        const int wid = blockIdx.x + wg * gridDim.x;
+        const int qd = warp & 3;
+        const int row = 32 * qd + lane;                 // TMEM lane = query row of the tile
+        const int rt = row / sc.G, rg = row - rt * sc.G;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
+        const uint32_t ts_addr = tmem + lane_base + C::COL_S + wg * 128;
+        const uint32_t to_addr = tmem + lane_base + C::COL_O + wg * D;
+        const uint32_t tp_addr = tmem + lane_base + C::COL_P + wg * C::P_STEP;
+        const float sl = a.scale_log2;
+
+        Walker w;
+        start(w, wg);
+        if (row == 0) {                                 // what the join reads of this worker
+            a.head[wid] = w.left > 0 && w.j > 0 ? (w.left >= w.k.nt - w.j ? 1 : 2) : 0;
+            a.tail[wid] = make_int4(0, 0, 0, 0);
+        }
+        int ts = 0, ko = 0;
+        bool fresh = true;                              // first tile of this worker's part of a unit
+        float m = -INFINITY, l = 0.f;                   // running max (of s * scale * log2(e)) and sum of exp2(. - m)
+        int j_from = w.j;
+        // the finished part whose O still sits in tensor memory
+        bool pend = false;
+        long long pend_row = -1;                        // token * H + head, or -1: no such row
+        int pend_slot = -1;                             // -1: whole unit; else the workspace slot of the part
+        float pm = 0.f, pl = 1.f;
+        while (true) {
+            const bool have = w.left > 0;
+            // rows of this warp that exist (the others' arithmetic is skipped)
+            const bool live = have && row < a.R && w.mt * sc.TM + rt < w.s.n;
+            const bool wlive = __any_sync(0xffffffffu, live);
+            float alpha = 1.f;
+            bool resc = false;
+            float x[128];
+            if (have) {
+                if (!wwait(&sb.s_full[wg], full_par(ts))) break;
+                tc_fence_after();
+                if (wlive) {
+                    float mt;
+                    {
+                        uint32_t r[2][64];
+                        float mc[2];
+#pragma unroll
+                        for (int ci = 0; ci < 2; ++ci) mc[ci] = tmem_ld_max_32x32b_x64(ts_addr + 64 * ci, r[ci]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int ci = 0; ci < 2; ++ci)
+#pragma unroll
+                            for (int u = 0; u < 64; ++u) x[64 * ci + u] = __uint_as_float(r[ci][u]);
+                        mt = fmaxf(mc[0], mc[1]);
+                    }
+                    tc_fence_before();
+                    if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
+                    const int kbase = w.k.tile(w.j) * 128;
+                    // every row sees the whole tile, unless the diagonal or the window's edge crosses it
+                    if (kbase + 127 > w.k.p0 || (kbase < w.k.p1 - sc.W + 1 && kbase + 127 >= sc.ns)) {
+                        const int p = w.k.p0 + rt;
+                        const int c_lo = p - sc.W + 1 - kbase;
+                        const int c_s = min(sc.ns, p + 1) - kbase;     // sinks: columns below it
+                        const uint32_t span = static_cast<uint32_t>(sc.W - 1);
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            x[i] = (static_cast<uint32_t>(i - c_lo) > span && i >= c_s) ? -INFINITY : x[i];
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+                        mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    }
+                    const float mts = mt * sl;
+                    if (mts > m + kRescaleLog2) {
+                        if (m != -INFINITY) {
+                            resc = true;
+                            alpha = fast_exp2(m - mts);
+                        }
+                        m = mts;
+                    }
+                    l *= alpha;
+                } else if (!C::P_OVER_S) {
+                    mbar_arrive(&sb.s_empty[wg]);
+                }
+            }
+            // the previous part's output leaves after the next one's first maximum, which
+            // gives its last P V time to complete
+            if ((fresh || !have) && pend) {
+                if (!wwait(&sb.o_full[wg], full_par(ko))) break;
+                tc_fence_after();
+                const bool wr = pend_row >= 0;
+                const float inv = pl > 0.f ? 1.f / pl : 0.f;
+                if (__any_sync(0xffffffffu, wr)) {
+#pragma unroll
+                    for (int ci = 0; ci < D / 32; ++ci) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(to_addr + 32 * ci, r);
+                        tmem_wait_ld();
+                        if (wr && pend_slot < 0) {
+                            float f[32];
+                            // (an empty row's accumulator holds exact zeros times its zero weights)
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) f[u] = __uint_as_float(r[u]);
+                            uint4* dst = reinterpret_cast<uint4*>(a.o + pend_row * D) + 4 * ci;
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) dst[u] = tcx::pack8(f + 8 * u, inv);
+                        } else if (wr) {
+                            uint4* dst = reinterpret_cast<uint4*>(a.part_o + ((size_t)pend_slot * a.R + row) * D) + 8 * ci;
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                dst[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                        }
+                    }
+                    if (wr && pend_slot >= 0) a.part_ml[(size_t)pend_slot * a.R + row] = make_float2(pm, pl);
+                    if (wr && pend_slot < 0 && a.lse) a.lse[pend_row] = pl > 0.f ? (pm + log2f(pl)) * kLn2 : -INFINITY;
+                }
+                tc_fence_before();
+                mbar_arrive(&sb.o_empty[wg]);
+                ++ko;
+                pend = false;
+            }
+            if (!have) break;
+            if (wlive) {
+                const float mu = (m == -INFINITY) ? 0.f : m;
+                const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(-mu, -mu);
+                uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+                uint32_t pka[32];                       // the first 64 keys' P, formed before the wait for the P buffer
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float y0, y1;
+                    tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x[2 * c], x[2 * c + 1]), sl2, nmu2), y0, y1);
+                    const float e0 = fast_exp2(y0);
+                    const float e1 = fast_exp2(y1);
+                    acc2[c & 3] = tcx::fadd2(acc2[c & 3], tcx::f2_pack(e0, e1));
+                    pka[c] = tcx::pack_bf16(e0, e1);
+                }
+                // the previous tile's P V has completed: O is stable, the P buffer free
+                // (P over S: already so, since this tile's S product waited for it)
+                if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
+                if (__any_sync(0xffffffffu, resc)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int ci = 0; ci < D / 16; ++ci) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(to_addr + 16 * ci, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) r[u] = __float_as_uint(__uint_as_float(r[u]) * alpha);
+                        tmem_st_32x32b_x16(to_addr + 16 * ci, r);
+                    }
+                    tmem_wait_st();
+                }
+                {
+                    uint32_t h0[16], h1[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) { h0[u] = pka[u]; h1[u] = pka[16 + u]; }
+                    tmem_st_32x32b_x16(tp_addr, h0);
+                    tmem_st_32x32b_x16(tp_addr + 16, h1);
+                }
+                uint32_t pk2[16];
+#pragma unroll
+                for (int c = 4; c < 8; ++c) {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        float y0, y1;
+                        const uint64_t s2 = tcx::f2_pack(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]);
+                        tcx::f2_unpack(tcx::ffma2(s2, sl2, nmu2), y0, y1);
+                        const float e0 = fast_exp2(y0);
+                        const float e1 = fast_exp2(y1);
+                        acc2[u & 3] = tcx::fadd2(acc2[u & 3], tcx::f2_pack(e0, e1));
+                        pk[u] = tcx::pack_bf16(e0, e1);
+                    }
+                    if (c & 1) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) pk2[8 + u] = pk[u];
+                        tmem_st_32x32b_x16(tp_addr + 16 * (c >> 1), pk2);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) pk2[u] = pk[u];
+                    }
+                }
+                tmem_wait_st();
+                float l4[8];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) tcx::f2_unpack(acc2[u], l4[2 * u], l4[2 * u + 1]);
+                l += ((l4[0] + l4[1]) + (l4[2] + l4[3])) + ((l4[4] + l4[5]) + (l4[6] + l4[7]));
+            } else if (!C::P_OVER_S) {
+                if (!wwait(&sb.p_empty[wg], empty_par(ts))) break;
+            }
+            tc_fence_before();
+            mbar_arrive(&sb.p_full[wg]);
+            ++ts;
+            fresh = w.last_tile();
+            if (fresh) {                                // this part of the unit is done: it leaves later
+                pend = true;
+                pend_row = live ? (long long)(w.s.row0 + w.mt * sc.TM + rt) * sc.H + w.h * sc.G + rg : -1;
+                const bool whole_end = w.j + 1 == w.k.nt;
+                pend_slot = j_from > 0 ? 2 * wid : (whole_end ? -1 : 2 * wid + 1);
+                if (pend_slot == 2 * wid + 1 && row == 0) a.tail[wid] = make_int4(w.b, w.mt, w.h, 1);
+                pm = m;
+                pl = l;
+                m = -INFINITY;
+                l = 0.f;
+            }
+            w.next(sc);
+            if (fresh) j_from = w.j;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// Joins the parts of the units that were cut: block w the unit that begins in worker
+// w's share and continues in the next ones.  With m = max_i m_i,
+//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, in the order of the stream.
+template <int D>
+__global__ void __launch_bounds__(256) sink_join_kernel(const FwdArgs a, int workers) {
+    const int w = blockIdx.x;
+    const int4 u = a.tail[w];
+    if (u.w == 0) return;
+    const SinkSched& sc = a.s;
+    const SeqInfo s = sink_seq(sc, u.x, nullptr);
+    int n = 1;                                          // parts: slot 2w+1, then slots 2(w+1), 2(w+2), ..
+    while (w + n < workers) {
+        const int h = a.head[w + n];
+        ++n;
+        if (h != 2) break;
+    }
+    constexpr int VEC = D / 4;                          // threads a row
+    for (int i = threadIdx.x; i < a.R * VEC; i += blockDim.x) {
+        const int row = i / VEC, c = i % VEC;
+        const int rt = row / sc.G, t = u.y * sc.TM + rt;
+        if (t >= s.n) continue;
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < n; ++k) {
+            const size_t slot = k == 0 ? 2 * w + 1 : 2 * (w + k);
+            const float2 ml = a.part_ml[slot * a.R + row];
+            if (ml.x == -INFINITY) continue;
+            const float4 o = reinterpret_cast<const float4*>(a.part_o + (slot * a.R + row) * D)[c];
+            const float mn = fmaxf(m, ml.x);
+            const float f0 = fast_exp2(m - mn), f1 = fast_exp2(ml.x - mn);
+            acc.x = acc.x * f0 + o.x * f1;
+            acc.y = acc.y * f0 + o.y * f1;
+            acc.z = acc.z * f0 + o.z * f1;
+            acc.w = acc.w * f0 + o.w * f1;
+            l = l * f0 + ml.y * f1;
+            m = mn;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const long long orow = (long long)(s.row0 + t) * sc.H + u.z * sc.G + (row - rt * sc.G);
+        reinterpret_cast<uint2*>(a.o + orow * D)[c] =
+            make_uint2(tcx::pack_bf16(acc.x * inv, acc.y * inv), tcx::pack_bf16(acc.z * inv, acc.w * inv));
+        if (c == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+}
+
+int rows_of_tile(const SinkShape& s, int* tm) {
+    const int G = s.H / s.Hkv;
+    int t = 128 / G;
+    if (t > s.max_q) t = s.max_q;
+    *tm = t;
+    return t * G;
+}
+
+struct Layout {
+    size_t o_off, ml_off, tail_off, head_off, total;
+};
+Layout layout(const SinkShape& s) {
+    int tm;
+    const size_t R = rows_of_tile(s, &tm);
+    Layout w;
+    w.o_off = 0;
+    w.ml_off = w.o_off + (size_t)2 * kMaxWorkers * R * s.d * 4;
+    w.tail_off = (w.ml_off + (size_t)2 * kMaxWorkers * R * 8 + 255) / 256 * 256;
+    w.head_off = w.tail_off + kMaxWorkers * 16;
+    w.total = (w.head_off + kMaxWorkers * 4 + 255) / 256 * 256;
+    return w;
+}
+
+template <int D>
+cudaError_t launch(const SinkShape& s, const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                   const CUtensorMap& tv, int grid, cudaStream_t st, int* launches) {
+    using C = Cfg<D>;
+    // the setmaxnreg split needs the whole launch allocation: refuse to launch a build that
+    // gave the kernel fewer registers a thread (its warps would wait forever)
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, sink_fwd_tc_kernel<D>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kThreads < 128 * kRegsCtrl + 256 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(sink_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    *launches += 1;
+    if (a.snap) return e;
+    GCA_LAUNCH("sink_join", st, sink_join_kernel<D><<<2 * grid, 256, 0, st>>>(a, 2 * grid));
+    if ((e = cudaGetLastError()) == cudaSuccess) *launches += 1;
+    return e;
+}
+
+}  // namespace
+
+size_t sink_fwd_workspace_bytes(const SinkShape& s) { return layout(s).total; }
+
+cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, const void* v,
+                            const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, void* o,
+                            float* lse, void* ws, int* status, cudaStream_t st, int* launches) {
+    FwdArgs a{};
+    a.s.B = s.B; a.s.L = s.L; a.s.H = s.H; a.s.Hkv = s.Hkv; a.s.G = s.H / s.Hkv;
+    a.s.W = s.W; a.s.ns = s.ns;
+    a.R = rows_of_tile(s, &a.s.TM);
+    a.s.nMT = (s.max_q + a.s.TM - 1) / a.s.TM;
+    a.s.paged = s.paged;
+    if (s.paged) a.s.p = PagedArgs{cu_q, kv_len, table, s.T, s.max_q, __builtin_ctz(s.page), s.n_pages, s.width};
+    if ((long long)s.B * a.s.nMT >= (1ll << 30)) return cudaErrorInvalidConfiguration;
+    const Layout w = layout(s);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    a.part_o = reinterpret_cast<float*>(base + w.o_off);
+    a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
+    a.tail = reinterpret_cast<int4*>(base + w.tail_off);
+    a.head = reinterpret_cast<int*>(base + w.head_off);
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse;
+    a.status = status;
+    a.scale_log2 = s.scale * kLog2e;
+    CUtensorMap tq, tk, tv;
+    const uint64_t kvcols = (uint64_t)s.Hkv * s.d;
+    bool ok = encode_bf16_3d(&tq, q, s.d, s.H, s.T, s.d, s.q_stride, a.s.G, a.s.TM);
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap* m = i ? &tv : &tk;
+        const void* p = i ? v : k;
+        ok = ok && (s.paged ? encode_bf16_3d(m, p, kvcols, s.page, s.n_pages, kvcols, kvcols * s.page, s.page, 1)
+                            : encode_bf16_3d(m, p, kvcols, s.L, s.B, s.kv_stride, (uint64_t)s.kv_stride * s.L, 128, 1));
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+    return s.d == 64 ? launch<64>(s, a, tq, tk, tv, grid, st, launches)
+                     : launch<128>(s, a, tq, tk, tv, grid, st, launches);
+}
+
+}  // namespace gca

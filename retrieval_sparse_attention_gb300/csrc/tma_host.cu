@@ -66,6 +66,21 @@ bool encode_bf16_seq(CUtensorMap* map, const void* base, uint64_t B, uint64_t L,
     return r == CUDA_SUCCESS;
 }
 
+bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2,
+                    uint64_t stride1, uint64_t stride2, uint32_t box1, uint32_t box2) {
+    std::call_once(g_once, resolve);
+    if (!g_encode) return false;
+    cuuint64_t dims[3] = {n0, n1, n2};
+    cuuint64_t strides[2] = {stride1 * 2, stride2 * 2};
+    cuuint32_t box[3] = {64, box1, box2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool encode_f32_box(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_elems,
                     uint32_t box_cols, uint32_t box_rows) {
     std::call_once(g_once, resolve);

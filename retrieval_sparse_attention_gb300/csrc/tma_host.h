@@ -25,6 +25,13 @@ bool encode_bf16_rows_box(CUtensorMap* map, const void* base, uint64_t rows, uin
 bool encode_bf16_seq(CUtensorMap* map, const void* base, uint64_t B, uint64_t L, uint64_t row_elems,
                      uint32_t box_rows);
 
+// Tensor map over a bf16 tensor of three dimensions (innermost first) whose two
+// outer strides are given in elements (multiples of 8), with a 128-byte swizzle
+// and a box whose innermost extent is 64 elements.  Elements outside the tensor
+// read as zeros and are not written.
+bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2,
+                    uint64_t stride1, uint64_t stride2, uint32_t box1, uint32_t box2);
+
 // Tensor map over a row-major fp32 matrix [rows, row_elems] (row stride
 // row_elems * 4 bytes, a multiple of 16), box of box_cols x box_rows (box_cols
 // * 4 a multiple of 16), no swizzle: the box lands in shared memory as
