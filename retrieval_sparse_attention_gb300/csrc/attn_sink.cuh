@@ -86,38 +86,4 @@ struct StreamPos {
     int left;
 };
 
-// A worker's walk over its share, one key tile at a time.
-struct Walker {
-    SeqInfo s;
-    KeyTiles k;
-    int b, mt, h, j, left;
-    __device__ __forceinline__ void init(const SinkSched& a, const StreamPos& p) {
-        b = p.b; mt = p.mt; h = p.h; j = p.j; left = p.left;
-        s = SeqInfo{0, 0, 0};
-        k = KeyTiles{0, 0, 0, 0, 0};
-        if (left > 0) {
-            s = sink_seq(a, b, nullptr);
-            k = key_tiles(a, s, mt);
-        }
-    }
-    // Does the segment of this unit that the worker holds end with the current tile?
-    __device__ __forceinline__ bool last_tile() const { return j + 1 == k.nt || left == 1; }
-    __device__ __forceinline__ void next(const SinkSched& a) {
-        --left;
-        if (++j < k.nt || left <= 0) return;
-        j = 0;
-        if (++h < a.Hkv) return;
-        h = 0;
-        ++mt;
-        k = key_tiles(a, s, mt);
-        while (k.nt == 0 && b + 1 < a.B) {
-            ++b;
-            mt = 0;
-            s = sink_seq(a, b, nullptr);
-            k = key_tiles(a, s, 0);
-        }
-        if (k.nt == 0) left = 0;           // cannot happen: the share ends inside the stream
-    }
-};
-
 }  // namespace gca

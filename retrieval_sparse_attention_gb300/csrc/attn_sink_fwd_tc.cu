@@ -16,7 +16,11 @@
 // order of the stream (no atomics: bitwise reproducible).
 //
 // One CTA per SM (12 warps), two workers per CTA:
-//   warp 0     Q tiles and the K ring, by TMA (lanes issue one page each)
+//   warp 0     walks the two shares and writes each part of a unit down as a record
+//              in shared memory, from which the other roles take their turns (one
+//              copy of that code: with a copy in every role the kernel outgrew the
+//              instruction cache and ran three times slower); Q tiles and the K
+//              ring, by TMA (lanes issue one page each)
 //   warp 3     the V ring
 //   warp 1     S = Q K^T   (M = 128, N = 128) into the worker's S buffer
 //   warp 2     O += P V    (A = P from tensor memory)
@@ -92,8 +96,21 @@ struct FwdArgs {
     float scale_log2;
 };
 
+// One worker's part of a unit: key tiles j0 .. j1 - 1 (j0 == j1: the share is done).
+struct __align__(16) Part {
+    int b, h, qrow, ntok;    // sequence, key head, first token's row, tokens of the query tile
+    int p0, p1, end;         // positions of the first and the last token, and behind the sequence
+    int k0, nsk;             // key tile j is j (j < nsk) or k0 + j - nsk
+    int j0, j1;
+    int slot;                // -1: the whole unit; else the workspace slot of its sums
+    __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
+};
+constexpr int kParts = 4;    // records a worker
+
 template <int STAGES>
-struct __align__(8) Bars {
+struct __align__(16) Bars {
+    Part part[2][kParts];
+    uint64_t part_full[2][kParts], part_empty[2][kParts];
     uint64_t q_full[2][2], q_empty[2][2];
     uint64_t k_full[STAGES], k_empty[STAGES];
     uint64_t v_full[STAGES], v_empty[STAGES];
@@ -104,90 +121,145 @@ struct __align__(8) Bars {
     uint32_t tmem;
     int abort;
     StreamPos pos[2];
-    long long total;
-    long long wsum[12];
+    int wsum[12];
 };
 
 __device__ __forceinline__ uint32_t full_par(int k) { return static_cast<uint32_t>(k) & 1u; }
 __device__ __forceinline__ uint32_t empty_par(int k) { return (static_cast<uint32_t>(k) & 1u) ^ 1u; }
+
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// tcx::wait_bar for the control warps, as little code as it takes: gives up after
+// kWaitNs or once another role of the CTA has.
+__device__ __forceinline__ bool wait_ctrl(int* abort_flag, uint64_t* bar, uint32_t parity, int* status) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 63u) continue;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (*((volatile int*)abort_flag)) return false;
+        if (t - t0 > tcx::kWaitNs) {
+            set_status(status, GCA_ERR_TIMEOUT);
+            *((volatile int*)abort_flag) = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// Bounded wait (0.1 s) for work in flight at the end.
+__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) {
+    mbar_wait(bar, parity, nullptr, 100000000ull);
+}
 
 // The CTA's two shares of the stream of key tiles (see StreamPos).  All threads take part.
 template <typename B>
 __device__ __forceinline__ void find_shares(const FwdArgs& a, B& sb) {
     const SinkSched& s = a.s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int E = s.B * s.nMT;
+    const int E = s.B * s.nMT;                      // entries e = b * nMT + mt, a run of them for each thread
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
-    // entries e = b * nMT + mt; consecutive entries of a thread mostly share b
-    auto walk = [&](auto f) {
+    int mine = 0, base = 0, total = 0, quota = 0;   // (the host bounds the stream's length)
+    // first pass: the tiles of this thread's entries; second: which entry holds a cut
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        int at = base;
         int b = e0 / s.nMT, mt = e0 - b * s.nMT;
         SeqInfo q{0, 0, 0};
+#pragma unroll 1
         for (int e = e0; e < e1; ++e) {
             if (e == e0 || mt == 0) q = sink_seq(s, b, a.status);
-            f(b, mt, key_tiles(s, q, mt).nt);
-            if (++mt == s.nMT) { mt = 0; ++b; }
-        }
-    };
-    long long mine = 0;
-    walk([&](int, int, int nt) { mine += nt; });
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) sb.wsum[warp] = inc;
-    if (tid < 2) sb.pos[tid] = StreamPos{0, 0, 0, 0, 0};
-    __syncthreads();
-    long long base = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) base += sb.wsum[w];
-        total += sb.wsum[w];
-    }
-    base = (base + inc - mine) * s.Hkv;
-    total *= s.Hkv;
-    const long long top = base + mine * s.Hkv;
-    const int workers = 2 * gridDim.x;
-    const long long quota = (total + workers - 1) / workers;
-    // this thread's entries hold positions base .. top - 1 of the stream
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const long long wid = blockIdx.x + (long long)w * gridDim.x;
-        const long long from = wid * quota, to = min(total, from + quota);
-#pragma unroll
-        for (int end = 0; end < 2; ++end) {
-            // the share's first tile, and its end (one past the last tile)
-            const long long x = end ? to : from;
-            if (from >= total) continue;
-            if (x >= total) {
-                if (tid == 0 && end) atomicAdd(&sb.pos[w].left, static_cast<int>(total - from));
-                continue;
-            }
-            if (x < base || x >= top) continue;
-            long long at = base;
-            walk([&](int b, int mt, int nt) {
-                const long long n = (long long)nt * s.Hkv;
-                if (x >= at && x < at + n) {
-                    int h = static_cast<int>((x - at) / nt), j = static_cast<int>((x - at) % nt);
+            const int nt = key_tiles(s, q, mt).nt;
+            if (pass == 0) {
+                mine += nt;
+            } else {
+                const int n = nt * s.Hkv;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    // worker w's share: its first tile (c even) and its end, one past its last tile
+                    const int w = c >> 1;
+                    const int from = static_cast<int>(blockIdx.x + w * gridDim.x) * quota;
+                    const int x = (c & 1) ? min(total, from + quota) : from;
+                    if (x < at || x >= at + n || from >= total) continue;
+                    int h = (x - at) / nt, j = (x - at) - h * nt;
                     const int skip = (a.snap && j > 0) ? nt - j : 0;      // up to the next unit
-                    if (end) {
-                        atomicAdd(&sb.pos[w].left, static_cast<int>(x - from) + skip);
+                    if (c & 1) {
+                        atomicAdd(&sb.pos[w].left, x - from + skip);
                     } else {
                         atomicAdd(&sb.pos[w].left, -skip);
+                        int m2 = mt;
                         if (skip) {
                             j = 0;
-                            if (++h == s.Hkv) { h = 0; ++mt; }           // (the walker skips empty query tiles)
+                            if (++h == s.Hkv) { h = 0; ++m2; }           // (perhaps no query tile of b: passed over later)
                         }
-                        sb.pos[w].b = b; sb.pos[w].mt = mt; sb.pos[w].h = h; sb.pos[w].j = j;
+                        sb.pos[w].b = b; sb.pos[w].mt = m2; sb.pos[w].h = h; sb.pos[w].j = j;
                     }
                 }
                 at += n;
-            });
+            }
+            if (++mt == s.nMT) { mt = 0; ++b; }
+        }
+        if (pass == 0) {
+            int inc = mine;
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            if (lane == 31) sb.wsum[warp] = inc;
+            if (tid < 2) sb.pos[tid] = StreamPos{0, 0, 0, 0, 0};
+            __syncthreads();
+#pragma unroll 1
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) base += sb.wsum[w];
+                total += sb.wsum[w];
+            }
+            base = (base + inc - mine) * s.Hkv;
+            total *= s.Hkv;
+            const int workers = 2 * gridDim.x;
+            quota = (total + workers - 1) / workers;
+            if (tid < 2) {                              // a share that ends with the stream
+                const int from = static_cast<int>(blockIdx.x + tid * gridDim.x) * quota;
+                if (from < total && from + quota >= total) atomicAdd(&sb.pos[tid].left, total - from);
+            }
         }
     }
     __syncthreads();
+}
+
+// The next part of a worker's share (one thread); moves `p` behind it.
+__device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wid) {
+    const SinkSched& s = a.s;
+    Part u{};
+    if (p.left <= 0) return u;
+    SeqInfo q = sink_seq(s, p.b, nullptr);
+    KeyTiles k = key_tiles(s, q, p.mt);
+    while (k.nt == 0 && p.b + 1 < s.B) {
+        ++p.b;
+        p.mt = 0;
+        q = sink_seq(s, p.b, nullptr);
+        k = key_tiles(s, q, 0);
+    }
+    u.b = p.b;
+    u.h = p.h;
+    u.qrow = q.row0 + p.mt * s.TM;
+    u.ntok = min(s.TM, q.n - p.mt * s.TM);
+    u.p0 = k.p0;
+    u.p1 = k.p1;
+    u.end = q.pos0 + q.n;
+    u.k0 = k.k0;
+    u.nsk = k.nsk;
+    u.j0 = p.j;
+    u.j1 = min(k.nt, p.j + p.left);
+    u.slot = u.j0 > 0 ? 2 * wid : (u.j1 < k.nt ? 2 * wid + 1 : -1);
+    if (u.j0 > 0) a.head[wid] = u.j1 < k.nt ? 2 : 1;    // what the join reads
+    if (u.slot == 2 * wid + 1) a.tail[wid] = make_int4(p.b, p.mt, p.h, 1);
+    p.left -= u.j1 - u.j0;
+    p.j = 0;
+    if (++p.h == s.Hkv) { p.h = 0; ++p.mt; }
+    return u;
 }
 
 template <int D>
@@ -201,13 +273,14 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __shared__ Bars<C::STAGES> sb;
     static_assert(C::SMEM + sizeof(Bars<C::STAGES>) <= kSmemMax, "shared memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto wait = [&](uint64_t* bar, uint32_t par) { return tcx::wait_bar(&sb.abort, bar, par, a.status); };
-    // the accesses after a wait are warp-collective: a wait that gave up in one lane does in all
-    auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
+            for (int u = 0; u < kParts; ++u) {
+                mbar_init(&sb.part_full[i][u], 1);
+                mbar_init(&sb.part_empty[i][u], 8);       // both producers, both issuers, 4 softmax warps
+            }
             for (int u = 0; u < 2; ++u) {
                 mbar_init(&sb.q_full[i][u], 1);
                 mbar_init(&sb.q_empty[i][u], 1);
@@ -243,126 +316,153 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = sb.tmem;
 
-    // Walkers start here; one whose snapped start fell behind its sequence's last query tile
-    // moves on to the next unit.
-    auto start = [&](Walker& w, int i) {
-        w.init(sc, sb.pos[i]);
-        while (w.left > 0 && w.k.nt == 0 && w.b + 1 < sc.B) {
-            ++w.b;
-            w.mt = 0;
-            w.s = sink_seq(sc, w.b, nullptr);
-            w.k = key_tiles(sc, w.s, 0);
-        }
-    };
-
+    // Every role takes the two workers' tiles in turn, in the same order: per turn the next
+    // part's record where the last one is used up, then one tile.  A role keeps the
+    // state of the worker at hand and of the other one, and swaps them after each turn:
+    // its code exists once (the instruction cache holds the whole kernel).
     if (warp < 4) {
     setmaxnreg_dec<kRegsCtrl>();
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(&sb.abort, bar, par, a.status); };
+    auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
     if (warp == 0 || warp == 3) {
         // ------------------------------------------------------------ producers (whole warps)
         const bool kl = warp == 0;
-        Walker wk[2];
-        start(wk[0], 0);
-        start(wk[1], 1);
+        struct State {
+            int j, j1, np, pg;                                        // next tile, end; parts taken so far; page of this lane's box
+            bool open;
+        };
+        State cur{0, 0, 0, 0, true}, oth = cur;
         Ring rg{0, 0};
-        int kq[2] = {0, 0};
         uint64_t* full = kl ? sb.k_full : sb.v_full;
         uint64_t* empty = kl ? sb.k_empty : sb.v_empty;
         const CUtensorMap* map = kl ? &tk : &tv;
         uint8_t* ring = sm + (kl ? C::OFF_K : C::OFF_V);
         const int nst = kl ? C::KST : C::VST;
         const int pages = sc.paged ? 128 >> sc.p.page_log2 : 1;       // boxes of a tile, one lane each
-        // page id of this lane's box of the walker's current tile; n_pages (outside the
-        // map: reads as zeros) where no row of the unit sees any of the page
-        auto lookup = [&](const Walker& w) {
-            if (!sc.paged || w.left <= 0 || lane >= pages) return 0;
-            const int c0 = w.k.tile(w.j) * 128 + (lane << sc.p.page_log2);
+        // page id of this lane's box of tile j; n_pages (outside the map: reads as zeros)
+        // where no row of the unit sees any of the page
+        auto lookup = [&](const Part& u) {
+            if (!sc.paged || cur.j >= cur.j1 || lane >= pages) return 0;
+            const int c0 = u.tile(cur.j) * 128 + (lane << sc.p.page_log2);
             const int c1 = c0 + (1 << sc.p.page_log2) - 1;
-            if (c0 > w.k.p1 || (c1 <= w.k.p0 - sc.W && c0 >= sc.ns)) return sc.p.n_pages;
-            int pg = sc.p.table[(size_t)w.b * sc.p.width + (c0 >> sc.p.page_log2)];
+            if (c0 > u.p1 || (c1 <= u.p0 - sc.W && c0 >= sc.ns)) return sc.p.n_pages;
+            int pg = sc.p.table[(size_t)u.b * sc.p.width + (c0 >> sc.p.page_log2)];
             if (pg < 0 || pg >= sc.p.n_pages) {
                 set_status(a.status, GCA_ERR_DEVICE_INDEX);
                 pg = sc.p.n_pages;
             }
             return pg;
         };
-        int pg[2] = {lookup(wk[0]), lookup(wk[1])};
-        bool ok = true;
-        uint32_t used = 0;                                            // stages (bits) and Q buffers in flight at the end
-        while (ok && (wk[0].left > 0 || wk[1].left > 0)) {
-#pragma unroll
+        if (kl && lane == 0)
             for (int i = 0; i < 2; ++i) {
-                Walker& w = wk[i];
-                if (w.left <= 0 || !ok) continue;
-                if (kl && (kq[i] == 0 || w.j == 0)) {                 // first tile of a unit's segment: its Q
-                    const int qb = kq[i] % C::QB;
-                    if (!wwait(&sb.q_empty[i][qb], empty_par(kq[i] / C::QB))) { ok = false; break; }
+                a.head[blockIdx.x + i * gridDim.x] = 0;
+                a.tail[blockIdx.x + i * gridDim.x] = make_int4(0, 0, 0, 0);
+            }
+        uint32_t used = 0;                                            // ring stages ever filled
+        int i = 0;
+#pragma unroll 1
+        for (; cur.open || oth.open; i ^= 1) {
+            if (cur.open && cur.j == cur.j1) {
+                const int r = cur.np % kParts;
+                if (kl) {
+                    if (!wwait(&sb.part_empty[i][r], empty_par(cur.np / kParts))) break;
                     if (lane == 0) {
-                        uint8_t* dst = sm + C::OFF_Q + (i * C::QB + qb) * C::TILE;
-                        mbar_arrive_expect_tx(&sb.q_full[i][qb], C::SUB * a.R * 128);
-#pragma unroll
-                        for (int c = 0; c < C::SUB; ++c)
-                            tma_load_3d(dst + c * C::STILE, &tq, &sb.q_full[i][qb], c * 64, w.h * sc.G,
-                                        w.s.row0 + w.mt * sc.TM);
+                        sb.part[i][r] = next_part(a, sb.pos[i], blockIdx.x + i * gridDim.x);
+                        mbar_arrive(&sb.part_full[i][r]);
                     }
-                    ++kq[i];
+                    __syncwarp();
+                } else if (!wwait(&sb.part_full[i][r], full_par(cur.np / kParts))) {
+                    break;
                 }
-                if (!wwait(&empty[rg.i], rg.ph ^ 1u)) { ok = false; break; }
+                const Part& u = sb.part[i][r];
+                cur.j = u.j0;
+                cur.j1 = u.j1;
+                cur.open = cur.j < cur.j1;
+                if (cur.open) {
+                    if (kl) {                                         // the unit's Q tile
+                        const int qb = cur.np % C::QB;
+                        if (!wwait(&sb.q_empty[i][qb], empty_par(cur.np / C::QB))) break;
+                        if (lane == 0) {
+                            uint8_t* dst = sm + C::OFF_Q + (i * C::QB + qb) * C::TILE;
+                            mbar_arrive_expect_tx(&sb.q_full[i][qb], C::SUB * a.R * 128);
+#pragma unroll
+                            for (int c = 0; c < C::SUB; ++c)
+                                tma_load_3d(dst + c * C::STILE, &tq, &sb.q_full[i][qb], c * 64, u.h * sc.G, u.qrow);
+                        }
+                    }
+                    ++cur.np;
+                    cur.pg = lookup(u);
+                }
+            }
+            if (cur.open) {
+                const Part& u = sb.part[i][(cur.np - 1) % kParts];
+                if (!wwait(&empty[rg.i], rg.ph ^ 1u)) break;
                 if (lane == 0) mbar_arrive_expect_tx(&full[rg.i], C::TILE);
                 __syncwarp();
                 if (lane < pages) {
-                    uint8_t* dst = ring + rg.i * C::TILE;
-                    const int col = w.h * D;
-                    if (sc.paged) {
-                        dst += (lane << sc.p.page_log2) * 128;
+                    uint8_t* dst = ring + rg.i * C::TILE + ((lane << sc.p.page_log2) * (sc.paged ? 128 : 0));
+                    const int y = sc.paged ? 0 : u.tile(cur.j) * 128, z = sc.paged ? cur.pg : u.b;
 #pragma unroll
-                        for (int c = 0; c < C::SUB; ++c)
-                            tma_load_3d(dst + c * C::STILE, map, &full[rg.i], col + c * 64, 0, pg[i]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < C::SUB; ++c)
-                            tma_load_3d(dst + c * C::STILE, map, &full[rg.i], col + c * 64, w.k.tile(w.j) * 128, w.b);
-                    }
+                    for (int c = 0; c < C::SUB; ++c)
+                        tma_load_3d(dst + c * C::STILE, map, &full[rg.i], u.h * D + c * 64, y, z);
                 }
                 used |= 1u << rg.i;
                 rg.next(nst);
-                w.next(sc);
-                pg[i] = lookup(w);                                    // a turn ahead of its use
+                ++cur.j;
+                cur.pg = lookup(u);                                   // a turn ahead of its use
+                if (cur.j == cur.j1) {                                // the record is read no more
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sb.part_empty[i][(cur.np - 1) % kParts]);
+                }
             }
+            const State t = cur;
+            cur = oth;
+            oth = t;
         }
+        const int q_loads[2] = {i == 0 ? cur.np : oth.np, i == 0 ? oth.np : cur.np};
         // no copy may still be writing shared memory when the CTA exits: the last load of
-        // each buffer has completed its current phase
+        // each buffer has completed its current phase (Q's have, where their products ran;
+        // after an abort they are given time)
         if (lane == 0) {
+#pragma unroll 1
             for (int i = 0; i < nst; ++i)
-                if (used >> i & 1u) mbar_wait(&full[i], i < rg.i ? rg.ph : rg.ph ^ 1u, nullptr, 100000000ull);
+                if (used >> i & 1u) wait_copy(&full[i], i < rg.i ? rg.ph : rg.ph ^ 1u);
             if (kl)
-                for (int i = 0; i < 2; ++i)
-                    for (int u = 0; u < C::QB; ++u) {
-                        const int n = (kq[i] - u + C::QB - 1) / C::QB;   // loads into buffer u
-                        if (n > 0) mbar_wait(&sb.q_full[i][u], full_par(n - 1), nullptr, 100000000ull);
-                    }
+#pragma unroll 1
+                for (int i = 0; i < 2 * C::QB; ++i) {
+                    const int w = i / C::QB, q = i % C::QB;
+                    const int n = (q_loads[w] - q + C::QB - 1) / C::QB;      // loads into buffer q
+                    if (n > 0) wait_copy(&sb.q_full[w][q], full_par(n - 1));
+                }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ S issuer
         if (lane == 0) {
-            Walker wk[2];
-            start(wk[0], 0);
-            start(wk[1], 1);
+            struct State {
+                int j, j1, np, ts;
+                bool open;
+            };
+            State cur{0, 0, 0, 0, true}, oth = cur;
             Ring kv{0, 0};
-            int kq[2] = {0, 0}, ts[2] = {0, 0};
-            bool fresh[2] = {true, true};
-            bool issued = false, ok = true;
+            bool issued = false;
             const uint32_t id_s = idesc_bf16(128, 128, false, false);
-            while (ok && (wk[0].left > 0 || wk[1].left > 0)) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    Walker& w = wk[i];
-                    if (w.left <= 0 || !ok) continue;
-                    const int qb = kq[i] % C::QB;
-                    if ((fresh[i] && !wait(&sb.q_full[i][qb], full_par(kq[i] / C::QB))) ||
-                        !wait(&sb.k_full[kv.i], kv.ph) || !wait(&sb.s_empty[i], empty_par(ts[i]))) {
-                        ok = false;
-                        break;
+#pragma unroll 1
+            for (int i = 0; cur.open || oth.open; i ^= 1) {
+                if (cur.open && cur.j == cur.j1) {
+                    const int r = cur.np % kParts;
+                    if (!wait(&sb.part_full[i][r], full_par(cur.np / kParts))) break;
+                    cur.j = sb.part[i][r].j0;
+                    cur.j1 = sb.part[i][r].j1;
+                    mbar_arrive(&sb.part_empty[i][r]);
+                    cur.open = cur.j < cur.j1;
+                    if (cur.open) {
+                        if (!wait(&sb.q_full[i][cur.np % C::QB], full_par(cur.np / C::QB))) break;
+                        ++cur.np;
                     }
+                }
+                if (cur.open) {
+                    const int qb = (cur.np - 1) % C::QB;
+                    if (!wait(&sb.k_full[kv.i], kv.ph) || !wait(&sb.s_empty[i], empty_par(cur.ts))) break;
                     tc_fence_after();
                     const uint32_t qaddr = smem_u32(sm + C::OFF_Q + (i * C::QB + qb) * C::TILE);
                     const uint32_t kaddr = smem_u32(sm + C::OFF_K + kv.i * C::TILE);
@@ -370,41 +470,58 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     mma_commit(&sb.s_full[i]);
                     mma_commit(&sb.k_empty[kv.i]);
                     issued = true;
-                    ++ts[i];
-                    fresh[i] = w.last_tile();
-                    if (fresh[i]) {
-                        mma_commit(&sb.q_empty[i][qb]);
-                        ++kq[i];
-                    }
+                    ++cur.ts;
+                    if (++cur.j == cur.j1) mma_commit(&sb.q_empty[i][qb]);
                     kv.next(C::KST);
-                    w.next(sc);
                 }
+                const State t = cur;
+                cur = oth;
+                oth = t;
             }
             if (issued) {
                 mma_commit(&sb.done);
-                mbar_wait(&sb.done, 0, nullptr, 100000000ull);
+                wait_copy(&sb.done, 0);
             }
         }
     } else {
         // ------------------------------------------------------------ P V issuer (whole warp: it also
         // clears the V rows behind a sequence's last token, whose cache rows may hold anything)
-        Walker wk[2];
-        start(wk[0], 0);
-        start(wk[1], 1);
+        struct State {
+            int j, j1, np, tp, k0, nsk, end;
+            bool open;
+        };
+        State cur{0, 0, 0, 0, 0, 0, 0, true}, oth = cur;
         Ring kv{0, 0};
-        int ko[2] = {0, 0}, tp[2] = {0, 0};
-        bool fresh[2] = {true, true};
-        bool issued = false, ok = true;
+        bool issued = false;
         const uint32_t id_o = idesc_bf16(128, 64, false, true);
-        while (ok && (wk[0].left > 0 || wk[1].left > 0)) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                Walker& w = wk[i];
-                if (w.left <= 0 || !ok) continue;
-                if (!wwait(&sb.v_full[kv.i], kv.ph)) { ok = false; break; }
+#pragma unroll 1
+        for (int i = 0; cur.open || oth.open; i ^= 1) {
+            bool first = false;
+            if (cur.open && cur.j == cur.j1) {
+                const int r = cur.np % kParts;
+                if (!wwait(&sb.part_full[i][r], full_par(cur.np / kParts))) break;
+                const Part& u = sb.part[i][r];
+                cur.j = u.j0;
+                cur.j1 = u.j1;
+                cur.k0 = u.k0;
+                cur.nsk = u.nsk;
+                cur.end = u.end;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sb.part_empty[i][r]);
+                cur.open = cur.j < cur.j1;
+                if (cur.open) {
+                    if (!wwait(&sb.o_empty[i], empty_par(cur.np))) break;
+                    ++cur.np;
+                    first = true;
+                }
+            }
+            if (cur.open) {
+                if (!wwait(&sb.v_full[kv.i], kv.ph)) break;
                 uint8_t* vt = sm + C::OFF_V + kv.i * C::TILE;
-                const int behind = w.s.pos0 + w.s.n - w.k.tile(w.j) * 128;      // first row behind the last token
+                const int kt = cur.j < cur.nsk ? cur.j : cur.k0 + cur.j - cur.nsk;
+                const int behind = cur.end - kt * 128;                  // first row behind the last token
                 if (sc.paged && behind < 128) {
+#pragma unroll 1
                     for (int r = max(behind, 0) * 8 + lane; r < 128 * 8; r += 32)
 #pragma unroll
                         for (int c = 0; c < C::SUB; ++c)
@@ -412,35 +529,38 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if ((fresh[i] && !wwait(&sb.o_empty[i], empty_par(ko[i]))) ||
-                    !wwait(&sb.p_full[i], full_par(tp[i]))) { ok = false; break; }
+                if (!wwait(&sb.p_full[i], full_par(cur.tp))) break;
+                ++cur.j;
                 if (lane == 0) {
                     tc_fence_after();
                     tcx::mma_ts_mn_dh<D, 8>(tmem + C::COL_O + i * D, tmem + C::COL_P + i * C::P_STEP, smem_u32(vt),
-                                            128, id_o, fresh[i] ? 0u : 1u);
+                                            128, id_o, first ? 0u : 1u);
                     mma_commit(&sb.v_empty[kv.i]);
                     mma_commit(&sb.p_empty[i]);
                     if (C::P_OVER_S) mma_commit(&sb.s_empty[i]);
-                    if (w.last_tile()) mma_commit(&sb.o_full[i]);
+                    if (cur.j == cur.j1) mma_commit(&sb.o_full[i]);
                 }
                 issued = true;
-                ++tp[i];
-                fresh[i] = w.last_tile();
-                if (fresh[i]) ++ko[i];
+                ++cur.tp;
                 kv.next(C::VST);
-                w.next(sc);
             }
+            const State t = cur;
+            cur = oth;
+            oth = t;
         }
         if (issued && lane == 0) {
             mma_commit(&sb.done2);
-            mbar_wait(&sb.done2, 0, nullptr, 100000000ull);
+            wait_copy(&sb.done2, 0);
         }
     }
     } else {
         // ------------------------------------------------------------ softmax + epilogue
         setmaxnreg_inc<kRegsSoftmax>();
+        // the accesses after a wait are warp-collective: a wait that gave up in one lane does in all
+        auto wwait = [&](uint64_t* bar, uint32_t par) {
+            return __all_sync(0xffffffffu, tcx::wait_bar(&sb.abort, bar, par, a.status));
+        };
         const int wg = (warp - 4) >> 2;
-        const int wid = blockIdx.x + wg * gridDim.x;
         const int qd = warp & 3;
         const int row = 32 * qd + lane;                 // TMEM lane = query row of the tile
         const int rt = row / sc.G, rg = row - rt * sc.G;
@@ -450,26 +570,31 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const uint32_t tp_addr = tmem + lane_base + C::COL_P + wg * C::P_STEP;
         const float sl = a.scale_log2;
 
-        Walker w;
-        start(w, wg);
-        if (row == 0) {                                 // what the join reads of this worker
-            a.head[wid] = w.left > 0 && w.j > 0 ? (w.left >= w.k.nt - w.j ? 1 : 2) : 0;
-            a.tail[wid] = make_int4(0, 0, 0, 0);
-        }
-        int ts = 0, ko = 0;
-        bool fresh = true;                              // first tile of this worker's part of a unit
+        Part w;
+        w.j0 = w.j1 = 0;
+        int ts = 0, ko = 0, np = 0, j = 0;
+        bool first = true;                              // at the first tile of a part
+        bool have = true, live = false, wlive = false;  // a tile to do; this row exists; some row of the warp does
         float m = -INFINITY, l = 0.f;                   // running max (of s * scale * log2(e)) and sum of exp2(. - m)
-        int j_from = w.j;
         // the finished part whose O still sits in tensor memory
         bool pend = false;
         long long pend_row = -1;                        // token * H + head, or -1: no such row
         int pend_slot = -1;                             // -1: whole unit; else the workspace slot of the part
         float pm = 0.f, pl = 1.f;
         while (true) {
-            const bool have = w.left > 0;
-            // rows of this warp that exist (the others' arithmetic is skipped)
-            const bool live = have && row < a.R && w.mt * sc.TM + rt < w.s.n;
-            const bool wlive = __any_sync(0xffffffffu, live);
+            if (first) {                                // the next part of the share
+                const int r = np % kParts;
+                if (!wwait(&sb.part_full[wg][r], full_par(np / kParts))) break;
+                w = sb.part[wg][r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sb.part_empty[wg][r]);
+                ++np;
+                j = w.j0;
+                have = w.j0 < w.j1;
+                // rows that do not exist are skipped, where a whole warp has no other
+                live = have && row < a.R && rt < w.ntok;
+                wlive = __any_sync(0xffffffffu, live);
+            }
             float alpha = 1.f;
             bool resc = false;
             float x[128];
@@ -492,16 +617,20 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     }
                     tc_fence_before();
                     if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
-                    const int kbase = w.k.tile(w.j) * 128;
+                    const int kbase = w.tile(j) * 128;
                     // every row sees the whole tile, unless the diagonal or the window's edge crosses it
-                    if (kbase + 127 > w.k.p0 || (kbase < w.k.p1 - sc.W + 1 && kbase + 127 >= sc.ns)) {
-                        const int p = w.k.p0 + rt;
-                        const int c_lo = p - sc.W + 1 - kbase;
-                        const int c_s = min(sc.ns, p + 1) - kbase;     // sinks: columns below it
-                        const uint32_t span = static_cast<uint32_t>(sc.W - 1);
+                    if (kbase + 127 > w.p0 || (kbase < w.p1 - sc.W + 1 && kbase + 127 >= sc.ns)) {
+                        // columns c_lo .. c_hi (the window) and those below c_s (sinks), as bits
+                        const int p = w.p0 + rt;
+                        const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase;
+                        const int c_s = min(sc.ns, p + 1) - kbase;
 #pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            x[i] = (static_cast<uint32_t>(i - c_lo) > span && i >= c_s) ? -INFINITY : x[i];
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t vis = (below(c_hi + 1 - 32 * i) & ~below(c_lo - 32 * i)) | below(c_s - 32 * i);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u)
+                                x[32 * i + u] = (vis >> u & 1u) ? x[32 * i + u] : -INFINITY;
+                        }
                         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
@@ -522,7 +651,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
             // the previous part's output leaves after the next one's first maximum, which
             // gives its last P V time to complete
-            if ((fresh || !have) && pend) {
+            if (first && pend) {
                 if (!wwait(&sb.o_full[wg], full_par(ko))) break;
                 tc_fence_after();
                 const bool wr = pend_row >= 0;
@@ -628,20 +757,16 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             tc_fence_before();
             mbar_arrive(&sb.p_full[wg]);
             ++ts;
-            fresh = w.last_tile();
-            if (fresh) {                                // this part of the unit is done: it leaves later
+            first = ++j == w.j1;
+            if (first) {                                // this part of the unit is done: it leaves later
                 pend = true;
-                pend_row = live ? (long long)(w.s.row0 + w.mt * sc.TM + rt) * sc.H + w.h * sc.G + rg : -1;
-                const bool whole_end = w.j + 1 == w.k.nt;
-                pend_slot = j_from > 0 ? 2 * wid : (whole_end ? -1 : 2 * wid + 1);
-                if (pend_slot == 2 * wid + 1 && row == 0) a.tail[wid] = make_int4(w.b, w.mt, w.h, 1);
+                pend_row = live ? (long long)(w.qrow + rt) * sc.H + w.h * sc.G + rg : -1;
+                pend_slot = w.slot;
                 pm = m;
                 pl = l;
                 m = -INFINITY;
                 l = 0.f;
             }
-            w.next(sc);
-            if (fresh) j_from = w.j;
         }
     }
 
@@ -746,6 +871,19 @@ cudaError_t launch(const SinkShape& s, const FwdArgs& a, const CUtensorMap& tq, 
 
 size_t sink_fwd_workspace_bytes(const SinkShape& s) { return layout(s).total; }
 
+bool sink_fwd_supported(const SinkShape& s) {
+    // the kernel counts key tiles and (sequence, query tile) pairs in 32 bits; quota * workers
+    // may pass the total by one share
+    int tm;
+    rows_of_tile(s, &tm);
+    const double nmt = (s.max_q + tm - 1) / tm;
+    const double keys = s.paged ? (double)s.width * s.page : s.L;
+    const double vis = (double)s.W + tm + s.ns;
+    const double tiles = (vis < keys ? vis : keys) / 128 + 3;
+    const double units = s.paged ? (double)s.T / tm + s.B : (double)s.B * nmt;
+    return s.B * nmt < 1e9 && units * s.Hkv * tiles < 1.9e9;
+}
+
 cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, const void* v,
                             const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, void* o,
                             float* lse, void* ws, int* status, cudaStream_t st, int* launches) {
@@ -756,7 +894,7 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     a.s.nMT = (s.max_q + a.s.TM - 1) / a.s.TM;
     a.s.paged = s.paged;
     if (s.paged) a.s.p = PagedArgs{cu_q, kv_len, table, s.T, s.max_q, __builtin_ctz(s.page), s.n_pages, s.width};
-    if ((long long)s.B * a.s.nMT >= (1ll << 30)) return cudaErrorInvalidConfiguration;
+    if (!sink_fwd_supported(s)) return cudaErrorInvalidConfiguration;
     const Layout w = layout(s);
     uint8_t* base = static_cast<uint8_t*>(ws);
     a.part_o = reinterpret_cast<float*>(base + w.o_off);

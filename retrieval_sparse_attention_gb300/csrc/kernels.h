@@ -140,6 +140,7 @@ struct SinkShape {
 };
 constexpr int kNoWindow = 0x40000000;
 
+bool sink_fwd_supported(const SinkShape& s);       // sizes that the kernel's 32-bit counts hold
 size_t sink_fwd_workspace_bytes(const SinkShape& s);
 cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, const void* v,
                             const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, void* o,
