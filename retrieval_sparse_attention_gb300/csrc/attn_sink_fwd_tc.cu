@@ -52,8 +52,8 @@ using tcx::Ring;
 
 constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168;
-constexpr int kRegsCtrl = 88;
-constexpr int kRegsSoftmax = 208;
+constexpr int kRegsCtrl = 72;
+constexpr int kRegsSoftmax = 216;
 static_assert(128 * kRegsCtrl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
 constexpr int kMaxCtas = 152;              // one per SM; the workspace is sized for them
@@ -570,31 +570,28 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const uint32_t tp_addr = tmem + lane_base + C::COL_P + wg * C::P_STEP;
         const float sl = a.scale_log2;
 
-        Part w;
-        w.j0 = w.j1 = 0;
-        int ts = 0, ko = 0, np = 0, j = 0;
+        int ts = 0, ko = 0, np = 0, j = 0, j1 = 0;
         bool first = true;                              // at the first tile of a part
         bool have = true, live = false, wlive = false;  // a tile to do; this row exists; some row of the warp does
         float m = -INFINITY, l = 0.f;                   // running max (of s * scale * log2(e)) and sum of exp2(. - m)
         // the finished part whose O still sits in tensor memory
         bool pend = false;
-        long long pend_row = -1;                        // token * H + head, or -1: no such row
+        int pend_row = -1;                              // token * H + head, or -1: no such row
         int pend_slot = -1;                             // -1: whole unit; else the workspace slot of the part
         float pm = 0.f, pl = 1.f;
         while (true) {
             if (first) {                                // the next part of the share
                 const int r = np % kParts;
                 if (!wwait(&sb.part_full[wg][r], full_par(np / kParts))) break;
-                w = sb.part[wg][r];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sb.part_empty[wg][r]);
                 ++np;
-                j = w.j0;
-                have = w.j0 < w.j1;
+                j = sb.part[wg][r].j0;
+                j1 = sb.part[wg][r].j1;
+                have = j < j1;
                 // rows that do not exist are skipped, where a whole warp has no other
-                live = have && row < a.R && rt < w.ntok;
+                live = have && row < a.R && rt < sb.part[wg][r].ntok;
                 wlive = __any_sync(0xffffffffu, live);
             }
+            const Part& w = sb.part[wg][(np - 1) % kParts];
             float alpha = 1.f;
             bool resc = false;
             float x[128];
@@ -667,7 +664,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             // (an empty row's accumulator holds exact zeros times its zero weights)
 #pragma unroll
                             for (int u = 0; u < 32; ++u) f[u] = __uint_as_float(r[u]);
-                            uint4* dst = reinterpret_cast<uint4*>(a.o + pend_row * D) + 4 * ci;
+                            uint4* dst = reinterpret_cast<uint4*>(a.o + (size_t)pend_row * D) + 4 * ci;
 #pragma unroll
                             for (int u = 0; u < 4; ++u) dst[u] = tcx::pack8(f + 8 * u, inv);
                         } else if (wr) {
@@ -757,11 +754,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             tc_fence_before();
             mbar_arrive(&sb.p_full[wg]);
             ++ts;
-            first = ++j == w.j1;
+            first = ++j == j1;
             if (first) {                                // this part of the unit is done: it leaves later
                 pend = true;
-                pend_row = live ? (long long)(w.qrow + rt) * sc.H + w.h * sc.G + rg : -1;
+                pend_row = live ? (w.qrow + rt) * sc.H + w.h * sc.G + rg : -1;
                 pend_slot = w.slot;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sb.part_empty[wg][(np - 1) % kParts]);
                 pm = m;
                 pl = l;
                 m = -INFINITY;
