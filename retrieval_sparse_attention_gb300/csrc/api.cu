@@ -326,7 +326,7 @@ gca_status_t swa_sink_check(const gca_swa_sink_params_t* p, SinkShape* out) {
     // a window that covers the row hides nothing, and then sinks add nothing
     s.W = p->window < p->L ? p->window : p->L;
     s.ns = s.W < p->L ? (p->sinks < p->L ? p->sinks : p->L) : 0;
-    if (!sink_fwd_supported(s)) return GCA_ERR_UNSUPPORTED;
+    if (!sink_fwd_supported(s) || !sink_bwd_supported(s)) return GCA_ERR_UNSUPPORTED;
     *out = s;
     return GCA_OK;
 }

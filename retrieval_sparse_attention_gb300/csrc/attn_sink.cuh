@@ -6,6 +6,8 @@
 
 #include "common.cuh"
 #include "gca.h"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace gca {
 
@@ -85,5 +87,107 @@ struct StreamPos {
     int b, mt, h, j;
     int left;
 };
+
+// The shares of this CTA (one worker each: worker blockIdx.x + w * gridDim.x, w < SHARES)
+// in a stream of equally long steps: sequence b has entries i < n, entry i takes
+// count(seq(b), i) steps for each of `heads` heads, in the order (b, i, head, step).
+// Every worker gets total / workers steps, rounded up.  All THREADS threads of the
+// CTA take part; ends with __syncthreads.  The host bounds the total below 2^31.
+template <int THREADS, int SHARES, class Seq, class Count>
+__device__ __forceinline__ void find_shares(int B, int n, int heads, int* wsum, StreamPos* pos, Seq seq,
+                                            Count count) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = B * n;                            // entries, a run of them for each thread
+    const int per = (E + THREADS - 1) / THREADS;
+    const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
+    int mine = 0, base = 0, total = 0, quota = 0;
+    // first pass: the steps of this thread's entries; second: which entry holds a cut
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        int at = base;
+        int b = e0 / n, i = e0 - b * n;
+        auto q = seq(min(b, B - 1));
+#pragma unroll 1
+        for (int e = e0; e < e1; ++e) {
+            if (e > e0 && i == 0) q = seq(b);
+            const int c = count(q, i);
+            if (pass == 0) {
+                mine += c;
+            } else {
+                const int len = c * heads;
+#pragma unroll 1
+                for (int k = 0; k < 2 * SHARES; ++k) {
+                    // worker w's share: its first step (k even) and its end, one past its last step
+                    const int w = k >> 1;
+                    const int from = static_cast<int>(blockIdx.x + w * gridDim.x) * quota;
+                    const int x = (k & 1) ? min(total, from + quota) : from;
+                    if (x < at || x >= at + len || from >= total) continue;
+                    if (k & 1) {
+                        atomicAdd(&pos[w].left, x - from);
+                    } else {
+                        const int h = (x - at) / c;
+                        pos[w].b = b; pos[w].mt = i; pos[w].h = h; pos[w].j = x - at - h * c;
+                    }
+                }
+                at += len;
+            }
+            if (++i == n) { i = 0; ++b; }
+        }
+        if (pass == 0) {
+            int inc = mine;
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            if (lane == 31) wsum[warp] = inc;
+            if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0};
+            __syncthreads();
+#pragma unroll 1
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w < warp) base += wsum[w];
+                total += wsum[w];
+            }
+            base = (base + inc - mine) * heads;
+            total *= heads;
+            const int workers = SHARES * gridDim.x;
+            quota = (total + workers - 1) / workers;
+            if (tid < SHARES) {                         // a share that ends with the stream
+                const int from = static_cast<int>(blockIdx.x + tid * gridDim.x) * quota;
+                if (from < total && from + quota >= total) atomicAdd(&pos[tid].left, total - from);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ uint32_t full_par(int k) { return static_cast<uint32_t>(k) & 1u; }
+__device__ __forceinline__ uint32_t empty_par(int k) { return (static_cast<uint32_t>(k) & 1u) ^ 1u; }
+
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// tcx::wait_bar for the control warps, as little code as it takes: gives up after
+// kWaitNs or once another role of the CTA has.
+__device__ __forceinline__ bool wait_ctrl(int* abort_flag, uint64_t* bar, uint32_t parity, int* status) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1; !tc::mbar_try_wait(bar, parity); ++n) {
+        if (n & 63u) continue;
+        const uint64_t t = tc::global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (*((volatile int*)abort_flag)) return false;
+        if (t - t0 > tcx::kWaitNs) {
+            set_status(status, GCA_ERR_TIMEOUT);
+            *((volatile int*)abort_flag) = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// Bounded wait (0.1 s) for work in flight at the end.
+__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) {
+    tc::mbar_wait(bar, parity, nullptr, 100000000ull);
+}
 
 }  // namespace gca

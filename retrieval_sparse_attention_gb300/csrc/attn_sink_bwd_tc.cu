@@ -1,0 +1,1144 @@
+// attn_sink_bwd_tc.cu -- gradients of the windowed attention with sinks on the
+// Blackwell tensor cores (bf16, d = 64 or 128).
+//
+// With p_ts = exp(attn_scale q_t . k_s - lse_t) over V(t) = { s <= t : s > t - W or
+// s < ns }, delta_t = dO_t . o_t and ds_ts = attn_scale p_ts (dO_t . v_s - delta_t):
+//   dQ_t = sum_s ds_ts k_s,   dK_s = sum_t ds_ts q_t,   dV_s = sum_t p_ts dO_t,
+// dK and dV summed over the query heads of the key head.  Four launches:
+//   vectors  -lse log2(e) and -attn_scale delta of every (token, query head), in the
+//            row order of both passes.
+//   pass A   query-major: the forward's 128-row query tiles (tokens x heads of a
+//            group); step = 64 keys: S = Q K^T, dP = dO V^T (M = 128, N = 64), ds over
+//            the columns of S that have been read, dQ += ds K (A from tensor memory).
+//   pass B   key-major: 128 keys of a key head; step = 64 queries of one query head:
+//            S^T = K Q^T, dP^T = V dO^T, dK += ds^T Q, dV += P^T dO (A from tensor
+//            memory).  The steps of an item are the queries whose window reaches its
+//            keys, for each head of the group, and for the items that hold sinks
+//            all later queries as well: those items are many times longer than the others.
+//   join     adds up the parts of the items that were cut.
+// Both passes cut the stream of all their steps into equal shares, one a CTA
+// (attn_sink.cuh), so a sink's long item is spread over as many CTAs as it takes
+// and short problems fill the machine; parts are fp32 sums in the workspace, added in
+// the order of the stream.  No atomics: bitwise reproducible.
+// Within a CTA (12 warps): warp 0 walks the share, writes its parts down as records
+// and loads; warp 1 issues S (pass B: and dP), warp 2 dQ (dK), warp 11 dP (dV), warps 3-10
+// are two math warpgroups that take alternate steps; a thread owns a query row
+// (pass A) or a key row (pass B), a lane of tensor memory, which is the layout of
+// the A operands that it writes.
+#include <math.h>
+
+#include "attn_sink.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.h"
+
+namespace gca {
+namespace {
+
+using namespace tc;
+using tcx::fast_exp2;
+using tcx::kLog2e;
+using tcx::Ring;
+
+constexpr int kThreads = 384;
+constexpr int kMaxCtas = 152;              // one per SM; the workspace is sized for them
+constexpr int kParts = 4;                  // part records in flight
+constexpr int kSmemMax = 232448;
+constexpr uint32_t TMEM_COLS = 512;
+
+struct BwdArgs {
+    SinkSched s;             // query tiles (pass A)
+    int nKT;                 // 128-key tiles a row (pass B)
+    int Lp;                  // L rounded up to 128
+    const __nv_bfloat16 *o, *g;
+    const float* lse;
+    float *nlA, *ndA;        // [B * Hkv * nMT][128]: rows of the query tiles
+    float *nlB, *ndB;        // [B * H][Lp]
+    __nv_bfloat16 *dq, *dk, *dv;
+    float* partA;            // [2 * workers][128][D]
+    float* partB;            // [2 * workers][2][128][D]: dK, dV
+    int4 *tailA, *tailB;     // [workers]: the item (b, i, h, 1) whose first part this worker holds, or .w = 0
+    int *headA, *headB;      // [workers]: 0, 1 (holds the last part of an earlier worker's item), 2 (a middle part)
+    int R;
+    int* status;
+    float scale_log2, scale;
+};
+
+// ============================================================================ vectors
+// A block: 32 tokens x 8 heads; delta from coalesced 16-byte reads, then both layouts.
+// Memory-bound: reads o, dO and lse once.
+template <int D>
+__global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
+    __shared__ float sd[8][33];
+    const SinkSched& sc = a.s;
+    constexpr int LPR = D / 8;                       // lanes a row
+    constexpr int RPW = 32 / LPR;                    // rows (heads) a warp reads at once
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nt = a.Lp / 32;
+    const int b = blockIdx.x / nt, t0 = (blockIdx.x % nt) * 32, h0 = blockIdx.y * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int tl = warp * 4 + i, t = t0 + tl;
+#pragma unroll
+        for (int u = 0; u < 8 / RPW; ++u) {
+            const int hl = u * RPW + lane / LPR, h = h0 + hl;
+            float acc = 0.f;
+            if (t < sc.L && h < sc.H) {
+                const size_t off = (((size_t)b * sc.L + t) * sc.H + h) * D + (lane % LPR) * 8;
+                const uint4 x = *reinterpret_cast<const uint4*>(a.o + off);
+                const uint4 y = *reinterpret_cast<const uint4*>(a.g + off);
+                const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&x);
+                const __nv_bfloat162* hy = reinterpret_cast<const __nv_bfloat162*>(&y);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float2 fx = __bfloat1622float2(hx[v]), fy = __bfloat1622float2(hy[v]);
+                    acc = fmaf(fx.x, fy.x, fmaf(fx.y, fy.y, acc));
+                }
+            }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+            if (lane % LPR == 0) sd[hl][tl] = acc;
+        }
+    }
+    __syncthreads();
+    // thread: token t0 + lane, head h0 + warp
+    const int t = t0 + lane, h = h0 + warp;
+    if (h >= sc.H) return;
+    const bool live = t < sc.L;
+    const float nl = live ? -a.lse[((size_t)b * sc.L + t) * sc.H + h] * kLog2e : 0.f;
+    const float nd = live ? -a.scale * sd[warp][lane] : 0.f;
+    const size_t ib = ((size_t)b * sc.H + h) * a.Lp + t;
+    a.nlB[ib] = nl;
+    a.ndB[ib] = nd;
+    if (live) {
+        const int hk = h / sc.G, mt = t / sc.TM;
+        const size_t ia = (((size_t)b * sc.Hkv + hk) * sc.nMT + mt) * 128 + (t - mt * sc.TM) * sc.G + h - hk * sc.G;
+        a.nlA[ia] = nl;
+        a.ndA[ia] = nd;
+    }
+}
+
+// Rows of an fp32 accumulator (D columns of this thread's lane) to bf16 in global memory.
+template <int D>
+__device__ __forceinline__ void store_rows_bf16(uint32_t taddr, __nv_bfloat16* dst, bool live) {
+#pragma unroll
+    for (int ci = 0; ci < D / 32; ++ci) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(taddr + 32 * ci, r);
+        tmem_wait_ld();
+        if (live) {
+            uint4* d4 = reinterpret_cast<uint4*>(dst) + 4 * ci;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) d4[u] = tcx::pack8u(r + 8 * u);
+        }
+    }
+}
+template <int D>
+__device__ __forceinline__ void store_rows_f32(uint32_t taddr, float* dst, bool live) {
+#pragma unroll
+    for (int ci = 0; ci < D / 32; ++ci) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(taddr + 32 * ci, r);
+        tmem_wait_ld();
+        if (live) {
+            uint4* d4 = reinterpret_cast<uint4*>(dst) + 8 * ci;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) d4[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+        }
+    }
+}
+
+// ============================================================================ pass A (dQ)
+namespace pa {
+
+// 64-key tiles of a query tile: nsk tiles of sinks from tile 0 on, then k0 .. of the window.
+struct Tiles {
+    int k0, nsk, nt;
+};
+__device__ __forceinline__ Tiles tiles(const SinkSched& s, int mt) {
+    Tiles k;
+    const int p0 = mt * s.TM, p1 = min(s.L, p0 + s.TM) - 1;
+    k.k0 = max(0, p0 - s.W + 1) >> 6;
+    k.nsk = min((s.ns + 63) >> 6, k.k0);
+    k.nt = k.nsk + (p1 >> 6) - k.k0 + 1;
+    return k;
+}
+
+struct __align__(16) Part {
+    int b, h, mt, k0, nsk;
+    int j0, j1;              // steps of this part (j0 == j1: the share is done)
+    int slot;                // -1: the whole item; else the workspace slot of its sums
+    __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int SUB = D / 64;
+    static constexpr int STILE = 128 * 128, SKEY = 64 * 128;      // bytes of a sub-tile: 128 rows, 64 rows
+    static constexpr int TILE = SUB * STILE, KTILE = SUB * SKEY;
+    static constexpr int ITEM = 2 * TILE;                         // Q, dO
+    static constexpr int SLOT = 2 * KTILE;                        // K, V
+    static constexpr int IBUF = 2;
+    static constexpr int NSLOT = D == 64 ? 8 : 3;
+    static constexpr int OFF_KV = IBUF * ITEM;
+    static constexpr int OFF_VEC = OFF_KV + NSLOT * SLOT;         // two vectors of 128 floats
+    static constexpr int SMEM = OFF_VEC + 1024 + 1024;
+    static constexpr int NX = 4, NY = 2;                          // 64-column buffers of S (then ds) and of dP
+    static constexpr int NACC = D == 64 ? 2 : 1;
+    static constexpr uint32_t COL_X = 0, COL_Y = NX * 64, COL_ACC = COL_Y + NY * 64;
+    static_assert(COL_ACC + NACC * D <= TMEM_COLS, "tensor memory");
+};
+
+template <class C>
+struct __align__(16) Bars {
+    Part part[kParts];
+    uint64_t part_full[kParts], part_empty[kParts];
+    uint64_t it_full[C::IBUF], it_empty[C::IBUF];
+    uint64_t vec_full, vec_empty;
+    uint64_t kv_full[C::NSLOT], kv_empty[C::NSLOT];
+    uint64_t x_full[C::NX], x_empty[C::NX], y_empty[C::NY];
+    uint64_t p_full[4];
+    uint64_t o_full[2], o_empty[2];      // per storing warpgroup (it sees every phase); per accumulator
+    uint64_t done[3];
+    uint32_t tmem;
+    int abort;
+    StreamPos pos;
+    int wsum[12];
+};
+
+__device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wid) {
+    const SinkSched& s = a.s;
+    Part u{};
+    if (p.left <= 0) return u;
+    const Tiles k = tiles(s, p.mt);
+    u.b = p.b; u.h = p.h; u.mt = p.mt;
+    u.k0 = k.k0; u.nsk = k.nsk;
+    u.j0 = p.j;
+    u.j1 = min(k.nt, p.j + p.left);
+    u.slot = u.j0 > 0 ? 2 * wid : (u.j1 < k.nt ? 2 * wid + 1 : -1);
+    if (u.j0 > 0) a.headA[wid] = u.j1 < k.nt ? 2 : 1;
+    if (u.slot == 2 * wid + 1) a.tailA[wid] = make_int4(p.b, p.mt, p.h, 1);
+    p.left -= u.j1 - u.j0;
+    p.j = 0;
+    if (++p.h == s.Hkv) {
+        p.h = 0;
+        if (++p.mt == s.nMT) { p.mt = 0; ++p.b; }
+    }
+    return u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
+                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                  const BwdArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+    __shared__ Bars<C> sb;
+    static_assert(C::SMEM + sizeof(Bars<C>) <= kSmemMax, "shared memory (pass A)");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(&sb.abort, bar, par, a.status); };
+    const SinkSched& sc = a.s;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(&sb.part_full[i], 1);
+            mbar_init(&sb.part_empty[i], 3 + 8);          // the issuers and the math warps
+        }
+        for (int i = 0; i < C::IBUF; ++i) {
+            mbar_init(&sb.it_full[i], 1);
+            mbar_init(&sb.it_empty[i], 2);                // S and dP issuers
+        }
+        mbar_init(&sb.vec_full, 1);
+        mbar_init(&sb.vec_empty, 256);
+        for (int i = 0; i < C::NSLOT; ++i) {
+            mbar_init(&sb.kv_full[i], 1);
+            mbar_init(&sb.kv_empty[i], 1);
+        }
+        for (int i = 0; i < C::NX; ++i) {
+            mbar_init(&sb.x_full[i], 2);
+            mbar_init(&sb.x_empty[i], 1);
+        }
+        for (int i = 0; i < C::NY; ++i) mbar_init(&sb.y_empty[i], 128);
+        for (int i = 0; i < 4; ++i) mbar_init(&sb.p_full[i], 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sb.o_full[i], 1);
+            mbar_init(&sb.o_empty[i], 128);
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&sb.done[i], 1);
+        sb.abort = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tdo);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sb.tmem, TMEM_COLS);
+        tmem_relinquish();
+    }
+    find_shares<kThreads, 1>(sc.B, sc.nMT, sc.Hkv, sb.wsum, &sb.pos, [](int) { return 0; },
+                             [&](int, int mt) { return tiles(sc, mt).nt; });
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sb.tmem;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ records and loads
+        if (lane == 0) {
+            Ring kv{0, 0};
+            int np = 0;
+            uint32_t used = 0;
+            a.headA[blockIdx.x] = 0;
+            a.tailA[blockIdx.x] = make_int4(0, 0, 0, 0);
+            bool ok = true;
+            while (ok) {
+                const int r = np % kParts, ib = np % C::IBUF;
+                if (!wait(&sb.part_empty[r], empty_par(np / kParts))) break;
+                sb.part[r] = next_part(a, sb.pos, blockIdx.x);
+                mbar_arrive(&sb.part_full[r]);
+                const Part& u = sb.part[r];
+                if (u.j0 == u.j1) break;
+                if (!wait(&sb.it_empty[ib], empty_par(np / C::IBUF)) || !wait(&sb.vec_empty, empty_par(np))) break;
+                uint8_t* it = sm + ib * C::ITEM;
+                mbar_arrive_expect_tx(&sb.vec_full, 1024);
+                mbar_arrive_expect_tx(&sb.it_full[ib], 2 * C::SUB * a.R * 128);
+#pragma unroll
+                for (int c = 0; c < C::SUB; ++c) {
+                    tma_load_4d(it + c * C::STILE, &tq, &sb.it_full[ib], c * 64, u.h * sc.G, u.mt * sc.TM, u.b);
+                    tma_load_4d(it + C::TILE + c * C::STILE, &tdo, &sb.it_full[ib], c * 64, u.h * sc.G, u.mt * sc.TM, u.b);
+                }
+                const size_t vrow = (((size_t)u.b * sc.Hkv + u.h) * sc.nMT + u.mt) * 128;
+                tcx::bulk_load(sm + C::OFF_VEC, a.nlA + vrow, 512, &sb.vec_full);
+                tcx::bulk_load(sm + C::OFF_VEC + 512, a.ndA + vrow, 512, &sb.vec_full);
+                ++np;
+                const int j1 = u.j1;
+#pragma unroll 1
+                for (int j = u.j0; j < j1; ++j) {
+                    if (!wait(&sb.kv_empty[kv.i], kv.ph ^ 1u)) { ok = false; break; }
+                    uint8_t* dst = sm + C::OFF_KV + kv.i * C::SLOT;
+                    mbar_arrive_expect_tx(&sb.kv_full[kv.i], C::SLOT);
+                    const int y = u.tile(j) * 64;
+#pragma unroll
+                    for (int c = 0; c < C::SUB; ++c) {
+                        tma_load_3d(dst + c * C::SKEY, &tk, &sb.kv_full[kv.i], u.h * D + c * 64, y, u.b);
+                        tma_load_3d(dst + C::KTILE + c * C::SKEY, &tv, &sb.kv_full[kv.i], u.h * D + c * 64, y, u.b);
+                    }
+                    used |= 1u << kv.i;
+                    kv.next(C::NSLOT);
+                }
+            }
+            // no copy may still be writing shared memory when the CTA exits
+#pragma unroll 1
+            for (int i = 0; i < C::NSLOT; ++i)
+                if (used >> i & 1u) wait_copy(&sb.kv_full[i], i < kv.i ? kv.ph : kv.ph ^ 1u);
+#pragma unroll 1
+            for (int q = 0; q < C::IBUF; ++q) {
+                const int n = (np - q + C::IBUF - 1) / C::IBUF;
+                if (n > 0) wait_copy(&sb.it_full[q], full_par(n - 1));
+            }
+            if (np > 0) wait_copy(&sb.vec_full, full_par(np - 1));
+        }
+    } else if (warp == 1 || warp == 11) {
+        // ------------------------------------------------------------ warp 1: S = Q K^T, warp 11: dP = dO V^T
+        // (two issuing threads: one alone cannot keep the tensor pipe fed)
+        const bool dpi = warp == 11;
+        if (lane == 0) {
+            Ring kv{0, 0};
+            int u = 0;
+            bool issued = false, ok = true;
+            const uint32_t id_s = idesc_bf16(128, 64, false, false);
+            for (int np = 0; ok; ++np) {
+                const int r = np % kParts, ib = np % C::IBUF;
+                if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
+                const int n = sb.part[r].j1 - sb.part[r].j0;
+                mbar_arrive(&sb.part_empty[r]);
+                if (n == 0) break;
+                if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
+                const uint32_t aaddr = smem_u32(sm + ib * C::ITEM) + (dpi ? C::TILE : 0);
+#pragma unroll 1
+                for (int j = 0; j < n; ++j, ++u) {
+                    const int xs = u % C::NX, ys = u % C::NY;
+                    if (!wait(&sb.kv_full[kv.i], kv.ph) ||
+                        !(dpi ? wait(&sb.y_empty[ys], empty_par(u / C::NY)) : wait(&sb.x_empty[xs], empty_par(u / C::NX)))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t baddr = smem_u32(sm + C::OFF_KV + kv.i * C::SLOT) + (dpi ? C::KTILE : 0);
+                    tcx::mma_kmajor_dh<D>(dpi ? tmem + C::COL_Y + ys * 64 : tmem + C::COL_X + xs * 64, aaddr, 128, baddr,
+                                          64, id_s, 0);
+                    mma_commit(&sb.x_full[xs]);
+                    issued = true;
+                    kv.next(C::NSLOT);
+                }
+                if (ok) mma_commit(&sb.it_empty[ib]);
+            }
+            if (issued) {
+                mma_commit(&sb.done[dpi ? 2 : 0]);
+                wait_copy(&sb.done[dpi ? 2 : 0], 0);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ dQ += ds K (A from tensor memory)
+        if (lane == 0) {
+            Ring kv{0, 0};
+            int u = 0;
+            bool issued = false, ok = true;
+            const uint32_t id_acc = idesc_bf16(128, 64, false, true);
+            for (int np = 0; ok; ++np) {
+                const int r = np % kParts, ob = np % C::NACC;
+                if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
+                const int n = sb.part[r].j1 - sb.part[r].j0;
+                mbar_arrive(&sb.part_empty[r]);
+                if (n == 0) break;
+                if (!wait(&sb.o_empty[ob], empty_par(np / C::NACC))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < n; ++j, ++u) {
+                    const int xs = u % C::NX;
+                    // (the K tile has landed: the S product of this step, before p_full, waited for it)
+                    if (!wait(&sb.p_full[u & 3], full_par(u >> 2))) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t kaddr = smem_u32(sm + C::OFF_KV + kv.i * C::SLOT);
+                    tcx::mma_ts_mn_dh<D, 4>(tmem + C::COL_ACC + ob * D, tmem + C::COL_X + xs * 64, kaddr, 64, id_acc,
+                                            j > 0 ? 1u : 0u);
+                    mma_commit(&sb.x_empty[xs]);
+                    mma_commit(&sb.kv_empty[kv.i]);       // S and dP are complete before ds exists
+                    issued = true;
+                    kv.next(C::NSLOT);
+                }
+                if (ok) mma_commit(&sb.o_full[np & 1]);
+            }
+            if (issued) {
+                mma_commit(&sb.done[1]);
+                wait_copy(&sb.done[1], 0);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ math warpgroups
+        auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
+        const int wg = (warp - 3) >> 2;
+        const int qd = warp & 3;
+        const int row = 32 * qd + lane;               // query row of the tile = lane of tensor memory
+        const int rt = row / sc.G, rg = row - rt * sc.G;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
+        const uint64_t sl2 = tcx::f2_pack(a.scale_log2, a.scale_log2);
+        const uint64_t sc2 = tcx::f2_pack(a.scale, a.scale);
+        int u = 0;
+        // the dQ rows of a part that this warpgroup stores leave after its first step of
+        // the next one, so the wait for the part's last product overlaps work
+        int pend = -1, pend_slot = -1;                // part number; workspace slot or -1
+        int pend_row = -1;                            // token * H + head, or -1: no such row
+        auto epilogue = [&]() {
+            const int ob = pend % C::NACC;
+            if (!wwait(&sb.o_full[pend & 1], full_par(pend >> 1))) return false;
+            tc_fence_after();
+            const uint32_t acc = tmem + lane_base + C::COL_ACC + ob * D;
+            if (pend_slot < 0)
+                store_rows_bf16<D>(acc, a.dq + (size_t)max(pend_row, 0) * D, pend_row >= 0);
+            else
+                store_rows_f32<D>(acc, a.partA + ((size_t)pend_slot * 128 + row) * D, pend_row >= 0);
+            tc_fence_before();
+            mbar_arrive(&sb.o_empty[ob]);
+            pend = -1;
+            return true;
+        };
+        bool ok = true;
+        for (int np = 0; ok; ++np) {
+            const int r = np % kParts;
+            if (!wwait(&sb.part_full[r], full_par(np / kParts))) break;
+            const Part& w = sb.part[r];
+            const int j0 = w.j0, j1 = w.j1, p0 = w.mt * sc.TM;
+            if (j0 == j1) break;
+            if (!wwait(&sb.vec_full, full_par(np))) break;
+            const float* vec = reinterpret_cast<const float*>(sm + C::OFF_VEC);
+            const float nl2 = vec[row], ndsc = vec[128 + row];
+            mbar_arrive(&sb.vec_empty);
+            const uint64_t nl22 = tcx::f2_pack(nl2, nl2), ndsc2 = tcx::f2_pack(ndsc, ndsc);
+            const int p = p0 + rt, plast = min(sc.L, p0 + sc.TM) - 1;
+#pragma unroll 1
+            for (int j = j0; j < j1; ++j, ++u) {
+                if ((u & 1) != wg) continue;
+                const int xs = u % C::NX, ys = u % C::NY;
+                if (!wwait(&sb.x_full[xs], full_par(u / C::NX))) { ok = false; break; }
+                tc_fence_after();
+                const int kbase = w.tile(j) * 64;
+                // every row sees the whole tile, unless the diagonal or the window's edge crosses it
+                const bool edge = kbase + 63 > p0 || (kbase < plast - sc.W + 1 && kbase + 63 >= sc.ns);
+                const uint32_t xb = tmem + lane_base + C::COL_X + xs * 64;
+                const uint32_t yb = tmem + lane_base + C::COL_Y + ys * 64;
+                const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
+#pragma unroll
+                for (int pc = 0; pc < 2; ++pc) {
+                    // keys kbase + 32 pc .. + 31: S (X columns 32 pc ..) and dP (Y columns 32 pc ..)
+                    uint32_t r0[16], r1[16], r2[16], r3[16];
+                    tmem_ld_32x32b_x16(xb + 32 * pc, r0);
+                    tmem_ld_32x32b_x16(xb + 32 * pc + 16, r1);
+                    tmem_ld_32x32b_x16(yb + 32 * pc, r2);
+                    tmem_ld_32x32b_x16(yb + 32 * pc + 16, r3);
+                    tmem_wait_ld();
+                    if (pc == 1) {                                // dP fully read: free its buffer
+                        tc_fence_before();
+                        mbar_arrive(&sb.y_empty[ys]);
+                    }
+                    const uint32_t vis = (below(c_hi + 1 - 32 * pc) & ~below(c_lo - 32 * pc)) | below(c_s - 32 * pc);
+                    uint32_t pk[16];
+                    auto body = [&](bool msk) {
+#pragma unroll
+                        for (int p2 = 0; p2 < 16; ++p2) {
+                            const uint32_t* rs = p2 < 8 ? r0 : r1;
+                            const uint32_t* rd = p2 < 8 ? r2 : r3;
+                            const int tt = 2 * (p2 & 7);
+                            float y0, y1;
+                            tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[tt]), __uint_as_float(rs[tt + 1])),
+                                                      sl2, nl22), y0, y1);
+                            float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
+                            if (msk) {
+                                e0 = (vis >> (2 * p2) & 1u) ? e0 : 0.f;
+                                e1 = (vis >> (2 * p2 + 1) & 1u) ? e1 : 0.f;
+                            }
+                            const uint64_t gd = tcx::ffma2(
+                                tcx::f2_pack(__uint_as_float(rd[tt]), __uint_as_float(rd[tt + 1])), sc2, ndsc2);
+                            pk[p2] = tcx::pack_bf16x2(tcx::fmul2(tcx::f2_pack(e0, e1), gd));
+                        }
+                    };
+                    if (edge) body(true);
+                    else body(false);
+                    tmem_st_32x32b_x16(xb + 16 * pc, pk);         // ds over S columns that have been read
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&sb.p_full[u & 3]);
+                if (pend >= 0 && !epilogue()) { ok = false; break; }
+            }
+            if (!ok) break;
+            if ((np & 1) == wg) {
+                // (a part shorter than two steps may leave this warpgroup's last one pending)
+                if (pend >= 0 && !epilogue()) break;
+                pend = np;
+                pend_slot = w.slot;
+                const bool live = row < a.R && p <= plast;
+                pend_row = live ? (w.b * sc.L + p) * sc.H + w.h * sc.G + rg : -1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sb.part_empty[r]);
+        }
+        if (ok && pend >= 0) epilogue();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+}  // namespace pa
+
+// ============================================================================ pass B (dK, dV)
+namespace pb {
+
+// Query blocks (64 queries) of key tile kt: g0 .. g0 + nw - 1 whose window reaches its
+// keys, and for tiles that hold sinks the nf blocks behind them, up to the row's end.
+struct Blocks {
+    int g0, nw, nf;
+};
+__device__ __forceinline__ Blocks blocks(const SinkSched& s, int kt) {
+    Blocks k;
+    k.g0 = kt * 2;
+    const int end = (s.L - 1) >> 6;
+    const int last = min(s.L - 1, kt * 128 + 127 + s.W - 1) >> 6;
+    k.nw = last - k.g0 + 1;
+    k.nf = kt * 128 < s.ns ? end - last : 0;
+    return k;
+}
+
+struct __align__(16) Part {
+    int b, h, kt;
+    int nw, nf;
+    int j0, j1;              // steps: (query head, window block), then (query head, far block)
+    int slot;
+};
+
+// A step's query head within the group and its query block, counted along.
+struct Step {
+    int g, i, n;             // i-th of n blocks, from block `first` on
+    int first, far_first, nf;
+    __device__ __forceinline__ void init(const Part& u, int G) {
+        const int nwin = G * u.nw;
+        far_first = 2 * u.kt + u.nw;
+        nf = u.nf;
+        if (u.j0 < nwin) {
+            first = 2 * u.kt;
+            n = u.nw;
+            g = u.j0 / n;
+            i = u.j0 - g * n;
+        } else {
+            first = far_first;
+            n = nf;
+            g = (u.j0 - nwin) / n;
+            i = u.j0 - nwin - g * n;
+        }
+    }
+    __device__ __forceinline__ int block() const { return first + i; }
+    __device__ __forceinline__ void next(int G) {
+        if (++i < n) return;
+        i = 0;
+        if (++g < G) return;
+        g = 0;
+        first = far_first;
+        n = nf;
+    }
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int SUB = D / 64;
+    static constexpr int STILE = 128 * 128, SQ = 64 * 128;
+    static constexpr int TILE = SUB * STILE, QTILE = SUB * SQ;
+    static constexpr int ITEM = 2 * TILE;                         // K, V
+    static constexpr int SLOT = 2 * QTILE + 1024;                 // Q, dO, two vectors of 64 floats
+    static constexpr int IBUF = D == 64 ? 2 : 1;
+    static constexpr int NSLOT = D == 64 ? 8 : 4;
+    static constexpr int OFF_ST = IBUF * ITEM;
+    static constexpr int SMEM = OFF_ST + NSLOT * SLOT + 1024;
+    static constexpr int NX = D == 64 ? 4 : 2, NY = 2;
+    static constexpr uint32_t COL_X = 0, COL_Y = NX * 64, COL_ACC = COL_Y + NY * 64;   // dK, dV
+    static_assert(COL_ACC + 2 * D <= TMEM_COLS, "tensor memory");
+};
+
+template <class C>
+struct __align__(16) Bars {
+    Part part[kParts];
+    uint64_t part_full[kParts], part_empty[kParts];
+    uint64_t it_full[C::IBUF], it_empty[C::IBUF];
+    uint64_t st_full[C::NSLOT], st_empty[C::NSLOT];
+    uint64_t x_full[C::NX], x_empty[C::NX], y_empty[C::NY];
+    uint64_t p_full[4];
+    uint64_t o_full[2], o_empty;         // o_full per storing warpgroup: it sees every phase
+    uint64_t done[3];
+    uint32_t tmem;
+    int abort;
+    StreamPos pos;
+    int wsum[12];
+};
+
+__device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wid) {
+    const SinkSched& s = a.s;
+    Part u{};
+    if (p.left <= 0) return u;
+    const Blocks k = blocks(s, p.mt);
+    const int n = s.G * (k.nw + k.nf);
+    u.b = p.b; u.h = p.h; u.kt = p.mt;
+    u.nw = k.nw; u.nf = k.nf;
+    u.j0 = p.j;
+    u.j1 = min(n, p.j + p.left);
+    u.slot = u.j0 > 0 ? 2 * wid : (u.j1 < n ? 2 * wid + 1 : -1);
+    if (u.j0 > 0) a.headB[wid] = u.j1 < n ? 2 : 1;
+    if (u.slot == 2 * wid + 1) a.tailB[wid] = make_int4(p.b, p.mt, p.h, 1);
+    p.left -= u.j1 - u.j0;
+    p.j = 0;
+    if (++p.h == s.Hkv) {
+        p.h = 0;
+        if (++p.mt == a.nKT) { p.mt = 0; ++p.b; }
+    }
+    return u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
+                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const BwdArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+    __shared__ Bars<C> sb;
+    static_assert(C::SMEM + sizeof(Bars<C>) <= kSmemMax, "shared memory (pass B)");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(&sb.abort, bar, par, a.status); };
+    const SinkSched& sc = a.s;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(&sb.part_full[i], 1);
+            mbar_init(&sb.part_empty[i], 3 + 8);          // the issuers and the math warps
+        }
+        for (int i = 0; i < C::IBUF; ++i) {
+            mbar_init(&sb.it_full[i], 1);
+            mbar_init(&sb.it_empty[i], 1);
+        }
+        for (int i = 0; i < C::NSLOT; ++i) {
+            mbar_init(&sb.st_full[i], 1);
+            mbar_init(&sb.st_empty[i], 2);                // the dK and the dV issuer
+        }
+        for (int i = 0; i < C::NX; ++i) {
+            mbar_init(&sb.x_full[i], 1);
+            mbar_init(&sb.x_empty[i], 2);
+        }
+        for (int i = 0; i < C::NY; ++i) mbar_init(&sb.y_empty[i], 128);
+        for (int i = 0; i < 4; ++i) mbar_init(&sb.p_full[i], 128);
+        mbar_init(&sb.o_full[0], 2);
+        mbar_init(&sb.o_full[1], 2);
+        mbar_init(&sb.o_empty, 128);
+        for (int i = 0; i < 3; ++i) mbar_init(&sb.done[i], 1);
+        sb.abort = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tdo);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sb.tmem, TMEM_COLS);
+        tmem_relinquish();
+    }
+    find_shares<kThreads, 1>(sc.B, a.nKT, sc.Hkv, sb.wsum, &sb.pos, [](int) { return 0; }, [&](int, int kt) {
+        const Blocks k = blocks(sc, kt);
+        return sc.G * (k.nw + k.nf);
+    });
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sb.tmem;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ records and loads
+        if (lane == 0) {
+            Ring st{0, 0};
+            int np = 0;
+            uint32_t used = 0;
+            a.headB[blockIdx.x] = 0;
+            a.tailB[blockIdx.x] = make_int4(0, 0, 0, 0);
+            bool ok = true;
+            while (ok) {
+                const int r = np % kParts, ib = np % C::IBUF;
+                if (!wait(&sb.part_empty[r], empty_par(np / kParts))) break;
+                sb.part[r] = next_part(a, sb.pos, blockIdx.x);
+                mbar_arrive(&sb.part_full[r]);
+                const Part& u = sb.part[r];
+                if (u.j0 == u.j1) break;
+                if (!wait(&sb.it_empty[ib], empty_par(np / C::IBUF))) break;
+                uint8_t* it = sm + ib * C::ITEM;
+                mbar_arrive_expect_tx(&sb.it_full[ib], C::ITEM);
+#pragma unroll
+                for (int c = 0; c < C::SUB; ++c) {
+                    tma_load_3d(it + c * C::STILE, &tk, &sb.it_full[ib], u.h * D + c * 64, u.kt * 128, u.b);
+                    tma_load_3d(it + C::TILE + c * C::STILE, &tv, &sb.it_full[ib], u.h * D + c * 64, u.kt * 128, u.b);
+                }
+                ++np;
+                Step sp;
+                sp.init(u, sc.G);
+                const int n = u.j1 - u.j0;
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+                    if (!wait(&sb.st_empty[st.i], st.ph ^ 1u)) { ok = false; break; }
+                    uint8_t* dst = sm + C::OFF_ST + st.i * C::SLOT;
+                    const int qb = sp.block() * 64, h = u.h * sc.G + sp.g;
+                    mbar_arrive_expect_tx(&sb.st_full[st.i], 2 * C::QTILE + 512);
+#pragma unroll
+                    for (int c = 0; c < C::SUB; ++c) {
+                        tma_load_4d(dst + c * C::SQ, &tq, &sb.st_full[st.i], c * 64, h, qb, u.b);
+                        tma_load_4d(dst + C::QTILE + c * C::SQ, &tdo, &sb.st_full[st.i], c * 64, h, qb, u.b);
+                    }
+                    const size_t vrow = ((size_t)u.b * sc.H + h) * a.Lp + qb;
+                    tcx::bulk_load(dst + 2 * C::QTILE, a.nlB + vrow, 256, &sb.st_full[st.i]);
+                    tcx::bulk_load(dst + 2 * C::QTILE + 256, a.ndB + vrow, 256, &sb.st_full[st.i]);
+                    used |= 1u << st.i;
+                    st.next(C::NSLOT);
+                    sp.next(sc.G);
+                }
+            }
+            // no copy may still be writing shared memory when the CTA exits
+#pragma unroll 1
+            for (int i = 0; i < C::NSLOT; ++i)
+                if (used >> i & 1u) wait_copy(&sb.st_full[i], i < st.i ? st.ph : st.ph ^ 1u);
+#pragma unroll 1
+            for (int q = 0; q < C::IBUF; ++q) {
+                const int n = (np - q + C::IBUF - 1) / C::IBUF;
+                if (n > 0) wait_copy(&sb.it_full[q], full_par(n - 1));
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ S^T = K Q^T, dP^T = V dO^T
+        if (lane == 0) {
+            Ring st{0, 0};
+            int u = 0;
+            bool issued = false, ok = true;
+            const uint32_t id_s = idesc_bf16(128, 64, false, false);
+            for (int np = 0; ok; ++np) {
+                const int r = np % kParts, ib = np % C::IBUF;
+                if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
+                const int n = sb.part[r].j1 - sb.part[r].j0;
+                mbar_arrive(&sb.part_empty[r]);
+                if (n == 0) break;
+                if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
+                const uint32_t kaddr = smem_u32(sm + ib * C::ITEM);
+#pragma unroll 1
+                for (int j = 0; j < n; ++j, ++u) {
+                    const int xs = u % C::NX, ys = u % C::NY;
+                    if (!wait(&sb.st_full[st.i], st.ph) || !wait(&sb.x_empty[xs], empty_par(u / C::NX)) ||
+                        !wait(&sb.y_empty[ys], empty_par(u / C::NY))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t qaddr = smem_u32(sm + C::OFF_ST + st.i * C::SLOT);
+                    tcx::mma_kmajor_dh<D>(tmem + C::COL_X + xs * 64, kaddr, 128, qaddr, 64, id_s, 0);
+                    tcx::mma_kmajor_dh<D>(tmem + C::COL_Y + ys * 64, kaddr + C::TILE, 128, qaddr + C::QTILE, 64, id_s, 0);
+                    mma_commit(&sb.x_full[xs]);
+                    issued = true;
+                    st.next(C::NSLOT);
+                }
+                if (ok) mma_commit(&sb.it_empty[ib]);     // K and V are read only by these products
+            }
+            if (issued) {
+                mma_commit(&sb.done[0]);
+                wait_copy(&sb.done[0], 0);
+            }
+        }
+    } else if (warp == 2 || warp == 11) {
+        // ------------------------------------------------------------ warp 2: dK += ds^T Q, warp 11: dV += P^T dO
+        const bool dvi = warp == 11;
+        if (lane == 0) {
+            Ring st{0, 0};
+            int u = 0;
+            bool issued = false, ok = true;
+            const uint32_t id_acc = idesc_bf16(128, 64, false, true);
+            const uint32_t d_acc = tmem + C::COL_ACC + (dvi ? D : 0);
+            for (int np = 0; ok; ++np) {
+                const int r = np % kParts;
+                if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
+                const int n = sb.part[r].j1 - sb.part[r].j0;
+                mbar_arrive(&sb.part_empty[r]);
+                if (n == 0) break;
+                if (!wait(&sb.o_empty, empty_par(np))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < n; ++j, ++u) {
+                    const int xs = u % C::NX;
+                    if (!wait(&sb.p_full[u & 3], full_par(u >> 2))) { ok = false; break; }
+                    tc_fence_after();
+                    // A: K = 16 query steps at X columns 0, 8, 32, 40 (ds^T) and 16, 24, 48, 56 (P^T)
+                    const uint32_t xaddr = smem_u32(sm + C::OFF_ST + st.i * C::SLOT) + (dvi ? C::QTILE : 0);
+                    const uint32_t xa = tmem + C::COL_X + xs * 64 + (dvi ? 16 : 0);
+#pragma unroll
+                    for (int c = 0; c < C::SUB; ++c) {
+                        const uint64_t xd = tcx::desc_head<D>(xaddr + c * C::SQ);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma_bf16_ts(d_acc + c * 64, xa + (ks >> 1) * 32 + (ks & 1) * 8, xd + (uint64_t)(ks * 128),
+                                            id_acc, (ks > 0 || j > 0) ? 1u : 0u);
+                    }
+                    mma_commit(&sb.x_empty[xs]);
+                    mma_commit(&sb.st_empty[st.i]);
+                    issued = true;
+                    st.next(C::NSLOT);
+                }
+                if (ok) mma_commit(&sb.o_full[np & 1]);
+            }
+            if (issued) {
+                mma_commit(&sb.done[dvi ? 2 : 1]);
+                wait_copy(&sb.done[dvi ? 2 : 1], 0);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ math warpgroups
+        auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
+        const int wg = (warp - 3) >> 2;
+        const int qd = warp & 3;
+        const int row = 32 * qd + lane;               // key row of the tile = lane of tensor memory
+        const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
+        const uint64_t sl2 = tcx::f2_pack(a.scale_log2, a.scale_log2);
+        const uint64_t sc2 = tcx::f2_pack(a.scale, a.scale);
+        Ring st{0, 0};
+        int u = 0;
+        bool ok = true;
+        for (int np = 0; ok; ++np) {
+            const int r = np % kParts;
+            if (!wwait(&sb.part_full[r], full_par(np / kParts))) break;
+            const Part& w = sb.part[r];
+            const int n = w.j1 - w.j0;
+            if (n == 0) break;
+            const int s0 = w.kt * 128, s = s0 + row;  // this thread's key
+            Step sp;
+            sp.init(w, sc.G);
+            // the last query that sees key s
+            const int last = min(sc.L - 1, s < sc.ns ? sc.L - 1 : s + sc.W - 1);
+#pragma unroll 1
+            for (int j = 0; j < n; ++j, ++u, st.next(C::NSLOT), sp.next(sc.G)) {
+                if ((u & 1) != wg) continue;
+                const int xs = u % C::NX, ys = u % C::NY;
+                // (x_full: the stage has landed too, so the phase of its barrier is the one meant)
+                if (!wwait(&sb.x_full[xs], full_par(u / C::NX)) || !wwait(&sb.st_full[st.i], st.ph)) { ok = false; break; }
+                tc_fence_after();
+                const int qb = sp.block() * 64;
+                const int c_lo = s - qb, c_hi = last - qb;
+                const uint8_t* vec = sm + C::OFF_ST + st.i * C::SLOT + 2 * C::QTILE;
+                const uint64_t* nl = reinterpret_cast<const uint64_t*>(vec);              // pairs
+                const uint64_t* nd = reinterpret_cast<const uint64_t*>(vec + 256);
+                const uint32_t xb = tmem + lane_base + C::COL_X + xs * 64;
+                const uint32_t yb = tmem + lane_base + C::COL_Y + ys * 64;
+                // does any key of this warp see any query of the block, and every key every query?
+                const bool some = __any_sync(0xffffffffu, c_hi >= 0 && c_lo <= 63 && c_hi >= c_lo);
+                const bool all = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 63);
+                if (!some) {
+                    tc_fence_before();
+                    mbar_arrive(&sb.y_empty[ys]);
+                    const uint32_t z[16] = {};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_st_32x32b_x16(xb + 16 * c, z);
+                } else {
+#pragma unroll
+                    for (int pc = 0; pc < 2; ++pc) {
+                        // queries qb + 32 pc .. + 31 of this key row
+                        uint32_t r0[16], r1[16], r2[16], r3[16];
+                        tmem_ld_32x32b_x16(xb + 32 * pc, r0);
+                        tmem_ld_32x32b_x16(xb + 32 * pc + 16, r1);
+                        tmem_ld_32x32b_x16(yb + 32 * pc, r2);
+                        tmem_ld_32x32b_x16(yb + 32 * pc + 16, r3);
+                        tmem_wait_ld();
+                        if (pc == 1) {
+                            tc_fence_before();
+                            mbar_arrive(&sb.y_empty[ys]);
+                        }
+                        const uint32_t vis = below(c_hi + 1 - 32 * pc) & ~below(c_lo - 32 * pc);
+                        uint32_t pd[16], pp[16];
+                        auto body = [&](bool msk) {
+#pragma unroll
+                            for (int p2 = 0; p2 < 16; ++p2) {
+                                const uint32_t* rs = p2 < 8 ? r0 : r1;
+                                const uint32_t* rd = p2 < 8 ? r2 : r3;
+                                const int tt = 2 * (p2 & 7);
+                                float y0, y1;
+                                tcx::f2_unpack(
+                                    tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[tt]), __uint_as_float(rs[tt + 1])), sl2,
+                                               nl[16 * pc + p2]), y0, y1);
+                                float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
+                                if (msk) {
+                                    e0 = (vis >> (2 * p2) & 1u) ? e0 : 0.f;
+                                    e1 = (vis >> (2 * p2 + 1) & 1u) ? e1 : 0.f;
+                                }
+                                const uint64_t ev = tcx::f2_pack(e0, e1);
+                                const uint64_t gd = tcx::ffma2(
+                                    tcx::f2_pack(__uint_as_float(rd[tt]), __uint_as_float(rd[tt + 1])), sc2,
+                                    nd[16 * pc + p2]);
+                                pd[p2] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
+                                pp[p2] = tcx::pack_bf16x2(ev);
+                            }
+                        };
+                        if (all) body(false);
+                        else body(true);
+                        // ds^T, then P^T, over the 32 S^T columns just read
+                        tmem_st_32x32b_x16(xb + 32 * pc, pd);
+                        tmem_st_32x32b_x16(xb + 32 * pc + 16, pp);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&sb.p_full[u & 3]);
+            }
+            if (!ok) break;
+            if ((np & 1) == wg) {                     // this part's sums of key s
+                if (!wwait(&sb.o_full[wg], full_par(np >> 1))) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + lane_base + C::COL_ACC;
+                const bool live = s < sc.L;
+                if (w.slot < 0) {
+                    const size_t orow = ((size_t)(w.b * sc.L + min(s, sc.L - 1)) * sc.Hkv + w.h) * D;
+                    store_rows_bf16<D>(acc, a.dk + orow, live);
+                    store_rows_bf16<D>(acc + D, a.dv + orow, live);
+                } else {
+                    float* dst = a.partB + ((size_t)w.slot * 256 + row) * D;
+                    store_rows_f32<D>(acc, dst, live);
+                    store_rows_f32<D>(acc + D, dst + 128 * D, live);
+                }
+                tc_fence_before();
+                mbar_arrive(&sb.o_empty);             // the next part may accumulate now
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sb.part_empty[r]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+}  // namespace pb
+
+// Adds up the parts of the items that were cut, in the order of the stream: block w the
+// item that begins in worker w's share and goes on in the next ones (pass A for
+// blockIdx.y = 0, pass B's dK and dV for 1 and 2).
+template <int D>
+__global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int workers) {
+    const SinkSched& sc = a.s;
+    const bool pass_a = blockIdx.y == 0;
+    const int w = blockIdx.x;
+    const int4 it = (pass_a ? a.tailA : a.tailB)[w];
+    if (it.w == 0) return;
+    const int* head = pass_a ? a.headA : a.headB;
+    int n = 1;
+    while (w + n < workers) {
+        const int h = head[w + n];
+        ++n;
+        if (h != 2) break;
+    }
+    constexpr int VEC = D / 4;
+    const size_t slot_rows = pass_a ? 128 : 256;
+    const float* base = pass_a ? a.partA : a.partB + (blockIdx.y == 2 ? 128 * D : 0);
+    const int rows = pass_a ? a.R : 128;
+    for (int i = threadIdx.x; i < rows * VEC; i += blockDim.x) {
+        const int row = i / VEC, c = i % VEC;
+        size_t orow;
+        if (pass_a) {
+            const int rt = row / sc.G, t = it.y * sc.TM + rt;
+            if (t >= sc.L) continue;
+            orow = (size_t)(it.x * sc.L + t) * sc.H + it.z * sc.G + (row - rt * sc.G);
+        } else {
+            const int s = it.y * 128 + row;
+            if (s >= sc.L) continue;
+            orow = (size_t)(it.x * sc.L + s) * sc.Hkv + it.z;
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < n; ++k) {
+            const size_t slot = k == 0 ? 2 * w + 1 : 2 * (w + k);
+            const float4 x = reinterpret_cast<const float4*>(base + (slot * slot_rows + row) * D)[c];
+            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+        }
+        __nv_bfloat16* dst = pass_a ? a.dq : blockIdx.y == 1 ? a.dk : a.dv;
+        reinterpret_cast<uint2*>(dst + orow * D)[c] =
+            make_uint2(tcx::pack_bf16(acc.x, acc.y), tcx::pack_bf16(acc.z, acc.w));
+    }
+}
+
+struct Layout {
+    size_t nlA, ndA, nlB, ndB, partA, partB, tailA, tailB, headA, headB, total;
+    int TM, R, nMT, Lp;
+};
+Layout layout(const SinkShape& s) {
+    Layout w;
+    const int G = s.H / s.Hkv;
+    w.TM = 128 / G < s.L ? 128 / G : s.L;
+    w.R = w.TM * G;
+    w.nMT = (s.L + w.TM - 1) / w.TM;
+    w.Lp = (s.L + 127) / 128 * 128;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    const size_t va = (size_t)s.B * s.Hkv * w.nMT * 128 * 4, vb = (size_t)s.B * s.H * w.Lp * 4;
+    w.nlA = take(va);
+    w.ndA = take(va);
+    w.nlB = take(vb);
+    w.ndB = take(vb);
+    w.partA = take((size_t)2 * kMaxCtas * 128 * s.d * 4);
+    w.partB = take((size_t)2 * kMaxCtas * 256 * s.d * 4);
+    w.tailA = take(kMaxCtas * 16);
+    w.tailB = take(kMaxCtas * 16);
+    w.headA = take(kMaxCtas * 4);
+    w.headB = take(kMaxCtas * 4);
+    w.total = at;
+    return w;
+}
+
+template <int D>
+cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[8], int grid, cudaStream_t st,
+                   int* launches) {
+    cudaError_t e;
+    const dim3 vgrid((unsigned)(s.B * (a.Lp / 32)), (unsigned)((s.H + 7) / 8));
+    GCA_LAUNCH("sink_bwd_vec", st, sink_bwd_vec_kernel<D><<<vgrid, 256, 0, st>>>(a));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(pa::sink_bwd_q_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  pa::Cfg<D>::SMEM)) != cudaSuccess)
+        return e;
+    GCA_LAUNCH("sink_bwd_q", st,
+               pa::sink_bwd_q_kernel<D><<<grid, kThreads, pa::Cfg<D>::SMEM, st>>>(m[0], m[1], m[2], m[3], a));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  pb::Cfg<D>::SMEM)) != cudaSuccess)
+        return e;
+    GCA_LAUNCH("sink_bwd_kv", st,
+               pb::sink_bwd_kv_kernel<D><<<grid, kThreads, pb::Cfg<D>::SMEM, st>>>(m[4], m[5], m[6], m[7], a));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    GCA_LAUNCH("sink_bwd_join", st, sink_bwd_join_kernel<D><<<dim3(grid, 3), 256, 0, st>>>(a, grid));
+    if ((e = cudaGetLastError()) == cudaSuccess) *launches += 4;
+    return e;
+}
+
+}  // namespace
+
+bool sink_bwd_supported(const SinkShape& s) {
+    // key-major steps counted in 32 bits
+    const double nkt = (s.L + 127) / 128, nb = nkt * 2;
+    const double win = (s.W + 127.0) / 64 + 2;
+    const double sinks = (s.ns + 127) / 128;
+    const double steps = nkt * (win < nb ? win : nb) + sinks * nb;
+    return (double)s.B * s.H * steps < 1.9e9 && (double)s.B * nkt * 4 < 2e9;
+}
+
+size_t sink_bwd_workspace_bytes(const SinkShape& s) { return layout(s).total; }
+
+cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, const void* v,
+                            const void* o, const float* lse, const void* dout, void* dq, void* dk,
+                            void* dv, void* ws, int* status, cudaStream_t st, int* launches) {
+    const Layout w = layout(s);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    BwdArgs a{};
+    a.s.B = s.B; a.s.L = s.L; a.s.H = s.H; a.s.Hkv = s.Hkv; a.s.G = s.H / s.Hkv;
+    a.s.W = s.W; a.s.ns = s.ns;
+    a.s.TM = w.TM;
+    a.s.nMT = w.nMT;
+    a.R = w.R;
+    a.nKT = w.Lp / 128;
+    a.Lp = w.Lp;
+    a.o = static_cast<const __nv_bfloat16*>(o);
+    a.g = static_cast<const __nv_bfloat16*>(dout);
+    a.lse = lse;
+    a.nlA = reinterpret_cast<float*>(base + w.nlA);
+    a.ndA = reinterpret_cast<float*>(base + w.ndA);
+    a.nlB = reinterpret_cast<float*>(base + w.nlB);
+    a.ndB = reinterpret_cast<float*>(base + w.ndB);
+    a.dq = static_cast<__nv_bfloat16*>(dq);
+    a.dk = static_cast<__nv_bfloat16*>(dk);
+    a.dv = static_cast<__nv_bfloat16*>(dv);
+    a.partA = reinterpret_cast<float*>(base + w.partA);
+    a.partB = reinterpret_cast<float*>(base + w.partB);
+    a.tailA = reinterpret_cast<int4*>(base + w.tailA);
+    a.tailB = reinterpret_cast<int4*>(base + w.tailB);
+    a.headA = reinterpret_cast<int*>(base + w.headA);
+    a.headB = reinterpret_cast<int*>(base + w.headB);
+    a.status = status;
+    a.scale = s.scale;
+    a.scale_log2 = s.scale * kLog2e;
+    const uint64_t d = s.d, H = s.H, L = s.L, B = s.B, kvcols = (uint64_t)s.Hkv * s.d;
+    const uint64_t qn[4] = {d, H, L, B};
+    const uint64_t qs[3] = {d, (uint64_t)s.q_stride, (uint64_t)s.q_stride * L}, gs[3] = {d, H * d, H * d * L};
+    const uint32_t boxa[3] = {(uint32_t)a.s.G, (uint32_t)a.s.TM, 1}, boxb[3] = {1, 64, 1};
+    CUtensorMap m[8];
+    bool ok = encode_bf16_4d(&m[0], q, qn, qs, boxa) && encode_bf16_4d(&m[1], dout, qn, gs, boxa) &&
+              encode_bf16_4d(&m[4], q, qn, qs, boxb) && encode_bf16_4d(&m[5], dout, qn, gs, boxb);
+    for (int i = 0; i < 2; ++i)
+        ok = ok && encode_bf16_3d(&m[2 + 4 * i], k, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1) &&
+             encode_bf16_3d(&m[3 + 4 * i], v, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1);
+    if (!ok) return cudaErrorInvalidValue;
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+    return s.d == 64 ? launch<64>(s, a, m, grid, st, launches) : launch<128>(s, a, m, grid, st, launches);
+}
+
+}  // namespace gca

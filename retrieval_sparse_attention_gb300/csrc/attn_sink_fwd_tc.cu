@@ -91,7 +91,6 @@ struct FwdArgs {
     int4* tail;              // [workers]: unit (b, mt, h, 1) whose first part this worker holds, or .w = 0
     int* head;               // [workers]: 0, 1 (holds the last part of an earlier worker's unit), 2 (a middle part)
     int R;                   // rows of a query tile: TM * G
-    int snap;                // cut the stream only between units
     int* status;
     float scale_log2;
 };
@@ -123,111 +122,6 @@ struct __align__(16) Bars {
     StreamPos pos[2];
     int wsum[12];
 };
-
-__device__ __forceinline__ uint32_t full_par(int k) { return static_cast<uint32_t>(k) & 1u; }
-__device__ __forceinline__ uint32_t empty_par(int k) { return (static_cast<uint32_t>(k) & 1u) ^ 1u; }
-
-// The lowest n bits (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
-
-// tcx::wait_bar for the control warps, as little code as it takes: gives up after
-// kWaitNs or once another role of the CTA has.
-__device__ __forceinline__ bool wait_ctrl(int* abort_flag, uint64_t* bar, uint32_t parity, int* status) {
-    uint64_t t0 = 0;
-#pragma unroll 1
-    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-        if (n & 63u) continue;
-        const uint64_t t = global_timer_ns();
-        if (t0 == 0) t0 = t;
-        if (*((volatile int*)abort_flag)) return false;
-        if (t - t0 > tcx::kWaitNs) {
-            set_status(status, GCA_ERR_TIMEOUT);
-            *((volatile int*)abort_flag) = 1;
-            return false;
-        }
-    }
-    return true;
-}
-// Bounded wait (0.1 s) for work in flight at the end.
-__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) {
-    mbar_wait(bar, parity, nullptr, 100000000ull);
-}
-
-// The CTA's two shares of the stream of key tiles (see StreamPos).  All threads take part.
-template <typename B>
-__device__ __forceinline__ void find_shares(const FwdArgs& a, B& sb) {
-    const SinkSched& s = a.s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int E = s.B * s.nMT;                      // entries e = b * nMT + mt, a run of them for each thread
-    const int per = (E + kThreads - 1) / kThreads;
-    const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
-    int mine = 0, base = 0, total = 0, quota = 0;   // (the host bounds the stream's length)
-    // first pass: the tiles of this thread's entries; second: which entry holds a cut
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        int at = base;
-        int b = e0 / s.nMT, mt = e0 - b * s.nMT;
-        SeqInfo q{0, 0, 0};
-#pragma unroll 1
-        for (int e = e0; e < e1; ++e) {
-            if (e == e0 || mt == 0) q = sink_seq(s, b, a.status);
-            const int nt = key_tiles(s, q, mt).nt;
-            if (pass == 0) {
-                mine += nt;
-            } else {
-                const int n = nt * s.Hkv;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    // worker w's share: its first tile (c even) and its end, one past its last tile
-                    const int w = c >> 1;
-                    const int from = static_cast<int>(blockIdx.x + w * gridDim.x) * quota;
-                    const int x = (c & 1) ? min(total, from + quota) : from;
-                    if (x < at || x >= at + n || from >= total) continue;
-                    int h = (x - at) / nt, j = (x - at) - h * nt;
-                    const int skip = (a.snap && j > 0) ? nt - j : 0;      // up to the next unit
-                    if (c & 1) {
-                        atomicAdd(&sb.pos[w].left, x - from + skip);
-                    } else {
-                        atomicAdd(&sb.pos[w].left, -skip);
-                        int m2 = mt;
-                        if (skip) {
-                            j = 0;
-                            if (++h == s.Hkv) { h = 0; ++m2; }           // (perhaps no query tile of b: passed over later)
-                        }
-                        sb.pos[w].b = b; sb.pos[w].mt = m2; sb.pos[w].h = h; sb.pos[w].j = j;
-                    }
-                }
-                at += n;
-            }
-            if (++mt == s.nMT) { mt = 0; ++b; }
-        }
-        if (pass == 0) {
-            int inc = mine;
-#pragma unroll 1
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += x;
-            }
-            if (lane == 31) sb.wsum[warp] = inc;
-            if (tid < 2) sb.pos[tid] = StreamPos{0, 0, 0, 0, 0};
-            __syncthreads();
-#pragma unroll 1
-            for (int w = 0; w < kThreads / 32; ++w) {
-                if (w < warp) base += sb.wsum[w];
-                total += sb.wsum[w];
-            }
-            base = (base + inc - mine) * s.Hkv;
-            total *= s.Hkv;
-            const int workers = 2 * gridDim.x;
-            quota = (total + workers - 1) / workers;
-            if (tid < 2) {                              // a share that ends with the stream
-                const int from = static_cast<int>(blockIdx.x + tid * gridDim.x) * quota;
-                if (from < total && from + quota >= total) atomicAdd(&sb.pos[tid].left, total - from);
-            }
-        }
-    }
-    __syncthreads();
-}
 
 // The next part of a worker's share (one thread); moves `p` behind it.
 __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wid) {
@@ -310,7 +204,9 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares(a, sb);
+    find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, sb.wsum, sb.pos,
+                             [&](int b) { return sink_seq(sc, b, a.status); },
+                             [&](const SeqInfo& q, int mt) { return key_tiles(sc, q, mt).nt; });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -860,7 +756,6 @@ cudaError_t launch(const SinkShape& s, const FwdArgs& a, const CUtensorMap& tq, 
     GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *launches += 1;
-    if (a.snap) return e;
     GCA_LAUNCH("sink_join", st, sink_join_kernel<D><<<2 * grid, 256, 0, st>>>(a, 2 * grid));
     if ((e = cudaGetLastError()) == cudaSuccess) *launches += 1;
     return e;

@@ -145,6 +145,7 @@ size_t sink_fwd_workspace_bytes(const SinkShape& s);
 cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, const void* v,
                             const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, void* o,
                             float* lse, void* ws, int* status, cudaStream_t st, int* launches);
+bool sink_bwd_supported(const SinkShape& s);
 size_t sink_bwd_workspace_bytes(const SinkShape& s);
 cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, const void* v,
                             const void* o, const float* lse, const void* dout, void* dq, void* dk,

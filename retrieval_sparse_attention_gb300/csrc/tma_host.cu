@@ -81,6 +81,21 @@ bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1
     return r == CUDA_SUCCESS;
 }
 
+bool encode_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&n)[4], const uint64_t (&stride)[3],
+                    const uint32_t (&box)[3]) {
+    std::call_once(g_once, resolve);
+    if (!g_encode) return false;
+    cuuint64_t dims[4] = {n[0], n[1], n[2], n[3]};
+    cuuint64_t strides[3] = {stride[0] * 2, stride[1] * 2, stride[2] * 2};
+    cuuint32_t bx[4] = {64, box[0], box[1], box[2]};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                          strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool encode_f32_box(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_elems,
                     uint32_t box_cols, uint32_t box_rows) {
     std::call_once(g_once, resolve);
