@@ -86,10 +86,11 @@ __device__ __forceinline__ KeyTiles key_tiles(const SinkSched& a, const SeqInfo&
 struct StreamPos {
     int b, mt, h, j;
     int left;
+    int wid;             // the worker's number, in the order of the stream
 };
 
-// The shares of this CTA (one worker each: worker blockIdx.x + w * gridDim.x, w < SHARES)
-// in a stream of equally long steps: sequence b has entries i < n, entry i takes
+// The shares of this CTA (SHARES workers, neighbours in the stream; where there are
+// fewer steps than CTAs, each CTA has one worker with a share at most) in a stream of equally long steps: sequence b has entries i < n, entry i takes
 // count(seq(b), i) steps for each of `heads` heads, in the order (b, i, head, step).
 // Every worker gets total / workers steps, rounded up.  All THREADS threads of the
 // CTA take part; ends with __syncthreads.  The host bounds the total below 2^31.
@@ -101,6 +102,10 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, int* wsum, 
     const int per = (E + THREADS - 1) / THREADS;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
     int mine = 0, base = 0, total = 0, quota = 0;
+    auto wid = [&](int w) {
+        return total <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x + w * gridDim.x)
+                                                    : static_cast<int>(blockIdx.x) * SHARES + w;
+    };
     // first pass: the steps of this thread's entries; second: which entry holds a cut
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -119,7 +124,7 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, int* wsum, 
                 for (int k = 0; k < 2 * SHARES; ++k) {
                     // worker w's share: its first step (k even) and its end, one past its last step
                     const int w = k >> 1;
-                    const int from = static_cast<int>(blockIdx.x + w * gridDim.x) * quota;
+                    const int from = wid(w) * quota;
                     const int x = (k & 1) ? min(total, from + quota) : from;
                     if (x < at || x >= at + len || from >= total) continue;
                     if (k & 1) {
@@ -141,7 +146,7 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, int* wsum, 
                 if (lane >= o) inc += x;
             }
             if (lane == 31) wsum[warp] = inc;
-            if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0};
+            if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0};
             __syncthreads();
 #pragma unroll 1
             for (int w = 0; w < THREADS / 32; ++w) {
@@ -153,7 +158,8 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, int* wsum, 
             const int workers = SHARES * gridDim.x;
             quota = (total + workers - 1) / workers;
             if (tid < SHARES) {                         // a share that ends with the stream
-                const int from = static_cast<int>(blockIdx.x + tid * gridDim.x) * quota;
+                const int from = wid(tid) * quota;
+                pos[tid].wid = wid(tid);
                 if (from < total && from + quota >= total) atomicAdd(&pos[tid].left, total - from);
             }
         }
@@ -188,6 +194,50 @@ __device__ __forceinline__ bool wait_ctrl(int* abort_flag, uint64_t* bar, uint32
 // Bounded wait (0.1 s) for work in flight at the end.
 __device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) {
     tc::mbar_wait(bar, parity, nullptr, 100000000ull);
+}
+
+// 32 fp32 columns of this lane's row of an accumulator, times `scale`, as bf16 to global
+// memory: row `row` of `out` (rows of ld elements; row < 0: none), columns col .. + 31.
+// Four lanes exchange their rows' 16-byte pieces, so that each store writes 64
+// consecutive bytes of a row (with a row per lane the 32 lanes of a store touch 32
+// lines, and the stores of a tile cost as much as half a key tile).
+__device__ __forceinline__ void store_row32(uint32_t taddr, __nv_bfloat16* out, int ld, int col, int row, float scale) {
+    const int lane = threadIdx.x & 31;
+    uint32_t q[4][4];
+    {
+        uint32_t r[32];
+        tc::tmem_ld_32x32b_x32(taddr, r);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                q[c][u] = tcx::pack_bf16(__uint_as_float(r[8 * c + 2 * u]) * scale,
+                                         __uint_as_float(r[8 * c + 2 * u + 1]) * scale);
+    }
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c & s) continue;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t give = up ? q[c][u] : q[c + s][u];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
+                if (up) q[c][u] = got;
+                else q[c + s][u] = got;
+            }
+        }
+    }
+    // lane 4 g + i now holds piece i of the rows of lanes 4 g .. 4 g + 3
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int rk = __shfl_sync(0xffffffffu, row, (lane & 28) + k);
+        if (rk >= 0)
+            *reinterpret_cast<uint4*>(out + (size_t)rk * ld + col + 8 * (lane & 3)) =
+                make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
+    }
 }
 
 }  // namespace gca

@@ -120,20 +120,12 @@ __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     }
 }
 
-// Rows of an fp32 accumulator (D columns of this thread's lane) to bf16 in global memory.
+// The D columns of this lane's row of an fp32 accumulator to global memory, as bf16 (row
+// < 0: none) or as they are.
 template <int D>
-__device__ __forceinline__ void store_rows_bf16(uint32_t taddr, __nv_bfloat16* dst, bool live) {
+__device__ __forceinline__ void store_rows_bf16(uint32_t taddr, __nv_bfloat16* out, int row) {
 #pragma unroll
-    for (int ci = 0; ci < D / 32; ++ci) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(taddr + 32 * ci, r);
-        tmem_wait_ld();
-        if (live) {
-            uint4* d4 = reinterpret_cast<uint4*>(dst) + 4 * ci;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) d4[u] = tcx::pack8u(r + 8 * u);
-        }
-    }
+    for (int ci = 0; ci < D / 32; ++ci) store_row32(taddr + 32 * ci, out, D, 32 * ci, row, 1.f);
 }
 template <int D>
 __device__ __forceinline__ void store_rows_f32(uint32_t taddr, float* dst, bool live) {
@@ -441,7 +433,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             tc_fence_after();
             const uint32_t acc = tmem + lane_base + C::COL_ACC + ob * D;
             if (pend_slot < 0)
-                store_rows_bf16<D>(acc, a.dq + (size_t)max(pend_row, 0) * D, pend_row >= 0);
+                store_rows_bf16<D>(acc, a.dq, pend_row);
             else
                 store_rows_f32<D>(acc, a.partA + ((size_t)pend_slot * 128 + row) * D, pend_row >= 0);
             tc_fence_before();
@@ -952,9 +944,9 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 const uint32_t acc = tmem + lane_base + C::COL_ACC;
                 const bool live = s < sc.L;
                 if (w.slot < 0) {
-                    const size_t orow = ((size_t)(w.b * sc.L + min(s, sc.L - 1)) * sc.Hkv + w.h) * D;
-                    store_rows_bf16<D>(acc, a.dk + orow, live);
-                    store_rows_bf16<D>(acc + D, a.dv + orow, live);
+                    const int orow = live ? (w.b * sc.L + s) * sc.Hkv + w.h : -1;
+                    store_rows_bf16<D>(acc, a.dk, orow);
+                    store_rows_bf16<D>(acc + D, a.dv, orow);
                 } else {
                     float* dst = a.partB + ((size_t)w.slot * 256 + row) * D;
                     store_rows_f32<D>(acc, dst, live);

@@ -102,9 +102,11 @@ struct __align__(16) Part {
     int k0, nsk;             // key tile j is j (j < nsk) or k0 + j - nsk
     int j0, j1;
     int slot;                // -1: the whole unit; else the workspace slot of its sums
+    int nar;                 // key tiles j < nar (one or none) are narrow: 32 columns hold all sinks
     __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
 };
 constexpr int kParts = 4;    // records a worker
+constexpr int kNarrow = 32;  // sinks up to here take a tile of this width, a fifth of a full tile's time
 
 template <int STAGES>
 struct __align__(16) Bars {
@@ -123,8 +125,10 @@ struct __align__(16) Bars {
     int wsum[12];
 };
 
-// The next part of a worker's share (one thread); moves `p` behind it.
-__device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wid) {
+// The next part of a share (one thread); moves `p` behind it.  A part that began in an
+// earlier share goes to worker wid's first slot, one that goes on in a later share to
+// the second slot of worker wid_tail.
+__device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wid_tail) {
     const SinkSched& s = a.s;
     Part u{};
     if (p.left <= 0) return u;
@@ -147,9 +151,10 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     u.nsk = k.nsk;
     u.j0 = p.j;
     u.j1 = min(k.nt, p.j + p.left);
-    u.slot = u.j0 > 0 ? 2 * wid : (u.j1 < k.nt ? 2 * wid + 1 : -1);
-    if (u.j0 > 0) a.head[wid] = u.j1 < k.nt ? 2 : 1;    // what the join reads
-    if (u.slot == 2 * wid + 1) a.tail[wid] = make_int4(p.b, p.mt, p.h, 1);
+    u.nar = k.nsk == 1 && s.ns <= kNarrow;
+    u.slot = u.j0 > 0 ? 2 * p.wid : (u.j1 < k.nt ? 2 * wid_tail + 1 : -1);
+    if (u.j0 > 0) a.head[p.wid] = u.j1 < k.nt ? 2 : 1;  // what the join reads
+    else if (u.slot >= 0) a.tail[wid_tail] = make_int4(p.b, p.mt, p.h, 1);
     p.left -= u.j1 - u.j0;
     p.j = 0;
     if (++p.h == s.Hkv) { p.h = 0; ++p.mt; }
@@ -249,11 +254,24 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
             return pg;
         };
-        if (kl && lane == 0)
+        bool alternate = false;
+        if (kl && lane == 0) {
             for (int i = 0; i < 2; ++i) {
-                a.head[blockIdx.x + i * gridDim.x] = 0;
-                a.tail[blockIdx.x + i * gridDim.x] = make_int4(0, 0, 0, 0);
+                a.head[sb.pos[i].wid] = 0;
+                a.tail[sb.pos[i].wid] = make_int4(0, 0, 0, 0);
             }
+            // Many short units: the workers take turns at those of both shares (neighbours in the
+            // stream, they mostly have the same tiles, and so the workers, whose turns are taken in
+            // lockstep, meet their slow tiles together: 0.81 -> XXX ms at B = 8 x 16K, W = 512, ns = 4).
+            // Long ones: each has its own share, so both end at the same time.
+            StreamPos& p = sb.pos[0];
+            const int both = p.left + sb.pos[1].left;
+            if (sb.pos[1].left > 0) {
+                const int nt = key_tiles(sc, sink_seq(sc, p.b, nullptr), p.mt).nt;
+                alternate = both >= 16 * nt && (p.j > 0 ? p.left >= nt - p.j : true);
+                if (alternate) p.left = both;
+            }
+        }
         uint32_t used = 0;                                            // ring stages ever filled
         int i = 0;
 #pragma unroll 1
@@ -263,7 +281,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (kl) {
                     if (!wwait(&sb.part_empty[i][r], empty_par(cur.np / kParts))) break;
                     if (lane == 0) {
-                        sb.part[i][r] = next_part(a, sb.pos[i], blockIdx.x + i * gridDim.x);
+                        sb.part[i][r] = next_part(a, sb.pos[alternate ? 0 : i], sb.pos[alternate ? 1 : i].wid);
                         mbar_arrive(&sb.part_full[i][r]);
                     }
                     __syncwarp();
@@ -335,13 +353,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // ------------------------------------------------------------ S issuer
         if (lane == 0) {
             struct State {
-                int j, j1, np, ts;
+                int j, j1, np, ts, nar;
                 bool open;
             };
-            State cur{0, 0, 0, 0, true}, oth = cur;
+            State cur{0, 0, 0, 0, 0, true}, oth = cur;
             Ring kv{0, 0};
             bool issued = false;
-            const uint32_t id_s = idesc_bf16(128, 128, false, false);
+            const uint32_t id_s = idesc_bf16(128, 128, false, false), id_n = idesc_bf16(128, kNarrow, false, false);
 #pragma unroll 1
             for (int i = 0; cur.open || oth.open; i ^= 1) {
                 if (cur.open && cur.j == cur.j1) {
@@ -349,6 +367,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     if (!wait(&sb.part_full[i][r], full_par(cur.np / kParts))) break;
                     cur.j = sb.part[i][r].j0;
                     cur.j1 = sb.part[i][r].j1;
+                    cur.nar = sb.part[i][r].nar;
                     mbar_arrive(&sb.part_empty[i][r]);
                     cur.open = cur.j < cur.j1;
                     if (cur.open) {
@@ -362,7 +381,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     tc_fence_after();
                     const uint32_t qaddr = smem_u32(sm + C::OFF_Q + (i * C::QB + qb) * C::TILE);
                     const uint32_t kaddr = smem_u32(sm + C::OFF_K + kv.i * C::TILE);
-                    tcx::mma_kmajor_dh<D>(tmem + C::COL_S + i * 128, qaddr, 128, kaddr, 128, id_s, 0);
+                    tcx::mma_kmajor_dh<D>(tmem + C::COL_S + i * 128, qaddr, 128, kaddr, 128, cur.j < cur.nar ? id_n : id_s,
+                                          0);
                     mma_commit(&sb.s_full[i]);
                     mma_commit(&sb.k_empty[kv.i]);
                     issued = true;
@@ -383,10 +403,10 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // ------------------------------------------------------------ P V issuer (whole warp: it also
         // clears the V rows behind a sequence's last token, whose cache rows may hold anything)
         struct State {
-            int j, j1, np, tp, k0, nsk, end;
+            int j, j1, np, tp, k0, nsk, end, nar;
             bool open;
         };
-        State cur{0, 0, 0, 0, 0, 0, 0, true}, oth = cur;
+        State cur{0, 0, 0, 0, 0, 0, 0, 0, true}, oth = cur;
         Ring kv{0, 0};
         bool issued = false;
         const uint32_t id_o = idesc_bf16(128, 64, false, true);
@@ -402,6 +422,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 cur.k0 = u.k0;
                 cur.nsk = u.nsk;
                 cur.end = u.end;
+                cur.nar = u.nar;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sb.part_empty[i][r]);
                 cur.open = cur.j < cur.j1;
@@ -426,11 +447,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     __syncwarp();
                 }
                 if (!wwait(&sb.p_full[i], full_par(cur.tp))) break;
+                const bool narrow = cur.j < cur.nar;
                 ++cur.j;
                 if (lane == 0) {
                     tc_fence_after();
-                    tcx::mma_ts_mn_dh<D, 8>(tmem + C::COL_O + i * D, tmem + C::COL_P + i * C::P_STEP, smem_u32(vt),
-                                            128, id_o, first ? 0u : 1u);
+                    const uint32_t to = tmem + C::COL_O + i * D, tp = tmem + C::COL_P + i * C::P_STEP;
+                    if (narrow) tcx::mma_ts_mn_dh<D, kNarrow / 16>(to, tp, smem_u32(vt), 128, id_o, first ? 0u : 1u);
+                    else tcx::mma_ts_mn_dh<D, 8>(to, tp, smem_u32(vt), 128, id_o, first ? 0u : 1u);
                     mma_commit(&sb.v_empty[kv.i]);
                     mma_commit(&sb.p_empty[i]);
                     if (C::P_OVER_S) mma_commit(&sb.s_empty[i]);
@@ -488,61 +511,9 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 wlive = __any_sync(0xffffffffu, live);
             }
             const Part& w = sb.part[wg][(np - 1) % kParts];
-            float alpha = 1.f;
-            bool resc = false;
-            float x[128];
-            if (have) {
-                if (!wwait(&sb.s_full[wg], full_par(ts))) break;
-                tc_fence_after();
-                if (wlive) {
-                    float mt;
-                    {
-                        uint32_t r[2][64];
-                        float mc[2];
-#pragma unroll
-                        for (int ci = 0; ci < 2; ++ci) mc[ci] = tmem_ld_max_32x32b_x64(ts_addr + 64 * ci, r[ci]);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int ci = 0; ci < 2; ++ci)
-#pragma unroll
-                            for (int u = 0; u < 64; ++u) x[64 * ci + u] = __uint_as_float(r[ci][u]);
-                        mt = fmaxf(mc[0], mc[1]);
-                    }
-                    tc_fence_before();
-                    if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
-                    const int kbase = w.tile(j) * 128;
-                    // every row sees the whole tile, unless the diagonal or the window's edge crosses it
-                    if (kbase + 127 > w.p0 || (kbase < w.p1 - sc.W + 1 && kbase + 127 >= sc.ns)) {
-                        // columns c_lo .. c_hi (the window) and those below c_s (sinks), as bits
-                        const int p = w.p0 + rt;
-                        const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase;
-                        const int c_s = min(sc.ns, p + 1) - kbase;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t vis = (below(c_hi + 1 - 32 * i) & ~below(c_lo - 32 * i)) | below(c_s - 32 * i);
-#pragma unroll
-                            for (int u = 0; u < 32; ++u)
-                                x[32 * i + u] = (vis >> u & 1u) ? x[32 * i + u] : -INFINITY;
-                        }
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
-                        mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    }
-                    const float mts = mt * sl;
-                    if (mts > m + kRescaleLog2) {
-                        if (m != -INFINITY) {
-                            resc = true;
-                            alpha = fast_exp2(m - mts);
-                        }
-                        m = mts;
-                    }
-                    l *= alpha;
-                } else if (!C::P_OVER_S) {
-                    mbar_arrive(&sb.s_empty[wg]);
-                }
-            }
-            // the previous part's output leaves after the next one's first maximum, which
+            if (have && !wwait(&sb.s_full[wg], full_par(ts))) break;
+            tc_fence_after();
+            // the previous part's output leaves once the next part's first S is there, which
             // gives its last P V time to complete
             if (first && pend) {
                 if (!wwait(&sb.o_full[wg], full_par(ko))) break;
@@ -550,24 +521,21 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 const bool wr = pend_row >= 0;
                 const float inv = pl > 0.f ? 1.f / pl : 0.f;
                 if (__any_sync(0xffffffffu, wr)) {
+                    if (pend_slot < 0) {
+#pragma unroll 1
+                        for (int ci = 0; ci < D / 32; ++ci)
+                            store_row32(to_addr + 32 * ci, a.o, D, 32 * ci, pend_row, inv);
+                    } else {
+#pragma unroll 1
+                        for (int ci = 0; ci < D / 16; ++ci) {
+                            uint32_t r[16];
+                            tmem_ld_32x32b_x16(to_addr + 16 * ci, r);
+                            tmem_wait_ld();
+                            uint4* dst = reinterpret_cast<uint4*>(a.part_o + ((size_t)pend_slot * a.R + row) * D) + 4 * ci;
+                            if (wr)
 #pragma unroll
-                    for (int ci = 0; ci < D / 32; ++ci) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(to_addr + 32 * ci, r);
-                        tmem_wait_ld();
-                        if (wr && pend_slot < 0) {
-                            float f[32];
-                            // (an empty row's accumulator holds exact zeros times its zero weights)
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) f[u] = __uint_as_float(r[u]);
-                            uint4* dst = reinterpret_cast<uint4*>(a.o + (size_t)pend_row * D) + 4 * ci;
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) dst[u] = tcx::pack8(f + 8 * u, inv);
-                        } else if (wr) {
-                            uint4* dst = reinterpret_cast<uint4*>(a.part_o + ((size_t)pend_slot * a.R + row) * D) + 8 * ci;
-#pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                dst[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                                for (int u = 0; u < 4; ++u)
+                                    dst[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
                         }
                     }
                     if (wr && pend_slot >= 0) a.part_ml[(size_t)pend_slot * a.R + row] = make_float2(pm, pl);
@@ -579,9 +547,115 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 pend = false;
             }
             if (!have) break;
-            if (wlive) {
+            float alpha = 1.f;
+            // the running maximum follows a tile's (in log2 units) only past a margin
+            auto follow = [&](float mts) {
+                alpha = 1.f;
+                if (mts > m + kRescaleLog2) {
+                    if (m != -INFINITY) alpha = fast_exp2(m - mts);
+                    m = mts;
+                }
+                l *= alpha;
+            };
+            // once the previous tile's P V has completed, O is stable and can be rescaled
+            auto rescale = [&]() {
+                if (__all_sync(0xffffffffu, alpha == 1.f)) return;
+                tc_fence_after();
+#pragma unroll 1
+                for (int ci = 0; ci < D / 16; ++ci) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(to_addr + 16 * ci, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) r[u] = __float_as_uint(__uint_as_float(r[u]) * alpha);
+                    tmem_st_32x32b_x16(to_addr + 16 * ci, r);
+                }
+                tmem_wait_st();
+            };
+            const int kbase = w.tile(j) * 128;
+            const bool narrow = j < w.nar;
+            if (!wlive) {
+                if (!C::P_OVER_S) {
+                    mbar_arrive(&sb.s_empty[wg]);
+                    if (!wwait(&sb.p_empty[wg], empty_par(ts))) break;
+                }
+            } else if (narrow || kbase + 127 > w.p0 || (kbase < w.p1 - sc.W + 1 && kbase + 127 >= sc.ns)) {
+                // The diagonal or the window's edge crosses the tile, or it is the narrow one: 32
+                // columns at a time, in two rounds (maximum, weights).  Slower by the column than
+                // the path below, but little code: both together stay in the instruction cache.
+                const int nch = narrow ? 1 : 4;
+                const int p = w.p0 + rt;
+                // visible: columns c_lo .. c_hi (the window) and those below c_s (sinks)
+                const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
+                auto visible = [&](int c) {
+                    return (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
+                };
+                float mt = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < nch; ++c) {
+                    const uint32_t vis = visible(c);
+                    if (!__any_sync(0xffffffffu, vis != 0)) continue;
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(ts_addr + 32 * c, r);
+                    tmem_wait_ld();
+                    float m4[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        m4[i & 3] = fmaxf(m4[i & 3], (vis >> i & 1u) ? __uint_as_float(r[i]) : -INFINITY);
+                    mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                }
+                follow(mt * sl);
                 const float mu = (m == -INFINITY) ? 0.f : m;
-                const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(-mu, -mu);
+                if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
+                rescale();
+#pragma unroll 1
+                for (int c = 0; c < nch; ++c) {
+                    const uint32_t vis = visible(c);
+                    uint32_t pk[16] = {};
+                    if (__any_sync(0xffffffffu, vis != 0)) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(ts_addr + 32 * c, r);
+                        tmem_wait_ld();
+                        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * i]), sl, -mu));
+                            float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * i + 1]), sl, -mu));
+                            e0 = (vis >> (2 * i) & 1u) ? e0 : 0.f;
+                            e1 = (vis >> (2 * i + 1) & 1u) ? e1 : 0.f;
+                            l4[2 * (i & 1)] += e0;
+                            l4[2 * (i & 1) + 1] += e1;
+                            pk[i] = tcx::pack_bf16(e0, e1);
+                        }
+                        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    }
+                    // (P over S: these columns of S have been read)
+                    tmem_st_32x32b_x16(tp_addr + 16 * c, pk);
+                }
+                tmem_wait_st();
+                if (!C::P_OVER_S) {
+                    tc_fence_before();
+                    mbar_arrive(&sb.s_empty[wg]);
+                }
+            } else {
+                // Every row sees the whole tile: its row of S into registers at once, the
+                // maximum from the load.
+                float x[128];
+                {
+                    uint32_t r[2][64];
+                    float mc[2];
+#pragma unroll
+                    for (int ci = 0; ci < 2; ++ci) mc[ci] = tmem_ld_max_32x32b_x64(ts_addr + 64 * ci, r[ci]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int ci = 0; ci < 2; ++ci)
+#pragma unroll
+                        for (int u = 0; u < 64; ++u) x[64 * ci + u] = __uint_as_float(r[ci][u]);
+                    tc_fence_before();
+                    if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
+                    follow(fmaxf(mc[0], mc[1]) * sl);
+                }
+                const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(-m, -m);
                 uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t pka[32];                       // the first 64 keys' P, formed before the wait for the P buffer
 #pragma unroll
@@ -596,19 +670,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 // the previous tile's P V has completed: O is stable, the P buffer free
                 // (P over S: already so, since this tile's S product waited for it)
                 if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
-                if (__any_sync(0xffffffffu, resc)) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int ci = 0; ci < D / 16; ++ci) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(to_addr + 16 * ci, r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) r[u] = __float_as_uint(__uint_as_float(r[u]) * alpha);
-                        tmem_st_32x32b_x16(to_addr + 16 * ci, r);
-                    }
-                    tmem_wait_st();
-                }
+                rescale();
                 {
                     uint32_t h0[16], h1[16];
 #pragma unroll
@@ -644,8 +706,6 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
                 for (int u = 0; u < 4; ++u) tcx::f2_unpack(acc2[u], l4[2 * u], l4[2 * u + 1]);
                 l += ((l4[0] + l4[1]) + (l4[2] + l4[3])) + ((l4[4] + l4[5]) + (l4[6] + l4[7]));
-            } else if (!C::P_OVER_S) {
-                if (!wwait(&sb.p_empty[wg], empty_par(ts))) break;
             }
             tc_fence_before();
             mbar_arrive(&sb.p_full[wg]);
