@@ -51,12 +51,12 @@ struct SinkSched {
     int W, ns;
     int TM;              // tokens per query tile: min(128 / G, longest sequence)
     int nMT;             // query tiles of the longest sequence
-    int paged;
     PagedArgs p;
 };
 
+template <bool PAGED>
 __device__ __forceinline__ SeqInfo sink_seq(const SinkSched& a, int b, int* status) {
-    if (!a.paged) return SeqInfo{b * a.L, a.L, 0};
+    if (!PAGED) return SeqInfo{b * a.L, a.L, 0};
     return paged_seq(a.p, b, status);
 }
 
@@ -173,28 +173,29 @@ __device__ __forceinline__ uint32_t empty_par(int k) { return (static_cast<uint3
 // The lowest n bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// tcx::wait_bar for the control warps, as little code as it takes: gives up after
-// kWaitNs or once another role of the CTA has.
-__device__ __forceinline__ bool wait_ctrl(int* abort_flag, uint64_t* bar, uint32_t parity, int* status) {
-    uint64_t t0 = 0;
+// Bounded wait in as little code as it takes (the kernels' hot code has to stay in the
+// instruction cache): each try may suspend the thread for up to 20 us, and after about
+// 2 s of tries the wait records GCA_ERR_TIMEOUT and gives up; the CTA's other roles then
+// run out of theirs.
+__device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity, int* status) {
+    const uint32_t addr = tc::smem_u32(bar);
 #pragma unroll 1
-    for (uint32_t n = 1; !tc::mbar_try_wait(bar, parity); ++n) {
-        if (n & 63u) continue;
-        const uint64_t t = tc::global_timer_ns();
-        if (t0 == 0) t0 = t;
-        if (*((volatile int*)abort_flag)) return false;
-        if (t - t0 > tcx::kWaitNs) {
-            set_status(status, GCA_ERR_TIMEOUT);
-            *((volatile int*)abort_flag) = 1;
-            return false;
-        }
+    for (int n = 0; n < 100000; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
     }
-    return true;
+    set_status(status, GCA_ERR_TIMEOUT);
+    return false;
 }
-// Bounded wait (0.1 s) for work in flight at the end.
-__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) {
-    tc::mbar_wait(bar, parity, nullptr, 100000000ull);
-}
+// Bounded wait for work in flight at the end.
+__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) { wait_ctrl(bar, parity, nullptr); }
 
 // 32 fp32 columns of this lane's row of an accumulator, times `scale`, as bf16 to global
 // memory: row `row` of `out` (rows of ld elements; row < 0: none), columns col .. + 31.

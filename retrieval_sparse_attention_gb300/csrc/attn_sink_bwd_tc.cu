@@ -195,7 +195,6 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty[2];      // per storing warpgroup (it sees every phase); per accumulator
     uint64_t done[3];
     uint32_t tmem;
-    int abort;
     StreamPos pos;
     int wsum[12];
 };
@@ -233,7 +232,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     __shared__ Bars<C> sb;
     static_assert(C::SMEM + sizeof(Bars<C>) <= kSmemMax, "shared memory (pass A)");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(&sb.abort, bar, par, a.status); };
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par, a.status); };
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
@@ -262,7 +261,6 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             mbar_init(&sb.o_empty[i], 128);
         }
         for (int i = 0; i < 3; ++i) mbar_init(&sb.done[i], 1);
-        sb.abort = 0;
         fence_barrier_init();
         prefetch_tmap(&tq);
         prefetch_tmap(&tdo);
@@ -616,7 +614,6 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty;         // o_full per storing warpgroup: it sees every phase
     uint64_t done[3];
     uint32_t tmem;
-    int abort;
     StreamPos pos;
     int wsum[12];
 };
@@ -655,7 +652,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __shared__ Bars<C> sb;
     static_assert(C::SMEM + sizeof(Bars<C>) <= kSmemMax, "shared memory (pass B)");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(&sb.abort, bar, par, a.status); };
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par, a.status); };
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
@@ -681,7 +678,6 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         mbar_init(&sb.o_full[1], 2);
         mbar_init(&sb.o_empty, 128);
         for (int i = 0; i < 3; ++i) mbar_init(&sb.done[i], 1);
-        sb.abort = 0;
         fence_barrier_init();
         prefetch_tmap(&tq);
         prefetch_tmap(&tdo);

@@ -120,7 +120,6 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty[2];
     uint64_t done, done2;
     uint32_t tmem;
-    int abort;
     StreamPos pos[2];
     int wsum[12];
 };
@@ -128,16 +127,17 @@ struct __align__(16) Bars {
 // The next part of a share (one thread); moves `p` behind it.  A part that began in an
 // earlier share goes to worker wid's first slot, one that goes on in a later share to
 // the second slot of worker wid_tail.
+template <bool PAGED>
 __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wid_tail) {
     const SinkSched& s = a.s;
     Part u{};
     if (p.left <= 0) return u;
-    SeqInfo q = sink_seq(s, p.b, nullptr);
+    SeqInfo q = sink_seq<PAGED>(s, p.b, nullptr);
     KeyTiles k = key_tiles(s, q, p.mt);
     while (k.nt == 0 && p.b + 1 < s.B) {
         ++p.b;
         p.mt = 0;
-        q = sink_seq(s, p.b, nullptr);
+        q = sink_seq<PAGED>(s, p.b, nullptr);
         k = key_tiles(s, q, 0);
     }
     u.b = p.b;
@@ -161,7 +161,7 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     return u;
 }
 
-template <int D>
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
 sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const FwdArgs a) {
@@ -199,7 +199,6 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         mbar_init(&sb.done, 1);
         mbar_init(&sb.done2, 1);
-        sb.abort = 0;
         fence_barrier_init();
         prefetch_tmap(&tq);
         prefetch_tmap(&tk);
@@ -210,7 +209,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_relinquish();
     }
     find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, sb.wsum, sb.pos,
-                             [&](int b) { return sink_seq(sc, b, a.status); },
+                             [&](int b) { return sink_seq<PAGED>(sc, b, a.status); },
                              [&](const SeqInfo& q, int mt) { return key_tiles(sc, q, mt).nt; });
     tc_fence_before();
     __syncthreads();
@@ -223,7 +222,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // its code exists once (the instruction cache holds the whole kernel).
     if (warp < 4) {
     setmaxnreg_dec<kRegsCtrl>();
-    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(&sb.abort, bar, par, a.status); };
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par, a.status); };
     auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
     if (warp == 0 || warp == 3) {
         // ------------------------------------------------------------ producers (whole warps)
@@ -239,11 +238,11 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const CUtensorMap* map = kl ? &tk : &tv;
         uint8_t* ring = sm + (kl ? C::OFF_K : C::OFF_V);
         const int nst = kl ? C::KST : C::VST;
-        const int pages = sc.paged ? 128 >> sc.p.page_log2 : 1;       // boxes of a tile, one lane each
+        const int pages = PAGED ? 128 >> sc.p.page_log2 : 1;       // boxes of a tile, one lane each
         // page id of this lane's box of tile j; n_pages (outside the map: reads as zeros)
         // where no row of the unit sees any of the page
         auto lookup = [&](const Part& u) {
-            if (!sc.paged || cur.j >= cur.j1 || lane >= pages) return 0;
+            if (!PAGED || cur.j >= cur.j1 || lane >= pages) return 0;
             const int c0 = u.tile(cur.j) * 128 + (lane << sc.p.page_log2);
             const int c1 = c0 + (1 << sc.p.page_log2) - 1;
             if (c0 > u.p1 || (c1 <= u.p0 - sc.W && c0 >= sc.ns)) return sc.p.n_pages;
@@ -267,7 +266,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             StreamPos& p = sb.pos[0];
             const int both = p.left + sb.pos[1].left;
             if (sb.pos[1].left > 0) {
-                const int nt = key_tiles(sc, sink_seq(sc, p.b, nullptr), p.mt).nt;
+                const int nt = key_tiles(sc, sink_seq<PAGED>(sc, p.b, nullptr), p.mt).nt;
                 alternate = both >= 16 * nt && (p.j > 0 ? p.left >= nt - p.j : true);
                 if (alternate) p.left = both;
             }
@@ -281,7 +280,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (kl) {
                     if (!wwait(&sb.part_empty[i][r], empty_par(cur.np / kParts))) break;
                     if (lane == 0) {
-                        sb.part[i][r] = next_part(a, sb.pos[alternate ? 0 : i], sb.pos[alternate ? 1 : i].wid);
+                        sb.part[i][r] = next_part<PAGED>(a, sb.pos[alternate ? 0 : i], sb.pos[alternate ? 1 : i].wid);
                         mbar_arrive(&sb.part_full[i][r]);
                     }
                     __syncwarp();
@@ -314,8 +313,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (lane == 0) mbar_arrive_expect_tx(&full[rg.i], C::TILE);
                 __syncwarp();
                 if (lane < pages) {
-                    uint8_t* dst = ring + rg.i * C::TILE + ((lane << sc.p.page_log2) * (sc.paged ? 128 : 0));
-                    const int y = sc.paged ? 0 : u.tile(cur.j) * 128, z = sc.paged ? cur.pg : u.b;
+                    uint8_t* dst = ring + rg.i * C::TILE + ((lane << sc.p.page_log2) * (PAGED ? 128 : 0));
+                    const int y = PAGED ? 0 : u.tile(cur.j) * 128, z = PAGED ? cur.pg : u.b;
 #pragma unroll
                     for (int c = 0; c < C::SUB; ++c)
                         tma_load_3d(dst + c * C::STILE, map, &full[rg.i], u.h * D + c * 64, y, z);
@@ -437,7 +436,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 uint8_t* vt = sm + C::OFF_V + kv.i * C::TILE;
                 const int kt = cur.j < cur.nsk ? cur.j : cur.k0 + cur.j - cur.nsk;
                 const int behind = cur.end - kt * 128;                  // first row behind the last token
-                if (sc.paged && behind < 128) {
+                if (PAGED && behind < 128) {
 #pragma unroll 1
                     for (int r = max(behind, 0) * 8 + lane; r < 128 * 8; r += 32)
 #pragma unroll
@@ -452,8 +451,14 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (lane == 0) {
                     tc_fence_after();
                     const uint32_t to = tmem + C::COL_O + i * D, tp = tmem + C::COL_P + i * C::P_STEP;
-                    if (narrow) tcx::mma_ts_mn_dh<D, kNarrow / 16>(to, tp, smem_u32(vt), 128, id_o, first ? 0u : 1u);
-                    else tcx::mma_ts_mn_dh<D, 8>(to, tp, smem_u32(vt), 128, id_o, first ? 0u : 1u);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        if (ks == kNarrow / 16 && narrow) break;
+#pragma unroll
+                        for (int c = 0; c < C::SUB; ++c)
+                            tc::mma_bf16_ts(to + 64 * c, tp + 8 * ks, tcx::desc_head<64>(smem_u32(vt) + c * C::STILE) + 128 * ks,
+                                            id_o, (first && ks == 0) ? 0u : 1u);
+                    }
                     mma_commit(&sb.v_empty[kv.i]);
                     mma_commit(&sb.p_empty[i]);
                     if (C::P_OVER_S) mma_commit(&sb.s_empty[i]);
@@ -477,7 +482,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         setmaxnreg_inc<kRegsSoftmax>();
         // the accesses after a wait are warp-collective: a wait that gave up in one lane does in all
         auto wwait = [&](uint64_t* bar, uint32_t par) {
-            return __all_sync(0xffffffffu, tcx::wait_bar(&sb.abort, bar, par, a.status));
+            return __all_sync(0xffffffffu, wait_ctrl(bar, par, a.status));
         };
         const int wg = (warp - 4) >> 2;
         const int qd = warp & 3;
@@ -736,13 +741,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 // Joins the parts of the units that were cut: block w the unit that begins in worker
 // w's share and continues in the next ones.  With m = max_i m_i,
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, in the order of the stream.
-template <int D>
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(256) sink_join_kernel(const FwdArgs a, int workers) {
     const int w = blockIdx.x;
     const int4 u = a.tail[w];
     if (u.w == 0) return;
     const SinkSched& sc = a.s;
-    const SeqInfo s = sink_seq(sc, u.x, nullptr);
+    const SeqInfo s = sink_seq<PAGED>(sc, u.x, nullptr);
     int n = 1;                                          // parts: slot 2w+1, then slots 2(w+1), 2(w+2), ..
     while (w + n < workers) {
         const int h = a.head[w + n];
@@ -801,22 +806,22 @@ Layout layout(const SinkShape& s) {
     return w;
 }
 
-template <int D>
-cudaError_t launch(const SinkShape& s, const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+template <int D, bool PAGED>
+cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                    const CUtensorMap& tv, int grid, cudaStream_t st, int* launches) {
     using C = Cfg<D>;
     // the setmaxnreg split needs the whole launch allocation: refuse to launch a build that
     // gave the kernel fewer registers a thread (its warps would wait forever)
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, sink_fwd_tc_kernel<D>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, sink_fwd_tc_kernel<D, PAGED>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * kThreads < 128 * kRegsCtrl + 256 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(sink_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(sink_fwd_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
+    GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D, PAGED><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *launches += 1;
-    GCA_LAUNCH("sink_join", st, sink_join_kernel<D><<<2 * grid, 256, 0, st>>>(a, 2 * grid));
+    GCA_LAUNCH("sink_join", st, sink_join_kernel<D, PAGED><<<2 * grid, 256, 0, st>>>(a, 2 * grid));
     if ((e = cudaGetLastError()) == cudaSuccess) *launches += 1;
     return e;
 }
@@ -846,7 +851,6 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     a.s.W = s.W; a.s.ns = s.ns;
     a.R = rows_of_tile(s, &a.s.TM);
     a.s.nMT = (s.max_q + a.s.TM - 1) / a.s.TM;
-    a.s.paged = s.paged;
     if (s.paged) a.s.p = PagedArgs{cu_q, kv_len, table, s.T, s.max_q, __builtin_ctz(s.page), s.n_pages, s.width};
     if (!sink_fwd_supported(s)) return cudaErrorInvalidConfiguration;
     const Layout w = layout(s);
@@ -873,8 +877,11 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    return s.d == 64 ? launch<64>(s, a, tq, tk, tv, grid, st, launches)
-                     : launch<128>(s, a, tq, tk, tv, grid, st, launches);
+    if (s.paged)
+        return s.d == 64 ? launch<64, true>(a, tq, tk, tv, grid, st, launches)
+                         : launch<128, true>(a, tq, tk, tv, grid, st, launches);
+    return s.d == 64 ? launch<64, false>(a, tq, tk, tv, grid, st, launches)
+                     : launch<128, false>(a, tq, tk, tv, grid, st, launches);
 }
 
 }  // namespace gca
