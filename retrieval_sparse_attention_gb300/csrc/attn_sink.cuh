@@ -94,8 +94,9 @@ struct StreamPos {
 // count(seq(b), i) steps for each of `heads` heads, in the order (b, i, head, step).
 // Every worker gets total / workers steps, rounded up.  All THREADS threads of the
 // CTA take part; ends with __syncthreads.  The host bounds the total below 2^31.
+// whole: cuts move to the next entry's or head's first step.
 template <int THREADS, int SHARES, class Seq, class Count>
-__device__ __forceinline__ void find_shares(int B, int n, int heads, int* wsum, StreamPos* pos, Seq seq,
+__device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole, int* wsum, StreamPos* pos, Seq seq,
                                             Count count) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = B * n;                            // entries, a run of them for each thread
@@ -127,11 +128,18 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, int* wsum, 
                     const int from = wid(w) * quota;
                     const int x = (k & 1) ? min(total, from + quota) : from;
                     if (x < at || x >= at + len || from >= total) continue;
+                    int h = (x - at) / c, j = x - at - h * c;
+                    const int skip = whole && j > 0 ? c - j : 0;
                     if (k & 1) {
-                        atomicAdd(&pos[w].left, x - from);
+                        atomicAdd(&pos[w].left, x - from + skip);
                     } else {
-                        const int h = (x - at) / c;
-                        pos[w].b = b; pos[w].mt = i; pos[w].h = h; pos[w].j = x - at - h * c;
+                        atomicAdd(&pos[w].left, -skip);
+                        int m = i;
+                        if (skip) {
+                            j = 0;
+                            if (++h == heads) { h = 0; ++m; }    // (no such entry: the walk passes over it)
+                        }
+                        pos[w].b = b; pos[w].mt = m; pos[w].h = h; pos[w].j = j;
                     }
                 }
                 at += len;
@@ -239,6 +247,41 @@ __device__ __forceinline__ void store_row32(uint32_t taddr, __nv_bfloat16* out, 
             *reinterpret_cast<uint4*>(out + (size_t)rk * ld + col + 8 * (lane & 3)) =
                 make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
     }
+}
+
+// Programmatic dependent launch within a call: a kernel lets its successor's CTAs start
+// as its own leave, and the successor waits for its completion before it reads or
+// writes anything.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
+
+// Parts of an item that begins in worker w's share and goes on in the next ones: w's own
+// and those of the workers behind it up to the first whose head is not a middle part.
+__device__ __forceinline__ int parts_of(const int* head, int w, int workers) {
+    const int lane = threadIdx.x & 31;
+    int n = 1;
+    for (int at = w + 1; at < workers; at += 32) {
+        const int h = at + lane < workers ? head[at + lane] : 0;
+        const unsigned ends = __ballot_sync(0xffffffffu, h != 2);
+        if (ends) return n + __ffs(ends);
+        n += 32;
+    }
+    return n;
 }
 
 }  // namespace gca

@@ -72,6 +72,7 @@ struct BwdArgs {
 template <int D>
 __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     __shared__ float sd[8][33];
+    pdl_release();
     const SinkSched& sc = a.s;
     constexpr int LPR = D / 8;                       // lanes a row
     constexpr int RPW = 32 / LPR;                    // rows (heads) a warp reads at once
@@ -271,9 +272,11 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares<kThreads, 1>(sc.B, sc.nMT, sc.Hkv, sb.wsum, &sb.pos, [](int) { return 0; },
+    find_shares<kThreads, 1>(sc.B, sc.nMT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; },
                              [&](int, int mt) { return tiles(sc, mt).nt; });
     tc_fence_before();
+    pdl_release();
+    pdl_wait();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sb.tmem;
@@ -688,11 +691,13 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares<kThreads, 1>(sc.B, a.nKT, sc.Hkv, sb.wsum, &sb.pos, [](int) { return 0; }, [&](int, int kt) {
+    find_shares<kThreads, 1>(sc.B, a.nKT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; }, [&](int, int kt) {
         const Blocks k = blocks(sc, kt);
         return sc.G * (k.nw + k.nf);
     });
     tc_fence_before();
+    pdl_release();
+    pdl_wait();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sb.tmem;
@@ -965,49 +970,41 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 }
 }  // namespace pb
 
-// Adds up the parts of the items that were cut, in the order of the stream: block w the
-// item that begins in worker w's share and goes on in the next ones (pass A for
-// blockIdx.y = 0, pass B's dK and dV for 1 and 2).
+// Adds up the parts of the items that were cut, in the order of the stream: blocks (w, *, *)
+// the item that begins in worker w's share and goes on in the next ones (pass A for
+// blockIdx.z = 0, pass B's dK and dV for 1 and 2).
 template <int D>
 __global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int workers) {
+    pdl_wait();
     const SinkSched& sc = a.s;
-    const bool pass_a = blockIdx.y == 0;
+    const bool pass_a = blockIdx.z == 0;
     const int w = blockIdx.x;
     const int4 it = (pass_a ? a.tailA : a.tailB)[w];
     if (it.w == 0) return;
-    const int* head = pass_a ? a.headA : a.headB;
-    int n = 1;
-    while (w + n < workers) {
-        const int h = head[w + n];
-        ++n;
-        if (h != 2) break;
-    }
+    const int n = parts_of(pass_a ? a.headA : a.headB, w, workers);
     constexpr int VEC = D / 4;
-    const size_t slot_rows = pass_a ? 128 : 256;
-    const float* base = pass_a ? a.partA : a.partB + (blockIdx.y == 2 ? 128 * D : 0);
-    const int rows = pass_a ? a.R : 128;
-    for (int i = threadIdx.x; i < rows * VEC; i += blockDim.x) {
-        const int row = i / VEC, c = i % VEC;
-        size_t orow;
-        if (pass_a) {
-            const int rt = row / sc.G, t = it.y * sc.TM + rt;
-            if (t >= sc.L) continue;
-            orow = (size_t)(it.x * sc.L + t) * sc.H + it.z * sc.G + (row - rt * sc.G);
-        } else {
-            const int s = it.y * 128 + row;
-            if (s >= sc.L) continue;
-            orow = (size_t)(it.x * sc.L + s) * sc.Hkv + it.z;
-        }
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < n; ++k) {
-            const size_t slot = k == 0 ? 2 * w + 1 : 2 * (w + k);
-            const float4 x = reinterpret_cast<const float4*>(base + (slot * slot_rows + row) * D)[c];
-            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-        }
-        __nv_bfloat16* dst = pass_a ? a.dq : blockIdx.y == 1 ? a.dk : a.dv;
-        reinterpret_cast<uint2*>(dst + orow * D)[c] =
-            make_uint2(tcx::pack_bf16(acc.x, acc.y), tcx::pack_bf16(acc.z, acc.w));
+    const int row = blockIdx.y * (256 / VEC) + threadIdx.x / VEC, c = threadIdx.x % VEC;
+    size_t orow;
+    if (pass_a) {
+        const int rt = row / sc.G, t = it.y * sc.TM + rt;
+        if (row >= a.R || t >= sc.L) return;
+        orow = (size_t)(it.x * sc.L + t) * sc.H + it.z * sc.G + (row - rt * sc.G);
+    } else {
+        const int s = it.y * 128 + row;
+        if (s >= sc.L) return;
+        orow = (size_t)(it.x * sc.L + s) * sc.Hkv + it.z;
     }
+    const size_t slot_rows = pass_a ? 128 : 256;
+    const float* base = pass_a ? a.partA : a.partB + (blockIdx.z == 2 ? 128 * D : 0);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+        const size_t slot = k == 0 ? 2 * w + 1 : 2 * (w + k);
+        const float4 x = reinterpret_cast<const float4*>(base + (slot * slot_rows + row) * D)[c];
+        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    __nv_bfloat16* dst = pass_a ? a.dq : blockIdx.z == 1 ? a.dk : a.dv;
+    reinterpret_cast<uint2*>(dst + orow * D)[c] = make_uint2(tcx::pack_bf16(acc.x, acc.y), tcx::pack_bf16(acc.z, acc.w));
 }
 
 struct Layout {
@@ -1053,16 +1050,17 @@ cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[
                                   pa::Cfg<D>::SMEM)) != cudaSuccess)
         return e;
     GCA_LAUNCH("sink_bwd_q", st,
-               pa::sink_bwd_q_kernel<D><<<grid, kThreads, pa::Cfg<D>::SMEM, st>>>(m[0], m[1], m[2], m[3], a));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+               e = launch_pdl(pa::sink_bwd_q_kernel<D>, dim3(grid), kThreads, pa::Cfg<D>::SMEM, st, m[0], m[1], m[2], m[3], a));
+    if (e != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   pb::Cfg<D>::SMEM)) != cudaSuccess)
         return e;
     GCA_LAUNCH("sink_bwd_kv", st,
-               pb::sink_bwd_kv_kernel<D><<<grid, kThreads, pb::Cfg<D>::SMEM, st>>>(m[4], m[5], m[6], m[7], a));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    GCA_LAUNCH("sink_bwd_join", st, sink_bwd_join_kernel<D><<<dim3(grid, 3), 256, 0, st>>>(a, grid));
-    if ((e = cudaGetLastError()) == cudaSuccess) *launches += 4;
+               e = launch_pdl(pb::sink_bwd_kv_kernel<D>, dim3(grid), kThreads, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
+    if (e != cudaSuccess) return e;
+    GCA_LAUNCH("sink_bwd_join", st,
+               e = launch_pdl(sink_bwd_join_kernel<D>, dim3(grid, 128 * D / 1024, 3), 256, 0, st, a, grid));
+    if (e == cudaSuccess) *launches += 4;
     return e;
 }
 

@@ -91,6 +91,7 @@ struct FwdArgs {
     int4* tail;              // [workers]: unit (b, mt, h, 1) whose first part this worker holds, or .w = 0
     int* head;               // [workers]: 0, 1 (holds the last part of an earlier worker's unit), 2 (a middle part)
     int R;                   // rows of a query tile: TM * G
+    int whole;               // shares end between units: nothing to join
     int* status;
     float scale_log2;
 };
@@ -208,7 +209,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, sb.wsum, sb.pos,
+    pdl_release();
+    find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, a.whole, sb.wsum, sb.pos,
                              [&](int b) { return sink_seq<PAGED>(sc, b, a.status); },
                              [&](const SeqInfo& q, int mt) { return key_tiles(sc, q, mt).nt; });
     tc_fence_before();
@@ -738,49 +740,46 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
 }
 
-// Joins the parts of the units that were cut: block w the unit that begins in worker
+// Joins the parts of the units that were cut: blocks (w, *) the unit that begins in worker
 // w's share and continues in the next ones.  With m = max_i m_i,
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, in the order of the stream.
+// A thread has four columns of a row; a block 16 rows (d = 64) or 8.
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(256) sink_join_kernel(const FwdArgs a, int workers) {
+    pdl_wait();
     const int w = blockIdx.x;
     const int4 u = a.tail[w];
     if (u.w == 0) return;
+    const int n = parts_of(a.head, w, workers);
     const SinkSched& sc = a.s;
     const SeqInfo s = sink_seq<PAGED>(sc, u.x, nullptr);
-    int n = 1;                                          // parts: slot 2w+1, then slots 2(w+1), 2(w+2), ..
-    while (w + n < workers) {
-        const int h = a.head[w + n];
-        ++n;
-        if (h != 2) break;
+    constexpr int VEC = D / 4;
+    const int row = blockIdx.y * (256 / VEC) + threadIdx.x / VEC, c = threadIdx.x % VEC;
+    const int rt = row / sc.G, t = u.y * sc.TM + rt;
+    if (row >= a.R || t >= s.n) return;
+    const auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * w + 1 : 2 * (w + k)) * a.R + row; };
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) m = fmaxf(m, a.part_ml[slot(k)].x);
+    const float mu = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+        const float2 ml = a.part_ml[slot(k)];
+        const float4 o = reinterpret_cast<const float4*>(a.part_o + slot(k) * D)[c];
+        const float f = fast_exp2(ml.x - mu);
+        acc.x = fmaf(o.x, f, acc.x);
+        acc.y = fmaf(o.y, f, acc.y);
+        acc.z = fmaf(o.z, f, acc.z);
+        acc.w = fmaf(o.w, f, acc.w);
+        l = fmaf(ml.y, f, l);
     }
-    constexpr int VEC = D / 4;                          // threads a row
-    for (int i = threadIdx.x; i < a.R * VEC; i += blockDim.x) {
-        const int row = i / VEC, c = i % VEC;
-        const int rt = row / sc.G, t = u.y * sc.TM + rt;
-        if (t >= s.n) continue;
-        float m = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < n; ++k) {
-            const size_t slot = k == 0 ? 2 * w + 1 : 2 * (w + k);
-            const float2 ml = a.part_ml[slot * a.R + row];
-            if (ml.x == -INFINITY) continue;
-            const float4 o = reinterpret_cast<const float4*>(a.part_o + (slot * a.R + row) * D)[c];
-            const float mn = fmaxf(m, ml.x);
-            const float f0 = fast_exp2(m - mn), f1 = fast_exp2(ml.x - mn);
-            acc.x = acc.x * f0 + o.x * f1;
-            acc.y = acc.y * f0 + o.y * f1;
-            acc.z = acc.z * f0 + o.z * f1;
-            acc.w = acc.w * f0 + o.w * f1;
-            l = l * f0 + ml.y * f1;
-            m = mn;
-        }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const long long orow = (long long)(s.row0 + t) * sc.H + u.z * sc.G + (row - rt * sc.G);
-        reinterpret_cast<uint2*>(a.o + orow * D)[c] =
-            make_uint2(tcx::pack_bf16(acc.x * inv, acc.y * inv), tcx::pack_bf16(acc.z * inv, acc.w * inv));
-        if (c == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const long long orow = (long long)(s.row0 + t) * sc.H + u.z * sc.G + (row - rt * sc.G);
+    reinterpret_cast<uint2*>(a.o + orow * D)[c] =
+        make_uint2(tcx::pack_bf16(acc.x * inv, acc.y * inv), tcx::pack_bf16(acc.z * inv, acc.w * inv));
+    if (c == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 int rows_of_tile(const SinkShape& s, int* tm) {
@@ -821,8 +820,11 @@ cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& t
     GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D, PAGED><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *launches += 1;
-    GCA_LAUNCH("sink_join", st, sink_join_kernel<D, PAGED><<<2 * grid, 256, 0, st>>>(a, 2 * grid));
-    if ((e = cudaGetLastError()) == cudaSuccess) *launches += 1;
+    if (a.whole) return e;
+    const int rows = 1024 / D;
+    GCA_LAUNCH("sink_join", st,
+               e = launch_pdl(sink_join_kernel<D, PAGED>, dim3(2 * grid, (a.R + rows - 1) / rows), 256, 0, st, a, 2 * grid));
+    if (e == cudaSuccess) *launches += 1;
     return e;
 }
 
@@ -863,6 +865,11 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     a.lse = lse;
     a.status = status;
     a.scale_log2 = s.scale * kLog2e;
+    // Units of few key tiles are left whole: the longest share is then longer by less than the
+    // launch that joins parts takes (3 to 4 key tiles).
+    const long long span = (long long)s.W + a.s.TM - 1;
+    const long long keys = s.paged ? (long long)s.width * s.page : s.L;
+    a.whole = (span < keys ? (span + 126) / 128 + 1 + (s.ns + 127) / 128 : (keys + 127) / 128) <= 4;
     CUtensorMap tq, tk, tv;
     const uint64_t kvcols = (uint64_t)s.Hkv * s.d;
     bool ok = encode_bf16_3d(&tq, q, s.d, s.H, s.T, s.d, s.q_stride, a.s.G, a.s.TM);
