@@ -13,6 +13,7 @@ include/gca.h next to each entry point.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -178,32 +179,29 @@ def swa_bwd(q, k, v, o, lse, dout, *, window, attn_scale=0.0, workspace=None):
 
 
 # --- windowed attention with sinks, and its paged K/V cache ----------------------------
-def _token_stride(t):
+def _token_stride(shape, stride):
     """Elements between consecutive tokens of a [..., tokens, heads, d] tensor whose heads
     are dense and whose batch rows follow each other (a dense tensor, or a slice of a
     packed projection)."""
-    if not t.is_cuda:
-        raise ValueError("GCA entry points take CUDA tensors")
-    h, d = t.shape[-2], t.shape[-1]
-    st = t.stride()
-    step = st[-3] if t.shape[-3] > 1 else (st[-4] if t.dim() == 4 and t.shape[0] > 1 else h * d)
-    if (d > 1 and st[-1] != 1) or (h > 1 and st[-2] != d) or step < h * d or \
-            (t.dim() == 4 and t.shape[0] > 1 and st[0] != t.shape[1] * step):
+    h, d = shape[-2], shape[-1]
+    batched = len(shape) == 4 and shape[0] > 1
+    step = stride[-3] if shape[-3] > 1 else (stride[0] if batched else h * d)
+    if (d > 1 and stride[-1] != 1) or (h > 1 and stride[-2] != d) or step < h * d or \
+            (batched and stride[0] != shape[1] * step):
         raise ValueError("token tensors need dense heads and equally spaced tokens")
     return step
 
 
-def _vp(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
-
-
-def _on_current_device(*ts):
+def _same_device(*ts):
     """The entries launch on the current device's stream: tensors of another device (or of
-    none) would be read through a foreign address."""
-    dev = torch.cuda.current_device() if ts[0].is_cuda else -1
+    none) would be read through a foreign address.  Returns the device index."""
+    dev = ts[0].get_device()
     for t in ts:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be CUDA tensors on the current device")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must be CUDA tensors on the current device")
+    return dev
 
 
 def _dense(t, shape, dtype, what):
@@ -211,6 +209,15 @@ def _dense(t, shape, dtype, what):
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
     if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous tensor of shape %s" % (what, tuple(shape)))
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _raw_stream(stream, dev):
+    # (the stream's handle alone: building a torch.cuda.Stream costs more than a launch)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def make_swa_sink_params(*, B, L, H, d, window, Hkv=None, sinks=0, dtype=torch.bfloat16,
@@ -226,8 +233,8 @@ def gca_swa_sink_fwd_workspace_size(params: GcaSwaSinkParams) -> int:
 
 def gca_swa_sink_fwd(params: GcaSwaSinkParams, q, k, v, o, lse, workspace, stream=None):
     _check("gca_swa_sink_fwd", _lib.load().gca_swa_sink_fwd(
-        ctypes.byref(params), _vp(q), _vp(k), _vp(v), _vp(o), _vp(lse), _vp(workspace),
-        workspace.numel() if workspace is not None else 0, _stream(stream)))
+        ctypes.byref(params), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(workspace),
+        workspace.numel() if workspace is not None else 0, _raw_stream(stream, q.get_device())))
 
 
 def gca_swa_sink_bwd_workspace_size(params: GcaSwaSinkParams) -> int:
@@ -237,30 +244,35 @@ def gca_swa_sink_bwd_workspace_size(params: GcaSwaSinkParams) -> int:
 def gca_swa_sink_bwd(params: GcaSwaSinkParams, q, k, v, o, lse, dout, dq, dk, dv, workspace,
                      stream=None):
     _check("gca_swa_sink_bwd", _lib.load().gca_swa_sink_bwd(
-        ctypes.byref(params), _vp(q), _vp(k), _vp(v), _vp(o), _vp(lse), _vp(dout), _vp(dq),
-        _vp(dk), _vp(dv), _vp(workspace), workspace.numel(), _stream(stream)))
+        ctypes.byref(params), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq),
+        _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+        _raw_stream(stream, q.get_device())))
+
+
+@functools.lru_cache(maxsize=256)
+def _swa_sink_plan(qs, qst, ks, kst, vs, vst, qt, kt, vt, window, sinks, attn_scale):
+    """What a call derives from its arguments' shapes, strides and types alone."""
+    if len(qs) != 4 or len(ks) != 4 or ks != vs or ks[:2] != qs[:2] or ks[3] != qs[3]:
+        raise ValueError("q must be [B, L, H, d] and k, v [B, L, Hkv, d]")
+    if qt != kt or qt != vt:
+        raise TypeError("q, k and v must have one dtype")
+    step = _token_stride(ks, kst)
+    if step != _token_stride(vs, vst):
+        raise ValueError("k and v must have one token stride")
+    B, L, H, d = qs
+    p = make_swa_sink_params(B=B, L=L, H=H, Hkv=ks[2], d=d, window=window, sinks=sinks, dtype=qt,
+                             attn_scale=attn_scale, q_stride=_token_stride(qs, qst), kv_stride=step)
+    return p, gca_swa_sink_fwd_workspace_size(p), gca_swa_sink_bwd_workspace_size(p)
 
 
 def _swa_sink_args(q, k, v, window, sinks, attn_scale):
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.shape[:2] != q.shape[:2] or \
-            k.shape[3] != q.shape[3]:
-        raise ValueError("q must be [B, L, H, d] and k, v [B, L, Hkv, d]")
-    if q.dtype != k.dtype or q.dtype != v.dtype:
-        raise TypeError("q, k and v must have one dtype")
-    _on_current_device(q, k, v)
-    kvs = _token_stride(k)
-    if kvs != _token_stride(v):
-        raise ValueError("k and v must have one token stride")
-    B, L, H, d = q.shape
-    return make_swa_sink_params(B=B, L=L, H=H, Hkv=k.shape[2], d=d, window=window, sinks=sinks,
-                                dtype=q.dtype, attn_scale=attn_scale, q_stride=_token_stride(q),
-                                kv_stride=kvs)
+    return _swa_sink_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), q.dtype,
+                          k.dtype, v.dtype, window, sinks, float(attn_scale))
 
 
 def _workspace(given, need, dev):
     if given is None:
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    _on_current_device(given)
     if given.dtype != torch.uint8 or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     return given
@@ -269,9 +281,10 @@ def _workspace(given, need, dev):
 def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, workspace=None):
     """Windowed self-attention with sinks: q [B, L, H, d], k, v [B, L, Hkv, d] (token strides
     may be those of a packed projection) -> (o [B, L, H, d], lse [B, L, H])."""
-    p = _swa_sink_args(q, k, v, window, sinks, attn_scale)
+    _same_device(q, k, v, workspace)
+    p, need, _ = _swa_sink_args(q, k, v, window, sinks, attn_scale)
     dev = q.device
-    ws = _workspace(workspace, gca_swa_sink_fwd_workspace_size(p), dev)
+    ws = _workspace(workspace, need, dev)
     o = torch.empty(q.shape, dtype=q.dtype, device=dev)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if with_lse else None
     gca_swa_sink_fwd(p, q, k, v, o, lse, ws)
@@ -280,13 +293,13 @@ def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, works
 
 def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, workspace=None):
     """Gradients of swa_sink_fwd: returns dense (dq, dk, dv)."""
-    p = _swa_sink_args(q, k, v, window, sinks, attn_scale)
-    _on_current_device(q, o, lse, dout)
+    _same_device(q, k, v, o, lse, dout, workspace)
+    p, _, need = _swa_sink_args(q, k, v, window, sinks, attn_scale)
     _dense(o, q.shape, q.dtype, "o")
     _dense(dout, q.shape, q.dtype, "dout")
     _dense(lse, q.shape[:3], torch.float32, "lse")
     dev = q.device
-    ws = _workspace(workspace, gca_swa_sink_bwd_workspace_size(p), dev)
+    ws = _workspace(workspace, need, dev)
     dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
     dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
     dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
@@ -306,8 +319,8 @@ def make_paged_params(*, B, total_q, Hkv, d, page, n_pages, table_width, H=None,
 def gca_paged_append(params: GcaPagedParams, k_new, v_new, cu_q, kv_len, table, k_cache, v_cache,
                      stream=None):
     _check("gca_paged_append", _lib.load().gca_paged_append(
-        ctypes.byref(params), _vp(k_new), _vp(v_new), _vp(cu_q), _vp(kv_len), _vp(table),
-        _vp(k_cache), _vp(v_cache), _stream(stream)))
+        ctypes.byref(params), _ptr(k_new), _ptr(v_new), _ptr(cu_q), _ptr(kv_len), _ptr(table),
+        _ptr(k_cache), _ptr(v_cache), _raw_stream(stream, k_cache.get_device())))
 
 
 def gca_paged_attn_workspace_size(params: GcaPagedParams) -> int:
@@ -317,39 +330,64 @@ def gca_paged_attn_workspace_size(params: GcaPagedParams) -> int:
 def gca_paged_attn(params: GcaPagedParams, q, k_cache, v_cache, cu_q, kv_len, table, o, lse,
                    workspace, stream=None):
     _check("gca_paged_attn", _lib.load().gca_paged_attn(
-        ctypes.byref(params), _vp(q), _vp(k_cache), _vp(v_cache), _vp(cu_q), _vp(kv_len),
-        _vp(table), _vp(o), _vp(lse), _vp(workspace), workspace.numel(), _stream(stream)))
+        ctypes.byref(params), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_q), _ptr(kv_len),
+        _ptr(table), _ptr(o), _ptr(lse), _ptr(workspace),
+        workspace.numel() if workspace is not None else 0, _raw_stream(stream, q.get_device())))
 
 
-def _paged_cache(tok, k_cache, v_cache, table, cu_q, kv_len):
-    """Checks what the paged entries address by: returns (n_pages, page, Hkv, d, B, width)."""
-    if k_cache.dim() != 4 or table.dim() != 2:
+@functools.lru_cache(maxsize=256)
+def _paged_plan(ts, tst, k_cache, v_cache, table, cu_q, kv_len, dtypes, attend, max_q, window, sinks,
+                attn_scale):
+    """What a paged call derives from shapes, strides and types alone (each cache or index
+    tensor comes as its shape and stride): parameters and workspace size."""
+    dt = dtypes[0]
+    if dtypes[1] != dt or dtypes[2] != dt:
+        raise TypeError("the caches must have the token tensors' dtype")
+    if any(t != torch.int32 for t in dtypes[3:6]):
+        raise TypeError("table, cu_q and kv_len must be int32")
+    if len(k_cache[0]) != 4 or len(table[0]) != 2:
         raise ValueError("caches must be [n_pages, page, Hkv, d] and table [B, table_width]")
-    _on_current_device(k_cache, v_cache, table, cu_q, kv_len, tok)
-    _dense(k_cache, k_cache.shape, tok.dtype, "k_cache")
-    _dense(v_cache, k_cache.shape, tok.dtype, "v_cache")
-    B, width = table.shape
-    _dense(table, (B, width), torch.int32, "table")
-    _dense(cu_q, (B + 1,), torch.int32, "cu_q")
-    _dense(kv_len, (B,), torch.int32, "kv_len")
-    return (*k_cache.shape, B, width)
+    n_pages, page, Hkv, d = k_cache[0]
+    B, width = table[0]
+    for name, (shape, stride), want in (("k_cache", k_cache, k_cache[0]), ("v_cache", v_cache, k_cache[0]),
+                                        ("table", table, (B, width)), ("cu_q", cu_q, (B + 1,)),
+                                        ("kv_len", kv_len, (B,))):
+        dense = 1
+        for n, s in zip(reversed(shape), reversed(stride)):
+            if n != 1 and s != dense:
+                raise ValueError("%s must be contiguous" % name)
+            dense *= n
+        if tuple(shape) != tuple(want):
+            raise ValueError("%s must have shape %s" % (name, tuple(want)))
+    if len(ts) != 3 or ts[2] != d or (not attend and ts[1] != Hkv):
+        raise ValueError("token tensors must be [T, heads, d] like the cache")
+    step = _token_stride(ts, tst)
+    p = make_paged_params(B=B, total_q=ts[0], max_q=max_q, H=ts[1], Hkv=Hkv, d=d, page=page,
+                          n_pages=n_pages, table_width=width, window=window, sinks=sinks, dtype=dt,
+                          attn_scale=attn_scale, q_stride=step if attend else 0,
+                          kv_stride=0 if attend else step)
+    return p, gca_paged_attn_workspace_size(p) if attend else 0
+
+
+def _paged_args(tok, k_cache, v_cache, table, cu_q, kv_len, attend, max_q, window=0, sinks=0, attn_scale=0.0):
+    return _paged_plan(tok.shape, tok.stride(), (k_cache.shape, k_cache.stride()),
+                       (v_cache.shape, v_cache.stride()), (table.shape, table.stride()),
+                       (cu_q.shape, cu_q.stride()), (kv_len.shape, kv_len.stride()),
+                       (tok.dtype, k_cache.dtype, v_cache.dtype, table.dtype, cu_q.dtype, kv_len.dtype),
+                       attend, max_q, window, sinks, float(attn_scale))
 
 
 def paged_append(k_new, v_new, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0):
     """Write new tokens into the paged cache, in place: k_new, v_new [T, Hkv, d]; caches
     [n_pages, page, Hkv, d]; table [B, table_width], cu_q [B + 1], kv_len [B] int32 on the
     device.  ``kv_len`` counts the new tokens."""
-    n_pages, page, Hkv, d, B, width = _paged_cache(k_new, k_cache, v_cache, table, cu_q, kv_len)
-    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != (Hkv, d) or v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must be [T, %d, %d]" % (Hkv, d))
+    _same_device(k_cache, v_cache, table, cu_q, kv_len, k_new, v_new)
+    p, _ = _paged_args(k_new, k_cache, v_cache, table, cu_q, kv_len, False, max_q)
     if v_new.dtype != k_new.dtype:
         raise TypeError("k_new and v_new must have one dtype")
-    _on_current_device(k_new, v_new)
-    kvs = _token_stride(k_new)
-    if kvs != _token_stride(v_new):
-        raise ValueError("k_new and v_new must have one token stride")
-    p = make_paged_params(B=B, total_q=k_new.shape[0], max_q=max_q, Hkv=Hkv, d=d, page=page,
-                          n_pages=n_pages, table_width=width, dtype=k_new.dtype, kv_stride=kvs)
+    if v_new.shape != k_new.shape or (v_new.stride() != k_new.stride() and
+                                      _token_stride(v_new.shape, v_new.stride()) != p.kv_stride):
+        raise ValueError("k_new and v_new must have one shape and one token stride")
     gca_paged_append(p, k_new, v_new, cu_q, kv_len, table, k_cache, v_cache)
 
 
@@ -358,21 +396,15 @@ def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, s
     """Attention of the new tokens q [T, H, d] over the paged cache -> (o [T, H, d], lse [T, H]
     or None).  ``max_q`` bounds the new tokens of one sequence (0: T); a host that knows it
     saves work.  Rows of o behind cu_q[B] are left as they were (``out`` supplies o)."""
-    n_pages, page, Hkv, d, B, width = _paged_cache(q, k_cache, v_cache, table, cu_q, kv_len)
-    if q.dim() != 3 or q.shape[2] != d:
-        raise ValueError("q must be [T, H, %d]" % d)
-    T, H = q.shape[0], q.shape[1]
-    p = make_paged_params(B=B, total_q=T, max_q=max_q, H=H, Hkv=Hkv, d=d, page=page,
-                          n_pages=n_pages, table_width=width, window=window, sinks=sinks,
-                          dtype=q.dtype, attn_scale=attn_scale, q_stride=_token_stride(q))
+    _same_device(q, k_cache, v_cache, table, cu_q, kv_len, out, workspace)
+    p, need = _paged_args(q, k_cache, v_cache, table, cu_q, kv_len, True, max_q, window, sinks, attn_scale)
     dev = q.device
-    ws = _workspace(workspace, gca_paged_attn_workspace_size(p), dev)
+    ws = _workspace(workspace, need, dev)
     if out is None:
-        out = torch.empty(T, H, d, dtype=q.dtype, device=dev)
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     else:
-        _on_current_device(out)
         _dense(out, q.shape, q.dtype, "out")
-    lse = torch.empty(T, H, dtype=torch.float32, device=dev) if with_lse else None
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if with_lse else None
     gca_paged_attn(p, q, k_cache, v_cache, cu_q, kv_len, table, out, lse, ws)
     return out, lse
 
