@@ -100,11 +100,17 @@ struct FwdArgs {
 struct __align__(16) Part {
     int b, h, qrow, ntok;    // sequence, key head, first token's row, tokens of the query tile
     int p0, p1, end;         // positions of the first and the last token, and behind the sequence
-    int k0, nsk;             // key tile j is j (j < nsk) or k0 + j - nsk
+    int k0, nsk, nw;         // key tiles: nsk of sinks from 0 on, nw of the window from k0 on
     int j0, j1;
     int slot;                // -1: the whole unit; else the workspace slot of its sums
     int nar;                 // key tiles j < nar (one or none) are narrow: 32 columns hold all sinks
-    __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
+    // The sinks come first and the window's first tile, which its edge crosses, last: the
+    // crossed tiles then mostly find a running maximum that they need not raise.
+    __device__ static __forceinline__ int tile(int j, int nsk, int k0, int nw) {
+        const int i = j - nsk + 1;
+        return i <= 0 ? j : i == nw ? k0 : k0 + i;
+    }
+    __device__ __forceinline__ int tile(int j) const { return tile(j, nsk, k0, nw); }
 };
 constexpr int kParts = 4;    // records a worker
 constexpr int kNarrow = 32;  // sinks up to here take a tile of this width, a fifth of a full tile's time
@@ -150,6 +156,7 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     u.end = q.pos0 + q.n;
     u.k0 = k.k0;
     u.nsk = k.nsk;
+    u.nw = k.nt - k.nsk;
     u.j0 = p.j;
     u.j1 = min(k.nt, p.j + p.left);
     u.nar = k.nsk == 1 && s.ns <= kNarrow;
@@ -404,13 +411,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // ------------------------------------------------------------ P V issuer (whole warp: it also
         // clears the V rows behind a sequence's last token, whose cache rows may hold anything)
         struct State {
-            int j, j1, np, tp, k0, nsk, end, nar;
+            int j, j1, np, tp, nar, end, nsk, k0, nw;
             bool open;
         };
-        State cur{0, 0, 0, 0, 0, 0, 0, 0, true}, oth = cur;
+        State cur{0, 0, 0, 0, 0, 0, 0, 0, 0, true}, oth = cur;
         Ring kv{0, 0};
         bool issued = false;
-        const uint32_t id_o = idesc_bf16(128, 64, false, true);
+        const uint32_t id_o = idesc_bf16(128, D, false, true);
 #pragma unroll 1
         for (int i = 0; cur.open || oth.open; i ^= 1) {
             bool first = false;
@@ -420,10 +427,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 const Part& u = sb.part[i][r];
                 cur.j = u.j0;
                 cur.j1 = u.j1;
-                cur.k0 = u.k0;
-                cur.nsk = u.nsk;
-                cur.end = u.end;
                 cur.nar = u.nar;
+                if (PAGED) {
+                    cur.end = u.end;
+                    cur.nsk = u.nsk;
+                    cur.k0 = u.k0;
+                    cur.nw = u.nw;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sb.part_empty[i][r]);
                 cur.open = cur.j < cur.j1;
@@ -436,9 +446,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (cur.open) {
                 if (!wwait(&sb.v_full[kv.i], kv.ph)) break;
                 uint8_t* vt = sm + C::OFF_V + kv.i * C::TILE;
-                const int kt = cur.j < cur.nsk ? cur.j : cur.k0 + cur.j - cur.nsk;
-                const int behind = cur.end - kt * 128;                  // first row behind the last token
-                if (PAGED && behind < 128) {
+                const int behind = cur.end - Part::tile(cur.j, cur.nsk, cur.k0, cur.nw) * 128;
+                if (PAGED && behind < 128) {                          // the tile has rows behind the last token
 #pragma unroll 1
                     for (int r = max(behind, 0) * 8 + lane; r < 128 * 8; r += 32)
 #pragma unroll
@@ -453,13 +462,11 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (lane == 0) {
                     tc_fence_after();
                     const uint32_t to = tmem + C::COL_O + i * D, tp = tmem + C::COL_P + i * C::P_STEP;
+                    const uint64_t vd = smem_desc(smem_u32(vt), C::STILE, 1024, 2);   // V: keys x D, D along N
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         if (ks == kNarrow / 16 && narrow) break;
-#pragma unroll
-                        for (int c = 0; c < C::SUB; ++c)
-                            tc::mma_bf16_ts(to + 64 * c, tp + 8 * ks, tcx::desc_head<64>(smem_u32(vt) + c * C::STILE) + 128 * ks,
-                                            id_o, (first && ks == 0) ? 0u : 1u);
+                        tc::mma_bf16_ts(to, tp + 8 * ks, vd + 128 * ks, id_o, (first && ks == 0) ? 0u : 1u);
                     }
                     mma_commit(&sb.v_empty[kv.i]);
                     mma_commit(&sb.p_empty[i]);
@@ -597,9 +604,20 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 auto visible = [&](int c) {
                     return (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
                 };
+                // the maximum over all columns bounds that over the visible ones: only where it would
+                // move the running one (or is no number) is the latter needed
+                bool exact = narrow;
+                if (!narrow) {
+                    uint32_t r[64];
+                    float mb = tmem_ld_max_32x32b_x64(ts_addr, r);
+                    tmem_wait_ld();
+                    const float mb2 = tmem_ld_max_32x32b_x64(ts_addr + 64, r);
+                    tmem_wait_ld();
+                    exact = __any_sync(0xffffffffu, !(mb * sl <= m + kRescaleLog2) || !(mb2 * sl <= m + kRescaleLog2));
+                }
                 float mt = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < nch; ++c) {
+                for (int c = 0; c < (exact ? nch : 0); ++c) {
                     const uint32_t vis = visible(c);
                     if (!__any_sync(0xffffffffu, vis != 0)) continue;
                     uint32_t r[32];
