@@ -21,8 +21,8 @@
 // and short problems fill the machine; parts are fp32 sums in the workspace, added in
 // the order of the stream.  No atomics: bitwise reproducible.
 // Within a CTA (12 warps): warp 0 walks the share, writes its parts down as records
-// and loads; warp 1 issues S (pass B: and dP), warp 2 dQ (dK), warp 11 dP (dV), warps 3-10
-// are two math warpgroups that take alternate steps; a thread owns a query row
+// and loads; warp 1 issues S, warp 11 dP, warp 2 dQ (dK and dV); warps 3-10 are two math
+// warpgroups that take alternate steps; a thread owns a query row
 // (pass A) or a key row (pass B), a lane of tensor memory, which is the layout of
 // the A operands that it writes.
 #include <math.h>
@@ -178,7 +178,7 @@ struct Cfg {
     static constexpr int OFF_KV = IBUF * ITEM;
     static constexpr int OFF_VEC = OFF_KV + NSLOT * SLOT;         // two vectors of 128 floats
     static constexpr int SMEM = OFF_VEC + 1024 + 1024;
-    static constexpr int NX = 4, NY = 2;                          // 64-column buffers of S (then ds) and of dP
+    static constexpr int NX = 3, NY = 3;                          // 64-column buffers of S (then ds) and of dP
     static constexpr int NACC = D == 64 ? 2 : 1;
     static constexpr uint32_t COL_X = 0, COL_Y = NX * 64, COL_ACC = COL_Y + NY * 64;
     static_assert(COL_ACC + NACC * D <= TMEM_COLS, "tensor memory");
@@ -383,7 +383,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             Ring kv{0, 0};
             int u = 0;
             bool issued = false, ok = true;
-            const uint32_t id_acc = idesc_bf16(128, 64, false, true);
+            const uint32_t id_acc = idesc_bf16(128, D, false, true);
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts, ob = np % C::NACC;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
@@ -399,8 +399,11 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     if (!wait(&sb.p_full[u & 3], full_par(u >> 2))) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t kaddr = smem_u32(sm + C::OFF_KV + kv.i * C::SLOT);
-                    tcx::mma_ts_mn_dh<D, 4>(tmem + C::COL_ACC + ob * D, tmem + C::COL_X + xs * 64, kaddr, 64, id_acc,
-                                            j > 0 ? 1u : 0u);
+                    const uint64_t kd = smem_desc(kaddr, C::SKEY, 1024, 2);      // K: keys x D, D along N
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc::mma_bf16_ts(tmem + C::COL_ACC + ob * D, tmem + C::COL_X + xs * 64 + 8 * ks, kd + 128 * ks, id_acc,
+                                        (ks > 0 || j > 0) ? 1u : 0u);
                     mma_commit(&sb.x_empty[xs]);
                     mma_commit(&sb.kv_empty[kv.i]);       // S and dP are complete before ds exists
                     issued = true;
@@ -601,7 +604,7 @@ struct Cfg {
     static constexpr int NSLOT = D == 64 ? 8 : 4;
     static constexpr int OFF_ST = IBUF * ITEM;
     static constexpr int SMEM = OFF_ST + NSLOT * SLOT + 1024;
-    static constexpr int NX = D == 64 ? 4 : 2, NY = 2;
+    static constexpr int NX = D == 64 ? 3 : 2, NY = NX;
     static constexpr uint32_t COL_X = 0, COL_Y = NX * 64, COL_ACC = COL_Y + NY * 64;   // dK, dV
     static_assert(COL_ACC + 2 * D <= TMEM_COLS, "tensor memory");
 };
@@ -665,20 +668,20 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         for (int i = 0; i < C::IBUF; ++i) {
             mbar_init(&sb.it_full[i], 1);
-            mbar_init(&sb.it_empty[i], 1);
+            mbar_init(&sb.it_empty[i], 2);
         }
         for (int i = 0; i < C::NSLOT; ++i) {
             mbar_init(&sb.st_full[i], 1);
-            mbar_init(&sb.st_empty[i], 2);                // the dK and the dV issuer
+            mbar_init(&sb.st_empty[i], 1);
         }
         for (int i = 0; i < C::NX; ++i) {
-            mbar_init(&sb.x_full[i], 1);
-            mbar_init(&sb.x_empty[i], 2);
+            mbar_init(&sb.x_full[i], 2);
+            mbar_init(&sb.x_empty[i], 1);
         }
         for (int i = 0; i < C::NY; ++i) mbar_init(&sb.y_empty[i], 128);
         for (int i = 0; i < 4; ++i) mbar_init(&sb.p_full[i], 128);
-        mbar_init(&sb.o_full[0], 2);
-        mbar_init(&sb.o_full[1], 2);
+        mbar_init(&sb.o_full[0], 1);
+        mbar_init(&sb.o_full[1], 1);
         mbar_init(&sb.o_empty, 128);
         for (int i = 0; i < 3; ++i) mbar_init(&sb.done[i], 1);
         fence_barrier_init();
@@ -759,8 +762,9 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (n > 0) wait_copy(&sb.it_full[q], full_par(n - 1));
             }
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ S^T = K Q^T, dP^T = V dO^T
+    } else if (warp == 1 || warp == 11) {
+        // ------------------------------------------------------------ warp 1: S^T = K Q^T, warp 11: dP^T = V dO^T
+        const bool dpi = warp == 11;
         if (lane == 0) {
             Ring st{0, 0};
             int u = 0;
@@ -773,39 +777,36 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 mbar_arrive(&sb.part_empty[r]);
                 if (n == 0) break;
                 if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
-                const uint32_t kaddr = smem_u32(sm + ib * C::ITEM);
+                const uint32_t aaddr = smem_u32(sm + ib * C::ITEM) + (dpi ? C::TILE : 0);
 #pragma unroll 1
                 for (int j = 0; j < n; ++j, ++u) {
-                    const int xs = u % C::NX, ys = u % C::NY;
-                    if (!wait(&sb.st_full[st.i], st.ph) || !wait(&sb.x_empty[xs], empty_par(u / C::NX)) ||
-                        !wait(&sb.y_empty[ys], empty_par(u / C::NY))) {
+                    const int xs = u % C::NX;
+                    if (!wait(&sb.st_full[st.i], st.ph) ||
+                        !wait(dpi ? &sb.y_empty[xs] : &sb.x_empty[xs], empty_par(u / C::NX))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t qaddr = smem_u32(sm + C::OFF_ST + st.i * C::SLOT);
-                    tcx::mma_kmajor_dh<D>(tmem + C::COL_X + xs * 64, kaddr, 128, qaddr, 64, id_s, 0);
-                    tcx::mma_kmajor_dh<D>(tmem + C::COL_Y + ys * 64, kaddr + C::TILE, 128, qaddr + C::QTILE, 64, id_s, 0);
+                    const uint32_t baddr = smem_u32(sm + C::OFF_ST + st.i * C::SLOT) + (dpi ? C::QTILE : 0);
+                    tcx::mma_kmajor_dh<D>(tmem + (dpi ? C::COL_Y : C::COL_X) + xs * 64, aaddr, 128, baddr, 64, id_s, 0);
                     mma_commit(&sb.x_full[xs]);
                     issued = true;
                     st.next(C::NSLOT);
                 }
-                if (ok) mma_commit(&sb.it_empty[ib]);     // K and V are read only by these products
+                if (ok) mma_commit(&sb.it_empty[ib]);     // K (V) is read only by these products
             }
             if (issued) {
-                mma_commit(&sb.done[0]);
-                wait_copy(&sb.done[0], 0);
+                mma_commit(&sb.done[dpi ? 2 : 0]);
+                wait_copy(&sb.done[dpi ? 2 : 0], 0);
             }
         }
-    } else if (warp == 2 || warp == 11) {
-        // ------------------------------------------------------------ warp 2: dK += ds^T Q, warp 11: dV += P^T dO
-        const bool dvi = warp == 11;
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ dK += ds^T Q, dV += P^T dO
         if (lane == 0) {
             Ring st{0, 0};
             int u = 0;
             bool issued = false, ok = true;
-            const uint32_t id_acc = idesc_bf16(128, 64, false, true);
-            const uint32_t d_acc = tmem + C::COL_ACC + (dvi ? D : 0);
+            const uint32_t id_acc = idesc_bf16(128, D, false, true);
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
@@ -819,16 +820,16 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     const int xs = u % C::NX;
                     if (!wait(&sb.p_full[u & 3], full_par(u >> 2))) { ok = false; break; }
                     tc_fence_after();
-                    // A: K = 16 query steps at X columns 0, 8, 32, 40 (ds^T) and 16, 24, 48, 56 (P^T)
-                    const uint32_t xaddr = smem_u32(sm + C::OFF_ST + st.i * C::SLOT) + (dvi ? C::QTILE : 0);
-                    const uint32_t xa = tmem + C::COL_X + xs * 64 + (dvi ? 16 : 0);
+                    // A: K = 16 query steps at X columns 0, 8, 32, 40 (ds^T) and 16, 24, 48, 56 (P^T);
+                    // B: queries x D with D along N
+                    const uint64_t qd = smem_desc(smem_u32(sm + C::OFF_ST + st.i * C::SLOT), C::SQ, 1024, 2);
+                    const uint32_t xa = tmem + C::COL_X + xs * 64;
 #pragma unroll
-                    for (int c = 0; c < C::SUB; ++c) {
-                        const uint64_t xd = tcx::desc_head<D>(xaddr + c * C::SQ);
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc::mma_bf16_ts(d_acc + c * 64, xa + (ks >> 1) * 32 + (ks & 1) * 8, xd + (uint64_t)(ks * 128),
-                                            id_acc, (ks > 0 || j > 0) ? 1u : 0u);
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint32_t col = xa + (ks >> 1) * 32 + (ks & 1) * 8;
+                        const uint32_t acc = (ks > 0 || j > 0) ? 1u : 0u;
+                        tc::mma_bf16_ts(tmem + C::COL_ACC, col, qd + 128 * ks, id_acc, acc);
+                        tc::mma_bf16_ts(tmem + C::COL_ACC + D, col + 16, qd + (C::QTILE >> 4) + 128 * ks, id_acc, acc);
                     }
                     mma_commit(&sb.x_empty[xs]);
                     mma_commit(&sb.st_empty[st.i]);
@@ -838,8 +839,8 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (ok) mma_commit(&sb.o_full[np & 1]);
             }
             if (issued) {
-                mma_commit(&sb.done[dvi ? 2 : 1]);
-                wait_copy(&sb.done[dvi ? 2 : 1], 0);
+                mma_commit(&sb.done[1]);
+                wait_copy(&sb.done[1], 0);
             }
         }
     } else {
