@@ -20,11 +20,11 @@
 // (attn_sink.cuh), so a sink's long item is spread over as many CTAs as it takes
 // and short problems fill the machine; parts are fp32 sums in the workspace, added in
 // the order of the stream.  No atomics: bitwise reproducible.
-// Within a CTA (12 warps): warp 0 walks the share, writes its parts down as records
-// and loads; warp 1 issues S, warp 11 dP, warp 2 dQ (dK and dV); warps 3-10 are two math
-// warpgroups that take alternate steps; a thread owns a query row
-// (pass A) or a key row (pass B), a lane of tensor memory, which is the layout of
-// the A operands that it writes.
+// Within a CTA: warp 0 walks the share, writes its parts down as records and loads; one
+// thread each issues S, dP, and dQ (pass B: dK and dV); the math warpgroups take
+// alternate steps (pass A: one of two each, pass B: two of four, half the queries
+// each); a thread owns a query row (pass A) or a key row (pass B), a lane of tensor
+// memory, which is the layout of the A operands that it writes.
 #include <math.h>
 
 #include "attn_sink.cuh"
@@ -42,7 +42,9 @@ using tcx::fast_exp2;
 using tcx::kLog2e;
 using tcx::Ring;
 
-constexpr int kThreads = 384;
+// Pass A: 4 control warps and 2 math warpgroups (with 4, as in pass B, 0.51 instead of 0.47 ms
+// at B = 8 x 16K).  Pass B: 4 math warpgroups, two to a step (with 2: 0.78 instead of 0.74 ms).
+constexpr int kThreadsA = 384, kThreadsB = 640;
 constexpr int kMaxCtas = 152;              // one per SM; the workspace is sized for them
 constexpr int kParts = 4;                  // part records in flight
 constexpr int kSmemMax = 232448;
@@ -121,17 +123,17 @@ __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     }
 }
 
-// The D columns of this lane's row of an fp32 accumulator to global memory, as bf16 (row
+// N columns of this lane's row of an fp32 accumulator to global memory, as bf16 (row
 // < 0: none) or as they are.
-template <int D>
-__device__ __forceinline__ void store_rows_bf16(uint32_t taddr, __nv_bfloat16* out, int row) {
-#pragma unroll
-    for (int ci = 0; ci < D / 32; ++ci) store_row32(taddr + 32 * ci, out, D, 32 * ci, row, 1.f);
+template <int N>
+__device__ __forceinline__ void store_rows_bf16(uint32_t taddr, __nv_bfloat16* out, int ld, int row) {
+#pragma unroll 1
+    for (int ci = 0; ci < N / 32; ++ci) store_row32(taddr + 32 * ci, out, ld, 32 * ci, row, 1.f);
 }
-template <int D>
+template <int N>
 __device__ __forceinline__ void store_rows_f32(uint32_t taddr, float* dst, bool live) {
-#pragma unroll
-    for (int ci = 0; ci < D / 32; ++ci) {
+#pragma unroll 1
+    for (int ci = 0; ci < N / 32; ++ci) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(taddr + 32 * ci, r);
         tmem_wait_ld();
@@ -163,6 +165,7 @@ struct __align__(16) Part {
     int b, h, mt, k0, nsk;
     int j0, j1;              // steps of this part (j0 == j1: the share is done)
     int slot;                // -1: the whole item; else the workspace slot of its sums
+    int nar;                 // steps of this part (its first, or none) that are narrow: 32 columns hold all sinks
     __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
 };
 
@@ -209,6 +212,7 @@ __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wi
     u.k0 = k.k0; u.nsk = k.nsk;
     u.j0 = p.j;
     u.j1 = min(k.nt, p.j + p.left);
+    u.nar = k.nsk == 1 && s.ns <= 32 && p.j == 0;
     u.slot = u.j0 > 0 ? 2 * wid : (u.j1 < k.nt ? 2 * wid + 1 : -1);
     if (u.j0 > 0) a.headA[wid] = u.j1 < k.nt ? 2 : 1;
     if (u.slot == 2 * wid + 1) a.tailA[wid] = make_int4(p.b, p.mt, p.h, 1);
@@ -222,7 +226,7 @@ __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wi
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsA, 1)
 sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const BwdArgs a) {
@@ -272,7 +276,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares<kThreads, 1>(sc.B, sc.nMT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; },
+    find_shares<kThreadsA, 1>(sc.B, sc.nMT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; },
                              [&](int, int mt) { return tiles(sc, mt).nt; });
     tc_fence_before();
     pdl_release();
@@ -345,11 +349,11 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             Ring kv{0, 0};
             int u = 0;
             bool issued = false, ok = true;
-            const uint32_t id_s = idesc_bf16(128, 64, false, false);
+            const uint32_t id_s = idesc_bf16(128, 64, false, false), id_n = idesc_bf16(128, 32, false, false);
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts, ib = np % C::IBUF;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
-                const int n = sb.part[r].j1 - sb.part[r].j0;
+                const int n = sb.part[r].j1 - sb.part[r].j0, nar = sb.part[r].nar;
                 mbar_arrive(&sb.part_empty[r]);
                 if (n == 0) break;
                 if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
@@ -365,7 +369,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     tc_fence_after();
                     const uint32_t baddr = smem_u32(sm + C::OFF_KV + kv.i * C::SLOT) + (dpi ? C::KTILE : 0);
                     tcx::mma_kmajor_dh<D>(dpi ? tmem + C::COL_Y + ys * 64 : tmem + C::COL_X + xs * 64, aaddr, 128, baddr,
-                                          64, id_s, 0);
+                                          64, j < nar ? id_n : id_s, 0);
                     mma_commit(&sb.x_full[xs]);
                     issued = true;
                     kv.next(C::NSLOT);
@@ -387,7 +391,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts, ob = np % C::NACC;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
-                const int n = sb.part[r].j1 - sb.part[r].j0;
+                const int n = sb.part[r].j1 - sb.part[r].j0, nar = sb.part[r].nar;
                 mbar_arrive(&sb.part_empty[r]);
                 if (n == 0) break;
                 if (!wait(&sb.o_empty[ob], empty_par(np / C::NACC))) break;
@@ -401,9 +405,11 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     const uint32_t kaddr = smem_u32(sm + C::OFF_KV + kv.i * C::SLOT);
                     const uint64_t kd = smem_desc(kaddr, C::SKEY, 1024, 2);      // K: keys x D, D along N
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
+                    for (int ks = 0; ks < 4; ++ks) {
+                        if (ks == 2 && j < nar) break;
                         tc::mma_bf16_ts(tmem + C::COL_ACC + ob * D, tmem + C::COL_X + xs * 64 + 8 * ks, kd + 128 * ks, id_acc,
                                         (ks > 0 || j > 0) ? 1u : 0u);
+                    }
                     mma_commit(&sb.x_empty[xs]);
                     mma_commit(&sb.kv_empty[kv.i]);       // S and dP are complete before ds exists
                     issued = true;
@@ -437,7 +443,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             tc_fence_after();
             const uint32_t acc = tmem + lane_base + C::COL_ACC + ob * D;
             if (pend_slot < 0)
-                store_rows_bf16<D>(acc, a.dq, pend_row);
+                store_rows_bf16<D>(acc, a.dq, D, pend_row);
             else
                 store_rows_f32<D>(acc, a.partA + ((size_t)pend_slot * 128 + row) * D, pend_row >= 0);
             tc_fence_before();
@@ -450,7 +456,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const int r = np % kParts;
             if (!wwait(&sb.part_full[r], full_par(np / kParts))) break;
             const Part& w = sb.part[r];
-            const int j0 = w.j0, j1 = w.j1, p0 = w.mt * sc.TM;
+            const int j0 = w.j0, j1 = w.j1, nar = w.nar, p0 = w.mt * sc.TM;
             if (j0 == j1) break;
             if (!wwait(&sb.vec_full, full_par(np))) break;
             const float* vec = reinterpret_cast<const float*>(sm + C::OFF_VEC);
@@ -466,12 +472,18 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 tc_fence_after();
                 const int kbase = w.tile(j) * 64;
                 // every row sees the whole tile, unless the diagonal or the window's edge crosses it
+                const bool narrow = j - j0 < nar;
                 const bool edge = kbase + 63 > p0 || (kbase < plast - sc.W + 1 && kbase + 63 >= sc.ns);
                 const uint32_t xb = tmem + lane_base + C::COL_X + xs * 64;
                 const uint32_t yb = tmem + lane_base + C::COL_Y + ys * 64;
                 const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
 #pragma unroll
                 for (int pc = 0; pc < 2; ++pc) {
+                    if (pc == 1 && narrow) {                      // (columns that no product wrote)
+                        tc_fence_before();
+                        mbar_arrive(&sb.y_empty[ys]);
+                        break;
+                    }
                     // keys kbase + 32 pc .. + 31: S (X columns 32 pc ..) and dP (Y columns 32 pc ..)
                     uint32_t r0[16], r1[16], r2[16], r3[16];
                     tmem_ld_32x32b_x16(xb + 32 * pc, r0);
@@ -621,7 +633,7 @@ struct __align__(16) Bars {
     uint64_t done[3];
     uint32_t tmem;
     StreamPos pos;
-    int wsum[12];
+    int wsum[20];
 };
 
 __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wid) {
@@ -647,7 +659,7 @@ __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wi
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsB, 1)
 sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                    const BwdArgs a) {
@@ -664,7 +676,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (threadIdx.x == 0) {
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sb.part_full[i], 1);
-            mbar_init(&sb.part_empty[i], 3 + 8);          // the issuers and the math warps
+            mbar_init(&sb.part_empty[i], 3 + 16);          // the issuers and the math warps
         }
         for (int i = 0; i < C::IBUF; ++i) {
             mbar_init(&sb.it_full[i], 1);
@@ -678,11 +690,11 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mbar_init(&sb.x_full[i], 2);
             mbar_init(&sb.x_empty[i], 1);
         }
-        for (int i = 0; i < C::NY; ++i) mbar_init(&sb.y_empty[i], 128);
-        for (int i = 0; i < 4; ++i) mbar_init(&sb.p_full[i], 128);
+        for (int i = 0; i < C::NY; ++i) mbar_init(&sb.y_empty[i], 256);
+        for (int i = 0; i < 4; ++i) mbar_init(&sb.p_full[i], 256);
         mbar_init(&sb.o_full[0], 1);
         mbar_init(&sb.o_full[1], 1);
-        mbar_init(&sb.o_empty, 128);
+        mbar_init(&sb.o_empty, 256);
         for (int i = 0; i < 3; ++i) mbar_init(&sb.done[i], 1);
         fence_barrier_init();
         prefetch_tmap(&tq);
@@ -694,7 +706,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares<kThreads, 1>(sc.B, a.nKT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; }, [&](int, int kt) {
+    find_shares<kThreadsB, 1>(sc.B, a.nKT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; }, [&](int, int kt) {
         const Blocks k = blocks(sc, kt);
         return sc.G * (k.nw + k.nf);
     });
@@ -762,9 +774,9 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (n > 0) wait_copy(&sb.it_full[q], full_par(n - 1));
             }
         }
-    } else if (warp == 1 || warp == 11) {
-        // ------------------------------------------------------------ warp 1: S^T = K Q^T, warp 11: dP^T = V dO^T
-        const bool dpi = warp == 11;
+    } else if (warp == 1 || warp == 3) {
+        // ------------------------------------------------------------ warp 1: S^T = K Q^T, warp 3: dP^T = V dO^T
+        const bool dpi = warp == 3;
         if (lane == 0) {
             Ring st{0, 0};
             int u = 0;
@@ -820,16 +832,16 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     const int xs = u % C::NX;
                     if (!wait(&sb.p_full[u & 3], full_par(u >> 2))) { ok = false; break; }
                     tc_fence_after();
-                    // A: K = 16 query steps at X columns 0, 8, 32, 40 (ds^T) and 16, 24, 48, 56 (P^T);
+                    // A: K = 16 query steps at X columns 0, 16, 32, 48 (ds^T) and 8, 24, 40, 56 (P^T);
                     // B: queries x D with D along N
                     const uint64_t qd = smem_desc(smem_u32(sm + C::OFF_ST + st.i * C::SLOT), C::SQ, 1024, 2);
                     const uint32_t xa = tmem + C::COL_X + xs * 64;
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
-                        const uint32_t col = xa + (ks >> 1) * 32 + (ks & 1) * 8;
+                        const uint32_t col = xa + 16 * ks;
                         const uint32_t acc = (ks > 0 || j > 0) ? 1u : 0u;
                         tc::mma_bf16_ts(tmem + C::COL_ACC, col, qd + 128 * ks, id_acc, acc);
-                        tc::mma_bf16_ts(tmem + C::COL_ACC + D, col + 16, qd + (C::QTILE >> 4) + 128 * ks, id_acc, acc);
+                        tc::mma_bf16_ts(tmem + C::COL_ACC + D, col + 8, qd + (C::QTILE >> 4) + 128 * ks, id_acc, acc);
                     }
                     mma_commit(&sb.x_empty[xs]);
                     mma_commit(&sb.st_empty[st.i]);
@@ -846,7 +858,8 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     } else {
         // ------------------------------------------------------------ math warpgroups
         auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
-        const int wg = (warp - 3) >> 2;
+        // warpgroup pair `wg` takes every other step; `half` of a step's columns each
+        const int wg = (warp - 4) >> 3, half = (warp >> 2) & 1;
         const int qd = warp & 3;
         const int row = 32 * qd + lane;               // key row of the tile = lane of tensor memory
         const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
@@ -888,51 +901,39 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     mbar_arrive(&sb.y_empty[ys]);
                     const uint32_t z[16] = {};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_st_32x32b_x16(xb + 16 * c, z);
+                    for (int c = 0; c < 2; ++c) tmem_st_32x32b_x16(xb + 32 * half + 16 * c, z);
                 } else {
+                    // this warpgroup's 32 queries, 16 at a time
 #pragma unroll
-                    for (int pc = 0; pc < 2; ++pc) {
-                        // queries qb + 32 pc .. + 31 of this key row
-                        uint32_t r0[16], r1[16], r2[16], r3[16];
-                        tmem_ld_32x32b_x16(xb + 32 * pc, r0);
-                        tmem_ld_32x32b_x16(xb + 32 * pc + 16, r1);
-                        tmem_ld_32x32b_x16(yb + 32 * pc, r2);
-                        tmem_ld_32x32b_x16(yb + 32 * pc + 16, r3);
+                    for (int cc = 0; cc < 2; ++cc) {
+                        const int c = 2 * half + cc;
+                        uint32_t rs[16], rd[16];
+                        tmem_ld_32x32b_x16(xb + 16 * c, rs);
+                        tmem_ld_32x32b_x16(yb + 16 * c, rd);
                         tmem_wait_ld();
-                        if (pc == 1) {
+                        if (cc == 1) {
                             tc_fence_before();
                             mbar_arrive(&sb.y_empty[ys]);
                         }
-                        const uint32_t vis = below(c_hi + 1 - 32 * pc) & ~below(c_lo - 32 * pc);
-                        uint32_t pd[16], pp[16];
-                        auto body = [&](bool msk) {
+                        const uint32_t vis = all ? 0xffffu : (below(c_hi + 1 - 16 * c) & ~below(c_lo - 16 * c));
+                        uint32_t pd[8], pp[8];
 #pragma unroll
-                            for (int p2 = 0; p2 < 16; ++p2) {
-                                const uint32_t* rs = p2 < 8 ? r0 : r1;
-                                const uint32_t* rd = p2 < 8 ? r2 : r3;
-                                const int tt = 2 * (p2 & 7);
-                                float y0, y1;
-                                tcx::f2_unpack(
-                                    tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[tt]), __uint_as_float(rs[tt + 1])), sl2,
-                                               nl[16 * pc + p2]), y0, y1);
-                                float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
-                                if (msk) {
-                                    e0 = (vis >> (2 * p2) & 1u) ? e0 : 0.f;
-                                    e1 = (vis >> (2 * p2 + 1) & 1u) ? e1 : 0.f;
-                                }
-                                const uint64_t ev = tcx::f2_pack(e0, e1);
-                                const uint64_t gd = tcx::ffma2(
-                                    tcx::f2_pack(__uint_as_float(rd[tt]), __uint_as_float(rd[tt + 1])), sc2,
-                                    nd[16 * pc + p2]);
-                                pd[p2] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
-                                pp[p2] = tcx::pack_bf16x2(ev);
-                            }
-                        };
-                        if (all) body(false);
-                        else body(true);
-                        // ds^T, then P^T, over the 32 S^T columns just read
-                        tmem_st_32x32b_x16(xb + 32 * pc, pd);
-                        tmem_st_32x32b_x16(xb + 32 * pc + 16, pp);
+                        for (int i = 0; i < 8; ++i) {
+                            float y0, y1;
+                            tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
+                                                      sl2, nl[8 * c + i]), y0, y1);
+                            float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
+                            e0 = (vis >> (2 * i) & 1u) ? e0 : 0.f;
+                            e1 = (vis >> (2 * i + 1) & 1u) ? e1 : 0.f;
+                            const uint64_t ev = tcx::f2_pack(e0, e1);
+                            const uint64_t gd = tcx::ffma2(tcx::f2_pack(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])),
+                                                           sc2, nd[8 * c + i]);
+                            pd[i] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
+                            pp[i] = tcx::pack_bf16x2(ev);
+                        }
+                        // ds^T, then P^T, over the 16 S^T columns just read
+                        tmem_st_32x32b_x8(xb + 16 * c, pd);
+                        tmem_st_32x32b_x8(xb + 16 * c + 8, pp);
                     }
                 }
                 tmem_wait_st();
@@ -943,17 +944,13 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if ((np & 1) == wg) {                     // this part's sums of key s
                 if (!wwait(&sb.o_full[wg], full_par(np >> 1))) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + lane_base + C::COL_ACC;
+                // dK rows by one warpgroup of the pair, dV rows by the other
+                const uint32_t acc = tmem + lane_base + C::COL_ACC + half * D;
                 const bool live = s < sc.L;
-                if (w.slot < 0) {
-                    const int orow = live ? (w.b * sc.L + s) * sc.Hkv + w.h : -1;
-                    store_rows_bf16<D>(acc, a.dk, orow);
-                    store_rows_bf16<D>(acc + D, a.dv, orow);
-                } else {
-                    float* dst = a.partB + ((size_t)w.slot * 256 + row) * D;
-                    store_rows_f32<D>(acc, dst, live);
-                    store_rows_f32<D>(acc + D, dst + 128 * D, live);
-                }
+                if (w.slot < 0)
+                    store_rows_bf16<D>(acc, half ? a.dv : a.dk, D, live ? (w.b * sc.L + s) * sc.Hkv + w.h : -1);
+                else
+                    store_rows_f32<D>(acc, a.partB + ((size_t)w.slot * 256 + half * 128 + row) * D, live);
                 tc_fence_before();
                 mbar_arrive(&sb.o_empty);             // the next part may accumulate now
             }
@@ -1051,13 +1048,13 @@ cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[
                                   pa::Cfg<D>::SMEM)) != cudaSuccess)
         return e;
     GCA_LAUNCH("sink_bwd_q", st,
-               e = launch_pdl(pa::sink_bwd_q_kernel<D>, dim3(grid), kThreads, pa::Cfg<D>::SMEM, st, m[0], m[1], m[2], m[3], a));
+               e = launch_pdl(pa::sink_bwd_q_kernel<D>, dim3(grid), kThreadsA, pa::Cfg<D>::SMEM, st, m[0], m[1], m[2], m[3], a));
     if (e != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   pb::Cfg<D>::SMEM)) != cudaSuccess)
         return e;
     GCA_LAUNCH("sink_bwd_kv", st,
-               e = launch_pdl(pb::sink_bwd_kv_kernel<D>, dim3(grid), kThreads, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
+               e = launch_pdl(pb::sink_bwd_kv_kernel<D>, dim3(grid), kThreadsB, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
     if (e != cudaSuccess) return e;
     GCA_LAUNCH("sink_bwd_join", st,
                e = launch_pdl(sink_bwd_join_kernel<D>, dim3(grid, 128 * D / 1024, 3), 256, 0, st, a, grid));

@@ -264,6 +264,13 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         : "memory");
 }
 
+// The 8-column form of tmem_st_32x32b_x16.
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Store counterpart of tmem_ld_16x32bx2_x16: threads 0-15 write lanes taddr.lane+0..15
 // at columns taddr.col .. +15, threads 16-31 the same lanes at columns
 // taddr.col + half_off .. +15.  Complete with tmem_wait_st.
