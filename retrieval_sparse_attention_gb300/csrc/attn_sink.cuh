@@ -202,6 +202,12 @@ __device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity, int* s
     set_status(status, GCA_ERR_TIMEOUT);
     return false;
 }
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // Bounded wait for work in flight at the end.
 __device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) { wait_ctrl(bar, parity, nullptr); }
 

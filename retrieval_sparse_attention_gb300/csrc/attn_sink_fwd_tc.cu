@@ -459,8 +459,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (!wwait(&sb.p_full[i], full_par(cur.tp))) break;
                 const bool narrow = cur.j < cur.nar;
                 ++cur.j;
-                if (lane == 0) {
-                    tc_fence_after();
+                tc_fence_after();
+                if (elect_one()) {
                     const uint32_t to = tmem + C::COL_O + i * D, tp = tmem + C::COL_P + i * C::P_STEP;
                     const uint64_t vd = smem_desc(smem_u32(vt), C::STILE, 1024, 2);   // V: keys x D, D along N
 #pragma unroll
@@ -481,7 +481,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             cur = oth;
             oth = t;
         }
-        if (issued && lane == 0) {
+        if (issued && elect_one()) {
             mma_commit(&sb.done2);
             wait_copy(&sb.done2, 0);
         }
