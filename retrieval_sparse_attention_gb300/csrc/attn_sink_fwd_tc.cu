@@ -102,6 +102,7 @@ struct __align__(16) Part {
     int p0, p1, end;         // positions of the first and the last token, and behind the sequence
     int k0, nsk, nw;         // key tiles: nsk of sinks from 0 on, nw of the window from k0 on
     int j0, j1;
+    int f0, f1, fl;          // tiles that every row sees whole: f0 <= j < f1, and j = fl
     int slot;                // -1: the whole unit; else the workspace slot of its sums
     int nar;                 // key tiles j < nar (one or none) are narrow: 32 columns hold all sinks
     // The sinks come first and the window's first tile, which its edge crosses, last: the
@@ -159,6 +160,11 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     u.nw = k.nt - k.nsk;
     u.j0 = p.j;
     u.j1 = min(k.nt, p.j + p.left);
+    // whole tiles lie between that of the last row's first key and that of the first row's last
+    const int lo = (max(0, k.p1 - s.W + 1) + 127) >> 7, hi = ((k.p0 + 1) >> 7) - 1;
+    u.f0 = k.nsk + max(lo - k.k0 - 1, 0);
+    u.f1 = min(k.nsk + hi - k.k0, k.nt - 1);
+    u.fl = lo <= k.k0 && k.k0 <= hi ? k.nt - 1 : -1;
     u.nar = k.nsk == 1 && s.ns <= kNarrow;
     u.slot = u.j0 > 0 ? 2 * p.wid : (u.j1 < k.nt ? 2 * wid_tail + 1 : -1);
     if (u.j0 > 0) a.head[p.wid] = u.j1 < k.nt ? 2 : 1;  // what the join reads
@@ -503,7 +509,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const uint32_t tp_addr = tmem + lane_base + C::COL_P + wg * C::P_STEP;
         const float sl = a.scale_log2;
 
-        int ts = 0, ko = 0, np = 0, j = 0, j1 = 0;
+        int ts = 0, ko = 0, np = 0, j = 0, j1 = 0, f0 = 0, f1 = 0, fl = 0;
         bool first = true;                              // at the first tile of a part
         bool have = true, live = false, wlive = false;  // a tile to do; this row exists; some row of the warp does
         float m = -INFINITY, l = 0.f;                   // running max (of s * scale * log2(e)) and sum of exp2(. - m)
@@ -519,6 +525,9 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 ++np;
                 j = sb.part[wg][r].j0;
                 j1 = sb.part[wg][r].j1;
+                f0 = sb.part[wg][r].f0;
+                f1 = sb.part[wg][r].f1;
+                fl = sb.part[wg][r].fl;
                 have = j < j1;
                 // rows that do not exist are skipped, where a whole warp has no other
                 live = have && row < a.R && rt < sb.part[wg][r].ntok;
@@ -586,14 +595,14 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 }
                 tmem_wait_st();
             };
-            const int kbase = w.tile(j) * 128;
-            const bool narrow = j < w.nar;
             if (!wlive) {
                 if (!C::P_OVER_S) {
                     mbar_arrive(&sb.s_empty[wg]);
                     if (!wwait(&sb.p_empty[wg], empty_par(ts))) break;
                 }
-            } else if (narrow || kbase + 127 > w.p0 || (kbase < w.p1 - sc.W + 1 && kbase + 127 >= sc.ns)) {
+            } else if (!((j >= f0 && j < f1) || j == fl)) {
+                const int kbase = w.tile(j) * 128;
+                const bool narrow = j < w.nar;
                 // The diagonal or the window's edge crosses the tile, or it is the narrow one: 32
                 // columns at a time, in two rounds (maximum, weights).  Slower by the column than
                 // the path below, but little code: both together stay in the instruction cache.
