@@ -103,7 +103,7 @@ struct __align__(16) Part {
     int k0, nsk, nw;         // key tiles: nsk of sinks from 0 on, nw of the window from k0 on
     int j0, j1;
     int f0, f1, fl;          // tiles that every row sees whole: f0 <= j < f1, and j = fl
-    int slot;                // -1: the whole unit; else the workspace slot of its sums
+    int slot;                // -1: the whole unit; else the first of its sums' rows in the workspace
     int nar;                 // key tiles j < nar (one or none) are narrow: 32 columns hold all sinks
     // The sinks come first and the window's first tile, which its edge crosses, last: the
     // crossed tiles then mostly find a running maximum that they need not raise.
@@ -166,9 +166,9 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     u.f1 = min(k.nsk + hi - k.k0, k.nt - 1);
     u.fl = lo <= k.k0 && k.k0 <= hi ? k.nt - 1 : -1;
     u.nar = k.nsk == 1 && s.ns <= kNarrow;
-    u.slot = u.j0 > 0 ? 2 * p.wid : (u.j1 < k.nt ? 2 * wid_tail + 1 : -1);
+    u.slot = u.j0 > 0 ? 2 * p.wid * a.R : (u.j1 < k.nt ? (2 * wid_tail + 1) * a.R : -1);
     if (u.j0 > 0) a.head[p.wid] = u.j1 < k.nt ? 2 : 1;  // what the join reads
-    else if (u.slot >= 0) a.tail[wid_tail] = make_int4(p.b, p.mt, p.h, 1);
+    else if (u.j1 < k.nt) a.tail[wid_tail] = make_int4(p.b, p.mt, p.h, 1);
     p.left -= u.j1 - u.j0;
     p.j = 0;
     if (++p.h == s.Hkv) { p.h = 0; ++p.mt; }
@@ -516,7 +516,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // the finished part whose O still sits in tensor memory
         bool pend = false;
         int pend_row = -1;                              // token * H + head, or -1: no such row
-        int pend_slot = -1;                             // -1: whole unit; else the workspace slot of the part
+        int pend_slot = -1;                             // -1: whole unit; else the row in the workspace
         float pm = 0.f, pl = 1.f;
         while (true) {
             if (first) {                                // the next part of the share
@@ -554,14 +554,14 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             uint32_t r[16];
                             tmem_ld_32x32b_x16(to_addr + 16 * ci, r);
                             tmem_wait_ld();
-                            uint4* dst = reinterpret_cast<uint4*>(a.part_o + ((size_t)pend_slot * a.R + row) * D) + 4 * ci;
+                            uint4* dst = reinterpret_cast<uint4*>(a.part_o + (size_t)pend_slot * D) + 4 * ci;
                             if (wr)
 #pragma unroll
                                 for (int u = 0; u < 4; ++u)
                                     dst[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
                         }
                     }
-                    if (wr && pend_slot >= 0) a.part_ml[(size_t)pend_slot * a.R + row] = make_float2(pm, pl);
+                    if (wr && pend_slot >= 0) a.part_ml[pend_slot] = make_float2(pm, pl);
                     if (wr && pend_slot < 0 && a.lse) a.lse[pend_row] = pl > 0.f ? (pm + log2f(pl)) * kLn2 : -INFINITY;
                 }
                 tc_fence_before();
@@ -748,7 +748,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (first) {                                // this part of the unit is done: it leaves later
                 pend = true;
                 pend_row = live ? (w.qrow + rt) * sc.H + w.h * sc.G + rg : -1;
-                pend_slot = w.slot;
+                pend_slot = w.slot < 0 ? -1 : w.slot + row;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sb.part_empty[wg][(np - 1) % kParts]);
                 pm = m;
@@ -900,11 +900,13 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     CUtensorMap tq, tk, tv;
     const uint64_t kvcols = (uint64_t)s.Hkv * s.d;
     bool ok = encode_bf16_3d(&tq, q, s.d, s.H, s.T, s.d, s.q_stride, a.s.G, a.s.TM);
+    // (d = 64: a head's row is 128 bytes, and 256-byte L2 fetches would bring a neighbour head's row
+    // that another CTA reads at another time: one token over 18K, 12 heads: 0.39 -> 0.28 ms)
     for (int i = 0; i < 2; ++i) {
         CUtensorMap* m = i ? &tv : &tk;
         const void* p = i ? v : k;
-        ok = ok && (s.paged ? encode_bf16_3d(m, p, kvcols, s.page, s.n_pages, kvcols, kvcols * s.page, s.page, 1)
-                            : encode_bf16_3d(m, p, kvcols, s.L, s.B, s.kv_stride, (uint64_t)s.kv_stride * s.L, 128, 1));
+        ok = ok && (s.paged ? encode_bf16_3d(m, p, kvcols, s.page, s.n_pages, kvcols, kvcols * s.page, s.page, 1, s.d == 128)
+                            : encode_bf16_3d(m, p, kvcols, s.L, s.B, s.kv_stride, (uint64_t)s.kv_stride * s.L, 128, 1, s.d == 128));
     }
     if (!ok) return cudaErrorInvalidValue;
     int dev = 0, sms = 0;

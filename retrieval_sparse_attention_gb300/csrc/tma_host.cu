@@ -67,7 +67,7 @@ bool encode_bf16_seq(CUtensorMap* map, const void* base, uint64_t B, uint64_t L,
 }
 
 bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2,
-                    uint64_t stride1, uint64_t stride2, uint32_t box1, uint32_t box2) {
+                    uint64_t stride1, uint64_t stride2, uint32_t box1, uint32_t box2, bool wide) {
     std::call_once(g_once, resolve);
     if (!g_encode) return false;
     cuuint64_t dims[3] = {n0, n1, n2};
@@ -76,7 +76,7 @@ bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_SWIZZLE_128B, wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

@@ -28,9 +28,10 @@ bool encode_bf16_seq(CUtensorMap* map, const void* base, uint64_t B, uint64_t L,
 // Tensor map over a bf16 tensor of three dimensions (innermost first) whose two
 // outer strides are given in elements (multiples of 8), with a 128-byte swizzle
 // and a box whose innermost extent is 64 elements.  Elements outside the tensor
-// read as zeros and are not written.
+// read as zeros and are not written.  wide: L2 fetches 256 bytes around what a load
+// touches, else 128.
 bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2,
-                    uint64_t stride1, uint64_t stride2, uint32_t box1, uint32_t box2);
+                    uint64_t stride1, uint64_t stride2, uint32_t box1, uint32_t box2, bool wide = true);
 
 // The same over four dimensions.
 bool encode_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&n)[4], const uint64_t (&stride)[3],
