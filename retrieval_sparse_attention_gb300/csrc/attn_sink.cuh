@@ -211,25 +211,22 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait for work in flight at the end.
 __device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) { wait_ctrl(bar, parity, nullptr); }
 
-// 32 fp32 columns of this lane's row of an accumulator, times `scale`, as bf16 to global
-// memory: row `row` of `out` (rows of ld elements; row < 0: none), columns col .. + 31.
-// Four lanes exchange their rows' 16-byte pieces, so that each store writes 64
-// consecutive bytes of a row (with a row per lane the 32 lanes of a store touch 32
-// lines, and the stores of a tile cost as much as half a key tile).
-__device__ __forceinline__ void store_row32(uint32_t taddr, __nv_bfloat16* out, int ld, int col, int row, float scale) {
+// 32 fp32 columns of this lane's row of an accumulator, times `scale`, as bf16 pairs.
+__device__ __forceinline__ void load_row32(uint32_t taddr, float scale, uint32_t* pk) {
+    uint32_t r[32];
+    tc::tmem_ld_32x32b_x32(taddr, r);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+        pk[u] = tcx::pack_bf16(__uint_as_float(r[2 * u]) * scale, __uint_as_float(r[2 * u + 1]) * scale);
+}
+
+// Those to global memory: row `row` (rows of ld elements; row < 0: none) from out on.  Four
+// lanes exchange their rows' 16-byte pieces, so that each store writes 64 consecutive
+// bytes of a row (with a row per lane the 32 lanes of a store touch 32 lines, and the
+// stores of a tile cost as much as half a key tile).
+__device__ __forceinline__ void store_row32(uint32_t* q, __nv_bfloat16* out, int ld, int row) {
     const int lane = threadIdx.x & 31;
-    uint32_t q[4][4];
-    {
-        uint32_t r[32];
-        tc::tmem_ld_32x32b_x32(taddr, r);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                q[c][u] = tcx::pack_bf16(__uint_as_float(r[8 * c + 2 * u]) * scale,
-                                         __uint_as_float(r[8 * c + 2 * u + 1]) * scale);
-    }
 #pragma unroll
     for (int s = 1; s <= 2; s <<= 1) {
         const bool up = lane & s;
@@ -238,10 +235,10 @@ __device__ __forceinline__ void store_row32(uint32_t taddr, __nv_bfloat16* out, 
             if (c & s) continue;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const uint32_t give = up ? q[c][u] : q[c + s][u];
+                const uint32_t give = up ? q[4 * c + u] : q[4 * (c + s) + u];
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
-                if (up) q[c][u] = got;
-                else q[c + s][u] = got;
+                if (up) q[4 * c + u] = got;
+                else q[4 * (c + s) + u] = got;
             }
         }
     }
@@ -250,8 +247,8 @@ __device__ __forceinline__ void store_row32(uint32_t taddr, __nv_bfloat16* out, 
     for (int k = 0; k < 4; ++k) {
         const int rk = __shfl_sync(0xffffffffu, row, (lane & 28) + k);
         if (rk >= 0)
-            *reinterpret_cast<uint4*>(out + (size_t)rk * ld + col + 8 * (lane & 3)) =
-                make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
+            *reinterpret_cast<uint4*>(out + (size_t)rk * ld + 8 * (lane & 3)) =
+                make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
     }
 }
 

@@ -546,8 +546,11 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (__any_sync(0xffffffffu, wr)) {
                     if (pend_slot < 0) {
 #pragma unroll 1
-                        for (int ci = 0; ci < D / 32; ++ci)
-                            store_row32(to_addr + 32 * ci, a.o, D, 32 * ci, pend_row, inv);
+                        for (int ci = 0; ci < D / 32; ++ci) {
+                            uint32_t pk[16];
+                            load_row32(to_addr + 32 * ci, inv, pk);
+                            store_row32(pk, a.o + 32 * ci, D, pend_row);
+                        }
                     } else {
 #pragma unroll 1
                         for (int ci = 0; ci < D / 16; ++ci) {
