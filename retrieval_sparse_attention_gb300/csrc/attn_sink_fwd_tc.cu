@@ -603,80 +603,36 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     mbar_arrive(&sb.s_empty[wg]);
                     if (!wwait(&sb.p_empty[wg], empty_par(ts))) break;
                 }
-            } else if (!((j >= f0 && j < f1) || j == fl)) {
-                const int kbase = w.tile(j) * 128;
-                const bool narrow = j < w.nar;
-                // The diagonal or the window's edge crosses the tile, or it is the narrow one: 32
-                // columns at a time, in two rounds (maximum, weights).  Slower by the column than
-                // the path below, but little code: both together stay in the instruction cache.
-                const int nch = narrow ? 1 : 4;
-                const int p = w.p0 + rt;
-                // visible: columns c_lo .. c_hi (the window) and those below c_s (sinks)
-                const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
-                auto visible = [&](int c) {
-                    return (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
-                };
-                // the maximum over all columns bounds that over the visible ones: only where it would
-                // move the running one (or is no number) is the latter needed
-                bool exact = narrow;
-                if (!narrow) {
-                    uint32_t r[64];
-                    float mb = tmem_ld_max_32x32b_x64(ts_addr, r);
-                    tmem_wait_ld();
-                    const float mb2 = tmem_ld_max_32x32b_x64(ts_addr + 64, r);
-                    tmem_wait_ld();
-                    exact = __any_sync(0xffffffffu, !(mb * sl <= m + kRescaleLog2) || !(mb2 * sl <= m + kRescaleLog2));
-                }
-                float mt = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < (exact ? nch : 0); ++c) {
-                    const uint32_t vis = visible(c);
-                    if (!__any_sync(0xffffffffu, vis != 0)) continue;
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(ts_addr + 32 * c, r);
-                    tmem_wait_ld();
-                    float m4[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
+            } else if (j < w.nar) {
+                // The narrow tile: all sinks in its first columns, and every row behind them.  (A
+                // unit's first tile: no O to rescale.)
+                uint32_t r[32], pk[16];
+                tmem_ld_32x32b_x32(ts_addr, r);
+                tmem_wait_ld();
+                tc_fence_before();
+                if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        m4[i & 3] = fmaxf(m4[i & 3], (vis >> i & 1u) ? __uint_as_float(r[i]) : -INFINITY);
-                    mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                for (int i = 0; i < 32; ++i) {
+                    r[i] = i < sc.ns ? r[i] : 0xff800000u;
+                    m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(r[i]));
                 }
-                follow(mt * sl);
-                const float mu = (m == -INFINITY) ? 0.f : m;
+                follow(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl);
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * i]), sl, -m));
+                    const float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * i + 1]), sl, -m));
+                    l4[2 * (i & 1)] += e0;
+                    l4[2 * (i & 1) + 1] += e1;
+                    pk[i] = tcx::pack_bf16(e0, e1);
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
-                rescale();
-#pragma unroll 1
-                for (int c = 0; c < nch; ++c) {
-                    const uint32_t vis = visible(c);
-                    uint32_t pk[16] = {};
-                    if (__any_sync(0xffffffffu, vis != 0)) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(ts_addr + 32 * c, r);
-                        tmem_wait_ld();
-                        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * i]), sl, -mu));
-                            float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * i + 1]), sl, -mu));
-                            e0 = (vis >> (2 * i) & 1u) ? e0 : 0.f;
-                            e1 = (vis >> (2 * i + 1) & 1u) ? e1 : 0.f;
-                            l4[2 * (i & 1)] += e0;
-                            l4[2 * (i & 1) + 1] += e1;
-                            pk[i] = tcx::pack_bf16(e0, e1);
-                        }
-                        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                    }
-                    // (P over S: these columns of S have been read)
-                    tmem_st_32x32b_x16(tp_addr + 16 * c, pk);
-                }
+                tmem_st_32x32b_x16(tp_addr, pk);
                 tmem_wait_st();
-                if (!C::P_OVER_S) {
-                    tc_fence_before();
-                    mbar_arrive(&sb.s_empty[wg]);
-                }
             } else {
-                // Every row sees the whole tile: its row of S into registers at once, the
-                // maximum from the load.
+                // The row of S into registers at once, the maximum from the load.
                 float x[128];
                 {
                     uint32_t r[2][64];
@@ -690,9 +646,31 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         for (int u = 0; u < 64; ++u) x[64 * ci + u] = __uint_as_float(r[ci][u]);
                     tc_fence_before();
                     if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
-                    follow(fmaxf(mc[0], mc[1]) * sl);
+                    float mt = fmaxf(mc[0], mc[1]);
+                    if (!((j >= f0 && j < f1) || j == fl)) {
+                        // The diagonal or the window's edge crosses the tile.  Visible: columns c_lo ..
+                        // c_hi (the window) and those below c_s (sinks), as bits.
+                        const int p = w.p0 + rt, kbase = w.tile(j) * 128;
+                        const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t vis = (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : -INFINITY;
+                        }
+                        // the maximum over all columns bounds that over the visible ones: only where it
+                        // would move the running one (or is no number) is the latter needed
+                        if (__any_sync(0xffffffffu, !(mt * sl <= m + kRescaleLog2))) {
+                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+                            mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                        }
+                    }
+                    follow(mt * sl);
                 }
-                const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(-m, -m);
+                const float mu = m == -INFINITY ? 0.f : m;
+                const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(-mu, -mu);
                 uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t pka[32];                       // the first 64 keys' P, formed before the wait for the P buffer
 #pragma unroll
