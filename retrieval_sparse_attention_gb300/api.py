@@ -196,10 +196,8 @@ def _same_device(*ts):
     """The entries launch on the current device's stream: tensors of another device (or of
     none) would be read through a foreign address.  Returns the device index."""
     dev = ts[0].get_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be CUDA tensors on the current device")
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch.cuda.current_device() or \
+            any([t is not None and t.get_device() != dev for t in ts]):
         raise ValueError("tensors must be CUDA tensors on the current device")
     return dev
 
@@ -336,29 +334,18 @@ def gca_paged_attn(params: GcaPagedParams, q, k_cache, v_cache, cu_q, kv_len, ta
 
 
 @functools.lru_cache(maxsize=256)
-def _paged_plan(ts, tst, k_cache, v_cache, table, cu_q, kv_len, dtypes, attend, max_q, window, sinks,
-                attn_scale):
-    """What a paged call derives from shapes, strides and types alone (each cache or index
-    tensor comes as its shape and stride): parameters and workspace size."""
-    dt = dtypes[0]
-    if dtypes[1] != dt or dtypes[2] != dt:
+def _paged_plan(ts, tst, cache, v_cache, table, cu_q, kv_len, dt, k_dt, v_dt, attend, max_q, window,
+                sinks, attn_scale):
+    """What a paged call derives from shapes, strides and types alone: parameters and
+    workspace size."""
+    if k_dt != dt or v_dt != dt:
         raise TypeError("the caches must have the token tensors' dtype")
-    if any(t != torch.int32 for t in dtypes[3:6]):
-        raise TypeError("table, cu_q and kv_len must be int32")
-    if len(k_cache[0]) != 4 or len(table[0]) != 2:
+    if len(cache) != 4 or len(table) != 2:
         raise ValueError("caches must be [n_pages, page, Hkv, d] and table [B, table_width]")
-    n_pages, page, Hkv, d = k_cache[0]
-    B, width = table[0]
-    for name, (shape, stride), want in (("k_cache", k_cache, k_cache[0]), ("v_cache", v_cache, k_cache[0]),
-                                        ("table", table, (B, width)), ("cu_q", cu_q, (B + 1,)),
-                                        ("kv_len", kv_len, (B,))):
-        dense = 1
-        for n, s in zip(reversed(shape), reversed(stride)):
-            if n != 1 and s != dense:
-                raise ValueError("%s must be contiguous" % name)
-            dense *= n
-        if tuple(shape) != tuple(want):
-            raise ValueError("%s must have shape %s" % (name, tuple(want)))
+    n_pages, page, Hkv, d = cache
+    B, width = table
+    if v_cache != cache or tuple(cu_q) != (B + 1,) or tuple(kv_len) != (B,):
+        raise ValueError("v_cache must be like k_cache, cu_q [%d] and kv_len [%d]" % (B + 1, B))
     if len(ts) != 3 or ts[2] != d or (not attend and ts[1] != Hkv):
         raise ValueError("token tensors must be [T, heads, d] like the cache")
     step = _token_stride(ts, tst)
@@ -370,11 +357,15 @@ def _paged_plan(ts, tst, k_cache, v_cache, table, cu_q, kv_len, dtypes, attend, 
 
 
 def _paged_args(tok, k_cache, v_cache, table, cu_q, kv_len, attend, max_q, window=0, sinks=0, attn_scale=0.0):
-    return _paged_plan(tok.shape, tok.stride(), (k_cache.shape, k_cache.stride()),
-                       (v_cache.shape, v_cache.stride()), (table.shape, table.stride()),
-                       (cu_q.shape, cu_q.stride()), (kv_len.shape, kv_len.stride()),
-                       (tok.dtype, k_cache.dtype, v_cache.dtype, table.dtype, cu_q.dtype, kv_len.dtype),
-                       attend, max_q, window, sinks, float(attn_scale))
+    i32 = torch.int32
+    if table.dtype != i32 or cu_q.dtype != i32 or kv_len.dtype != i32:
+        raise TypeError("table, cu_q and kv_len must be int32")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and table.is_contiguous() and
+            cu_q.is_contiguous() and kv_len.is_contiguous()):
+        raise ValueError("the caches, table, cu_q and kv_len must be contiguous")
+    return _paged_plan(tok.shape, tok.stride(), k_cache.shape, v_cache.shape, table.shape, cu_q.shape,
+                       kv_len.shape, tok.dtype, k_cache.dtype, v_cache.dtype, attend, max_q, window, sinks,
+                       attn_scale)
 
 
 def paged_append(k_new, v_new, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0):

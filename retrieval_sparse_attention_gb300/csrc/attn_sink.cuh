@@ -4,8 +4,11 @@
 
 #include <stdint.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "gca.h"
+#include "kernels.h"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -272,6 +275,32 @@ inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
 }
+
+// What a launch needs of the current device and context, looked up once for each: the
+// kernels' attributes are set in a context, so a new one (after cudaDeviceReset, for
+// instance) sets them again.
+struct LaunchSetup {
+    std::mutex mu;
+    unsigned long long ctx = 0;
+    int dev = -1, sms = 0;
+    // Runs `set` (cudaError_t()) unless it has run for the current device and context.
+    template <class F>
+    cudaError_t once(F set, int* sms_out) {
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lock(mu);
+        const unsigned long long c = current_context_id();
+        if (c == 0 || c != ctx || d != dev) {
+            if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d)) != cudaSuccess) return e;
+            if ((e = set()) != cudaSuccess) return e;
+            ctx = current_context_id();
+            dev = d;
+        }
+        *sms_out = sms;
+        return cudaSuccess;
+    }
+};
 
 // Parts of an item that begins in worker w's share and goes on in the next ones: w's own
 // and those of the workers behind it up to the first whose head is not a middle part.

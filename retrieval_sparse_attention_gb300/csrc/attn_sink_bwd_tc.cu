@@ -1077,21 +1077,27 @@ Layout layout(const SinkShape& s) {
 }
 
 template <int D>
-cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[8], int grid, cudaStream_t st,
+cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[8], cudaStream_t st,
                    int* launches) {
-    cudaError_t e;
+    static LaunchSetup setup;
+    int sms = 0;
+    cudaError_t e = setup.once(
+        [] {
+            const cudaError_t r = cudaFuncSetAttribute(pa::sink_bwd_q_kernel<D>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, pa::Cfg<D>::SMEM);
+            if (r != cudaSuccess) return r;
+            return cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        pb::Cfg<D>::SMEM);
+        },
+        &sms);
+    if (e != cudaSuccess) return e;
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
     const dim3 vgrid((unsigned)(s.B * (a.Lp / 32)), (unsigned)((s.H + 7) / 8));
     GCA_LAUNCH("sink_bwd_vec", st, sink_bwd_vec_kernel<D><<<vgrid, 256, 0, st>>>(a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(pa::sink_bwd_q_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  pa::Cfg<D>::SMEM)) != cudaSuccess)
-        return e;
     GCA_LAUNCH("sink_bwd_q", st,
                e = launch_pdl(pa::sink_bwd_q_kernel<D>, dim3(grid), kThreadsA, pa::Cfg<D>::SMEM, st, m[0], m[1], m[2], m[3], a));
     if (e != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  pb::Cfg<D>::SMEM)) != cudaSuccess)
-        return e;
     GCA_LAUNCH("sink_bwd_kv", st,
                e = launch_pdl(pb::sink_bwd_kv_kernel<D>, dim3(grid), kThreadsB, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
     if (e != cudaSuccess) return e;
@@ -1157,11 +1163,7 @@ cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, co
         ok = ok && encode_bf16_3d(&m[2 + 4 * i], k, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1) &&
              encode_bf16_3d(&m[3 + 4 * i], v, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1);
     if (!ok) return cudaErrorInvalidValue;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    return s.d == 64 ? launch<64>(s, a, m, grid, st, launches) : launch<128>(s, a, m, grid, st, launches);
+    return s.d == 64 ? launch<64>(s, a, m, st, launches) : launch<128>(s, a, m, st, launches);
 }
 
 }  // namespace gca

@@ -815,16 +815,23 @@ Layout layout(const SinkShape& s) {
 
 template <int D, bool PAGED>
 cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                   const CUtensorMap& tv, int grid, cudaStream_t st, int* launches) {
+                   const CUtensorMap& tv, cudaStream_t st, int* launches) {
     using C = Cfg<D>;
-    // the setmaxnreg split needs the whole launch allocation: refuse to launch a build that
-    // gave the kernel fewer registers a thread (its warps would wait forever)
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, sink_fwd_tc_kernel<D, PAGED>);
+    static LaunchSetup setup;
+    int sms = 0;
+    cudaError_t e = setup.once(
+        [] {
+            // the setmaxnreg split needs the whole launch allocation: refuse to launch a build that
+            // gave the kernel fewer registers a thread (its warps would wait forever)
+            cudaFuncAttributes fa;
+            const cudaError_t r = cudaFuncGetAttributes(&fa, sink_fwd_tc_kernel<D, PAGED>);
+            if (r != cudaSuccess) return r;
+            if (fa.numRegs * kThreads < 128 * kRegsCtrl + 256 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
+            return cudaFuncSetAttribute(sink_fwd_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        },
+        &sms);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs * kThreads < 128 * kRegsCtrl + 256 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(sink_fwd_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
     GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D, PAGED><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *launches += 1;
@@ -890,15 +897,11 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
                             : encode_bf16_3d(m, p, kvcols, s.L, s.B, s.kv_stride, (uint64_t)s.kv_stride * s.L, 128, 1, s.d == 128));
     }
     if (!ok) return cudaErrorInvalidValue;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
     if (s.paged)
-        return s.d == 64 ? launch<64, true>(a, tq, tk, tv, grid, st, launches)
-                         : launch<128, true>(a, tq, tk, tv, grid, st, launches);
-    return s.d == 64 ? launch<64, false>(a, tq, tk, tv, grid, st, launches)
-                     : launch<128, false>(a, tq, tk, tv, grid, st, launches);
+        return s.d == 64 ? launch<64, true>(a, tq, tk, tv, st, launches)
+                         : launch<128, true>(a, tq, tk, tv, st, launches);
+    return s.d == 64 ? launch<64, false>(a, tq, tk, tv, st, launches)
+                     : launch<128, false>(a, tq, tk, tv, st, launches);
 }
 
 }  // namespace gca

@@ -52,7 +52,7 @@ def rows(q, k, v, qpos, kpos, window, sinks, scale=None):
 
 def forward(q, k, v, window, sinks, scale=None):
     """[B, L, H, d] -> o, lse, bounds."""
-    pos = torch.arange(q.shape[1])
+    pos = torch.arange(q.shape[1], device=q.device)
     out = [rows(q[b], k[b], v[b], pos, pos, window, sinks, scale) for b in range(q.shape[0])]
     return [torch.stack(x) for x in zip(*out)]
 
@@ -64,7 +64,7 @@ def backward(q, k, v, o, lse, g, window, sinks, scale=None):
     Hkv = k.shape[2]
     G = H // Hkv
     scale = d ** -0.5 if not scale else scale
-    pos = torch.arange(L)
+    pos = torch.arange(L, device=q.device)
     see = visible(pos, pos, window, sinks)
     res, bnd = [], []
     for b in range(B):

@@ -89,6 +89,21 @@ def test_long_cache_split_over_the_machine():
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("H,Hkv,d,page,window,sinks", [(8, 2, 128, 64, 0, 0), (12, 12, 64, 16, 512, 4),
+                                                       (6, 2, 64, 128, 700, 40), (4, 4, 128, 32, 100, 1)])
+def test_serving_batch(H, Hkv, d, page, window, sinks):
+    # many sequences of all kinds together: shares of many units, whole and cut
+    g = torch.Generator().manual_seed(d + page)
+    n = 40
+    qs = [int(x) for x in torch.tensor([0, 1, 1, 1, 7, 130, 300, 513])[torch.randint(8, (n,), generator=g)]]
+    kvs = [max(q, int(x)) for q, x in zip(qs, torch.randint(1, 3000, (n,), generator=g))]
+    c = Cache(qs, kvs, H, Hkv, d, page, seed=7)
+    o, lse = api.paged_attn(*c.cuda(), max_q=513, window=window, sinks=sinks, with_lse=True)
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == 0
+    c.check(o, lse, window, sinks)
+
+
 def test_tokens_before_the_first_position_see_nothing():
     c = Cache([5, 4], [3, 0], 2, 1, 64, 16)
     o, lse = api.paged_attn(*c.cuda(), with_lse=True)

@@ -164,6 +164,30 @@ def test_other_stream_and_graph():
     assert all(torch.equal(x, y) for x, y in zip(want + gw, got + gg))
 
 
+# enough key tiles for shares of many units, whole and cut, and for a sink's long item to be
+# spread over many shares; the 64-bit reference on the GPU
+@pytest.mark.parametrize("B,L,H,Hkv,d,window,sinks", [(2, 4000, 12, 12, 64, 512, 4), (2, 3001, 8, 2, 128, 700, 16),
+                                                      (1, 5003, 6, 1, 64, 1200, 40), (3, 2500, 5, 5, 128, 130, 1),
+                                                      (1, 6000, 4, 2, 64, 6000, 0), (5, 1900, 9, 3, 64, 257, 200)])
+def test_every_element_of_longer_rows(B, L, H, Hkv, d, window, sinks):
+    q, k, v, g = (x.cuda() for x in inputs(B, L, H, Hkv, d, seed=L))
+    o, lse = api.swa_sink_fwd(q, k, v, window=window, sinks=sinks)
+    grads = api.swa_sink_bwd(q, k, v, o, lse, g, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == 0
+    for b in range(B):
+        one = slice(b, b + 1)
+        ro, rl, bo, bl = ref.forward(q[one], k[one], v[one], window, sinks)
+        ref.within("o", o[one], ro.cpu(), bo.cpu())
+        ref.within("lse", lse[one], rl.cpu(), bl.cpu())
+        del ro, rl, bo, bl
+        want, bounds = ref.backward(q[one], k[one], v[one], o[one], lse[one], g[one], window, sinks)
+        for name, a, w, c in zip(("dq", "dk", "dv"), grads, want, bounds):
+            ref.within(name, a[one], w.cpu(), c.cpu())
+        del want, bounds
+    torch.cuda.empty_cache()
+
+
 def test_full_size_sampled():
     # the 12-head model's batch: single rows against the reference on what they see
     B, L, H, d, W, ns = 8, 16384, 12, 64, 512, 4
@@ -173,7 +197,9 @@ def test_full_size_sampled():
     dq, dk, dv = api.swa_sink_bwd(q, k, v, o, lse, g, window=W, sinks=ns)
     torch.cuda.synchronize()
     assert api.gca_get_status() == 0
-    for b, t in [(0, 0), (7, L - 1), (3, 511), (3, 515), (5, 128), (2, 9999), (6, 4097)]:
+    rng = torch.Generator().manual_seed(1)
+    some = [(int(torch.randint(B, (1,), generator=rng)), int(torch.randint(L, (1,), generator=rng))) for _ in range(40)]
+    for b, t in [(0, 0), (7, L - 1), (3, 511), (3, 515), (5, 128), (2, 9999), (6, 4097)] + some:
         kpos = torch.cat([torch.arange(min(ns, max(0, t - W + 1))), torch.arange(max(0, t - W + 1), t + 1)])
         qpos = torch.tensor([t])
         kk, vv = k[b].cpu()[kpos], v[b].cpu()[kpos]
