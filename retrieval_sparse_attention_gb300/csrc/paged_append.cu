@@ -6,28 +6,57 @@
 namespace gca {
 namespace {
 
-// One warp per new token: 16-byte vectors of its K and V rows.
+// One warp per row of the token tensors: the lanes look for the sequence that the row belongs
+// to, 32 at a time, then copy the row's 16-byte vectors, four of K and of V in flight
+// each.  Bound by memory: reads and writes every new row once.  (A warp for each of the
+// first max_q tokens of every sequence, without the search, took 20 us for eight chunks of
+// 0.9-2K tokens x 12 heads of 64, most of it for warps without a token; the search brings it to 16.)
 __global__ void __launch_bounds__(256)
 paged_append_kernel(PagedArgs p, const uint4* k_new, const uint4* v_new, int src_vec, int row_vec,
                     uint4* k_cache, uint4* v_cache, int B, int* status) {
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * warps + (threadIdx.x >> 5);
-    const int b = static_cast<int>(w / p.max_q), i = static_cast<int>(w % p.max_q);
-    if (b >= B) return;
-    const SeqInfo s = paged_seq(p, b, status);
-    if (i >= s.n) return;
-    const int pos = s.pos0 + i;
-    if (pos < 0) return;
-    const int pg = p.table[(size_t)b * p.width + (pos >> p.page_log2)];
+    const int lane = threadIdx.x & 31;
+    const int tid = blockIdx.x * blockDim.x + threadIdx.x;
+    const int row = tid >> 5;
+    // contradicting entries are reported whether a row belongs to them or not
+    for (int b = tid; b < B; b += gridDim.x * blockDim.x) paged_seq(p, b, status);
+    if (row >= p.T) return;
+    int seq = -1, pos = 0;
+    for (int b0 = 0; b0 < B && seq < 0; b0 += 32) {
+        SeqInfo s{0, 0, 0};
+        if (b0 + lane < B) s = paged_seq(p, b0 + lane, nullptr);
+        const unsigned hit = __ballot_sync(0xffffffffu, row >= s.row0 && row < s.row0 + s.n);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            seq = b0 + l;
+            pos = __shfl_sync(0xffffffffu, s.pos0 + row - s.row0, l);
+        }
+    }
+    if (seq < 0 || pos < 0) return;
+    const int pg = p.table[(size_t)seq * p.width + (pos >> p.page_log2)];
     if (pg < 0 || pg >= p.n_pages) {
         if (lane == 0) set_status(status, GCA_ERR_DEVICE_INDEX);
         return;
     }
     const size_t dst = (((size_t)pg << p.page_log2) + (pos & ((1 << p.page_log2) - 1))) * row_vec;
-    const size_t src = (size_t)(s.row0 + i) * src_vec;
-    for (int c = lane; c < row_vec; c += 32) {
-        k_cache[dst + c] = k_new[src + c];
-        v_cache[dst + c] = v_new[src + c];
+    const size_t src = (size_t)row * src_vec;
+    for (int c0 = 0; c0 < row_vec; c0 += 128) {
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + 32 * i + lane;
+            if (c < row_vec) {
+                x[i] = k_new[src + c];
+                y[i] = v_new[src + c];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + 32 * i + lane;
+            if (c < row_vec) {
+                k_cache[dst + c] = x[i];
+                v_cache[dst + c] = y[i];
+            }
+        }
     }
 }
 
@@ -38,9 +67,7 @@ cudaError_t launch_paged_append(const SinkShape& s, const void* k_new, const voi
                                 void* k_cache, void* v_cache, int* status, cudaStream_t st,
                                 int* launches) {
     PagedArgs p{cu_q, kv_len, table, s.T, s.max_q, __builtin_ctz(s.page), s.n_pages, s.width};
-    const long long warps = (long long)s.B * s.max_q;
-    const long long blocks = (warps + 7) / 8;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const long long blocks = ((long long)s.T + 7) / 8;
     GCA_LAUNCH("paged_append", st,
                paged_append_kernel<<<(unsigned)blocks, 256, 0, st>>>(
                    p, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), s.kv_stride / 8,
