@@ -534,10 +534,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 wlive = __any_sync(0xffffffffu, live);
             }
             const Part& w = sb.part[wg][(np - 1) % kParts];
-            if (have && !wwait(&sb.s_full[wg], full_par(ts))) break;
-            tc_fence_after();
-            // the previous part's output leaves once the next part's first S is there, which
-            // gives its last P V time to complete
+            // the previous part's output leaves while the next part's Q and first S are on their way
             if (first && pend) {
                 if (!wwait(&sb.o_full[wg], full_par(ko))) break;
                 tc_fence_after();
@@ -572,7 +569,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 ++ko;
                 pend = false;
             }
-            if (!have) break;
+            if (!have || !wwait(&sb.s_full[wg], full_par(ts))) break;
+            tc_fence_after();
             float alpha = 1.f;
             // the running maximum follows a tile's (in log2 units) only past a margin
             auto follow = [&](float mts) {
