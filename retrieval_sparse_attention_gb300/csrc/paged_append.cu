@@ -15,11 +15,11 @@ __global__ void __launch_bounds__(256)
 paged_append_kernel(PagedArgs p, const uint4* k_new, const uint4* v_new, int src_vec, int row_vec,
                     uint4* k_cache, uint4* v_cache, int B, int* status) {
     const int lane = threadIdx.x & 31;
-    const int tid = blockIdx.x * blockDim.x + threadIdx.x;
-    const int row = tid >> 5;
+    const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     // contradicting entries are reported whether a row belongs to them or not
-    for (int b = tid; b < B; b += gridDim.x * blockDim.x) paged_seq(p, b, status);
-    if (row >= p.T) return;
+    for (long long b = tid; b < B; b += (long long)gridDim.x * blockDim.x) paged_seq(p, (int)b, status);
+    if (tid >> 5 >= p.T) return;
+    const int row = (int)(tid >> 5);
     int seq = -1, pos = 0;
     for (int b0 = 0; b0 < B && seq < 0; b0 += 32) {
         SeqInfo s{0, 0, 0};
