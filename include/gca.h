@@ -318,7 +318,8 @@ size_t gca_swa_sink_bwd_workspace_size(const gca_swa_sink_params_t* params);
  * delta_t = dout_t . o_t and ds_ts = attn_scale p_ts (dout_t . v_s - delta_t):
  *   dq_t = sum_s ds_ts k_s,  dk_s = sum_t ds_ts q_t,  dv_s = sum_t p_ts dout_t,
  *   dk and dv summed over the query heads of the key head as well.
- *   q, k, v as in the forward; o, lse from it; dout [B, L, H, d] dense.
+ *   q, k, v as in the forward; o, lse from it; dout [B, L, H, d] dense; all of
+ *   them finite (a token's NaN may reach the gradients of tokens near it).
  *   dq [B, L, H, d]; dk, dv [B, L, Hkv, d]: dense, fully overwritten; fp32
  *   accumulation in a fixed order, no atomics (bitwise reproducible).
  *   workspace: >= gca_swa_sink_bwd_workspace_size() bytes, 256-byte aligned.
@@ -367,7 +368,8 @@ typedef struct {
  *   tokens whose page is not in [0, n_pages) are not written (the latter records
  *   GCA_ERR_DEVICE_INDEX); no other row of the cache changes.  With a window,
  *   tokens that no later token can see (neither sinks nor among the last
- *   window + new tokens) are still written.
+ *   window + new tokens) are still written.  Where the table gives two tokens of
+ *   the call one row of the cache, that row is left with parts of either.
  */
 gca_status_t gca_paged_append(const gca_paged_params_t* params, const void* k_new,
                               const void* v_new, const int32_t* cu_q, const int32_t* kv_len,
@@ -385,8 +387,11 @@ size_t gca_paged_attn_workspace_size(const gca_paged_params_t* params);
  *   sees nothing: its output is 0 and its lse -inf.
  *   Only pages that hold a visible token are looked up, so the table entries of
  *   pages that left the window may be anything.  Such a page outside
- *   [0, n_pages) reads as zeros and records GCA_ERR_DEVICE_INDEX.  Cache rows at or
- *   behind kv_len may hold anything (NaN included).
+ *   [0, n_pages) reads as zeros and records GCA_ERR_DEVICE_INDEX.  Cache rows that
+ *   no new token sees (at or behind kv_len, or between the sinks and the window of a
+ *   sequence's first new token) may hold anything, NaN included; the others must be
+ *   finite.  Sequences may share pages, and a page may stand more than once in a row
+ *   of the table.
  *   workspace: >= gca_paged_attn_workspace_size() bytes, 256-byte aligned,
  *   contents need not be initialised; calls that may overlap need their own.
  */

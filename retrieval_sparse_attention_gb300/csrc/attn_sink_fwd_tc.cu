@@ -415,12 +415,12 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
     } else {
         // ------------------------------------------------------------ P V issuer (whole warp: it also
-        // clears the V rows behind a sequence's last token, whose cache rows may hold anything)
+        // clears the V rows that no token of the unit sees: such rows of the cache may hold anything)
         struct State {
-            int j, j1, np, tp, nar, end, nsk, k0, nw;
+            int j, j1, np, tp, nar, lo, end, nsk, k0, nw;
             bool open;
         };
-        State cur{0, 0, 0, 0, 0, 0, 0, 0, 0, true}, oth = cur;
+        State cur{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, true}, oth = cur;
         Ring kv{0, 0};
         bool issued = false;
         const uint32_t id_o = idesc_bf16(128, D, false, true);
@@ -435,6 +435,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 cur.j1 = u.j1;
                 cur.nar = u.nar;
                 if (PAGED) {
+                    cur.lo = u.p0 - sc.W + 1;
                     cur.end = u.end;
                     cur.nsk = u.nsk;
                     cur.k0 = u.k0;
@@ -452,15 +453,23 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (cur.open) {
                 if (!wwait(&sb.v_full[kv.i], kv.ph)) break;
                 uint8_t* vt = sm + C::OFF_V + kv.i * C::TILE;
-                const int behind = cur.end - Part::tile(cur.j, cur.nsk, cur.k0, cur.nw) * 128;
-                if (PAGED && behind < 128) {                          // the tile has rows behind the last token
+                if (PAGED) {
+                    // rows a0 .. a1 - 1 lie between the sinks and the first token's window, rows from a2
+                    // on behind the last token
+                    const int base = Part::tile(cur.j, cur.nsk, cur.k0, cur.nw) * 128;
+                    const int a0 = max(sc.ns - base, 0), a1 = min(cur.lo - base, cur.j < cur.nar ? kNarrow : 128);
+                    const int a2 = max(cur.end - base, 0);
+                    if (a0 < a1 || a2 < 128) {
 #pragma unroll 1
-                    for (int r = max(behind, 0) * 8 + lane; r < 128 * 8; r += 32)
+                        for (int r = (a0 < a1 ? a0 : a2) * 8 + lane; r < 128 * 8; r += 32) {
+                            if (r >= a1 * 8 && r < a2 * 8) continue;
 #pragma unroll
-                        for (int c = 0; c < C::SUB; ++c)
-                            reinterpret_cast<uint4*>(vt + c * C::STILE)[r] = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                            for (int c = 0; c < C::SUB; ++c)
+                                reinterpret_cast<uint4*>(vt + c * C::STILE)[r] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
                 }
                 if (!wwait(&sb.p_full[i], full_par(cur.tp))) break;
                 const bool narrow = cur.j < cur.nar;

@@ -140,6 +140,78 @@ def test_pages_that_left_the_window_are_not_looked_up():
     c.check(o, lse, 100, 4)
 
 
+@pytest.mark.parametrize("qs,kvs,H,Hkv,d,page,window,sinks", [b for b in BATCHES if b[6]] + [
+    ([1, 9], [1300, 700], 4, 2, 128, 128, 200, 130), ([1, 1], [5000, 400], 12, 12, 64, 128, 300, 0),
+    ([260, 1], [4000, 90], 2, 1, 128, 16, 65, 7), ([1, 0], [129, 40], 2, 2, 64, 64, 1, 0)])
+def test_cache_rows_that_no_new_token_sees_may_hold_anything(qs, kvs, H, Hkv, d, page, window, sinks):
+    # rows between the sinks and the first new token's window, in pages that hold visible rows too
+    c = Cache(qs, kvs, H, Hkv, d, page, seed=sum(kvs))
+    hidden = 0
+    for b, (n, kv) in enumerate(zip(qs, kvs)):
+        for s in range(min(sinks, kv), max(kv - n - window + 1, 0)) if n else range(kv):
+            for x, bad in ((c.kc, float("nan")), (c.vc, [float("nan"), float("inf")][s % 2])):
+                x[c.table[b, s // page], s % page] = bad
+            hidden += 1
+    assert hidden
+    o, lse = api.paged_attn(*c.cuda(), max_q=max(qs), window=window, sinks=sinks, with_lse=True)
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == 0
+    c.check(o, lse, window, sinks)
+
+
+def test_pages_may_be_shared():
+    # three sequences with the same first pages, and a page that stands twice in one table row
+    c = Cache([1, 5, 40], [200, 300, 170], 4, 2, 64, 16, seed=3)
+    for b in (1, 2):
+        c.table[b, :6] = c.table[0, :6]
+        c.k[b][:96], c.v[b][:96] = c.k[0][:96], c.v[0][:96]
+    c.table[1, 9] = c.table[1, 7]
+    c.k[1][144:160], c.v[1][144:160] = c.k[1][112:128], c.v[1][112:128]
+    for window, sinks in ((0, 0), (90, 20)):
+        o, lse = api.paged_attn(*c.cuda(), window=window, sinks=sinks, with_lse=True)
+        c.check(o, lse, window, sinks)
+    assert api.gca_get_status() == 0
+
+
+def test_rows_far_into_the_token_tensors():
+    # the call's tokens are rows behind 2^26 others (32 lanes a row: past 32 bits of threads)
+    c = Cache([3, 2], [40, 9], 1, 1, 64, 16, seed=5)
+    q, kc, vc, table, cu, kv = c.cuda()
+    first = 2 ** 26 + 1
+    big = torch.empty(first + 6, 1, 64, dtype=torch.bfloat16, device="cuda")
+    cu = cu + first
+    big[first:first + 5] = q
+    o, lse = api.paged_attn(big, kc, vc, table, cu, kv, max_q=3, with_lse=True)
+    c.check(o[first:first + 5], lse[first:first + 5], 0, 0)
+    kc.zero_()
+    vc.zero_()
+    api.paged_append(big, big, kc, vc, table, cu, kv, max_q=3)
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == 0
+    for row, (b, s) in enumerate([(0, 37), (0, 38), (0, 39), (1, 7), (1, 8)]):
+        for x in (kc, vc):
+            assert torch.equal(x[table[b, s // 16].item(), s % 16], big[first + row])
+    assert int((kc.abs().sum(-1) > 0).sum()) == 5
+
+
+def test_two_streams_at_once():
+    # calls that overlap, each with its own workspace, and what they give one after the other
+    a = Cache([1] * 8, [4000 + 300 * i for i in range(8)], 8, 2, 128, 64, seed=8)
+    b = Cache([300, 20], [2500, 900], 12, 12, 64, 16, seed=9)
+    ta, tb = a.cuda(), b.cuda()
+    want = api.paged_attn(*ta, max_q=1, with_lse=True) + api.paged_attn(*tb, window=512, sinks=4, with_lse=True)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        with torch.cuda.stream(sa):
+            ga = api.paged_attn(*ta, max_q=1, with_lse=True)
+        with torch.cuda.stream(sb):
+            gb = api.paged_attn(*tb, window=512, sinks=4, with_lse=True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(ga + gb, want))
+    assert api.gca_get_status() == 0
+
+
 def test_a_bad_page_reads_as_zeros_and_is_reported():
     c = Cache([1, 2], [100, 200], 2, 1, 64, 32)
     for bad in (-1, c.n_pages, 2 ** 31 - 1, -2 ** 31):

@@ -164,6 +164,49 @@ def test_other_stream_and_graph():
     assert all(torch.equal(x, y) for x, y in zip(want + gw, got + gg))
 
 
+def test_two_streams_at_once():
+    # calls that overlap, each with its own workspace, against the same calls one after the other
+    a = [x.cuda() for x in inputs(4, 2000, 6, 2, 64, seed=10)]
+    b = [x.cuda() for x in inputs(1, 5000, 8, 2, 128, seed=11)]
+
+    def step(t, window, sinks):
+        o, lse = api.swa_sink_fwd(*t[:3], window=window, sinks=sinks)
+        return (o, lse) + api.swa_sink_bwd(*t[:3], o, lse, t[3], window=window, sinks=sinks)
+
+    want = step(a, 512, 4) + step(b, 900, 16)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(6):
+        with torch.cuda.stream(sa):
+            ga = step(a, 512, 4)
+        with torch.cuda.stream(sb):
+            gb = step(b, 900, 16)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(ga + gb, want))
+    assert api.gca_get_status() == 0
+
+
+def test_graphs_that_share_a_workspace():
+    # two captured calls of different shapes over one workspace, replayed in turn on one stream
+    a = [x.cuda() for x in inputs(1, 3000, 4, 2, 64, seed=12)]
+    b = [x.cuda() for x in inputs(2, 900, 8, 1, 128, seed=13)]
+    want = api.swa_sink_fwd(*a[:3], window=700, sinks=4) + api.swa_sink_fwd(*b[:3], window=300, sinks=1)
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    graphs, got = [], []
+    for t, window, sinks in ((a, 700, 4), (b, 300, 1)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.extend(api.swa_sink_fwd(*t[:3], window=window, sinks=sinks, workspace=ws))
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert api.gca_get_status() == 0
+
+
 # enough key tiles for shares of many units, whole and cut, and for a sink's long item to be
 # spread over many shares; the 64-bit reference on the GPU
 @pytest.mark.parametrize("B,L,H,Hkv,d,window,sinks", [(2, 4000, 12, 12, 64, 512, 4), (2, 3001, 8, 2, 128, 700, 16),
