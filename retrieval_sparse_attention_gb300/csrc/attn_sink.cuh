@@ -178,6 +178,71 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole,
     __syncthreads();
 }
 
+// The same for dense sequences, which all have the same entries: the stream's order is
+// (sequence, head, i, step), so that a worker follows one head along the sequence and
+// finds most of an entry's tiles in the L2 cache, where its last entries brought them.
+// The entries of one (sequence, head) are summed up; the cuts divide by their total.
+template <int THREADS, int SHARES, class Count>
+__device__ __forceinline__ void find_shares_dense(int B, int n, int heads, bool whole, int* wsum, StreamPos* pos,
+                                                  Count count) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (n + THREADS - 1) / THREADS;
+    const int e0 = min(n, tid * per), e1 = min(n, e0 + per);
+    int mine = 0;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) mine += count(e);
+    int inc = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0};
+    __syncthreads();
+    int base = inc - mine, row = 0;
+#pragma unroll 1
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += wsum[w];
+        row += wsum[w];
+    }
+    const int total = row * heads * B, workers = SHARES * gridDim.x;
+    const int quota = (total + workers - 1) / workers;
+#pragma unroll 1
+    for (int k = 0; k < 2 * SHARES; ++k) {
+        // worker w's share: its first step (k even) and its end, one past its last step
+        const int w = k >> 1;
+        const int wid = total <= static_cast<int>(gridDim.x) ? blockIdx.x + w * gridDim.x : blockIdx.x * SHARES + w;
+        if (tid == 0 && (k & 1)) pos[w].wid = wid;
+        const int from = wid * quota;
+        if (from >= total) continue;
+        const int x = (k & 1) ? min(total, from + quota) : from;
+        int bh = x / row;
+        const int r = x - bh * row;
+        int at = base;
+#pragma unroll 1
+        for (int e = e0; e < e1; ++e) {
+            const int c = count(e);
+            if (r >= at && r < at + c) {
+                const int skip = whole && r > at ? at + c - r : 0;
+                if (k & 1) {
+                    atomicAdd(&pos[w].left, x - from + skip);
+                } else {
+                    atomicAdd(&pos[w].left, -skip);
+                    int i = e;
+                    if (skip && ++i == n) { i = 0; ++bh; }
+                    pos[w].b = bh / heads;
+                    pos[w].h = bh % heads;
+                    pos[w].mt = i;
+                    pos[w].j = skip ? 0 : r - at;
+                }
+            }
+            at += c;
+        }
+    }
+    __syncthreads();
+}
+
 __device__ __forceinline__ uint32_t full_par(int k) { return static_cast<uint32_t>(k) & 1u; }
 __device__ __forceinline__ uint32_t empty_par(int k) { return (static_cast<uint32_t>(k) & 1u) ^ 1u; }
 

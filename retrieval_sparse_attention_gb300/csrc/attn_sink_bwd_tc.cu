@@ -212,9 +212,9 @@ __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wi
     if (u.slot == 2 * wid + 1) a.tailA[wid] = make_int4(p.b, p.mt, p.h, 1);
     p.left -= u.j1 - u.j0;
     p.j = 0;
-    if (++p.h == s.Hkv) {
-        p.h = 0;
-        if (++p.mt == s.nMT) { p.mt = 0; ++p.b; }
+    if (++p.mt == s.nMT) {
+        p.mt = 0;
+        if (++p.h == s.Hkv) { p.h = 0; ++p.b; }
     }
     return u;
 }
@@ -270,8 +270,8 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares<kThreadsA, 1>(sc.B, sc.nMT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; },
-                             [&](int, int mt) { return tiles(sc, mt).nt; });
+    find_shares_dense<kThreadsA, 1>(sc.B, sc.nMT, sc.Hkv, false, sb.wsum, &sb.pos,
+                                   [&](int mt) { return tiles(sc, mt).nt; });
     tc_fence_before();
     pdl_release();
     pdl_wait();
@@ -653,9 +653,9 @@ __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wi
     if (u.slot == 2 * wid + 1) a.tailB[wid] = make_int4(p.b, p.mt, p.h, 1);
     p.left -= u.j1 - u.j0;
     p.j = 0;
-    if (++p.h == s.Hkv) {
-        p.h = 0;
-        if (++p.mt == a.nKT) { p.mt = 0; ++p.b; }
+    if (++p.mt == a.nKT) {
+        p.mt = 0;
+        if (++p.h == s.Hkv) { p.h = 0; ++p.b; }
     }
     return u;
 }
@@ -708,7 +708,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares<kThreadsB, 1>(sc.B, a.nKT, sc.Hkv, false, sb.wsum, &sb.pos, [](int) { return 0; }, [&](int, int kt) {
+    find_shares_dense<kThreadsB, 1>(sc.B, a.nKT, sc.Hkv, false, sb.wsum, &sb.pos, [&](int kt) {
         const Blocks k = blocks(sc, kt);
         return sc.G * (k.nw + k.nf);
     });

@@ -60,6 +60,7 @@ constexpr int kMaxCtas = 152;              // one per SM; the workspace is sized
 constexpr int kMaxWorkers = 2 * kMaxCtas;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t TMEM_COLS = 512;
+constexpr size_t kHalfL2 = 64u << 20;
 constexpr int kSmemMax = 232448;
 
 template <int D>
@@ -68,7 +69,9 @@ struct Cfg {
     static constexpr int STILE = 128 * 128;               // bytes of a 128-row sub-tile
     static constexpr int TILE = SUB * STILE;
     static constexpr int QB = D == 64 ? 2 : 1;            // Q buffers a worker
-    static constexpr int KST = D == 64 ? 4 : 2;
+    // (d = 64: a fourth K stage takes 0.203 instead of 0.196 ms at W = 128, and 279 instead of
+    // 273 us for one token over 18K)
+    static constexpr int KST = D == 64 ? 3 : 2;
     static constexpr int VST = D == 64 ? 6 : 3;
     static constexpr int STAGES = VST;
     static constexpr int OFF_Q = 0;
@@ -142,7 +145,7 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     if (p.left <= 0) return u;
     SeqInfo q = sink_seq<PAGED>(s, p.b, nullptr);
     KeyTiles k = key_tiles(s, q, p.mt);
-    while (k.nt == 0 && p.b + 1 < s.B) {
+    while (PAGED && k.nt == 0 && p.b + 1 < s.B) {
         ++p.b;
         p.mt = 0;
         q = sink_seq<PAGED>(s, p.b, nullptr);
@@ -171,7 +174,12 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     else if (u.j1 < k.nt) a.tail[wid_tail] = make_int4(p.b, p.mt, p.h, 1);
     p.left -= u.j1 - u.j0;
     p.j = 0;
-    if (++p.h == s.Hkv) { p.h = 0; ++p.mt; }
+    if (PAGED) {
+        if (++p.h == s.Hkv) { p.h = 0; ++p.mt; }
+    } else if (++p.mt == s.nMT) {
+        p.mt = 0;
+        if (++p.h == s.Hkv) { p.h = 0; ++p.b; }
+    }
     return u;
 }
 
@@ -223,9 +231,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_relinquish();
     }
     pdl_release();
-    find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, a.whole, sb.wsum, sb.pos,
-                             [&](int b) { return sink_seq<PAGED>(sc, b, a.status); },
-                             [&](const SeqInfo& q, int mt) { return key_tiles(sc, q, mt).nt; });
+    if (PAGED)
+        find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, a.whole, sb.wsum, sb.pos,
+                                 [&](int b) { return sink_seq<PAGED>(sc, b, a.status); },
+                                 [&](const SeqInfo& q, int mt) { return key_tiles(sc, q, mt).nt; });
+    else
+        find_shares_dense<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, a.whole, sb.wsum, sb.pos,
+                                       [&](int mt) { return key_tiles(sc, SeqInfo{0, sc.L, 0}, mt).nt; });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -274,15 +286,19 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 a.head[sb.pos[i].wid] = 0;
                 a.tail[sb.pos[i].wid] = make_int4(0, 0, 0, 0);
             }
-            // Many short units: the workers take turns at those of both shares (neighbours in the
-            // stream, they mostly have the same tiles, and so the workers, whose turns are taken in
-            // lockstep, meet their slow tiles together: 0.81 -> XXX ms at B = 8 x 16K, W = 512, ns = 4).
-            // Long ones: each has its own share, so both end at the same time.
+            // Dense rows: where the tiles that all workers go through for one unit each fill more than
+            // half of the L2 cache, the two workers take turns at the units of both shares, neighbours
+            // in the sequence, so that one finds the tiles the other has just read (B = 8 x 16K, 12
+            // heads of 64, W = 2048: 0.85 instead of 1.22 ms; 64K, 16/4 heads of 128, W = 1024: 0.53
+            // instead of 0.65).  Shorter windows stay in the cache anyway, and the workers, whose turns
+            // then fall apart, meet fewer slow tiles together (W = 512, ns = 4: 0.37 instead of 0.38).
+            // Few units: each worker has its own share, so both end at the same time.
             StreamPos& p = sb.pos[0];
             const int both = p.left + sb.pos[1].left;
-            if (sb.pos[1].left > 0) {
+            if (!PAGED && sb.pos[1].left > 0) {
                 const int nt = key_tiles(sc, sink_seq<PAGED>(sc, p.b, nullptr), p.mt).nt;
-                alternate = both >= 16 * nt && (p.j > 0 ? p.left >= nt - p.j : true);
+                alternate = both >= 16 * nt && (p.j > 0 ? p.left >= nt - p.j : true) &&
+                            static_cast<size_t>(nt) * (4 * C::TILE) * gridDim.x > kHalfL2;
                 if (alternate) p.left = both;
             }
         }
