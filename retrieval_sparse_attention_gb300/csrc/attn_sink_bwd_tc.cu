@@ -171,7 +171,7 @@ struct Cfg {
     static constexpr int ITEM = 2 * TILE;                         // Q, dO
     static constexpr int SLOT = 2 * KTILE;                        // K, V
     static constexpr int IBUF = 2;
-    static constexpr int NSLOT = D == 64 ? 8 : 3;
+    static constexpr int NSLOT = D == 64 ? 6 : 3;
     static constexpr int OFF_KV = IBUF * ITEM;
     static constexpr int OFF_VEC = OFF_KV + NSLOT * SLOT;         // two vectors of 128 floats
     static constexpr int SMEM = OFF_VEC + 1024 + 1024;
@@ -945,38 +945,45 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
                     for (int c = 0; c < 2; ++c) tmem_st_32x32b_x16(xb + 32 * half + 16 * c, z);
                 } else {
-                    // this warpgroup's 32 queries, 16 at a time
+                    // (without the masks where every key sees every query: 0.64 instead of 0.67 ms at
+                    // B = 8 x 16K)
+                    auto body = [&](bool msk) {
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        const int c = 2 * half + cc;
-                        uint32_t rs[16], rd[16];
-                        tmem_ld_32x32b_x16(xb + 16 * c, rs);
-                        tmem_ld_32x32b_x16(yb + 16 * c, rd);
-                        tmem_wait_ld();
-                        if (cc == 1) {
-                            tc_fence_before();
-                            mbar_arrive(&sb.y_empty[ys]);
-                        }
-                        const uint32_t vis = all ? 0xffffu : (below(c_hi + 1 - 16 * c) & ~below(c_lo - 16 * c));
-                        uint32_t pd[8], pp[8];
+                        for (int cc = 0; cc < 2; ++cc) {
+                            const int c = 2 * half + cc;
+                            uint32_t rs[16], rd[16];
+                            tmem_ld_32x32b_x16(xb + 16 * c, rs);
+                            tmem_ld_32x32b_x16(yb + 16 * c, rd);
+                            tmem_wait_ld();
+                            if (cc == 1) {
+                                tc_fence_before();
+                                mbar_arrive(&sb.y_empty[ys]);
+                            }
+                            const uint32_t vis = below(c_hi + 1 - 16 * c) & ~below(c_lo - 16 * c);
+                            uint32_t pd[8], pp[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float y0, y1;
-                            tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
-                                                      sl2, nl[8 * c + i]), y0, y1);
-                            float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
-                            e0 = (vis >> (2 * i) & 1u) ? e0 : 0.f;
-                            e1 = (vis >> (2 * i + 1) & 1u) ? e1 : 0.f;
-                            const uint64_t ev = tcx::f2_pack(e0, e1);
-                            const uint64_t gd = tcx::ffma2(tcx::f2_pack(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])),
-                                                           sc2, nd[8 * c + i]);
-                            pd[i] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
-                            pp[i] = tcx::pack_bf16x2(ev);
+                            for (int i = 0; i < 8; ++i) {
+                                float y0, y1;
+                                tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
+                                                          sl2, nl[8 * c + i]), y0, y1);
+                                float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
+                                if (msk) {
+                                    e0 = (vis >> (2 * i) & 1u) ? e0 : 0.f;
+                                    e1 = (vis >> (2 * i + 1) & 1u) ? e1 : 0.f;
+                                }
+                                const uint64_t ev = tcx::f2_pack(e0, e1);
+                                const uint64_t gd = tcx::ffma2(tcx::f2_pack(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])),
+                                                               sc2, nd[8 * c + i]);
+                                pd[i] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
+                                pp[i] = tcx::pack_bf16x2(ev);
+                            }
+                            // ds^T, then P^T, over the 16 S^T columns just read
+                            tmem_st_32x32b_x8(xb + 16 * c, pd);
+                            tmem_st_32x32b_x8(xb + 16 * c + 8, pp);
                         }
-                        // ds^T, then P^T, over the 16 S^T columns just read
-                        tmem_st_32x32b_x8(xb + 16 * c, pd);
-                        tmem_st_32x32b_x8(xb + 16 * c + 8, pp);
-                    }
+                    };
+                    if (all) body(false);
+                    else body(true);
                 }
                 tmem_wait_st();
                 tc_fence_before();
