@@ -251,9 +251,9 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 
 // Bounded wait in as little code as it takes (the kernels' hot code has to stay in the
 // instruction cache): each try may suspend the thread for up to 20 us, and after about
-// 2 s of tries the wait records GCA_ERR_TIMEOUT and gives up; the CTA's other roles then
-// run out of theirs.
-__device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity, int* status) {
+// 2 s of tries the wait gives up; its role then ends early, which it notes in the CTA's
+// `gave_up`, and the CTA's other roles run out of their waits.
+__device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity) {
     const uint32_t addr = tc::smem_u32(bar);
 #pragma unroll 1
     for (int n = 0; n < 100000; ++n) {
@@ -267,7 +267,6 @@ __device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity, int* s
             : "memory");
         if (ok) return true;
     }
-    set_status(status, GCA_ERR_TIMEOUT);
     return false;
 }
 // One lane of a converged warp, the same one each time.
@@ -277,7 +276,7 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 // Bounded wait for work in flight at the end.
-__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) { wait_ctrl(bar, parity, nullptr); }
+__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) { wait_ctrl(bar, parity); }
 
 // 32 fp32 columns of this lane's row of an accumulator, times `scale`, as bf16 pairs.
 __device__ __forceinline__ void load_row32(uint32_t taddr, float scale, uint32_t* pk) {

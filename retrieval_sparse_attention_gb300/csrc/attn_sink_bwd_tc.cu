@@ -193,6 +193,7 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty[2];      // per storing warpgroup (it sees every phase); per accumulator
     uint64_t done[3];
     uint32_t tmem;
+    int gave_up;
     StreamPos pos;
     int wsum[12];
 };
@@ -231,10 +232,11 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     __shared__ Bars<C> sb;
     static_assert(C::SMEM + sizeof(Bars<C>) <= kSmemMax, "shared memory (pass A)");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par, a.status); };
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par); };
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
+        sb.gave_up = 0;
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sb.part_full[i], 1);
             mbar_init(&sb.part_empty[i], 3 + 8);          // the issuers and the math warps
@@ -287,14 +289,14 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             uint32_t used = 0;
             a.headA[blockIdx.x] = 0;
             a.tailA[blockIdx.x] = make_int4(0, 0, 0, 0);
-            bool ok = true;
+            bool ok = true, done = false;
             while (ok) {
                 const int r = np % kParts, ib = np % C::IBUF;
                 if (!wait(&sb.part_empty[r], empty_par(np / kParts))) break;
                 sb.part[r] = next_part(a, sb.pos, blockIdx.x);
                 mbar_arrive(&sb.part_full[r]);
                 const Part& u = sb.part[r];
-                if (u.j0 == u.j1) break;
+                if (u.j0 == u.j1) { done = true; break; }
                 if (!wait(&sb.it_empty[ib], empty_par(np / C::IBUF)) || !wait(&sb.vec_empty, empty_par(np))) break;
                 uint8_t* it = sm + ib * C::ITEM;
                 mbar_arrive_expect_tx(&sb.vec_full, 1024);
@@ -324,6 +326,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     kv.next(C::NSLOT);
                 }
             }
+            if (!done) sb.gave_up = 1;
             // no copy may still be writing shared memory when the CTA exits
 #pragma unroll 1
             for (int i = 0; i < C::NSLOT; ++i)
@@ -342,14 +345,14 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         if (lane == 0) {
             Ring kv{0, 0};
             int u = 0;
-            bool issued = false, ok = true;
+            bool issued = false, ok = true, done = false;
             const uint32_t id_s = idesc_bf16(128, 64, false, false), id_n = idesc_bf16(128, 32, false, false);
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts, ib = np % C::IBUF;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
                 const int n = sb.part[r].j1 - sb.part[r].j0, nar = sb.part[r].nar;
                 mbar_arrive(&sb.part_empty[r]);
-                if (n == 0) break;
+                if (n == 0) { done = true; break; }
                 if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
                 const uint32_t aaddr = smem_u32(sm + ib * C::ITEM) + (dpi ? C::TILE : 0);
 #pragma unroll 1
@@ -370,6 +373,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 }
                 if (ok) mma_commit(&sb.it_empty[ib]);
             }
+            if (!done) sb.gave_up = 1;
             if (issued) {
                 mma_commit(&sb.done[dpi ? 2 : 0]);
                 wait_copy(&sb.done[dpi ? 2 : 0], 0);
@@ -380,14 +384,14 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         if (lane == 0) {
             Ring kv{0, 0};
             int u = 0;
-            bool issued = false, ok = true;
+            bool issued = false, ok = true, done = false;
             const uint32_t id_acc = idesc_bf16(128, D, false, true);
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts, ob = np % C::NACC;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
                 const int n = sb.part[r].j1 - sb.part[r].j0, nar = sb.part[r].nar;
                 mbar_arrive(&sb.part_empty[r]);
-                if (n == 0) break;
+                if (n == 0) { done = true; break; }
                 if (!wait(&sb.o_empty[ob], empty_par(np / C::NACC))) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -411,6 +415,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 }
                 if (ok) mma_commit(&sb.o_full[np & 1]);
             }
+            if (!done) sb.gave_up = 1;
             if (issued) {
                 mma_commit(&sb.done[1]);
                 wait_copy(&sb.done[1], 0);
@@ -453,13 +458,13 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             pend = -1;
             return true;
         };
-        bool ok = true;
+        bool ok = true, done = false;
         for (int np = 0; ok; ++np) {
             const int r = np % kParts;
             if (!wwait(&sb.part_full[r], full_par(np / kParts))) break;
             const Part& w = sb.part[r];
             const int j0 = w.j0, j1 = w.j1, nar = w.nar, p0 = w.mt * sc.TM;
-            if (j0 == j1) break;
+            if (j0 == j1) { done = true; break; }
             if (!wwait(&sb.vec_full, full_par(np))) break;
             const float* vec = reinterpret_cast<const float*>(sm + C::OFF_VEC);
             const float nl2 = vec[row], ndsc = vec[128 + row];
@@ -539,11 +544,13 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.part_empty[r]);
         }
-        if (ok && pend >= 0) epilogue();
+        if (done && pend >= 0) done = epilogue();
+        if (!done) sb.gave_up = 1;
     }
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && sb.gave_up) set_status(a.status, GCA_ERR_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
@@ -634,6 +641,7 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty;         // o_full per storing warpgroup: it sees every phase
     uint64_t done[3];
     uint32_t tmem;
+    int gave_up;
     StreamPos pos;
     int wsum[20];
 };
@@ -672,10 +680,11 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __shared__ Bars<C> sb;
     static_assert(C::SMEM + sizeof(Bars<C>) <= kSmemMax, "shared memory (pass B)");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par, a.status); };
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par); };
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
+        sb.gave_up = 0;
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sb.part_full[i], 1);
             mbar_init(&sb.part_empty[i], 3 + 16);          // the issuers and the math warps
@@ -727,14 +736,14 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             uint32_t used = 0;
             a.headB[blockIdx.x] = 0;
             a.tailB[blockIdx.x] = make_int4(0, 0, 0, 0);
-            bool ok = true;
+            bool ok = true, done = false;
             while (ok) {
                 const int r = np % kParts, ib = np % C::IBUF;
                 if (!wait(&sb.part_empty[r], empty_par(np / kParts))) break;
                 sb.part[r] = next_part(a, sb.pos, blockIdx.x);
                 mbar_arrive(&sb.part_full[r]);
                 const Part& u = sb.part[r];
-                if (u.j0 == u.j1) break;
+                if (u.j0 == u.j1) { done = true; break; }
                 if (!wait(&sb.it_empty[ib], empty_par(np / C::IBUF))) break;
                 uint8_t* it = sm + ib * C::ITEM;
                 mbar_arrive_expect_tx(&sb.it_full[ib], C::ITEM);
@@ -766,6 +775,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     sp.next(sc.G);
                 }
             }
+            if (!done) sb.gave_up = 1;
             // no copy may still be writing shared memory when the CTA exits
 #pragma unroll 1
             for (int i = 0; i < C::NSLOT; ++i)
@@ -782,14 +792,14 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (lane == 0) {
             Ring st{0, 0};
             int u = 0;
-            bool issued = false, ok = true;
+            bool issued = false, ok = true, done = false;
             const uint32_t id_s = idesc_bf16(128, 64, false, false);
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts, ib = np % C::IBUF;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
                 const int n = sb.part[r].j1 - sb.part[r].j0;
                 mbar_arrive(&sb.part_empty[r]);
-                if (n == 0) break;
+                if (n == 0) { done = true; break; }
                 if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
                 const uint32_t aaddr = smem_u32(sm + ib * C::ITEM) + (dpi ? C::TILE : 0);
 #pragma unroll 1
@@ -809,6 +819,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 }
                 if (ok) mma_commit(&sb.it_empty[ib]);     // K (V) is read only by these products
             }
+            if (!done) sb.gave_up = 1;
             if (issued) {
                 mma_commit(&sb.done[dpi ? 2 : 0]);
                 wait_copy(&sb.done[dpi ? 2 : 0], 0);
@@ -819,14 +830,14 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (lane == 0) {
             Ring st{0, 0};
             int u = 0;
-            bool issued = false, ok = true;
+            bool issued = false, ok = true, done = false;
             const uint32_t id_acc = idesc_bf16(128, D, false, true);
             for (int np = 0; ok; ++np) {
                 const int r = np % kParts;
                 if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
                 const int n = sb.part[r].j1 - sb.part[r].j0;
                 mbar_arrive(&sb.part_empty[r]);
-                if (n == 0) break;
+                if (n == 0) { done = true; break; }
                 if (!wait(&sb.o_empty, empty_par(np))) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -852,6 +863,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 }
                 if (ok) mma_commit(&sb.o_full[np & 1]);
             }
+            if (!done) sb.gave_up = 1;
             if (issued) {
                 mma_commit(&sb.done[1]);
                 wait_copy(&sb.done[1], 0);
@@ -909,13 +921,13 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             pend = -1;
             return true;
         };
-        bool ok = true;
+        bool ok = true, done = false;
         for (int np = 0; ok; ++np) {
             const int r = np % kParts;
             if (!wwait(&sb.part_full[r], full_par(np / kParts))) break;
             const Part& w = sb.part[r];
             const int n = w.j1 - w.j0;
-            if (n == 0) break;
+            if (n == 0) { done = true; break; }
             const int s0 = w.kt * 128, s = s0 + row;  // this thread's key
             Step sp;
             sp.init(w, sc.G);
@@ -1002,11 +1014,13 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.part_empty[r]);
         }
-        if (ok && pend >= 0) epilogue();
+        if (done && pend >= 0) done = epilogue();
+        if (!done) sb.gave_up = 1;
     }
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && sb.gave_up) set_status(a.status, GCA_ERR_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);

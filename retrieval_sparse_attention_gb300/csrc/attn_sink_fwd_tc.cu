@@ -131,6 +131,7 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty[2];
     uint64_t done, done2;
     uint32_t tmem;
+    int gave_up;
     StreamPos pos[2];
     int wsum[12];
 };
@@ -197,6 +198,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
+        sb.gave_up = 0;
         for (int i = 0; i < 2; ++i) {
             for (int u = 0; u < kParts; ++u) {
                 mbar_init(&sb.part_full[i][u], 1);
@@ -249,7 +251,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     // its code exists once (the instruction cache holds the whole kernel).
     if (warp < 4) {
     setmaxnreg_dec<kRegsCtrl>();
-    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par, a.status); };
+    auto wait = [&](uint64_t* bar, uint32_t par) { return wait_ctrl(bar, par); };
     auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
     if (warp == 0 || warp == 3) {
         // ------------------------------------------------------------ producers (whole warps)
@@ -363,6 +365,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             cur = oth;
             oth = t;
         }
+        if (cur.open || oth.open) sb.gave_up = 1;
         const int q_loads[2] = {i == 0 ? cur.np : oth.np, i == 0 ? oth.np : cur.np};
         // no copy may still be writing shared memory when the CTA exits: the last load of
         // each buffer has completed its current phase (Q's have, where their products ran;
@@ -424,6 +427,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 cur = oth;
                 oth = t;
             }
+            if (cur.open || oth.open) sb.gave_up = 1;
             if (issued) {
                 mma_commit(&sb.done);
                 wait_copy(&sb.done, 0);
@@ -512,6 +516,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             cur = oth;
             oth = t;
         }
+        if (cur.open || oth.open) sb.gave_up = 1;
         if (issued && elect_one()) {
             mma_commit(&sb.done2);
             wait_copy(&sb.done2, 0);
@@ -522,7 +527,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         setmaxnreg_inc<kRegsSoftmax>();
         // the accesses after a wait are warp-collective: a wait that gave up in one lane does in all
         auto wwait = [&](uint64_t* bar, uint32_t par) {
-            return __all_sync(0xffffffffu, wait_ctrl(bar, par, a.status));
+            return __all_sync(0xffffffffu, wait_ctrl(bar, par));
         };
         const int wg = (warp - 4) >> 2;
         const int qd = warp & 3;
@@ -761,10 +766,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 l = 0.f;
             }
         }
+        if (have) sb.gave_up = 1;
     }
 
     tc_fence_before();
     __syncthreads();
+    // (one report a CTA: with one at each wait the code grew by 3 KB and the kernel took 5% longer)
+    if (threadIdx.x == 0 && sb.gave_up) set_status(a.status, GCA_ERR_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
