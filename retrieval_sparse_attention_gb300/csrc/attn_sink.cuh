@@ -278,41 +278,41 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait for work in flight at the end.
 __device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) { wait_ctrl(bar, parity); }
 
-// 32 fp32 columns of this lane's row of an accumulator, times `scale`, as bf16 pairs.
-__device__ __forceinline__ void load_row32(uint32_t taddr, float scale, uint32_t* pk) {
-    uint32_t r[32];
+// 32 fp32 columns of the warp's 32 rows of an accumulator (a row a lane), times this lane's
+// `scale`, as bf16 pairs in the order that store_rows32 takes: four lanes have 64
+// consecutive bytes of a row, eight rows at a time.  The exchange between lanes goes
+// through the accumulator's own columns, written by rows and read back four lanes a row.
+// (With a row per lane the 32 lanes of a store touch 32 lines, and a tile's stores cost
+// as much as half a key tile; with shuffles in place of tensor memory the forward took
+// 0.333 instead of 0.325 ms at B = 8 x 16K, W = 512.)
+__device__ __forceinline__ void load_rows32(uint32_t taddr, float scale, uint32_t (&q)[16]) {
+    uint32_t r[32], pk[16];
     tc::tmem_ld_32x32b_x32(taddr, r);
     tc::tmem_wait_ld();
+    const uint64_t s2 = tcx::f2_pack(scale, scale);
 #pragma unroll
-    for (int u = 0; u < 16; ++u)
-        pk[u] = tcx::pack_bf16(__uint_as_float(r[2 * u]) * scale, __uint_as_float(r[2 * u + 1]) * scale);
+    for (int u = 0; u < 16; ++u)                        // pair u: column 4 (u % 4) + u / 4
+        pk[4 * (u & 3) + (u >> 2)] = tcx::pack_bf16x2(
+            tcx::fmul2(tcx::f2_pack(__uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1])), s2));
+    tc::tmem_st_32x32b_x16(taddr, pk);
+    tc::tmem_wait_st();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {                       // rows 16 h ..
+        uint32_t x[8];
+        tc::tmem_ld_16x128b_x4(taddr + (h << 20), x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[8 * h + 4 * (i & 1) + (i >> 1)] = x[i];
+    }
 }
 
-// Those to global memory: row `row` (rows of ld elements; row < 0: none) from out on.  Four
-// lanes exchange their rows' 16-byte pieces, so that each store writes 64 consecutive
-// bytes of a row (with a row per lane the 32 lanes of a store touch 32 lines, and the
-// stores of a tile cost as much as half a key tile).
-__device__ __forceinline__ void store_row32(uint32_t* q, __nv_bfloat16* out, int ld, int row) {
+// Those to global memory: this lane's row is row `row` (rows of ld elements; row < 0: none)
+// from out on.
+__device__ __forceinline__ void store_rows32(const uint32_t* q, __nv_bfloat16* out, int ld, int row) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int s = 1; s <= 2; s <<= 1) {
-        const bool up = lane & s;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (c & s) continue;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t give = up ? q[4 * c + u] : q[4 * (c + s) + u];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
-                if (up) q[4 * c + u] = got;
-                else q[4 * (c + s) + u] = got;
-            }
-        }
-    }
-    // lane 4 g + i now holds piece i of the rows of lanes 4 g .. 4 g + 3
-#pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int rk = __shfl_sync(0xffffffffu, row, (lane & 28) + k);
+        const int rk = __shfl_sync(0xffffffffu, row, 8 * k + (lane >> 2));
         if (rk >= 0)
             *reinterpret_cast<uint4*>(out + (size_t)rk * ld + 8 * (lane & 3)) =
                 make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);

@@ -443,13 +443,13 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const uint32_t acc = tmem + lane_base + C::COL_ACC + ob * D;
             if (pend_slot < 0) {
                 // (into registers first: the accumulator is free before the stores)
-                uint32_t pk[D / 2];
+                uint32_t pk[D / 32][16];
 #pragma unroll
-                for (int ci = 0; ci < D / 32; ++ci) load_row32(acc + 32 * ci, 1.f, pk + 16 * ci);
+                for (int ci = 0; ci < D / 32; ++ci) load_rows32(acc + 32 * ci, 1.f, pk[ci]);
                 tc_fence_before();
                 mbar_arrive(&sb.o_empty[ob]);
 #pragma unroll
-                for (int ci = 0; ci < D / 32; ++ci) store_row32(pk + 16 * ci, a.dq + 32 * ci, D, pend_row);
+                for (int ci = 0; ci < D / 32; ++ci) store_rows32(pk[ci], a.dq + 32 * ci, D, pend_row);
             } else {
                 store_rows_f32<D>(acc, a.partA + ((size_t)pend_slot * 128 + row) * D, pend_row >= 0);
                 tc_fence_before();
@@ -895,22 +895,22 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if constexpr (D == 64) {
                     // into registers first: the next part may accumulate before the stores
                     uint32_t pk[2][16];
-                    load_row32(acc, 1.f, pk[0]);
-                    load_row32(acc + 32, 1.f, pk[1]);
+                    load_rows32(acc, 1.f, pk[0]);
+                    load_rows32(acc + 32, 1.f, pk[1]);
                     tc_fence_before();
                     mbar_arrive(&sb.o_empty);
-                    store_row32(pk[0], out, D, pend_row);
-                    store_row32(pk[1], out + 32, D, pend_row);
+                    store_rows32(pk[0], out, D, pend_row);
+                    store_rows32(pk[1], out + 32, D, pend_row);
                 } else {
 #pragma unroll 1
                     for (int ci = 0; ci < D / 32; ++ci) {         // (too many for the registers)
                         uint32_t pk[16];
-                        load_row32(acc + 32 * ci, 1.f, pk);
+                        load_rows32(acc + 32 * ci, 1.f, pk);
                         if (ci + 1 == D / 32) {
                             tc_fence_before();
                             mbar_arrive(&sb.o_empty);
                         }
-                        store_row32(pk, out + 32 * ci, D, pend_row);
+                        store_rows32(pk, out + 32 * ci, D, pend_row);
                     }
                 }
             } else {

@@ -575,8 +575,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll 1
                         for (int ci = 0; ci < D / 32; ++ci) {
                             uint32_t pk[16];
-                            load_row32(to_addr + 32 * ci, inv, pk);
-                            store_row32(pk, a.o + 32 * ci, D, pend_row);
+                            load_rows32(to_addr + 32 * ci, inv, pk);
+                            store_rows32(pk, a.o + 32 * ci, D, pend_row);
                         }
                     } else {
 #pragma unroll 1
@@ -639,22 +639,28 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 tmem_wait_ld();
                 tc_fence_before();
                 if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
+                const uint32_t nvis = below(sc.ns);
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    r[i] = i < sc.ns ? r[i] : 0xff800000u;
+                    r[i] = (nvis >> i & 1u) ? r[i] : 0xff800000u;
                     m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(r[i]));
                 }
                 follow(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl);
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                float l4[4];
+                const uint64_t nsl2 = tcx::f2_pack(sl, sl), nnm2 = tcx::f2_pack(-m, -m);
+                uint64_t la[2] = {0ull, 0ull};
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * i]), sl, -m));
-                    const float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * i + 1]), sl, -m));
-                    l4[2 * (i & 1)] += e0;
-                    l4[2 * (i & 1) + 1] += e1;
-                    pk[i] = tcx::pack_bf16(e0, e1);
+                    float y0, y1;
+                    tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                                              nsl2, nnm2), y0, y1);
+                    const uint64_t e = tcx::f2_pack(fast_exp2(y0), fast_exp2(y1));
+                    la[i & 1] = tcx::fadd2(la[i & 1], e);
+                    pk[i] = tcx::pack_bf16x2(e);
                 }
+                tcx::f2_unpack(la[0], l4[0], l4[1]);
+                tcx::f2_unpack(la[1], l4[2], l4[3]);
                 l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
                 tmem_st_32x32b_x16(tp_addr, pk);

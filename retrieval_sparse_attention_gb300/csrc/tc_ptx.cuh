@@ -271,6 +271,14 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
                  : "memory");
 }
 
+// 16 lanes x 16 columns, eight registers a thread: register 2 i + u of thread t holds lane
+// taddr.lane + t / 4 + 8 u, column taddr.col + 4 i + t % 4.  Complete with tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld_16x128b_x4(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
 // Store counterpart of tmem_ld_16x32bx2_x16: threads 0-15 write lanes taddr.lane+0..15
 // at columns taddr.col .. +15, threads 16-31 the same lanes at columns
 // taddr.col + half_off .. +15.  Complete with tmem_wait_st.
