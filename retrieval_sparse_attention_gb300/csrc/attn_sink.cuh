@@ -1,5 +1,6 @@
-// attn_sink.cuh -- what the kernels of the windowed attention with sinks share:
-// the paged-cache bookkeeping of one sequence and of one cached token.
+// attn_sink.cuh -- what the kernels of the windowed attention with sinks share: a paged
+// call's sequences, the units of work and their equal shares, bounded waits, the way of
+// an accumulator's rows to global memory, and their launches.
 #pragma once
 
 #include <stdint.h>
@@ -93,8 +94,9 @@ struct StreamPos {
 };
 
 // The shares of this CTA (SHARES workers, neighbours in the stream; where there are
-// fewer steps than CTAs, each CTA has one worker with a share at most) in a stream of equally long steps: sequence b has entries i < n, entry i takes
-// count(seq(b), i) steps for each of `heads` heads, in the order (b, i, head, step).
+// fewer steps than CTAs, each CTA has one worker with a share at most) in a stream of
+// equally long steps: sequence b has entries i < n, entry i takes count(seq(b), i)
+// steps for each of `heads` heads, in the order (b, i, head, step).
 // Every worker gets total / workers steps, rounded up.  All THREADS threads of the
 // CTA take part; ends with __syncthreads.  The host bounds the total below 2^31.
 // whole: cuts move to the next entry's or head's first step.

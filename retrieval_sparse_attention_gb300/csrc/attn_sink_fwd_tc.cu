@@ -13,14 +13,13 @@
 // the sequences' lengths (on the device: a captured graph follows them).  A
 // unit cut by a share's end leaves unnormalised fp32 sums with their maxima in
 // the workspace, two slots a worker, and a second small kernel joins them in the
-// order of the stream (no atomics: bitwise reproducible).
+// order of the stream (no atomics: bitwise reproducible).  Units of up to four
+// tiles are not cut, which saves the second launch.
 //
 // One CTA per SM (12 warps), two workers per CTA:
 //   warp 0     walks the two shares and writes each part of a unit down as a record
-//              in shared memory, from which the other roles take their turns (one
-//              copy of that code: with a copy in every role the kernel outgrew the
-//              instruction cache and ran three times slower); Q tiles and the K
-//              ring, by TMA (lanes issue one page each)
+//              in shared memory, from which the other roles take their turns; Q
+//              tiles and the K ring, by TMA (lanes issue one page each)
 //   warp 3     the V ring
 //   warp 1     S = Q K^T   (M = 128, N = 128) into the worker's S buffer
 //   warp 2     O += P V    (A = P from tensor memory)
@@ -32,6 +31,27 @@
 // The online softmax keeps a stale maximum: sums are rescaled only when a tile's
 // maximum exceeds it by more than 2^8, so P <= 256 and its rounding to bf16
 // (relative 2^-8, the operand type of P V) is all that is lost.
+// Tiles that every row sees whole take the row's maximum from the load itself; the
+// others are masked in registers.  Up to 32 sinks take a tile of 32 columns.
+//
+// Measured (GB300; fractions of the measured 6.7 TB/s and 2.0 PFLOP/s):
+//   B = 8 x 16K, 12 heads of 64, W = 512: 0.324 ms, with 4 sinks 0.352 (2.3 TB/s);
+//   W = 2048 0.82 ms; 64K, 16/4 heads of 128, W = 1024, 16 sinks: 0.53-0.57 ms (0.97
+//   PFLOP/s, 49%); four chunks of 1.5-2K over 6-16K, 16/4 heads of 128: 0.43 ms
+//   (1.36 PFLOP/s, 68%); 32 tokens over caches of 4-33K, 24/8 heads of 128: 0.335
+//   ms (6.7 TB/s, 99%); one token over 777: 12 us in a graph, 7 of them this kernel.
+// What bounds it.  Single tokens over long caches: the cache's bytes.  d = 128 with
+// many rows: the chain S -> softmax -> P V of each worker, ~3,200 cycles a pair of
+// tiles of which the products fill ~2,450.  d = 64: instruction issue (48% of the
+// slots) and the chain of one tile's softmax, 1,250 to 1,850 cycles for a warp that
+// shares its sub-partition with one of the other worker; products fill 28% of the
+// time, exponentials 29% of their pipe.  The hot code of all roles has to stay in the
+// instruction cache, and is near its end: ~100 instructions more (a role's loop
+// unrolled over the two workers) cost 25%, 3 KB less gained 5 to 8%.
+// Tried and not kept: tiles of 64 keys with two or three S buffers a worker (1.3
+// to 1.5 times slower: the issuing warps' ~1,000 cycles a turn), two pipelines of own
+// control warps a CTA, P V started at half of P, barriers tested ahead of their
+// waits, masks skipped for 32 columns that a warp sees whole.
 #include <math.h>
 
 #include "attn_sink.cuh"
@@ -52,7 +72,7 @@ using tcx::Ring;
 
 constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168;
-constexpr int kRegsCtrl = 72;
+constexpr int kRegsCtrl = 72;                // (the control roles use 64)
 constexpr int kRegsSoftmax = 216;
 static_assert(128 * kRegsCtrl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
@@ -117,7 +137,7 @@ struct __align__(16) Part {
     __device__ __forceinline__ int tile(int j) const { return tile(j, nsk, k0, nw); }
 };
 constexpr int kParts = 4;    // records a worker
-constexpr int kNarrow = 32;  // sinks up to here take a tile of this width, a fifth of a full tile's time
+constexpr int kNarrow = 32;  // sinks up to here take a tile of this width (28 us at B = 8 x 16K, a full tile 60)
 
 template <int STAGES>
 struct __align__(16) Bars {
@@ -785,7 +805,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
 }
 
-// Joins the parts of the units that were cut: blocks (w, *) the unit that begins in worker
+// Joins the parts of the units that were cut (3 us after the forward, most of it launch: at most 303
+// units of 128 rows are cut): blocks (w, *) the unit that begins in worker
 // w's share and continues in the next ones.  With m = max_i m_i,
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, in the order of the stream.
 // A thread has four columns of a row; a block 16 rows (d = 64) or 8.
