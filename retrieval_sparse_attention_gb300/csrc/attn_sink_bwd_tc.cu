@@ -27,12 +27,14 @@
 // memory, which is the layout of the A operands that it writes.
 //
 // Measured (GB300), B = 8 x 16K, 12 heads of 64, W = 512, 4 sinks: vectors 0.07 ms (6.2
-// TB/s), pass A 0.435, pass B 0.63, join 0.01: 1.14 ms in all, 1.01 without sinks (the
+// TB/s), pass A 0.435, pass B 0.62, join 0.01: 1.13 ms in all, 1.00 without sinks (the
 // plain window's gradients, gca_swa_bwd, 1.22).  2 x 16K, 16/4 heads of 128, W = 1024, 16
 // sinks: 0.05, 0.385, 0.52, 0.02: 0.98 ms.  3 x 1000, 6/2 heads: 33 us in a graph.
 // What bounds it: pass A and B keep the tensor pipe 31% and 33% busy and the issue
 // slots 49% and 51%; the math warps' latency a step and the issuing threads' share of
-// the slots pace them.  A sink's far steps cost as much as others (0.10 ms of pass B)
+// the slots pace them (pass B, a clock trace: a step every 1,165 cycles; a math pair's two
+// steps take 2 x 1,165 of which its arithmetic 1,310 and its waits and stores the rest; the
+// loading thread needs 900 a step, the accumulating products' issuer 780).  A sink's far steps cost as much as others (0.10 ms of pass B)
 // although 32 of their 128 key rows at most carry anything; taking them in pass A,
 // where sinks have narrow steps, would need its dK and dV sums joined across all CTAs.
 #include <math.h>
@@ -55,6 +57,10 @@ using tcx::Ring;
 // Pass A: 4 control warps and 2 math warpgroups (with 4, as in pass B, 0.51 instead of 0.47 ms
 // at B = 8 x 16K).  Pass B: 4 math warpgroups, two to a step (with 2: 0.78 instead of 0.74 ms).
 constexpr int kThreadsA = 384, kThreadsB = 640;
+// Pass B's register split: the control roles use 64, and the math warps spill at the launch's 96 (0.635
+// instead of 0.62 ms at B = 8 x 16K).
+constexpr int kRegsB = 96, kRegsCtrlB = 64, kRegsMathB = 104;
+static_assert(128 * kRegsCtrlB + 512 * kRegsMathB <= kThreadsB * kRegsB, "register split exceeds the launch allocation");
 constexpr int kMaxCtas = 152;              // one per SM; the workspace is sized for them
 constexpr int kParts = 4;                  // part records in flight
 constexpr int kSmemMax = 232448;
@@ -738,149 +744,152 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = sb.tmem;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ records and loads
-        if (lane == 0) {
-            Ring st{0, 0};
-            int np = 0;
-            uint32_t used = 0;
-            a.headB[blockIdx.x] = 0;
-            a.tailB[blockIdx.x] = make_int4(0, 0, 0, 0);
-            bool ok = true, done = false;
-            while (ok) {
-                const int r = np % kParts, ib = np % C::IBUF;
-                if (!wait(&sb.part_empty[r], empty_par(np / kParts))) break;
-                sb.part[r] = next_part(a, sb.pos, blockIdx.x);
-                mbar_arrive(&sb.part_full[r]);
-                const Part& u = sb.part[r];
-                if (u.j0 == u.j1) { done = true; break; }
-                if (!wait(&sb.it_empty[ib], empty_par(np / C::IBUF))) break;
-                uint8_t* it = sm + ib * C::ITEM;
-                mbar_arrive_expect_tx(&sb.it_full[ib], C::ITEM);
-#pragma unroll
-                for (int c = 0; c < C::SUB; ++c) {
-                    tma_load_3d(it + c * C::STILE, &tk, &sb.it_full[ib], u.h * D + c * 64, u.kt * 128, u.b);
-                    tma_load_3d(it + C::TILE + c * C::STILE, &tv, &sb.it_full[ib], u.h * D + c * 64, u.kt * 128, u.b);
-                }
-                ++np;
-                Step sp;
-                sp.init(u, sc.G);
-                const int n = u.j1 - u.j0;
-#pragma unroll 1
-                for (int j = 0; j < n; ++j) {
-                    if (!wait(&sb.st_empty[st.i], st.ph ^ 1u)) { ok = false; break; }
-                    uint8_t* dst = sm + C::OFF_ST + st.i * C::SLOT;
-                    const int qb = sp.block() * 64, h = u.h * sc.G + sp.g;
-                    mbar_arrive_expect_tx(&sb.st_full[st.i], 2 * C::QTILE + 512);
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsCtrlB>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ records and loads
+            if (lane == 0) {
+                Ring st{0, 0};
+                int np = 0;
+                uint32_t used = 0;
+                a.headB[blockIdx.x] = 0;
+                a.tailB[blockIdx.x] = make_int4(0, 0, 0, 0);
+                bool ok = true, done = false;
+                while (ok) {
+                    const int r = np % kParts, ib = np % C::IBUF;
+                    if (!wait(&sb.part_empty[r], empty_par(np / kParts))) break;
+                    sb.part[r] = next_part(a, sb.pos, blockIdx.x);
+                    mbar_arrive(&sb.part_full[r]);
+                    const Part& u = sb.part[r];
+                    if (u.j0 == u.j1) { done = true; break; }
+                    if (!wait(&sb.it_empty[ib], empty_par(np / C::IBUF))) break;
+                    uint8_t* it = sm + ib * C::ITEM;
+                    mbar_arrive_expect_tx(&sb.it_full[ib], C::ITEM);
 #pragma unroll
                     for (int c = 0; c < C::SUB; ++c) {
-                        tma_load_4d(dst + c * C::SQ, &tq, &sb.st_full[st.i], c * 64, h, qb, u.b);
-                        tma_load_4d(dst + C::QTILE + c * C::SQ, &tdo, &sb.st_full[st.i], c * 64, h, qb, u.b);
+                        tma_load_3d(it + c * C::STILE, &tk, &sb.it_full[ib], u.h * D + c * 64, u.kt * 128, u.b);
+                        tma_load_3d(it + C::TILE + c * C::STILE, &tv, &sb.it_full[ib], u.h * D + c * 64, u.kt * 128, u.b);
                     }
-                    const size_t vrow = ((size_t)u.b * sc.H + h) * a.Lp + qb;
-                    tcx::bulk_load(dst + 2 * C::QTILE, a.nlB + vrow, 256, &sb.st_full[st.i]);
-                    tcx::bulk_load(dst + 2 * C::QTILE + 256, a.ndB + vrow, 256, &sb.st_full[st.i]);
-                    used |= 1u << st.i;
-                    st.next(C::NSLOT);
-                    sp.next(sc.G);
-                }
-            }
-            if (!done) sb.gave_up = 1;
-            // no copy may still be writing shared memory when the CTA exits
+                    ++np;
+                    Step sp;
+                    sp.init(u, sc.G);
+                    const int n = u.j1 - u.j0;
 #pragma unroll 1
-            for (int i = 0; i < C::NSLOT; ++i)
-                if (used >> i & 1u) wait_copy(&sb.st_full[i], i < st.i ? st.ph : st.ph ^ 1u);
-#pragma unroll 1
-            for (int q = 0; q < C::IBUF; ++q) {
-                const int n = (np - q + C::IBUF - 1) / C::IBUF;
-                if (n > 0) wait_copy(&sb.it_full[q], full_par(n - 1));
-            }
-        }
-    } else if (warp == 1 || warp == 3) {
-        // ------------------------------------------------------------ warp 1: S^T = K Q^T, warp 3: dP^T = V dO^T
-        const bool dpi = warp == 3;
-        if (lane == 0) {
-            Ring st{0, 0};
-            int u = 0;
-            bool issued = false, ok = true, done = false;
-            const uint32_t id_s = idesc_bf16(128, 64, false, false);
-            for (int np = 0; ok; ++np) {
-                const int r = np % kParts, ib = np % C::IBUF;
-                if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
-                const int n = sb.part[r].j1 - sb.part[r].j0;
-                mbar_arrive(&sb.part_empty[r]);
-                if (n == 0) { done = true; break; }
-                if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
-                const uint32_t aaddr = smem_u32(sm + ib * C::ITEM) + (dpi ? C::TILE : 0);
-#pragma unroll 1
-                for (int j = 0; j < n; ++j, ++u) {
-                    const int xs = u % C::NX;
-                    if (!wait(&sb.st_full[st.i], st.ph) ||
-                        !wait(dpi ? &sb.y_empty[xs] : &sb.x_empty[xs], empty_par(u / C::NX))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t baddr = smem_u32(sm + C::OFF_ST + st.i * C::SLOT) + (dpi ? C::QTILE : 0);
-                    tcx::mma_kmajor_dh<D>(tmem + (dpi ? C::COL_Y : C::COL_X) + xs * 64, aaddr, 128, baddr, 64, id_s, 0);
-                    mma_commit(&sb.x_full[xs]);
-                    issued = true;
-                    st.next(C::NSLOT);
-                }
-                if (ok) mma_commit(&sb.it_empty[ib]);     // K (V) is read only by these products
-            }
-            if (!done) sb.gave_up = 1;
-            if (issued) {
-                mma_commit(&sb.done[dpi ? 2 : 0]);
-                wait_copy(&sb.done[dpi ? 2 : 0], 0);
-            }
-        }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ dK += ds^T Q, dV += P^T dO
-        if (lane == 0) {
-            Ring st{0, 0};
-            int u = 0;
-            bool issued = false, ok = true, done = false;
-            const uint32_t id_acc = idesc_bf16(128, D, false, true);
-            for (int np = 0; ok; ++np) {
-                const int r = np % kParts;
-                if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
-                const int n = sb.part[r].j1 - sb.part[r].j0;
-                mbar_arrive(&sb.part_empty[r]);
-                if (n == 0) { done = true; break; }
-                if (!wait(&sb.o_empty, empty_par(np))) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int j = 0; j < n; ++j, ++u) {
-                    const int xs = u % C::NX;
-                    if (!wait(&sb.p_full[u & 3], full_par(u >> 2))) { ok = false; break; }
-                    tc_fence_after();
-                    // A: K = 16 query steps at X columns 0, 16, 32, 48 (ds^T) and 8, 24, 40, 56 (P^T);
-                    // B: queries x D with D along N
-                    const uint64_t qd = smem_desc(smem_u32(sm + C::OFF_ST + st.i * C::SLOT), C::SQ, 1024, 2);
-                    const uint32_t xa = tmem + C::COL_X + xs * 64;
+                    for (int j = 0; j < n; ++j) {
+                        if (!wait(&sb.st_empty[st.i], st.ph ^ 1u)) { ok = false; break; }
+                        uint8_t* dst = sm + C::OFF_ST + st.i * C::SLOT;
+                        const int qb = sp.block() * 64, h = u.h * sc.G + sp.g;
+                        mbar_arrive_expect_tx(&sb.st_full[st.i], 2 * C::QTILE + 512);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const uint32_t col = xa + 16 * ks;
-                        const uint32_t acc = (ks > 0 || j > 0) ? 1u : 0u;
-                        tc::mma_bf16_ts(tmem + C::COL_ACC, col, qd + 128 * ks, id_acc, acc);
-                        tc::mma_bf16_ts(tmem + C::COL_ACC + D, col + 8, qd + (C::QTILE >> 4) + 128 * ks, id_acc, acc);
+                        for (int c = 0; c < C::SUB; ++c) {
+                            tma_load_4d(dst + c * C::SQ, &tq, &sb.st_full[st.i], c * 64, h, qb, u.b);
+                            tma_load_4d(dst + C::QTILE + c * C::SQ, &tdo, &sb.st_full[st.i], c * 64, h, qb, u.b);
+                        }
+                        const size_t vrow = ((size_t)u.b * sc.H + h) * a.Lp + qb;
+                        tcx::bulk_load(dst + 2 * C::QTILE, a.nlB + vrow, 256, &sb.st_full[st.i]);
+                        tcx::bulk_load(dst + 2 * C::QTILE + 256, a.ndB + vrow, 256, &sb.st_full[st.i]);
+                        used |= 1u << st.i;
+                        st.next(C::NSLOT);
+                        sp.next(sc.G);
                     }
-                    mma_commit(&sb.x_empty[xs]);
-                    mma_commit(&sb.st_empty[st.i]);
-                    issued = true;
-                    st.next(C::NSLOT);
                 }
-                if (ok) mma_commit(&sb.o_full[np & 1]);
+                if (!done) sb.gave_up = 1;
+                // no copy may still be writing shared memory when the CTA exits
+#pragma unroll 1
+                for (int i = 0; i < C::NSLOT; ++i)
+                    if (used >> i & 1u) wait_copy(&sb.st_full[i], i < st.i ? st.ph : st.ph ^ 1u);
+#pragma unroll 1
+                for (int q = 0; q < C::IBUF; ++q) {
+                    const int n = (np - q + C::IBUF - 1) / C::IBUF;
+                    if (n > 0) wait_copy(&sb.it_full[q], full_par(n - 1));
+                }
             }
-            if (!done) sb.gave_up = 1;
-            if (issued) {
-                mma_commit(&sb.done[1]);
-                wait_copy(&sb.done[1], 0);
+        } else if (warp == 1 || warp == 3) {
+            // ------------------------------------------------------------ warp 1: S^T = K Q^T, warp 3: dP^T = V dO^T
+            const bool dpi = warp == 3;
+            if (lane == 0) {
+                Ring st{0, 0};
+                int u = 0;
+                bool issued = false, ok = true, done = false;
+                const uint32_t id_s = idesc_bf16(128, 64, false, false);
+                for (int np = 0; ok; ++np) {
+                    const int r = np % kParts, ib = np % C::IBUF;
+                    if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
+                    const int n = sb.part[r].j1 - sb.part[r].j0;
+                    mbar_arrive(&sb.part_empty[r]);
+                    if (n == 0) { done = true; break; }
+                    if (!wait(&sb.it_full[ib], full_par(np / C::IBUF))) break;
+                    const uint32_t aaddr = smem_u32(sm + ib * C::ITEM) + (dpi ? C::TILE : 0);
+#pragma unroll 1
+                    for (int j = 0; j < n; ++j, ++u) {
+                        const int xs = u % C::NX;
+                        if (!wait(&sb.st_full[st.i], st.ph) ||
+                            !wait(dpi ? &sb.y_empty[xs] : &sb.x_empty[xs], empty_par(u / C::NX))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t baddr = smem_u32(sm + C::OFF_ST + st.i * C::SLOT) + (dpi ? C::QTILE : 0);
+                        tcx::mma_kmajor_dh<D>(tmem + (dpi ? C::COL_Y : C::COL_X) + xs * 64, aaddr, 128, baddr, 64, id_s, 0);
+                        mma_commit(&sb.x_full[xs]);
+                        issued = true;
+                        st.next(C::NSLOT);
+                    }
+                    if (ok) mma_commit(&sb.it_empty[ib]);     // K (V) is read only by these products
+                }
+                if (!done) sb.gave_up = 1;
+                if (issued) {
+                    mma_commit(&sb.done[dpi ? 2 : 0]);
+                    wait_copy(&sb.done[dpi ? 2 : 0], 0);
+                }
+            }
+        } else {
+            // ------------------------------------------------------------ dK += ds^T Q, dV += P^T dO
+            if (lane == 0) {
+                Ring st{0, 0};
+                int u = 0;
+                bool issued = false, ok = true, done = false;
+                const uint32_t id_acc = idesc_bf16(128, D, false, true);
+                for (int np = 0; ok; ++np) {
+                    const int r = np % kParts;
+                    if (!wait(&sb.part_full[r], full_par(np / kParts))) break;
+                    const int n = sb.part[r].j1 - sb.part[r].j0;
+                    mbar_arrive(&sb.part_empty[r]);
+                    if (n == 0) { done = true; break; }
+                    if (!wait(&sb.o_empty, empty_par(np))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int j = 0; j < n; ++j, ++u) {
+                        const int xs = u % C::NX;
+                        if (!wait(&sb.p_full[u & 3], full_par(u >> 2))) { ok = false; break; }
+                        tc_fence_after();
+                        // A: K = 16 query steps at X columns 0, 16, 32, 48 (ds^T) and 8, 24, 40, 56 (P^T);
+                        // B: queries x D with D along N
+                        const uint64_t qd = smem_desc(smem_u32(sm + C::OFF_ST + st.i * C::SLOT), C::SQ, 1024, 2);
+                        const uint32_t xa = tmem + C::COL_X + xs * 64;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            const uint32_t col = xa + 16 * ks;
+                            const uint32_t acc = (ks > 0 || j > 0) ? 1u : 0u;
+                            tc::mma_bf16_ts(tmem + C::COL_ACC, col, qd + 128 * ks, id_acc, acc);
+                            tc::mma_bf16_ts(tmem + C::COL_ACC + D, col + 8, qd + (C::QTILE >> 4) + 128 * ks, id_acc, acc);
+                        }
+                        mma_commit(&sb.x_empty[xs]);
+                        mma_commit(&sb.st_empty[st.i]);
+                        issued = true;
+                        st.next(C::NSLOT);
+                    }
+                    if (ok) mma_commit(&sb.o_full[np & 1]);
+                }
+                if (!done) sb.gave_up = 1;
+                if (issued) {
+                    mma_commit(&sb.done[1]);
+                    wait_copy(&sb.done[1], 0);
+                }
             }
         }
     } else {
-        // ------------------------------------------------------------ math warpgroups
+        setmaxnreg_inc<kRegsMathB>();
         auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, wait(bar, par)); };
         // warpgroup pair `wg` takes every other step; `half` of a step's columns each
         const int wg = (warp - 4) >> 3, half = (warp >> 2) & 1;
@@ -1038,8 +1047,8 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 }
 }  // namespace pb
 
-// Adds up the parts of the items that were cut (10 to 18 us, launch and latency), in the order of the stream: blocks (w, *, *)
-// the item that begins in worker w's share and goes on in the next ones (pass A for
+// Adds up the parts of the items that were cut (10 to 18 us, launch and latency), in the order
+// of the stream: blocks (w, *, *) the item that begins in worker w's share and goes on in the next ones (pass A for
 // blockIdx.z = 0, pass B's dK and dV for 1 and 2).
 template <int D>
 __global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int workers) {
@@ -1117,6 +1126,10 @@ cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[
             const cudaError_t r = cudaFuncSetAttribute(pa::sink_bwd_q_kernel<D>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, pa::Cfg<D>::SMEM);
             if (r != cudaSuccess) return r;
+            // (a build that gave the kernel fewer registers would wait forever at the split: refuse it)
+            cudaFuncAttributes fa;
+            if (const cudaError_t x = cudaFuncGetAttributes(&fa, pb::sink_bwd_kv_kernel<D>)) return x;
+            if (fa.numRegs < kRegsB) return cudaErrorInvalidConfiguration;
             return cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         pb::Cfg<D>::SMEM);
         },
