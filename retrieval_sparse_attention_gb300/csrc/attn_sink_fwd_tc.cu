@@ -475,7 +475,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 cur.j1 = u.j1;
                 cur.nar = u.nar;
                 if (PAGED) {
-                    cur.lo = u.p0 - sc.W + 1;
+                    cur.lo = max(u.p0 - sc.W + 1, 0);
                     cur.end = u.end;
                     cur.nsk = u.nsk;
                     cur.k0 = u.k0;
@@ -494,19 +494,25 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (!wwait(&sb.v_full[kv.i], kv.ph)) break;
                 uint8_t* vt = sm + C::OFF_V + kv.i * C::TILE;
                 if (PAGED) {
-                    // rows a0 .. a1 - 1 lie between the sinks and the first token's window, rows from a2
-                    // on behind the last token
-                    const int base = Part::tile(cur.j, cur.nsk, cur.k0, cur.nw) * 128;
-                    const int a0 = max(sc.ns - base, 0), a1 = min(cur.lo - base, cur.j < cur.nar ? kNarrow : 128);
-                    const int a2 = max(cur.end - base, 0);
-                    if (a0 < a1 || a2 < 128) {
+                    // Rows that no token of the unit sees are cleared, in pages that hold some that one
+                    // does (the other pages were read as zeros): rows a0 .. a1 - 1 between the sinks and
+                    // the first token's window, rows a2 .. a3 - 1 behind the last token.
+                    const int base = Part::tile(cur.j, cur.nsk, cur.k0, cur.nw) * 128, pg = 1 << sc.p.page_log2;
+                    const int edge = cur.lo - base;                   // the tile that the window's edge crosses, or the sinks'
+                    auto row = [](int x) { return min(max(x, 0), 128); };
+                    const int a0 = row((sc.ns > base ? sc.ns : cur.lo & -pg) - base);
+                    const int a1 = row(edge < 128 ? edge : min(((sc.ns + pg - 1) & -pg) - base, cur.j < cur.nar ? kNarrow : 128));
+                    const int a2 = row(cur.end - base), a3 = row(((cur.end + pg - 1) & -pg) - base);
+                    if (a0 < a1 || a2 < a3) {
+                        auto clear = [&](int r0, int r1) {            // rows r0 .. r1 - 1, eight vectors each
 #pragma unroll 1
-                        for (int r = (a0 < a1 ? a0 : a2) * 8 + lane; r < 128 * 8; r += 32) {
-                            if (r >= a1 * 8 && r < a2 * 8) continue;
+                            for (int r = r0 * 8 + lane; r < r1 * 8; r += 32)
 #pragma unroll
-                            for (int c = 0; c < C::SUB; ++c)
-                                reinterpret_cast<uint4*>(vt + c * C::STILE)[r] = make_uint4(0, 0, 0, 0);
-                        }
+                                for (int c = 0; c < C::SUB; ++c)
+                                    reinterpret_cast<uint4*>(vt + c * C::STILE)[r] = make_uint4(0, 0, 0, 0);
+                        };
+                        clear(a0, a1);
+                        clear(a2, a3);
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
