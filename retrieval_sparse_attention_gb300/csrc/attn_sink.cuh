@@ -91,6 +91,8 @@ struct StreamPos {
     int b, mt, h, j;
     int left;
     int wid;             // the worker's number, in the order of the stream
+    int qb = -1;         // paged: the sequence that q describes (kept from part to part)
+    SeqInfo q = {0, 0, 0};
 };
 
 // The shares of this CTA (SHARES workers, neighbours in the stream; where there are
@@ -159,7 +161,7 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole,
                 if (lane >= o) inc += x;
             }
             if (lane == 31) wsum[warp] = inc;
-            if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0};
+            if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0, -1, {0, 0, 0}};
             __syncthreads();
 #pragma unroll 1
             for (int w = 0; w < THREADS / 32; ++w) {
@@ -200,7 +202,7 @@ __device__ __forceinline__ void find_shares_dense(int B, int n, int heads, bool 
         if (lane >= o) inc += x;
     }
     if (lane == 31) wsum[warp] = inc;
-    if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0};
+    if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0, -1, {0, 0, 0}};
     __syncthreads();
     int base = inc - mine, row = 0;
 #pragma unroll 1
@@ -253,8 +255,8 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 
 // Bounded wait in as little code as it takes (the kernels' hot code has to stay in the
 // instruction cache): each try may suspend the thread for up to 20 us, and after about
-// 2 s of tries the wait gives up; its role then ends early, which it notes in the CTA's
-// `gave_up`, and the CTA's other roles run out of their waits.
+// 2 s of tries the wait gives up; its role then ends early and notes it for the CTA's
+// report, and the CTA's other roles run out of their waits.
 __device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity) {
     const uint32_t addr = tc::smem_u32(bar);
 #pragma unroll 1

@@ -209,7 +209,7 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty[2];      // per storing warpgroup (it sees every phase); per accumulator
     uint64_t done[3];
     uint32_t tmem;
-    int gave_up;
+    int error;
     StreamPos pos;
     int wsum[12];
 };
@@ -252,7 +252,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
-        sb.gave_up = 0;
+        sb.error = 0;
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sb.part_full[i], 1);
             mbar_init(&sb.part_empty[i], 3 + 8);          // the issuers and the math warps
@@ -342,7 +342,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     kv.next(C::NSLOT);
                 }
             }
-            if (!done) sb.gave_up = 1;
+            if (!done) sb.error = GCA_ERR_TIMEOUT;
             // no copy may still be writing shared memory when the CTA exits
 #pragma unroll 1
             for (int i = 0; i < C::NSLOT; ++i)
@@ -389,7 +389,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 }
                 if (ok) mma_commit(&sb.it_empty[ib]);
             }
-            if (!done) sb.gave_up = 1;
+            if (!done) sb.error = GCA_ERR_TIMEOUT;
             if (issued) {
                 mma_commit(&sb.done[dpi ? 2 : 0]);
                 wait_copy(&sb.done[dpi ? 2 : 0], 0);
@@ -431,7 +431,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 }
                 if (ok) mma_commit(&sb.o_full[np & 1]);
             }
-            if (!done) sb.gave_up = 1;
+            if (!done) sb.error = GCA_ERR_TIMEOUT;
             if (issued) {
                 mma_commit(&sb.done[1]);
                 wait_copy(&sb.done[1], 0);
@@ -561,12 +561,12 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             if (lane == 0) mbar_arrive(&sb.part_empty[r]);
         }
         if (done && pend >= 0) done = epilogue();
-        if (!done) sb.gave_up = 1;
+        if (!done) sb.error = GCA_ERR_TIMEOUT;
     }
 
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && sb.gave_up) set_status(a.status, GCA_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && sb.error) set_status(a.status, sb.error);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
@@ -657,7 +657,7 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty;         // o_full per storing warpgroup: it sees every phase
     uint64_t done[3];
     uint32_t tmem;
-    int gave_up;
+    int error;
     StreamPos pos;
     int wsum[20];
 };
@@ -700,7 +700,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
-        sb.gave_up = 0;
+        sb.error = 0;
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sb.part_full[i], 1);
             mbar_init(&sb.part_empty[i], 3 + 16);          // the issuers and the math warps
@@ -793,7 +793,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         sp.next(sc.G);
                     }
                 }
-                if (!done) sb.gave_up = 1;
+                if (!done) sb.error = GCA_ERR_TIMEOUT;
                 // no copy may still be writing shared memory when the CTA exits
 #pragma unroll 1
                 for (int i = 0; i < C::NSLOT; ++i)
@@ -837,7 +837,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     }
                     if (ok) mma_commit(&sb.it_empty[ib]);     // K (V) is read only by these products
                 }
-                if (!done) sb.gave_up = 1;
+                if (!done) sb.error = GCA_ERR_TIMEOUT;
                 if (issued) {
                     mma_commit(&sb.done[dpi ? 2 : 0]);
                     wait_copy(&sb.done[dpi ? 2 : 0], 0);
@@ -881,7 +881,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     }
                     if (ok) mma_commit(&sb.o_full[np & 1]);
                 }
-                if (!done) sb.gave_up = 1;
+                if (!done) sb.error = GCA_ERR_TIMEOUT;
                 if (issued) {
                     mma_commit(&sb.done[1]);
                     wait_copy(&sb.done[1], 0);
@@ -1034,12 +1034,12 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (lane == 0) mbar_arrive(&sb.part_empty[r]);
         }
         if (done && pend >= 0) done = epilogue();
-        if (!done) sb.gave_up = 1;
+        if (!done) sb.error = GCA_ERR_TIMEOUT;
     }
 
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && sb.gave_up) set_status(a.status, GCA_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && sb.error) set_status(a.status, sb.error);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);

@@ -151,7 +151,7 @@ struct __align__(16) Bars {
     uint64_t o_full[2], o_empty[2];
     uint64_t done, done2;
     uint32_t tmem;
-    int gave_up;
+    int error;           // what the CTA has to report, or 0
     StreamPos pos[2];
     int wsum[12];
 };
@@ -164,13 +164,23 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     const SinkSched& s = a.s;
     Part u{};
     if (p.left <= 0) return u;
-    SeqInfo q = sink_seq<PAGED>(s, p.b, nullptr);
-    KeyTiles k = key_tiles(s, q, p.mt);
-    while (PAGED && k.nt == 0 && p.b + 1 < s.B) {
-        ++p.b;
+    SeqInfo q;
+    KeyTiles k;
+#pragma unroll 1
+    while (true) {
+        if (!PAGED) {
+            q = sink_seq<PAGED>(s, p.b, nullptr);
+        } else {
+            if (p.qb != p.b) {
+                p.q = sink_seq<PAGED>(s, p.b, nullptr);
+                p.qb = p.b;
+            }
+            q = p.q;
+        }
+        k = key_tiles(s, q, p.mt);
+        if (!PAGED || k.nt > 0 || p.b + 1 == s.B) break;
+        ++p.b;                                          // (no such query tile in this sequence)
         p.mt = 0;
-        q = sink_seq<PAGED>(s, p.b, nullptr);
-        k = key_tiles(s, q, 0);
     }
     u.b = p.b;
     u.h = p.h;
@@ -218,7 +228,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const SinkSched& sc = a.s;
 
     if (threadIdx.x == 0) {
-        sb.gave_up = 0;
+        sb.error = 0;
         for (int i = 0; i < 2; ++i) {
             for (int u = 0; u < kParts; ++u) {
                 mbar_init(&sb.part_full[i][u], 1);
@@ -297,7 +307,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (c0 > u.p1 || (c1 <= u.p0 - sc.W && c0 >= sc.ns)) return sc.p.n_pages;
             int pg = sc.p.table[(size_t)u.b * sc.p.width + (c0 >> sc.p.page_log2)];
             if (pg < 0 || pg >= sc.p.n_pages) {
-                set_status(a.status, GCA_ERR_DEVICE_INDEX);
+                sb.error = GCA_ERR_DEVICE_INDEX;
                 pg = sc.p.n_pages;
             }
             return pg;
@@ -385,7 +395,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             cur = oth;
             oth = t;
         }
-        if (cur.open || oth.open) sb.gave_up = 1;
+        if (cur.open || oth.open) sb.error = GCA_ERR_TIMEOUT;
         const int q_loads[2] = {i == 0 ? cur.np : oth.np, i == 0 ? oth.np : cur.np};
         // no copy may still be writing shared memory when the CTA exits: the last load of
         // each buffer has completed its current phase (Q's have, where their products ran;
@@ -447,7 +457,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 cur = oth;
                 oth = t;
             }
-            if (cur.open || oth.open) sb.gave_up = 1;
+            if (cur.open || oth.open) sb.error = GCA_ERR_TIMEOUT;
             if (issued) {
                 mma_commit(&sb.done);
                 wait_copy(&sb.done, 0);
@@ -542,7 +552,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             cur = oth;
             oth = t;
         }
-        if (cur.open || oth.open) sb.gave_up = 1;
+        if (cur.open || oth.open) sb.error = GCA_ERR_TIMEOUT;
         if (issued && elect_one()) {
             mma_commit(&sb.done2);
             wait_copy(&sb.done2, 0);
@@ -798,13 +808,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 l = 0.f;
             }
         }
-        if (have) sb.gave_up = 1;
+        if (have) sb.error = GCA_ERR_TIMEOUT;
     }
 
     tc_fence_before();
     __syncthreads();
     // (one report a CTA: with one at each wait the code grew by 3 KB and the kernel took 5% longer)
-    if (threadIdx.x == 0 && sb.gave_up) set_status(a.status, GCA_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && sb.error) set_status(a.status, sb.error);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
