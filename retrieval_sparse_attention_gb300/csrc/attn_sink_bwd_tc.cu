@@ -15,7 +15,7 @@
 //            memory).  The steps of an item are the queries whose window reaches its
 //            keys, for each head of the group, and for the items that hold sinks
 //            all later queries as well: those items are many times longer than the others.
-//   join     adds up the parts of the items that were cut.
+//   join     adds up the parts of the items that were cut, if any.
 // Both passes cut the stream of all their steps into equal shares, one a CTA
 // (attn_sink.cuh), so a sink's long item is spread over as many CTAs as it takes
 // and short problems fill the machine; parts are fp32 sums in the workspace, added in
@@ -80,6 +80,7 @@ struct BwdArgs {
     int4 *tailA, *tailB;     // [workers]: the item (b, i, h, 1) whose first part this worker holds, or .w = 0
     int *headA, *headB;      // [workers]: 0, 1 (holds the last part of an earlier worker's item), 2 (a middle part)
     int R;
+    int wholeA, wholeB;      // shares end between items: nothing to join
     int* status;
     float scale_log2, scale;
 };
@@ -288,7 +289,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares_dense<kThreadsA, 1>(sc.B, sc.nMT, sc.Hkv, false, sb.wsum, &sb.pos,
+    find_shares_dense<kThreadsA, 1>(sc.B, sc.nMT, sc.Hkv, a.wholeA, sb.wsum, &sb.pos,
                                    [&](int mt) { return tiles(sc, mt).nt; });
     tc_fence_before();
     pdl_release();
@@ -733,7 +734,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tmem_alloc(&sb.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    find_shares_dense<kThreadsB, 1>(sc.B, a.nKT, sc.Hkv, false, sb.wsum, &sb.pos, [&](int kt) {
+    find_shares_dense<kThreadsB, 1>(sc.B, a.nKT, sc.Hkv, a.wholeB, sb.wsum, &sb.pos, [&](int kt) {
         const Blocks k = blocks(sc, kt);
         return sc.G * (k.nw + k.nf);
     });
@@ -1145,9 +1146,11 @@ cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[
     GCA_LAUNCH("sink_bwd_kv", st,
                e = launch_pdl(pb::sink_bwd_kv_kernel<D>, dim3(grid), kThreadsB, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
     if (e != cudaSuccess) return e;
+    *launches += 3;
+    if (a.wholeA && a.wholeB) return e;
     GCA_LAUNCH("sink_bwd_join", st,
                e = launch_pdl(sink_bwd_join_kernel<D>, dim3(grid, 128 * D / 1024, 3), 256, 0, st, a, grid));
-    if (e == cudaSuccess) *launches += 4;
+    if (e == cudaSuccess) *launches += 1;
     return e;
 }
 
@@ -1196,6 +1199,20 @@ cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, co
     a.status = status;
     a.scale = s.scale;
     a.scale_log2 = s.scale * kLog2e;
+    // Items are left whole where the longest share is then longer than the mean by less than a cut's
+    // sums and the join take, C steps (2 x 4K, 12 heads of 64, W = 512: 83 instead of 96 us), but not
+    // pass A's where pass B's are cut, unless shares are short: the join is launched anyway, and long
+    // shares are more even with cuts (B = 8 x 16K with sinks: 437 instead of 441 us).  Items with
+    // sinks, many times longer than the others, are always cut.
+    auto excess = [](long long items, long long steps) {
+        return (items + kMaxCtas - 1) / kMaxCtas * steps - items * steps / kMaxCtas;
+    };
+    constexpr long long C = 12;
+    const long long spanA = s.W + a.s.TM - 1 < s.L ? s.W + a.s.TM - 1 : s.L, spanB = s.W + 127 < s.L ? s.W + 127 : s.L;
+    const long long itemsA = (long long)s.B * s.Hkv * a.s.nMT, stepsA = (spanA + 62) / 64 + 1 + (s.ns + 63) / 64;
+    const long long itemsB = (long long)s.B * s.Hkv * a.nKT, stepsB = a.s.G * ((spanB + 62) / 64 + 1);
+    a.wholeB = s.ns == 0 && excess(itemsB, stepsB) <= C;
+    a.wholeA = (a.wholeB || itemsA * stepsA <= 40 * kMaxCtas) && excess(itemsA, stepsA) <= C;
     const uint64_t d = s.d, H = s.H, L = s.L, B = s.B, kvcols = (uint64_t)s.Hkv * s.d;
     const uint64_t qn[4] = {d, H, L, B};
     const uint64_t qs[3] = {d, (uint64_t)s.q_stride, (uint64_t)s.q_stride * L}, gs[3] = {d, H * d, H * d * L};

@@ -13,8 +13,8 @@
 // the sequences' lengths (on the device: a captured graph follows them).  A
 // unit cut by a share's end leaves unnormalised fp32 sums with their maxima in
 // the workspace, two slots a worker, and a second small kernel joins them in the
-// order of the stream (no atomics: bitwise reproducible).  Units of up to four
-// tiles are not cut, which saves the second launch.
+// order of the stream (no atomics: bitwise reproducible).  Where whole units make
+// shares that are even enough they are not cut, which saves the second launch.
 //
 // One CTA per SM (12 warps), two workers per CTA:
 //   warp 0     walks the two shares and writes each part of a unit down as a record
@@ -954,11 +954,18 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     a.lse = lse;
     a.status = status;
     a.scale_log2 = s.scale * kLog2e;
-    // Units of few key tiles are left whole: the longest share is then longer by less than the
-    // launch that joins parts takes (3 to 4 key tiles).
+    // Cutting units costs a join and sums in the workspace, the time of some C tiles by the measurements;
+    // leaving them whole costs the difference between the longest share and the mean.  (4K tokens, 12
+    // heads of 64, W = 384: 17.8 us whole, 25.3 cut; B = 8 x 16K, W = 512, 4 sinks 0.343 and 0.353 ms;
+    // a token of 4 x 128 columns over 7 tiles 16.7 and 11.3 us.)  Few tiles a unit only: ragged
+    // lengths make shares of whole units less even than this counts.
     const long long span = (long long)s.W + a.s.TM - 1;
     const long long keys = s.paged ? (long long)s.width * s.page : s.L;
-    a.whole = (span < keys ? (span + 126) / 128 + 1 + (s.ns + 127) / 128 : (keys + 127) / 128) <= 4;
+    const long long nt = span < keys ? (span + 126) / 128 + 1 + (s.ns + 127) / 128 : (keys + 127) / 128;
+    const long long pairs = (long long)s.B * a.s.nMT, packed = (long long)s.T / a.s.TM + s.B;
+    const long long units = s.Hkv * (s.paged && packed < pairs ? packed : pairs);
+    const long long C = (s.d == 64 ? 6 : 3) + a.R * s.d / 1536;
+    a.whole = nt <= 2 * C + 2 && (units + kMaxWorkers - 1) / kMaxWorkers * nt * kMaxWorkers <= units * nt + C * kMaxWorkers;
     CUtensorMap tq, tk, tv;
     const uint64_t kvcols = (uint64_t)s.Hkv * s.d;
     bool ok = encode_bf16_3d(&tq, q, s.d, s.H, s.T, s.d, s.q_stride, a.s.G, a.s.TM);
