@@ -27,9 +27,9 @@
 // memory, which is the layout of the A operands that it writes.
 //
 // Measured (GB300), B = 8 x 16K, 12 heads of 64, W = 512, 4 sinks: vectors 0.07 ms (6.2
-// TB/s), pass A 0.435, pass B 0.62, join 0.01: 1.13 ms in all, 1.00 without sinks (the
+// TB/s), pass A 0.435, pass B 0.62, join 0.01: 1.13 ms in all, 1.00 without sinks and join (the
 // plain window's gradients, gca_swa_bwd, 1.22).  2 x 16K, 16/4 heads of 128, W = 1024, 16
-// sinks: 0.05, 0.385, 0.52, 0.02: 0.98 ms.  3 x 1000, 6/2 heads: 33 us in a graph.
+// sinks: 0.05, 0.385, 0.52, 0.02: 0.98 ms.  3 x 1000, 6/2 heads: 37 us.
 // What bounds it: pass A and B keep the tensor pipe 31% and 33% busy and the issue
 // slots 49% and 51%; the math warps' latency a step and the issuing threads' share of
 // the slots pace them (pass B, a clock trace: a step every 1,165 cycles; a math pair's two

@@ -80,6 +80,18 @@ def test_every_element(qs, kvs, H, Hkv, d, page, window, sinks):
         c.check(o, lse, window, sinks)
 
 
+@pytest.mark.parametrize("qs,kvs,H,Hkv,d,page,window,sinks", [
+    ([1, 1], [2000, 900], 16, 4, 128, 64, 600, 16), ([1, 1, 1], [5000, 4900, 130], 6, 6, 64, 16, 1500, 4),
+    ([1, 2], [4000, 1000], 8, 2, 64, 32, 3000, 130), ([300, 1], [4000, 4000], 12, 12, 64, 64, 2500, 4)])
+def test_windows_whose_units_are_cut(qs, kvs, H, Hkv, d, page, window, sinks):
+    c = Cache(qs, kvs, H, Hkv, d, page, seed=sum(kvs))
+    o, lse = api.paged_attn(*c.cuda(), max_q=max(qs), window=window, sinks=sinks, with_lse=True)
+    assert api.gca_last_launch_count() == 2                # the join too
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == 0
+    c.check(o, lse, window, sinks)
+
+
 def test_long_cache_split_over_the_machine():
     # one token over a long cache, and a chunk beside it: the key axis is divided and joined
     c = Cache([1, 3, 1], [30000, 9000, 70], 4, 2, 128, 64, seed=1)

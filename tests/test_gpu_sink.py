@@ -231,6 +231,13 @@ def test_every_element_of_longer_rows(B, L, H, Hkv, d, window, sinks):
     torch.cuda.empty_cache()
 
 
+# a few units more than there are workers, of many tiles each: windows whose units are cut
+@pytest.mark.parametrize("B,L,H,Hkv,d,window,sinks", [(1, 3300, 12, 12, 64, 1500, 4), (1, 2464, 16, 4, 128, 1800, 16),
+                                                      (1, 3290, 12, 12, 64, 2000, 0)])
+def test_windows_whose_units_are_cut(B, L, H, Hkv, d, window, sinks):
+    test_every_element_of_longer_rows(B, L, H, Hkv, d, window, sinks)
+
+
 def test_full_size_sampled():
     # the 12-head model's batch: single rows against the reference on what they see
     B, L, H, d, W, ns = 8, 16384, 12, 64, 512, 4
