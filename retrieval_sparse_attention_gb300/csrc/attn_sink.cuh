@@ -110,6 +110,8 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole,
     const int per = (E + THREADS - 1) / THREADS;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
     int mine = 0, base = 0, total = 0, quota = 0;
+    const int b0 = e0 / n, i0 = e0 - b0 * n;
+    const auto q0 = seq(min(b0, B - 1));
     auto wid = [&](int w) {
         return total <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x + w * gridDim.x)
                                                     : static_cast<int>(blockIdx.x) * SHARES + w;
@@ -118,8 +120,8 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole,
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         int at = base;
-        int b = e0 / n, i = e0 - b * n;
-        auto q = seq(min(b, B - 1));
+        int b = b0, i = i0;
+        auto q = q0;
 #pragma unroll 1
         for (int e = e0; e < e1; ++e) {
             if (e > e0 && i == 0) q = seq(b);
@@ -163,7 +165,7 @@ __device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole,
             if (lane == 31) wsum[warp] = inc;
             if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0, -1, {0, 0, 0}};
             __syncthreads();
-#pragma unroll 1
+#pragma unroll
             for (int w = 0; w < THREADS / 32; ++w) {
                 if (w < warp) base += wsum[w];
                 total += wsum[w];
@@ -205,7 +207,7 @@ __device__ __forceinline__ void find_shares_dense(int B, int n, int heads, bool 
     if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0, -1, {0, 0, 0}};
     __syncthreads();
     int base = inc - mine, row = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) base += wsum[w];
         row += wsum[w];

@@ -227,36 +227,38 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const SinkSched& sc = a.s;
 
-    if (threadIdx.x == 0) {
-        sb.error = 0;
-        for (int i = 0; i < 2; ++i) {
-            for (int u = 0; u < kParts; ++u) {
-                mbar_init(&sb.part_full[i][u], 1);
-                mbar_init(&sb.part_empty[i][u], 8);       // both producers, both issuers, 4 softmax warps
-            }
-            for (int u = 0; u < 2; ++u) {
-                mbar_init(&sb.q_full[i][u], 1);
-                mbar_init(&sb.q_empty[i][u], 1);
-            }
-            mbar_init(&sb.s_full[i], 1);
-            mbar_init(&sb.s_empty[i], C::P_OVER_S ? 1 : 128);
-            mbar_init(&sb.p_full[i], 128);
-            mbar_init(&sb.p_empty[i], 1);
-            mbar_init(&sb.o_full[i], 1);
-            mbar_init(&sb.o_empty[i], 128);
+    if (warp == 0) {                                      // a barrier a lane
+        if (lane < 2 * kParts) {
+            mbar_init(&sb.part_full[0][lane], 1);
+            mbar_init(&sb.part_empty[0][lane], 8);        // both producers, both issuers, 4 softmax warps
         }
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&sb.k_full[i], 1);
-            mbar_init(&sb.k_empty[i], 1);
-            mbar_init(&sb.v_full[i], 1);
-            mbar_init(&sb.v_empty[i], 1);
+        if (lane < 4) {
+            mbar_init(&sb.q_full[0][lane], 1);
+            mbar_init(&sb.q_empty[0][lane], 1);
         }
-        mbar_init(&sb.done, 1);
-        mbar_init(&sb.done2, 1);
+        if (lane < 2) {
+            mbar_init(&sb.s_full[lane], 1);
+            mbar_init(&sb.s_empty[lane], C::P_OVER_S ? 1 : 128);
+            mbar_init(&sb.p_full[lane], 128);
+            mbar_init(&sb.p_empty[lane], 1);
+            mbar_init(&sb.o_full[lane], 1);
+            mbar_init(&sb.o_empty[lane], 128);
+        }
+        if (lane < C::STAGES) {
+            mbar_init(&sb.k_full[lane], 1);
+            mbar_init(&sb.k_empty[lane], 1);
+            mbar_init(&sb.v_full[lane], 1);
+            mbar_init(&sb.v_empty[lane], 1);
+        }
+        if (lane == 0) {
+            sb.error = 0;
+            mbar_init(&sb.done, 1);
+            mbar_init(&sb.done2, 1);
+            prefetch_tmap(&tq);
+            prefetch_tmap(&tk);
+            prefetch_tmap(&tv);
+        }
         fence_barrier_init();
-        prefetch_tmap(&tq);
-        prefetch_tmap(&tk);
-        prefetch_tmap(&tv);
     }
     if (warp == 1) {
         tmem_alloc(&sb.tmem, TMEM_COLS);

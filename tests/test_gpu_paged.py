@@ -304,6 +304,14 @@ def test_append_writes_its_rows_and_no_others(qs, kvs, Hkv, d, page, max_q):
     assert same(kc, want_k) and same(vc, want_v)
 
 
+def test_append_to_many_sequences():
+    # far more than a warp looks at together, idle ones and chunks among single tokens
+    g = torch.Generator().manual_seed(6)
+    qs = [int(x) for x in torch.tensor([0, 1, 1, 1, 2, 0, 60])[torch.randint(7, (700,), generator=g)]]
+    kvs = [q + int(x) for q, x in zip(qs, torch.randint(0, 50, (700,), generator=g))]
+    test_append_writes_its_rows_and_no_others(qs, kvs, 2, 64, 16, 60)
+
+
 def test_append_reports_a_bad_page_and_writes_the_rest():
     c = Cache([40], [40], 1, 1, 64, 16)
     c.table[0, 1] = c.n_pages
