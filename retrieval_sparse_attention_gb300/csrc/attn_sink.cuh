@@ -98,96 +98,108 @@ struct StreamPos {
 // The shares of this CTA (SHARES workers, neighbours in the stream; where there are
 // fewer steps than CTAs, each CTA has one worker with a share at most) in a stream of
 // equally long steps: sequence b has entries i < n, entry i takes count(seq(b), i)
-// steps for each of `heads` heads, in the order (b, i, head, step).
-// Every worker gets total / workers steps, rounded up.  All THREADS threads of the
-// CTA take part; ends with __syncthreads.  The host bounds the total below 2^31.
-// whole: cuts move to the next entry's or head's first step.
+// steps for each of `heads` heads, in the order (b, head, i, step): a worker follows one
+// head along the sequence and finds most of an entry's tiles in the L2 cache, where its
+// last entries brought them.  Every worker gets total / workers steps, rounded up.  All
+// THREADS threads of the CTA take part; ends with __syncthreads.  The host bounds the
+// total below 2^31.  whole: cuts move to the next entry's first step, which may be one that
+// the sequence does not have (the walk passes over it).
 template <int THREADS, int SHARES, class Seq, class Count>
-__device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole, int* wsum, StreamPos* pos, Seq seq,
-                                            Count count) {
+__device__ __forceinline__ void find_shares(int B, int n, int heads, bool whole, int* wsum, int (*found)[3],
+                                            StreamPos* pos, Seq seq, Count count) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = B * n;                            // entries, a run of them for each thread
     const int per = (E + THREADS - 1) / THREADS;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
-    int mine = 0, base = 0, total = 0, quota = 0;
     const int b0 = e0 / n, i0 = e0 - b0 * n;
     const auto q0 = seq(min(b0, B - 1));
-    auto wid = [&](int w) {
-        return total <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x + w * gridDim.x)
-                                                    : static_cast<int>(blockIdx.x) * SHARES + w;
-    };
-    // first pass: the steps of this thread's entries; second: which entry holds a cut
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        int at = base;
+    auto each = [&](auto f) {                       // f(sequence, entry, steps) for this thread's entries
         int b = b0, i = i0;
         auto q = q0;
 #pragma unroll 1
         for (int e = e0; e < e1; ++e) {
             if (e > e0 && i == 0) q = seq(b);
-            const int c = count(q, i);
-            if (pass == 0) {
-                mine += c;
-            } else {
-                const int len = c * heads;
-#pragma unroll 1
-                for (int k = 0; k < 2 * SHARES; ++k) {
-                    // worker w's share: its first step (k even) and its end, one past its last step
-                    const int w = k >> 1;
-                    const int from = wid(w) * quota;
-                    const int x = (k & 1) ? min(total, from + quota) : from;
-                    if (x < at || x >= at + len || from >= total) continue;
-                    int h = (x - at) / c, j = x - at - h * c;
-                    const int skip = whole && j > 0 ? c - j : 0;
-                    if (k & 1) {
-                        atomicAdd(&pos[w].left, x - from + skip);
-                    } else {
-                        atomicAdd(&pos[w].left, -skip);
-                        int m = i;
-                        if (skip) {
-                            j = 0;
-                            if (++h == heads) { h = 0; ++m; }    // (no such entry: the walk passes over it)
-                        }
-                        pos[w].b = b; pos[w].mt = m; pos[w].h = h; pos[w].j = j;
-                    }
-                }
-                at += len;
-            }
+            f(b, i, count(q, i));
             if (++i == n) { i = 0; ++b; }
         }
-        if (pass == 0) {
-            int inc = mine;
+    };
+    int mine = 0;
+    each([&](int, int, int c) { mine += c; });
+    int inc = mine;
 #pragma unroll 1
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += x;
-            }
-            if (lane == 31) wsum[warp] = inc;
-            if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0, -1, {0, 0, 0}};
-            __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    if (tid < SHARES) pos[tid] = StreamPos{0, 0, 0, 0, 0, 0, -1, {0, 0, 0}};
+    __syncthreads();
+    int base = inc - mine, row = 0;                 // steps of one head: before this thread's entries, in all
 #pragma unroll
-            for (int w = 0; w < THREADS / 32; ++w) {
-                if (w < warp) base += wsum[w];
-                total += wsum[w];
-            }
-            base = (base + inc - mine) * heads;
-            total *= heads;
-            const int workers = SHARES * gridDim.x;
-            quota = (total + workers - 1) / workers;
-            if (tid < SHARES) {                         // a share that ends with the stream
-                const int from = wid(tid) * quota;
-                pos[tid].wid = wid(tid);
-                if (from < total && from + quota >= total) atomicAdd(&pos[tid].left, total - from);
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += wsum[w];
+        row += wsum[w];
+    }
+    const int total = row * heads, workers = SHARES * gridDim.x;
+    const int quota = (total + workers - 1) / workers;
+    auto wid = [&](int w) {
+        return total <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x + w * gridDim.x)
+                                                    : static_cast<int>(blockIdx.x) * SHARES + w;
+    };
+    // worker w's share: its first step (k = 2 w) and its end, one past its last step (2 w + 1)
+    auto cut = [&](int k) {
+        const int from = wid(k >> 1) * quota;
+        return from >= total ? total : (k & 1) ? min(total, from + quota) : from;
+    };
+    if (tid < SHARES) {                             // a share that ends with the stream
+        const int from = cut(2 * tid);
+        pos[tid].wid = wid(tid);
+        if (from < total && from + quota >= total) atomicAdd(&pos[tid].left, total - from);
+    }
+    if (n > 1) {
+        // the sequence of each cut: where its steps begin and end
+        if (tid < 2 * SHARES) {
+            found[tid][0] = 0;
+            found[tid][1] = row;
+        }
+        __syncthreads();
+        int at = base;
+        each([&](int, int i, int c) {
+            if (i == 0)
+#pragma unroll 1
+                for (int k = 0; k < 2 * SHARES; ++k) {
+                    if (at * heads <= cut(k)) atomicMax(&found[k][0], at);
+                    else atomicMin(&found[k][1], at);
+                }
+            at += c;
+        });
+        __syncthreads();
+    }
+    // which entry holds a cut
+    int at = base;
+    each([&](int b, int i, int c) {
+#pragma unroll 1
+        for (int k = 0; k < 2 * SHARES; ++k) {
+            const int x = cut(k), first = n > 1 ? found[k][0] : at, len = n > 1 ? found[k][1] - first : c;
+            const int r = x - first * heads;
+            if (x == total || c == 0 || r < 0 || r >= len * heads) continue;
+            const int h = r / len, j = first + r - h * len - at;
+            if (j < 0 || j >= c || h >= heads) continue;
+            const int w = k >> 1, skip = whole && j > 0 ? c - j : 0;
+            if (k & 1) {
+                atomicAdd(&pos[w].left, x - wid(w) * quota + skip);
+            } else {
+                atomicAdd(&pos[w].left, -skip);
+                pos[w].b = b; pos[w].h = h; pos[w].mt = i + (skip > 0); pos[w].j = skip ? 0 : j;
             }
         }
-    }
+        at += c;
+    });
     __syncthreads();
 }
 
-// The same for dense sequences, which all have the same entries: the stream's order is
-// (sequence, head, i, step), so that a worker follows one head along the sequence and
-// finds most of an entry's tiles in the L2 cache, where its last entries brought them.
-// The entries of one (sequence, head) are summed up; the cuts divide by their total.
+// The same for dense sequences, which all have the same entries: those of one (sequence, head)
+// are summed up, and the cuts divide by their total.
 template <int THREADS, int SHARES, class Count>
 __device__ __forceinline__ void find_shares_dense(int B, int n, int heads, bool whole, int* wsum, StreamPos* pos,
                                                   Count count) {

@@ -153,7 +153,7 @@ struct __align__(16) Bars {
     uint32_t tmem;
     int error;           // what the CTA has to report, or 0
     StreamPos pos[2];
-    int wsum[12];
+    int wsum[12], found[4][3];
 };
 
 // The next part of a share (one thread); moves `p` behind it.  A part that began in an
@@ -165,23 +165,26 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     Part u{};
     if (p.left <= 0) return u;
     SeqInfo q;
-    KeyTiles k;
+    if (!PAGED) {
+        q = sink_seq<PAGED>(s, p.b, nullptr);
+    } else {
+        // to the next query tile that exists: of this head, of the sequence's next one, of a later sequence
 #pragma unroll 1
-    while (true) {
-        if (!PAGED) {
-            q = sink_seq<PAGED>(s, p.b, nullptr);
-        } else {
+        while (true) {
             if (p.qb != p.b) {
                 p.q = sink_seq<PAGED>(s, p.b, nullptr);
                 p.qb = p.b;
             }
             q = p.q;
+            if (p.mt * s.TM < q.n) break;
+            p.mt = 0;
+            if (q.n > 0 && ++p.h < s.Hkv) break;
+            p.h = 0;
+            if (p.b + 1 == s.B) { p.left = 0; return u; }
+            ++p.b;
         }
-        k = key_tiles(s, q, p.mt);
-        if (!PAGED || k.nt > 0 || p.b + 1 == s.B) break;
-        ++p.b;                                          // (no such query tile in this sequence)
-        p.mt = 0;
     }
+    const KeyTiles k = key_tiles(s, q, p.mt);
     u.b = p.b;
     u.h = p.h;
     u.qrow = q.row0 + p.mt * s.TM;
@@ -205,9 +208,7 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     else if (u.j1 < k.nt) a.tail[wid_tail] = make_int4(p.b, p.mt, p.h, 1);
     p.left -= u.j1 - u.j0;
     p.j = 0;
-    if (PAGED) {
-        if (++p.h == s.Hkv) { p.h = 0; ++p.mt; }
-    } else if (++p.mt == s.nMT) {
+    if (++p.mt == s.nMT && !PAGED) {
         p.mt = 0;
         if (++p.h == s.Hkv) { p.h = 0; ++p.b; }
     }
@@ -266,7 +267,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     pdl_release();
     if (PAGED)
-        find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, a.whole, sb.wsum, sb.pos,
+        find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, a.whole, sb.wsum, sb.found, sb.pos,
                                  [&](int b) { return sink_seq<PAGED>(sc, b, a.status); },
                                  [&](const SeqInfo& q, int mt) { return key_tiles(sc, q, mt).nt; });
     else
@@ -320,7 +321,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 a.head[sb.pos[i].wid] = 0;
                 a.tail[sb.pos[i].wid] = make_int4(0, 0, 0, 0);
             }
-            // Dense rows: where the tiles that all workers go through for one unit each fill more than
+            // Where the tiles that all workers go through for one unit each fill more than
             // half of the L2 cache, the two workers take turns at the units of both shares, neighbours
             // in the sequence, so that one finds the tiles the other has just read (B = 8 x 16K, 12
             // heads of 64, W = 2048: 0.85 instead of 1.22 ms; 64K, 16/4 heads of 128, W = 1024: 0.53
@@ -329,7 +330,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             // Few units: each worker has its own share, so both end at the same time.
             StreamPos& p = sb.pos[0];
             const int both = p.left + sb.pos[1].left;
-            if (!PAGED && sb.pos[1].left > 0) {
+            if (sb.pos[1].left > 0) {
                 const int nt = key_tiles(sc, sink_seq<PAGED>(sc, p.b, nullptr), p.mt).nt;
                 alternate = both >= 16 * nt && (p.j > 0 ? p.left >= nt - p.j : true) &&
                             static_cast<size_t>(nt) * (4 * C::TILE) * gridDim.x > kHalfL2;
