@@ -75,8 +75,8 @@ struct BwdArgs {
     float *nlA, *ndA;        // [B * Hkv * nMT][128]: rows of the query tiles
     float *nlB, *ndB;        // [B * H][Lp]
     __nv_bfloat16 *dq, *dk, *dv;
-    float* partA;            // [2 * workers][128][D]
-    float* partB;            // [2 * workers][2][128][D]: dK, dV
+    float* partA;            // [2 * workers][D / 4][128][4]
+    float* partB;            // [2 * workers][2][D / 4][128][4]: dK, dV
     int4 *tailA, *tailB;     // [workers]: the item (b, i, h, 1) whose first part this worker holds, or .w = 0
     int *headA, *headB;      // [workers]: 0, 1 (holds the last part of an earlier worker's item), 2 (a middle part)
     int R;
@@ -140,18 +140,19 @@ __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     }
 }
 
-// N columns of this lane's row of an fp32 accumulator to the workspace.
+// N columns of this lane's row of an fp32 accumulator to a [N / 4][128][4] array of the
+// workspace (rows side by side: the lanes of a store write 512 consecutive bytes).
 template <int N>
-__device__ __forceinline__ void store_rows_f32(uint32_t taddr, float* dst, bool live) {
+__device__ __forceinline__ void store_rows_f32(uint32_t taddr, float* dst, int row, bool live) {
 #pragma unroll 1
     for (int ci = 0; ci < N / 32; ++ci) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(taddr + 32 * ci, r);
         tmem_wait_ld();
         if (live) {
-            uint4* d4 = reinterpret_cast<uint4*>(dst) + 8 * ci;
+            uint4* d4 = reinterpret_cast<uint4*>(dst) + 8 * ci * 128 + row;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) d4[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+            for (int u = 0; u < 8; ++u) d4[u * 128] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
         }
     }
 }
@@ -468,7 +469,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
 #pragma unroll
                 for (int ci = 0; ci < D / 32; ++ci) store_rows32(pk[ci], a.dq + 32 * ci, D, pend_row);
             } else {
-                store_rows_f32<D>(acc, a.partA + ((size_t)pend_slot * 128 + row) * D, pend_row >= 0);
+                store_rows_f32<D>(acc, a.partA + (size_t)pend_slot * 128 * D, row, pend_row >= 0);
                 tc_fence_before();
                 mbar_arrive(&sb.o_empty[ob]);
             }
@@ -934,7 +935,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     }
                 }
             } else {
-                store_rows_f32<D>(acc, a.partB + ((size_t)pend_slot * 256 + half * 128 + row) * D, pend_row >= 0);
+                store_rows_f32<D>(acc, a.partB + ((size_t)pend_slot * 256 + half * 128) * D, row, pend_row >= 0);
                 tc_fence_before();
                 mbar_arrive(&sb.o_empty);
             }
@@ -1061,7 +1062,8 @@ __global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int
     if (it.w == 0) return;
     const int n = parts_of(pass_a ? a.headA : a.headB, w, workers);
     constexpr int VEC = D / 4;
-    const int row = blockIdx.y * (256 / VEC) + threadIdx.x / VEC, c = threadIdx.x % VEC;
+    constexpr int ROWS = 256 / VEC;
+    const int row = blockIdx.y * ROWS + threadIdx.x % ROWS, c = threadIdx.x / ROWS;
     size_t orow;
     if (pass_a) {
         const int rt = row / sc.G, t = it.y * sc.TM + rt;
@@ -1078,7 +1080,7 @@ __global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
         const size_t slot = k == 0 ? 2 * w + 1 : 2 * (w + k);
-        const float4 x = reinterpret_cast<const float4*>(base + (slot * slot_rows + row) * D)[c];
+        const float4 x = reinterpret_cast<const float4*>(base + slot * slot_rows * D)[c * 128 + row];
         acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
     }
     __nv_bfloat16* dst = pass_a ? a.dq : blockIdx.z == 1 ? a.dk : a.dv;

@@ -109,7 +109,7 @@ struct FwdArgs {
     SinkSched s;
     __nv_bfloat16* o;
     float* lse;
-    float* part_o;           // [2 * workers][R][D]
+    float4* part_o;          // [2 * workers][D / 4][R], for R < 1024 / D [2 * workers][R][D / 4]
     float2* part_ml;         // [2 * workers][R]: maximum (log2 units), sum
     int4* tail;              // [workers]: unit (b, mt, h, 1) whose first part this worker holds, or .w = 0
     int* head;               // [workers]: 0, 1 (holds the last part of an earlier worker's unit), 2 (a middle part)
@@ -585,7 +585,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // the finished part whose O still sits in tensor memory
         bool pend = false;
         int pend_row = -1;                              // token * H + head, or -1: no such row
-        int pend_slot = -1;                             // -1: whole unit; else the row in the workspace
+        int pend_slot = -1;                             // -1: whole unit; else its sums' first row in the workspace
         float pm = 0.f, pl = 1.f;
         while (true) {
             if (first) {                                // the next part of the share
@@ -623,14 +623,16 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             uint32_t r[16];
                             tmem_ld_32x32b_x16(to_addr + 16 * ci, r);
                             tmem_wait_ld();
-                            uint4* dst = reinterpret_cast<uint4*>(a.part_o + (size_t)pend_slot * D) + 4 * ci;
+                            // (rows side by side: the lanes of a store write 512 consecutive bytes)
+                            const int cs = a.R < 1024 / D ? 1 : a.R, rs = a.R < 1024 / D ? D / 4 : 1;
+                            uint4* dst = reinterpret_cast<uint4*>(a.part_o) + (size_t)pend_slot * (D / 4) + 4 * ci * cs + row * rs;
                             if (wr)
 #pragma unroll
                                 for (int u = 0; u < 4; ++u)
-                                    dst[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                                    dst[u * cs] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
                         }
                     }
-                    if (wr && pend_slot >= 0) a.part_ml[pend_slot] = make_float2(pm, pl);
+                    if (wr && pend_slot >= 0) a.part_ml[pend_slot + row] = make_float2(pm, pl);
                     if (wr && pend_slot < 0 && a.lse) a.lse[pend_row] = pl > 0.f ? (pm + log2f(pl)) * kLn2 : -INFINITY;
                 }
                 tc_fence_before();
@@ -802,7 +804,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (first) {                                // this part of the unit is done: it leaves later
                 pend = true;
                 pend_row = live ? (w.qrow + rt) * sc.H + w.h * sc.G + rg : -1;
-                pend_slot = w.slot < 0 ? -1 : w.slot + row;
+                pend_slot = w.slot;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sb.part_empty[wg][(np - 1) % kParts]);
                 pm = m;
@@ -839,20 +841,23 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const FwdArgs a, int wor
     const SinkSched& sc = a.s;
     const SeqInfo s = sink_seq<PAGED>(sc, u.x, nullptr);
     constexpr int VEC = D / 4;
-    const int row = blockIdx.y * (256 / VEC) + threadIdx.x / VEC, c = threadIdx.x % VEC;
+    constexpr int ROWS = 256 / VEC;
+    const bool few = a.R < ROWS;                        // (one block: its lanes along the columns)
+    const int row = blockIdx.y * ROWS + (few ? threadIdx.x / VEC : threadIdx.x % ROWS);
+    const int c = few ? threadIdx.x % VEC : threadIdx.x / ROWS;
     const int rt = row / sc.G, t = u.y * sc.TM + rt;
     if (row >= a.R || t >= s.n) return;
-    const auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * w + 1 : 2 * (w + k)) * a.R + row; };
+    const auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * w + 1 : 2 * (w + k)) * a.R; };   // first row of its sums
     float m = -INFINITY;
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) m = fmaxf(m, a.part_ml[slot(k)].x);
+    for (int k = 0; k < n; ++k) m = fmaxf(m, a.part_ml[slot(k) + row].x);
     const float mu = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-        const float2 ml = a.part_ml[slot(k)];
-        const float4 o = reinterpret_cast<const float4*>(a.part_o + slot(k) * D)[c];
+        const float2 ml = a.part_ml[slot(k) + row];
+        const float4 o = a.part_o[slot(k) * VEC + (few ? row * VEC + c : c * a.R + row)];
         const float f = fast_exp2(ml.x - mu);
         acc.x = fmaf(o.x, f, acc.x);
         acc.y = fmaf(o.y, f, acc.y);
@@ -949,7 +954,7 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     if (!sink_fwd_supported(s)) return cudaErrorInvalidConfiguration;
     const Layout w = layout(s);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    a.part_o = reinterpret_cast<float*>(base + w.o_off);
+    a.part_o = reinterpret_cast<float4*>(base + w.o_off);
     a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
     a.tail = reinterpret_cast<int4*>(base + w.tail_off);
     a.head = reinterpret_cast<int*>(base + w.head_off);
@@ -958,16 +963,17 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     a.status = status;
     a.scale_log2 = s.scale * kLog2e;
     // Cutting units costs a join and sums in the workspace, the time of some C tiles by the measurements;
-    // leaving them whole costs the difference between the longest share and the mean.  (4K tokens, 12
-    // heads of 64, W = 384: 17.8 us whole, 25.3 cut; B = 8 x 16K, W = 512, 4 sinks 0.343 and 0.353 ms;
-    // a token of 4 x 128 columns over 7 tiles 16.7 and 11.3 us.)  Few tiles a unit only: ragged
+    // leaving them whole costs the difference between the longest share and the mean.  (312 units of 15
+    // tiles, 12 heads of 64: 28.4 us whole, 33.1 cut; 308 of 17, 16/4 heads of 128: 34.6 and 43.4; B =
+    // 8 x 16K, W = 512, 4 sinks: 0.339 and 0.348 ms; a token of 4 x 128 columns over 7 tiles: 16.7 and
+    // 11.3 us.)  Few tiles a unit only: ragged
     // lengths make shares of whole units less even than this counts.
     const long long span = (long long)s.W + a.s.TM - 1;
     const long long keys = s.paged ? (long long)s.width * s.page : s.L;
     const long long nt = span < keys ? (span + 126) / 128 + 1 + (s.ns + 127) / 128 : (keys + 127) / 128;
     const long long pairs = (long long)s.B * a.s.nMT, packed = (long long)s.T / a.s.TM + s.B;
     const long long units = s.Hkv * (s.paged && packed < pairs ? packed : pairs);
-    const long long C = (s.d == 64 ? 6 : 3) + a.R * s.d / 1536;
+    const long long C = (s.d == 64 ? 6 : 3) + a.R * s.d / 896;
     a.whole = nt <= 2 * C + 2 && (units + kMaxWorkers - 1) / kMaxWorkers * nt * kMaxWorkers <= units * nt + C * kMaxWorkers;
     CUtensorMap tq, tk, tv;
     const uint64_t kvcols = (uint64_t)s.Hkv * s.d;
