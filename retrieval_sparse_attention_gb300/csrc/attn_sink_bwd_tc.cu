@@ -26,10 +26,17 @@
 // each); a thread owns a query row (pass A) or a key row (pass B), a lane of tensor
 // memory, which is the layout of the A operands that it writes.
 //
+// Roundings: P and ds to bf16, the type of the products' operands (relative 2^-8 at most, as
+// the gradients' own rounding, and as many random terms' errors they add up to about as much as
+// that: rms 1.7e-3 each); delta takes o as the forward rounded it (rms 5e-4 of a gradient).
+// Together 2.4e-3 to 2.6e-3 of a gradient's norm, where its own rounding alone is 1.7e-3.
+// Scores, lse, dP, delta and all sums are fp32.  (ds as two bf16 operands would halve the
+// excess for a third more products and a quarter more arithmetic in pass A.)
+//
 // Measured (GB300), B = 8 x 16K, 12 heads of 64, W = 512, 4 sinks: vectors 0.07 ms (6.2
-// TB/s), pass A 0.435, pass B 0.62, join 0.01: 1.13 ms in all, 1.00 without sinks and join (the
+// TB/s), pass A 0.433, pass B 0.615, join 0.01: 1.125 ms in all, 0.99 without sinks and join (the
 // plain window's gradients, gca_swa_bwd, 1.22).  2 x 16K, 16/4 heads of 128, W = 1024, 16
-// sinks: 0.05, 0.385, 0.52, 0.02: 0.98 ms.  3 x 1000, 6/2 heads: 37 us.
+// sinks: 0.05, 0.387, 0.515, 0.02: 0.976 ms.  3 x 1000, 6/2 heads: 38 us.
 // What bounds it: pass A and B keep the tensor pipe 31% and 33% busy and the issue
 // slots 49% and 51%; the math warps' latency a step and the issuing threads' share of
 // the slots pace them (pass B, a clock trace: a step every 1,165 cycles; a math pair's two

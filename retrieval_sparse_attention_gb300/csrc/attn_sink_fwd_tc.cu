@@ -35,9 +35,9 @@
 // others are masked in registers.  Up to 32 sinks take a tile of 32 columns.
 //
 // Measured (GB300; fractions of the measured 6.7 TB/s and 2.0 PFLOP/s):
-//   B = 8 x 16K, 12 heads of 64, W = 512: 0.310 ms, with 4 sinks 0.343 (2.4 TB/s);
-//   W = 2048 0.81 ms; 64K, 16/4 heads of 128, W = 1024, 16 sinks: 0.53-0.57 ms (0.97
-//   PFLOP/s, 48%); four chunks of 1.5-2K over 6-16K, 16/4 heads of 128: 0.43 ms
+//   B = 8 x 16K, 12 heads of 64, W = 512: 0.308 ms, with 4 sinks 0.340 (2.4 TB/s);
+//   W = 2048 0.81 ms; 64K, 16/4 heads of 128, W = 1024, 16 sinks: 0.52-0.55 ms (1.0
+//   PFLOP/s, 50%); four chunks of 1.5-2K over 6-16K, 16/4 heads of 128: 0.43 ms
 //   (1.37 PFLOP/s, 69%); 32 tokens over caches of 4-33K, 24/8 heads of 128: 0.335
 //   ms (6.7 TB/s, 99%); one token over 777, W = 512: 12 us in a graph.
 // What bounds it.  Single tokens over long caches: the cache's bytes.  d = 128 with

@@ -206,6 +206,31 @@ def test_rows_far_into_the_token_tensors():
     assert int((kc.abs().sum(-1) > 0).sum()) == 5
 
 
+@pytest.mark.parametrize("d,window", [(64, 900), (128, 500)])
+def test_many_units_of_long_windows(d, window):
+    # so many that the two workers of a CTA share one stretch of units: the same bits as from
+    # calls on a few of the heads, dense and through the cache
+    B, L, H, page = 2, 2600, 64, 64
+    g = torch.Generator().manual_seed(d)
+    q, k, v = (torch.randn(B, L, H, d, generator=g).to(torch.bfloat16).cuda() for _ in range(3))
+    o, lse = api.swa_sink_fwd(q, k, v, window=window, sinks=4)
+    assert api.gca_last_launch_count() == 1
+    for h in (0, 31, 62):
+        heads = slice(h, h + 2)
+        a, b = api.swa_sink_fwd(*(x[:, :, heads].contiguous() for x in (q, k, v)), window=window, sinks=4)
+        assert torch.equal(o[:, :, heads], a) and torch.equal(lse[:, :, heads], b)
+    n = -(-L // page)
+    table = torch.randperm(B * n, generator=g).view(B, n).to(torch.int32).cuda()
+    kc, vc = (torch.full((B * n, page, H, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cu = torch.tensor([0, L, 2 * L], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([L, L], dtype=torch.int32, device="cuda")
+    api.paged_append(k.view(B * L, H, d), v.view(B * L, H, d), kc, vc, table, cu, kv)
+    a, b = api.paged_attn(q.view(B * L, H, d), kc, vc, table, cu, kv, max_q=L, window=window, sinks=4, with_lse=True)
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == 0
+    assert torch.equal(a.view_as(o), o) and torch.equal(b.view_as(lse), lse)
+
+
 def test_two_streams_at_once():
     # calls that overlap, each with its own workspace, and what they give one after the other
     a = Cache([1] * 8, [4000 + 300 * i for i in range(8)], 8, 2, 128, 64, seed=8)
