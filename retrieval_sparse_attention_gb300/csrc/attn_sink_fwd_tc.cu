@@ -308,8 +308,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const int c0 = u.tile(cur.j) * 128 + (lane << sc.p.page_log2);
             const int c1 = c0 + (1 << sc.p.page_log2) - 1;
             if (c0 > u.p1 || (c1 <= u.p0 - sc.W && c0 >= sc.ns)) return sc.p.n_pages;
-            int pg = sc.p.table[(size_t)u.b * sc.p.width + (c0 >> sc.p.page_log2)];
-            if (pg < 0 || pg >= sc.p.n_pages) {
+            int pg = __ldg(sc.p.table + (size_t)u.b * sc.p.width + (c0 >> sc.p.page_log2));
+            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(sc.p.n_pages)) {
                 sb.error = GCA_ERR_DEVICE_INDEX;
                 pg = sc.p.n_pages;
             }
