@@ -293,7 +293,8 @@ typedef struct {
                              (a slice of a packed q/k/v projection has this form)           */
 } gca_swa_sink_params_t;
 
-/* Bytes of device workspace gca_swa_sink_fwd needs (0 for invalid parameters). */
+/* Bytes of device workspace gca_swa_sink_fwd needs (0 for invalid parameters; 256 where the call leaves
+   its workspace untouched). */
 size_t gca_swa_sink_fwd_workspace_size(const gca_swa_sink_params_t* params);
 
 /*
@@ -375,7 +376,8 @@ gca_status_t gca_paged_append(const gca_paged_params_t* params, const void* k_ne
                               const void* v_new, const int32_t* cu_q, const int32_t* kv_len,
                               const int32_t* table, void* k_cache, void* v_cache, void* stream);
 
-/* Bytes of device workspace gca_paged_attn needs (0 for invalid parameters). */
+/* Bytes of device workspace gca_paged_attn needs (0 for invalid parameters; 256 where the call leaves
+   its workspace untouched). */
 size_t gca_paged_attn_workspace_size(const gca_paged_params_t* params);
 
 /*

@@ -268,9 +268,17 @@ def _swa_sink_args(q, k, v, window, sinks, attn_scale):
                           k.dtype, v.dtype, window, sinks, float(attn_scale))
 
 
+_UNTOUCHED = 256       # the size of a workspace that a call does not touch
+_untouched = {}
+
+
 def _workspace(given, need, dev):
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
+        if need != _UNTOUCHED:
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+        given = _untouched.get(dev)
+        if given is None:
+            given = _untouched[dev] = torch.empty(need, dtype=torch.uint8, device=dev)
     if given.dtype != torch.uint8 or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     return given

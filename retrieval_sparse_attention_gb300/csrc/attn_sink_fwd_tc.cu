@@ -203,9 +203,16 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     u.f1 = min(k.nsk + hi - k.k0, k.nt - 1);
     u.fl = lo <= k.k0 && k.k0 <= hi ? k.nt - 1 : -1;
     u.nar = k.nsk == 1 && s.ns <= kNarrow;
-    u.slot = u.j0 > 0 ? 2 * p.wid * a.R : (u.j1 < k.nt ? (2 * wid_tail + 1) * a.R : -1);
-    if (u.j0 > 0) a.head[p.wid] = u.j1 < k.nt ? 2 : 1;  // what the join reads
-    else if (u.j1 < k.nt) a.tail[wid_tail] = make_int4(p.b, p.mt, p.h, 1);
+    u.slot = -1;
+    if (!a.whole) {                                           // (left whole: there is no workspace to write to)
+        if (u.j0 > 0) {
+            u.slot = 2 * p.wid * a.R;
+            a.head[p.wid] = u.j1 < k.nt ? 2 : 1;              // what the join reads
+        } else if (u.j1 < k.nt) {
+            u.slot = (2 * wid_tail + 1) * a.R;
+            a.tail[wid_tail] = make_int4(p.b, p.mt, p.h, 1);
+        }
+    }
     p.left -= u.j1 - u.j0;
     p.j = 0;
     if (++p.mt == s.nMT && !PAGED) {
@@ -317,7 +324,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         };
         bool alternate = false;
         if (kl && lane == 0) {
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2 && !a.whole; ++i) {
                 a.head[sb.pos[i].wid] = 0;
                 a.tail[sb.pos[i].wid] = make_int4(0, 0, 0, 0);
             }
@@ -895,6 +902,25 @@ Layout layout(const SinkShape& s) {
     return w;
 }
 
+// Are the units left whole?
+bool whole_units(const SinkShape& s) {
+    int tm;
+    const int R = rows_of_tile(s, &tm);
+    // Cutting units costs a join and sums in the workspace, the time of some C tiles by the measurements;
+    // leaving them whole costs the difference between the longest share and the mean.  (312 units of 15
+    // tiles, 12 heads of 64: 28.4 us whole, 33.1 cut; 308 of 17, 16/4 heads of 128: 34.6 and 43.4; B =
+    // 8 x 16K, W = 512, 4 sinks: 0.339 and 0.348 ms; a token of 4 x 128 columns over 7 tiles: 16.7 and
+    // 11.3 us.)  Few tiles a unit only: ragged lengths make shares of whole units less even than this
+    // counts.
+    const long long span = (long long)s.W + tm - 1;
+    const long long keys = s.paged ? (long long)s.width * s.page : s.L;
+    const long long nt = span < keys ? (span + 126) / 128 + 1 + (s.ns + 127) / 128 : (keys + 127) / 128;
+    const long long pairs = (long long)s.B * ((s.max_q + tm - 1) / tm), packed = (long long)s.T / tm + s.B;
+    const long long units = s.Hkv * (s.paged && packed < pairs ? packed : pairs);
+    const long long C = (s.d == 64 ? 6 : 3) + R * s.d / 896;
+    return nt <= 2 * C + 2 && (units + kMaxWorkers - 1) / kMaxWorkers * nt * kMaxWorkers <= units * nt + C * kMaxWorkers;
+}
+
 template <int D, bool PAGED>
 cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                    const CUtensorMap& tv, cudaStream_t st, int* launches) {
@@ -927,7 +953,7 @@ cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& t
 
 }  // namespace
 
-size_t sink_fwd_workspace_bytes(const SinkShape& s) { return layout(s).total; }
+size_t sink_fwd_workspace_bytes(const SinkShape& s) { return whole_units(s) ? 256 : layout(s).total; }
 
 bool sink_fwd_supported(const SinkShape& s) {
     // the kernel counts key tiles and (sequence, query tile) pairs in 32 bits; quota * workers
@@ -962,19 +988,7 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     a.lse = lse;
     a.status = status;
     a.scale_log2 = s.scale * kLog2e;
-    // Cutting units costs a join and sums in the workspace, the time of some C tiles by the measurements;
-    // leaving them whole costs the difference between the longest share and the mean.  (312 units of 15
-    // tiles, 12 heads of 64: 28.4 us whole, 33.1 cut; 308 of 17, 16/4 heads of 128: 34.6 and 43.4; B =
-    // 8 x 16K, W = 512, 4 sinks: 0.339 and 0.348 ms; a token of 4 x 128 columns over 7 tiles: 16.7 and
-    // 11.3 us.)  Few tiles a unit only: ragged
-    // lengths make shares of whole units less even than this counts.
-    const long long span = (long long)s.W + a.s.TM - 1;
-    const long long keys = s.paged ? (long long)s.width * s.page : s.L;
-    const long long nt = span < keys ? (span + 126) / 128 + 1 + (s.ns + 127) / 128 : (keys + 127) / 128;
-    const long long pairs = (long long)s.B * a.s.nMT, packed = (long long)s.T / a.s.TM + s.B;
-    const long long units = s.Hkv * (s.paged && packed < pairs ? packed : pairs);
-    const long long C = (s.d == 64 ? 6 : 3) + a.R * s.d / 896;
-    a.whole = nt <= 2 * C + 2 && (units + kMaxWorkers - 1) / kMaxWorkers * nt * kMaxWorkers <= units * nt + C * kMaxWorkers;
+    a.whole = whole_units(s);
     CUtensorMap tq, tk, tv;
     const uint64_t kvcols = (uint64_t)s.Hkv * s.d;
     bool ok = encode_bf16_3d(&tq, q, s.d, s.H, s.T, s.d, s.q_stride, a.s.G, a.s.TM);

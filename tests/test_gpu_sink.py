@@ -141,6 +141,17 @@ def test_deterministic_and_fully_written():
     assert api.gca_get_status() == 0
 
 
+def test_a_workspace_of_256_bytes_stays_untouched():
+    q, k, v, _ = (x.cuda() for x in inputs(1, 900, 6, 2, 64, seed=15))
+    p = api.make_swa_sink_params(B=1, L=900, H=6, Hkv=2, d=64, window=200, sinks=4)
+    assert api.gca_swa_sink_fwd_workspace_size(p) == 256
+    want = api.swa_sink_fwd(q, k, v, window=200, sinks=4)
+    ws = torch.full((256,), 77, dtype=torch.uint8, device="cuda")
+    got = api.swa_sink_fwd(q, k, v, window=200, sinks=4, workspace=ws)
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and (ws == 77).all()
+    assert api.gca_last_launch_count() == 1
+
+
 def test_other_stream_and_graph():
     q, k, v, g = (x.cuda() for x in inputs(1, 700, 4, 2, 64, seed=8))
     want = api.swa_sink_fwd(q, k, v, window=200, sinks=4)
