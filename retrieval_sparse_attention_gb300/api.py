@@ -196,10 +196,17 @@ def _same_device(*ts):
     """The entries launch on the current device's stream: tensors of another device (or of
     none) would be read through a foreign address.  Returns the device index."""
     dev = ts[0].get_device()
-    if dev < 0 or dev != torch.cuda.current_device() or \
-            any([t is not None and t.get_device() != dev for t in ts]):
+    ok = dev >= 0 and dev == torch._C._cuda_getDevice()     # (current_device() without its setup)
+    for t in ts:
+        ok = ok and (t is None or t.get_device() == dev)
+    if not ok:
         raise ValueError("tensors must be CUDA tensors on the current device")
     return dev
+
+
+def _empty_like(t):
+    """A dense tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _dense(t, shape, dtype, what):
@@ -291,7 +298,7 @@ def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, works
     p, need, _ = _swa_sink_args(q, k, v, window, sinks, attn_scale)
     dev = q.device
     ws = _workspace(workspace, need, dev)
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    o = _empty_like(q)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if with_lse else None
     gca_swa_sink_fwd(p, q, k, v, o, lse, ws)
     return o, lse
@@ -306,9 +313,7 @@ def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, worksp
     _dense(lse, q.shape[:3], torch.float32, "lse")
     dev = q.device
     ws = _workspace(workspace, need, dev)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dq, dk, dv = _empty_like(q), _empty_like(k), _empty_like(v)
     gca_swa_sink_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, ws)
     return dq, dk, dv
 
@@ -400,7 +405,7 @@ def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, s
     dev = q.device
     ws = _workspace(workspace, need, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = _empty_like(q)
     else:
         _dense(out, q.shape, q.dtype, "out")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if with_lse else None
