@@ -70,7 +70,6 @@ __device__ __forceinline__ SeqInfo sink_seq(const SinkSched& a, int b, int* stat
 struct KeyTiles {
     int p0, p1;          // positions of its first and last token
     int k0, nsk, nt;
-    __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
 };
 __device__ __forceinline__ KeyTiles key_tiles(const SinkSched& a, const SeqInfo& s, int mt) {
     KeyTiles k;

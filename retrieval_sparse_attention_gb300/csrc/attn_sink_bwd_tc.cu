@@ -41,8 +41,8 @@
 // slots 49% and 51%; the math warps' latency a step and the issuing threads' share of
 // the slots pace them (pass B, a clock trace: a step every 1,165 cycles; a math pair's two
 // steps take 2 x 1,165 of which its arithmetic 1,310 and its waits and stores the rest; the
-// loading thread needs 900 a step, the accumulating products' issuer 780).  A sink's far steps cost as much as others (0.10 ms of pass B)
-// although 32 of their 128 key rows at most carry anything; taking them in pass A,
+// loading thread needs 900 a step, the accumulating products' issuer 780).  A sink's far
+// steps cost as much as others (0.10 ms of pass B) although 32 of their 128 key rows at most carry anything; taking them in pass A,
 // where sinks have narrow steps, would need its dK and dV sums joined across all CTAs.
 #include <math.h>
 
@@ -1227,11 +1227,12 @@ cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, co
     const uint64_t qs[3] = {d, (uint64_t)s.q_stride, (uint64_t)s.q_stride * L}, gs[3] = {d, H * d, H * d * L};
     const uint32_t boxa[3] = {(uint32_t)a.s.G, (uint32_t)a.s.TM, 1}, boxb[3] = {1, 64, 1};
     CUtensorMap m[8];
-    bool ok = encode_bf16_4d(&m[0], q, qn, qs, boxa) && encode_bf16_4d(&m[1], dout, qn, gs, boxa) &&
-              encode_bf16_4d(&m[4], q, qn, qs, boxb) && encode_bf16_4d(&m[5], dout, qn, gs, boxb);
+    const bool wide = s.d == 128;             // (d = 64: a head's row is 128 bytes, as in the forward; pass A -1%)
+    bool ok = encode_bf16_4d(&m[0], q, qn, qs, boxa, wide) && encode_bf16_4d(&m[1], dout, qn, gs, boxa, wide) &&
+              encode_bf16_4d(&m[4], q, qn, qs, boxb, wide) && encode_bf16_4d(&m[5], dout, qn, gs, boxb, wide);
     for (int i = 0; i < 2; ++i)
-        ok = ok && encode_bf16_3d(&m[2 + 4 * i], k, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1) &&
-             encode_bf16_3d(&m[3 + 4 * i], v, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1);
+        ok = ok && encode_bf16_3d(&m[2 + 4 * i], k, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1, wide) &&
+             encode_bf16_3d(&m[3 + 4 * i], v, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1, wide);
     if (!ok) return cudaErrorInvalidValue;
     return s.d == 64 ? launch<64>(s, a, m, st, launches) : launch<128>(s, a, m, st, launches);
 }

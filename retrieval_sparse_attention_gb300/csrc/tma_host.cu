@@ -82,7 +82,7 @@ bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1
 }
 
 bool encode_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&n)[4], const uint64_t (&stride)[3],
-                    const uint32_t (&box)[3]) {
+                    const uint32_t (&box)[3], bool wide) {
     std::call_once(g_once, resolve);
     if (!g_encode) return false;
     cuuint64_t dims[4] = {n[0], n[1], n[2], n[3]};
@@ -91,7 +91,7 @@ bool encode_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&n)[4], 
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                           strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_SWIZZLE_128B, wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

@@ -35,7 +35,7 @@ bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1
 
 // The same over four dimensions.
 bool encode_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&n)[4], const uint64_t (&stride)[3],
-                    const uint32_t (&box)[3]);
+                    const uint32_t (&box)[3], bool wide = true);
 
 // Tensor map over a row-major fp32 matrix [rows, row_elems] (row stride
 // row_elems * 4 bytes, a multiple of 16), box of box_cols x box_rows (box_cols
