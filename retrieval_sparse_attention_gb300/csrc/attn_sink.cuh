@@ -5,6 +5,8 @@
 
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -41,6 +43,14 @@ __device__ __forceinline__ SeqInfo paged_seq(const PagedArgs& a, int b, int* sta
         s = SeqInfo{0, 0, 0};
     }
     return s;
+}
+
+// Sum over i = 1 .. n of min(cap, step i + 1): the tiles of a row's n query tiles, of which the i-th
+// ends in tile step i at most and sees no more than cap.
+constexpr double kMaxSteps = 2.1e9;              // a stream's end plus one share (1/152 of it) stays below 2^31
+inline double causal_sum(double n, double step, double cap) {
+    const double m = std::min(n, std::max(0.0, std::floor((cap - 1) / step)));
+    return step * m * (m + 1) / 2 + m + (n - m) * cap;
 }
 
 // ---------------------------------------------------------------------------

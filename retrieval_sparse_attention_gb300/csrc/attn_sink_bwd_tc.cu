@@ -1166,12 +1166,16 @@ cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[
 }  // namespace
 
 bool sink_bwd_supported(const SinkShape& s) {
-    // key-major steps counted in 32 bits
+    // steps are counted in 32 bits: key-major ones
     const double nkt = (s.L + 127) / 128, nb = nkt * 2;
     const double win = (s.W + 127.0) / 64 + 2;
     const double sinks = (s.ns + 127) / 128;
     const double steps = nkt * (win < nb ? win : nb) + sinks * nb;
-    return (double)s.B * s.H * steps < 1.9e9 && (double)s.B * nkt * 4 < 2e9;
+    if ((double)s.B * s.H * steps >= 1.9e9 || (double)s.B * nkt * 4 >= 2e9) return false;
+    // query-major ones too: where 128 / G rounds down, a tile's rows are few and its steps up to twice as many
+    const int G = s.H / s.Hkv, tm = std::min(128 / G, s.L);
+    const double cap = ((double)s.W + tm + s.ns) / 64 + 3;
+    return (double)s.B * s.Hkv * causal_sum((s.L + tm - 1) / tm, tm / 64.0, cap) < kMaxSteps;
 }
 
 size_t sink_bwd_workspace_bytes(const SinkShape& s) { return layout(s).total; }
