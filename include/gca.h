@@ -279,6 +279,10 @@ gca_status_t gca_swa_bwd(const gca_swa_params_t* params, const void* q, const vo
  * with H / Hkv consecutive query heads sharing a key head (query head h reads
  * key head h / (H / Hkv)).  sinks = 0 is the plain window; window >= L is full
  * causal attention.
+ * Sizes: B * L * H below 2^31, and up to about 2.1e9 tiles of 128 (token, query
+ * head) rows x 128 keys that some of them see (full causal attention over 1M
+ * tokens with 16 query heads has 0.54e9), for the gradients about half as many;
+ * larger calls return GCA_ERR_UNSUPPORTED.
  */
 typedef struct {
     int B, L;             /* rows, tokens per row (any L >= 1)                              */

@@ -314,7 +314,7 @@ gca_status_t sink_common(int H, int Hkv, int d, gca_dtype_t dtype, float attn_sc
     return GCA_OK;
 }
 
-gca_status_t swa_sink_check(const gca_swa_sink_params_t* p, SinkShape* out) {
+gca_status_t swa_sink_check(const gca_swa_sink_params_t* p, bool (*supported)(const SinkShape&), SinkShape* out) {
     if (!p) return GCA_ERR_INVALID_ARG;
     SinkShape s{};
     if (p->B < 1 || p->L < 1 || p->window < 1 || p->sinks < 0) return GCA_ERR_INVALID_ARG;
@@ -326,7 +326,7 @@ gca_status_t swa_sink_check(const gca_swa_sink_params_t* p, SinkShape* out) {
     // a window that covers the row hides nothing, and then sinks add nothing
     s.W = p->window < p->L ? p->window : p->L;
     s.ns = s.W < p->L ? (p->sinks < p->L ? p->sinks : p->L) : 0;
-    if (!sink_fwd_supported(s) || !sink_bwd_supported(s)) return GCA_ERR_UNSUPPORTED;
+    if (!supported(s)) return GCA_ERR_UNSUPPORTED;
     *out = s;
     return GCA_OK;
 }
@@ -358,7 +358,7 @@ gca_status_t paged_check(const gca_paged_params_t* p, SinkShape* out) {
 
 size_t gca_swa_sink_fwd_workspace_size(const gca_swa_sink_params_t* params) {
     SinkShape s;
-    if (swa_sink_check(params, &s) != GCA_OK) return 0;
+    if (swa_sink_check(params, sink_fwd_supported, &s) != GCA_OK) return 0;
     return sink_fwd_workspace_bytes(s);
 }
 
@@ -366,7 +366,7 @@ gca_status_t gca_swa_sink_fwd(const gca_swa_sink_params_t* params, const void* q
                               const void* v, void* o, float* lse, void* workspace, size_t ws_bytes,
                               void* stream) {
     SinkShape s;
-    gca_status_t r = swa_sink_check(params, &s);
+    gca_status_t r = swa_sink_check(params, sink_fwd_supported, &s);
     if (r != GCA_OK) return r;
     if ((r = check_ptrs({q, k, v, o})) != GCA_OK) return r;
     if (lse && !aligned16(lse)) return GCA_ERR_INVALID_ARG;
@@ -382,7 +382,7 @@ gca_status_t gca_swa_sink_fwd(const gca_swa_sink_params_t* params, const void* q
 
 size_t gca_swa_sink_bwd_workspace_size(const gca_swa_sink_params_t* params) {
     SinkShape s;
-    if (swa_sink_check(params, &s) != GCA_OK) return 0;
+    if (swa_sink_check(params, sink_bwd_supported, &s) != GCA_OK) return 0;
     return sink_bwd_workspace_bytes(s);
 }
 
@@ -391,7 +391,7 @@ gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q
                               void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes,
                               void* stream) {
     SinkShape s;
-    gca_status_t r = swa_sink_check(params, &s);
+    gca_status_t r = swa_sink_check(params, sink_bwd_supported, &s);
     if (r != GCA_OK) return r;
     if ((r = check_ptrs({q, k, v, o, lse, dout, dq, dk, dv})) != GCA_OK) return r;
     if ((r = check_workspace(workspace, ws_bytes, sink_bwd_workspace_bytes(s))) != GCA_OK) return r;

@@ -1166,16 +1166,14 @@ cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[
 }  // namespace
 
 bool sink_bwd_supported(const SinkShape& s) {
-    // steps are counted in 32 bits: key-major ones
-    const double nkt = (s.L + 127) / 128, nb = nkt * 2;
-    const double win = (s.W + 127.0) / 64 + 2;
-    const double sinks = (s.ns + 127) / 128;
-    const double steps = nkt * (win < nb ? win : nb) + sinks * nb;
-    if ((double)s.B * s.H * steps >= 1.9e9 || (double)s.B * nkt * 4 >= 2e9) return false;
-    // query-major ones too: where 128 / G rounds down, a tile's rows are few and its steps up to twice as many
-    const int G = s.H / s.Hkv, tm = std::min(128 / G, s.L);
-    const double cap = ((double)s.W + tm + s.ns) / 64 + 3;
-    return (double)s.B * s.Hkv * causal_sum((s.L + tm - 1) / tm, tm / 64.0, cap) < kMaxSteps;
+    // steps are counted in 32 bits.  Key-major ones, a query head: tile kt has the blocks from 2 kt on
+    // that its window reaches, with sinks all to the row's end
+    const double nkt = (s.L + 127) / 128, nb = (s.L + 63) / 64, nst = (s.ns + 127) / 128;
+    const double kv = nst * nb - nst * (nst - 1) + causal_sum(nkt - nst, 2, (s.W + 126.0) / 64 + 1);
+    // query-major ones, a key head: where 128 / G rounds down, a tile's rows are few and its steps more
+    const int tm = std::min(128 / (s.H / s.Hkv), s.L);
+    const double q = causal_sum((s.L + tm - 1) / tm, tm / 64.0, ((double)s.W + tm + s.ns) / 64 + 3);
+    return s.B * s.H * kv < kMaxSteps && s.B * s.Hkv * q < kMaxSteps && s.B * nkt * 4 < 2e9;
 }
 
 size_t sink_bwd_workspace_bytes(const SinkShape& s) { return layout(s).total; }

@@ -961,11 +961,11 @@ bool sink_fwd_supported(const SinkShape& s) {
     int tm;
     rows_of_tile(s, &tm);
     const double nmt = (s.max_q + tm - 1) / tm;
-    const double keys = s.paged ? (double)s.width * s.page : s.L;
     const double vis = (double)s.W + tm + s.ns;
-    const double tiles = (vis < keys ? vis : keys) / 128 + 3;
-    const double units = s.paged ? (double)s.T / tm + s.B : (double)s.B * nmt;
-    return s.B * nmt < 1e9 && units * s.Hkv * tiles < 1.9e9;
+    if (s.B * nmt >= 1e9) return false;
+    if (!s.paged) return s.B * s.Hkv * causal_sum(nmt, tm / 128.0, vis / 128 + 3) < kMaxSteps;
+    const double keys = (double)s.width * s.page, units = (double)s.T / tm + s.B;
+    return units * s.Hkv * (std::min(vis, keys) / 128 + 3) < kMaxSteps;
 }
 
 cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, const void* v,

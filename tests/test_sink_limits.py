@@ -59,3 +59,60 @@ def test_steps_of_supported_gradients_fit_32_bits():
             n = streams(B, L, H, Hkv, 64, window, sinks)
             assert n + n // 152 + 200 < 2 ** 31, (B, L, H, Hkv, window, sinks)      # a share past the end
     assert 0 < refused < 60
+
+
+def key_major_steps(B, L, H, window, sinks):
+    """64-query blocks of each (row, query head, 128-key tile)."""
+    W = min(window, L)
+    ns = min(sinks, L) if W < L else 0
+    last = (L - 1) >> 6
+    return B * H * sum((last if s0 < ns else min(L - 1, s0 + 127 + W - 1) >> 6) - s0 // 64 + 1 for s0 in range(0, L, 128))
+
+
+def forward_tiles(B, L, H, Hkv, window, sinks):
+    W = min(window, L)
+    ns = min(sinks, L) if W < L else 0
+    TM = min(128 * Hkv // H, L)
+    total = 0
+    for p0 in range(0, L, TM):
+        k0 = max(0, p0 - W + 1) >> 7
+        total += min((ns + 127) >> 7, k0) + ((min(L, p0 + TM) - 1) >> 7) - k0 + 1
+    return B * Hkv * total
+
+
+def test_the_forward_has_limits_of_its_own(lib):
+    # full causal attention over 1M tokens: 0.54e9 key tiles and 1.07e9 gradient steps, and its double
+    for H, Hkv, bwd in ((16, 4, True), (32, 8, False)):
+        p = api.make_swa_sink_params(B=1, L=2 ** 20, H=H, Hkv=Hkv, d=128, window=2 ** 20)
+        assert api.gca_swa_sink_fwd_workspace_size(p) > 0
+        assert (api.gca_swa_sink_bwd_workspace_size(p) > 0) == bwd
+        # (a workspace that is missing is what stops the call)
+        assert lib.gca_swa_sink_fwd(ctypes.byref(p), *[FAKE] * 5, None, 0, None) == WORKSPACE
+        got = lib.gca_swa_sink_bwd(ctypes.byref(p), *[FAKE] * 9, None, 0, None)
+        assert got == (WORKSPACE if bwd else UNSUPPORTED)
+
+
+def test_limits_follow_the_counts():
+    # what is taken fits 32 bits with a share past the end; what is refused is not far below
+    rng = random.Random(4)
+    seen = set()
+    for _ in range(150):
+        Hkv = rng.choice([1, 2, 4, 8])
+        H = Hkv * rng.choice([1, 2, 3, 7, 12, 16, 48, 70, 128])
+        L = rng.randrange(20000, 400000)
+        B = int(2 ** rng.uniform(0, 10))
+        while B * L * H >= 2 ** 31 and B > 1:
+            B //= 2
+        if B * L * H >= 2 ** 31:
+            continue
+        window, sinks = rng.choice([rng.randrange(1, L), L, 3000]), rng.choice([0, 4, 500, L // 2, L])
+        p = api.make_swa_sink_params(B=B, L=L, H=H, Hkv=Hkv, d=64, window=window, sinks=sinks)
+        fwd = forward_tiles(B, L, H, Hkv, window, sinks)
+        bwd = max(key_major_steps(B, L, H, window, sinks), streams(B, L, H, Hkv, 64, window, sinks))
+        for n, size in ((fwd, api.gca_swa_sink_fwd_workspace_size(p)), (bwd, api.gca_swa_sink_bwd_workspace_size(p))):
+            if size:
+                assert n + n // 152 + 400 < 2 ** 31, (B, L, H, Hkv, window, sinks)
+            else:
+                assert n > 1.8e9, (B, L, H, Hkv, window, sinks)
+            seen.add((n == fwd, size > 0))
+    assert len(seen) == 4
