@@ -354,7 +354,7 @@ typedef struct {
     int B;                /* sequences, >= 1                                                */
     int total_q;          /* rows of the token tensors, >= 0 (0: nothing is enqueued)       */
     int max_q;            /* at least the new tokens of any one sequence; 0 => total_q      */
-    int H, Hkv, d;        /* as in gca_swa_sink_params_t (H is not used by the append)      */
+    int H, Hkv, d;        /* as in gca_swa_sink_params_t                                    */
     int page;             /* tokens per page: 16, 32, 64 or 128                             */
     int n_pages;          /* pages in the cache                                             */
     int table_width;      /* table entries per sequence                                     */
@@ -367,7 +367,8 @@ typedef struct {
 } gca_paged_params_t;
 
 /*
- * gca_paged_append -- write new tokens into the cache.
+ * gca_paged_append -- write new tokens into the cache.  Takes the attention's
+ *   parameters, of which H may be 0.
  *   k_new, v_new [total_q, Hkv, d]; token i of sequence b goes to its position
  *   kv_len[b] - (cu_q[b+1] - cu_q[b]) + i.  Tokens at negative positions and
  *   tokens whose page is not in [0, n_pages) are not written (the latter records

@@ -331,26 +331,31 @@ gca_status_t swa_sink_check(const gca_swa_sink_params_t* p, bool (*supported)(co
     return GCA_OK;
 }
 
-gca_status_t paged_check(const gca_paged_params_t* p, SinkShape* out) {
+// attend: for gca_paged_attn; the append takes H = 0 and is bound by none of the attention's counts
+gca_status_t paged_check(const gca_paged_params_t* p, bool attend, SinkShape* out) {
     if (!p) return GCA_ERR_INVALID_ARG;
     SinkShape s{};
     if (p->B < 1 || p->total_q < 0 || p->max_q < 0 || p->n_pages < 1 || p->table_width < 1 || p->page < 1 ||
         p->window < 0 || p->sinks < 0)
         return GCA_ERR_INVALID_ARG;
-    gca_status_t r = sink_common(p->H, p->Hkv, p->d, p->dtype, p->attn_scale, p->q_stride, p->kv_stride, &s);
+    const int H = !attend && p->H == 0 ? p->Hkv : p->H;
+    gca_status_t r = sink_common(H, p->Hkv, p->d, p->dtype, p->attn_scale, p->q_stride, p->kv_stride, &s);
     if (r != GCA_OK) return r;
     if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return GCA_ERR_UNSUPPORTED;
-    if ((long long)p->total_q * p->H >= (1ll << 31) || (long long)p->table_width * p->page > kNoWindow / 2 ||
-        (long long)p->B * p->table_width >= (1ll << 31) || p->B > 65535)
+    if ((long long)p->table_width * p->page > kNoWindow / 2 || (long long)p->B * p->table_width >= (1ll << 31) ||
+        p->B > 65535)
         return GCA_ERR_UNSUPPORTED;
     s.B = p->B; s.T = p->total_q;
     s.max_q = p->max_q > 0 && p->max_q < p->total_q ? p->max_q : p->total_q;
     s.page = p->page; s.n_pages = p->n_pages; s.width = p->table_width;
-    const int cap = p->table_width * p->page;
-    s.W = p->window > 0 && p->window < cap ? p->window : kNoWindow;
-    s.ns = s.W == kNoWindow ? 0 : (p->sinks < cap ? p->sinks : cap);
     s.paged = 1;
-    if (s.T > 0 && !sink_fwd_supported(s)) return GCA_ERR_UNSUPPORTED;
+    if (attend) {
+        if ((long long)p->total_q * p->H >= (1ll << 31)) return GCA_ERR_UNSUPPORTED;
+        const int cap = p->table_width * p->page;
+        s.W = p->window > 0 && p->window < cap ? p->window : kNoWindow;
+        s.ns = s.W == kNoWindow ? 0 : (p->sinks < cap ? p->sinks : cap);
+        if (s.T > 0 && !sink_fwd_supported(s)) return GCA_ERR_UNSUPPORTED;
+    }
     *out = s;
     return GCA_OK;
 }
@@ -408,7 +413,7 @@ gca_status_t gca_paged_append(const gca_paged_params_t* params, const void* k_ne
                               const void* v_new, const int32_t* cu_q, const int32_t* kv_len,
                               const int32_t* table, void* k_cache, void* v_cache, void* stream) {
     SinkShape s;
-    gca_status_t r = paged_check(params, &s);
+    gca_status_t r = paged_check(params, false, &s);
     if (r != GCA_OK) return r;
     if (s.T == 0) {
         t_launches = 0;
@@ -426,7 +431,7 @@ gca_status_t gca_paged_append(const gca_paged_params_t* params, const void* k_ne
 
 size_t gca_paged_attn_workspace_size(const gca_paged_params_t* params) {
     SinkShape s;
-    if (paged_check(params, &s) != GCA_OK || s.T == 0) return 0;
+    if (paged_check(params, true, &s) != GCA_OK || s.T == 0) return 0;
     return sink_fwd_workspace_bytes(s);
 }
 
@@ -435,7 +440,7 @@ gca_status_t gca_paged_attn(const gca_paged_params_t* params, const void* q, con
                             const int32_t* table, void* o, float* lse, void* workspace,
                             size_t ws_bytes, void* stream) {
     SinkShape s;
-    gca_status_t r = paged_check(params, &s);
+    gca_status_t r = paged_check(params, true, &s);
     if (r != GCA_OK) return r;
     if (s.T == 0) {
         t_launches = 0;

@@ -116,3 +116,27 @@ def test_limits_follow_the_counts():
                 assert n > 1.8e9, (B, L, H, Hkv, window, sinks)
             seen.add((n == fwd, size > 0))
     assert len(seen) == 4
+
+
+def paged(**kw):
+    base = dict(B=4, total_q=0, max_q=0, H=0, Hkv=2, d=64, page=16, n_pages=10, table_width=3, window=0, sinks=0,
+                dtype=0, attn_scale=0.0, q_stride=0, kv_stride=0)
+    base.update(kw)
+    return _lib.GcaPagedParams(**base)
+
+
+def test_the_append_needs_no_query_heads(lib):
+    p = paged()
+    # nothing to write: only the parameters are checked
+    assert lib.gca_paged_append(ctypes.byref(p), *[None] * 7, None) == 0
+    assert lib.gca_paged_attn(ctypes.byref(p), *[None] * 9, 0, None) == 1
+
+
+def test_the_append_has_no_limit_of_tiles(lib):
+    # 2^30 new tokens over 2^29 cached ones are too many key tiles to attend over, not too many rows
+    p = paged(B=3, total_q=2 ** 30, H=2, Hkv=2, n_pages=2 ** 27, table_width=2 ** 25)
+    assert lib.gca_paged_attn(ctypes.byref(p), *[None] * 9, 0, None) == UNSUPPORTED
+    # (tensors that are missing are what stops the call)
+    assert lib.gca_paged_append(ctypes.byref(p), *[None] * 7, None) == 1
+    assert lib.gca_paged_append(ctypes.byref(paged(page=24)), *[None] * 7, None) == UNSUPPORTED
+    assert lib.gca_paged_append(ctypes.byref(paged(Hkv=0)), *[None] * 7, None) == 1
