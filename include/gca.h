@@ -309,7 +309,8 @@ size_t gca_swa_sink_fwd_workspace_size(const gca_swa_sink_params_t* params);
  *   needed later by gca_swa_sink_bwd.  fp32 accumulation, bf16 output.
  *   workspace: >= gca_swa_sink_fwd_workspace_size() bytes, 256-byte aligned,
  *   contents need not be initialised; calls that may overlap need their own.
- *   K and V must be finite wherever some token of the row sees them.
+ *   K and V must be finite wherever some token of the row sees them.  A token
+ *   whose q is not finite gets NaN, in o and lse, and leaves the others alone.
  */
 gca_status_t gca_swa_sink_fwd(const gca_swa_sink_params_t* params, const void* q, const void* k,
                               const void* v, void* o, float* lse, void* workspace, size_t ws_bytes,
@@ -391,7 +392,8 @@ size_t gca_paged_attn_workspace_size(const gca_paged_params_t* params);
  * formula at the tokens' positions.
  *   q [total_q, H, d] -> o [total_q, H, d] dense; lse [total_q, H] fp32 or NULL.
  *   A token at a negative position (kv_len below the number of new tokens)
- *   sees nothing: its output is 0 and its lse -inf.
+ *   sees nothing: its output is 0 and its lse -inf.  A token that sees keys and
+ *   whose q is not finite gets NaN in both.
  *   Only pages that hold a visible token are looked up, so the table entries of
  *   pages that left the window may be anything.  Such a page outside
  *   [0, n_pages) reads as zeros and records GCA_ERR_DEVICE_INDEX.  Cache rows that

@@ -615,7 +615,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 if (!wwait(&sb.o_full[wg], full_par(ko))) break;
                 tc_fence_after();
                 const bool wr = pend_row >= 0;
-                const float inv = pl > 0.f ? 1.f / pl : 0.f;
+                const float inv = pl == 0.f ? 0.f : 1.f / pl;
                 if (__any_sync(0xffffffffu, wr)) {
                     if (pend_slot < 0) {
 #pragma unroll 1
@@ -640,7 +640,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         }
                     }
                     if (wr && pend_slot >= 0) a.part_ml[pend_slot + row] = make_float2(pm, pl);
-                    if (wr && pend_slot < 0 && a.lse) a.lse[pend_row] = pl > 0.f ? (pm + log2f(pl)) * kLn2 : -INFINITY;
+                    if (wr && pend_slot < 0 && a.lse) a.lse[pend_row] = pl == 0.f ? -INFINITY : (pm + log2f(pl)) * kLn2;
                 }
                 tc_fence_before();
                 mbar_arrive(&sb.o_empty[wg]);
@@ -815,7 +815,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sb.part_empty[wg][(np - 1) % kParts]);
                 pm = m;
-                pl = l;
+                // (a row that sees keys has a sum above 0, or scores that are no numbers or all -inf: NaN then)
+                pl = l == 0.f && w.slot < 0 && w.p0 + rt >= 0 ? NAN : l;
                 m = -INFINITY;
                 l = 0.f;
             }
@@ -872,11 +873,12 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const FwdArgs a, int wor
         acc.w = fmaf(o.w, f, acc.w);
         l = fmaf(ml.y, f, l);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (l == 0.f && s.pos0 + t >= 0) l = NAN;           // as in the forward
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const long long orow = (long long)(s.row0 + t) * sc.H + u.z * sc.G + (row - rt * sc.G);
     reinterpret_cast<uint2*>(a.o + orow * D)[c] =
         make_uint2(tcx::pack_bf16(acc.x * inv, acc.y * inv), tcx::pack_bf16(acc.z * inv, acc.w * inv));
-    if (c == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (c == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 int rows_of_tile(const SinkShape& s, int* tm) {
