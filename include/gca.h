@@ -349,7 +349,10 @@ gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q
  *   read on the device only, so a captured call follows their contents.
  * A sequence whose entries contradict each other (cu_q decreasing or beyond
  * total_q, more than max_q new tokens, kv_len below 0 or beyond
- * table_width * page) is left out and GCA_ERR_DEVICE_INDEX recorded.
+ * table_width * page) is left out and GCA_ERR_DEVICE_INDEX recorded.  Behind a
+ * sequence whose cu_q decreases others could claim its predecessors' rows:
+ * gca_paged_attn leaves them all out, gca_paged_append writes a row that is
+ * claimed twice for one of the two.
  */
 typedef struct {
     int B;                /* sequences, >= 1                                                */

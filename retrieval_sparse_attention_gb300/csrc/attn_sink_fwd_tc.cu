@@ -234,6 +234,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     static_assert(C::SMEM + sizeof(Bars<C::STAGES>) <= kSmemMax, "shared memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const SinkSched& sc = a.s;
+    const int down = PAGED ? first_decrease<kThreads>(sc.p, sc.B) : 0;
 
     if (warp == 0) {                                      // a barrier a lane
         if (lane < 2 * kParts) {
@@ -274,7 +275,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     pdl_release();
     if (PAGED)
-        find_shares<kThreads, 2>(sc.B, sc.nMT, sc.Hkv, a.whole, sb.wsum, sb.found, sb.pos,
+        find_shares<kThreads, 2>(ascending_seqs(down, sc.B, sb.wsum, a.status), sc.nMT, sc.Hkv, a.whole, sb.wsum,
+                                 sb.found, sb.pos,
                                  [&](int b) { return sink_seq<PAGED>(sc, b, a.status); },
                                  [&](const SeqInfo& q, int mt) { return key_tiles(sc, q, mt).nt; });
     else

@@ -5,6 +5,8 @@ import torch
 
 from retrieval_sparse_attention_gb300 import api
 
+import sink_reference as ref
+
 pytestmark = pytest.mark.gpu
 
 BAD_INDEX = 6
@@ -73,3 +75,70 @@ def test_queries_over_the_cache_that_are_not_finite(n, kv):
                 assert torch.isnan(ob[t, h]).all() and torch.isnan(lseb[t, h])
     if kv < n:
         assert torch.isneginf(lseb[:n - kv]).all() and (ob[:n - kv] == 0).all()
+
+
+def served(cu, T):
+    """The sequences that a cu_q leaves in: those before the first whose entries decrease."""
+    down = [b for b in range(len(cu) - 1) if cu[b + 1] < cu[b]]
+    return [b for b in range(down[0]) if 0 <= cu[b] and cu[b + 1] <= T]
+
+
+def random_cu(g, B, T):
+    cu = torch.randint(0, T + 1, (B + 1,), generator=g).sort().values
+    for i in torch.randint(0, B + 1, (max(1, B // 20),), generator=g).tolist():
+        cu[i] = int(torch.randint(-2, T + 5, (1,), generator=g))
+    return cu.tolist()
+
+
+G = torch.Generator().manual_seed(77)
+DOWN = [([0, 5, 3], 5), ([5, 3, 4], 5), ([0, 2, 1, 9], 9), ([0, 5, 3, 3, 8], 8), ([0, 5, 3, 8, 8, 9, 12], 12), ([0, 100, 2, 9, 9], 9), ([4, 2, 2, 6], 6),
+        ([0, 300, 0, 300, 0, 300, 300], 300), ([0, 150] * 40 + [150, 170], 170), ([0, 1] * 250 + [1, 2], 2),
+        (list(range(600)) + [100, 900], 900), (list(range(0, 500, 2)) + [499, 499, 498, 500], 500),
+        (random_cu(G, 50, 200), 200), (random_cu(G, 700, 900), 900), (random_cu(G, 33, 40), 40)]
+
+
+@pytest.mark.parametrize("cu,T", DOWN)
+@pytest.mark.parametrize("window", [0, 20])
+def test_sequences_behind_a_decreasing_entry_are_left_out(cu, T, window):
+    # they could claim rows of earlier ones
+    B, page, H, Hkv, d = len(cu) - 1, 16, 2, 1, 64
+    g = torch.Generator().manual_seed(B)
+    kv = torch.randint(0, 50, (B,), generator=g).tolist()
+    table = torch.randperm(4 * B, generator=g).view(B, 4)
+    kc, vc = (torch.randn(4 * B, page, Hkv, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(T, H, d, generator=g).to(torch.bfloat16)
+    out = torch.full((T, H, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    args = (kc.cuda(), vc.cuda(), table.to(torch.int32).cuda(), ints(*cu), ints(*kv))
+    o, _ = api.paged_attn(q.cuda(), *args, window=window, sinks=3, out=out)
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == BAD_INDEX
+    left = torch.ones(T, dtype=torch.bool)
+    for b in served(cu, T):
+        n, rows = cu[b + 1] - cu[b], slice(cu[b], cu[b + 1])
+        left[rows] = False
+        k, v = (x[table[b]].flatten(0, 1)[:kv[b]] for x in (kc, vc))
+        pos = torch.arange(kv[b] - n, kv[b])
+        blind = min(n, max(0, n - kv[b]))            # tokens before the first position see nothing
+        assert (o[rows][:blind] == 0).all()
+        if blind < n:
+            ro, _, bo, _ = ref.rows(q[rows][blind:], k, v, pos[blind:], torch.arange(kv[b]), window, 3)
+            ref.within("o of sequence %d" % b, o[rows][blind:], ro, bo)
+    assert (o[left.cuda()] == 3.0).all()
+    # the append: a row of the cache is as it was, or one of those that its sequence claims for this place
+    claims = {}
+    for b in range(B):
+        if 0 <= cu[b] <= cu[b + 1] <= T:
+            for i in range(cu[b], cu[b + 1]):
+                p = kv[b] - cu[b + 1] + i
+                claims.setdefault(i, []).append((int(table[b, p // page]), p % page) if p >= 0 else None)
+    kn = torch.randn(T, Hkv, d, generator=g).to(torch.bfloat16)
+    api.paged_append(kn.cuda(), kn.cuda(), *args)
+    torch.cuda.synchronize()
+    assert api.gca_get_status() == BAD_INDEX
+    got, want = args[0].cpu(), kc.clone()
+    for i, places in claims.items():
+        hit = [x for x in places if x and torch.equal(got[x], kn[i])]
+        assert len(hit) == 1 or (not hit and None in places)
+        for x in hit:
+            want[x] = kn[i]
+    assert torch.equal(got, want)
