@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -225,11 +226,23 @@ def _raw_stream(stream, dev):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _params(cls, **fields):
+    """The C struct; its integers have 32 bits, of which ctypes would keep a larger one's lowest.
+    (A call's window, sinks or max_q beyond that are all tokens, as the largest that fits.)"""
+    for name, x in fields.items():
+        if name != "attn_scale" and not -_INT_MAX <= operator.index(x) <= _INT_MAX:
+            raise ValueError("%s does not fit 32 bits: %d" % (name, x))
+    return cls(**fields)
+
+
 def make_swa_sink_params(*, B, L, H, d, window, Hkv=None, sinks=0, dtype=torch.bfloat16,
                          attn_scale=0.0, q_stride=0, kv_stride=0) -> GcaSwaSinkParams:
-    return GcaSwaSinkParams(B=B, L=L, H=H, Hkv=H if Hkv is None else Hkv, d=d, window=window,
-                            sinks=sinks, dtype=dtype_code(dtype), attn_scale=attn_scale,
-                            q_stride=q_stride, kv_stride=kv_stride)
+    return _params(GcaSwaSinkParams, B=B, L=L, H=H, Hkv=H if Hkv is None else Hkv, d=d, window=window,
+                   sinks=sinks, dtype=dtype_code(dtype), attn_scale=attn_scale, q_stride=q_stride,
+                   kv_stride=kv_stride)
 
 
 def gca_swa_sink_fwd_workspace_size(params: GcaSwaSinkParams) -> int:
@@ -265,12 +278,16 @@ def _swa_sink_plan(qs, qst, ks, kst, vs, vst, qt, kt, vt, window, sinks, attn_sc
     if step != _token_stride(vs, vst):
         raise ValueError("k and v must have one token stride")
     B, L, H, d = qs
-    p = make_swa_sink_params(B=B, L=L, H=H, Hkv=ks[2], d=d, window=window, sinks=sinks, dtype=qt,
-                             attn_scale=attn_scale, q_stride=_token_stride(qs, qst), kv_stride=step)
+    p = make_swa_sink_params(B=B, L=L, H=H, Hkv=ks[2], d=d, window=min(window, _INT_MAX),
+                             sinks=min(sinks, _INT_MAX), dtype=qt, attn_scale=attn_scale,
+                             q_stride=_token_stride(qs, qst), kv_stride=step)
     return p, gca_swa_sink_fwd_workspace_size(p), gca_swa_sink_bwd_workspace_size(p)
 
 
 def _swa_sink_args(q, k, v, window, sinks, attn_scale):
+    # (a plan is kept by these numbers' values, never by a tensor's identity, and 30.0 is not 30)
+    if type(window) is not int or type(sinks) is not int:
+        window, sinks = operator.index(window), operator.index(sinks)
     return _swa_sink_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), q.dtype,
                           k.dtype, v.dtype, window, sinks, float(attn_scale))
 
@@ -321,10 +338,10 @@ def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, worksp
 def make_paged_params(*, B, total_q, Hkv, d, page, n_pages, table_width, H=None, max_q=0, window=0,
                       sinks=0, dtype=torch.bfloat16, attn_scale=0.0, q_stride=0,
                       kv_stride=0) -> GcaPagedParams:
-    return GcaPagedParams(B=B, total_q=total_q, max_q=max_q, H=Hkv if H is None else H, Hkv=Hkv,
-                          d=d, page=page, n_pages=n_pages, table_width=table_width, window=window,
-                          sinks=sinks, dtype=dtype_code(dtype), attn_scale=attn_scale,
-                          q_stride=q_stride, kv_stride=kv_stride)
+    return _params(GcaPagedParams, B=B, total_q=total_q, max_q=max_q, H=Hkv if H is None else H,
+                   Hkv=Hkv, d=d, page=page, n_pages=n_pages, table_width=table_width, window=window,
+                   sinks=sinks, dtype=dtype_code(dtype), attn_scale=attn_scale, q_stride=q_stride,
+                   kv_stride=kv_stride)
 
 
 def gca_paged_append(params: GcaPagedParams, k_new, v_new, cu_q, kv_len, table, k_cache, v_cache,
@@ -362,14 +379,17 @@ def _paged_plan(ts, tst, cache, v_cache, table, cu_q, kv_len, dt, k_dt, v_dt, at
     if len(ts) != 3 or ts[2] != d or (not attend and ts[1] != Hkv):
         raise ValueError("token tensors must be [T, heads, d] like the cache")
     step = _token_stride(ts, tst)
-    p = make_paged_params(B=B, total_q=ts[0], max_q=max_q, H=ts[1], Hkv=Hkv, d=d, page=page,
-                          n_pages=n_pages, table_width=width, window=window, sinks=sinks, dtype=dt,
+    p = make_paged_params(B=B, total_q=ts[0], max_q=min(max_q, _INT_MAX), H=ts[1], Hkv=Hkv, d=d,
+                          page=page, n_pages=n_pages, table_width=width,
+                          window=min(window, _INT_MAX), sinks=min(sinks, _INT_MAX), dtype=dt,
                           attn_scale=attn_scale, q_stride=step if attend else 0,
                           kv_stride=0 if attend else step)
     return p, gca_paged_attn_workspace_size(p) if attend else 0
 
 
 def _paged_args(tok, k_cache, v_cache, table, cu_q, kv_len, attend, max_q, window=0, sinks=0, attn_scale=0.0):
+    if type(max_q) is not int or type(window) is not int or type(sinks) is not int:
+        max_q, window, sinks = operator.index(max_q), operator.index(window), operator.index(sinks)
     i32 = torch.int32
     if table.dtype != i32 or cu_q.dtype != i32 or kv_len.dtype != i32:
         raise TypeError("table, cu_q and kv_len must be int32")
@@ -377,8 +397,8 @@ def _paged_args(tok, k_cache, v_cache, table, cu_q, kv_len, attend, max_q, windo
             cu_q.is_contiguous() and kv_len.is_contiguous()):
         raise ValueError("the caches, table, cu_q and kv_len must be contiguous")
     return _paged_plan(tok.shape, tok.stride(), k_cache.shape, v_cache.shape, table.shape, cu_q.shape,
-                       kv_len.shape, tok.dtype, k_cache.dtype, v_cache.dtype, attend, max_q, window, sinks,
-                       attn_scale)
+                       kv_len.shape, tok.dtype, k_cache.dtype, v_cache.dtype, attend, max_q, window,
+                       sinks, float(attn_scale))
 
 
 def paged_append(k_new, v_new, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0):
