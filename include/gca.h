@@ -353,6 +353,11 @@ gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q
  * sequence whose cu_q decreases others could claim its predecessors' rows:
  * gca_paged_attn leaves them all out, gca_paged_append writes a row that is
  * claimed twice for one of the two.
+ * Sizes: B up to 65535, B * table_width below 2^31, table_width * page up to 2^29;
+ * for gca_paged_attn total_q * H below 2^31, max_q (total_q where it is 0) up to
+ * 2^30, and the key tiles of gca_swa_sink_params_t's limit, each sequence counted
+ * at the table's whole width or its window.  Larger calls return
+ * GCA_ERR_UNSUPPORTED.
  */
 typedef struct {
     int B;                /* sequences, >= 1                                                */

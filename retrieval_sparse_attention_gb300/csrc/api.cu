@@ -350,7 +350,8 @@ gca_status_t paged_check(const gca_paged_params_t* p, bool attend, SinkShape* ou
     s.page = p->page; s.n_pages = p->n_pages; s.width = p->table_width;
     s.paged = 1;
     if (attend) {
-        if ((long long)p->total_q * p->H >= (1ll << 31)) return GCA_ERR_UNSUPPORTED;
+        // (positions from -max_q on, less a window of kNoWindow, have to fit 32 bits)
+        if ((long long)p->total_q * p->H >= (1ll << 31) || s.max_q > kNoWindow) return GCA_ERR_UNSUPPORTED;
         const int cap = p->table_width * p->page;
         s.W = p->window > 0 && p->window < cap ? p->window : kNoWindow;
         s.ns = s.W == kNoWindow ? 0 : (p->sinks < cap ? p->sinks : cap);

@@ -140,3 +140,12 @@ def test_the_append_has_no_limit_of_tiles(lib):
     assert lib.gca_paged_append(ctypes.byref(p), *[None] * 7, None) == 1
     assert lib.gca_paged_append(ctypes.byref(paged(page=24)), *[None] * 7, None) == UNSUPPORTED
     assert lib.gca_paged_append(ctypes.byref(paged(Hkv=0)), *[None] * 7, None) == 1
+
+
+def test_positions_of_new_tokens_fit_32_bits(lib):
+    # the first of n tokens stands at -n where nothing is cached, and its window 2^30 before that
+    for n, max_q, code in ((2 ** 30 + 1, 0, UNSUPPORTED), (2 ** 30, 0, 1), (2 ** 31 - 1, 1000, 1)):
+        assert -min(n, max_q or n) - 2 ** 30 >= -2 ** 31 or code == UNSUPPORTED
+        p = paged(B=1, total_q=n, max_q=max_q, H=1, Hkv=1)
+        # (tensors that are missing are what stops the others)
+        assert lib.gca_paged_attn(ctypes.byref(p), *[None] * 9, 0, None) == code
