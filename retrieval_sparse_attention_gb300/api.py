@@ -211,6 +211,8 @@ def _empty_like(t):
 
 
 def _dense(t, shape, dtype, what):
+    if t is None:
+        raise ValueError("%s is needed" % what)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
     if tuple(t.shape) != tuple(shape) or not t.is_contiguous():

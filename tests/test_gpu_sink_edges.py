@@ -142,3 +142,10 @@ def test_sequences_behind_a_decreasing_entry_are_left_out(cu, T, window):
         for x in hit:
             want[x] = kn[i]
     assert torch.equal(got, want)
+
+
+def test_gradients_need_the_forwards_lse():
+    q, k, v, g = (torch.ones(1, 8, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    o, lse = api.swa_sink_fwd(q, k, v, window=4, sinks=0, with_lse=False)
+    with pytest.raises(ValueError, match="lse"):
+        api.swa_sink_bwd(q, k, v, o, lse, g, window=4, sinks=0)

@@ -68,3 +68,9 @@ def test_floats_are_no_counts():
         with pytest.raises(TypeError):
             f(30, 4.0)
     assert dense(True).window == 1
+
+
+def test_a_missing_lse_is_named():
+    # (as from a forward without it)
+    with pytest.raises(ValueError, match="lse"):
+        api._dense(None, (1, 8, 2), torch.float32, "lse")
