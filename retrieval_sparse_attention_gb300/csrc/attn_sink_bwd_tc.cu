@@ -34,9 +34,9 @@
 // excess for a third more products and a quarter more arithmetic in pass A.)
 //
 // Measured (GB300), B = 8 x 16K, 12 heads of 64, W = 512, 4 sinks: vectors 0.07 ms (6.2
-// TB/s), pass A 0.433, pass B 0.615, join 0.01: 1.125 ms in all, 0.99 without sinks and join (the
+// TB/s), pass A 0.433, pass B 0.615, join 0.01: 1.12 ms in all, 0.99 without sinks and join (the
 // plain window's gradients, gca_swa_bwd, 1.22).  2 x 16K, 16/4 heads of 128, W = 1024, 16
-// sinks: 0.05, 0.387, 0.515, 0.02: 0.976 ms.  3 x 1000, 6/2 heads: 38 us.
+// sinks: 0.05, 0.387, 0.515, 0.02: 0.98-1.01 ms.  3 x 1000, 6/2 heads: 38 us.
 // What bounds it: pass A and B keep the tensor pipe 31% and 33% busy and the issue
 // slots 49% and 51%; the math warps' latency a step and the issuing threads' share of
 // the slots pace them (pass B, a clock trace: a step every 1,165 cycles; a math pair's two

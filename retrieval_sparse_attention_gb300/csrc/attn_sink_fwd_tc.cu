@@ -35,19 +35,21 @@
 // others are masked in registers.  Up to 32 sinks take a tile of 32 columns.
 //
 // Measured (GB300; fractions of the measured 6.7 TB/s and 2.0 PFLOP/s):
-//   B = 8 x 16K, 12 heads of 64, W = 512: 0.308 ms, with 4 sinks 0.340 (2.4 TB/s);
-//   W = 2048 0.81 ms; 64K, 16/4 heads of 128, W = 1024, 16 sinks: 0.52-0.55 ms (1.0
-//   PFLOP/s, 50%); four chunks of 1.5-2K over 6-16K, 16/4 heads of 128: 0.43 ms
-//   (1.37 PFLOP/s, 69%); 32 tokens over caches of 4-33K, 24/8 heads of 128: 0.335
-//   ms (6.7 TB/s, 99%); one token over 777, W = 512: 12 us in a graph.
+//   B = 8 x 16K, 12 heads of 64, W = 512: 0.307 ms, with 4 sinks 0.340 (2.4 TB/s);
+//   W = 2048 0.83 ms; 64K, 16/4 heads of 128, W = 1024, 16 sinks: 0.55-0.58 ms (1.0
+//   PFLOP/s, 49%); four chunks of 1.5-2K over 6-16K, 16/4 heads of 128: 0.42 ms
+//   (1.37 PFLOP/s, 69%); 32 tokens over caches of 4-33K, 24/8 heads of 128: 0.326 to
+//   0.337 ms in a loop, 0.343 to 0.353 with a cold L2 (6.3-6.5 TB/s, 95-97%); a token
+//   each of 64 requests, 12 heads of 64, W = 512: 38 us in a graph; one over 777: 12 us.
 // What bounds it.  Single tokens over long caches: the cache's bytes.  d = 128 with
 // many rows: the chain S -> softmax -> P V of each worker, ~3,200 cycles a pair of
-// tiles of which the products fill ~2,450.  d = 64: instruction issue (48% of the
-// slots) and the chain of one tile's softmax, 1,250 to 1,850 cycles for a warp that
-// shares its sub-partition with one of the other worker; products fill 28% of the
-// time, exponentials 29% of their pipe.  The hot code of all roles has to stay in the
-// instruction cache, and is near its end: ~100 instructions more (a role's loop
-// unrolled over the two workers) cost 25%, 3 KB less gained 5 to 8%.
+// tiles of which the products fill ~2,450.  d = 64: no unit near its rate (issue slots
+// 50%, products 24-30% of the time, exponentials as much of their pipe, L2 23% of its rate);
+// what is left is latency: the chain of one tile's softmax, 1,250 to 1,850 cycles for a warp
+// that shares its sub-partition with one of the other worker, and the issuing warps' turns.
+// The hot code of all roles has to stay in the instruction cache, and is near its end: ~100
+// instructions more (a role's loop unrolled over the two workers) cost 25%, 3 KB less gained
+// 5 to 8%.
 // Tried and not kept: tiles of 64 keys with two or three S buffers a worker (1.3
 // to 1.5 times slower: the issuing warps' ~1,000 cycles a turn), two pipelines of own
 // control warps a CTA, P V started at half of P, barriers tested ahead of their
@@ -914,8 +916,8 @@ bool whole_units(const SinkShape& s) {
     // leaving them whole costs the difference between the longest share and the mean.  (312 units of 15
     // tiles, 12 heads of 64: 28.4 us whole, 33.1 cut; 308 of 17, 16/4 heads of 128: 34.6 and 43.4; B =
     // 8 x 16K, W = 512, 4 sinks: 0.339 and 0.348 ms; a token of 4 x 128 columns over 7 tiles: 16.7 and
-    // 11.3 us.)  Few tiles a unit only: ragged lengths make shares of whole units less even than this
-    // counts.
+    // 11.3 us.)  C is fitted to these and to a few shapes around them, not derived.  Few tiles a unit only:
+    // ragged lengths make shares of whole units less even than this counts.
     const long long span = (long long)s.W + tm - 1;
     const long long keys = s.paged ? (long long)s.width * s.page : s.L;
     const long long nt = span < keys ? (span + 126) / 128 + 1 + (s.ns + 127) / 128 : (keys + 127) / 128;
