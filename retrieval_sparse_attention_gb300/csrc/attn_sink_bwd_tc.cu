@@ -29,7 +29,7 @@
 // Roundings: P and ds to bf16, the type of the products' operands (relative 2^-8 at most, as
 // the gradients' own rounding, and as many random terms' errors they add up to about as much as
 // that: rms 1.7e-3 each); delta takes o as the forward rounded it (rms 5e-4 of a gradient).
-// Together 2.4e-3 to 2.6e-3 of a gradient's norm, where its own rounding alone is 1.7e-3.
+// Together 2.4e-3 to 2.7e-3 of a gradient's norm, where its own rounding alone is 1.7e-3.
 // Scores, lse, dP, delta and all sums are fp32.  (ds as two bf16 operands would halve the
 // excess for a third more products and a quarter more arithmetic in pass A.)
 //
