@@ -336,6 +336,36 @@ gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q
                               void* stream);
 
 /*
+ * Transformed scores: the three attention calls on either side of this text
+ * (gca_swa_sink_fwd, gca_swa_sink_bwd and gca_paged_attn) with scores that are
+ * capped by a tanh or lowered by the distance before the softmax.  With
+ * x = attn_scale q_t . k_s, the softmax is over
+ *   softcap > 0:  softcap tanh(x / softcap), which keeps every score within +-softcap
+ *                 (a product of +-inf counts as +-softcap);
+ *   slopes:       x - slopes[h] (t - s) for query head h at distance t - s >= 0.
+ * Masks, lse, layouts, workspaces and everything else are those of the plain
+ * calls; so are the gradients, which pass through the transform (the slopes are
+ * constants).  A score is off by 2^-20 softcap at most besides the product's own
+ * rounding.
+ * softcap: 0 (none) or 2^-10 .. 2^10, else GCA_ERR_UNSUPPORTED (GCA_ERR_INVALID_ARG
+ * below 0 or not finite).  Both at once: GCA_ERR_UNSUPPORTED.  Neither, or a null
+ * pointer in place of the struct: the plain call.
+ */
+typedef struct {
+    float softcap;        /* cap of the scores, 0: none                                     */
+    const float* slopes;  /* device, [H] fp32, finite, or NULL                              */
+} gca_score_t;
+
+gca_status_t gca_swa_sink_fwd_scored(const gca_swa_sink_params_t* params, const gca_score_t* score,
+                                     const void* q, const void* k, const void* v, void* o,
+                                     float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+gca_status_t gca_swa_sink_bwd_scored(const gca_swa_sink_params_t* params, const gca_score_t* score,
+                                     const void* q, const void* k, const void* v, const void* o,
+                                     const float* lse, const void* dout, void* dq, void* dk,
+                                     void* dv, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Paged K/V cache of the window self-attention, for generation: the keys and
  * values of B running sequences live in pages of `page` tokens,
  *   k_cache, v_cache [n_pages, page, Hkv, d],
@@ -416,6 +446,13 @@ gca_status_t gca_paged_attn(const gca_paged_params_t* params, const void* q, con
                             const void* v_cache, const int32_t* cu_q, const int32_t* kv_len,
                             const int32_t* table, void* o, float* lse, void* workspace,
                             size_t ws_bytes, void* stream);
+
+/* gca_paged_attn with transformed scores (gca_score_t). */
+gca_status_t gca_paged_attn_scored(const gca_paged_params_t* params, const gca_score_t* score,
+                                   const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* cu_q, const int32_t* kv_len,
+                                   const int32_t* table, void* o, float* lse, void* workspace,
+                                   size_t ws_bytes, void* stream);
 
 /*
  * gca_get_status -- synchronise `stream`, then return and clear the device

@@ -28,7 +28,8 @@ EXPORTED = ("gca_score_topk", "gca_fwd", "gca_bwd_workspace_size", "gca_bwd",
             "gca_gather_chunks", "gca_swa_fwd", "gca_swa_bwd_workspace_size", "gca_swa_bwd",
             "gca_swa_sink_fwd_workspace_size", "gca_swa_sink_fwd",
             "gca_swa_sink_bwd_workspace_size", "gca_swa_sink_bwd", "gca_paged_append",
-            "gca_paged_attn_workspace_size", "gca_paged_attn", "gca_debug_stall_next_decode")
+            "gca_paged_attn_workspace_size", "gca_paged_attn", "gca_swa_sink_fwd_scored",
+            "gca_swa_sink_bwd_scored", "gca_paged_attn_scored", "gca_debug_stall_next_decode")
 
 
 class GcaParams(ctypes.Structure):
@@ -63,6 +64,11 @@ class GcaPagedParams(ctypes.Structure):
                 ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("attn_scale", ctypes.c_float), ("q_stride", ctypes.c_int),
                 ("kv_stride", ctypes.c_int)]
+
+
+class GcaScore(ctypes.Structure):
+    """Mirror of gca_score_t."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
 
 
 class GcaError(RuntimeError):
@@ -107,6 +113,12 @@ def load() -> ctypes.CDLL:
             "gca_paged_append": ([ctypes.POINTER(GcaPagedParams)] + [vp] * 8, i32),
             "gca_paged_attn_workspace_size": ([ctypes.POINTER(GcaPagedParams)], sz),
             "gca_paged_attn": ([ctypes.POINTER(GcaPagedParams)] + [vp] * 9 + [sz, vp], i32),
+            "gca_swa_sink_fwd_scored": ([ctypes.POINTER(GcaSwaSinkParams),
+                                         ctypes.POINTER(GcaScore)] + [vp] * 6 + [sz, vp], i32),
+            "gca_swa_sink_bwd_scored": ([ctypes.POINTER(GcaSwaSinkParams),
+                                         ctypes.POINTER(GcaScore)] + [vp] * 10 + [sz, vp], i32),
+            "gca_paged_attn_scored": ([ctypes.POINTER(GcaPagedParams), ctypes.POINTER(GcaScore)] +
+                                      [vp] * 9 + [sz, vp], i32),
             "gca_get_status": ([vp], i32),
             "gca_status_string": ([i32], ctypes.c_char_p),
             "gca_last_launch_count": ([], i32),

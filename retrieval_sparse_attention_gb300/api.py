@@ -19,7 +19,7 @@ import operator
 import torch
 
 from . import _lib
-from ._lib import (GCA_BF16, GCA_F32, GcaError, GcaPagedParams, GcaParams, GcaSwaParams,
+from ._lib import (GCA_BF16, GCA_F32, GcaError, GcaPagedParams, GcaParams, GcaScore, GcaSwaParams,
                    GcaSwaSinkParams)
 
 _DT = {torch.bfloat16: GCA_BF16, torch.float32: GCA_F32}
@@ -257,6 +257,14 @@ def gca_swa_sink_fwd(params: GcaSwaSinkParams, q, k, v, o, lse, workspace, strea
         workspace.numel() if workspace is not None else 0, _raw_stream(stream, q.get_device())))
 
 
+def gca_swa_sink_fwd_scored(params: GcaSwaSinkParams, score: GcaScore, q, k, v, o, lse, workspace,
+                            stream=None):
+    _check("gca_swa_sink_fwd_scored", _lib.load().gca_swa_sink_fwd_scored(
+        ctypes.byref(params), ctypes.byref(score), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+        _ptr(workspace), workspace.numel() if workspace is not None else 0,
+        _raw_stream(stream, q.get_device())))
+
+
 def gca_swa_sink_bwd_workspace_size(params: GcaSwaSinkParams) -> int:
     return int(_lib.load().gca_swa_sink_bwd_workspace_size(ctypes.byref(params)))
 
@@ -267,6 +275,25 @@ def gca_swa_sink_bwd(params: GcaSwaSinkParams, q, k, v, o, lse, dout, dq, dk, dv
         ctypes.byref(params), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq),
         _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
         _raw_stream(stream, q.get_device())))
+
+
+def gca_swa_sink_bwd_scored(params: GcaSwaSinkParams, score: GcaScore, q, k, v, o, lse, dout, dq,
+                            dk, dv, workspace, stream=None):
+    _check("gca_swa_sink_bwd_scored", _lib.load().gca_swa_sink_bwd_scored(
+        ctypes.byref(params), ctypes.byref(score), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+        _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+        _raw_stream(stream, q.get_device())))
+
+
+def _score(softcap, slopes, H, dev):
+    """The transform of a call's scores, or None where it asks for none."""
+    softcap = float(softcap)
+    if slopes is None:
+        return GcaScore(softcap, None) if softcap else None
+    _dense(slopes, (H,), torch.float32, "slopes")
+    if slopes.get_device() != dev:
+        raise ValueError("tensors must be CUDA tensors on the current device")
+    return GcaScore(softcap, slopes.data_ptr())
 
 
 @functools.lru_cache(maxsize=256)
@@ -310,22 +337,30 @@ def _workspace(given, need, dev):
     return given
 
 
-def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, workspace=None):
+def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, workspace=None,
+                 softcap=0.0, slopes=None):
     """Windowed self-attention with sinks: q [B, L, H, d], k, v [B, L, Hkv, d] (token strides
-    may be those of a packed projection) -> (o [B, L, H, d], lse [B, L, H])."""
-    _same_device(q, k, v, workspace)
+    may be those of a packed projection) -> (o [B, L, H, d], lse [B, L, H]).  ``softcap`` caps
+    the scores by a tanh, ``slopes`` [H] fp32 lowers them by the distance (one of the two)."""
+    index = _same_device(q, k, v, workspace)
+    score = _score(softcap, slopes, q.shape[-2], index)
     p, need, _ = _swa_sink_args(q, k, v, window, sinks, attn_scale)
     dev = q.device
     ws = _workspace(workspace, need, dev)
     o = _empty_like(q)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if with_lse else None
-    gca_swa_sink_fwd(p, q, k, v, o, lse, ws)
+    if score is None:
+        gca_swa_sink_fwd(p, q, k, v, o, lse, ws)
+    else:
+        gca_swa_sink_fwd_scored(p, score, q, k, v, o, lse, ws)
     return o, lse
 
 
-def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, workspace=None):
+def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, workspace=None,
+                 softcap=0.0, slopes=None):
     """Gradients of swa_sink_fwd: returns dense (dq, dk, dv)."""
-    _same_device(q, k, v, o, lse, dout, workspace)
+    index = _same_device(q, k, v, o, lse, dout, workspace)
+    score = _score(softcap, slopes, q.shape[-2], index)
     p, _, need = _swa_sink_args(q, k, v, window, sinks, attn_scale)
     _dense(o, q.shape, q.dtype, "o")
     _dense(dout, q.shape, q.dtype, "dout")
@@ -333,7 +368,10 @@ def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, worksp
     dev = q.device
     ws = _workspace(workspace, need, dev)
     dq, dk, dv = _empty_like(q), _empty_like(k), _empty_like(v)
-    gca_swa_sink_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, ws)
+    if score is None:
+        gca_swa_sink_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, ws)
+    else:
+        gca_swa_sink_bwd_scored(p, score, q, k, v, o, lse, dout, dq, dk, dv, ws)
     return dq, dk, dv
 
 
@@ -362,6 +400,14 @@ def gca_paged_attn(params: GcaPagedParams, q, k_cache, v_cache, cu_q, kv_len, ta
     _check("gca_paged_attn", _lib.load().gca_paged_attn(
         ctypes.byref(params), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_q), _ptr(kv_len),
         _ptr(table), _ptr(o), _ptr(lse), _ptr(workspace),
+        workspace.numel() if workspace is not None else 0, _raw_stream(stream, q.get_device())))
+
+
+def gca_paged_attn_scored(params: GcaPagedParams, score: GcaScore, q, k_cache, v_cache, cu_q, kv_len,
+                          table, o, lse, workspace, stream=None):
+    _check("gca_paged_attn_scored", _lib.load().gca_paged_attn_scored(
+        ctypes.byref(params), ctypes.byref(score), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_q),
+        _ptr(kv_len), _ptr(table), _ptr(o), _ptr(lse), _ptr(workspace),
         workspace.numel() if workspace is not None else 0, _raw_stream(stream, q.get_device())))
 
 
@@ -418,11 +464,13 @@ def paged_append(k_new, v_new, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0
 
 
 def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, sinks=0,
-               attn_scale=0.0, with_lse=False, out=None, workspace=None):
+               attn_scale=0.0, with_lse=False, out=None, workspace=None, softcap=0.0, slopes=None):
     """Attention of the new tokens q [T, H, d] over the paged cache -> (o [T, H, d], lse [T, H]
     or None).  ``max_q`` bounds the new tokens of one sequence (0: T); a host that knows it
-    saves work.  Rows of o behind cu_q[B] are left as they were (``out`` supplies o)."""
-    _same_device(q, k_cache, v_cache, table, cu_q, kv_len, out, workspace)
+    saves work.  Rows of o behind cu_q[B] are left as they were (``out`` supplies o).  ``softcap``
+    and ``slopes`` as in swa_sink_fwd."""
+    index = _same_device(q, k_cache, v_cache, table, cu_q, kv_len, out, workspace)
+    score = _score(softcap, slopes, q.shape[-2], index)
     p, need = _paged_args(q, k_cache, v_cache, table, cu_q, kv_len, True, max_q, window, sinks, attn_scale)
     dev = q.device
     ws = _workspace(workspace, need, dev)
@@ -431,7 +479,10 @@ def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, s
     else:
         _dense(out, q.shape, q.dtype, "out")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if with_lse else None
-    gca_paged_attn(p, q, k_cache, v_cache, cu_q, kv_len, table, out, lse, ws)
+    if score is None:
+        gca_paged_attn(p, q, k_cache, v_cache, cu_q, kv_len, table, out, lse, ws)
+    else:
+        gca_paged_attn_scored(p, score, q, k_cache, v_cache, cu_q, kv_len, table, out, lse, ws)
     return out, lse
 
 

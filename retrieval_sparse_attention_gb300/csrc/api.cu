@@ -331,6 +331,16 @@ gca_status_t swa_sink_check(const gca_swa_sink_params_t* p, bool (*supported)(co
     return GCA_OK;
 }
 
+// The transform of the scores that a call asks for, if any.
+gca_status_t score_check(const gca_score_t* p, SinkShape* s) {
+    if (!p) return GCA_OK;
+    if (!(p->softcap >= 0.f) || isinf(p->softcap) || !aligned16(p->slopes)) return GCA_ERR_INVALID_ARG;
+    if (p->softcap > 0.f && (p->softcap < 0x1p-10f || p->softcap > 0x1p10f || p->slopes)) return GCA_ERR_UNSUPPORTED;
+    s->softcap = p->softcap;
+    s->slopes = p->slopes;
+    return GCA_OK;
+}
+
 // attend: for gca_paged_attn; the append takes H = 0 and is bound by none of the attention's counts
 gca_status_t paged_check(const gca_paged_params_t* p, bool attend, SinkShape* out) {
     if (!p) return GCA_ERR_INVALID_ARG;
@@ -371,9 +381,16 @@ size_t gca_swa_sink_fwd_workspace_size(const gca_swa_sink_params_t* params) {
 gca_status_t gca_swa_sink_fwd(const gca_swa_sink_params_t* params, const void* q, const void* k,
                               const void* v, void* o, float* lse, void* workspace, size_t ws_bytes,
                               void* stream) {
+    return gca_swa_sink_fwd_scored(params, nullptr, q, k, v, o, lse, workspace, ws_bytes, stream);
+}
+
+gca_status_t gca_swa_sink_fwd_scored(const gca_swa_sink_params_t* params, const gca_score_t* score,
+                                     const void* q, const void* k, const void* v, void* o,
+                                     float* lse, void* workspace, size_t ws_bytes, void* stream) {
     SinkShape s;
     gca_status_t r = swa_sink_check(params, sink_fwd_supported, &s);
     if (r != GCA_OK) return r;
+    if ((r = score_check(score, &s)) != GCA_OK) return r;
     if ((r = check_ptrs({q, k, v, o})) != GCA_OK) return r;
     if (lse && !aligned16(lse)) return GCA_ERR_INVALID_ARG;
     if ((r = check_workspace(workspace, ws_bytes, sink_fwd_workspace_bytes(s))) != GCA_OK) return r;
@@ -396,9 +413,18 @@ gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q
                               const void* v, const void* o, const float* lse, const void* dout,
                               void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes,
                               void* stream) {
+    return gca_swa_sink_bwd_scored(params, nullptr, q, k, v, o, lse, dout, dq, dk, dv, workspace,
+                                   ws_bytes, stream);
+}
+
+gca_status_t gca_swa_sink_bwd_scored(const gca_swa_sink_params_t* params, const gca_score_t* score,
+                                     const void* q, const void* k, const void* v, const void* o,
+                                     const float* lse, const void* dout, void* dq, void* dk,
+                                     void* dv, void* workspace, size_t ws_bytes, void* stream) {
     SinkShape s;
     gca_status_t r = swa_sink_check(params, sink_bwd_supported, &s);
     if (r != GCA_OK) return r;
+    if ((r = score_check(score, &s)) != GCA_OK) return r;
     if ((r = check_ptrs({q, k, v, o, lse, dout, dq, dk, dv})) != GCA_OK) return r;
     if ((r = check_workspace(workspace, ws_bytes, sink_bwd_workspace_bytes(s))) != GCA_OK) return r;
     int* st = status_word();
@@ -440,9 +466,19 @@ gca_status_t gca_paged_attn(const gca_paged_params_t* params, const void* q, con
                             const void* v_cache, const int32_t* cu_q, const int32_t* kv_len,
                             const int32_t* table, void* o, float* lse, void* workspace,
                             size_t ws_bytes, void* stream) {
+    return gca_paged_attn_scored(params, nullptr, q, k_cache, v_cache, cu_q, kv_len, table, o, lse,
+                                 workspace, ws_bytes, stream);
+}
+
+gca_status_t gca_paged_attn_scored(const gca_paged_params_t* params, const gca_score_t* score,
+                                   const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* cu_q, const int32_t* kv_len,
+                                   const int32_t* table, void* o, float* lse, void* workspace,
+                                   size_t ws_bytes, void* stream) {
     SinkShape s;
     gca_status_t r = paged_check(params, true, &s);
     if (r != GCA_OK) return r;
+    if ((r = score_check(score, &s)) != GCA_OK) return r;
     if (s.T == 0) {
         t_launches = 0;
         return GCA_OK;

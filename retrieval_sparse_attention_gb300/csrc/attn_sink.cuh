@@ -328,6 +328,32 @@ __device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity) {
     }
     return false;
 }
+// ---------------------------------------------------------------------------
+// Transforms of the score x = a q_t . k_s before the softmax (gca_score_t).
+//   cap:  c tanh(x / c).  With E = exp(2 x / c) and r = 1 / (1 + E), tanh(x / c) = 1 - 2 r, so the
+//         score in log2 units is C - 2 C r with C = c log2(e), one FMA from r, and the derivative
+//         by x is 1 - tanh^2 = 4 r (1 - r).  r falls as the score rises, from 1 to 0; E = inf and E = 0 are
+//         its ends.  In units of 2^-23 c a score is off by 3/4 (the exponent's roundings), 1 (exp2), 3
+//         (1 + E and its reciprocal, where r is near 1) and 2 (the FMAs): 2^-20 c at most, for the largest
+//         c that the entries take 2^-10, half the rounding of a probability to bf16.
+//   bias: x - slope_h (t - s), with slope_h log2(e) in log2 units.
+// ---------------------------------------------------------------------------
+enum ScoreKind { kScorePlain = 0, kScoreCap = 1, kScoreBias = 2 };
+
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// r of two scores; `in` is 2 a log2(e) / c
+__device__ __forceinline__ void cap_r2(float x0, float x1, uint64_t in2, float& r0, float& r1) {
+    float y0, y1;
+    tcx::f2_unpack(tcx::fmul2(tcx::f2_pack(x0, x1), in2), y0, y1);
+    tcx::f2_unpack(tcx::fadd2(tcx::f2_pack(tcx::fast_exp2(y0), tcx::fast_exp2(y1)), tcx::f2_pack(1.f, 1.f)), y0, y1);
+    r0 = fast_rcp(y0);
+    r1 = fast_rcp(y1);
+}
+
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;

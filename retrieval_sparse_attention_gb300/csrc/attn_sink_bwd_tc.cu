@@ -89,13 +89,32 @@ struct BwdArgs {
     int R;
     int wholeA, wholeB;      // shares end between items: nothing to join
     int* status;
-    float scale_log2, scale;
+    float scale_log2, scale; // scale: of ds; four times that with a cap, whose derivative is 4 r (1 - r)
+    const float* slopes;     // [H], of a distance bias
+    float cap_in, cap_log2;  // 2 scale log2(e) / c and c log2(e), of a cap c (attn_sink.cuh)
 };
+
+// The exponent of p from a product x (two at a time), nl being -lse log2(e) and what of the score does
+// not depend on x:
+//   plain, bias  scale_log2 x + nl      cap  -2 C r + nl, with C in nl
+// and with a cap r (1 - r), which ds takes besides p.
+template <int SCORE>
+__device__ __forceinline__ uint64_t exponent2(uint32_t x0, uint32_t x1, uint64_t sl2, uint64_t cap_in2, uint64_t nl,
+                                              uint64_t& bend) {
+    if constexpr (SCORE == kScoreCap) {
+        float r0, r1;
+        cap_r2(__uint_as_float(x0), __uint_as_float(x1), cap_in2, r0, r1);
+        const uint64_t r = tcx::f2_pack(r0, r1);
+        bend = tcx::ffma2(tcx::f2_pack(-r0, -r1), r, r);
+        return tcx::ffma2(r, sl2, nl);
+    }
+    return tcx::ffma2(tcx::f2_pack(__uint_as_float(x0), __uint_as_float(x1)), sl2, nl);
+}
 
 // ============================================================================ vectors
 // A block: 32 tokens x 8 heads; delta from coalesced 16-byte reads, then both layouts.
 // Memory-bound: reads o, dO and lse once (B = 8 x 16K, 12 heads of 64: 0.43 GB in 70 us, 6.2 TB/s).
-template <int D>
+template <int D, int SCORE>
 __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     __shared__ float sd[8][33];
     pdl_release();
@@ -134,10 +153,13 @@ __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     const int t = t0 + lane, h = h0 + warp;
     if (h >= sc.H) return;
     const bool live = t < sc.L;
-    const float nl = live ? -a.lse[((size_t)b * sc.L + t) * sc.H + h] * kLog2e : 0.f;
+    float nl = live ? -a.lse[((size_t)b * sc.L + t) * sc.H + h] * kLog2e : 0.f;
+    if (SCORE == kScoreCap) nl += a.cap_log2;
     const float nd = live ? -a.scale * sd[warp][lane] : 0.f;
     const size_t ib = ((size_t)b * sc.H + h) * a.Lp + t;
-    a.nlB[ib] = nl;
+    // (a bias as far as the query's place in its block of 64 goes: pass B adds that between the key
+    // and the block, a number of its own size that loses nothing)
+    a.nlB[ib] = SCORE == kScoreBias ? fmaf(-a.slopes[h] * kLog2e, static_cast<float>(t & 63), nl) : nl;
     a.ndB[ib] = nd;
     if (live) {
         const int hk = h / sc.G, mt = t / sc.TM;
@@ -245,7 +267,7 @@ __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wi
     return u;
 }
 
-template <int D>
+template <int D, int SCORE>
 __global__ void __launch_bounds__(kThreadsA, 1)
 sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -454,7 +476,8 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         const int row = 32 * qd + lane;               // query row of the tile = lane of tensor memory
         const int rt = row / sc.G, rg = row - rt * sc.G;
         const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
-        const uint64_t sl2 = tcx::f2_pack(a.scale_log2, a.scale_log2);
+        const float sl = SCORE == kScoreCap ? -2.f * a.cap_log2 : a.scale_log2;
+        const uint64_t sl2 = tcx::f2_pack(sl, sl), cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
         const uint64_t sc2 = tcx::f2_pack(a.scale, a.scale);
         int u = 0;
         // the dQ rows of a part that this warpgroup stores leave after its first step of
@@ -490,6 +513,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const Part& w = sb.part[r];
             const int j0 = w.j0, j1 = w.j1, nar = w.nar, p0 = w.mt * sc.TM;
             if (j0 == j1) { done = true; break; }
+            const float slope = SCORE == kScoreBias ? __ldg(a.slopes + w.h * sc.G + rg) * kLog2e : 0.f;
             if (!wwait(&sb.vec_full, full_par(np))) break;
             const float* vec = reinterpret_cast<const float*>(sm + C::OFF_VEC);
             const float nl2 = vec[row], ndsc = vec[128 + row];
@@ -508,6 +532,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 const bool edge = kbase + 63 > p0 || (kbase < plast - sc.W + 1 && kbase + 63 >= sc.ns);
                 const uint32_t xb = tmem + lane_base + C::COL_X + xs * 64;
                 const uint32_t yb = tmem + lane_base + C::COL_Y + ys * 64;
+                const float off = SCORE == kScoreBias ? fmaf(slope, static_cast<float>(kbase - p), nl2) : nl2;
                 const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
 #pragma unroll
                 for (int pc = 0; pc < 2; ++pc) {
@@ -536,8 +561,11 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                             const uint32_t* rd = p2 < 8 ? r2 : r3;
                             const int tt = 2 * (p2 & 7);
                             float y0, y1;
-                            tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[tt]), __uint_as_float(rs[tt + 1])),
-                                                      sl2, nl22), y0, y1);
+                            uint64_t bend = 0, nl = nl22;
+                            if (SCORE == kScoreBias)
+                                nl = tcx::ffma2(tcx::f2_pack(32.f * pc + 2 * p2, 32.f * pc + 2 * p2 + 1), tcx::f2_pack(slope, slope),
+                                                tcx::f2_pack(off, off));
+                            tcx::f2_unpack(exponent2<SCORE>(rs[tt], rs[tt + 1], sl2, cap_in2, nl, bend), y0, y1);
                             float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
                             if (msk) {
                                 e0 = (vis >> (2 * p2) & 1u) ? e0 : 0.f;
@@ -545,7 +573,9 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                             }
                             const uint64_t gd = tcx::ffma2(
                                 tcx::f2_pack(__uint_as_float(rd[tt]), __uint_as_float(rd[tt + 1])), sc2, ndsc2);
-                            pk[p2] = tcx::pack_bf16x2(tcx::fmul2(tcx::f2_pack(e0, e1), gd));
+                            uint64_t ev = tcx::f2_pack(e0, e1);
+                            if (SCORE == kScoreCap) ev = tcx::fmul2(ev, bend);
+                            pk[p2] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
                         }
                     };
                     if (edge) body(true);
@@ -693,7 +723,7 @@ __device__ __forceinline__ Part next_part(const BwdArgs& a, StreamPos& p, int wi
     return u;
 }
 
-template <int D>
+template <int D, int SCORE>
 __global__ void __launch_bounds__(kThreadsB, 1)
 sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -905,7 +935,8 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const int qd = warp & 3;
         const int row = 32 * qd + lane;               // key row of the tile = lane of tensor memory
         const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
-        const uint64_t sl2 = tcx::f2_pack(a.scale_log2, a.scale_log2);
+        const float sl = SCORE == kScoreCap ? -2.f * a.cap_log2 : a.scale_log2;
+        const uint64_t sl2 = tcx::f2_pack(sl, sl), cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
         const uint64_t sc2 = tcx::f2_pack(a.scale, a.scale);
         Ring st{0, 0};
         int u = 0;
@@ -965,10 +996,12 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             for (int j = 0; j < n; ++j, ++u, st.next(C::NSLOT), sp.next(sc.G)) {
                 if ((u & 1) != wg) continue;
                 const int xs = u % C::NX, ys = u % C::NY;
+                const float slope = SCORE == kScoreBias ? __ldg(a.slopes + w.h * sc.G + sp.g) * kLog2e : 0.f;
                 // (x_full: the stage has landed too, so the phase of its barrier is the one meant)
                 if (!wwait(&sb.x_full[xs], full_par(u / C::NX)) || !wwait(&sb.st_full[st.i], st.ph)) { ok = false; break; }
                 tc_fence_after();
                 const int qb = sp.block() * 64;
+                const float off = slope * static_cast<float>(s - qb);
                 const int c_lo = s - qb, c_hi = last - qb;
                 const uint8_t* vec = sm + C::OFF_ST + st.i * C::SLOT + 2 * C::QTILE;
                 const uint64_t* nl = reinterpret_cast<const uint64_t*>(vec);              // pairs
@@ -1004,8 +1037,9 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 float y0, y1;
-                                tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
-                                                          sl2, nl[8 * c + i]), y0, y1);
+                                uint64_t bend = 0, y = exponent2<SCORE>(rs[2 * i], rs[2 * i + 1], sl2, cap_in2, nl[8 * c + i], bend);
+                                if (SCORE == kScoreBias) y = tcx::fadd2(y, tcx::f2_pack(off, off));
+                                tcx::f2_unpack(y, y0, y1);
                                 float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
                                 if (msk) {
                                     e0 = (vis >> (2 * i) & 1u) ? e0 : 0.f;
@@ -1014,7 +1048,7 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                 const uint64_t ev = tcx::f2_pack(e0, e1);
                                 const uint64_t gd = tcx::ffma2(tcx::f2_pack(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])),
                                                                sc2, nd[8 * c + i]);
-                                pd[i] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
+                                pd[i] = tcx::pack_bf16x2(tcx::fmul2(SCORE == kScoreCap ? tcx::fmul2(ev, bend) : ev, gd));
                                 pp[i] = tcx::pack_bf16x2(ev);
                             }
                             // ds^T, then P^T, over the 16 S^T columns just read
@@ -1126,34 +1160,34 @@ Layout layout(const SinkShape& s) {
     return w;
 }
 
-template <int D>
+template <int D, int SCORE>
 cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[8], cudaStream_t st,
                    int* launches) {
     static LaunchSetup setup;
     int sms = 0;
     cudaError_t e = setup.once(
         [] {
-            const cudaError_t r = cudaFuncSetAttribute(pa::sink_bwd_q_kernel<D>,
+            const cudaError_t r = cudaFuncSetAttribute(pa::sink_bwd_q_kernel<D, SCORE>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, pa::Cfg<D>::SMEM);
             if (r != cudaSuccess) return r;
             // (a build that gave the kernel fewer registers would wait forever at the split: refuse it)
             cudaFuncAttributes fa;
-            if (const cudaError_t x = cudaFuncGetAttributes(&fa, pb::sink_bwd_kv_kernel<D>)) return x;
+            if (const cudaError_t x = cudaFuncGetAttributes(&fa, pb::sink_bwd_kv_kernel<D, SCORE>)) return x;
             if (fa.numRegs < kRegsB) return cudaErrorInvalidConfiguration;
-            return cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(pb::sink_bwd_kv_kernel<D, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         pb::Cfg<D>::SMEM);
         },
         &sms);
     if (e != cudaSuccess) return e;
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
     const dim3 vgrid((unsigned)(s.B * (a.Lp / 32)), (unsigned)((s.H + 7) / 8));
-    GCA_LAUNCH("sink_bwd_vec", st, sink_bwd_vec_kernel<D><<<vgrid, 256, 0, st>>>(a));
+    GCA_LAUNCH("sink_bwd_vec", st, sink_bwd_vec_kernel<D, SCORE><<<vgrid, 256, 0, st>>>(a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     GCA_LAUNCH("sink_bwd_q", st,
-               e = launch_pdl(pa::sink_bwd_q_kernel<D>, dim3(grid), kThreadsA, pa::Cfg<D>::SMEM, st, m[0], m[1], m[2], m[3], a));
+               e = launch_pdl(pa::sink_bwd_q_kernel<D, SCORE>, dim3(grid), kThreadsA, pa::Cfg<D>::SMEM, st, m[0], m[1], m[2], m[3], a));
     if (e != cudaSuccess) return e;
     GCA_LAUNCH("sink_bwd_kv", st,
-               e = launch_pdl(pb::sink_bwd_kv_kernel<D>, dim3(grid), kThreadsB, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
+               e = launch_pdl(pb::sink_bwd_kv_kernel<D, SCORE>, dim3(grid), kThreadsB, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
     if (e != cudaSuccess) return e;
     *launches += 3;
     if (a.wholeA && a.wholeB) return e;
@@ -1208,8 +1242,13 @@ cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, co
     a.headA = reinterpret_cast<int*>(base + w.headA);
     a.headB = reinterpret_cast<int*>(base + w.headB);
     a.status = status;
-    a.scale = s.scale;
+    a.scale = s.softcap > 0.f ? 4.f * s.scale : s.scale;
     a.scale_log2 = s.scale * kLog2e;
+    a.slopes = s.slopes;
+    if (s.softcap > 0.f) {
+        a.cap_in = 2.f * a.scale_log2 / s.softcap;
+        a.cap_log2 = s.softcap * kLog2e;
+    }
     // Items are left whole where the longest share is then longer than the mean by less than a cut's
     // sums and the join take, C steps (2 x 4K, 12 heads of 64, W = 512: 83 instead of 96 us), but not
     // pass A's where pass B's are cut, unless shares are short: the join is launched anyway, and long
@@ -1236,7 +1275,11 @@ cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, co
         ok = ok && encode_bf16_3d(&m[2 + 4 * i], k, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1, wide) &&
              encode_bf16_3d(&m[3 + 4 * i], v, kvcols, L, B, s.kv_stride, s.kv_stride * L, i ? 128 : 64, 1, wide);
     if (!ok) return cudaErrorInvalidValue;
-    return s.d == 64 ? launch<64>(s, a, m, st, launches) : launch<128>(s, a, m, st, launches);
+    if (s.softcap > 0.f)
+        return s.d == 64 ? launch<64, kScoreCap>(s, a, m, st, launches) : launch<128, kScoreCap>(s, a, m, st, launches);
+    if (s.slopes)
+        return s.d == 64 ? launch<64, kScoreBias>(s, a, m, st, launches) : launch<128, kScoreBias>(s, a, m, st, launches);
+    return s.d == 64 ? launch<64, kScorePlain>(s, a, m, st, launches) : launch<128, kScorePlain>(s, a, m, st, launches);
 }
 
 }  // namespace gca

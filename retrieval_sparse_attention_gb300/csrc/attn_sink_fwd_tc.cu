@@ -119,6 +119,8 @@ struct FwdArgs {
     int whole;               // shares end between units: nothing to join
     int* status;
     float scale_log2;
+    const float* slopes;     // [H], of a distance bias
+    float cap_in, cap_log2;  // 2 scale log2(e) / c and c log2(e), of a cap c
 };
 
 // One worker's part of a unit: key tiles j0 .. j1 - 1 (j0 == j1: the share is done).
@@ -224,7 +226,7 @@ __device__ __forceinline__ Part next_part(const FwdArgs& a, StreamPos& p, int wi
     return u;
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int SCORE>
 __global__ void __launch_bounds__(kThreads, 1)
 sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const FwdArgs a) {
@@ -587,7 +589,25 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const uint32_t ts_addr = tmem + lane_base + C::COL_S + wg * 128;
         const uint32_t to_addr = tmem + lane_base + C::COL_O + wg * D;
         const uint32_t tp_addr = tmem + lane_base + C::COL_P + wg * C::P_STEP;
-        const float sl = a.scale_log2;
+        // A score in log2 units is v sl + so, v being what the tile's registers hold: the product, with a
+        // cap its r (attn_sink.cuh: falling in the score, so its least is the greatest score), with a
+        // bias the score itself.  A column that a row does not see holds kHidden.
+        constexpr bool CAP = SCORE == kScoreCap, BIAS = SCORE == kScoreBias;
+        constexpr float kHidden = CAP ? INFINITY : -INFINITY;
+        const float sl = CAP ? -2.f * a.cap_log2 : BIAS ? 1.f : a.scale_log2, so = CAP ? a.cap_log2 : 0.f;
+        const uint64_t cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
+        float slope = 0.f;                              // of this row's head, in log2 units
+        auto greater = [](float x, float y) { return CAP ? fminf(x, y) : fmaxf(x, y); };
+        auto log2_of = [&](float v) { return CAP ? fmaf(v, sl, so) : v * sl; };
+        auto less = [&](float max) { return CAP ? so - max : -max; };
+        // products of columns c, c + 1, whose keys are `from` + c, + 1 positions from the row's own
+        auto transform = [&](float& x0, float& x1, int c, uint64_t from) {
+            if constexpr (CAP) cap_r2(x0, x1, cap_in2, x0, x1);
+            if constexpr (BIAS)
+                tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x0, x1), tcx::f2_pack(a.scale_log2, a.scale_log2),
+                                          tcx::ffma2(tcx::f2_pack((float)c, (float)(c + 1)), tcx::f2_pack(slope, slope), from)),
+                               x0, x1);
+        };
 
         int ts = 0, ko = 0, np = 0, j = 0, j1 = 0, f0 = 0, f1 = 0, fl = 0;
         bool first = true;                              // at the first tile of a part
@@ -612,6 +632,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 // rows that do not exist are skipped, where a whole warp has no other
                 live = have && row < a.R && rt < sb.part[wg][r].ntok;
                 wlive = __any_sync(0xffffffffu, live);
+                if (BIAS && have) slope = __ldg(a.slopes + sb.part[wg][r].h * sc.G + rg) * kLog2e;
             }
             const Part& w = sb.part[wg][(np - 1) % kParts];
             // the previous part's output leaves while the next part's Q and first S are on their way
@@ -692,15 +713,25 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 tc_fence_before();
                 if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
                 const uint32_t nvis = below(sc.ns);
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if constexpr (SCORE != kScorePlain) {
+                    const float off = slope * static_cast<float>(-w.p0 - rt);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float x0 = __uint_as_float(r[i]), x1 = __uint_as_float(r[i + 1]);
+                        transform(x0, x1, i, tcx::f2_pack(off, off));
+                        r[i] = __float_as_uint(x0);
+                        r[i + 1] = __float_as_uint(x1);
+                    }
+                }
+                float m4[4] = {kHidden, kHidden, kHidden, kHidden};
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    r[i] = (nvis >> i & 1u) ? r[i] : 0xff800000u;
-                    m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(r[i]));
+                    r[i] = (nvis >> i & 1u) ? r[i] : (CAP ? 0x7f800000u : 0xff800000u);
+                    m4[i & 3] = greater(m4[i & 3], __uint_as_float(r[i]));
                 }
-                follow(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl);
+                follow(log2_of(greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]))));
                 float l4[4];
-                const uint64_t nsl2 = tcx::f2_pack(sl, sl), nnm2 = tcx::f2_pack(-m, -m);
+                const uint64_t nsl2 = tcx::f2_pack(sl, sl), nnm2 = tcx::f2_pack(less(m), less(m));
                 uint64_t la[2] = {0ull, 0ull};
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -733,7 +764,14 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     tc_fence_before();
                     if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
                     float mt = fmaxf(mc[0], mc[1]);
-                    if (!((j >= f0 && j < f1) || j == fl)) {
+                    if constexpr (SCORE != kScorePlain) {
+                        const float off = slope * static_cast<float>(w.tile(j) * 128 - w.p0 - rt);
+#pragma unroll
+                        for (int i = 0; i < 128; i += 2) transform(x[i], x[i + 1], i, tcx::f2_pack(off, off));
+                        if (CAP) mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));   // (of the greatest product)
+                    }
+                    const bool whole = (j >= f0 && j < f1) || j == fl;
+                    if (!whole) {
                         // The diagonal or the window's edge crosses the tile.  Visible: columns c_lo ..
                         // c_hi (the window) and those below c_s (sinks), as bits.
                         const int p = w.p0 + rt, kbase = w.tile(j) * 128;
@@ -742,21 +780,22 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         for (int c = 0; c < 4; ++c) {
                             const uint32_t vis = (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : -INFINITY;
-                        }
-                        // the maximum over all columns bounds that over the visible ones: only where it
-                        // would move the running one (or is no number) is the latter needed
-                        if (__any_sync(0xffffffffu, !(mt * sl <= m + kRescaleLog2))) {
-                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
-                            mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : kHidden;
                         }
                     }
-                    follow(mt * sl);
+                    // the maximum over all columns bounds that over the visible ones: only where it
+                    // would move the running one (or is no number) is the latter needed (with a bias
+                    // the products' maximum says nothing: always)
+                    if (BIAS || (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2)))) {
+                        float m4[4] = {kHidden, kHidden, kHidden, kHidden};
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) m4[i & 3] = greater(m4[i & 3], x[i]);
+                        mt = greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]));
+                    }
+                    follow(log2_of(mt));
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
-                const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(-mu, -mu);
+                const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(less(mu), less(mu));
                 uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t pka[32];                       // the first 64 keys' P, formed before the wait for the P buffer
 #pragma unroll
@@ -927,7 +966,7 @@ bool whole_units(const SinkShape& s) {
     return nt <= 2 * C + 2 && (units + kMaxWorkers - 1) / kMaxWorkers * nt * kMaxWorkers <= units * nt + C * kMaxWorkers;
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int SCORE>
 cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                    const CUtensorMap& tv, cudaStream_t st, int* launches) {
     using C = Cfg<D>;
@@ -938,15 +977,15 @@ cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& t
             // the setmaxnreg split needs the whole launch allocation: refuse to launch a build that
             // gave the kernel fewer registers a thread (its warps would wait forever)
             cudaFuncAttributes fa;
-            const cudaError_t r = cudaFuncGetAttributes(&fa, sink_fwd_tc_kernel<D, PAGED>);
+            const cudaError_t r = cudaFuncGetAttributes(&fa, sink_fwd_tc_kernel<D, PAGED, SCORE>);
             if (r != cudaSuccess) return r;
             if (fa.numRegs * kThreads < 128 * kRegsCtrl + 256 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
-            return cudaFuncSetAttribute(sink_fwd_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            return cudaFuncSetAttribute(sink_fwd_tc_kernel<D, PAGED, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         },
         &sms);
     if (e != cudaSuccess) return e;
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D, PAGED><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
+    GCA_LAUNCH("sink_fwd_tc", st, sink_fwd_tc_kernel<D, PAGED, SCORE><<<grid, kThreads, C::SMEM, st>>>(tq, tk, tv, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *launches += 1;
     if (a.whole) return e;
@@ -955,6 +994,16 @@ cudaError_t launch(const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& t
                e = launch_pdl(sink_join_kernel<D, PAGED>, dim3(2 * grid, (a.R + rows - 1) / rows), 256, 0, st, a, 2 * grid));
     if (e == cudaSuccess) *launches += 1;
     return e;
+}
+
+template <int SCORE>
+cudaError_t launch_shape(const SinkShape& s, const FwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, cudaStream_t st, int* launches) {
+    if (s.paged)
+        return s.d == 64 ? launch<64, true, SCORE>(a, tq, tk, tv, st, launches)
+                         : launch<128, true, SCORE>(a, tq, tk, tv, st, launches);
+    return s.d == 64 ? launch<64, false, SCORE>(a, tq, tk, tv, st, launches)
+                     : launch<128, false, SCORE>(a, tq, tk, tv, st, launches);
 }
 
 }  // namespace
@@ -994,6 +1043,11 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     a.lse = lse;
     a.status = status;
     a.scale_log2 = s.scale * kLog2e;
+    a.slopes = s.slopes;
+    if (s.softcap > 0.f) {
+        a.cap_in = 2.f * a.scale_log2 / s.softcap;
+        a.cap_log2 = s.softcap * kLog2e;
+    }
     a.whole = whole_units(s);
     CUtensorMap tq, tk, tv;
     const uint64_t kvcols = (uint64_t)s.Hkv * s.d;
@@ -1007,11 +1061,9 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
                             : encode_bf16_3d(m, p, kvcols, s.L, s.B, s.kv_stride, (uint64_t)s.kv_stride * s.L, 128, 1, s.d == 128));
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (s.paged)
-        return s.d == 64 ? launch<64, true>(a, tq, tk, tv, st, launches)
-                         : launch<128, true>(a, tq, tk, tv, st, launches);
-    return s.d == 64 ? launch<64, false>(a, tq, tk, tv, st, launches)
-                     : launch<128, false>(a, tq, tk, tv, st, launches);
+    if (s.softcap > 0.f) return launch_shape<kScoreCap>(s, a, tq, tk, tv, st, launches);
+    if (s.slopes) return launch_shape<kScoreBias>(s, a, tq, tk, tv, st, launches);
+    return launch_shape<kScorePlain>(s, a, tq, tk, tv, st, launches);
 }
 
 }  // namespace gca

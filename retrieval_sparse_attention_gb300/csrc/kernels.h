@@ -137,6 +137,8 @@ struct SinkShape {
     int q_stride, kv_stride;      // elements between consecutive tokens
     float scale;
     int paged;
+    float softcap;                // 0: none
+    const float* slopes;          // [H] of a distance bias, or null
 };
 constexpr int kNoWindow = 0x40000000;
 
