@@ -29,7 +29,8 @@
  *  - dtype GCA_F32 : d in {16, 32, 64}, S in {16, 32, 64} (fp32 FFMA path)
  *  - 1 <= topk <= 32, landmark dimension <= 8192, chunks per row <= 16384.
  *  - sliding-window entries: see gca_swa_params_t, gca_swa_sink_params_t and
- *    gca_paged_params_t.
+ *    gca_paged_params_t; rotary positions: gca_rope_params_t; a cache's pages:
+ *    gca_pages_params_t.
  */
 #ifndef GCA_H_
 #define GCA_H_
@@ -48,7 +49,8 @@ typedef enum {
     GCA_ERR_WORKSPACE = 3,     /* workspace missing or too small             */
     GCA_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed          */
     GCA_ERR_TIMEOUT = 5,       /* a bounded device-side wait ran out         */
-    GCA_ERR_DEVICE_INDEX = 6   /* the device saw an index outside its range  */
+    GCA_ERR_DEVICE_INDEX = 6,  /* the device saw an index outside its range  */
+    GCA_ERR_NO_PAGES = 7       /* a paged cache had too few free pages       */
 } gca_status_t;
 
 typedef enum { GCA_BF16 = 0, GCA_F32 = 1 } gca_dtype_t;
@@ -366,6 +368,42 @@ gca_status_t gca_swa_sink_bwd_scored(const gca_swa_sink_params_t* params, const 
                                      void* dv, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Rotary positions.  Pair i of a head's first `rot` columns, (x, y), of a token at
+ * position p is turned by the angle p f_i,
+ *   x' = mscale (x cos - y sin),  y' = mscale (x sin + y cos),
+ * the pairs being columns (i, i + rot/2), or (2i, 2i + 1) with `interleaved`; the
+ * other columns are copied.  Arithmetic in fp32, one rounding.
+ *   freqs [rot/2] int64, device: f_i as a fraction of a turn, f_i / (2 pi) modulo 1
+ *     in units of 2^-64 (signed or not is the same), so that angles are exact at any
+ *     position: scaled positions for long contexts are other numbers here.
+ *   The gradient of the turn is the turn by the negative angle (`inverse`).
+ */
+typedef struct {
+    int T;                /* tokens, >= 0 (0: nothing is enqueued)                          */
+    int L;                /* token t is at position start + t % L (without `positions`)     */
+    int start;            /* >= 0, start + L up to 2^31 - 1                                 */
+    int H, Hkv, d;        /* heads of q and of k, either may be 0; d = 32, 64, 128 or 256   */
+    int rot;              /* columns that turn: a multiple of 16, 16 .. d                   */
+    int interleaved;      /* 0: pairs are rot/2 columns apart; 1: neighbours                */
+    int inverse;          /* 1: by the negative angle                                       */
+    gca_dtype_t dtype;    /* GCA_BF16 or GCA_F32                                            */
+    float mscale;         /* factor of the turned columns, >= 0; 0 => 1                     */
+    int q_stride, k_stride;       /* elements between consecutive tokens; 0 => H*d, Hkv*d;  */
+    int q_out_stride, k_out_stride; /* multiples of 8, up to 2^24                            */
+} gca_rope_params_t;
+
+/*
+ * gca_rope -- turn q [T, H, d] and k [T, Hkv, d] (a null pointer where H or Hkv is 0).
+ *   positions [T] int32 (device, any sign) or NULL: start + t % L.
+ *   q_out, k_out may be q and k themselves with the same strides (in place), but must not
+ *   overlap them, or each other, in any other way.
+ *   Up to 2^31 warps of 128 slots (16 columns each) of a token in all.
+ */
+gca_status_t gca_rope(const gca_rope_params_t* params, const void* q, const void* k,
+                      const int64_t* freqs, const int32_t* positions, void* q_out, void* k_out,
+                      void* stream);
+
+/*
  * Paged K/V cache of the window self-attention, for generation: the keys and
  * values of B running sequences live in pages of `page` tokens,
  *   k_cache, v_cache [n_pages, page, Hkv, d],
@@ -453,6 +491,101 @@ gca_status_t gca_paged_attn_scored(const gca_paged_params_t* params, const gca_s
                                    const int32_t* cu_q, const int32_t* kv_len,
                                    const int32_t* table, void* o, float* lse, void* workspace,
                                    size_t ws_bytes, void* stream);
+
+/*
+ * gca_paged_rope_append -- gca_paged_append of keys turned by their positions, and the
+ * new tokens' queries turned by theirs, in one launch.
+ *   rope: rot, interleaved and mscale are taken (d, heads, strides and types are the
+ *     paged call's; k_new and v_new share kv_stride).
+ *   q [total_q, H, d] -> q_out [total_q, H, d] dense: rows that belong to no sequence are
+ *     left as they were; a token at a negative position is turned by that.  q_out must
+ *     not overlap q unless q is dense and q_out is q.
+ */
+gca_status_t gca_paged_rope_append(const gca_paged_params_t* params, const gca_rope_params_t* rope,
+                                   const void* q, const void* k_new, const void* v_new,
+                                   const int64_t* freqs, const int32_t* cu_q,
+                                   const int32_t* kv_len, const int32_t* table, void* q_out,
+                                   void* k_cache, void* v_cache, void* stream);
+
+/*
+ * Pages.  Which pages of a cache are free, and how many table entries hold each of the
+ * others, is kept in one device array of gca_page_pool_ints() int32: n_pages counts,
+ * a bit a page (set: free; bit p % 32 of word p / 32), and n_pages words of scratch.
+ * The entries below read and write it, the table [B, table_width] and kv_len [B] on the
+ * device only, so captured calls follow their contents.  They keep this state: a page's
+ * count is the number of entries that hold it, entries that hold none are -1, and a
+ * sequence's unfinished last page is held by it alone.  Free pages are taken lowest
+ * first; the results depend on the arguments alone.  One pool, its table and lengths
+ * belong to any number of caches (layers): only the data is moved for each.
+ * Calls on one pool must follow each other.  Limits: B up to 4096, n_pages up to 2^24,
+ * table_width * page up to 2^29, B * table_width below 2^31.
+ */
+typedef struct {
+    int B;                /* sequences (rows of the table)                                  */
+    int page;             /* tokens per page: 16, 32, 64 or 128                             */
+    int n_pages;          /* pages of the cache                                             */
+    int table_width;      /* table entries per sequence                                     */
+    int window, sinks;    /* gca_paged_reserve: as in gca_paged_params_t                    */
+} gca_pages_params_t;
+
+/* int32 words of a pool (0 for n_pages out of range). */
+size_t gca_page_pool_ints(int n_pages);
+
+/* gca_page_pool_init -- all pages free. */
+gca_status_t gca_page_pool_init(int n_pages, int32_t* pool, void* stream);
+
+/*
+ * gca_paged_reserve -- room for the new tokens of a step: before its gca_paged_append and
+ * gca_paged_attn.  kv_len counts the tokens so far and, afterwards, the new ones
+ * (cu_q, as there) too.  For each sequence that has new tokens
+ *   - with a window: entries whose tokens lie behind the sinks and outside the
+ *     first new token's window are let go (-1), from the window downwards as far as
+ *     they hold pages; a page that no entry holds any more is free, for this call too;
+ *   - entries of the new tokens that hold no page get the lowest free ones, in the
+ *     order of the sequences.
+ * A sequence that cannot be served keeps its entries and gets the length -1 - n for its n
+ * tokens: the paged calls leave it out, and the next reservation takes it up again.  That
+ * is one whose entries, with those of the sequences before it, are more than there are
+ * free pages (GCA_ERR_NO_PAGES is recorded), or whose cu_q or length contradicts
+ * itself or passes the table's end (GCA_ERR_DEVICE_INDEX).
+ */
+gca_status_t gca_paged_reserve(const gca_pages_params_t* params, const int32_t* cu_q,
+                               int32_t* kv_len, int32_t* table, int32_t* pool, void* stream);
+
+/*
+ * gca_paged_fork -- every slot b goes on from what slot parent[b] holds, all at once:
+ * parent[b] = b leaves it, another slot's number makes it a copy of that one (a fork, or
+ * beams that change places), -1 empties it.
+ *   Pages are shared; of an unfinished last page the slot itself, or else the first of its
+ *   children, goes on with the page, and the others get a fresh one:
+ *   pairs [B, 2] int32: (page, fresh page) for gca_paged_copy, or -1, -1.
+ *   Pages are let go as in gca_paged_reserve, after fresh ones have been taken from those
+ *   free before.  Where these are too few nothing changes, all pairs are -2, -2
+ *   and GCA_ERR_NO_PAGES is recorded.  A parent outside -1 .. B-1 counts as b itself
+ *   (GCA_ERR_DEVICE_INDEX).
+ */
+gca_status_t gca_paged_fork(const gca_pages_params_t* params, const int32_t* parent,
+                            int32_t* kv_len, int32_t* table, int32_t* pool, int32_t* pairs,
+                            void* stream);
+
+/*
+ * gca_paged_compact -- move pages to the cache's front.  With n pages in use, the
+ * highest one from page n on goes to the lowest hole below, the second to the second, and
+ * so on, up to max_moves of them; table and counts follow.
+ *   pairs [max_moves, 2] int32: (from, to) for gca_paged_copy, unused ones -1, -1.
+ */
+gca_status_t gca_paged_compact(const gca_pages_params_t* params, int max_moves, int32_t* table,
+                               int32_t* pool, int32_t* pairs, void* stream);
+
+/*
+ * gca_paged_copy -- copy pages within a cache, K and V: page pairs[i][0] to page
+ * pairs[i][1] for n pairs (int32, device).  Pairs with a negative number are passed over, those
+ * with one >= n_pages too (GCA_ERR_DEVICE_INDEX).  No page may be a pair's target and
+ * belong to another pair as well: it is left with parts of either.
+ *   page_bytes: of one page of K (or of V), a multiple of 16, up to 2^30.
+ */
+gca_status_t gca_paged_copy(size_t page_bytes, int n_pages, const int32_t* pairs, int n,
+                            void* k_cache, void* v_cache, void* stream);
 
 /*
  * gca_get_status -- synchronise `stream`, then return and clear the device

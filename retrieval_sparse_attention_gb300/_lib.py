@@ -17,7 +17,7 @@ GCA_F32 = 1
 
 STATUS_NAMES = {0: "GCA_OK", 1: "GCA_ERR_INVALID_ARG", 2: "GCA_ERR_UNSUPPORTED",
                 3: "GCA_ERR_WORKSPACE", 4: "GCA_ERR_CUDA", 5: "GCA_ERR_TIMEOUT",
-                6: "GCA_ERR_DEVICE_INDEX"}
+                6: "GCA_ERR_DEVICE_INDEX", 7: "GCA_ERR_NO_PAGES"}
 
 #: every symbol the headers under include/ declare
 EXPORTED = ("gca_score_topk", "gca_fwd", "gca_bwd_workspace_size", "gca_bwd",
@@ -29,7 +29,9 @@ EXPORTED = ("gca_score_topk", "gca_fwd", "gca_bwd_workspace_size", "gca_bwd",
             "gca_swa_sink_fwd_workspace_size", "gca_swa_sink_fwd",
             "gca_swa_sink_bwd_workspace_size", "gca_swa_sink_bwd", "gca_paged_append",
             "gca_paged_attn_workspace_size", "gca_paged_attn", "gca_swa_sink_fwd_scored",
-            "gca_swa_sink_bwd_scored", "gca_paged_attn_scored", "gca_debug_stall_next_decode")
+            "gca_swa_sink_bwd_scored", "gca_paged_attn_scored", "gca_rope", "gca_paged_rope_append",
+            "gca_page_pool_ints", "gca_page_pool_init", "gca_paged_reserve", "gca_paged_fork",
+            "gca_paged_compact", "gca_paged_copy", "gca_debug_stall_next_decode")
 
 
 class GcaParams(ctypes.Structure):
@@ -69,6 +71,22 @@ class GcaPagedParams(ctypes.Structure):
 class GcaScore(ctypes.Structure):
     """Mirror of gca_score_t."""
     _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
+
+
+class GcaRopeParams(ctypes.Structure):
+    """Mirror of gca_rope_params_t."""
+    _fields_ = [("T", ctypes.c_int), ("L", ctypes.c_int), ("start", ctypes.c_int),
+                ("H", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("mscale", ctypes.c_float), ("q_stride", ctypes.c_int),
+                ("k_stride", ctypes.c_int), ("q_out_stride", ctypes.c_int),
+                ("k_out_stride", ctypes.c_int)]
+
+
+class GcaPagesParams(ctypes.Structure):
+    """Mirror of gca_pages_params_t."""
+    _fields_ = [("B", ctypes.c_int), ("page", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("table_width", ctypes.c_int), ("window", ctypes.c_int), ("sinks", ctypes.c_int)]
 
 
 class GcaError(RuntimeError):
@@ -119,6 +137,15 @@ def load() -> ctypes.CDLL:
                                          ctypes.POINTER(GcaScore)] + [vp] * 10 + [sz, vp], i32),
             "gca_paged_attn_scored": ([ctypes.POINTER(GcaPagedParams), ctypes.POINTER(GcaScore)] +
                                       [vp] * 9 + [sz, vp], i32),
+            "gca_rope": ([ctypes.POINTER(GcaRopeParams)] + [vp] * 7, i32),
+            "gca_paged_rope_append": ([ctypes.POINTER(GcaPagedParams),
+                                       ctypes.POINTER(GcaRopeParams)] + [vp] * 11, i32),
+            "gca_page_pool_ints": ([i32], sz),
+            "gca_page_pool_init": ([i32, vp, vp], i32),
+            "gca_paged_reserve": ([ctypes.POINTER(GcaPagesParams)] + [vp] * 5, i32),
+            "gca_paged_fork": ([ctypes.POINTER(GcaPagesParams)] + [vp] * 6, i32),
+            "gca_paged_compact": ([ctypes.POINTER(GcaPagesParams), i32] + [vp] * 4, i32),
+            "gca_paged_copy": ([sz, i32, vp, i32, vp, vp, vp], i32),
             "gca_get_status": ([vp], i32),
             "gca_status_string": ([i32], ctypes.c_char_p),
             "gca_last_launch_count": ([], i32),

@@ -14,13 +14,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import operator
 
 import torch
 
 from . import _lib
-from ._lib import (GCA_BF16, GCA_F32, GcaError, GcaPagedParams, GcaParams, GcaScore, GcaSwaParams,
-                   GcaSwaSinkParams)
+from ._lib import (GCA_BF16, GCA_F32, GcaError, GcaPagedParams, GcaPagesParams, GcaParams,
+                   GcaRopeParams, GcaScore, GcaSwaParams, GcaSwaSinkParams)
 
 _DT = {torch.bfloat16: GCA_BF16, torch.float32: GCA_F32}
 
@@ -179,7 +180,7 @@ def swa_bwd(q, k, v, o, lse, dout, *, window, attn_scale=0.0, workspace=None):
     return dq, dk, dv
 
 
-# --- windowed attention with sinks, and its paged K/V cache ----------------------------
+# --- what the following share ------------------------------------------------------------
 def _token_stride(shape, stride):
     """Elements between consecutive tokens of a [..., tokens, heads, d] tensor whose heads
     are dense and whose batch rows follow each other (a dense tensor, or a slice of a
@@ -235,11 +236,115 @@ def _params(cls, **fields):
     """The C struct; its integers have 32 bits, of which ctypes would keep a larger one's lowest.
     (A call's window, sinks or max_q beyond that are all tokens, as the largest that fits.)"""
     for name, x in fields.items():
-        if name != "attn_scale" and not -_INT_MAX <= operator.index(x) <= _INT_MAX:
+        if name not in ("attn_scale", "mscale") and not -_INT_MAX <= operator.index(x) <= _INT_MAX:
             raise ValueError("%s does not fit 32 bits: %d" % (name, x))
     return cls(**fields)
 
 
+# --- rotary positions ------------------------------------------------------------------
+def rope_table(inv_freq, device="cuda"):
+    """``freqs`` of the rotary calls, [rot/2] int64, from the pairs' angles a position in
+    radians (a tensor or a sequence; taken in 64 bits)."""
+    inv = torch.as_tensor(inv_freq, dtype=torch.float64).detach().cpu()
+    if inv.dim() != 1 or not bool(torch.isfinite(inv).all()):
+        raise ValueError("inv_freq must be finite, one number a pair")
+    turns = inv / (2 * math.pi)
+    part = (turns - turns.round()) * 2.0 ** 64             # -2^63 .. 2^63, the same angle at both ends
+    return torch.where(part >= 2.0 ** 63, -2.0 ** 63, part).to(torch.int64).to(device)
+
+
+def rope_freqs(rot, *, base=10000.0, scaling="none", factor=1.0, trained_len=0, beta_fast=32.0,
+               beta_slow=1.0, device="cuda"):
+    """``freqs`` for f_i = base^(-2i/rot), or for contexts ``factor`` times as long:
+    "linear": f_i / factor;
+    "ntk": base * factor^(rot/(rot-2)), which leaves the fastest pair and divides the slowest's;
+    "yarn": pairs that turn at least ``beta_fast`` times over ``trained_len`` positions stay,
+    those that turn ``beta_slow`` times or less are divided, between them a mixture, linear in the
+    logarithm of the turns (the queries' and keys' usual factor for it, 1 + 0.1 ln(factor),
+    is the calls' ``mscale``)."""
+    rot = operator.index(rot)
+    if rot < 4 or rot % 2 or not (base > 1 and factor > 0):
+        raise ValueError("rot must be even, from 4 on, base above 1 and factor above 0")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError("scaling must be none, linear, ntk or yarn")
+    if scaling == "ntk":
+        base = base * factor ** (rot / (rot - 2))
+    inv = float(base) ** -(torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        if trained_len < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn needs trained_len and beta_fast > beta_slow > 0")
+        turns = trained_len * inv / (2 * math.pi)
+        keep = (torch.log(turns / beta_slow) / math.log(beta_fast / beta_slow)).clamp(0, 1)
+        inv = inv * keep + inv / factor * (1 - keep)
+    return rope_table(inv, device)
+
+
+def gca_rope(params: GcaRopeParams, q, k, freqs, positions, q_out, k_out, stream=None):
+    _check("gca_rope", _lib.load().gca_rope(
+        ctypes.byref(params), _ptr(q), _ptr(k), _ptr(freqs), _ptr(positions), _ptr(q_out), _ptr(k_out),
+        _raw_stream(stream, freqs.get_device())))
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_plan(qs, qst, ks, kst, qt, kt, pairs, pos, start, interleaved, mscale, inverse, inplace):
+    """What a call derives from its arguments' shapes, strides and types alone."""
+    lead, d = (qs or ks)[:-2], (qs or ks)[-1]
+    if len(lead) not in (1, 2) or (qs and ks and (ks[:-2] != lead or ks[-1] != d)):
+        raise ValueError("q must be [T, H, d] or [B, L, H, d], k the same with its own heads")
+    if qt is not None and kt is not None and qt != kt:
+        raise TypeError("q and k must have one dtype")
+    if pos is not None and tuple(pos) != tuple(lead):
+        raise ValueError("positions must be like q's tokens, %s" % (tuple(lead),))
+    H, Hkv = qs[-2] if qs else 0, ks[-2] if ks else 0
+    # (tensors without tokens have strides of no meaning)
+    a, b = (_token_stride(x, st) if x and math.prod(lead) else 0 for x, st in ((qs, qst), (ks, kst)))
+    L = lead[-1]
+    return _params(GcaRopeParams, T=math.prod(lead), L=max(L, 1), start=start, H=H, Hkv=Hkv, d=d,
+                   rot=2 * pairs, interleaved=interleaved, inverse=inverse,
+                   dtype=dtype_code(qt if qt is not None else kt), mscale=mscale, q_stride=a, k_stride=b,
+                   q_out_stride=a if inplace else 0, k_out_stride=b if inplace else 0)
+
+
+def _rope_freqs(freqs):
+    if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous int64 tensor [rot/2], as from rope_freqs")
+    return freqs.shape[0]
+
+
+def _rope(q, k, freqs, positions, start, interleaved, mscale, inplace, inverse):
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
+    _same_device(freqs, q, k, positions)
+    if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 tensor")
+    p = _rope_plan(None if q is None else q.shape, None if q is None else q.stride(),
+                   None if k is None else k.shape, None if k is None else k.stride(),
+                   None if q is None else q.dtype, None if k is None else k.dtype, _rope_freqs(freqs),
+                   None if positions is None else positions.shape, operator.index(start),
+                   bool(interleaved), float(mscale), inverse, bool(inplace))
+    qo = q if inplace or q is None else _empty_like(q)
+    ko = k if inplace or k is None else _empty_like(k)
+    gca_rope(p, q, k, freqs, positions, qo, ko)
+    return qo, ko
+
+
+def rope(q, k, freqs, *, positions=None, start=0, interleaved=False, mscale=1.0, inplace=False):
+    """Rotary positions: q [B, L, H, d] (or [T, H, d]), k [B, L, Hkv, d], either None; token
+    strides may be those of a packed projection -> the turned (q, k), dense, or q and k
+    themselves with ``inplace``.  Tokens are at ``positions`` ([B, L] or [T], int32), or at
+    start, start + 1, ...  The first 2 * len(freqs) columns of a head turn (``rope_freqs``), in
+    pairs of columns half of that apart or of neighbours (``interleaved``)."""
+    return _rope(q, k, freqs, positions, start, interleaved, mscale, inplace, False)
+
+
+def rope_bwd(dq, dk, freqs, *, positions=None, start=0, interleaved=False, mscale=1.0, inplace=False):
+    """Gradients of ``rope`` into its arguments, from those of its results."""
+    return _rope(dq, dk, freqs, positions, start, interleaved, mscale, inplace, True)
+
+
+# --- windowed attention with sinks ------------------------------------------------------
 def make_swa_sink_params(*, B, L, H, d, window, Hkv=None, sinks=0, dtype=torch.bfloat16,
                          attn_scale=0.0, q_stride=0, kv_stride=0) -> GcaSwaSinkParams:
     return _params(GcaSwaSinkParams, B=B, L=L, H=H, Hkv=H if Hkv is None else Hkv, d=d, window=window,
@@ -484,6 +589,180 @@ def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, s
     else:
         gca_paged_attn_scored(p, score, q, k_cache, v_cache, cu_q, kv_len, table, out, lse, ws)
     return out, lse
+
+
+def gca_paged_rope_append(params: GcaPagedParams, rope: GcaRopeParams, q, k_new, v_new, freqs, cu_q,
+                          kv_len, table, q_out, k_cache, v_cache, stream=None):
+    _check("gca_paged_rope_append", _lib.load().gca_paged_rope_append(
+        ctypes.byref(params), ctypes.byref(rope), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(freqs),
+        _ptr(cu_q), _ptr(kv_len), _ptr(table), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+        _raw_stream(stream, k_cache.get_device())))
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_rope_plan(qs, qst, ks, kst, vs, vst, cache, v_cache, table, cu_q, kv_len, qt, kt, vt, k_dt,
+                     v_dt, pairs, max_q, interleaved, mscale):
+    if qt != kt or vt != kt:
+        raise TypeError("q, k_new and v_new must have one dtype")
+    if len(qs) != 3 or len(ks) != 3 or ks != vs or qs[0] != ks[0] or qs[2] != ks[2]:
+        raise ValueError("q must be [T, H, d] and k_new, v_new [T, Hkv, d]")
+    p, _ = _paged_plan.__wrapped__(ks, kst, cache, v_cache, table, cu_q, kv_len, kt, k_dt, v_dt, False,
+                                   max_q, 0, 0, 0.0)
+    if _token_stride(vs, vst) != p.kv_stride:
+        raise ValueError("k_new and v_new must have one token stride")
+    p.H, p.q_stride = qs[1], _token_stride(qs, qst)
+    return p, _params(GcaRopeParams, T=ks[0], L=1, start=0, H=qs[1], Hkv=ks[1], d=ks[2], rot=2 * pairs,
+                      interleaved=interleaved, inverse=0, dtype=dtype_code(kt), mscale=mscale,
+                      q_stride=0, k_stride=0, q_out_stride=0, k_out_stride=0)
+
+
+def paged_rope_append(q, k_new, v_new, freqs, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0,
+                      interleaved=False, mscale=1.0, out=None):
+    """paged_append of keys turned by their positions (``rope``), and the new tokens' queries
+    q [T, H, d] turned by theirs -> q' [T, H, d] (``out`` supplies it; rows behind cu_q[B] are left
+    as they were)."""
+    _same_device(k_cache, v_cache, table, cu_q, kv_len, q, k_new, v_new, freqs, out)
+    if type(max_q) is not int:
+        max_q = operator.index(max_q)
+    _paged_ints(table, cu_q, kv_len)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous")
+    p, r = _paged_rope_plan(q.shape, q.stride(), k_new.shape, k_new.stride(), v_new.shape, v_new.stride(),
+                            k_cache.shape, v_cache.shape, table.shape, cu_q.shape, kv_len.shape, q.dtype,
+                            k_new.dtype, v_new.dtype, k_cache.dtype, v_cache.dtype, _rope_freqs(freqs),
+                            max_q, bool(interleaved), float(mscale))
+    if out is None:
+        out = _empty_like(q)
+    else:
+        _dense(out, q.shape, q.dtype, "out")
+    gca_paged_rope_append(p, r, q, k_new, v_new, freqs, cu_q, kv_len, table, out, k_cache, v_cache)
+    return out
+
+
+# --- the pages of a paged cache ----------------------------------------------------------
+def gca_page_pool_ints(n_pages: int) -> int:
+    return int(_lib.load().gca_page_pool_ints(n_pages))
+
+
+def gca_page_pool_init(n_pages, pool, stream=None):
+    _check("gca_page_pool_init", _lib.load().gca_page_pool_init(n_pages, _ptr(pool),
+                                                                _raw_stream(stream, pool.get_device())))
+
+
+def gca_paged_reserve(params: GcaPagesParams, cu_q, kv_len, table, pool, stream=None):
+    _check("gca_paged_reserve", _lib.load().gca_paged_reserve(
+        ctypes.byref(params), _ptr(cu_q), _ptr(kv_len), _ptr(table), _ptr(pool),
+        _raw_stream(stream, pool.get_device())))
+
+
+def gca_paged_fork(params: GcaPagesParams, parent, kv_len, table, pool, pairs, stream=None):
+    _check("gca_paged_fork", _lib.load().gca_paged_fork(
+        ctypes.byref(params), _ptr(parent), _ptr(kv_len), _ptr(table), _ptr(pool), _ptr(pairs),
+        _raw_stream(stream, pool.get_device())))
+
+
+def gca_paged_compact(params: GcaPagesParams, max_moves, table, pool, pairs, stream=None):
+    _check("gca_paged_compact", _lib.load().gca_paged_compact(
+        ctypes.byref(params), max_moves, _ptr(table), _ptr(pool), _ptr(pairs),
+        _raw_stream(stream, pool.get_device())))
+
+
+def gca_paged_copy(page_bytes, n_pages, pairs, n, k_cache, v_cache, stream=None):
+    _check("gca_paged_copy", _lib.load().gca_paged_copy(
+        page_bytes, n_pages, _ptr(pairs), n, _ptr(k_cache), _ptr(v_cache),
+        _raw_stream(stream, k_cache.get_device())))
+
+
+def page_pool(n_pages, device="cuda"):
+    """The pages of a new cache, all free: what the calls below keep."""
+    n = operator.index(n_pages)
+    ints = gca_page_pool_ints(n) if 0 < n <= _INT_MAX else 0
+    if ints == 0:
+        raise ValueError("n_pages must be 1 .. 2^24")
+    pool = torch.empty(ints, dtype=torch.int32, device=device)
+    with torch.cuda.device(pool.device):
+        gca_page_pool_init(n, pool)
+    return pool
+
+
+@functools.lru_cache(maxsize=256)
+def _pages_plan(table, kv_len, ints, page, window, sinks):
+    if len(table) != 2 or (kv_len is not None and tuple(kv_len) != (table[0],)):
+        raise ValueError("table must be [B, table_width] and kv_len [B]")
+    n = ints * 32 // 65                                    # ints = 2 n + ceil(n / 32)
+    if 2 * n + -(-n // 32) != ints or n < 1:
+        raise ValueError("pool must be what page_pool returned")
+    return _params(GcaPagesParams, B=table[0], page=page, n_pages=n, table_width=table[1],
+                   window=min(window, _INT_MAX), sinks=min(sinks, _INT_MAX))
+
+
+def _paged_ints(*ts):
+    for t in ts:
+        if t.dtype != torch.int32:
+            raise TypeError("table, pool, pairs, parent, cu_q and kv_len must be int32")
+        if not t.is_contiguous():
+            raise ValueError("table, pool, pairs, parent, cu_q and kv_len must be contiguous")
+
+
+def _pages_args(table, kv_len, pool, page, window=0, sinks=0):
+    return _pages_plan(table.shape, None if kv_len is None else kv_len.shape, pool.numel(),
+                       operator.index(page), operator.index(window), operator.index(sinks))
+
+
+def paged_reserve(table, cu_q, kv_len, pool, *, page, window=0, sinks=0):
+    """Room for a step's new tokens, in place: with a window, pages that left it are let go; the
+    entries of the new tokens get pages; kv_len counts the new tokens afterwards, as the step's
+    paged_append and paged_attn take it (-1 - n for n tokens that could not grow)."""
+    _same_device(pool, table, cu_q, kv_len)
+    _paged_ints(table, cu_q, kv_len, pool)
+    p = _pages_args(table, kv_len, pool, page, window, sinks)
+    if cu_q.shape != (p.B + 1,):
+        raise ValueError("cu_q must be [%d]" % (p.B + 1))
+    gca_paged_reserve(p, cu_q, kv_len, table, pool)
+
+
+def paged_fork(table, kv_len, parent, pool, *, page):
+    """Every slot goes on from what slot parent[b] holds (b itself: unchanged; -1: empty), in
+    place -> pairs [B, 2] of pages for paged_copy, which each cache (layer) needs before its next use."""
+    _same_device(pool, table, kv_len, parent)
+    _paged_ints(table, kv_len, parent, pool)
+    p = _pages_args(table, kv_len, pool, page)
+    if parent.shape != (p.B,):
+        raise ValueError("parent must be [%d]" % p.B)
+    pairs = torch.empty((p.B, 2), dtype=torch.int32, device=pool.device)
+    gca_paged_fork(p, parent, kv_len, table, pool, pairs)
+    return pairs
+
+
+def paged_compact(table, pool, *, max_moves):
+    """Move up to max_moves pages to the cache's front (table and counts, in place) -> pairs
+    [max_moves, 2] of pages for paged_copy, which each cache (layer) needs before its next use."""
+    _same_device(pool, table)
+    _paged_ints(table, pool)
+    p = _pages_args(table, None, pool, 16)                 # (a page's tokens do not matter)
+    n = operator.index(max_moves)
+    if not 1 <= n <= 1 << 24:
+        raise ValueError("max_moves must be 1 .. 2^24")
+    pairs = torch.empty((n, 2), dtype=torch.int32, device=pool.device)
+    gca_paged_compact(p, n, table, pool, pairs)
+    return pairs
+
+
+def paged_copy(k_cache, v_cache, pairs):
+    """Copy pages of one cache, K and V in place: page pairs[i, 0] to page pairs[i, 1] (int32 [n, 2]
+    on the device; negative: no copy)."""
+    _same_device(k_cache, v_cache, pairs)
+    _paged_ints(pairs)
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n, 2]")
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or not (
+            k_cache.is_contiguous() and v_cache.is_contiguous()) or k_cache.dim() < 2:
+        raise ValueError("the caches must be contiguous, [n_pages, ...] and alike")
+    n_pages = k_cache.shape[0]
+    if n_pages > _INT_MAX or pairs.shape[0] > _INT_MAX:
+        raise ValueError("too many pages")
+    gca_paged_copy(k_cache.numel() // max(n_pages, 1) * k_cache.element_size(), n_pages, pairs,
+                   pairs.shape[0], k_cache, v_cache)
 
 
 def gather_chunks(cache_k, cache_v, idx):

@@ -147,6 +147,7 @@ const char* gca_status_string(gca_status_t s) {
         case GCA_ERR_CUDA: return "GCA_ERR_CUDA";
         case GCA_ERR_TIMEOUT: return "GCA_ERR_TIMEOUT";
         case GCA_ERR_DEVICE_INDEX: return "GCA_ERR_DEVICE_INDEX";
+        case GCA_ERR_NO_PAGES: return "GCA_ERR_NO_PAGES";
     }
     return "GCA_ERR_UNKNOWN";
 }
@@ -492,6 +493,194 @@ gca_status_t gca_paged_attn_scored(const gca_paged_params_t* params, const gca_s
     r = from_cuda(launch_sink_fwd(s, q, k_cache, v_cache, cu_q, kv_len, table, o, lse, workspace, st,
                                   static_cast<cudaStream_t>(stream), &n));
     if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+namespace {
+// One tensor's token stride: whole 16-byte vectors, no shorter than a token.
+bool rope_stride(int given, int heads, int d, int* out) {
+    *out = given ? given : heads * d;
+    return given >= 0 && (heads == 0 || (*out >= heads * d && *out % 8 == 0));
+}
+
+gca_status_t rope_columns(const gca_rope_params_t* p, int d, RopeShape* s) {
+    if (p->rot < 1 || p->rot > d || !(p->mscale >= 0.f) || isinf(p->mscale)) return GCA_ERR_INVALID_ARG;
+    if (p->rot % 16 != 0) return GCA_ERR_UNSUPPORTED;
+    s->rot = p->rot;
+    s->interleaved = p->interleaved != 0;
+    s->inverse = p->inverse != 0;
+    s->mscale = p->mscale > 0.f ? p->mscale : 1.f;
+    return GCA_OK;
+}
+
+gca_status_t rope_check(const gca_rope_params_t* p, bool positions, RopeShape* out) {
+    if (!p) return GCA_ERR_INVALID_ARG;
+    RopeShape s{};
+    if (p->T < 0 || p->H < 0 || p->Hkv < 0 || p->H + (long long)p->Hkv < 1 || p->d < 1) return GCA_ERR_INVALID_ARG;
+    if (p->dtype != GCA_BF16 && p->dtype != GCA_F32) return GCA_ERR_INVALID_ARG;
+    if (!positions && (p->L < 1 || p->start < 0 || (long long)p->start + p->L > 0x7fffffffll)) return GCA_ERR_INVALID_ARG;
+    if ((p->d != 32 && p->d != 64 && p->d != 128 && p->d != 256) || p->H > 4096 || p->Hkv > 4096) return GCA_ERR_UNSUPPORTED;
+    s.T = p->T; s.L = positions ? 1 : p->L; s.start = p->start;
+    s.H = p->H; s.Hkv = p->Hkv; s.d = p->d;
+    s.dtype = p->dtype;
+    if (!rope_stride(p->q_stride, p->H, p->d, &s.q_stride) || !rope_stride(p->k_stride, p->Hkv, p->d, &s.k_stride) ||
+        !rope_stride(p->q_out_stride, p->H, p->d, &s.qo_stride) || !rope_stride(p->k_out_stride, p->Hkv, p->d, &s.ko_stride))
+        return GCA_ERR_INVALID_ARG;
+    if (s.q_stride > (1 << 24) || s.k_stride > (1 << 24) || s.qo_stride > (1 << 24) || s.ko_stride > (1 << 24))
+        return GCA_ERR_UNSUPPORTED;
+    const long long units = ((long long)(s.H + s.Hkv) * (s.d / 16) + 127) / 128;
+    if (s.T * units > 0x7fffffffll) return GCA_ERR_UNSUPPORTED;
+    const gca_status_t r = rope_columns(p, p->d, &s);
+    if (r == GCA_OK) *out = s;
+    return r;
+}
+
+constexpr int kMaxPoolPages = 1 << 24;
+
+gca_status_t pages_check(const gca_pages_params_t* p, PageShape* out) {
+    if (!p || p->B < 1 || p->n_pages < 1 || p->table_width < 1 || p->page < 1 || p->window < 0 || p->sinks < 0)
+        return GCA_ERR_INVALID_ARG;
+    if ((p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) || p->B > 4096 || p->n_pages > kMaxPoolPages ||
+        (long long)p->table_width * p->page > kNoWindow / 2 || (long long)p->B * p->table_width >= (1ll << 31))
+        return GCA_ERR_UNSUPPORTED;
+    PageShape s{};
+    s.B = p->B; s.page = p->page; s.n_pages = p->n_pages; s.width = p->table_width;
+    s.W = p->window; s.ns = p->sinks;
+    *out = s;
+    return GCA_OK;
+}
+}  // namespace
+
+gca_status_t gca_rope(const gca_rope_params_t* params, const void* q, const void* k,
+                      const int64_t* freqs, const int32_t* positions, void* q_out, void* k_out,
+                      void* stream) {
+    RopeShape s;
+    gca_status_t r = rope_check(params, positions != nullptr, &s);
+    if (r != GCA_OK) return r;
+    if (s.T == 0) {
+        t_launches = 0;
+        return GCA_OK;
+    }
+    if ((r = check_ptrs({freqs})) != GCA_OK) return r;
+    if (s.H && (r = check_ptrs({q, q_out})) != GCA_OK) return r;
+    if (s.Hkv && (r = check_ptrs({k, k_out})) != GCA_OK) return r;
+    if (positions && !aligned16(positions)) return GCA_ERR_INVALID_ARG;
+    int n = 0;
+    r = from_cuda(launch_rope(s, q, k, freqs, positions, q_out, k_out, static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+gca_status_t gca_paged_rope_append(const gca_paged_params_t* params, const gca_rope_params_t* rope,
+                                   const void* q, const void* k_new, const void* v_new,
+                                   const int64_t* freqs, const int32_t* cu_q,
+                                   const int32_t* kv_len, const int32_t* table, void* q_out,
+                                   void* k_cache, void* v_cache, void* stream) {
+    SinkShape s;
+    RopeShape rs{};
+    gca_status_t r = paged_check(params, false, &s);
+    if (r != GCA_OK) return r;
+    if (!rope || params->H < 1) return GCA_ERR_INVALID_ARG;
+    if ((r = rope_columns(rope, s.d, &rs)) != GCA_OK) return r;
+    if (rs.inverse) return GCA_ERR_UNSUPPORTED;
+    const long long units = ((long long)(s.H + 2 * s.Hkv) * (s.d / 16) + 127) / 128;
+    if (s.T * units > 0x7fffffffll) return GCA_ERR_UNSUPPORTED;
+    if (s.T == 0) {
+        t_launches = 0;
+        return GCA_OK;
+    }
+    if ((r = check_ptrs({q, k_new, v_new, freqs, cu_q, kv_len, table, q_out, k_cache, v_cache})) != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    int n = 0;
+    r = from_cuda(launch_paged_rope_append(s, rs, q, k_new, v_new, freqs, cu_q, kv_len, table, q_out, k_cache,
+                                           v_cache, st, static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+size_t gca_page_pool_ints(int n_pages) {
+    if (n_pages < 1 || n_pages > kMaxPoolPages) return 0;
+    return 2 * (size_t)n_pages + (n_pages + 31) / 32;
+}
+
+gca_status_t gca_page_pool_init(int n_pages, int32_t* pool, void* stream) {
+    if (n_pages < 1) return GCA_ERR_INVALID_ARG;
+    if (n_pages > kMaxPoolPages) return GCA_ERR_UNSUPPORTED;
+    gca_status_t r = check_ptrs({pool});
+    if (r != GCA_OK) return r;
+    PageShape s{};
+    s.n_pages = n_pages;
+    s.pool = pool;
+    int n = 0;
+    r = from_cuda(launch_pool_init(s, static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+gca_status_t gca_paged_reserve(const gca_pages_params_t* params, const int32_t* cu_q,
+                               int32_t* kv_len, int32_t* table, int32_t* pool, void* stream) {
+    PageShape s;
+    gca_status_t r = pages_check(params, &s);
+    if (r != GCA_OK) return r;
+    if ((r = check_ptrs({cu_q, kv_len, table, pool})) != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    s.pool = pool;
+    int n = 0;
+    r = from_cuda(launch_paged_reserve(s, cu_q, kv_len, table, st, static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+gca_status_t gca_paged_fork(const gca_pages_params_t* params, const int32_t* parent,
+                            int32_t* kv_len, int32_t* table, int32_t* pool, int32_t* pairs,
+                            void* stream) {
+    PageShape s;
+    gca_status_t r = pages_check(params, &s);
+    if (r != GCA_OK) return r;
+    if ((r = check_ptrs({parent, kv_len, table, pool, pairs})) != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    s.pool = pool;
+    int n = 0;
+    r = from_cuda(launch_paged_fork(s, parent, kv_len, table, pairs, st, static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+gca_status_t gca_paged_compact(const gca_pages_params_t* params, int max_moves, int32_t* table,
+                               int32_t* pool, int32_t* pairs, void* stream) {
+    PageShape s;
+    gca_status_t r = pages_check(params, &s);
+    if (r != GCA_OK) return r;
+    if (max_moves < 1) return GCA_ERR_INVALID_ARG;
+    if (max_moves > kMaxPoolPages) return GCA_ERR_UNSUPPORTED;
+    if ((r = check_ptrs({table, pool, pairs})) != GCA_OK) return r;
+    s.pool = pool;
+    int n = 0;
+    r = from_cuda(launch_paged_compact(s, max_moves, table, pairs, static_cast<cudaStream_t>(stream), &n));
+    if (r == GCA_OK) t_launches = n;
+    return r;
+}
+
+gca_status_t gca_paged_copy(size_t page_bytes, int n_pages, const int32_t* pairs, int n,
+                            void* k_cache, void* v_cache, void* stream) {
+    if (page_bytes == 0 || page_bytes % 16 != 0 || n_pages < 1 || n < 0) return GCA_ERR_INVALID_ARG;
+    const long long pieces = (long long)((page_bytes + 16383) / 16384);
+    if (page_bytes > (1u << 30) || 2 * pieces * n > 0x7fffffffll) return GCA_ERR_UNSUPPORTED;
+    if (n == 0) {
+        t_launches = 0;
+        return GCA_OK;
+    }
+    gca_status_t r = check_ptrs({pairs, k_cache, v_cache});
+    if (r != GCA_OK) return r;
+    int* st = status_word();
+    if (!st) return GCA_ERR_CUDA;
+    int c = 0;
+    r = from_cuda(launch_paged_copy(page_bytes, n_pages, pairs, n, k_cache, v_cache, st,
+                                    static_cast<cudaStream_t>(stream), &c));
+    if (r == GCA_OK) t_launches = c;
     return r;
 }
 

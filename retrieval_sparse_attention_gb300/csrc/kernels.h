@@ -157,6 +157,40 @@ cudaError_t launch_paged_append(const SinkShape& s, const void* k_new, const voi
                                 void* k_cache, void* v_cache, int* status, cudaStream_t st,
                                 int* launches);
 
+// Rotary positions.
+struct RopeShape {
+    int T, L, start;              // tokens; position start + t % L where the call gives none
+    int H, Hkv, d, rot;
+    int interleaved, inverse;
+    int q_stride, k_stride, qo_stride, ko_stride;   // elements between consecutive tokens
+    gca_dtype_t dtype;
+    float mscale;
+};
+cudaError_t launch_rope(const RopeShape& s, const void* q, const void* k, const int64_t* freqs,
+                        const int32_t* positions, void* q_out, void* k_out, cudaStream_t st,
+                        int* launches);
+// (of r: rot, interleaved and mscale)
+cudaError_t launch_paged_rope_append(const SinkShape& s, const RopeShape& r, const void* q, const void* k_new,
+                                     const void* v_new, const int64_t* freqs, const int32_t* cu_q,
+                                     const int32_t* kv_len, const int32_t* table, void* q_out, void* k_cache,
+                                     void* v_cache, int* status, cudaStream_t st, int* launches);
+
+// The pages of a paged cache: counts, free bits and scratch words in one array.
+struct PageShape {
+    int B, page, n_pages, width, W, ns;       // W = 0: no window
+    int32_t* pool;
+    int words() const { return (n_pages + 31) / 32; }
+};
+cudaError_t launch_pool_init(const PageShape& s, cudaStream_t st, int* launches);
+cudaError_t launch_paged_reserve(const PageShape& s, const int32_t* cu_q, int32_t* kv_len, int32_t* table,
+                                 int* status, cudaStream_t st, int* launches);
+cudaError_t launch_paged_fork(const PageShape& s, const int32_t* parent, int32_t* kv_len, int32_t* table,
+                              int32_t* pairs, int* status, cudaStream_t st, int* launches);
+cudaError_t launch_paged_compact(const PageShape& s, int max_moves, int32_t* table, int32_t* pairs,
+                                 cudaStream_t st, int* launches);
+cudaError_t launch_paged_copy(size_t page_bytes, int n_pages, const int32_t* pairs, int n, void* k_cache,
+                              void* v_cache, int* status, cudaStream_t st, int* launches);
+
 cudaError_t launch_synth_fill(void* dst, size_t n, gca_dtype_t dt, uint64_t seed, uint64_t tid,
                               uint64_t first, cudaStream_t st);
 

@@ -7,9 +7,7 @@ namespace gca {
 namespace {
 
 // One warp per row of the token tensors: the lanes look for the sequence that the row belongs
-// to, 32 at a time, first where it is if all have equally many tokens, then from the first
-// on (a token each of 2000 sequences: 3.6 us, without the guess 17.3); then they copy the row's 16-byte
-// vectors, four of K and of V in flight each.  Bound by memory: reads and writes every new
+// to, then they copy the row's 16-byte vectors, four of K and of V in flight each.  Bound by memory: reads and writes every new
 // row once (four prompts of 16K, 8 heads of 128: 77 us, 6.8 TB/s; eight chunks of 0.9-2K, 12 heads
 // of 64: 16 us with cold caches, 8.6 with warm ones).  A warp for each of the first max_q
 // tokens of every sequence, without the search, took 20 us for the chunks; two or four rows a
@@ -23,19 +21,8 @@ paged_append_kernel(PagedArgs p, const uint4* k_new, const uint4* v_new, int src
     for (long long b = tid; b < B; b += (long long)gridDim.x * blockDim.x) paged_seq(p, (int)b, status);
     if (tid >> 5 >= p.T) return;
     const int row = (int)(tid >> 5);
-    int seq = -1, pos = 0;
-    const int guess = max(min(static_cast<int>(static_cast<long long>(row) * B / p.T) - 16, B - 32), 0);
-    for (int k = -32; k < B && seq < 0; k += 32) {
-        const int b0 = k < 0 ? guess : k;
-        SeqInfo s{0, 0, 0};
-        if (b0 + lane < B) s = paged_seq(p, b0 + lane, nullptr);
-        const unsigned hit = __ballot_sync(0xffffffffu, row >= s.row0 && row < s.row0 + s.n);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            seq = b0 + l;
-            pos = __shfl_sync(0xffffffffu, s.pos0 + row - s.row0, l);
-        }
-    }
+    int pos = 0;
+    const int seq = seq_of_row(p, B, row, &pos);
     if (seq < 0 || pos < 0) return;
     const int pg = p.table[(size_t)seq * p.width + (pos >> p.page_log2)];
     if (pg < 0 || pg >= p.n_pages) {

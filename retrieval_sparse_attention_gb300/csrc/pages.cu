@@ -1,0 +1,447 @@
+// pages.cu -- the pages of the paged K/V cache: reservation for new tokens, forks of
+// sequences, compaction (whole numbers on tables and counts), and the copy of pages.
+//
+// The pool: refs[n], how many table entries hold a page; a bit a page, set while none does;
+// and n scratch words.  Free pages are taken lowest first, so results depend on the
+// arguments alone, whatever order the counts fell in.
+//
+// Reservation, and what a fork or a compaction decides, are one CTA's work: a few thousand
+// numbers and a bit a page, all of it latency.  Tables are then rewritten by as
+// many CTAs as their entries need.  Pages are copied at the memory's rate.
+#include "attn_sink.cuh"
+#include "kernels.h"
+
+namespace gca {
+namespace {
+
+constexpr int kThreads = 1024;           // of the CTA that decides
+constexpr int kMaxSeqs = 4096;           // (api.cu checks)
+
+struct PageArgs {
+    int32_t *refs, *list;
+    uint32_t* words;
+    int n, n_words;
+    int B, width, page_log2, W, ns;
+    int32_t* table;
+    int* status;
+};
+
+PageArgs page_args(const PageShape& s, int32_t* table, int* status) {
+    PageArgs a{};
+    a.refs = s.pool;
+    a.words = reinterpret_cast<uint32_t*>(s.pool + s.n_pages);
+    a.list = s.pool + s.n_pages + s.words();
+    a.n = s.n_pages; a.n_words = s.words();
+    a.B = s.B; a.width = s.width; a.page_log2 = s.page ? __builtin_ctz(s.page) : 0; a.W = s.W; a.ns = s.ns;
+    a.table = table;
+    a.status = status;
+    return a;
+}
+
+// Changes the count of page e by delta; where that leaves none, the page is free.
+__device__ __forceinline__ void count_page(const PageArgs& a, int e, int delta) {
+    if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.n)) {
+        set_status(a.status, GCA_ERR_DEVICE_INDEX);
+        return;
+    }
+    if (atomicAdd(a.refs + e, delta) + delta == 0) atomicOr(a.words + (e >> 5), 1u << (e & 31));
+}
+
+// Word w of the free bits, as the last writer of this launch or an earlier one left it.
+__device__ __forceinline__ uint32_t free_word(const PageArgs& a, int w) {
+    const uint32_t x = __ldcg(a.words + w);
+    return w == a.n_words - 1 && (a.n & 31) ? x & ((1u << (a.n & 31)) - 1) : x;
+}
+
+// Sum of v over the threads before this one, and over all (all kThreads threads).
+__device__ __forceinline__ int block_scan(int v, int* wsum, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    __syncthreads();                     // (wsum may still be read from the last scan)
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int x = wsum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    total = __shfl_sync(0xffffffffu, x, 31);
+    const int before = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
+    return inc - v + (warp ? before : 0);
+}
+
+// This thread's run of the n items that all threads share.
+__device__ __forceinline__ void run_of(int n, int& i0, int& i1) {
+    const int per = (n + kThreads - 1) / kThreads;
+    i0 = min(n, static_cast<int>(threadIdx.x) * per);
+    i1 = min(n, i0 + per);
+}
+
+// The `want` lowest free pages to list[0 ..], ascending; returns how many there are of them.
+__device__ __forceinline__ int lowest_free(const PageArgs& a, int want, int* wsum) {
+    int w0, w1, mine = 0, total;
+    run_of(a.n_words, w0, w1);
+    for (int w = w0; w < w1; ++w) mine += __popc(free_word(a, w));
+    int r = block_scan(mine, wsum, total);
+    for (int w = w0; w < w1 && r < want; ++w)
+        for (uint32_t x = free_word(a, w); x && r < want; x &= x - 1) a.list[r++] = 32 * w + __ffs(x) - 1;
+    __syncthreads();
+    return min(want, total);
+}
+
+__device__ __forceinline__ void take_page(const PageArgs& a, int e) {
+    atomicAnd(a.words + (e >> 5), ~(1u << (e & 31)));
+    a.refs[e] = 1;
+}
+
+__global__ void __launch_bounds__(256) pool_init_kernel(PageArgs a) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < a.n) a.refs[i] = 0;
+    if (i < a.n) a.list[i] = 0;
+    if (i < a.n_words) a.words[i] = i == a.n_words - 1 && (a.n & 31) ? (1u << (a.n & 31)) - 1 : 0xffffffffu;
+}
+
+// ---------------------------------------------------------------------------
+// Reservation.  A warp per sequence lets go of the pages behind its window and counts the
+// entries that its new tokens lack; a scan over the sequences and one over the free
+// bits give every lacking entry its page.
+// ---------------------------------------------------------------------------
+struct Reserve {
+    int old, add;            // tokens before, new ones
+    int e0, e1;              // table entries of the new tokens
+    bool bad;                // contradicting, or past the table's end
+};
+__device__ __forceinline__ Reserve reserve_of(const PageArgs& a, const int32_t* cu_q, const int32_t* kv_len, int b) {
+    const int c0 = cu_q[b], c1 = cu_q[b + 1], kv = kv_len[b];
+    Reserve r;
+    r.old = kv < 0 ? ~kv : kv;
+    const long long add = (long long)c1 - c0, cap = (long long)a.width << a.page_log2;
+    r.bad = c0 < 0 || add < 0 || r.old + add > cap;
+    r.add = r.bad ? 0 : static_cast<int>(add);
+    r.e0 = r.old >> a.page_log2;
+    r.e1 = r.add ? ((r.old + r.add - 1) >> a.page_log2) + 1 : r.e0;
+    return r;
+}
+
+__global__ void __launch_bounds__(kThreads) paged_reserve_kernel(const PageArgs a, const int32_t* cu_q, int32_t* kv_len) {
+    __shared__ int end[kMaxSeqs];        // entries that the sequences up to this one lack
+    __shared__ int wsum[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int b = warp; b < a.B; b += kThreads / 32) {
+        const Reserve r = reserve_of(a, cu_q, kv_len, b);
+        int32_t* row = a.table + (size_t)b * a.width;
+        if (a.W && r.add) {
+            // whole entries that no token from `old` on sees, downwards as far as they hold pages
+            const int lo = (int)(((long long)a.ns + (1 << a.page_log2) - 1) >> a.page_log2);
+            int hi = max(0, r.old - a.W + 1) >> a.page_log2;
+            while (hi > lo) {
+                const int i = hi - 1 - lane;
+                const int e = i >= lo ? row[i] : -1;
+                const unsigned stop = __ballot_sync(0xffffffffu, e < 0);
+                const int n = stop ? __ffs(stop) - 1 : 32;
+                if (lane < n) {
+                    row[i] = -1;
+                    count_page(a, e, -1);
+                }
+                hi -= 32;
+                if (n < 32) break;
+            }
+            __syncwarp();
+        }
+        int need = 0;
+        for (int i = r.e0 + lane; i < r.e1; i += 32) need += row[i] < 0;
+        need = __reduce_add_sync(0xffffffffu, need);
+        if (lane == 0) end[b] = need;
+    }
+    __syncthreads();
+    int b0, b1, mine = 0, total;
+    run_of(a.B, b0, b1);
+    for (int b = b0; b < b1; ++b) mine += end[b];
+    int at = block_scan(mine, wsum, total);
+    for (int b = b0; b < b1; ++b) end[b] = at += end[b];
+    __syncthreads();
+    const int have = total ? lowest_free(a, min(total, a.n), wsum) : 0;
+    for (int b = warp; b < a.B; b += kThreads / 32) {
+        const Reserve r = reserve_of(a, cu_q, kv_len, b);
+        int from = b ? end[b - 1] : 0;
+        const bool none = end[b] > from && end[b] > have;
+        if (lane == 0) {
+            if (r.bad) set_status(a.status, GCA_ERR_DEVICE_INDEX);
+            else if (none) set_status(a.status, GCA_ERR_NO_PAGES);
+        }
+        __syncwarp();
+        if (lane == 0) kv_len[b] = r.bad || none ? ~r.old : r.old + r.add;
+        if (none) continue;
+        int32_t* row = a.table + (size_t)b * a.width;
+        for (int i0 = r.e0; i0 < r.e1; i0 += 32) {
+            const int i = i0 + lane;
+            const bool lacks = i < r.e1 && row[i] < 0;
+            const unsigned all = __ballot_sync(0xffffffffu, lacks);
+            if (lacks) {
+                const int e = a.list[from + __popc(all & ((1u << lane) - 1))];
+                row[i] = e;
+                take_page(a, e);
+            }
+            from += __popc(all);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Fork.  One CTA finds for every slot whether it copies its parent's last page, takes the pages
+// for that and sets the lengths; then CTAs of kCols columns of the whole table each
+// rewrite it in place and move the counts.
+// ---------------------------------------------------------------------------
+constexpr int kRefused = -2;             // in pairs: the fork did not happen
+constexpr int kCols = 8;
+
+// A slot's parent, itself where the argument is out of range.
+__device__ __forceinline__ int parent_of(const int32_t* parent, int b, int B) {
+    const int p = parent[b];
+    return p < -1 || p >= B ? b : p;
+}
+
+__global__ void __launch_bounds__(kThreads)
+paged_fork_plan_kernel(const PageArgs a, const int32_t* parent, int32_t* kv_len, int32_t* pairs) {
+    __shared__ int keeper[kMaxSeqs];     // the child that goes on with the slot's last page; -1: the slot itself
+    __shared__ int old[kMaxSeqs];        // lengths as they were
+    __shared__ int wsum[32];
+    pdl_release();
+    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+        keeper[b] = a.B;
+        old[b] = kv_len[b];
+        if (parent[b] < -1 || parent[b] >= a.B) set_status(a.status, GCA_ERR_DEVICE_INDEX);
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+        const int p = parent_of(parent, b, a.B);
+        if (p >= 0) atomicMin(&keeper[p], p == b ? -1 : b);
+    }
+    __syncthreads();
+    // the page that slot b copies, or -1
+    auto copied = [&](int b) {
+        const int p = parent_of(parent, b, a.B);
+        if (p < 0 || keeper[p] == (p == b ? -1 : b)) return -1;
+        const int len = old[p] < 0 ? ~old[p] : old[p], last = len >> a.page_log2;
+        if (!(len & ((1 << a.page_log2) - 1)) || last >= a.width) return -1;
+        const int e = a.table[(size_t)p * a.width + last];
+        return static_cast<unsigned>(e) < static_cast<unsigned>(a.n) ? e : -1;
+    };
+    int b0, b1, mine = 0, total;
+    run_of(a.B, b0, b1);
+    for (int b = b0; b < b1; ++b) mine += copied(b) >= 0;
+    int at = block_scan(mine, wsum, total);
+    const bool ok = total <= a.n && (total == 0 || lowest_free(a, total, wsum) == total);
+    if (!ok && threadIdx.x == 0) set_status(a.status, GCA_ERR_NO_PAGES);
+    for (int b = b0; b < b1; ++b) {
+        const int src = copied(b);
+        int2 pr = ok ? make_int2(-1, -1) : make_int2(kRefused, kRefused);
+        if (ok && src >= 0) {
+            pr = make_int2(src, a.list[at++]);
+            take_page(a, pr.y);
+        }
+        reinterpret_cast<int2*>(pairs)[b] = pr;
+        if (ok) {
+            const int p = parent_of(parent, b, a.B);
+            kv_len[b] = p < 0 ? 0 : old[p];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256)
+paged_fork_table_kernel(const PageArgs a, const int32_t* parent, const int32_t* kv_len, const int32_t* pairs) {
+    extern __shared__ int smem[];
+    int* entry = smem;                   // [B][kCols]: the table as it was
+    int* children = smem + a.B * kCols;  // [B]
+    int* tail = children + a.B;          // [B]: the entry of the slot's unfinished page, or -1
+    for (int b = threadIdx.x; b < a.B; b += 256) {
+        children[b] = 0;
+        tail[b] = -1;
+    }
+    pdl_wait();
+    if (pairs[0] == kRefused) return;
+    const int c0 = blockIdx.x * kCols, cols = min(kCols, a.width - c0);
+    for (int i = threadIdx.x; i < a.B * kCols; i += 256)
+        entry[i] = i % kCols < cols ? a.table[(size_t)(i / kCols) * a.width + c0 + i % kCols] : -1;
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.B; b += 256) {
+        const int p = parent_of(parent, b, a.B);
+        if (p < 0) continue;
+        atomicAdd(&children[p], 1);
+        const int kv = kv_len[b], len = kv < 0 ? ~kv : kv;       // (the parent's)
+        if (len & ((1 << a.page_log2) - 1)) tail[p] = len >> a.page_log2;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.B * kCols; i += 256) {
+        const int b = i / kCols, c = c0 + i % kCols, e = entry[i];
+        if (i % kCols >= cols) continue;
+        if (e >= 0) {                    // of the unfinished page one child goes on, of the others all
+            const int now = c == tail[b] ? min(children[b], 1) : children[b];
+            if (now != 1) count_page(a, e, now - 1);
+        }
+        const int p = parent_of(parent, b, a.B);
+        if (p == b) continue;
+        int to = p < 0 ? -1 : entry[p * kCols + i % kCols];
+        if (p >= 0 && c == tail[p] && pairs[2 * b + 1] >= 0) to = pairs[2 * b + 1];
+        a.table[(size_t)b * a.width + c] = to;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Compaction: of m used pages from n_used on, as many holes lie below; the i-th highest goes to
+// the i-th lowest hole.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads) paged_compact_plan_kernel(const PageArgs a, int max_moves, int32_t* pairs) {
+    __shared__ int wsum[32];
+    pdl_release();
+    int w0, w1, mine = 0, free;
+    run_of(a.n_words, w0, w1);
+    for (int w = w0; w < w1; ++w) mine += __popc(free_word(a, w));
+    block_scan(mine, wsum, free);
+    const int used = a.n - free;
+    // word w's free pages below `used`; its used ones from there on
+    auto holes = [&](int w) { return free_word(a, w) & below(used - 32 * w); };
+    auto high = [&](int w) { return ~free_word(a, w) & ~below(used - 32 * w) & below(a.n - 32 * w); };
+    int nh = 0, nu = 0, m, also;
+    for (int w = w0; w < w1; ++w) {
+        nh += __popc(holes(w));
+        nu += __popc(high(w));
+    }
+    int h = block_scan(nh, wsum, m);
+    int u = block_scan(nu, wsum, also);
+    const int moves = min(min(m, also), max_moves);
+    for (int r = moves + threadIdx.x; r < max_moves; r += kThreads) reinterpret_cast<int2*>(pairs)[r] = make_int2(-1, -1);
+    // where the used pages from `used` on go: list[e], e itself for those that stay
+    for (int e = max(used, 1) + threadIdx.x; e < a.n; e += kThreads) a.list[e] = e;
+    if (threadIdx.x == 0) a.list[0] = used ? used : a.n;         // (page 0 never moves: the first entry that may)
+    for (int w = w0; w < w1; ++w) {
+        for (uint32_t x = holes(w); x; x &= x - 1, ++h)
+            if (h < moves) pairs[2 * h + 1] = 32 * w + __ffs(x) - 1;
+        for (uint32_t x = high(w); x; x &= x - 1, ++u)
+            if (also - 1 - u < moves) pairs[2 * (also - 1 - u)] = 32 * w + __ffs(x) - 1;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < moves; r += kThreads) {
+        const int src = pairs[2 * r], dst = pairs[2 * r + 1];
+        a.list[src] = dst;
+        a.refs[dst] = a.refs[src];
+        a.refs[src] = 0;
+        atomicAnd(a.words + (dst >> 5), ~(1u << (dst & 31)));
+        atomicOr(a.words + (src >> 5), 1u << (src & 31));
+    }
+}
+
+__global__ void __launch_bounds__(256) paged_compact_table_kernel(const PageArgs a) {
+    pdl_wait();
+    const int first = a.list[0];
+    const long long n = (long long)a.B * a.width, step = (long long)gridDim.x * 256;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const int e = a.table[i];
+        if (e >= first && e < a.n) a.table[i] = a.list[e];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Copy: a CTA per piece of a page, of K or of V; every load before its stores.
+// ---------------------------------------------------------------------------
+constexpr int kCopyThreads = 256, kCopyVecs = 4;
+
+__global__ void __launch_bounds__(kCopyThreads)
+paged_copy_kernel(const int2* pairs, int n_pages, int page_vecs, int pieces, uint4* k_cache, uint4* v_cache, int* status) {
+    const int item = blockIdx.x / pieces, piece = blockIdx.x - item * pieces;
+    const int2 pr = __ldg(pairs + (item >> 1));
+    if (pr.x < 0 || pr.y < 0 || pr.x == pr.y) return;
+    if (pr.x >= n_pages || pr.y >= n_pages) {
+        if (threadIdx.x == 0) set_status(status, GCA_ERR_DEVICE_INDEX);
+        return;
+    }
+    uint4* c = item & 1 ? v_cache : k_cache;
+    const uint4* src = c + (size_t)pr.x * page_vecs;
+    uint4* dst = c + (size_t)pr.y * page_vecs;
+    const int v0 = piece * (kCopyThreads * kCopyVecs) + threadIdx.x;
+    uint4 x[kCopyVecs];
+#pragma unroll
+    for (int i = 0; i < kCopyVecs; ++i)
+        if (v0 + i * kCopyThreads < page_vecs) x[i] = __ldcs(src + v0 + i * kCopyThreads);
+#pragma unroll
+    for (int i = 0; i < kCopyVecs; ++i)
+        if (v0 + i * kCopyThreads < page_vecs) __stcs(dst + v0 + i * kCopyThreads, x[i]);
+}
+
+}  // namespace
+
+cudaError_t launch_pool_init(const PageShape& s, cudaStream_t st, int* launches) {
+    const PageArgs a = page_args(s, nullptr, nullptr);
+    GCA_LAUNCH("pool_init", st, pool_init_kernel<<<(a.n + 255) / 256, 256, 0, st>>>(a));
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+cudaError_t launch_paged_reserve(const PageShape& s, const int32_t* cu_q, int32_t* kv_len, int32_t* table,
+                                 int* status, cudaStream_t st, int* launches) {
+    const PageArgs a = page_args(s, table, status);
+    GCA_LAUNCH("paged_reserve", st, paged_reserve_kernel<<<1, kThreads, 0, st>>>(a, cu_q, kv_len));
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+cudaError_t launch_paged_fork(const PageShape& s, const int32_t* parent, int32_t* kv_len, int32_t* table,
+                              int32_t* pairs, int* status, cudaStream_t st, int* launches) {
+    const PageArgs a = page_args(s, table, status);
+    static LaunchSetup setup;
+    int sms;
+    cudaError_t e = setup.once(
+        [] {
+            return cudaFuncSetAttribute(paged_fork_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kMaxSeqs * (kCols + 2) * 4);
+        },
+        &sms);
+    if (e != cudaSuccess) return e;
+    GCA_LAUNCH("paged_fork_plan", st, paged_fork_plan_kernel<<<1, kThreads, 0, st>>>(a, parent, kv_len, pairs));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    *launches += 1;
+    GCA_LAUNCH("paged_fork_table", st,
+               e = launch_pdl(paged_fork_table_kernel, dim3((a.width + kCols - 1) / kCols), 256,
+                              (size_t)a.B * (kCols + 2) * 4, st, a, parent, static_cast<const int32_t*>(kv_len),
+                              static_cast<const int32_t*>(pairs)));
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+cudaError_t launch_paged_compact(const PageShape& s, int max_moves, int32_t* table, int32_t* pairs,
+                                 cudaStream_t st, int* launches) {
+    const PageArgs a = page_args(s, table, nullptr);
+    GCA_LAUNCH("paged_compact_plan", st, paged_compact_plan_kernel<<<1, kThreads, 0, st>>>(a, max_moves, pairs));
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    *launches += 1;
+    const long long blocks = ((long long)a.B * a.width + 255) / 256;
+    GCA_LAUNCH("paged_compact_table", st,
+               e = launch_pdl(paged_compact_table_kernel, dim3((unsigned)std::min<long long>(blocks, 2048)), 256, 0, st, a));
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+cudaError_t launch_paged_copy(size_t page_bytes, int n_pages, const int32_t* pairs, int n, void* k_cache,
+                              void* v_cache, int* status, cudaStream_t st, int* launches) {
+    const int vecs = static_cast<int>(page_bytes / 16), per = kCopyThreads * kCopyVecs, pieces = (vecs + per - 1) / per;
+    const long long blocks = 2ll * n * pieces;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    GCA_LAUNCH("paged_copy", st,
+               paged_copy_kernel<<<(unsigned)blocks, kCopyThreads, 0, st>>>(
+                   reinterpret_cast<const int2*>(pairs), n_pages, vecs, pieces, static_cast<uint4*>(k_cache),
+                   static_cast<uint4*>(v_cache), status));
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+}  // namespace gca

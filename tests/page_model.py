@@ -1,0 +1,93 @@
+"""The pages of a paged cache as a program on Python lists, one thing after the other: what
+gca_paged_reserve, gca_paged_fork and gca_paged_compact are to do."""
+
+
+class Pages:
+    def __init__(self, B, width, n_pages, page):
+        self.B, self.width, self.n, self.page = B, width, n_pages, page
+        self.table = [[-1] * width for _ in range(B)]
+        self.kv = [0] * B
+        self.refs = [0] * n_pages
+        self.status = 0
+
+    def free(self):
+        return [p for p in range(self.n) if self.refs[p] == 0]
+
+    def bad(self, code):
+        self.status = self.status or code
+
+    def reserve(self, cu, window=0, sinks=0):
+        page, plans = self.page, []
+        for b in range(self.B):
+            row, kv = self.table[b], self.kv[b]
+            old = -1 - kv if kv < 0 else kv
+            n = cu[b + 1] - cu[b]
+            wrong = n < 0 or cu[b] < 0 or old + n > self.width * page
+            if window and n and not wrong:
+                i = max(0, old - window + 1) // page - 1
+                while i * page >= sinks and i >= 0 and row[i] >= 0:
+                    self.refs[row[i]] -= 1
+                    row[i] = -1
+                    i -= 1
+            plans.append((old, n, wrong))
+        free, at, total = self.free(), 0, 0
+        for b, (old, n, wrong) in enumerate(plans):
+            row = self.table[b]
+            if wrong:
+                self.bad(6)
+                self.kv[b] = -1 - old
+                continue
+            lack = [i for i in range(old // page, -(-(old + n) // page)) if row[i] < 0] if n else []
+            total += len(lack)
+            if lack and total > len(free):
+                self.bad(7)
+                self.kv[b] = -1 - old
+                continue
+            for i in lack:
+                row[i] = free[at]
+                self.refs[free[at]] = 1
+                at += 1
+            self.kv[b] = old + n
+
+    def fork(self, parent):
+        page = self.page
+        if any(p < -1 or p >= self.B for p in parent):
+            self.bad(6)
+        parent = [b if p < -1 or p >= self.B else p for b, p in enumerate(parent)]
+        rows, kv = [list(r) for r in self.table], list(self.kv)
+        free, pairs, keeper = self.free(), [(-1, -1)] * self.B, {}
+        for b, p in enumerate(parent):
+            if p >= 0 and (p == b or p not in keeper):
+                keeper[p] = b
+        copies = []
+        for b, p in enumerate(parent):
+            if p < 0 or keeper[p] == b:
+                continue
+            n = -1 - kv[p] if kv[p] < 0 else kv[p]
+            if n % page and rows[p][n // page] >= 0:
+                copies.append((b, n // page, rows[p][n // page]))
+        if len(copies) > len(free):
+            self.bad(7)
+            return [(-2, -2)] * self.B
+        self.table = [list(rows[p]) if p >= 0 else [-1] * self.width for p in parent]
+        self.kv = [kv[p] if p >= 0 else 0 for p in parent]
+        for (b, i, src), dst in zip(copies, free):
+            pairs[b] = (src, dst)
+            self.table[b][i] = dst
+        self.refs = [0] * self.n
+        for row in self.table:
+            for e in row:
+                if e >= 0:
+                    self.refs[e] += 1
+        return pairs
+
+    def compact(self, max_moves):
+        used = [p for p in range(self.n) if self.refs[p]]
+        holes = [p for p in self.free() if p < len(used)]
+        high = [p for p in reversed(used) if p >= len(used)]
+        moves = list(zip(high, holes))[:max_moves]
+        to = dict(moves)
+        for src, dst in moves:
+            self.refs[dst], self.refs[src] = self.refs[src], 0
+        self.table = [[to.get(e, e) for e in row] for row in self.table]
+        return moves + [(-1, -1)] * (max_moves - len(moves))
