@@ -365,13 +365,44 @@ __device__ __forceinline__ float fast_rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// r of two scores; `in` is 2 a log2(e) / c
-__device__ __forceinline__ void cap_r2(float x0, float x1, uint64_t in2, float& r0, float& r1) {
-    float y0, y1;
-    tcx::f2_unpack(tcx::fmul2(tcx::f2_pack(x0, x1), in2), y0, y1);
-    tcx::f2_unpack(tcx::fadd2(tcx::f2_pack(tcx::fast_exp2(y0), tcx::fast_exp2(y1)), tcx::f2_pack(1.f, 1.f)), y0, y1);
-    r0 = fast_rcp(y0);
-    r1 = fast_rcp(y1);
+// Exponents up to here are taken as they are: r = 2^-30 is as good as none, and four such E's product
+// is finite.
+constexpr float kCapMax = 30.f;
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float z;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+// r of four scores from their products; `in` is 2 a log2(e) / c.  One reciprocal, of the product
+// of the four denominators, in place of four, whose pipe takes half as many a cycle as exp2's.
+// CLAMP: products may pass kCapMax / in.
+template <bool CLAMP>
+__device__ __forceinline__ void cap_r4(float (&x)[4], uint64_t in2) {
+    float e[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) tcx::f2_unpack(tcx::fmul2(tcx::f2_pack(x[i], x[i + 1]), in2), e[i], e[i + 1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = tcx::fast_exp2(CLAMP ? min_nan(e[i], kCapMax) : e[i]);
+    const uint64_t one = tcx::f2_pack(1.f, 1.f);
+    const uint64_t u = tcx::fadd2(tcx::f2_pack(e[0], e[1]), one), v = tcx::fadd2(tcx::f2_pack(e[2], e[3]), one);
+    float s0, s1;
+    tcx::f2_unpack(tcx::fmul2(u, v), s0, s1);
+    const float q = fast_rcp(s0 * s1);
+    const uint64_t t = tcx::f2_pack(q * s1, q * s0);
+    tcx::f2_unpack(tcx::fmul2(t, v), x[0], x[1]);
+    tcx::f2_unpack(tcx::fmul2(t, u), x[2], x[3]);
+}
+// The same in place on 16 accumulator columns.
+__device__ __forceinline__ void cap_r16(uint32_t* r, uint64_t in2) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = __uint_as_float(r[i + u]);
+        cap_r4<true>(x, in2);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) r[i + u] = __float_as_uint(x[u]);
+    }
 }
 
 // One lane of a converged warp, the same one each time.

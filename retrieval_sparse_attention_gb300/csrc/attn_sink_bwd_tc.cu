@@ -96,19 +96,14 @@ struct BwdArgs {
 
 // The exponent of p from a product x (two at a time), nl being -lse log2(e) and what of the score does
 // not depend on x:
-//   plain, bias  scale_log2 x + nl      cap  -2 C r + nl, with C in nl
+//   plain, bias  scale_log2 x + nl      cap, x being r (attn_sink.cuh)  -2 C x + nl, with C in nl
 // and with a cap r (1 - r), which ds takes besides p.
 template <int SCORE>
-__device__ __forceinline__ uint64_t exponent2(uint32_t x0, uint32_t x1, uint64_t sl2, uint64_t cap_in2, uint64_t nl,
-                                              uint64_t& bend) {
-    if constexpr (SCORE == kScoreCap) {
-        float r0, r1;
-        cap_r2(__uint_as_float(x0), __uint_as_float(x1), cap_in2, r0, r1);
-        const uint64_t r = tcx::f2_pack(r0, r1);
-        bend = tcx::ffma2(tcx::f2_pack(-r0, -r1), r, r);
-        return tcx::ffma2(r, sl2, nl);
-    }
-    return tcx::ffma2(tcx::f2_pack(__uint_as_float(x0), __uint_as_float(x1)), sl2, nl);
+__device__ __forceinline__ uint64_t exponent2(uint32_t x0, uint32_t x1, uint64_t sl2, uint64_t nl, uint64_t& bend) {
+    const float f0 = __uint_as_float(x0), f1 = __uint_as_float(x1);
+    const uint64_t x = tcx::f2_pack(f0, f1);
+    if (SCORE == kScoreCap) bend = tcx::ffma2(tcx::f2_pack(-f0, -f1), x, x);
+    return tcx::ffma2(x, sl2, nl);
 }
 
 // ============================================================================ vectors
@@ -554,6 +549,10 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     }
                     const uint32_t vis = (below(c_hi + 1 - 32 * pc) & ~below(c_lo - 32 * pc)) | below(c_s - 32 * pc);
                     uint32_t pk[16];
+                    if constexpr (SCORE == kScoreCap) {
+                        cap_r16(r0, cap_in2);
+                        cap_r16(r1, cap_in2);
+                    }
                     auto body = [&](bool msk) {
 #pragma unroll
                         for (int p2 = 0; p2 < 16; ++p2) {
@@ -565,7 +564,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                             if (SCORE == kScoreBias)
                                 nl = tcx::ffma2(tcx::f2_pack(32.f * pc + 2 * p2, 32.f * pc + 2 * p2 + 1), tcx::f2_pack(slope, slope),
                                                 tcx::f2_pack(off, off));
-                            tcx::f2_unpack(exponent2<SCORE>(rs[tt], rs[tt + 1], sl2, cap_in2, nl, bend), y0, y1);
+                            tcx::f2_unpack(exponent2<SCORE>(rs[tt], rs[tt + 1], sl2, nl, bend), y0, y1);
                             float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
                             if (msk) {
                                 e0 = (vis >> (2 * p2) & 1u) ? e0 : 0.f;
@@ -1032,12 +1031,13 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                 tc_fence_before();
                                 mbar_arrive(&sb.y_empty[ys]);
                             }
+                            if constexpr (SCORE == kScoreCap) cap_r16(rs, cap_in2);
                             const uint32_t vis = below(c_hi + 1 - 16 * c) & ~below(c_lo - 16 * c);
                             uint32_t pd[8], pp[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 float y0, y1;
-                                uint64_t bend = 0, y = exponent2<SCORE>(rs[2 * i], rs[2 * i + 1], sl2, cap_in2, nl[8 * c + i], bend);
+                                uint64_t bend = 0, y = exponent2<SCORE>(rs[2 * i], rs[2 * i + 1], sl2, nl[8 * c + i], bend);
                                 if (SCORE == kScoreBias) y = tcx::fadd2(y, tcx::f2_pack(off, off));
                                 tcx::f2_unpack(y, y0, y1);
                                 float e0 = fast_exp2(y0), e1 = fast_exp2(y1);

@@ -600,13 +600,12 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         auto greater = [](float x, float y) { return CAP ? fminf(x, y) : fmaxf(x, y); };
         auto log2_of = [&](float v) { return CAP ? fmaf(v, sl, so) : v * sl; };
         auto less = [&](float max) { return CAP ? so - max : -max; };
-        // products of columns c, c + 1, whose keys are `from` + c, + 1 positions from the row's own
-        auto transform = [&](float& x0, float& x1, int c, uint64_t from) {
-            if constexpr (CAP) cap_r2(x0, x1, cap_in2, x0, x1);
-            if constexpr (BIAS)
-                tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x0, x1), tcx::f2_pack(a.scale_log2, a.scale_log2),
-                                          tcx::ffma2(tcx::f2_pack((float)c, (float)(c + 1)), tcx::f2_pack(slope, slope), from)),
-                               x0, x1);
+        // products of columns c, c + 1, whose keys are `from` + c, + 1 positions from the row's own, to
+        // scores with their bias
+        auto biased = [&](float& x0, float& x1, int c, uint64_t from) {
+            tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x0, x1), tcx::f2_pack(a.scale_log2, a.scale_log2),
+                                      tcx::ffma2(tcx::f2_pack((float)c, (float)(c + 1)), tcx::f2_pack(slope, slope), from)),
+                           x0, x1);
         };
 
         int ts = 0, ko = 0, np = 0, j = 0, j1 = 0, f0 = 0, f1 = 0, fl = 0;
@@ -713,12 +712,18 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 tc_fence_before();
                 if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
                 const uint32_t nvis = below(sc.ns);
-                if constexpr (SCORE != kScorePlain) {
+                if constexpr (CAP) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = (nvis >> i & 1u) ? r[i] : 0xff800000u;   // (as below: no NaN)
+                    cap_r16(r, cap_in2);
+                    cap_r16(r + 16, cap_in2);
+                }
+                if constexpr (BIAS) {
                     const float off = slope * static_cast<float>(-w.p0 - rt);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float x0 = __uint_as_float(r[i]), x1 = __uint_as_float(r[i + 1]);
-                        transform(x0, x1, i, tcx::f2_pack(off, off));
+                        biased(x0, x1, i, tcx::f2_pack(off, off));
                         r[i] = __float_as_uint(x0);
                         r[i + 1] = __float_as_uint(x1);
                     }
@@ -764,25 +769,42 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     tc_fence_before();
                     if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
                     float mt = fmaxf(mc[0], mc[1]);
-                    if constexpr (SCORE != kScorePlain) {
-                        const float off = slope * static_cast<float>(w.tile(j) * 128 - w.p0 - rt);
-#pragma unroll
-                        for (int i = 0; i < 128; i += 2) transform(x[i], x[i + 1], i, tcx::f2_pack(off, off));
-                        if (CAP) mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));   // (of the greatest product)
-                    }
+                    // The diagonal or the window's edge crosses the tile, or all rows see it whole.  Visible:
+                    // columns c_lo .. c_hi (the window) and those below c_s (sinks), as bits.
                     const bool whole = (j >= f0 && j < f1) || j == fl;
-                    if (!whole) {
-                        // The diagonal or the window's edge crosses the tile.  Visible: columns c_lo ..
-                        // c_hi (the window) and those below c_s (sinks), as bits.
-                        const int p = w.p0 + rt, kbase = w.tile(j) * 128;
+                    const int p = w.p0 + rt, kbase = w.tile(j) * 128;
+                    auto hide = [&](float with) {
                         const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const uint32_t vis = (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : kHidden;
+                            for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : with;
                         }
+                    };
+                    // (four scores share a reciprocal: a hidden cache row's NaN must not get there)
+                    if (CAP && PAGED && !whole) hide(-INFINITY);
+                    if constexpr (CAP) {
+                        const float lim = kCapMax / a.cap_in;
+                        if (__any_sync(0xffffffffu, !(mt <= lim))) {      // (hardly ever)
+#pragma unroll
+                            for (int i = 0; i < 128; ++i) x[i] = min_nan(x[i], lim);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 128; i += 4) {
+                            float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+                            cap_r4<false>(y, cap_in2);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) x[i + u] = y[u];
+                        }
+                        mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));    // r of the greatest product
                     }
+                    if constexpr (BIAS) {
+                        const float off = slope * static_cast<float>(kbase - p);
+#pragma unroll
+                        for (int i = 0; i < 128; i += 2) biased(x[i], x[i + 1], i, tcx::f2_pack(off, off));
+                    }
+                    if (!whole) hide(kHidden);
                     // the maximum over all columns bounds that over the visible ones: only where it
                     // would move the running one (or is no number) is the latter needed (with a bias
                     // the products' maximum says nothing: always)
