@@ -397,7 +397,7 @@ typedef struct {
  *   positions [T] int32 (device, any sign) or NULL: start + t % L.
  *   q_out, k_out may be q and k themselves with the same strides (in place), but must not
  *   overlap them, or each other, in any other way.
- *   Up to 2^31 warps of 128 slots (16 columns each) of a token in all.
+ *   T * (H + Hkv) * d up to 2^42.
  */
 gca_status_t gca_rope(const gca_rope_params_t* params, const void* q, const void* k,
                       const int64_t* freqs, const int32_t* positions, void* q_out, void* k_out,
@@ -499,7 +499,7 @@ gca_status_t gca_paged_attn_scored(const gca_paged_params_t* params, const gca_s
  *     paged call's; k_new and v_new share kv_stride).
  *   q [total_q, H, d] -> q_out [total_q, H, d] dense: rows that belong to no sequence are
  *     left as they were; a token at a negative position is turned by that.  q_out must
- *     not overlap q unless q is dense and q_out is q.
+ *     not overlap q unless q is dense and q_out is q.  total_q * (H + 2 Hkv) * d up to 2^42.
  */
 gca_status_t gca_paged_rope_append(const gca_paged_params_t* params, const gca_rope_params_t* rope,
                                    const void* q, const void* k_new, const void* v_new,

@@ -198,12 +198,13 @@ def _same_device(*ts):
     """The entries launch on the current device's stream: tensors of another device (or of
     none) would be read through a foreign address.  Returns the device index."""
     dev = ts[0].get_device()
-    ok = dev >= 0 and dev == torch._C._cuda_getDevice()     # (current_device() without its setup)
-    for t in ts:
-        ok = ok and (t is None or t.get_device() == dev)
-    if not ok:
-        raise ValueError("tensors must be CUDA tensors on the current device")
-    return dev
+    if dev >= 0 and dev == torch._C._cuda_getDevice():      # (current_device() without its setup)
+        for t in ts:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            return dev
+    raise ValueError("tensors must be CUDA tensors on the current device")
 
 
 def _empty_like(t):
@@ -319,11 +320,12 @@ def _rope(q, k, freqs, positions, start, interleaved, mscale, inplace, inverse):
     _same_device(freqs, q, k, positions)
     if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
         raise ValueError("positions must be a contiguous int32 tensor")
-    p = _rope_plan(None if q is None else q.shape, None if q is None else q.stride(),
-                   None if k is None else k.shape, None if k is None else k.stride(),
-                   None if q is None else q.dtype, None if k is None else k.dtype, _rope_freqs(freqs),
-                   None if positions is None else positions.shape, operator.index(start),
-                   bool(interleaved), float(mscale), inverse, bool(inplace))
+    if type(start) is not int:
+        start = operator.index(start)
+    qs, qst, qt = (None, None, None) if q is None else (q.shape, q.stride(), q.dtype)
+    ks, kst, kt = (None, None, None) if k is None else (k.shape, k.stride(), k.dtype)
+    p = _rope_plan(qs, qst, ks, kst, qt, kt, _rope_freqs(freqs), None if positions is None else positions.shape,
+                   start, bool(interleaved), float(mscale), inverse, bool(inplace))
     qo = q if inplace or q is None else _empty_like(q)
     ko = k if inplace or k is None else _empty_like(k)
     gca_rope(p, q, k, freqs, positions, qo, ko)
@@ -594,9 +596,9 @@ def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, s
 def gca_paged_rope_append(params: GcaPagedParams, rope: GcaRopeParams, q, k_new, v_new, freqs, cu_q,
                           kv_len, table, q_out, k_cache, v_cache, stream=None):
     _check("gca_paged_rope_append", _lib.load().gca_paged_rope_append(
-        ctypes.byref(params), ctypes.byref(rope), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(freqs),
-        _ptr(cu_q), _ptr(kv_len), _ptr(table), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
-        _raw_stream(stream, k_cache.get_device())))
+        ctypes.byref(params), ctypes.byref(rope), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        freqs.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(), q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, k_cache.get_device())))
 
 
 @functools.lru_cache(maxsize=256)

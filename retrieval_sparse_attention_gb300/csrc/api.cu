@@ -503,6 +503,8 @@ bool rope_stride(int given, int heads, int d, int* out) {
     return given >= 0 && (heads == 0 || (*out >= heads * d && *out % 8 == 0));
 }
 
+constexpr long long kMaxRopeSlots = 1ll << 38;    // (the kernels' blocks, 8 warps each, stay below 2^31)
+
 gca_status_t rope_columns(const gca_rope_params_t* p, int d, RopeShape* s) {
     if (p->rot < 1 || p->rot > d || !(p->mscale >= 0.f) || isinf(p->mscale)) return GCA_ERR_INVALID_ARG;
     if (p->rot % 16 != 0) return GCA_ERR_UNSUPPORTED;
@@ -528,8 +530,8 @@ gca_status_t rope_check(const gca_rope_params_t* p, bool positions, RopeShape* o
         return GCA_ERR_INVALID_ARG;
     if (s.q_stride > (1 << 24) || s.k_stride > (1 << 24) || s.qo_stride > (1 << 24) || s.ko_stride > (1 << 24))
         return GCA_ERR_UNSUPPORTED;
-    const long long units = ((long long)(s.H + s.Hkv) * (s.d / 16) + 127) / 128;
-    if (s.T * units > 0x7fffffffll) return GCA_ERR_UNSUPPORTED;
+    const long long slots = (long long)(s.H + s.Hkv) * (s.d / 16);
+    if (s.T * slots > kMaxRopeSlots) return GCA_ERR_UNSUPPORTED;
     const gca_status_t r = rope_columns(p, p->d, &s);
     if (r == GCA_OK) *out = s;
     return r;
@@ -583,8 +585,7 @@ gca_status_t gca_paged_rope_append(const gca_paged_params_t* params, const gca_r
     if (!rope || params->H < 1) return GCA_ERR_INVALID_ARG;
     if ((r = rope_columns(rope, s.d, &rs)) != GCA_OK) return r;
     if (rs.inverse) return GCA_ERR_UNSUPPORTED;
-    const long long units = ((long long)(s.H + 2 * s.Hkv) * (s.d / 16) + 127) / 128;
-    if (s.T * units > 0x7fffffffll) return GCA_ERR_UNSUPPORTED;
+    if ((long long)s.T * (s.H + 2 * s.Hkv) * (s.d / 16) > kMaxRopeSlots) return GCA_ERR_UNSUPPORTED;
     if (s.T == 0) {
         t_launches = 0;
         return GCA_OK;

@@ -16,6 +16,10 @@ namespace {
 
 constexpr int kThreads = 1024;           // of the CTA that decides
 constexpr int kMaxSeqs = 4096;           // (api.cu checks)
+// Tables of so many entries are rewritten by the CTA that decides, which saves a launch (fork of 8 slots, 392
+// entries: 6.2 us against 6.8 in two launches, and 3 us of host time; of 256 slots, 12,000 entries: 16 against
+// 12.4).
+constexpr int kSmallTable = 6144;
 
 struct PageArgs {
     int32_t *refs, *list;
@@ -74,6 +78,28 @@ __device__ __forceinline__ int block_scan(int v, int* wsum, int& total) {
     total = __shfl_sync(0xffffffffu, x, 31);
     const int before = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
     return inc - v + (warp ? before : 0);
+}
+
+__device__ __forceinline__ int2 add(int2 a, int2 b) { return make_int2(a.x + b.x, a.y + b.y); }
+// Two sums at once.
+__device__ __forceinline__ int2 block_scan2(int2 v, int2* wsum, int2& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto up = [&](int2 x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int2 y = make_int2(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o));
+            if (lane >= o) x = add(x, y);
+        }
+        return x;
+    };
+    const int2 inc = up(v);
+    __syncthreads();
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    const int2 x = up(wsum[lane]);
+    total = make_int2(__shfl_sync(0xffffffffu, x.x, 31), __shfl_sync(0xffffffffu, x.y, 31));
+    const int2 before = make_int2(__shfl_sync(0xffffffffu, x.x, (warp + 31) & 31), __shfl_sync(0xffffffffu, x.y, (warp + 31) & 31));
+    return add(make_int2(inc.x - v.x, inc.y - v.y), warp ? before : make_int2(0, 0));
 }
 
 // This thread's run of the n items that all threads share.
@@ -195,8 +221,8 @@ __global__ void __launch_bounds__(kThreads) paged_reserve_kernel(const PageArgs 
 
 // ---------------------------------------------------------------------------
 // Fork.  One CTA finds for every slot whether it copies its parent's last page, takes the pages
-// for that and sets the lengths; then CTAs of kCols columns of the whole table each
-// rewrite it in place and move the counts.
+// for that and sets the lengths; then it rewrites the table in place and moves the counts, or, for
+// tables of more than kSmallTable entries, CTAs of kCols columns each do.
 // ---------------------------------------------------------------------------
 constexpr int kRefused = -2;             // in pairs: the fork did not happen
 constexpr int kCols = 8;
@@ -207,12 +233,71 @@ __device__ __forceinline__ int parent_of(const int32_t* parent, int b, int B) {
     return p < -1 || p >= B ? b : p;
 }
 
+// Rewrites columns c0 .. of the table, in place, and moves the counts: one CTA, with room for
+// B * (cols + 2) numbers.  COLS of them, or where that is 0 all.
+template <int COLS>
+__device__ __forceinline__ void fork_columns(const PageArgs& a, const int32_t* parent, const int32_t* kv_len,
+                                             const int32_t* pairs, int c0, int* room) {
+    const int cols = COLS ? COLS : a.width;
+    int* entry = room;                   // [B][cols]: the table as it was
+    int* children = room + a.B * cols;   // [B]
+    int* tail = children + a.B;          // [B]: the entry of the slot's unfinished page, or -1
+    const int n = a.B * cols;
+    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+        children[b] = 0;
+        tail[b] = -1;
+    }
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int c = c0 + i % cols;     // (the last CTA's may lie past the row)
+        entry[i] = c < a.width ? a.table[(size_t)(i / cols) * a.width + c] : -1;
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+        const int p = parent_of(parent, b, a.B);
+        if (p < 0) continue;
+        atomicAdd(&children[p], 1);
+        const int kv = kv_len[b], len = kv < 0 ? ~kv : kv;       // (the parent's)
+        if (len & ((1 << a.page_log2) - 1)) tail[p] = len >> a.page_log2;
+    }
+    __syncthreads();
+    constexpr int U = 4;                 // (counts in flight)
+    for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+        int e[U], delta[U], left[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kThreads, b = i / cols;
+            e[u] = i < n ? entry[i] : -1;
+            delta[u] = 0;
+            // of the unfinished page one child goes on, of the others all
+            if (e[u] >= 0) delta[u] = (c0 + i % cols == tail[b] ? min(children[b], 1) : children[b]) - 1;
+            if (delta[u] && e[u] >= a.n) set_status(a.status, GCA_ERR_DEVICE_INDEX);
+            if (e[u] >= a.n) delta[u] = 0;
+            if (delta[u]) left[u] = atomicAdd(a.refs + e[u], delta[u]) + delta[u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kThreads, b = i / cols, c = c0 + i % cols;
+            if (delta[u] && left[u] == 0) atomicOr(a.words + (e[u] >> 5), 1u << (e[u] & 31));
+            if (i >= n || c >= a.width) continue;
+            const int p = parent_of(parent, b, a.B);
+            if (p == b) continue;
+            int to = p < 0 ? -1 : entry[p * cols + i % cols];
+            if (p >= 0 && c == tail[p] && pairs[2 * b + 1] >= 0) to = pairs[2 * b + 1];
+            a.table[(size_t)b * a.width + c] = to;
+        }
+    }
+}
+
+// ALL: rewrites the table as well.
+template <bool ALL>
 __global__ void __launch_bounds__(kThreads)
 paged_fork_plan_kernel(const PageArgs a, const int32_t* parent, int32_t* kv_len, int32_t* pairs) {
+    extern __shared__ int room[];
     __shared__ int keeper[kMaxSeqs];     // the child that goes on with the slot's last page; -1: the slot itself
     __shared__ int old[kMaxSeqs];        // lengths as they were
     __shared__ int wsum[32];
-    pdl_release();
+    if (!ALL) pdl_release();
     for (int b = threadIdx.x; b < a.B; b += kThreads) {
         keeper[b] = a.B;
         old[b] = kv_len[b];
@@ -252,54 +337,45 @@ paged_fork_plan_kernel(const PageArgs a, const int32_t* parent, int32_t* kv_len,
             kv_len[b] = p < 0 ? 0 : old[p];
         }
     }
+    if (ALL && ok) {
+        __syncthreads();
+        fork_columns<0>(a, parent, kv_len, pairs, 0, room);
+    }
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 paged_fork_table_kernel(const PageArgs a, const int32_t* parent, const int32_t* kv_len, const int32_t* pairs) {
-    extern __shared__ int smem[];
-    int* entry = smem;                   // [B][kCols]: the table as it was
-    int* children = smem + a.B * kCols;  // [B]
-    int* tail = children + a.B;          // [B]: the entry of the slot's unfinished page, or -1
-    for (int b = threadIdx.x; b < a.B; b += 256) {
-        children[b] = 0;
-        tail[b] = -1;
-    }
+    extern __shared__ int room[];
     pdl_wait();
     if (pairs[0] == kRefused) return;
-    const int c0 = blockIdx.x * kCols, cols = min(kCols, a.width - c0);
-    for (int i = threadIdx.x; i < a.B * kCols; i += 256)
-        entry[i] = i % kCols < cols ? a.table[(size_t)(i / kCols) * a.width + c0 + i % kCols] : -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < a.B; b += 256) {
-        const int p = parent_of(parent, b, a.B);
-        if (p < 0) continue;
-        atomicAdd(&children[p], 1);
-        const int kv = kv_len[b], len = kv < 0 ? ~kv : kv;       // (the parent's)
-        if (len & ((1 << a.page_log2) - 1)) tail[p] = len >> a.page_log2;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.B * kCols; i += 256) {
-        const int b = i / kCols, c = c0 + i % kCols, e = entry[i];
-        if (i % kCols >= cols) continue;
-        if (e >= 0) {                    // of the unfinished page one child goes on, of the others all
-            const int now = c == tail[b] ? min(children[b], 1) : children[b];
-            if (now != 1) count_page(a, e, now - 1);
-        }
-        const int p = parent_of(parent, b, a.B);
-        if (p == b) continue;
-        int to = p < 0 ? -1 : entry[p * kCols + i % kCols];
-        if (p >= 0 && c == tail[p] && pairs[2 * b + 1] >= 0) to = pairs[2 * b + 1];
-        a.table[(size_t)b * a.width + c] = to;
-    }
+    fork_columns<kCols>(a, parent, kv_len, pairs, blockIdx.x * kCols, room);
 }
 
 // ---------------------------------------------------------------------------
 // Compaction: of m used pages from n_used on, as many holes lie below; the i-th highest goes to
 // the i-th lowest hole.
 // ---------------------------------------------------------------------------
+// The entries of the table whose pages have moved; thread i of n.
+__device__ __forceinline__ void compact_entries(const PageArgs& a, long long i, long long n) {
+    const int first = a.list[0];
+    const long long entries = (long long)a.B * a.width;
+    constexpr int U = 4;
+    for (; i < entries; i += U * n) {
+        int e[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) e[u] = i + u * n < entries ? a.table[i + u * n] : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (e[u] >= first && e[u] < a.n) a.table[i + u * n] = a.list[e[u]];
+    }
+}
+
+// ALL: rewrites the table as well.
+template <bool ALL>
 __global__ void __launch_bounds__(kThreads) paged_compact_plan_kernel(const PageArgs a, int max_moves, int32_t* pairs) {
     __shared__ int wsum[32];
-    pdl_release();
+    __shared__ int2 wsum2[32];
+    if (!ALL) pdl_release();
     int w0, w1, mine = 0, free;
     run_of(a.n_words, w0, w1);
     for (int w = w0; w < w1; ++w) mine += __popc(free_word(a, w));
@@ -308,14 +384,11 @@ __global__ void __launch_bounds__(kThreads) paged_compact_plan_kernel(const Page
     // word w's free pages below `used`; its used ones from there on
     auto holes = [&](int w) { return free_word(a, w) & below(used - 32 * w); };
     auto high = [&](int w) { return ~free_word(a, w) & ~below(used - 32 * w) & below(a.n - 32 * w); };
-    int nh = 0, nu = 0, m, also;
-    for (int w = w0; w < w1; ++w) {
-        nh += __popc(holes(w));
-        nu += __popc(high(w));
-    }
-    int h = block_scan(nh, wsum, m);
-    int u = block_scan(nu, wsum, also);
-    const int moves = min(min(m, also), max_moves);
+    int2 mine2 = make_int2(0, 0), m;
+    for (int w = w0; w < w1; ++w) mine2 = add(mine2, make_int2(__popc(holes(w)), __popc(high(w))));
+    const int2 from = block_scan2(mine2, wsum2, m);
+    int h = from.x, u = m.y - 1 - from.y;
+    const int moves = min(min(m.x, m.y), max_moves);
     for (int r = moves + threadIdx.x; r < max_moves; r += kThreads) reinterpret_cast<int2*>(pairs)[r] = make_int2(-1, -1);
     // where the used pages from `used` on go: list[e], e itself for those that stay
     for (int e = max(used, 1) + threadIdx.x; e < a.n; e += kThreads) a.list[e] = e;
@@ -323,8 +396,8 @@ __global__ void __launch_bounds__(kThreads) paged_compact_plan_kernel(const Page
     for (int w = w0; w < w1; ++w) {
         for (uint32_t x = holes(w); x; x &= x - 1, ++h)
             if (h < moves) pairs[2 * h + 1] = 32 * w + __ffs(x) - 1;
-        for (uint32_t x = high(w); x; x &= x - 1, ++u)
-            if (also - 1 - u < moves) pairs[2 * (also - 1 - u)] = 32 * w + __ffs(x) - 1;
+        for (uint32_t x = high(w); x; x &= x - 1, --u)
+            if (u < moves) pairs[2 * u] = 32 * w + __ffs(x) - 1;
     }
     __syncthreads();
     for (int r = threadIdx.x; r < moves; r += kThreads) {
@@ -335,16 +408,15 @@ __global__ void __launch_bounds__(kThreads) paged_compact_plan_kernel(const Page
         atomicAnd(a.words + (dst >> 5), ~(1u << (dst & 31)));
         atomicOr(a.words + (src >> 5), 1u << (src & 31));
     }
+    if (ALL) {
+        __syncthreads();
+        compact_entries(a, threadIdx.x, kThreads);
+    }
 }
 
 __global__ void __launch_bounds__(256) paged_compact_table_kernel(const PageArgs a) {
     pdl_wait();
-    const int first = a.list[0];
-    const long long n = (long long)a.B * a.width, step = (long long)gridDim.x * 256;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const int e = a.table[i];
-        if (e >= first && e < a.n) a.table[i] = a.list[e];
-    }
+    compact_entries(a, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
 }
 
 // ---------------------------------------------------------------------------
@@ -398,20 +470,28 @@ cudaError_t launch_paged_fork(const PageShape& s, const int32_t* parent, int32_t
     const PageArgs a = page_args(s, table, status);
     static LaunchSetup setup;
     int sms;
+    const bool small = (long long)a.B * a.width <= kSmallTable;
+    const int room = a.B * (small ? a.width + 2 : kCols + 2) * 4;
     cudaError_t e = setup.once(
         [] {
+            const cudaError_t r = cudaFuncSetAttribute(paged_fork_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (kSmallTable + 2 * kMaxSeqs) * 4);
+            if (r != cudaSuccess) return r;
             return cudaFuncSetAttribute(paged_fork_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         kMaxSeqs * (kCols + 2) * 4);
         },
         &sms);
     if (e != cudaSuccess) return e;
-    GCA_LAUNCH("paged_fork_plan", st, paged_fork_plan_kernel<<<1, kThreads, 0, st>>>(a, parent, kv_len, pairs));
+    GCA_LAUNCH("paged_fork_plan", st, {
+        if (small) paged_fork_plan_kernel<true><<<1, kThreads, room, st>>>(a, parent, kv_len, pairs);
+        else paged_fork_plan_kernel<false><<<1, kThreads, 0, st>>>(a, parent, kv_len, pairs);
+    });
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *launches += 1;
+    if (small) return e;
     GCA_LAUNCH("paged_fork_table", st,
-               e = launch_pdl(paged_fork_table_kernel, dim3((a.width + kCols - 1) / kCols), 256,
-                              (size_t)a.B * (kCols + 2) * 4, st, a, parent, static_cast<const int32_t*>(kv_len),
-                              static_cast<const int32_t*>(pairs)));
+               e = launch_pdl(paged_fork_table_kernel, dim3((a.width + kCols - 1) / kCols), kThreads, room, st, a, parent,
+                              static_cast<const int32_t*>(kv_len), static_cast<const int32_t*>(pairs)));
     if (e == cudaSuccess) *launches += 1;
     return e;
 }
@@ -419,13 +499,19 @@ cudaError_t launch_paged_fork(const PageShape& s, const int32_t* parent, int32_t
 cudaError_t launch_paged_compact(const PageShape& s, int max_moves, int32_t* table, int32_t* pairs,
                                  cudaStream_t st, int* launches) {
     const PageArgs a = page_args(s, table, nullptr);
-    GCA_LAUNCH("paged_compact_plan", st, paged_compact_plan_kernel<<<1, kThreads, 0, st>>>(a, max_moves, pairs));
+    const long long entries = (long long)a.B * a.width;
+    const bool small = entries <= kSmallTable;
+    GCA_LAUNCH("paged_compact_plan", st, {
+        if (small) paged_compact_plan_kernel<true><<<1, kThreads, 0, st>>>(a, max_moves, pairs);
+        else paged_compact_plan_kernel<false><<<1, kThreads, 0, st>>>(a, max_moves, pairs);
+    });
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     *launches += 1;
-    const long long blocks = ((long long)a.B * a.width + 255) / 256;
+    if (small) return e;
     GCA_LAUNCH("paged_compact_table", st,
-               e = launch_pdl(paged_compact_table_kernel, dim3((unsigned)std::min<long long>(blocks, 2048)), 256, 0, st, a));
+               e = launch_pdl(paged_compact_table_kernel, dim3((unsigned)std::min<long long>((entries + 1023) / 1024, 2048)),
+                              256, 0, st, a));
     if (e == cudaSuccess) *launches += 1;
     return e;
 }

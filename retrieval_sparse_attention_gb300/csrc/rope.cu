@@ -15,7 +15,7 @@
 // Work.  A slot is 16 columns of a head whose pairs belong together (8 and 8 columns rot/2
 // apart, or 16 neighbours), two 16-byte vectors of bf16, owned by one thread, so a tensor may be
 // turned in place.  A lane has the same slot of every head it meets (32 / (d/16) heads a step): it
-// forms its eight sines and cosines once a token.  A warp has up to four steps of a token, all
+// forms its eight sines and cosines once a token.  A warp has up to kSteps steps of a token, all
 // loaded before the angles are formed.
 // Bound by memory: reads and writes q and k once.
 #include "attn_sink.cuh"
@@ -25,7 +25,10 @@ namespace gca {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSteps = 4;        // of 32 slots a warp
+// Steps of 32 slots that a warp takes at most (by its registers).  A kernel has as many as it takes: with
+// room for five, three steps are 5% slower (8 x 16K, 12/12 heads of 64: 127 instead of 121 us).
+template <class T>
+constexpr int kSteps = sizeof(T) == 2 ? 5 : 3;
 
 // Sine and cosine of `a` units of 2^-32 turns.
 template <class T>
@@ -156,13 +159,13 @@ struct RopeArgs {
     int inverse;
 };
 
-template <class T, bool INTER>
+template <class T, bool INTER, int STEPS>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     const int lane = threadIdx.x & 31;
     const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const long long t = unit / a.units;
     if (t >= a.T) return;
-    const int first = static_cast<int>(unit - t * a.units) * (32 * kSteps) + lane;
+    const int first = static_cast<int>(unit - t * a.units) * (32 * STEPS) + lane;
     const int j = first & ((1 << a.log2_n) - 1);                 // the same in every step
     int ca, cb;
     columns<INTER>(j, a.rot, ca, cb);
@@ -172,9 +175,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
                              : static_cast<const T*>(k) + (size_t)t * ks + (size_t)(h - a.H) * a.d;
         return const_cast<T*>(p);
     };
-    Vec<T> x[kSteps], y[kSteps];
+    Vec<T> x[STEPS], y[STEPS];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < STEPS; ++i)
         if (first + 32 * i < a.slots) {
             const T* p = at(i, a.q, a.k, a.qs, a.ks);
             x[i].load(p + ca);
@@ -184,10 +187,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
         Turn tn;
         angles<T>(a.freqs, j, a.pos ? __ldg(a.pos + t) : a.start + static_cast<int>(t % a.L), a.m, a.inverse, tn);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) turn<T, INTER>(x[i], y[i], tn);
+        for (int i = 0; i < STEPS; ++i) turn<T, INTER>(x[i], y[i], tn);
     }
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < STEPS; ++i)
         if (first + 32 * i < a.slots) {
             T* p = at(i, a.qo, a.ko, a.qos, a.kos);
             x[i].store(p + ca);
@@ -206,7 +209,7 @@ struct AppendArgs {
 };
 
 // Slots of a row: its queries', its keys', its values'.
-template <bool INTER>
+template <bool INTER, int STEPS>
 __global__ void __launch_bounds__(kThreads) paged_rope_append_kernel(const AppendArgs a) {
     using T = __nv_bfloat16;
     const int lane = threadIdx.x & 31;
@@ -215,13 +218,13 @@ __global__ void __launch_bounds__(kThreads) paged_rope_append_kernel(const Appen
     for (long long b = tid; b < a.B; b += (long long)gridDim.x * kThreads) paged_seq(a.p, (int)b, a.status);
     const long long unit = tid >> 5, row = unit / a.units;
     if (row >= a.p.T) return;
-    const int first = static_cast<int>(unit - row * a.units) * (32 * kSteps) + lane;
+    const int first = static_cast<int>(unit - row * a.units) * (32 * STEPS) + lane;
     const int j = first & ((1 << a.log2_n) - 1);
     int ca, cb;
     columns<INTER>(j, a.rot, ca, cb);
-    Vec<T> x[kSteps], y[kSteps];
+    Vec<T> x[STEPS], y[STEPS];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < STEPS; ++i)
         if (first + 32 * i < a.slots) {
             const int h = (first + 32 * i) >> a.log2_n;
             const T* p = h < a.H ? a.q + row * a.qs + (size_t)h * a.d
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) paged_rope_append_kernel(const Appen
     Turn tn;
     if (16 * j < a.rot) angles<T>(a.freqs, j, pos, a.m, false, tn);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < STEPS; ++i)
         if (first + 32 * i < a.slots) {
             const int h = (first + 32 * i) >> a.log2_n;
             const bool val = h >= a.H + a.Hkv;
@@ -258,6 +261,31 @@ __global__ void __launch_bounds__(kThreads) paged_rope_append_kernel(const Appen
             x[i].store(p + (val ? 16 * j : ca));
             y[i].store(p + (val ? 16 * j + 8 : cb));
         }
+}
+
+// Steps a warp: as few warps a token as max_steps allows, with equally many steps (12/12 heads of 64 into
+// the cache: 144 slots, one warp of five steps), and more warps where all of them would be less than four
+// an SM (a token each of 64 requests, 24/8 heads of 128: 3.1 instead of 3.5 us).
+int steps_of(int T, int slots, int max_steps) {
+    const int n = (slots + 31) / 32;
+    const int per = static_cast<int>(std::min<long long>(max_steps, std::max<long long>(1, (long long)T * n / (4 * 152))));
+    const int units = (n + per - 1) / per;
+    return (n + units - 1) / units;
+}
+
+template <class T, int STEPS>
+void launch_steps(const RopeArgs& a, bool inter, unsigned blocks, cudaStream_t st) {
+    if (inter) rope_kernel<T, true, STEPS><<<blocks, kThreads, 0, st>>>(a);
+    else rope_kernel<T, false, STEPS><<<blocks, kThreads, 0, st>>>(a);
+}
+template <int STEPS>
+void launch_steps(const AppendArgs& a, bool inter, unsigned blocks, cudaStream_t st) {
+    if (inter) paged_rope_append_kernel<true, STEPS><<<blocks, kThreads, 0, st>>>(a);
+    else paged_rope_append_kernel<false, STEPS><<<blocks, kThreads, 0, st>>>(a);
+}
+
+unsigned blocks_of(int T, int units) {
+    return static_cast<unsigned>(((long long)T * units + kThreads / 32 - 1) / (kThreads / 32));
 }
 
 }  // namespace
@@ -273,17 +301,25 @@ cudaError_t launch_rope(const RopeShape& s, const void* q, const void* k, const 
     a.qs = s.q_stride; a.ks = s.k_stride; a.qos = s.qo_stride; a.kos = s.ko_stride;
     a.log2_n = __builtin_ctz(s.d / 16);
     a.slots = (s.H + s.Hkv) << a.log2_n;
-    a.units = (a.slots + 32 * kSteps - 1) / (32 * kSteps);
     a.m = s.mscale;
     a.inverse = s.inverse;
-    const long long blocks = ((long long)s.T * a.units + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    const unsigned n = static_cast<unsigned>(blocks);
+    const bool half = s.dtype == GCA_BF16;
+    const int steps = steps_of(s.T, a.slots, half ? kSteps<__nv_bfloat16> : kSteps<float>);
+    a.units = (a.slots + 32 * steps - 1) / (32 * steps);
+    const unsigned n = blocks_of(s.T, a.units);
     GCA_LAUNCH("rope", st, {
-        if (s.dtype == GCA_BF16 && s.interleaved) rope_kernel<__nv_bfloat16, true><<<n, kThreads, 0, st>>>(a);
-        else if (s.dtype == GCA_BF16) rope_kernel<__nv_bfloat16, false><<<n, kThreads, 0, st>>>(a);
-        else if (s.interleaved) rope_kernel<float, true><<<n, kThreads, 0, st>>>(a);
-        else rope_kernel<float, false><<<n, kThreads, 0, st>>>(a);
+        if (!half) {
+            if (steps == 1) launch_steps<float, 1>(a, s.interleaved, n, st);
+            else if (steps == 2) launch_steps<float, 2>(a, s.interleaved, n, st);
+            else launch_steps<float, 3>(a, s.interleaved, n, st);
+        } else {
+            using T = __nv_bfloat16;
+            if (steps == 1) launch_steps<T, 1>(a, s.interleaved, n, st);
+            else if (steps == 2) launch_steps<T, 2>(a, s.interleaved, n, st);
+            else if (steps == 3) launch_steps<T, 3>(a, s.interleaved, n, st);
+            else if (steps == 4) launch_steps<T, 4>(a, s.interleaved, n, st);
+            else launch_steps<T, 5>(a, s.interleaved, n, st);
+        }
     });
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) *launches += 1;
@@ -304,14 +340,17 @@ cudaError_t launch_paged_rope_append(const SinkShape& s, const RopeShape& r, con
     a.qs = s.q_stride; a.kvs = s.kv_stride;
     a.log2_n = __builtin_ctz(s.d / 16);
     a.slots = (s.H + 2 * s.Hkv) << a.log2_n;
-    a.units = (a.slots + 32 * kSteps - 1) / (32 * kSteps);
     a.m = r.mscale;
     a.status = status;
-    const long long blocks = ((long long)s.T * a.units + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const int steps = steps_of(s.T, a.slots, kSteps<T>);
+    a.units = (a.slots + 32 * steps - 1) / (32 * steps);
+    const unsigned n = blocks_of(s.T, a.units);
     GCA_LAUNCH("paged_rope_append", st, {
-        if (r.interleaved) paged_rope_append_kernel<true><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-        else paged_rope_append_kernel<false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+        if (steps == 1) launch_steps<1>(a, r.interleaved, n, st);
+        else if (steps == 2) launch_steps<2>(a, r.interleaved, n, st);
+        else if (steps == 3) launch_steps<3>(a, r.interleaved, n, st);
+        else if (steps == 4) launch_steps<4>(a, r.interleaved, n, st);
+        else launch_steps<5>(a, r.interleaved, n, st);
     });
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) *launches += 1;
