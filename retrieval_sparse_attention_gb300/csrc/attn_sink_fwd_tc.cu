@@ -592,7 +592,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // A score in log2 units is v sl + so, v being what the tile's registers hold: the product, with a
         // cap its r (attn_sink.cuh: falling in the score, so its least is the greatest score), with a
         // bias the score itself.  A column that a row does not see holds kHidden.
-        constexpr bool CAP = SCORE == kScoreCap, BIAS = SCORE == kScoreBias;
+        constexpr bool CAP = SCORE == kScoreCap, BIAS = SCORE == kScoreBias, FEW = CAP && PAGED;
         constexpr float kHidden = CAP ? INFINITY : -INFINITY;
         const float sl = CAP ? -2.f * a.cap_log2 : BIAS ? 1.f : a.scale_log2, so = CAP ? a.cap_log2 : 0.f;
         const uint64_t cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
@@ -611,6 +611,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         int ts = 0, ko = 0, np = 0, j = 0, j1 = 0, f0 = 0, f1 = 0, fl = 0;
         bool first = true;                              // at the first tile of a part
         bool have = true, live = false, wlive = false;  // a tile to do; this row exists; some row of the warp does
+        bool few = false;                               // no more than eight rows exist
         float m = -INFINITY, l = 0.f;                   // running max (of s * scale * log2(e)) and sum of exp2(. - m)
         // the finished part whose O still sits in tensor memory
         bool pend = false;
@@ -631,6 +632,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 // rows that do not exist are skipped, where a whole warp has no other
                 live = have && row < a.R && rt < sb.part[wg][r].ntok;
                 wlive = __any_sync(0xffffffffu, live);
+                if (FEW) few = sb.part[wg][r].ntok * sc.G <= 8;
                 if (BIAS && have) slope = __ldg(a.slopes + sb.part[wg][r].h * sc.G + rg) * kLog2e;
             }
             const Part& w = sb.part[wg][(np - 1) % kParts];
@@ -681,7 +683,6 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     if (m != -INFINITY) alpha = fast_exp2(m - mts);
                     m = mts;
                 }
-                l *= alpha;
             };
             // once the previous tile's P V has completed, O is stable and can be rescaled
             auto rescale = [&]() {
@@ -703,6 +704,76 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     mbar_arrive(&sb.s_empty[wg]);
                     if (!wwait(&sb.p_empty[wg], empty_par(ts))) break;
                 }
+            } else if (FEW && few) {
+                // Eight rows or less (a token): four lanes a row, each with two columns of eight, so
+                // the arithmetic takes a quarter of the instructions that a row a lane takes.  The row's
+                // statistics then go back to its lane.
+                const int fr = lane >> 2, fc = 2 * (lane & 3);
+                float x[32];
+                {
+                    uint32_t r[64];
+                    tmem_ld_16x256b_x16(ts_addr, r);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        x[2 * i] = __uint_as_float(r[4 * i]);
+                        x[2 * i + 1] = __uint_as_float(r[4 * i + 1]);
+                    }
+                }
+                const int p = w.p0 + fr / sc.G, kbase = w.tile(j) * 128;
+                const bool whole = (j >= f0 && j < f1) || j == fl;
+                auto hide = [&](float with) {
+                    const int lo = p - sc.W + 1 - kbase - fc, hi = p - kbase - fc, cs = min(sc.ns, p + 1) - kbase - fc;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int c = 8 * (i >> 1) + (i & 1);
+                        if ((c < lo || c > hi) && c >= cs) x[i] = with;
+                    }
+                };
+                if (!whole) hide(-INFINITY);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+                    cap_r4<true>(y, cap_in2);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) x[i + u] = y[u];
+                }
+                if (!whole) hide(kHidden);
+                float mt = x[0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mt = greater(mt, x[i]);
+                mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+                mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+                const float m_row = m;
+                m = __shfl_sync(0xffffffffu, m_row, fr);
+                follow(log2_of(mt));
+                const float mu = m == -INFINITY ? 0.f : m, nmu = less(mu);
+                float sum[2] = {0.f, 0.f};
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float e0 = fast_exp2(fmaf(x[2 * i], sl, nmu)), e1 = fast_exp2(fmaf(x[2 * i + 1], sl, nmu));
+                    sum[0] += e0;
+                    sum[1] += e1;
+                    pk[2 * i] = tcx::pack_bf16(e0, e1);
+                    pk[2 * i + 1] = 0u;
+                }
+                float add = sum[0] + sum[1];
+                add += __shfl_xor_sync(0xffffffffu, add, 1);
+                add += __shfl_xor_sync(0xffffffffu, add, 2);
+                // back to a row a lane
+                const int from = 4 * (lane & 7);
+                const float m_new = __shfl_sync(0xffffffffu, m, from), al = __shfl_sync(0xffffffffu, alpha, from);
+                add = __shfl_sync(0xffffffffu, add, from);
+                m = live ? m_new : m_row;
+                alpha = live ? al : 1.f;
+                l = live ? l * alpha + add : 0.f;
+                if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
+                rescale();
+                tmem_st_16x128b_x16(tp_addr, pk);
+                tmem_wait_st();
             } else if (j < w.nar) {
                 // The narrow tile: all sinks in its first columns, and every row behind them.  (A
                 // unit's first tile: no O to rescale.)
@@ -735,6 +806,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     m4[i & 3] = greater(m4[i & 3], __uint_as_float(r[i]));
                 }
                 follow(log2_of(greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]))));
+                l *= alpha;
                 float l4[4];
                 const uint64_t nsl2 = tcx::f2_pack(sl, sl), nnm2 = tcx::f2_pack(less(m), less(m));
                 uint64_t la[2] = {0ull, 0ull};
@@ -815,6 +887,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         mt = greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]));
                     }
                     follow(log2_of(mt));
+                    l *= alpha;
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
                 const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(less(mu), less(mu));
