@@ -508,8 +508,9 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const Part& w = sb.part[r];
             const int j0 = w.j0, j1 = w.j1, nar = w.nar, p0 = w.mt * sc.TM;
             if (j0 == j1) { done = true; break; }
-            const float slope = SCORE == kScoreBias ? __ldg(a.slopes + w.h * sc.G + rg) * kLog2e : 0.f;
+            const float slope_in = SCORE == kScoreBias ? __ldg(a.slopes + w.h * sc.G + rg) : 0.f;
             if (!wwait(&sb.vec_full, full_par(np))) break;
+            const float slope = slope_in * kLog2e;
             const float* vec = reinterpret_cast<const float*>(sm + C::OFF_VEC);
             const float nl2 = vec[row], ndsc = vec[128 + row];
             mbar_arrive(&sb.vec_empty);
@@ -554,6 +555,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                         cap_r16(r1, cap_in2);
                     }
                     auto body = [&](bool msk) {
+                        uint64_t tb = 0;                          // a bias' pair
 #pragma unroll
                         for (int p2 = 0; p2 < 16; ++p2) {
                             const uint32_t* rs = p2 < 8 ? r0 : r1;
@@ -561,9 +563,12 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                             const int tt = 2 * (p2 & 7);
                             float y0, y1;
                             uint64_t bend = 0, nl = nl22;
-                            if (SCORE == kScoreBias)
-                                nl = tcx::ffma2(tcx::f2_pack(32.f * pc + 2 * p2, 32.f * pc + 2 * p2 + 1), tcx::f2_pack(slope, slope),
-                                                tcx::f2_pack(off, off));
+                            if (SCORE == kScoreBias) {          // (eight pairs by additions, as in the forward)
+                                const float k = 32.f * pc + 2 * p2;
+                                tb = p2 % 8 == 0 ? tcx::f2_pack(fmaf(slope, k, off), fmaf(slope, k + 1.f, off))
+                                                 : tcx::fadd2(tb, tcx::f2_pack(2.f * slope, 2.f * slope));
+                                nl = tb;
+                            }
                             tcx::f2_unpack(exponent2<SCORE>(rs[tt], rs[tt + 1], sl2, nl, bend), y0, y1);
                             float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
                             if (msk) {
@@ -995,12 +1000,12 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             for (int j = 0; j < n; ++j, ++u, st.next(C::NSLOT), sp.next(sc.G)) {
                 if ((u & 1) != wg) continue;
                 const int xs = u % C::NX, ys = u % C::NY;
-                const float slope = SCORE == kScoreBias ? __ldg(a.slopes + w.h * sc.G + sp.g) * kLog2e : 0.f;
+                const float slope = SCORE == kScoreBias ? __ldg(a.slopes + w.h * sc.G + sp.g) : 0.f;   // (waited for at its use)
                 // (x_full: the stage has landed too, so the phase of its barrier is the one meant)
                 if (!wwait(&sb.x_full[xs], full_par(u / C::NX)) || !wwait(&sb.st_full[st.i], st.ph)) { ok = false; break; }
                 tc_fence_after();
                 const int qb = sp.block() * 64;
-                const float off = slope * static_cast<float>(s - qb);
+                const float off = slope * kLog2e * static_cast<float>(s - qb);
                 const int c_lo = s - qb, c_hi = last - qb;
                 const uint8_t* vec = sm + C::OFF_ST + st.i * C::SLOT + 2 * C::QTILE;
                 const uint64_t* nl = reinterpret_cast<const uint64_t*>(vec);              // pairs

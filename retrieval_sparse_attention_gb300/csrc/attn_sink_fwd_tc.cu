@@ -589,23 +589,24 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const uint32_t ts_addr = tmem + lane_base + C::COL_S + wg * 128;
         const uint32_t to_addr = tmem + lane_base + C::COL_O + wg * D;
         const uint32_t tp_addr = tmem + lane_base + C::COL_P + wg * C::P_STEP;
-        // A score in log2 units is v sl + so, v being what the tile's registers hold: the product, with a
-        // cap its r (attn_sink.cuh: falling in the score, so its least is the greatest score), with a
-        // bias the score itself.  A column that a row does not see holds kHidden.
+        // A score in log2 units is v sl + so, v being what the tile's registers hold: the product, or with a
+        // cap its r (attn_sink.cuh: falling in the score, so its least is the greatest score); a bias comes
+        // on top of that.  A column that a row does not see holds kHidden.
         constexpr bool CAP = SCORE == kScoreCap, BIAS = SCORE == kScoreBias, FEW = CAP && PAGED;
         constexpr float kHidden = CAP ? INFINITY : -INFINITY;
-        const float sl = CAP ? -2.f * a.cap_log2 : BIAS ? 1.f : a.scale_log2, so = CAP ? a.cap_log2 : 0.f;
+        const float sl = CAP ? -2.f * a.cap_log2 : a.scale_log2, so = CAP ? a.cap_log2 : 0.f;
         const uint64_t cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
-        float slope = 0.f;                              // of this row's head, in log2 units
+        float slope_in = 0.f;                           // of this row's head, as loaded (its wait is at its use)
+        float slope = 0.f;                              // in log2 units
         auto greater = [](float x, float y) { return CAP ? fminf(x, y) : fmaxf(x, y); };
         auto log2_of = [&](float v) { return CAP ? fmaf(v, sl, so) : v * sl; };
         auto less = [&](float max) { return CAP ? so - max : -max; };
-        // products of columns c, c + 1, whose keys are `from` + c, + 1 positions from the row's own, to
-        // scores with their bias
-        auto biased = [&](float& x0, float& x1, int c, uint64_t from) {
-            tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x0, x1), tcx::f2_pack(a.scale_log2, a.scale_log2),
-                                      tcx::ffma2(tcx::f2_pack((float)c, (float)(c + 1)), tcx::f2_pack(slope, slope), from)),
-                           x0, x1);
+        // the bias of columns 2 c and 2 c + 1 less a base, where column 0 has `from` (taken in turn: eight
+        // pairs by additions, which take no constants)
+        auto tilt = [&](uint64_t& b, int c, float from) {
+            b = c % 8 == 0 ? tcx::f2_pack(fmaf(slope, static_cast<float>(2 * c), from), fmaf(slope, static_cast<float>(2 * c + 1), from))
+                           : tcx::fadd2(b, tcx::f2_pack(2.f * slope, 2.f * slope));
+            return b;
         };
 
         int ts = 0, ko = 0, np = 0, j = 0, j1 = 0, f0 = 0, f1 = 0, fl = 0;
@@ -633,7 +634,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 live = have && row < a.R && rt < sb.part[wg][r].ntok;
                 wlive = __any_sync(0xffffffffu, live);
                 if (FEW) few = sb.part[wg][r].ntok * sc.G <= 8;
-                if (BIAS && have) slope = __ldg(a.slopes + sb.part[wg][r].h * sc.G + rg) * kLog2e;
+                if (BIAS && have) slope_in = __ldg(a.slopes + sb.part[wg][r].h * sc.G + rg);
             }
             const Part& w = sb.part[wg][(np - 1) % kParts];
             // the previous part's output leaves while the next part's Q and first S are on their way
@@ -675,6 +676,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
             if (!have || !wwait(&sb.s_full[wg], full_par(ts))) break;
             tc_fence_after();
+            if (BIAS) slope = slope_in * kLog2e;
             float alpha = 1.f;
             // the running maximum follows a tile's (in log2 units) only past a margin
             auto follow = [&](float mts) {
@@ -789,32 +791,35 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     cap_r16(r, cap_in2);
                     cap_r16(r + 16, cap_in2);
                 }
-                if constexpr (BIAS) {
-                    const float off = slope * static_cast<float>(-w.p0 - rt);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float x0 = __uint_as_float(r[i]), x1 = __uint_as_float(r[i + 1]);
-                        biased(x0, x1, i, tcx::f2_pack(off, off));
-                        r[i] = __float_as_uint(x0);
-                        r[i + 1] = __float_as_uint(x1);
-                    }
-                }
                 float m4[4] = {kHidden, kHidden, kHidden, kHidden};
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    r[i] = (nvis >> i & 1u) ? r[i] : (CAP ? 0x7f800000u : 0xff800000u);
-                    m4[i & 3] = greater(m4[i & 3], __uint_as_float(r[i]));
+                for (int i = 0; i < 32; ++i) r[i] = (nvis >> i & 1u) ? r[i] : (CAP ? 0x7f800000u : 0xff800000u);
+                const uint64_t nsl2 = tcx::f2_pack(sl, sl);
+                const float off = slope * static_cast<float>(-w.p0 - rt);
+                uint64_t tb = 0;
+                if constexpr (BIAS) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float y0, y1;
+                        tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), nsl2,
+                                                  tilt(tb, i, off)), y0, y1);
+                        m4[i & 3] = fmaxf(m4[i & 3], fmaxf(y0, y1));
+                    }
+                    follow(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) m4[i & 3] = greater(m4[i & 3], __uint_as_float(r[i]));
+                    follow(log2_of(greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]))));
                 }
-                follow(log2_of(greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]))));
                 l *= alpha;
                 float l4[4];
-                const uint64_t nsl2 = tcx::f2_pack(sl, sl), nnm2 = tcx::f2_pack(less(m), less(m));
+                const uint64_t nnm2 = tcx::f2_pack(less(m), less(m));
                 uint64_t la[2] = {0ull, 0ull};
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float y0, y1;
                     tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                                              nsl2, nnm2), y0, y1);
+                                              nsl2, BIAS ? tilt(tb, i, off - m) : nnm2), y0, y1);
                     const uint64_t e = tcx::f2_pack(fast_exp2(y0), fast_exp2(y1));
                     la[i & 1] = tcx::fadd2(la[i & 1], e);
                     pk[i] = tcx::pack_bf16x2(e);
@@ -827,7 +832,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 tmem_wait_st();
             } else {
                 // The row of S into registers at once, the maximum from the load.
-                float x[128];
+                float x[128], off = 0.f;                // off: the bias of column 0
                 {
                     uint32_t r[2][64];
                     float mc[2];
@@ -871,32 +876,64 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         }
                         mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));    // r of the greatest product
                     }
-                    if constexpr (BIAS) {
-                        const float off = slope * static_cast<float>(kbase - p);
-#pragma unroll
-                        for (int i = 0; i < 128; i += 2) biased(x[i], x[i + 1], i, tcx::f2_pack(off, off));
-                    }
                     if (!whole) hide(kHidden);
-                    // the maximum over all columns bounds that over the visible ones: only where it
-                    // would move the running one (or is no number) is the latter needed (with a bias
-                    // the products' maximum says nothing: always)
-                    if (BIAS || (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2)))) {
-                        float m4[4] = {kHidden, kHidden, kHidden, kHidden};
+                    if constexpr (BIAS) {
+                        // Bounds of the greatest scores of the columns' halves: the greatest product and the
+                        // greatest bias (none above 0 where it falls).  Where the bound moves the
+                        // running maximum it takes its place, unless it may lie more than 2^60 above the
+                        // true one (sums would be too small): in tiles with hidden columns their
+                        // products are left out first, and a bias so steep within 64 columns
+                        // takes the scores themselves.
+                        off = slope * static_cast<float>(kbase - p);
+                        const float top0 = slope > 0.f ? fmaf(63.f, slope, off) : off;
+                        const float top1 = slope > 0.f ? fminf(fmaf(127.f, slope, off), 0.f) : fmaf(64.f, slope, off);
+                        auto bound = [&]() { return fmaxf(fmaf(mc[0], sl, top0), fmaf(mc[1], sl, top1)); };
+                        mt = bound();
+                        if (!whole && __any_sync(0xffffffffu, !(mt <= m + kRescaleLog2))) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) m4[i & 3] = greater(m4[i & 3], x[i]);
-                        mt = greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]));
+                            for (int h = 0; h < 2; ++h) {
+                                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                                for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[64 * h + i]);
+                                mc[h] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            }
+                            mt = bound();
+                        }
+                        if (__any_sync(0xffffffffu, fabsf(slope) * 63.f > 60.f && !(mt <= m + kRescaleLog2))) {
+                            mt = -INFINITY;
+                            uint64_t tb = 0;
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) {
+                                float y0, y1;
+                                tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x[2 * c], x[2 * c + 1]), tcx::f2_pack(sl, sl), tilt(tb, c, off)),
+                                               y0, y1);
+                                mt = fmaxf(mt, fmaxf(y0, y1));
+                            }
+                        }
+                        follow(mt);
+                    } else {
+                        // the maximum over all columns bounds that over the visible ones: only where it
+                        // would move the running one (or is no number) is the latter needed
+                        if (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2))) {
+                            float m4[4] = {kHidden, kHidden, kHidden, kHidden};
+#pragma unroll
+                            for (int i = 0; i < 128; ++i) m4[i & 3] = greater(m4[i & 3], x[i]);
+                            mt = greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]));
+                        }
+                        follow(log2_of(mt));
                     }
-                    follow(log2_of(mt));
                     l *= alpha;
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
                 const uint64_t sl2 = tcx::f2_pack(sl, sl), nmu2 = tcx::f2_pack(less(mu), less(mu));
+                uint64_t tb = 0;
+                auto addend = [&](int c) { return BIAS ? tilt(tb, c, off - mu) : nmu2; };    // of columns 2 c, 2 c + 1
                 uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t pka[32];                       // the first 64 keys' P, formed before the wait for the P buffer
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     float y0, y1;
-                    tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x[2 * c], x[2 * c + 1]), sl2, nmu2), y0, y1);
+                    tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x[2 * c], x[2 * c + 1]), sl2, addend(c)), y0, y1);
                     const float e0 = fast_exp2(y0);
                     const float e1 = fast_exp2(y1);
                     acc2[c & 3] = tcx::fadd2(acc2[c & 3], tcx::f2_pack(e0, e1));
@@ -921,7 +958,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     for (int u = 0; u < 8; ++u) {
                         float y0, y1;
                         const uint64_t s2 = tcx::f2_pack(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]);
-                        tcx::f2_unpack(tcx::ffma2(s2, sl2, nmu2), y0, y1);
+                        tcx::f2_unpack(tcx::ffma2(s2, sl2, addend(8 * c + u)), y0, y1);
                         const float e0 = fast_exp2(y0);
                         const float e1 = fast_exp2(y1);
                         acc2[u & 3] = tcx::fadd2(acc2[u & 3], tcx::f2_pack(e0, e1));
