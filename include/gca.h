@@ -345,10 +345,11 @@ gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q
  *   softcap > 0:  softcap tanh(x / softcap), which keeps every score within +-softcap
  *                 (a product of +-inf counts as +-softcap);
  *   slopes:       x - slopes[h] (t - s) for query head h at distance t - s >= 0.
- * Masks, lse, layouts, workspaces and everything else are those of the plain
- * calls; so are the gradients, which pass through the transform (the slopes are
- * constants).  A score is off by 2^-20 softcap at most besides the product's own
- * rounding.
+ * Masks, lse, layouts and everything else are those of the plain calls, the forwards'
+ * workspaces too.  The gradients pass through the transform (the slopes are constants);
+ * they need gca_swa_sink_bwd_scored_workspace_size() bytes and take delta_t as
+ * sum_s p_ts dout_t . v_s (o gives a first value of it, which its rounding is put right
+ * of).  A score is off by 2^-20 softcap at most besides the product's own rounding.
  * softcap: 0 (none) or 2^-10 .. 2^10, else GCA_ERR_UNSUPPORTED (GCA_ERR_INVALID_ARG
  * below 0 or not finite).  Both at once: GCA_ERR_UNSUPPORTED.  Neither, or a null
  * pointer in place of the struct: the plain call.
@@ -361,6 +362,9 @@ typedef struct {
 gca_status_t gca_swa_sink_fwd_scored(const gca_swa_sink_params_t* params, const gca_score_t* score,
                                      const void* q, const void* k, const void* v, void* o,
                                      float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace gca_swa_sink_bwd_scored needs (0 for invalid parameters). */
+size_t gca_swa_sink_bwd_scored_workspace_size(const gca_swa_sink_params_t* params);
 
 gca_status_t gca_swa_sink_bwd_scored(const gca_swa_sink_params_t* params, const gca_score_t* score,
                                      const void* q, const void* k, const void* v, const void* o,

@@ -29,7 +29,7 @@ EXPORTED = ("gca_score_topk", "gca_fwd", "gca_bwd_workspace_size", "gca_bwd",
             "gca_swa_sink_fwd_workspace_size", "gca_swa_sink_fwd",
             "gca_swa_sink_bwd_workspace_size", "gca_swa_sink_bwd", "gca_paged_append",
             "gca_paged_attn_workspace_size", "gca_paged_attn", "gca_swa_sink_fwd_scored",
-            "gca_swa_sink_bwd_scored", "gca_paged_attn_scored", "gca_rope", "gca_paged_rope_append",
+            "gca_swa_sink_bwd_scored_workspace_size", "gca_swa_sink_bwd_scored", "gca_paged_attn_scored", "gca_rope", "gca_paged_rope_append",
             "gca_page_pool_ints", "gca_page_pool_init", "gca_paged_reserve", "gca_paged_fork",
             "gca_paged_compact", "gca_paged_copy", "gca_debug_stall_next_decode")
 
@@ -133,6 +133,7 @@ def load() -> ctypes.CDLL:
             "gca_paged_attn": ([ctypes.POINTER(GcaPagedParams)] + [vp] * 9 + [sz, vp], i32),
             "gca_swa_sink_fwd_scored": ([ctypes.POINTER(GcaSwaSinkParams),
                                          ctypes.POINTER(GcaScore)] + [vp] * 6 + [sz, vp], i32),
+            "gca_swa_sink_bwd_scored_workspace_size": ([ctypes.POINTER(GcaSwaSinkParams)], sz),
             "gca_swa_sink_bwd_scored": ([ctypes.POINTER(GcaSwaSinkParams),
                                          ctypes.POINTER(GcaScore)] + [vp] * 10 + [sz, vp], i32),
             "gca_paged_attn_scored": ([ctypes.POINTER(GcaPagedParams), ctypes.POINTER(GcaScore)] +

@@ -384,6 +384,10 @@ def gca_swa_sink_bwd(params: GcaSwaSinkParams, q, k, v, o, lse, dout, dq, dk, dv
         _raw_stream(stream, q.get_device())))
 
 
+def gca_swa_sink_bwd_scored_workspace_size(params: GcaSwaSinkParams) -> int:
+    return int(_lib.load().gca_swa_sink_bwd_scored_workspace_size(ctypes.byref(params)))
+
+
 def gca_swa_sink_bwd_scored(params: GcaSwaSinkParams, score: GcaScore, q, k, v, o, lse, dout, dq,
                             dk, dv, workspace, stream=None):
     _check("gca_swa_sink_bwd_scored", _lib.load().gca_swa_sink_bwd_scored(
@@ -417,7 +421,8 @@ def _swa_sink_plan(qs, qst, ks, kst, vs, vst, qt, kt, vt, window, sinks, attn_sc
     p = make_swa_sink_params(B=B, L=L, H=H, Hkv=ks[2], d=d, window=min(window, _INT_MAX),
                              sinks=min(sinks, _INT_MAX), dtype=qt, attn_scale=attn_scale,
                              q_stride=_token_stride(qs, qst), kv_stride=step)
-    return p, gca_swa_sink_fwd_workspace_size(p), gca_swa_sink_bwd_workspace_size(p)
+    return (p, gca_swa_sink_fwd_workspace_size(p), gca_swa_sink_bwd_workspace_size(p),
+            gca_swa_sink_bwd_scored_workspace_size(p))
 
 
 def _swa_sink_args(q, k, v, window, sinks, attn_scale):
@@ -451,7 +456,7 @@ def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, works
     the scores by a tanh, ``slopes`` [H] fp32 lowers them by the distance (one of the two)."""
     index = _same_device(q, k, v, workspace)
     score = _score(softcap, slopes, q.shape[-2], index)
-    p, need, _ = _swa_sink_args(q, k, v, window, sinks, attn_scale)
+    p, need, _, _ = _swa_sink_args(q, k, v, window, sinks, attn_scale)
     dev = q.device
     ws = _workspace(workspace, need, dev)
     o = _empty_like(q)
@@ -468,12 +473,12 @@ def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, worksp
     """Gradients of swa_sink_fwd: returns dense (dq, dk, dv)."""
     index = _same_device(q, k, v, o, lse, dout, workspace)
     score = _score(softcap, slopes, q.shape[-2], index)
-    p, _, need = _swa_sink_args(q, k, v, window, sinks, attn_scale)
+    p, _, plain, scored = _swa_sink_args(q, k, v, window, sinks, attn_scale)
     _dense(o, q.shape, q.dtype, "o")
     _dense(dout, q.shape, q.dtype, "dout")
     _dense(lse, q.shape[:3], torch.float32, "lse")
     dev = q.device
-    ws = _workspace(workspace, need, dev)
+    ws = _workspace(workspace, plain if score is None else scored, dev)
     dq, dk, dv = _empty_like(q), _empty_like(k), _empty_like(v)
     if score is None:
         gca_swa_sink_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, ws)

@@ -407,7 +407,13 @@ gca_status_t gca_swa_sink_fwd_scored(const gca_swa_sink_params_t* params, const 
 size_t gca_swa_sink_bwd_workspace_size(const gca_swa_sink_params_t* params) {
     SinkShape s;
     if (swa_sink_check(params, sink_bwd_supported, &s) != GCA_OK) return 0;
-    return sink_bwd_workspace_bytes(s);
+    return sink_bwd_workspace_bytes(s, false);
+}
+
+size_t gca_swa_sink_bwd_scored_workspace_size(const gca_swa_sink_params_t* params) {
+    SinkShape s;
+    if (swa_sink_check(params, sink_bwd_supported, &s) != GCA_OK) return 0;
+    return sink_bwd_workspace_bytes(s, true);
 }
 
 gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q, const void* k,
@@ -427,7 +433,8 @@ gca_status_t gca_swa_sink_bwd_scored(const gca_swa_sink_params_t* params, const 
     if (r != GCA_OK) return r;
     if ((r = score_check(score, &s)) != GCA_OK) return r;
     if ((r = check_ptrs({q, k, v, o, lse, dout, dq, dk, dv})) != GCA_OK) return r;
-    if ((r = check_workspace(workspace, ws_bytes, sink_bwd_workspace_bytes(s))) != GCA_OK) return r;
+    const bool scored = s.softcap > 0.f || s.slopes;
+    if ((r = check_workspace(workspace, ws_bytes, sink_bwd_workspace_bytes(s, scored))) != GCA_OK) return r;
     int* st = status_word();
     if (!st) return GCA_ERR_CUDA;
     int n = 0;

@@ -82,7 +82,9 @@ struct BwdArgs {
     float *nlA, *ndA;        // [B * Hkv * nMT][128]: rows of the query tiles
     float *nlB, *ndB;        // [B * H][Lp]
     __nv_bfloat16 *dq, *dk, *dv;
-    float* partA;            // [2 * workers][D / 4][128][4]
+    float* partA;            // [2 * workers][D / 4][128][4], exact: [2 * workers][2][D / 4][128][4]
+    float* sigA;             // exact: [2 * workers][128], sums of the parts' rows
+    float* sigx;             // exact: [workers][2][128], from one math warpgroup to the other
     float* partB;            // [2 * workers][2][D / 4][128][4]: dK, dV
     int4 *tailA, *tailB;     // [workers]: the item (b, i, h, 1) whose first part this worker holds, or .w = 0
     int *headA, *headB;      // [workers]: 0, 1 (holds the last part of an earlier worker's item), 2 (a middle part)
@@ -164,6 +166,23 @@ __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     }
 }
 
+// 32 columns of an fp32 accumulator (a row a lane), less `f` times another's, in place.
+__device__ __forceinline__ void less_rows32(uint32_t acc, uint32_t other, float f) {
+    uint32_t x[32], y[32];
+    tmem_ld_32x32b_x32(acc, x);
+    tmem_ld_32x32b_x32(other, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t z[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            z[i] = __float_as_uint(fmaf(-f, __uint_as_float(y[16 * h + i]), __uint_as_float(x[16 * h + i])));
+        tmem_st_32x32b_x16(acc + 16 * h, z);
+    }
+    tmem_wait_st();
+}
+
 // N columns of this lane's row of an fp32 accumulator to a [N / 4][128][4] array of the
 // workspace (rows side by side: the lanes of a store write 512 consecutive bytes).
 template <int N>
@@ -182,6 +201,15 @@ __device__ __forceinline__ void store_rows_f32(uint32_t taddr, float* dst, int r
 }
 
 // ============================================================================ pass A (dQ)
+// Exact delta, where the scores are transformed.  delta_t = dO_t . o_t takes o as the forward rounded it: its
+// P to bf16, then o.  Where a few keys have most of a row's weight, dP - delta is a difference of near
+// numbers, and that rounding is what limits the gradients (16 tokens with a distance bias: 5.1e-3 of dK's
+// norm, of which the gradients' own rounding is 1.7e-3).  But sum_s p_ts = 1, so
+//   sigma_t = a sum_s p_ts (dP_ts - delta~_t) = a (delta_t - delta~_t)
+// is what the rounded delta~ lacks, in fp32 from numbers that pass A has at hand, and with
+// k_t = sum_s p_ts (1 - tanh^2) K_s, a product more beside ds K,
+//   dQ_t = sum_s ds~_ts K_s - sigma_t k_t.
+// Pass B, which comes after, takes the delta that pass A has put right.
 namespace pa {
 
 // 64-key tiles of a query tile: nsk tiles of sinks from tile 0 on, then k0 .. of the window.
@@ -205,7 +233,7 @@ struct __align__(16) Part {
     __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : k0 + j - nsk; }
 };
 
-template <int D>
+template <int D, bool EXACT>
 struct Cfg {
     static constexpr int SUB = D / 64;
     static constexpr int STILE = 128 * 128, SKEY = 64 * 128;      // bytes of a sub-tile: 128 rows, 64 rows
@@ -217,10 +245,12 @@ struct Cfg {
     static constexpr int OFF_KV = IBUF * ITEM;
     static constexpr int OFF_VEC = OFF_KV + NSLOT * SLOT;         // two vectors of 128 floats
     static constexpr int SMEM = OFF_VEC + 1024 + 1024;
-    static constexpr int NX = 3, NY = 3;                          // 64-column buffers of S (then ds) and of dP
-    static constexpr int NACC = D == 64 ? 2 : 1;
+    // 64-column buffers of S (then ds, exact: and p beside it) and of dP
+    static constexpr int NX = EXACT && D == 128 ? 2 : 3, NY = NX;
+    static constexpr int NACC = D == 64 && !EXACT ? 2 : 1;
+    static constexpr int ACC = EXACT ? 2 * D : D;                 // columns of an accumulator: dQ, exact: and k
     static constexpr uint32_t COL_X = 0, COL_Y = NX * 64, COL_ACC = COL_Y + NY * 64;
-    static_assert(COL_ACC + NACC * D <= TMEM_COLS, "tensor memory");
+    static_assert(COL_ACC + NACC * ACC <= TMEM_COLS, "tensor memory");
 };
 
 template <class C>
@@ -233,6 +263,7 @@ struct __align__(16) Bars {
     uint64_t x_full[C::NX], x_empty[C::NX], y_empty[C::NY];
     uint64_t p_full[4];
     uint64_t o_full[2], o_empty[2];      // per storing warpgroup (it sees every phase); per accumulator
+    uint64_t sig_full[2], sig_empty[2];  // exact: the other warpgroup's sigma of a part, per storing warpgroup
     uint64_t done[3];
     uint32_t tmem;
     int error;
@@ -267,7 +298,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const BwdArgs a) {
-    using C = Cfg<D>;
+    constexpr bool EXACT = SCORE != kScorePlain;
+    using C = Cfg<D, EXACT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -302,6 +334,10 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sb.o_full[i], 1);
             mbar_init(&sb.o_empty[i], 128);
+            if (EXACT) {
+                mbar_init(&sb.sig_full[i], 128);
+                mbar_init(&sb.sig_empty[i], 128);
+            }
         }
         for (int i = 0; i < 3; ++i) mbar_init(&sb.done[i], 1);
         fence_barrier_init();
@@ -447,8 +483,13 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
                         if (ks == 2 && j < nar) break;
-                        tc::mma_bf16_ts(tmem + C::COL_ACC + ob * D, tmem + C::COL_X + xs * 64 + 8 * ks, kd + 128 * ks, id_acc,
-                                        (ks > 0 || j > 0) ? 1u : 0u);
+                        const uint32_t more = (ks > 0 || j > 0) ? 1u : 0u, acc = tmem + C::COL_ACC + ob * C::ACC;
+                        if constexpr (EXACT) {
+                            tc::mma_bf16_ts(acc, tmem + C::COL_X + xs * 64 + 16 * ks, kd + 128 * ks, id_acc, more);
+                            tc::mma_bf16_ts(acc + D, tmem + C::COL_X + xs * 64 + 16 * ks + 8, kd + 128 * ks, id_acc, more);
+                        } else {
+                            tc::mma_bf16_ts(acc, tmem + C::COL_X + xs * 64 + 8 * ks, kd + 128 * ks, id_acc, more);
+                        }
                     }
                     mma_commit(&sb.x_empty[xs]);
                     mma_commit(&sb.kv_empty[kv.i]);       // S and dP are complete before ds exists
@@ -479,22 +520,52 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         // the next one, so the wait for the part's last product overlaps work
         int pend = -1, pend_slot = -1;                // part number; workspace slot or -1
         int pend_row = -1;                            // token * H + head, or -1: no such row
+        // exact: this warpgroup's sigma of the part, and where -a delta~ stands for pass B
+        float sigma = 0.f;
+        float* pend_nd = nullptr;
+        float* const sigx = a.sigx + blockIdx.x * 256 + row;
         auto epilogue = [&]() {
             const int ob = pend % C::NACC;
+            if (EXACT) {
+                const int w = pend & 1;               // (this warpgroup)
+                if (!wwait(&sb.sig_full[w], full_par(pend >> 1))) return false;
+                sigma += *reinterpret_cast<volatile float*>(sigx + 128 * w);
+                mbar_arrive(&sb.sig_empty[w]);
+                if (pend_row >= 0) {
+                    if (pend_slot < 0) *pend_nd -= sigma;
+                    else a.sigA[pend_slot * 128 + row] = sigma;
+                }
+            }
             if (!wwait(&sb.o_full[pend & 1], full_par(pend >> 1))) return false;
             tc_fence_after();
-            const uint32_t acc = tmem + lane_base + C::COL_ACC + ob * D;
+            const uint32_t acc = tmem + lane_base + C::COL_ACC + ob * C::ACC;
             if (pend_slot < 0) {
-                // (into registers first: the accumulator is free before the stores)
-                uint32_t pk[D / 32][16];
+                if constexpr (EXACT) {
+#pragma unroll 1
+                    for (int ci = 0; ci < D / 32; ++ci) {
+                        uint32_t pk[16];
+                        less_rows32(acc + 32 * ci, acc + D + 32 * ci, sigma);
+                        load_rows32(acc + 32 * ci, 1.f, pk);
+                        if (ci + 1 == D / 32) {
+                            tc_fence_before();
+                            mbar_arrive(&sb.o_empty[ob]);
+                        }
+                        store_rows32(pk, a.dq + 32 * ci, D, pend_row);
+                    }
+                } else {
+                    // (into registers first: the accumulator is free before the stores)
+                    uint32_t pk[D / 32][16];
 #pragma unroll
-                for (int ci = 0; ci < D / 32; ++ci) load_rows32(acc + 32 * ci, 1.f, pk[ci]);
-                tc_fence_before();
-                mbar_arrive(&sb.o_empty[ob]);
+                    for (int ci = 0; ci < D / 32; ++ci) load_rows32(acc + 32 * ci, 1.f, pk[ci]);
+                    tc_fence_before();
+                    mbar_arrive(&sb.o_empty[ob]);
 #pragma unroll
-                for (int ci = 0; ci < D / 32; ++ci) store_rows32(pk[ci], a.dq + 32 * ci, D, pend_row);
+                    for (int ci = 0; ci < D / 32; ++ci) store_rows32(pk[ci], a.dq + 32 * ci, D, pend_row);
+                }
             } else {
-                store_rows_f32<D>(acc, a.partA + (size_t)pend_slot * 128 * D, row, pend_row >= 0);
+                float* part = a.partA + (size_t)pend_slot * 128 * C::ACC;
+                store_rows_f32<D>(acc, part, row, pend_row >= 0);
+                if (EXACT) store_rows_f32<D>(acc + D, part + 128 * D, row, pend_row >= 0);
                 tc_fence_before();
                 mbar_arrive(&sb.o_empty[ob]);
             }
@@ -516,6 +587,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             mbar_arrive(&sb.vec_empty);
             const uint64_t nl22 = tcx::f2_pack(nl2, nl2), ndsc2 = tcx::f2_pack(ndsc, ndsc);
             const int p = p0 + rt, plast = min(sc.L, p0 + sc.TM) - 1;
+            uint64_t sg2 = 0ull;                          // exact: sums of p times a (dP - delta~)
 #pragma unroll 1
             for (int j = j0; j < j1; ++j, ++u) {
                 if ((u & 1) != wg) continue;
@@ -549,7 +621,7 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                         mbar_arrive(&sb.y_empty[ys]);
                     }
                     const uint32_t vis = (below(c_hi + 1 - 32 * pc) & ~below(c_lo - 32 * pc)) | below(c_s - 32 * pc);
-                    uint32_t pk[16];
+                    uint32_t pk[16], pp[16];                      // ds, and exact: p (with a cap times r (1 - r))
                     if constexpr (SCORE == kScoreCap) {
                         cap_r16(r0, cap_in2);
                         cap_r16(r1, cap_in2);
@@ -578,13 +650,30 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                             const uint64_t gd = tcx::ffma2(
                                 tcx::f2_pack(__uint_as_float(rd[tt]), __uint_as_float(rd[tt + 1])), sc2, ndsc2);
                             uint64_t ev = tcx::f2_pack(e0, e1);
+                            if (EXACT) sg2 = tcx::ffma2(ev, gd, sg2);
                             if (SCORE == kScoreCap) ev = tcx::fmul2(ev, bend);
+                            if (EXACT) pp[p2] = tcx::pack_bf16x2(ev);
                             pk[p2] = tcx::pack_bf16x2(tcx::fmul2(ev, gd));
                         }
                     };
                     if (edge) body(true);
                     else body(false);
-                    tmem_st_32x32b_x16(xb + 16 * pc, pk);         // ds over S columns that have been read
+                    // over S columns that have been read: ds; exact: ds and p of 16 keys each, side by side
+                    if constexpr (EXACT) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t d8[8], p8[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                d8[i] = pk[8 * h + i];
+                                p8[i] = pp[8 * h + i];
+                            }
+                            tmem_st_32x32b_x8(xb + 32 * pc + 16 * h, d8);
+                            tmem_st_32x32b_x8(xb + 32 * pc + 16 * h + 8, p8);
+                        }
+                    } else {
+                        tmem_st_32x32b_x16(xb + 16 * pc, pk);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -592,6 +681,12 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 if (pend >= 0 && !epilogue()) { ok = false; break; }
             }
             if (!ok) break;
+            float part_sigma = 0.f;
+            if (EXACT) {
+                float s0, s1;
+                tcx::f2_unpack(sg2, s0, s1);
+                part_sigma = s0 + s1;
+            }
             if ((np & 1) == wg) {
                 // (a part shorter than two steps may leave this warpgroup's last one pending)
                 if (pend >= 0 && !epilogue()) break;
@@ -599,6 +694,14 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 pend_slot = w.slot;
                 const bool live = row < a.R && p <= plast;
                 pend_row = live ? (w.b * sc.L + p) * sc.H + w.h * sc.G + rg : -1;
+                if (EXACT) {
+                    sigma = part_sigma;
+                    pend_nd = a.ndB + ((size_t)w.b * sc.H + w.h * sc.G + rg) * a.Lp + p;
+                }
+            } else if (EXACT) {
+                if (!wwait(&sb.sig_empty[np & 1], empty_par(np >> 1))) break;
+                *reinterpret_cast<volatile float*>(sigx + 128 * (np & 1)) = part_sigma;
+                mbar_arrive(&sb.sig_full[np & 1]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.part_empty[r]);
@@ -1097,12 +1200,14 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 
 // Adds up the parts of the items that were cut (10 to 18 us, launch and latency), in the order
 // of the stream: blocks (w, *, *) the item that begins in worker w's share and goes on in the next ones (pass A for
-// blockIdx.z = 0, pass B's dK and dV for 1 and 2).
-template <int D>
-__global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int workers) {
+// blockIdx.z + z0 = 0, pass B's dK and dV for 1 and 2).  EXACT: pass A's before pass B, with its delta.
+template <int D, bool EXACT>
+__global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int workers, int z0) {
+    pdl_release();
     pdl_wait();
     const SinkSched& sc = a.s;
-    const bool pass_a = blockIdx.z == 0;
+    const int z = blockIdx.z + z0;
+    const bool pass_a = z == 0;
     const int w = blockIdx.x;
     const int4 it = (pass_a ? a.tailA : a.tailB)[w];
     if (it.w == 0) return;
@@ -1110,34 +1215,46 @@ __global__ void __launch_bounds__(256) sink_bwd_join_kernel(const BwdArgs a, int
     constexpr int VEC = D / 4;
     constexpr int ROWS = 256 / VEC;
     const int row = blockIdx.y * ROWS + threadIdx.x % ROWS, c = threadIdx.x / ROWS;
-    size_t orow;
+    size_t orow, ndrow = 0;
     if (pass_a) {
         const int rt = row / sc.G, t = it.y * sc.TM + rt;
         if (row >= a.R || t >= sc.L) return;
         orow = (size_t)(it.x * sc.L + t) * sc.H + it.z * sc.G + (row - rt * sc.G);
+        ndrow = ((size_t)it.x * sc.H + it.z * sc.G + (row - rt * sc.G)) * a.Lp + t;
     } else {
         const int s = it.y * 128 + row;
         if (s >= sc.L) return;
         orow = (size_t)(it.x * sc.L + s) * sc.Hkv + it.z;
     }
-    const size_t slot_rows = pass_a ? 128 : 256;
-    const float* base = pass_a ? a.partA : a.partB + (blockIdx.z == 2 ? 128 * D : 0);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const size_t slot_rows = pass_a && !EXACT ? 128 : 256;
+    const float* base = pass_a ? a.partA : a.partB + (z == 2 ? 128 * D : 0);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), kk = acc;
+    float sigma = 0.f;
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
         const size_t slot = k == 0 ? 2 * w + 1 : 2 * (w + k);
         const float4 x = reinterpret_cast<const float4*>(base + slot * slot_rows * D)[c * 128 + row];
         acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+        if (EXACT && pass_a) {
+            const float4 y = reinterpret_cast<const float4*>(base + (slot * slot_rows + 128) * D)[c * 128 + row];
+            kk.x += y.x; kk.y += y.y; kk.z += y.z; kk.w += y.w;
+            sigma += a.sigA[slot * 128 + row];
+        }
     }
-    __nv_bfloat16* dst = pass_a ? a.dq : blockIdx.z == 1 ? a.dk : a.dv;
+    if (EXACT && pass_a) {
+        acc = make_float4(fmaf(-sigma, kk.x, acc.x), fmaf(-sigma, kk.y, acc.y), fmaf(-sigma, kk.z, acc.z),
+                          fmaf(-sigma, kk.w, acc.w));
+        if (c == 0) a.ndB[ndrow] -= sigma;
+    }
+    __nv_bfloat16* dst = pass_a ? a.dq : z == 1 ? a.dk : a.dv;
     reinterpret_cast<uint2*>(dst + orow * D)[c] = make_uint2(tcx::pack_bf16(acc.x, acc.y), tcx::pack_bf16(acc.z, acc.w));
 }
 
 struct Layout {
-    size_t nlA, ndA, nlB, ndB, partA, partB, tailA, tailB, headA, headB, total;
+    size_t nlA, ndA, nlB, ndB, partA, partB, tailA, tailB, headA, headB, sigA, sigx, total;
     int TM, R, nMT, Lp;
 };
-Layout layout(const SinkShape& s) {
+Layout layout(const SinkShape& s, bool exact) {
     Layout w;
     const int G = s.H / s.Hkv;
     w.TM = 128 / G < s.L ? 128 / G : s.L;
@@ -1155,12 +1272,14 @@ Layout layout(const SinkShape& s) {
     w.ndA = take(va);
     w.nlB = take(vb);
     w.ndB = take(vb);
-    w.partA = take((size_t)2 * kMaxCtas * 128 * s.d * 4);
+    w.partA = take((size_t)2 * kMaxCtas * 128 * s.d * (exact ? 8 : 4));
     w.partB = take((size_t)2 * kMaxCtas * 256 * s.d * 4);
     w.tailA = take(kMaxCtas * 16);
     w.tailB = take(kMaxCtas * 16);
     w.headA = take(kMaxCtas * 4);
     w.headB = take(kMaxCtas * 4);
+    w.sigA = take(exact ? (size_t)2 * kMaxCtas * 128 * 4 : 0);
+    w.sigx = take(exact ? (size_t)kMaxCtas * 256 * 4 : 0);
     w.total = at;
     return w;
 }
@@ -1168,12 +1287,13 @@ Layout layout(const SinkShape& s) {
 template <int D, int SCORE>
 cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[8], cudaStream_t st,
                    int* launches) {
+    constexpr bool EXACT = SCORE != kScorePlain;
     static LaunchSetup setup;
     int sms = 0;
     cudaError_t e = setup.once(
         [] {
             const cudaError_t r = cudaFuncSetAttribute(pa::sink_bwd_q_kernel<D, SCORE>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, pa::Cfg<D>::SMEM);
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, pa::Cfg<D, EXACT>::SMEM);
             if (r != cudaSuccess) return r;
             // (a build that gave the kernel fewer registers would wait forever at the split: refuse it)
             cudaFuncAttributes fa;
@@ -1189,15 +1309,23 @@ cudaError_t launch(const SinkShape& s, const BwdArgs& a, const CUtensorMap (&m)[
     GCA_LAUNCH("sink_bwd_vec", st, sink_bwd_vec_kernel<D, SCORE><<<vgrid, 256, 0, st>>>(a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     GCA_LAUNCH("sink_bwd_q", st,
-               e = launch_pdl(pa::sink_bwd_q_kernel<D, SCORE>, dim3(grid), kThreadsA, pa::Cfg<D>::SMEM, st, m[0], m[1], m[2], m[3], a));
+               e = launch_pdl(pa::sink_bwd_q_kernel<D, SCORE>, dim3(grid), kThreadsA, pa::Cfg<D, EXACT>::SMEM, st, m[0], m[1], m[2], m[3], a));
     if (e != cudaSuccess) return e;
+    const int joins = 128 * D / 1024;
+    if (EXACT && !a.wholeA) {
+        GCA_LAUNCH("sink_bwd_join", st,
+                   e = launch_pdl(sink_bwd_join_kernel<D, EXACT>, dim3(grid, joins, 1), 256, 0, st, a, grid, 0));
+        if (e != cudaSuccess) return e;
+        *launches += 1;
+    }
     GCA_LAUNCH("sink_bwd_kv", st,
                e = launch_pdl(pb::sink_bwd_kv_kernel<D, SCORE>, dim3(grid), kThreadsB, pb::Cfg<D>::SMEM, st, m[4], m[5], m[6], m[7], a));
     if (e != cudaSuccess) return e;
     *launches += 3;
-    if (a.wholeA && a.wholeB) return e;
+    if (a.wholeB && (EXACT || a.wholeA)) return e;
+    const int z0 = EXACT ? 1 : 0;
     GCA_LAUNCH("sink_bwd_join", st,
-               e = launch_pdl(sink_bwd_join_kernel<D>, dim3(grid, 128 * D / 1024, 3), 256, 0, st, a, grid));
+               e = launch_pdl(sink_bwd_join_kernel<D, EXACT>, dim3(grid, joins, 3 - z0), 256, 0, st, a, grid, z0));
     if (e == cudaSuccess) *launches += 1;
     return e;
 }
@@ -1215,12 +1343,12 @@ bool sink_bwd_supported(const SinkShape& s) {
     return s.B * s.H * kv < kMaxSteps && s.B * s.Hkv * q < kMaxSteps && s.B * nkt * 4 < 2e9;
 }
 
-size_t sink_bwd_workspace_bytes(const SinkShape& s) { return layout(s).total; }
+size_t sink_bwd_workspace_bytes(const SinkShape& s, bool scored) { return layout(s, scored).total; }
 
 cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, const void* v,
                             const void* o, const float* lse, const void* dout, void* dq, void* dk,
                             void* dv, void* ws, int* status, cudaStream_t st, int* launches) {
-    const Layout w = layout(s);
+    const Layout w = layout(s, s.softcap > 0.f || s.slopes);
     uint8_t* base = static_cast<uint8_t*>(ws);
     BwdArgs a{};
     a.s.B = s.B; a.s.L = s.L; a.s.H = s.H; a.s.Hkv = s.Hkv; a.s.G = s.H / s.Hkv;
@@ -1246,6 +1374,8 @@ cudaError_t launch_sink_bwd(const SinkShape& s, const void* q, const void* k, co
     a.tailB = reinterpret_cast<int4*>(base + w.tailB);
     a.headA = reinterpret_cast<int*>(base + w.headA);
     a.headB = reinterpret_cast<int*>(base + w.headB);
+    a.sigA = reinterpret_cast<float*>(base + w.sigA);
+    a.sigx = reinterpret_cast<float*>(base + w.sigx);
     a.status = status;
     a.scale = s.softcap > 0.f ? 4.f * s.scale : s.scale;
     a.scale_log2 = s.scale * kLog2e;

@@ -10,6 +10,9 @@ FMAs).  A bias b adds 8 E |b| (the slope's and the distance's roundings and thos
 sums), and where a block's 64 queries carry part of it, 8 E 64 |slope|.
 With score errors e_s a weight p_s is off by p_s (e_s + sum p e), and lse by sum p e.
 The cap's derivative 4 r (1 - r) is off by 2^-20 (r by 2^-21.4, 4 (1 - 2 r) times).
+Gradients take delta_t = sum_s p_ts dP_ts, a sum in fp32 like the others.  For dq it stands
+as the o given with delta~ = dO . o and a correction sigma times sum_s p_ts K_s, whose p are
+rounded to bf16: U |sigma| sum p |K| more, sigma = scale (delta - delta~).
 """
 import torch
 
@@ -75,12 +78,14 @@ def backward(q, k, v, o, lse, g, window, sinks, cap=0.0, slopes=None, scale=None
         p = torch.exp(s - lse[b].t()[..., None]).masked_fill(~see, 0)
         dp = torch.einsum("mhd,shd->hms", g[b], vv)
         da = torch.einsum("mhd,shd->hms", g[b].abs(), vv.abs())
-        dl = (g[b] * o[b]).sum(-1).t()[..., None]
-        dla = (g[b] * o[b]).abs().sum(-1).t()[..., None]
-        ds = turn * p * (dp - dl)
         es = err + 4 * E * lse[b].t().abs()[..., None]
+        dl = (p * dp).sum(-1, keepdim=True)
+        dla = (g[b] * o[b]).abs().sum(-1).t()[..., None]
+        err_dl = (p * (es * dp.abs() + d * E * (da + dla))).sum(-1, keepdim=True) + L * E * (p * (dp.abs() + dla)).sum(-1, keepdim=True)
+        sigma = top * (dl - (g[b] * o[b]).sum(-1).t()[..., None]).abs()
+        ds = turn * p * (dp - dl)
         err_p = p * (U + 2 * es)
-        err_ds = ds.abs() * (U + 2 * es) * 1.01 + top * p * d * E * (da + dla) * 2
+        err_ds = ds.abs() * (U + 2 * es) * 1.01 + top * p * (d * E * (da + dla) * 2 + err_dl)
         if cap:
             err_ds = err_ds + 2.0 ** -20 * top * p * (dp - dl).abs()
 
@@ -90,7 +95,7 @@ def backward(q, k, v, o, lse, g, window, sinks, cap=0.0, slopes=None, scale=None
         dk = fold(torch.einsum("hms,mhd->shd", ds, q[b]))
         dv = fold(torch.einsum("hms,mhd->shd", p, g[b]))
         n = G * L * E                                                       # sums of up to G L terms in fp32
-        bq = torch.einsum("hms,shd->mhd", err_ds + n * ds.abs(), kk.abs())
+        bq = torch.einsum("hms,shd->mhd", err_ds + n * ds.abs() + (U * 1.01 + n) * sigma * p, kk.abs())
         bk = fold(torch.einsum("hms,mhd->shd", err_ds + n * ds.abs(), q[b].abs()))
         bv = fold(torch.einsum("hms,mhd->shd", err_p + n * p, g[b].abs()))
         res.append((dq, dk, dv))
