@@ -421,10 +421,23 @@ __device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) { wait
 // (With a row per lane the 32 lanes of a store touch 32 lines, and a tile's stores cost
 // as much as half a key tile; with shuffles in place of tensor memory the forward took
 // 0.333 instead of 0.325 ms at B = 8 x 16K, W = 512.)
-__device__ __forceinline__ void load_rows32(uint32_t taddr, float scale, uint32_t (&q)[16]) {
+// MORE: with f times another accumulator's columns on top.
+template <bool MORE = false>
+__device__ __forceinline__ void load_rows32(uint32_t taddr, float scale, uint32_t (&q)[16], uint32_t other = 0, float f = 0.f) {
     uint32_t r[32], pk[16];
     tc::tmem_ld_32x32b_x32(taddr, r);
     tc::tmem_wait_ld();
+    if constexpr (MORE) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t y[16];
+            tc::tmem_ld_32x32b_x16(other + 16 * h, y);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                r[16 * h + i] = __float_as_uint(fmaf(f, __uint_as_float(y[i]), __uint_as_float(r[16 * h + i])));
+        }
+    }
     const uint64_t s2 = tcx::f2_pack(scale, scale);
 #pragma unroll
     for (int u = 0; u < 16; ++u)                        // pair u: column 4 (u % 4) + u / 4

@@ -166,23 +166,6 @@ __global__ void __launch_bounds__(256) sink_bwd_vec_kernel(const BwdArgs a) {
     }
 }
 
-// 32 columns of an fp32 accumulator (a row a lane), less `f` times another's, in place.
-__device__ __forceinline__ void less_rows32(uint32_t acc, uint32_t other, float f) {
-    uint32_t x[32], y[32];
-    tmem_ld_32x32b_x32(acc, x);
-    tmem_ld_32x32b_x32(other, y);
-    tmem_wait_ld();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t z[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            z[i] = __float_as_uint(fmaf(-f, __uint_as_float(y[16 * h + i]), __uint_as_float(x[16 * h + i])));
-        tmem_st_32x32b_x16(acc + 16 * h, z);
-    }
-    tmem_wait_st();
-}
-
 // N columns of this lane's row of an fp32 accumulator to a [N / 4][128][4] array of the
 // workspace (rows side by side: the lanes of a store write 512 consecutive bytes).
 template <int N>
@@ -540,12 +523,19 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             tc_fence_after();
             const uint32_t acc = tmem + lane_base + C::COL_ACC + ob * C::ACC;
             if (pend_slot < 0) {
-                if constexpr (EXACT) {
+                if constexpr (EXACT && D == 64) {
+                    uint32_t pk[2][16];
+#pragma unroll
+                    for (int ci = 0; ci < 2; ++ci) load_rows32<true>(acc + 32 * ci, 1.f, pk[ci], acc + D + 32 * ci, -sigma);
+                    tc_fence_before();
+                    mbar_arrive(&sb.o_empty[ob]);
+#pragma unroll
+                    for (int ci = 0; ci < 2; ++ci) store_rows32(pk[ci], a.dq + 32 * ci, D, pend_row);
+                } else if constexpr (EXACT) {
 #pragma unroll 1
-                    for (int ci = 0; ci < D / 32; ++ci) {
+                    for (int ci = 0; ci < D / 32; ++ci) {         // (too many for the registers)
                         uint32_t pk[16];
-                        less_rows32(acc + 32 * ci, acc + D + 32 * ci, sigma);
-                        load_rows32(acc + 32 * ci, 1.f, pk);
+                        load_rows32<true>(acc + 32 * ci, 1.f, pk, acc + D + 32 * ci, -sigma);
                         if (ci + 1 == D / 32) {
                             tc_fence_before();
                             mbar_arrive(&sb.o_empty[ob]);
