@@ -284,7 +284,7 @@ def rope_freqs(rot, *, base=10000.0, scaling="none", factor=1.0, trained_len=0, 
 
 def gca_rope(params: GcaRopeParams, q, k, freqs, positions, q_out, k_out, stream=None):
     _check("gca_rope", _lib.load().gca_rope(
-        ctypes.byref(params), _ptr(q), _ptr(k), _ptr(freqs), _ptr(positions), _ptr(q_out), _ptr(k_out),
+        ctypes.byref(params), _ptr(q), _ptr(k), freqs.data_ptr(), _ptr(positions), _ptr(q_out), _ptr(k_out),
         _raw_stream(stream, freqs.get_device())))
 
 
@@ -658,25 +658,25 @@ def gca_page_pool_init(n_pages, pool, stream=None):
 
 def gca_paged_reserve(params: GcaPagesParams, cu_q, kv_len, table, pool, stream=None):
     _check("gca_paged_reserve", _lib.load().gca_paged_reserve(
-        ctypes.byref(params), _ptr(cu_q), _ptr(kv_len), _ptr(table), _ptr(pool),
+        ctypes.byref(params), cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(), pool.data_ptr(),
         _raw_stream(stream, pool.get_device())))
 
 
 def gca_paged_fork(params: GcaPagesParams, parent, kv_len, table, pool, pairs, stream=None):
     _check("gca_paged_fork", _lib.load().gca_paged_fork(
-        ctypes.byref(params), _ptr(parent), _ptr(kv_len), _ptr(table), _ptr(pool), _ptr(pairs),
-        _raw_stream(stream, pool.get_device())))
+        ctypes.byref(params), parent.data_ptr(), kv_len.data_ptr(), table.data_ptr(), pool.data_ptr(),
+        pairs.data_ptr(), _raw_stream(stream, pool.get_device())))
 
 
 def gca_paged_compact(params: GcaPagesParams, max_moves, table, pool, pairs, stream=None):
     _check("gca_paged_compact", _lib.load().gca_paged_compact(
-        ctypes.byref(params), max_moves, _ptr(table), _ptr(pool), _ptr(pairs),
+        ctypes.byref(params), max_moves, table.data_ptr(), pool.data_ptr(), pairs.data_ptr(),
         _raw_stream(stream, pool.get_device())))
 
 
 def gca_paged_copy(page_bytes, n_pages, pairs, n, k_cache, v_cache, stream=None):
     _check("gca_paged_copy", _lib.load().gca_paged_copy(
-        page_bytes, n_pages, _ptr(pairs), n, _ptr(k_cache), _ptr(v_cache),
+        page_bytes, n_pages, pairs.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(),
         _raw_stream(stream, k_cache.get_device())))
 
 
@@ -704,16 +704,18 @@ def _pages_plan(table, kv_len, ints, page, window, sinks):
 
 
 def _paged_ints(*ts):
+    i32 = torch.int32
     for t in ts:
-        if t.dtype != torch.int32:
+        if t.dtype is not i32:
             raise TypeError("table, pool, pairs, parent, cu_q and kv_len must be int32")
         if not t.is_contiguous():
             raise ValueError("table, pool, pairs, parent, cu_q and kv_len must be contiguous")
 
 
 def _pages_args(table, kv_len, pool, page, window=0, sinks=0):
-    return _pages_plan(table.shape, None if kv_len is None else kv_len.shape, pool.numel(),
-                       operator.index(page), operator.index(window), operator.index(sinks))
+    if type(page) is not int or type(window) is not int or type(sinks) is not int:
+        page, window, sinks = operator.index(page), operator.index(window), operator.index(sinks)
+    return _pages_plan(table.shape, None if kv_len is None else kv_len.shape, pool.numel(), page, window, sinks)
 
 
 def paged_reserve(table, cu_q, kv_len, pool, *, page, window=0, sinks=0):
@@ -736,7 +738,7 @@ def paged_fork(table, kv_len, parent, pool, *, page):
     p = _pages_args(table, kv_len, pool, page)
     if parent.shape != (p.B,):
         raise ValueError("parent must be [%d]" % p.B)
-    pairs = torch.empty((p.B, 2), dtype=torch.int32, device=pool.device)
+    pairs = pool.new_empty((p.B, 2))
     gca_paged_fork(p, parent, kv_len, table, pool, pairs)
     return pairs
 
@@ -750,7 +752,7 @@ def paged_compact(table, pool, *, max_moves):
     n = operator.index(max_moves)
     if not 1 <= n <= 1 << 24:
         raise ValueError("max_moves must be 1 .. 2^24")
-    pairs = torch.empty((n, 2), dtype=torch.int32, device=pool.device)
+    pairs = pool.new_empty((n, 2))
     gca_paged_compact(p, n, table, pool, pairs)
     return pairs
 

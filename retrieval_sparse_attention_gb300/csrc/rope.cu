@@ -24,7 +24,7 @@
 namespace gca {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 // Steps of 32 slots that a warp takes at most (by its registers).  A kernel has as many as it takes: with
 // room for five, three steps are 5% slower (8 x 16K, 12/12 heads of 64: 127 instead of 121 us).
 template <class T>
