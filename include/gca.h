@@ -518,8 +518,9 @@ gca_status_t gca_paged_rope_append(const gca_paged_params_t* params, const gca_r
  * The entries below read and write it, the table [B, table_width] and kv_len [B] on the
  * device only, so captured calls follow their contents.  They keep this state: a page's
  * count is the number of entries that hold it, entries that hold none are -1, and a
- * sequence's unfinished last page is held by it alone.  Free pages are taken lowest
- * first; the results depend on the arguments alone.  One pool, its table and lengths
+ * sequence's unfinished last page is held by it alone.  (A host may set a length back,
+ * where the page that then is the last is not shared: its entries stay.)  Free pages are
+ * taken lowest first; the results depend on the arguments alone.  One pool, its table and lengths
  * belong to any number of caches (layers): only the data is moved for each.
  * Calls on one pool must follow each other.  Limits: B up to 4096, n_pages up to 2^24,
  * table_width * page up to 2^29, B * table_width below 2^31.
@@ -560,8 +561,9 @@ gca_status_t gca_paged_reserve(const gca_pages_params_t* params, const int32_t* 
  * gca_paged_fork -- every slot b goes on from what slot parent[b] holds, all at once:
  * parent[b] = b leaves it, another slot's number makes it a copy of that one (a fork, or
  * beams that change places), -1 empties it.
- *   Pages are shared; of an unfinished last page the slot itself, or else the first of its
- *   children, goes on with the page, and the others get a fresh one:
+ *   Whole pages are shared; with an unfinished last page (and what entries there are behind
+ *   it) the slot itself, or else the first of its children, goes on, and the others get a
+ *   fresh one:
  *   pairs [B, 2] int32: (page, fresh page) for gca_paged_copy, or -1, -1.
  *   Pages are let go as in gca_paged_reserve, after fresh ones have been taken from those
  *   free before.  Where these are too few nothing changes, all pairs are -2, -2

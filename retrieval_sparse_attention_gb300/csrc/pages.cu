@@ -234,18 +234,21 @@ __device__ __forceinline__ int parent_of(const int32_t* parent, int b, int B) {
 }
 
 // Rewrites columns c0 .. of the table, in place, and moves the counts: one CTA, with room for
-// B * (cols + 2) numbers.  COLS of them, or where that is 0 all.
+// B * (cols + 3) numbers.  COLS of them, or where that is 0 all.  A slot's whole pages are shared by its
+// children; the entries from its unfinished page on (behind the length there may be some where that was set
+// back) stay with the child that goes on, so that none is written by two.
 template <int COLS>
 __device__ __forceinline__ void fork_columns(const PageArgs& a, const int32_t* parent, const int32_t* kv_len,
                                              const int32_t* pairs, int c0, int* room) {
     const int cols = COLS ? COLS : a.width;
     int* entry = room;                   // [B][cols]: the table as it was
     int* children = room + a.B * cols;   // [B]
-    int* tail = children + a.B;          // [B]: the entry of the slot's unfinished page, or -1
+    int* tail = children + a.B;          // [B]: the first entry that is not a whole page
+    int* keeper = tail + a.B;            // [B]: the child that goes on; -1: the slot itself
     const int n = a.B * cols;
     for (int b = threadIdx.x; b < a.B; b += kThreads) {
         children[b] = 0;
-        tail[b] = -1;
+        keeper[b] = a.B;
     }
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -257,8 +260,9 @@ __device__ __forceinline__ void fork_columns(const PageArgs& a, const int32_t* p
         const int p = parent_of(parent, b, a.B);
         if (p < 0) continue;
         atomicAdd(&children[p], 1);
-        const int kv = kv_len[b], len = kv < 0 ? ~kv : kv;       // (the parent's)
-        if (len & ((1 << a.page_log2) - 1)) tail[p] = len >> a.page_log2;
+        atomicMin(&keeper[p], p == b ? -1 : b);
+        const int kv = kv_len[b];
+        tail[p] = (kv < 0 ? ~kv : kv) >> a.page_log2;            // (the length is the parent's)
     }
     __syncthreads();
     constexpr int U = 4;                 // (counts in flight)
@@ -269,8 +273,7 @@ __device__ __forceinline__ void fork_columns(const PageArgs& a, const int32_t* p
             const int i = i0 + u * kThreads, b = i / cols;
             e[u] = i < n ? entry[i] : -1;
             delta[u] = 0;
-            // of the unfinished page one child goes on, of the others all
-            if (e[u] >= 0) delta[u] = (c0 + i % cols == tail[b] ? min(children[b], 1) : children[b]) - 1;
+            if (e[u] >= 0) delta[u] = (children[b] && c0 + i % cols >= tail[b] ? 1 : children[b]) - 1;
             if (delta[u] && e[u] >= a.n) set_status(a.status, GCA_ERR_DEVICE_INDEX);
             if (e[u] >= a.n) delta[u] = 0;
             if (delta[u]) left[u] = atomicAdd(a.refs + e[u], delta[u]) + delta[u];
@@ -283,7 +286,7 @@ __device__ __forceinline__ void fork_columns(const PageArgs& a, const int32_t* p
             const int p = parent_of(parent, b, a.B);
             if (p == b) continue;
             int to = p < 0 ? -1 : entry[p * cols + i % cols];
-            if (p >= 0 && c == tail[p] && pairs[2 * b + 1] >= 0) to = pairs[2 * b + 1];
+            if (p >= 0 && c >= tail[p] && keeper[p] != b) to = c == tail[p] && pairs[2 * b + 1] >= 0 ? pairs[2 * b + 1] : -1;
             a.table[(size_t)b * a.width + c] = to;
         }
     }
@@ -471,14 +474,14 @@ cudaError_t launch_paged_fork(const PageShape& s, const int32_t* parent, int32_t
     static LaunchSetup setup;
     int sms;
     const bool small = (long long)a.B * a.width <= kSmallTable;
-    const int room = a.B * (small ? a.width + 2 : kCols + 2) * 4;
+    const int room = a.B * (small ? a.width + 3 : kCols + 3) * 4;
     cudaError_t e = setup.once(
         [] {
             const cudaError_t r = cudaFuncSetAttribute(paged_fork_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (kSmallTable + 2 * kMaxSeqs) * 4);
+                                                       (kSmallTable + 3 * kMaxSeqs) * 4);
             if (r != cudaSuccess) return r;
             return cudaFuncSetAttribute(paged_fork_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kMaxSeqs * (kCols + 2) * 4);
+                                        kMaxSeqs * (kCols + 3) * 4);
         },
         &sms);
     if (e != cudaSuccess) return e;

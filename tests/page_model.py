@@ -69,7 +69,10 @@ class Pages:
         if len(copies) > len(free):
             self.bad(7)
             return [(-2, -2)] * self.B
-        self.table = [list(rows[p]) if p >= 0 else [-1] * self.width for p in parent]
+        # (entries behind the length, of one that was set back, stay with the child that goes on)
+        ends = [(-1 - n if n < 0 else n) // page for n in kv]
+        self.table = [[-1] * self.width if p < 0 else list(rows[p]) if keeper[p] == b else
+                      [e if i < ends[p] else -1 for i, e in enumerate(rows[p])] for b, p in enumerate(parent)]
         self.kv = [kv[p] if p >= 0 else 0 for p in parent]
         for (b, i, src), dst in zip(copies, free):
             pairs[b] = (src, dst)

@@ -77,6 +77,28 @@ def test_any_sequence_of_calls(B, width, n_pages, page, seed):
         s.check()
 
 
+def test_forks_of_sequences_that_were_set_back():
+    # pages behind the length: one child keeps them, and no two write the same page afterwards
+    m = Pages(5, 8, 40, 16)
+    s = Device(m)
+    m.reserve([0, 100, 100, 150, 150, 200])
+    api.paged_reserve(s.table, ints([0, 100, 100, 150, 150, 200]), s.kv, s.pool, page=16)
+    for lens in ([20, 0, 32, 0, 50], [5, 0, 1, 0, 16]):
+        m.kv = list(lens)
+        s.kv.copy_(ints(lens))
+        for parent in ([0, 0, 2, 2, 0], [1, 0, 0, 2, 4]):
+            pairs = m.fork(parent)
+            got = api.paged_fork(s.table, s.kv, ints(parent), s.pool, page=16)
+            assert [tuple(x) for x in got.tolist()] == pairs
+            s.check()
+        cu = [0, 30, 60, 90, 120, 150]
+        m.reserve(cu)
+        api.paged_reserve(s.table, ints(cu), s.kv, s.pool, page=16)
+        s.check()
+        for b, n in enumerate(m.kv):                     # what a sequence writes next it holds alone
+            assert n < 0 or n % 16 == 0 or m.refs[m.table[b][n // 16]] == 1
+
+
 def test_contradicting_arguments_are_reported():
     m = Pages(4, 4, 20, 16)
     s = Device(m)
