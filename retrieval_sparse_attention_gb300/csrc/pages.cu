@@ -110,13 +110,13 @@ __device__ __forceinline__ void run_of(int n, int& i0, int& i1) {
 }
 
 // The `want` lowest free pages to list[0 ..], ascending; returns how many there are of them.
-__device__ __forceinline__ int lowest_free(const PageArgs& a, int want, int* wsum) {
+__device__ __forceinline__ int lowest_free(const PageArgs& a, int want, int* wsum, int* list) {
     int w0, w1, mine = 0, total;
     run_of(a.n_words, w0, w1);
     for (int w = w0; w < w1; ++w) mine += __popc(free_word(a, w));
     int r = block_scan(mine, wsum, total);
     for (int w = w0; w < w1 && r < want; ++w)
-        for (uint32_t x = free_word(a, w); x && r < want; x &= x - 1) a.list[r++] = 32 * w + __ffs(x) - 1;
+        for (uint32_t x = free_word(a, w); x && r < want; x &= x - 1) list[r++] = 32 * w + __ffs(x) - 1;
     __syncthreads();
     return min(want, total);
 }
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256) pool_init_kernel(PageArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Reservation.  A warp per sequence lets go of the pages behind its window and counts the
+// Reservation.  Half a warp per sequence lets go of the pages behind its window and counts the
 // entries that its new tokens lack; a scan over the sequences and one over the free
 // bits give every lacking entry its page.
 // ---------------------------------------------------------------------------
@@ -157,33 +157,38 @@ __device__ __forceinline__ Reserve reserve_of(const PageArgs& a, const int32_t* 
 
 __global__ void __launch_bounds__(kThreads) paged_reserve_kernel(const PageArgs a, const int32_t* cu_q, int32_t* kv_len) {
     __shared__ int end[kMaxSeqs];        // entries that the sequences up to this one lack
+    __shared__ int few[kThreads];        // the free pages, where they are no more
     __shared__ int wsum[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int b = warp; b < a.B; b += kThreads / 32) {
-        const Reserve r = reserve_of(a, cu_q, kv_len, b);
+    // half a warp a sequence: 64 of them at once
+    const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15, first = (threadIdx.x >> 5) * 2;
+    constexpr int kStep = kThreads / 16;
+    for (int b0 = first; b0 < a.B; b0 += kStep) {
+        const int b = b0 + half;
+        Reserve r{};
+        if (b < a.B) r = reserve_of(a, cu_q, kv_len, b);
         int32_t* row = a.table + (size_t)b * a.width;
-        if (a.W && r.add) {
+        if (a.W) {
             // whole entries that no token from `old` on sees, downwards as far as they hold pages
             const int lo = (int)(((long long)a.ns + (1 << a.page_log2) - 1) >> a.page_log2);
-            int hi = max(0, r.old - a.W + 1) >> a.page_log2;
-            while (hi > lo) {
-                const int i = hi - 1 - lane;
+            int hi = r.add ? max(0, r.old - a.W + 1) >> a.page_log2 : 0;
+            while (__any_sync(0xffffffffu, hi > lo)) {
+                const int i = hi - 1 - hl;
                 const int e = i >= lo ? row[i] : -1;
-                const unsigned stop = __ballot_sync(0xffffffffu, e < 0);
-                const int n = stop ? __ffs(stop) - 1 : 32;
-                if (lane < n) {
+                const unsigned stop = (__ballot_sync(0xffffffffu, e < 0) >> (16 * half)) & 0xffffu;
+                const int n = stop ? __ffs(stop) - 1 : 16;
+                if (hl < n) {
                     row[i] = -1;
                     count_page(a, e, -1);
                 }
-                hi -= 32;
-                if (n < 32) break;
+                hi = n < 16 ? lo : hi - 16;
             }
             __syncwarp();
         }
         int need = 0;
-        for (int i = r.e0 + lane; i < r.e1; i += 32) need += row[i] < 0;
-        need = __reduce_add_sync(0xffffffffu, need);
-        if (lane == 0) end[b] = need;
+        for (int i = r.e0 + hl; i < r.e1; i += 16) need += row[i] < 0;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) need += __shfl_xor_sync(0xffffffffu, need, o);
+        if (hl == 0 && b < a.B) end[b] = need;
     }
     __syncthreads();
     int b0, b1, mine = 0, total;
@@ -192,25 +197,28 @@ __global__ void __launch_bounds__(kThreads) paged_reserve_kernel(const PageArgs 
     int at = block_scan(mine, wsum, total);
     for (int b = b0; b < b1; ++b) end[b] = at += end[b];
     __syncthreads();
-    const int have = total ? lowest_free(a, min(total, a.n), wsum) : 0;
-    for (int b = warp; b < a.B; b += kThreads / 32) {
-        const Reserve r = reserve_of(a, cu_q, kv_len, b);
-        int from = b ? end[b - 1] : 0;
-        const bool none = end[b] > from && end[b] > have;
-        if (lane == 0) {
+    int* const list = total <= kThreads ? few : a.list;
+    const int have = total ? lowest_free(a, min(total, a.n), wsum, list) : 0;
+    for (int b0 = first; b0 < a.B; b0 += kStep) {
+        const int b = b0 + half;
+        const bool on = b < a.B;
+        Reserve r{};
+        if (on) r = reserve_of(a, cu_q, kv_len, b);
+        int from = on && b ? end[b - 1] : 0;
+        const bool none = on && end[b] > from && end[b] > have;
+        __syncwarp();                    // (every lane has read the length)
+        if (on && hl == 0) {
             if (r.bad) set_status(a.status, GCA_ERR_DEVICE_INDEX);
             else if (none) set_status(a.status, GCA_ERR_NO_PAGES);
+            kv_len[b] = r.bad || none ? ~r.old : r.old + r.add;
         }
-        __syncwarp();
-        if (lane == 0) kv_len[b] = r.bad || none ? ~r.old : r.old + r.add;
-        if (none) continue;
+        const int e1 = none ? r.e0 : r.e1;
         int32_t* row = a.table + (size_t)b * a.width;
-        for (int i0 = r.e0; i0 < r.e1; i0 += 32) {
-            const int i = i0 + lane;
-            const bool lacks = i < r.e1 && row[i] < 0;
-            const unsigned all = __ballot_sync(0xffffffffu, lacks);
+        for (int i = r.e0 + hl; __any_sync(0xffffffffu, i - hl < e1); i += 16) {
+            const bool lacks = i < e1 && row[i] < 0;
+            const unsigned all = (__ballot_sync(0xffffffffu, lacks) >> (16 * half)) & 0xffffu;
             if (lacks) {
-                const int e = a.list[from + __popc(all & ((1u << lane) - 1))];
+                const int e = list[from + __popc(all & ((1u << hl) - 1))];
                 row[i] = e;
                 take_page(a, e);
             }
@@ -325,7 +333,7 @@ paged_fork_plan_kernel(const PageArgs a, const int32_t* parent, int32_t* kv_len,
     run_of(a.B, b0, b1);
     for (int b = b0; b < b1; ++b) mine += copied(b) >= 0;
     int at = block_scan(mine, wsum, total);
-    const bool ok = total <= a.n && (total == 0 || lowest_free(a, total, wsum) == total);
+    const bool ok = total <= a.n && (total == 0 || lowest_free(a, total, wsum, a.list) == total);
     if (!ok && threadIdx.x == 0) set_status(a.status, GCA_ERR_NO_PAGES);
     for (int b = b0; b < b1; ++b) {
         const int src = copied(b);
