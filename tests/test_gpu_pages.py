@@ -339,3 +339,15 @@ def test_a_captured_generation():
     assert eager.kv.tolist() == [n + 60 for n in kv0]
     # pages behind the window came back: the sequences hold a window each
     assert int((eager.pool[:n_pages] > 0).sum()) <= B * (window // page + 3)
+
+
+def test_copies_beyond_32_bits():
+    # 2.6e9 elements of a cache: pages at its end
+    n, shape = 20000, (128, 8, 128)
+    k = torch.zeros(n, *shape, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    x, y = (torch.randn(shape, device="cuda").to(torch.bfloat16) for _ in range(2))
+    k[n - 1], v[n - 2] = x, y
+    api.paged_copy(k, v, ints([(n - 1, 3), (n - 2, n - 3)]))
+    assert api.gca_get_status() == 0
+    assert torch.equal(k[3], x) and torch.equal(v[n - 3], y) and not v[3].any() and not k[n - 3].any() and not k[4].any()

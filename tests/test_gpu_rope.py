@@ -214,3 +214,15 @@ def test_append_bad_pages_and_lengths():
         api.paged_rope_append(q.float(), k, v, api.rope_freqs(64), kc, vc, table, cu, kv)
     with pytest.raises(TypeError):
         api.paged_rope_append(q, k, v, api.rope_freqs(64), kc, vc, table, cu, kv.long())
+
+
+def test_elements_beyond_32_bits():
+    # 2.46e9 elements of q: the last tokens are turned as if they were alone
+    T, H, d = 300000, 64, 128
+    q = torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda")
+    tail = normal(5, H, d, seed=9)
+    q[-5:] = tail
+    freqs = api.rope_freqs(d)
+    api.rope(q, None, freqs, inplace=True)
+    want, _ = api.rope(tail, None, freqs, start=T - 5)
+    assert torch.equal(q[-5:], want) and not q[:1000].any()

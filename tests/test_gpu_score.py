@@ -194,3 +194,62 @@ def test_refusals():
         api.swa_sink_fwd(q, k, v, window=8, sinks=0, slopes=torch.ones(2))
     with pytest.raises(ValueError):
         api.swa_sink_fwd(q, k, v, window=8, sinks=0, slopes=torch.ones(3, device="cuda"))
+
+
+@pytest.mark.parametrize("cap,bias", [(9.0, False), (0.0, True)])
+def test_training_step_captured_and_on_another_stream(cap, bias):
+    # (a workspace that the caller keeps, units cut and joined in both passes)
+    q, k, v, g = (x.cuda() for x in inputs(2, 700, 8, 2, 64, seed=21))
+    kw = dict(window=300, sinks=3, softcap=cap, slopes=slopes_of(8).cuda() if bias else None)
+    p = api.make_swa_sink_params(B=2, L=700, H=8, Hkv=2, d=64, window=300, sinks=3)
+    ws = torch.empty(api.gca_swa_sink_bwd_scored_workspace_size(p), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > api.gca_swa_sink_bwd_workspace_size(p)
+
+    def step():
+        o, lse = api.swa_sink_fwd(q, k, v, **kw)
+        return [o, lse, *api.swa_sink_bwd(q, k, v, o, lse, g, workspace=ws, **kw)]
+    want = step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = step()
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    q.mul_(0.5)
+    graph.replay()
+    held = [x.clone() for x in got]
+    assert not torch.equal(held[0], want[0])
+    ws.fill_(255)                                # (what a workspace held before does not matter)
+    assert all(torch.equal(a, b) for a, b in zip(held, step()))
+    assert api.gca_get_status() == 0
+
+
+def test_gradients_need_their_own_workspace():
+    q, k, v, g = (x.cuda() for x in inputs(1, 200, 2, 2, 64, seed=22))
+    kw = dict(window=50, sinks=0, softcap=5.0)
+    o, lse = api.swa_sink_fwd(q, k, v, **kw)
+    p = api.make_swa_sink_params(B=1, L=200, H=2, d=64, window=50)
+    small = torch.empty(api.gca_swa_sink_bwd_workspace_size(p), dtype=torch.uint8, device="cuda")
+    with pytest.raises(GcaError) as e:
+        api.swa_sink_bwd(q, k, v, o, lse, g, workspace=small, **kw)
+    assert e.value.code == 3
+
+
+def test_rows_of_a_few_keys():
+    # 16 tokens, scores of several units: dP - delta is a difference of near numbers.  The roundings of the
+    # result and of ds are 1.7e-3 of the norm each (uniform within half a step of bf16, relative to a
+    # value anywhere between two powers of two), 2.4e-3 together; an eighth more for so few values
+    for cap, slopes in ((0.0, slopes_of(6)), (50.0, None), (3.0, None)):
+        q, k, v, g = inputs(4, 16, 6, 2, 64, seed=23)
+        q = q * 3
+        kw = dict(window=16, sinks=1, softcap=cap, slopes=None if slopes is None else slopes.cuda())
+        x = [t.cuda() for t in (q, k, v)]
+        o, lse = api.swa_sink_fwd(*x, **kw)
+        got = api.swa_sink_bwd(*x, o, lse, g.cuda(), **kw)
+        ro, rl, _, _ = ref.forward(q, k, v, 16, 1, cap, slopes)
+        want, _ = ref.backward(q, k, v, ro, rl, g, 16, 1, cap, slopes)
+        for a, b in zip(got[:2], want[:2]):
+            assert float((a.double().cpu() - b).norm() / b.norm()) <= 2.7e-3
