@@ -41,6 +41,9 @@
 //   (1.37 PFLOP/s, 69%); 32 tokens over caches of 4-33K, 24/8 heads of 128: 0.326 to
 //   0.337 ms in a loop, 0.343 to 0.353 with a cold L2 (6.3-6.5 TB/s, 95-97%); a token
 //   each of 64 requests, 12 heads of 64, W = 512: 38 us in a graph; one over 777: 12 us.
+// Transformed scores (attn_sink.cuh): the first shape with a cap and 4 sinks 0.60 ms (XU 44% busy, issue slots
+// 55%: twice the instructions a score, on the same two warps a sub-partition); the 32 tokens with a cap 0.344 to
+// 0.355 ms, as without; a serving batch of 48, 12 heads of 64, W = 512: 49 us, with a bias 52.
 // What bounds it.  Single tokens over long caches: the cache's bytes.  d = 128 with
 // many rows: the chain S -> softmax -> P V of each worker, ~3,200 cycles a pair of
 // tiles of which the products fill ~2,450.  d = 64: no unit near its rate (issue slots

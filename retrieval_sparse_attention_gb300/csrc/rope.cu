@@ -17,7 +17,12 @@
 // turned in place.  A lane has the same slot of every head it meets (32 / (d/16) heads a step): it
 // forms its eight sines and cosines once a token.  A warp has up to kSteps steps of a token, all
 // loaded before the angles are formed.
-// Bound by memory: reads and writes q and k once.
+//
+// Measured (GB300): 8 x 16K tokens, 12/12 heads of 64, bf16: 115 us, at the copy rate (0.40 GB read and as
+// much written, of which 0.34 reach memory within the kernel); 517 tokens 2.3 us.  Into the cache: eight
+// chunks of 0.9-2K, 12/12 heads of 64: 19.5 us (6.0 TB/s, 89% of the copy rate); a token each of 64 requests,
+// 24/8 heads of 128: 3.0 us.  Bound by memory; the write to the cache also by the chain of a row's
+// sequence, its page and the store, which more warps a row lengthen (two steps a warp: 24 us).
 #include "attn_sink.cuh"
 #include "kernels.h"
 
