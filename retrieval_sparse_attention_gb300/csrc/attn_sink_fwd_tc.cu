@@ -849,81 +849,103 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     tc_fence_before();
                     if (!C::P_OVER_S) mbar_arrive(&sb.s_empty[wg]);
                     float mt = fmaxf(mc[0], mc[1]);
-                    // The diagonal or the window's edge crosses the tile, or all rows see it whole.  Visible:
-                    // columns c_lo .. c_hi (the window) and those below c_s (sinks), as bits.
-                    const bool whole = (j >= f0 && j < f1) || j == fl;
-                    const int p = w.p0 + rt, kbase = w.tile(j) * 128;
-                    auto hide = [&](float with) {
-                        const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
+                    if constexpr (SCORE == kScorePlain) {
+                        if (!((j >= f0 && j < f1) || j == fl)) {
+                            // The diagonal or the window's edge crosses the tile.  Visible: columns c_lo ..
+                            // c_hi (the window) and those below c_s (sinks), as bits.
+                            const int p = w.p0 + rt, kbase = w.tile(j) * 128;
+                            const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t vis = (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t vis = (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : with;
-                        }
-                    };
-                    // (four scores share a reciprocal: a hidden cache row's NaN must not get there)
-                    if (CAP && PAGED && !whole) hide(-INFINITY);
-                    if constexpr (CAP) {
-                        const float lim = kCapMax / a.cap_in;
-                        if (__any_sync(0xffffffffu, !(mt <= lim))) {      // (hardly ever)
-#pragma unroll
-                            for (int i = 0; i < 128; ++i) x[i] = min_nan(x[i], lim);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 128; i += 4) {
-                            float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
-                            cap_r4<false>(y, cap_in2);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) x[i + u] = y[u];
-                        }
-                        mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));    // r of the greatest product
-                    }
-                    if (!whole) hide(kHidden);
-                    if constexpr (BIAS) {
-                        // Bounds of the greatest scores of the columns' halves: the greatest product and the
-                        // greatest bias (none above 0 where it falls).  Where the bound moves the
-                        // running maximum it takes its place, unless it may lie more than 2^60 above the
-                        // true one (sums would be too small): in tiles with hidden columns their
-                        // products are left out first, and a bias so steep within 64 columns
-                        // takes the scores themselves.
-                        off = slope * static_cast<float>(kbase - p);
-                        const float top0 = slope > 0.f ? fmaf(63.f, slope, off) : off;
-                        const float top1 = slope > 0.f ? fminf(fmaf(127.f, slope, off), 0.f) : fmaf(64.f, slope, off);
-                        auto bound = [&]() { return fmaxf(fmaf(mc[0], sl, top0), fmaf(mc[1], sl, top1)); };
-                        mt = bound();
-                        if (!whole && __any_sync(0xffffffffu, !(mt <= m + kRescaleLog2))) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
+                                for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : -INFINITY;
+                            }
+                            // the maximum over all columns bounds that over the visible ones: only where it
+                            // would move the running one (or is no number) is the latter needed
+                            if (__any_sync(0xffffffffu, !(mt * sl <= m + kRescaleLog2))) {
                                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                                for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[64 * h + i]);
-                                mc[h] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                            }
-                            mt = bound();
-                        }
-                        if (__any_sync(0xffffffffu, fabsf(slope) * 63.f > 60.f && !(mt <= m + kRescaleLog2))) {
-                            mt = -INFINITY;
-                            uint64_t tb = 0;
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) {
-                                float y0, y1;
-                                tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x[2 * c], x[2 * c + 1]), tcx::f2_pack(sl, sl), tilt(tb, c, off)),
-                                               y0, y1);
-                                mt = fmaxf(mt, fmaxf(y0, y1));
+                                for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+                                mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                             }
                         }
-                        follow(mt);
+                        follow(mt * sl);
                     } else {
-                        // the maximum over all columns bounds that over the visible ones: only where it
-                        // would move the running one (or is no number) is the latter needed
-                        if (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2))) {
-                            float m4[4] = {kHidden, kHidden, kHidden, kHidden};
+                        const bool whole = (j >= f0 && j < f1) || j == fl;
+                        const int p = w.p0 + rt, kbase = w.tile(j) * 128;
+                        auto hide = [&](float with) {
+                            const int c_lo = p - sc.W + 1 - kbase, c_hi = p - kbase, c_s = min(sc.ns, p + 1) - kbase;
 #pragma unroll
-                            for (int i = 0; i < 128; ++i) m4[i & 3] = greater(m4[i & 3], x[i]);
-                            mt = greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]));
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t vis = (below(c_hi + 1 - 32 * c) & ~below(c_lo - 32 * c)) | below(c_s - 32 * c);
+#pragma unroll
+                                for (int u = 0; u < 32; ++u) x[32 * c + u] = (vis >> u & 1u) ? x[32 * c + u] : with;
+                            }
+                        };
+                        // (four scores share a reciprocal: a hidden cache row's NaN must not get there)
+                        if (CAP && PAGED && !whole) hide(-INFINITY);
+                        if constexpr (CAP) {
+                            const float lim = kCapMax / a.cap_in;
+                            if (__any_sync(0xffffffffu, !(mt <= lim))) {      // (hardly ever)
+#pragma unroll
+                                for (int i = 0; i < 128; ++i) x[i] = min_nan(x[i], lim);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 128; i += 4) {
+                                float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+                                cap_r4<false>(y, cap_in2);
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) x[i + u] = y[u];
+                            }
+                            mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));    // r of the greatest product
                         }
-                        follow(log2_of(mt));
+                        if (!whole) hide(kHidden);
+                        if constexpr (BIAS) {
+                            // Bounds of the greatest scores of the columns' halves: the greatest product and the
+                            // greatest bias (none above 0 where it falls).  Where the bound moves the
+                            // running maximum it takes its place, unless it may lie more than 2^60 above the
+                            // true one (sums would be too small): in tiles with hidden columns their
+                            // products are left out first, and a bias so steep within 64 columns
+                            // takes the scores themselves.
+                            off = slope * static_cast<float>(kbase - p);
+                            const float top0 = slope > 0.f ? fmaf(63.f, slope, off) : off;
+                            const float top1 = slope > 0.f ? fminf(fmaf(127.f, slope, off), 0.f) : fmaf(64.f, slope, off);
+                            auto bound = [&]() { return fmaxf(fmaf(mc[0], sl, top0), fmaf(mc[1], sl, top1)); };
+                            mt = bound();
+                            if (!whole && __any_sync(0xffffffffu, !(mt <= m + kRescaleLog2))) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                                    for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[64 * h + i]);
+                                    mc[h] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                                }
+                                mt = bound();
+                            }
+                            if (__any_sync(0xffffffffu, fabsf(slope) * 63.f > 60.f && !(mt <= m + kRescaleLog2))) {
+                                mt = -INFINITY;
+                                uint64_t tb = 0;
+#pragma unroll
+                                for (int c = 0; c < 64; ++c) {
+                                    float y0, y1;
+                                    tcx::f2_unpack(tcx::ffma2(tcx::f2_pack(x[2 * c], x[2 * c + 1]), tcx::f2_pack(sl, sl), tilt(tb, c, off)),
+                                                   y0, y1);
+                                    mt = fmaxf(mt, fmaxf(y0, y1));
+                                }
+                            }
+                            follow(mt);
+                        } else {
+                            // the maximum over all columns bounds that over the visible ones: only where it
+                            // would move the running one (or is no number) is the latter needed
+                            if (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2))) {
+                                float m4[4] = {kHidden, kHidden, kHidden, kHidden};
+#pragma unroll
+                                for (int i = 0; i < 128; ++i) m4[i & 3] = greater(m4[i & 3], x[i]);
+                                mt = greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]));
+                            }
+                            follow(log2_of(mt));
+                        }
                     }
                     l *= alpha;
                 }
