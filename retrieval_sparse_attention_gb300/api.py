@@ -194,17 +194,21 @@ def _token_stride(shape, stride):
     return step
 
 
+_FOREIGN = "tensors must be CUDA tensors on the current device"
+_current_device = torch._C._cuda_getDevice
+
+
 def _same_device(*ts):
     """The entries launch on the current device's stream: tensors of another device (or of
     none) would be read through a foreign address.  Returns the device index."""
     dev = ts[0].get_device()
-    if dev >= 0 and dev == torch._C._cuda_getDevice():      # (current_device() without its setup)
+    if dev >= 0 and dev == _current_device():               # (current_device() without its setup)
         for t in ts:
             if t is not None and t.get_device() != dev:
                 break
         else:
             return dev
-    raise ValueError("tensors must be CUDA tensors on the current device")
+    raise ValueError(_FOREIGN)
 
 
 def _empty_like(t):
@@ -309,26 +313,42 @@ def _rope_plan(qs, qst, ks, kst, qt, kt, pairs, pos, start, interleaved, mscale,
 
 
 def _rope_freqs(freqs):
-    if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    shape = freqs.shape
+    if freqs.dtype is not torch.int64 or len(shape) != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous int64 tensor [rot/2], as from rope_freqs")
-    return freqs.shape[0]
+    return shape[0]
 
 
+# (The calls below are made between a model's other ones, and each step of Python shows in a small
+# one: they test their tensors in one expression and call the library directly.)
 def _rope(q, k, freqs, positions, start, interleaved, mscale, inplace, inverse):
-    if q is None and k is None:
-        raise ValueError("q or k is needed")
-    _same_device(freqs, q, k, positions)
-    if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
-        raise ValueError("positions must be a contiguous int32 tensor")
+    dev = freqs.get_device()
+    if dev < 0 or dev != _current_device() or (q is not None and q.get_device() != dev) or \
+            (k is not None and k.get_device() != dev):
+        raise ValueError(_FOREIGN)
+    pos = at = None
+    if positions is not None:
+        if positions.get_device() != dev:
+            raise ValueError(_FOREIGN)
+        if positions.dtype is not torch.int32 or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 tensor")
+        pos, at = positions.shape, positions.data_ptr()
     if type(start) is not int:
         start = operator.index(start)
-    qs, qst, qt = (None, None, None) if q is None else (q.shape, q.stride(), q.dtype)
-    ks, kst, kt = (None, None, None) if k is None else (k.shape, k.stride(), k.dtype)
-    p = _rope_plan(qs, qst, ks, kst, qt, kt, _rope_freqs(freqs), None if positions is None else positions.shape,
-                   start, bool(interleaved), float(mscale), inverse, bool(inplace))
-    qo = q if inplace or q is None else _empty_like(q)
-    ko = k if inplace or k is None else _empty_like(k)
-    gca_rope(p, q, k, freqs, positions, qo, ko)
+    qs = qst = qt = ks = kst = kt = None
+    if q is not None:
+        qs, qst, qt = q.shape, q.stride(), q.dtype
+    if k is not None:
+        ks, kst, kt = k.shape, k.stride(), k.dtype
+    elif q is None:
+        raise ValueError("q or k is needed")
+    p = _rope_plan(qs, qst, ks, kst, qt, kt, _rope_freqs(freqs), pos, start, bool(interleaved), float(mscale),
+                   inverse, bool(inplace))
+    qo, ko = (q, k) if inplace else (None if q is None else _empty_like(q), None if k is None else _empty_like(k))
+    code = _lib.load().gca_rope(ctypes.byref(p), _ptr(q), _ptr(k), freqs.data_ptr(), at, _ptr(qo), _ptr(ko),
+                                _raw_stream(None, dev))
+    if code:
+        raise GcaError("gca_rope", code)
     return qo, ko
 
 
@@ -403,7 +423,7 @@ def _score(softcap, slopes, H, dev):
         return GcaScore(softcap, None) if softcap else None
     _dense(slopes, (H,), torch.float32, "slopes")
     if slopes.get_device() != dev:
-        raise ValueError("tensors must be CUDA tensors on the current device")
+        raise ValueError(_FOREIGN)
     return GcaScore(softcap, slopes.data_ptr())
 
 
@@ -628,7 +648,12 @@ def paged_rope_append(q, k_new, v_new, freqs, k_cache, v_cache, table, cu_q, kv_
     """paged_append of keys turned by their positions (``rope``), and the new tokens' queries
     q [T, H, d] turned by theirs -> q' [T, H, d] (``out`` supplies it; rows behind cu_q[B] are left
     as they were)."""
-    _same_device(k_cache, v_cache, table, cu_q, kv_len, q, k_new, v_new, freqs, out)
+    dev = k_cache.get_device()
+    if dev < 0 or dev != _current_device() or v_cache.get_device() != dev or table.get_device() != dev or \
+            cu_q.get_device() != dev or kv_len.get_device() != dev or q.get_device() != dev or \
+            k_new.get_device() != dev or v_new.get_device() != dev or freqs.get_device() != dev or \
+            (out is not None and out.get_device() != dev):
+        raise ValueError(_FOREIGN)
     if type(max_q) is not int:
         max_q = operator.index(max_q)
     _paged_ints(table, cu_q, kv_len)
@@ -642,7 +667,12 @@ def paged_rope_append(q, k_new, v_new, freqs, k_cache, v_cache, table, cu_q, kv_
         out = _empty_like(q)
     else:
         _dense(out, q.shape, q.dtype, "out")
-    gca_paged_rope_append(p, r, q, k_new, v_new, freqs, cu_q, kv_len, table, out, k_cache, v_cache)
+    code = _lib.load().gca_paged_rope_append(
+        ctypes.byref(p), ctypes.byref(r), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), freqs.data_ptr(),
+        cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(), out.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), _raw_stream(None, dev))
+    if code:
+        raise GcaError("gca_paged_rope_append", code)
     return out
 
 
@@ -722,56 +752,78 @@ def paged_reserve(table, cu_q, kv_len, pool, *, page, window=0, sinks=0):
     """Room for a step's new tokens, in place: with a window, pages that left it are let go; the
     entries of the new tokens get pages; kv_len counts the new tokens afterwards, as the step's
     paged_append and paged_attn take it (-1 - n for n tokens that could not grow)."""
-    _same_device(pool, table, cu_q, kv_len)
+    dev = pool.get_device()
+    if dev < 0 or dev != _current_device() or table.get_device() != dev or cu_q.get_device() != dev or \
+            kv_len.get_device() != dev:
+        raise ValueError(_FOREIGN)
     _paged_ints(table, cu_q, kv_len, pool)
     p = _pages_args(table, kv_len, pool, page, window, sinks)
     if cu_q.shape != (p.B + 1,):
         raise ValueError("cu_q must be [%d]" % (p.B + 1))
-    gca_paged_reserve(p, cu_q, kv_len, table, pool)
+    code = _lib.load().gca_paged_reserve(ctypes.byref(p), cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
+                                         pool.data_ptr(), _raw_stream(None, dev))
+    if code:
+        raise GcaError("gca_paged_reserve", code)
 
 
 def paged_fork(table, kv_len, parent, pool, *, page):
     """Every slot goes on from what slot parent[b] holds (b itself: unchanged; -1: empty), in
     place -> pairs [B, 2] of pages for paged_copy, which each cache (layer) needs before its next use."""
-    _same_device(pool, table, kv_len, parent)
+    dev = pool.get_device()
+    if dev < 0 or dev != _current_device() or table.get_device() != dev or kv_len.get_device() != dev or \
+            parent.get_device() != dev:
+        raise ValueError(_FOREIGN)
     _paged_ints(table, kv_len, parent, pool)
     p = _pages_args(table, kv_len, pool, page)
     if parent.shape != (p.B,):
         raise ValueError("parent must be [%d]" % p.B)
     pairs = pool.new_empty((p.B, 2))
-    gca_paged_fork(p, parent, kv_len, table, pool, pairs)
+    code = _lib.load().gca_paged_fork(ctypes.byref(p), parent.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
+                                      pool.data_ptr(), pairs.data_ptr(), _raw_stream(None, dev))
+    if code:
+        raise GcaError("gca_paged_fork", code)
     return pairs
 
 
 def paged_compact(table, pool, *, max_moves):
     """Move up to max_moves pages to the cache's front (table and counts, in place) -> pairs
     [max_moves, 2] of pages for paged_copy, which each cache (layer) needs before its next use."""
-    _same_device(pool, table)
+    dev = pool.get_device()
+    if dev < 0 or dev != _current_device() or table.get_device() != dev:
+        raise ValueError(_FOREIGN)
     _paged_ints(table, pool)
     p = _pages_args(table, None, pool, 16)                 # (a page's tokens do not matter)
     n = operator.index(max_moves)
     if not 1 <= n <= 1 << 24:
         raise ValueError("max_moves must be 1 .. 2^24")
     pairs = pool.new_empty((n, 2))
-    gca_paged_compact(p, n, table, pool, pairs)
+    code = _lib.load().gca_paged_compact(ctypes.byref(p), n, table.data_ptr(), pool.data_ptr(), pairs.data_ptr(),
+                                         _raw_stream(None, dev))
+    if code:
+        raise GcaError("gca_paged_compact", code)
     return pairs
 
 
 def paged_copy(k_cache, v_cache, pairs):
     """Copy pages of one cache, K and V in place: page pairs[i, 0] to page pairs[i, 1] (int32 [n, 2]
     on the device; negative: no copy)."""
-    _same_device(k_cache, v_cache, pairs)
+    dev = k_cache.get_device()
+    if dev < 0 or dev != _current_device() or v_cache.get_device() != dev or pairs.get_device() != dev:
+        raise ValueError(_FOREIGN)
     _paged_ints(pairs)
-    if pairs.dim() != 2 or pairs.shape[1] != 2:
+    ps, shape = pairs.shape, k_cache.shape
+    if len(ps) != 2 or ps[1] != 2:
         raise ValueError("pairs must be [n, 2]")
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or not (
-            k_cache.is_contiguous() and v_cache.is_contiguous()) or k_cache.dim() < 2:
+    if len(shape) < 2 or shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or not (
+            k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous, [n_pages, ...] and alike")
-    n_pages = k_cache.shape[0]
-    if n_pages > _INT_MAX or pairs.shape[0] > _INT_MAX:
+    n_pages = shape[0]
+    if n_pages > _INT_MAX or ps[0] > _INT_MAX:
         raise ValueError("too many pages")
-    gca_paged_copy(k_cache.numel() // max(n_pages, 1) * k_cache.element_size(), n_pages, pairs,
-                   pairs.shape[0], k_cache, v_cache)
+    code = _lib.load().gca_paged_copy(math.prod(shape[1:]) * k_cache.element_size(), n_pages, pairs.data_ptr(), ps[0],
+                                      k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(None, dev))
+    if code:
+        raise GcaError("gca_paged_copy", code)
 
 
 def gather_chunks(cache_k, cache_v, idx):
