@@ -551,8 +551,8 @@ gca_status_t gca_page_pool_init(int n_pages, int32_t* pool, void* stream);
  * A sequence that cannot be served keeps its entries and gets the length -1 - n for its n
  * tokens: the paged calls leave it out, and the next reservation takes it up again.  That
  * is one whose entries, with those of the sequences before it, are more than there are
- * free pages (GCA_ERR_NO_PAGES is recorded), or whose cu_q or length contradicts
- * itself or passes the table's end (GCA_ERR_DEVICE_INDEX).
+ * free pages (GCA_ERR_NO_PAGES), or whose cu_q or length contradicts itself or passes
+ * the table's end (GCA_ERR_DEVICE_INDEX); the first such sequence's code is recorded.
  */
 gca_status_t gca_paged_reserve(const gca_pages_params_t* params, const int32_t* cu_q,
                                int32_t* kv_len, int32_t* table, int32_t* pool, void* stream);

@@ -161,9 +161,11 @@ __global__ void __launch_bounds__(kThreads) paged_reserve_kernel(const PageArgs 
     __shared__ int end[kMaxSeqs];        // entries that the sequences up to this one lack
     __shared__ int few[kThreads];        // the free pages, where they are no more
     __shared__ int wsum[32];
+    __shared__ int failed;               // the first sequence that cannot be served, times 2, and 1 for want of pages
     // half a warp a sequence: 64 of them at once
     const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15, first = (threadIdx.x >> 5) * 2;
     constexpr int kStep = kThreads / 16;
+    if (threadIdx.x == 0) failed = 0x7fffffff;
     for (int b0 = first; b0 < a.B; b0 += kStep) {
         const int b = b0 + half;
         Reserve r{};
@@ -210,8 +212,7 @@ __global__ void __launch_bounds__(kThreads) paged_reserve_kernel(const PageArgs 
         const bool none = on && end[b] > from && end[b] > have;
         __syncwarp();                    // (every lane has read the length)
         if (on && hl == 0) {
-            if (r.bad) set_status(a.status, GCA_ERR_DEVICE_INDEX);
-            else if (none) set_status(a.status, GCA_ERR_NO_PAGES);
+            if (r.bad || none) atomicMin(&failed, 2 * b + (r.bad ? 0 : 1));
             kv_len[b] = r.bad || none ? ~r.old : r.old + r.add;
         }
         const int e1 = none ? r.e0 : r.e1;
@@ -227,6 +228,8 @@ __global__ void __launch_bounds__(kThreads) paged_reserve_kernel(const PageArgs 
             from += __popc(all);
         }
     }
+    __syncthreads();
+    if (threadIdx.x == 0 && failed != 0x7fffffff) set_status(a.status, failed & 1 ? GCA_ERR_NO_PAGES : GCA_ERR_DEVICE_INDEX);
 }
 
 // ---------------------------------------------------------------------------

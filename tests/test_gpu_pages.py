@@ -47,7 +47,8 @@ def ints(x):
 
 
 @pytest.mark.parametrize("B,width,n_pages,page,seed", [(1, 1, 1, 16, 0), (5, 8, 24, 16, 1), (40, 70, 1500, 16, 2), (7, 40, 100, 32, 3),
-                                                       (300, 9, 1300, 16, 4), (3, 300, 33, 128, 5), (64, 20, 2000, 64, 6)])
+                                                       (300, 9, 1300, 16, 4), (3, 300, 33, 128, 5), (64, 20, 2000, 64, 6),
+                                                       (70, 101, 4000, 16, 7), (4096, 1, 3000, 16, 8), (4096, 3, 9000, 16, 9)])
 def test_any_sequence_of_calls(B, width, n_pages, page, seed):
     r = random.Random(seed)
     m = Pages(B, width, n_pages, page)

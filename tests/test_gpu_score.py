@@ -57,6 +57,12 @@ def test_scores_far_beyond_the_cap(d):
     check(q, k, v, g, 300, 4, 2.0 ** -10)
 
 
+def test_a_scale_of_its_own():
+    q, k, v, g = inputs(2, 300, 4, 2, 64, seed=14)
+    check(q, k, v, g, 100, 4, 6.0, scale=0.4)
+    check(q, k, v, g, 100, 4, 0.0, slopes_of(4), scale=0.03)
+
+
 def test_infinite_products_count_as_the_cap():
     # (1e38 x 64 keys of 1e2 overflow fp32: the tanh of either is the same number)
     q, k, v, g = inputs(1, 300, 2, 2, 64, seed=8)
@@ -137,7 +143,10 @@ PAGED = [([1], [1], 1, 1, 64, 16, 0, 0), ([1], [777], 12, 12, 64, 64, 512, 4), (
          ([130, 1, 257], [130, 1000, 700], 4, 4, 64, 128, 0, 0), ([200], [900], 8, 1, 128, 64, 100, 16),
          ([33, 5], [33, 4000], 3, 1, 64, 64, 129, 33), ([1] * 20, list(range(1, 400, 20)), 8, 1, 64, 16, 0, 0),
          ([2, 1], [600, 601], 128, 1, 64, 32, 30, 1), ([1, 3, 1], [30000, 9000, 70], 4, 2, 128, 64, 0, 0),
-         ([5, 4], [3, 0], 2, 1, 64, 16, 0, 0)]
+         ([5, 4], [3, 0], 2, 1, 64, 16, 0, 0),
+         # units of eight rows and less: chunks of a few tokens, groups that do not divide eight
+         ([2, 4, 8, 3], [40, 700, 130, 129], 4, 4, 64, 16, 100, 3), ([2, 4, 1, 3], [600, 5, 257, 128], 4, 2, 128, 64, 0, 0),
+         ([2, 1, 2], [3000, 200, 131], 6, 2, 64, 32, 130, 40), ([1, 1], [500, 20], 5, 1, 128, 16, 33, 1)]
 
 
 @pytest.mark.parametrize("qs,kvs,H,Hkv,d,page,window,sinks", PAGED)
