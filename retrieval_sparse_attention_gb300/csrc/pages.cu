@@ -115,10 +115,11 @@ __device__ __forceinline__ void run_of(int n, int& i0, int& i1) {
 __device__ __forceinline__ int lowest_free(const PageArgs& a, int want, int* wsum, int* list) {
     int w0, w1, mine = 0, total;
     run_of(a.n_words, w0, w1);
-    for (int w = w0; w < w1; ++w) mine += __popc(free_word(a, w));
+    const uint32_t x0 = w0 < w1 ? free_word(a, w0) : 0;          // (up to 32768 pages a thread has no other)
+    for (int w = w0; w < w1; ++w) mine += __popc(w == w0 ? x0 : free_word(a, w));
     int r = block_scan(mine, wsum, total);
     for (int w = w0; w < w1 && r < want; ++w)
-        for (uint32_t x = free_word(a, w); x && r < want; x &= x - 1) list[r++] = 32 * w + __ffs(x) - 1;
+        for (uint32_t x = w == w0 ? x0 : free_word(a, w); x && r < want; x &= x - 1) list[r++] = 32 * w + __ffs(x) - 1;
     __syncthreads();
     return min(want, total);
 }
@@ -394,12 +395,14 @@ __global__ void __launch_bounds__(kThreads) paged_compact_plan_kernel(const Page
     if (!ALL) pdl_release();
     int w0, w1, mine = 0, free;
     run_of(a.n_words, w0, w1);
-    for (int w = w0; w < w1; ++w) mine += __popc(free_word(a, w));
+    const uint32_t x0 = w0 < w1 ? free_word(a, w0) : 0;          // (up to 32768 pages a thread has no other)
+    auto word = [&](int w) { return w == w0 ? x0 : free_word(a, w); };
+    for (int w = w0; w < w1; ++w) mine += __popc(word(w));
     block_scan(mine, wsum, free);
     const int used = a.n - free;
     // word w's free pages below `used`; its used ones from there on
-    auto holes = [&](int w) { return free_word(a, w) & below(used - 32 * w); };
-    auto high = [&](int w) { return ~free_word(a, w) & ~below(used - 32 * w) & below(a.n - 32 * w); };
+    auto holes = [&](int w) { return word(w) & below(used - 32 * w); };
+    auto high = [&](int w) { return ~word(w) & ~below(used - 32 * w) & below(a.n - 32 * w); };
     int2 mine2 = make_int2(0, 0), m;
     for (int w = w0; w < w1; ++w) mine2 = add(mine2, make_int2(__popc(holes(w)), __popc(high(w))));
     const int2 from = block_scan2(mine2, wsum2, m);
