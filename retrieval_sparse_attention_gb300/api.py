@@ -217,6 +217,8 @@ def _empty_like(t):
 
 
 def _dense(t, shape, dtype, what):
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
     if t is None:
         raise ValueError("%s is needed" % what)
     if t.dtype != dtype:
@@ -418,7 +420,8 @@ def gca_swa_sink_bwd_scored(params: GcaSwaSinkParams, score: GcaScore, q, k, v, 
 
 def _score(softcap, slopes, H, dev):
     """The transform of a call's scores, or None where it asks for none."""
-    softcap = float(softcap)
+    if type(softcap) is not float:
+        softcap = float(softcap)
     if slopes is None:
         return GcaScore(softcap, None) if softcap else None
     _dense(slopes, (H,), torch.float32, "slopes")
@@ -475,8 +478,8 @@ def swa_sink_fwd(q, k, v, *, window, sinks, attn_scale=0.0, with_lse=True, works
     may be those of a packed projection) -> (o [B, L, H, d], lse [B, L, H]).  ``softcap`` caps
     the scores by a tanh, ``slopes`` [H] fp32 lowers them by the distance (one of the two)."""
     index = _same_device(q, k, v, workspace)
-    score = _score(softcap, slopes, q.shape[-2], index)
     p, need, _, _ = _swa_sink_args(q, k, v, window, sinks, attn_scale)
+    score = _score(softcap, slopes, p.H, index)
     dev = q.device
     ws = _workspace(workspace, need, dev)
     o = _empty_like(q)
@@ -492,8 +495,8 @@ def swa_sink_bwd(q, k, v, o, lse, dout, *, window, sinks, attn_scale=0.0, worksp
                  softcap=0.0, slopes=None):
     """Gradients of swa_sink_fwd: returns dense (dq, dk, dv)."""
     index = _same_device(q, k, v, o, lse, dout, workspace)
-    score = _score(softcap, slopes, q.shape[-2], index)
     p, _, plain, scored = _swa_sink_args(q, k, v, window, sinks, attn_scale)
+    score = _score(softcap, slopes, p.H, index)
     _dense(o, q.shape, q.dtype, "o")
     _dense(dout, q.shape, q.dtype, "dout")
     _dense(lse, q.shape[:3], torch.float32, "lse")
@@ -602,8 +605,8 @@ def paged_attn(q, k_cache, v_cache, table, cu_q, kv_len, *, max_q=0, window=0, s
     saves work.  Rows of o behind cu_q[B] are left as they were (``out`` supplies o).  ``softcap``
     and ``slopes`` as in swa_sink_fwd."""
     index = _same_device(q, k_cache, v_cache, table, cu_q, kv_len, out, workspace)
-    score = _score(softcap, slopes, q.shape[-2], index)
     p, need = _paged_args(q, k_cache, v_cache, table, cu_q, kv_len, True, max_q, window, sinks, attn_scale)
+    score = _score(softcap, slopes, p.H, index)
     dev = q.device
     ws = _workspace(workspace, need, dev)
     if out is None:
