@@ -548,7 +548,7 @@ gca_status_t gca_page_pool_init(int n_pages, int32_t* pool, void* stream);
  *     they hold pages; a page that no entry holds any more is free, for this call too;
  *   - entries of the new tokens that hold no page get the lowest free ones, in the
  *     order of the sequences.
- * A sequence that cannot be served keeps its entries and gets the length -1 - n for its n
+ * A sequence that cannot be served gets no entries and the length -1 - n for its n
  * tokens: the paged calls leave it out, and the next reservation takes it up again.  That
  * is one whose entries, with those of the sequences before it, are more than there are
  * free pages (GCA_ERR_NO_PAGES), or whose cu_q or length contradicts itself or passes

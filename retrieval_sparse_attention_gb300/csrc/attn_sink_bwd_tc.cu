@@ -600,6 +600,18 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                         mbar_arrive(&sb.y_empty[ys]);
                         break;
                     }
+                    const uint32_t vis = (below(c_hi + 1 - 32 * pc) & ~below(c_lo - 32 * pc)) | below(c_s - 32 * pc);
+                    // (columns that no row of the warp sees: an eighth of the step's arithmetic at W = 512)
+                    if (EXACT && edge && !__any_sync(0xffffffffu, vis != 0u)) {
+                        if (pc == 1) {
+                            tc_fence_before();
+                            mbar_arrive(&sb.y_empty[ys]);
+                        }
+                        const uint32_t z[16] = {};
+                        tmem_st_32x32b_x16(xb + 32 * pc, z);
+                        tmem_st_32x32b_x16(xb + 32 * pc + 16, z);
+                        continue;
+                    }
                     // keys kbase + 32 pc .. + 31: S (X columns 32 pc ..) and dP (Y columns 32 pc ..)
                     uint32_t r0[16], r1[16], r2[16], r3[16];
                     tmem_ld_32x32b_x16(xb + 32 * pc, r0);
@@ -611,7 +623,6 @@ sink_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                         tc_fence_before();
                         mbar_arrive(&sb.y_empty[ys]);
                     }
-                    const uint32_t vis = (below(c_hi + 1 - 32 * pc) & ~below(c_lo - 32 * pc)) | below(c_s - 32 * pc);
                     uint32_t pk[16], pp[16];                      // ds, and exact: p (with a cap times r (1 - r))
                     if constexpr (SCORE == kScoreCap) {
                         cap_r16(r0, cap_in2);
