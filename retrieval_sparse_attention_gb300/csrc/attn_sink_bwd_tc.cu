@@ -1133,6 +1133,16 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
                         for (int cc = 0; cc < 2; ++cc) {
                             const int c = 2 * half + cc;
+                            const uint32_t vis = below(c_hi + 1 - 16 * c) & ~below(c_lo - 16 * c);
+                            if (SCORE != kScorePlain && msk && !__any_sync(0xffffffffu, (vis & 0xffffu) != 0u)) {
+                                if (cc == 1) {                       // (queries that no key of the warp meets)
+                                    tc_fence_before();
+                                    mbar_arrive(&sb.y_empty[ys]);
+                                }
+                                const uint32_t z[16] = {};
+                                tmem_st_32x32b_x16(xb + 16 * c, z);
+                                continue;
+                            }
                             uint32_t rs[16], rd[16];
                             tmem_ld_32x32b_x16(xb + 16 * c, rs);
                             tmem_ld_32x32b_x16(yb + 16 * c, rd);
@@ -1142,7 +1152,6 @@ sink_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                 mbar_arrive(&sb.y_empty[ys]);
                             }
                             if constexpr (SCORE == kScoreCap) cap_r16(rs, cap_in2);
-                            const uint32_t vis = below(c_hi + 1 - 16 * c) & ~below(c_lo - 16 * c);
                             uint32_t pd[8], pp[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
