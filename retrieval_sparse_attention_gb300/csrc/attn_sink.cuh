@@ -358,7 +358,10 @@ __device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity) {
 //         c that the entries take 2^-10, half the rounding of a probability to bf16.
 //   bias: x - slope_h (t - s), with slope_h log2(e) in log2 units.
 // ---------------------------------------------------------------------------
-enum ScoreKind { kScorePlain = 0, kScoreCap = 1, kScoreBias = 2 };
+// A cap bounds the scores: where 2 C leaves room in an exponent the forward takes weights against a fixed
+// maximum, with no running one to find and no sums to rescale (kScoreCapFixed; the gradients, which know
+// lse, make no difference).
+enum ScoreKind { kScorePlain = 0, kScoreCap = 1, kScoreBias = 2, kScoreCapFixed = 3 };
 
 __device__ __forceinline__ float fast_rcp(float x) {
     float y;

@@ -124,6 +124,7 @@ struct FwdArgs {
     float scale_log2;
     const float* slopes;     // [H], of a distance bias
     float cap_in, cap_log2;  // 2 scale log2(e) / c and c log2(e), of a cap c
+    float cap_max;           // the fixed maximum, in log2 units
 };
 
 // One worker's part of a unit: key tiles j0 .. j1 - 1 (j0 == j1: the share is done).
@@ -595,7 +596,9 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // A score in log2 units is v sl + so, v being what the tile's registers hold: the product, or with a
         // cap its r (attn_sink.cuh: falling in the score, so its least is the greatest score); a bias comes
         // on top of that.  A column that a row does not see holds kHidden.
-        constexpr bool CAP = SCORE == kScoreCap, BIAS = SCORE == kScoreBias, FEW = CAP && PAGED;
+        constexpr bool FIXED = SCORE == kScoreCapFixed, CAP = SCORE == kScoreCap || FIXED, BIAS = SCORE == kScoreBias;
+        constexpr bool FEW = CAP && PAGED;
+        const float m_first = FIXED ? a.cap_max : -INFINITY;     // a running maximum's first value
         constexpr float kHidden = CAP ? INFINITY : -INFINITY;
         const float sl = CAP ? -2.f * a.cap_log2 : a.scale_log2, so = CAP ? a.cap_log2 : 0.f;
         const uint64_t cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
@@ -616,7 +619,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         bool first = true;                              // at the first tile of a part
         bool have = true, live = false, wlive = false;  // a tile to do; this row exists; some row of the warp does
         bool few = false;                               // no more than eight rows exist
-        float m = -INFINITY, l = 0.f;                   // running max (of s * scale * log2(e)) and sum of exp2(. - m)
+        float m = m_first, l = 0.f;                     // running max (of s * scale * log2(e)) and sum of exp2(. - m)
         // the finished part whose O still sits in tensor memory
         bool pend = false;
         int pend_row = -1;                              // token * H + head, or -1: no such row
@@ -684,6 +687,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             // the running maximum follows a tile's (in log2 units) only past a margin
             auto follow = [&](float mts) {
                 alpha = 1.f;
+                if (FIXED) return;
                 if (mts > m + kRescaleLog2) {
                     if (m != -INFINITY) alpha = fast_exp2(m - mts);
                     m = mts;
@@ -691,7 +695,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             };
             // once the previous tile's P V has completed, O is stable and can be rescaled
             auto rescale = [&]() {
-                if (__all_sync(0xffffffffu, alpha == 1.f)) return;
+                if (FIXED || __all_sync(0xffffffffu, alpha == 1.f)) return;
                 tc_fence_after();
 #pragma unroll 1
                 for (int ci = 0; ci < D / 16; ++ci) {
@@ -746,14 +750,16 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     for (int u = 0; u < 4; ++u) x[i + u] = y[u];
                 }
                 if (!whole) hide(kHidden);
-                float mt = x[0];
-#pragma unroll
-                for (int i = 1; i < 32; ++i) mt = greater(mt, x[i]);
-                mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-                mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
                 const float m_row = m;
-                m = __shfl_sync(0xffffffffu, m_row, fr);
-                follow(log2_of(mt));
+                if constexpr (!FIXED) {
+                    float mt = x[0];
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) mt = greater(mt, x[i]);
+                    mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+                    mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+                    m = __shfl_sync(0xffffffffu, m_row, fr);
+                    follow(log2_of(mt));
+                }
                 const float mu = m == -INFINITY ? 0.f : m, nmu = less(mu);
                 float sum[2] = {0.f, 0.f};
                 uint32_t pk[32];
@@ -770,10 +776,12 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 add += __shfl_xor_sync(0xffffffffu, add, 2);
                 // back to a row a lane
                 const int from = 4 * (lane & 7);
-                const float m_new = __shfl_sync(0xffffffffu, m, from), al = __shfl_sync(0xffffffffu, alpha, from);
                 add = __shfl_sync(0xffffffffu, add, from);
-                m = live ? m_new : m_row;
-                alpha = live ? al : 1.f;
+                if constexpr (!FIXED) {
+                    const float m_new = __shfl_sync(0xffffffffu, m, from), al = __shfl_sync(0xffffffffu, alpha, from);
+                    m = live ? m_new : m_row;
+                    alpha = live ? al : 1.f;
+                }
                 l = live ? l * alpha + add : 0.f;
                 if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
                 rescale();
@@ -809,7 +817,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         m4[i & 3] = fmaxf(m4[i & 3], fmaxf(y0, y1));
                     }
                     follow(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                } else {
+                } else if constexpr (!FIXED) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) m4[i & 3] = greater(m4[i & 3], __uint_as_float(r[i]));
                     follow(log2_of(greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]))));
@@ -898,7 +906,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) x[i + u] = y[u];
                             }
-                            mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));    // r of the greatest product
+                            if (!FIXED) mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));    // r of the greatest product
                         }
                         if (!whole) hide(kHidden);
                         if constexpr (BIAS) {
@@ -935,7 +943,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                 }
                             }
                             follow(mt);
-                        } else {
+                        } else if constexpr (!FIXED) {
                             // the maximum over all columns bounds that over the visible ones: only where it
                             // would move the running one (or is no number) is the latter needed
                             if (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2))) {
@@ -1017,7 +1025,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 pm = m;
                 // (a row that sees keys has a sum above 0, or scores that are no numbers or all -inf: NaN then)
                 pl = l == 0.f && w.slot < 0 && w.p0 + rt >= 0 ? NAN : l;
-                m = -INFINITY;
+                m = m_first;
                 l = 0.f;
             }
         }
@@ -1204,6 +1212,9 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     if (s.softcap > 0.f) {
         a.cap_in = 2.f * a.scale_log2 / s.softcap;
         a.cap_log2 = s.softcap * kLog2e;
+        // weights from 2^-110 (or 2^-2C) to 2^40 at most: none is lost, and sums of 2^20 values up to 2^60
+        // are finite
+        a.cap_max = a.cap_log2 - fmaxf(2.f * a.cap_log2 - 110.f, 0.f);
     }
     a.whole = whole_units(s);
     CUtensorMap tq, tk, tv;
@@ -1218,6 +1229,7 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
                             : encode_bf16_3d(m, p, kvcols, s.L, s.B, s.kv_stride, (uint64_t)s.kv_stride * s.L, 128, 1, s.d == 128));
     }
     if (!ok) return cudaErrorInvalidValue;
+    if (s.softcap > 0.f && a.cap_log2 <= 75.f) return launch_shape<kScoreCapFixed>(s, a, tq, tk, tv, st, launches);
     if (s.softcap > 0.f) return launch_shape<kScoreCap>(s, a, tq, tk, tv, st, launches);
     if (s.slopes) return launch_shape<kScoreBias>(s, a, tq, tk, tv, st, launches);
     return launch_shape<kScorePlain>(s, a, tq, tk, tv, st, launches);
