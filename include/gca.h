@@ -343,7 +343,7 @@ gca_status_t gca_swa_sink_bwd(const gca_swa_sink_params_t* params, const void* q
  * capped by a tanh or lowered by the distance before the softmax.  With
  * x = attn_scale q_t . k_s, the softmax is over
  *   softcap > 0:  softcap tanh(x / softcap), which keeps every score within +-softcap
- *                 (a product of +-inf counts as +-softcap);
+ *                 (a product of +-inf counts as +-softcap); V within +-2^36;
  *   slopes:       x - slopes[h] (t - s) for query head h at distance t - s >= 0.
  * Masks, lse, layouts and everything else are those of the plain calls, the forwards'
  * workspaces too.  The gradients pass through the transform (the slopes are constants);

@@ -41,8 +41,9 @@
 //   (1.37 PFLOP/s, 69%); 32 tokens over caches of 4-33K, 24/8 heads of 128: 0.326 to
 //   0.337 ms in a loop, 0.343 to 0.353 with a cold L2 (6.3-6.5 TB/s, 95-97%); a token
 //   each of 64 requests, 12 heads of 64, W = 512: 38 us in a graph; one over 777: 12 us.
-// Transformed scores (attn_sink.cuh): the first shape with a cap and 4 sinks 0.60 ms (XU 44% busy, issue slots
-// 55%: twice the instructions a score, on the same two warps a sub-partition); the 32 tokens with a cap 0.344 to
+// Transformed scores (attn_sink.cuh): the first shape with a cap and 4 sinks 0.52 ms (0.60 with a running
+// maximum, of which the XU is 44% busy and the issue slots 55%: twice the instructions a score, on the same
+// two warps a sub-partition); the 32 tokens with a cap 0.344 to
 // 0.355 ms, as without; a serving batch of 48, 12 heads of 64, W = 512: 49 us, with a bias 52.
 // What bounds it.  Single tokens over long caches: the cache's bytes.  d = 128 with
 // many rows: the chain S -> softmax -> P V of each worker, ~3,200 cycles a pair of
@@ -1212,9 +1213,9 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     if (s.softcap > 0.f) {
         a.cap_in = 2.f * a.scale_log2 / s.softcap;
         a.cap_log2 = s.softcap * kLog2e;
-        // weights from 2^-110 (or 2^-2C) to 2^40 at most: none is lost, and sums of 2^20 values up to 2^60
-        // are finite
-        a.cap_max = a.cap_log2 - fmaxf(2.f * a.cap_log2 - 110.f, 0.f);
+        // weights from 2^-80 (or 2^-2C) on, up to 2^70 at most (C = 75): products with values from 2^-46 on are
+        // normal numbers, and sums of 2^20 values up to 2^36 are finite
+        a.cap_max = a.cap_log2 - fmaxf(2.f * a.cap_log2 - 80.f, 0.f);
     }
     a.whole = whole_units(s);
     CUtensorMap tq, tk, tv;

@@ -57,6 +57,30 @@ def test_scores_far_beyond_the_cap(d):
     check(q, k, v, g, 300, 4, 2.0 ** -10)
 
 
+@pytest.mark.parametrize("cap", [30.0, 51.9, 52.1])
+def test_scores_at_either_cap(cap):
+    # rows whose scores all lie near -cap, and near +cap, with small and large values: on either side of
+    # the largest cap that is taken against a fixed maximum (51.98)
+    g = torch.Generator().manual_seed(17)
+    L, d = 300, 64
+    u = torch.sign(torch.randn(1, 1, 1, d, generator=g))
+    k = (u * 2 + 0.1 * torch.randn(1, L, 1, d, generator=g)).to(torch.bfloat16)
+    q = torch.cat([-8 * u.expand(1, L, 1, d), 8 * u.expand(1, L, 1, d)], 2)
+    q = (q + 0.1 * torch.randn(1, L, 2, d, generator=g)).to(torch.bfloat16)
+    v = torch.randn(1, L, 1, d, generator=g)
+    v[..., :20] *= 2.0 ** -40
+    v[..., 20:40] *= 2.0 ** 33
+    v = v.to(torch.bfloat16)
+    dout = torch.randn(1, L, 2, d, generator=g).to(torch.bfloat16)
+    kw = dict(window=120, sinks=3, softcap=cap)
+    o, lse = api.swa_sink_fwd(q.cuda(), k.cuda(), v.cuda(), **kw)
+    ro, rl, bo, bl = ref.forward(q, k, v, 120, 3, cap)
+    ref.within("o", o, ro, bo)
+    ref.within("lse", lse, rl, bl)
+    assert lse[0, :, 0].max() < -0.6 * cap and lse[0, :, 1].min() > 0.6 * cap
+    check(q, k, v.clamp(-4, 4), dout, 120, 3, cap)
+
+
 def test_a_scale_of_its_own():
     q, k, v, g = inputs(2, 300, 4, 2, 64, seed=14)
     check(q, k, v, g, 100, 4, 6.0, scale=0.4)
