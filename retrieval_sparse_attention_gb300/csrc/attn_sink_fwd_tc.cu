@@ -41,7 +41,7 @@
 //   (1.37 PFLOP/s, 69%); 32 tokens over caches of 4-33K, 24/8 heads of 128: 0.326 to
 //   0.337 ms in a loop, 0.343 to 0.353 with a cold L2 (6.3-6.5 TB/s, 95-97%); a token
 //   each of 64 requests, 12 heads of 64, W = 512: 38 us in a graph; one over 777: 12 us.
-// Transformed scores (attn_sink.cuh): the first shape with a cap and 4 sinks 0.52 ms (0.60 with a running
+// Transformed scores (attn_sink.cuh): the first shape with a cap and 4 sinks 0.56 ms (0.60 with a running
 // maximum, of which the XU is 44% busy and the issue slots 55%: twice the instructions a score, on the same
 // two warps a sub-partition); the 32 tokens with a cap 0.344 to
 // 0.355 ms, as without; a serving batch of 48, 12 heads of 64, W = 512: 49 us, with a bias 52.
@@ -125,7 +125,7 @@ struct FwdArgs {
     float scale_log2;
     const float* slopes;     // [H], of a distance bias
     float cap_in, cap_log2;  // 2 scale log2(e) / c and c log2(e), of a cap c
-    float cap_max;           // the fixed maximum, in log2 units
+    float cap_lo, cap_hi;    // limits of a row's fixed maximum, in log2 units
 };
 
 // One worker's part of a unit: key tiles j0 .. j1 - 1 (j0 == j1: the share is done).
@@ -599,7 +599,6 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // on top of that.  A column that a row does not see holds kHidden.
         constexpr bool FIXED = SCORE == kScoreCapFixed, CAP = SCORE == kScoreCap || FIXED, BIAS = SCORE == kScoreBias;
         constexpr bool FEW = CAP && PAGED;
-        const float m_first = FIXED ? a.cap_max : -INFINITY;     // a running maximum's first value
         constexpr float kHidden = CAP ? INFINITY : -INFINITY;
         const float sl = CAP ? -2.f * a.cap_log2 : a.scale_log2, so = CAP ? a.cap_log2 : 0.f;
         const uint64_t cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
@@ -620,7 +619,8 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         bool first = true;                              // at the first tile of a part
         bool have = true, live = false, wlive = false;  // a tile to do; this row exists; some row of the warp does
         bool few = false;                               // no more than eight rows exist
-        float m = m_first, l = 0.f;                     // running max (of s * scale * log2(e)) and sum of exp2(. - m)
+        bool fresh = true;                              // at a part's first tile
+        float m = -INFINITY, l = 0.f;                   // running max (of s * scale * log2(e)) and sum of exp2(. - m)
         // the finished part whose O still sits in tensor memory
         bool pend = false;
         int pend_row = -1;                              // token * H + head, or -1: no such row
@@ -637,6 +637,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 f1 = sb.part[wg][r].f1;
                 fl = sb.part[wg][r].fl;
                 have = j < j1;
+                fresh = true;
                 // rows that do not exist are skipped, where a whole warp has no other
                 live = have && row < a.R && rt < sb.part[wg][r].ntok;
                 wlive = __any_sync(0xffffffffu, live);
@@ -686,9 +687,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (BIAS) slope = slope_in * kLog2e;
             float alpha = 1.f;
             // the running maximum follows a tile's (in log2 units) only past a margin
+            // (FIXED: the part's first tile sets it, within limits that leave room for every score)
             auto follow = [&](float mts) {
                 alpha = 1.f;
-                if (FIXED) return;
+                if (FIXED) {
+                    m = fminf(fmaxf(mts, a.cap_lo), a.cap_hi);
+                    return;
+                }
                 if (mts > m + kRescaleLog2) {
                     if (m != -INFINITY) alpha = fast_exp2(m - mts);
                     m = mts;
@@ -752,13 +757,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 }
                 if (!whole) hide(kHidden);
                 const float m_row = m;
-                if constexpr (!FIXED) {
+                m = __shfl_sync(0xffffffffu, m_row, fr);
+                if (!FIXED || fresh) {
                     float mt = x[0];
 #pragma unroll
                     for (int i = 1; i < 32; ++i) mt = greater(mt, x[i]);
                     mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
                     mt = greater(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-                    m = __shfl_sync(0xffffffffu, m_row, fr);
                     follow(log2_of(mt));
                 }
                 const float mu = m == -INFINITY ? 0.f : m, nmu = less(mu);
@@ -778,11 +783,9 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 // back to a row a lane
                 const int from = 4 * (lane & 7);
                 add = __shfl_sync(0xffffffffu, add, from);
-                if constexpr (!FIXED) {
-                    const float m_new = __shfl_sync(0xffffffffu, m, from), al = __shfl_sync(0xffffffffu, alpha, from);
-                    m = live ? m_new : m_row;
-                    alpha = live ? al : 1.f;
-                }
+                const float m_new = __shfl_sync(0xffffffffu, m, from), al = __shfl_sync(0xffffffffu, alpha, from);
+                m = live ? m_new : m_row;
+                alpha = live ? al : 1.f;
                 l = live ? l * alpha + add : 0.f;
                 if (!C::P_OVER_S && !wwait(&sb.p_empty[wg], empty_par(ts))) break;
                 rescale();
@@ -818,7 +821,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         m4[i & 3] = fmaxf(m4[i & 3], fmaxf(y0, y1));
                     }
                     follow(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                } else if constexpr (!FIXED) {
+                } else {                                // (always a part's first)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) m4[i & 3] = greater(m4[i & 3], __uint_as_float(r[i]));
                     follow(log2_of(greater(greater(m4[0], m4[1]), greater(m4[2], m4[3]))));
@@ -907,7 +910,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) x[i + u] = y[u];
                             }
-                            if (!FIXED) mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));    // r of the greatest product
+                            if (!FIXED || fresh) mt = fast_rcp(1.f + fast_exp2(mt * a.cap_in));   // r of the greatest product
                         }
                         if (!whole) hide(kHidden);
                         if constexpr (BIAS) {
@@ -944,7 +947,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                 }
                             }
                             follow(mt);
-                        } else if constexpr (!FIXED) {
+                        } else if (!FIXED || fresh) {
                             // the maximum over all columns bounds that over the visible ones: only where it
                             // would move the running one (or is no number) is the latter needed
                             if (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2))) {
@@ -1015,6 +1018,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
             tc_fence_before();
             mbar_arrive(&sb.p_full[wg]);
+            fresh = false;
             ++ts;
             first = ++j == j1;
             if (first) {                                // this part of the unit is done: it leaves later
@@ -1026,7 +1030,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 pm = m;
                 // (a row that sees keys has a sum above 0, or scores that are no numbers or all -inf: NaN then)
                 pl = l == 0.f && w.slot < 0 && w.p0 + rt >= 0 ? NAN : l;
-                m = m_first;
+                m = -INFINITY;
                 l = 0.f;
             }
         }
@@ -1213,9 +1217,10 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
     if (s.softcap > 0.f) {
         a.cap_in = 2.f * a.scale_log2 / s.softcap;
         a.cap_log2 = s.softcap * kLog2e;
-        // weights from 2^-80 (or 2^-2C) on, up to 2^70 at most (C = 75): products with values from 2^-46 on are
+        // weights from 2^-100 to 2^70 whatever the scores: none is lost, products with values from 2^-26 on are
         // normal numbers, and sums of 2^20 values up to 2^36 are finite
-        a.cap_max = a.cap_log2 - fmaxf(2.f * a.cap_log2 - 80.f, 0.f);
+        a.cap_lo = a.cap_log2 - 70.f;
+        a.cap_hi = 100.f - a.cap_log2;
     }
     a.whole = whole_units(s);
     CUtensorMap tq, tk, tv;
