@@ -360,7 +360,8 @@ __device__ __forceinline__ bool wait_ctrl(uint64_t* bar, uint32_t parity) {
 // ---------------------------------------------------------------------------
 // A cap bounds the scores: where 2 C leaves room in an exponent the forward takes a row's weights against
 // the maximum of its first tile, with no running one to follow and no sums to rescale (kScoreCapFixed; the
-// gradients, which know lse, make no difference).  (Against one number for all rows it takes 0.52 ms in
+// gradients, which know lse, make no difference; a token a sequence, which costs the cache's bytes,
+// follows its maximum).  (Against one number for all rows it takes 0.52 ms in
 // place of 0.56 at 8 x 16K, but the greatest weight of a row is then no power of two: its rounding makes
 // 2.4e-3 of 1.7e-3 where a row has few keys, and of one key's value something else.)
 enum ScoreKind { kScorePlain = 0, kScoreCap = 1, kScoreBias = 2, kScoreCapFixed = 3 };

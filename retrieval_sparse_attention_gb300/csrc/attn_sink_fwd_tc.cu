@@ -602,6 +602,12 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         constexpr float kHidden = CAP ? INFINITY : -INFINITY;
         const float sl = CAP ? -2.f * a.cap_log2 : a.scale_log2, so = CAP ? a.cap_log2 : 0.f;
         const uint64_t cap_in2 = tcx::f2_pack(a.cap_in, a.cap_in);
+        // A token a sequence: the maximum is followed closely, which makes a row's greatest weight 1.  Else its
+        // rounding to bf16, which a row that few keys rule does not average out, adds to the output's (calls with
+        // a bias: 1.33 times the output's rounding on average and 1.49 at most, so 1.18 and 1.40).  The cache's
+        // bytes bound such calls: a serving batch of 48 takes 56 us either way.
+        const bool close = PAGED && SCORE != kScorePlain && sc.TM == 1;
+        const float margin = close ? 0.f : kRescaleLog2;
         float slope_in = 0.f;                           // of this row's head, as loaded (its wait is at its use)
         float slope = 0.f;                              // in log2 units
         auto greater = [](float x, float y) { return CAP ? fminf(x, y) : fmaxf(x, y); };
@@ -694,7 +700,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     m = fminf(fmaxf(mts, a.cap_lo), a.cap_hi);
                     return;
                 }
-                if (mts > m + kRescaleLog2) {
+                if (mts > m + margin) {
                     if (m != -INFINITY) alpha = fast_exp2(m - mts);
                     m = mts;
                 }
@@ -875,7 +881,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             }
                             // the maximum over all columns bounds that over the visible ones: only where it
                             // would move the running one (or is no number) is the latter needed
-                            if (__any_sync(0xffffffffu, !(mt * sl <= m + kRescaleLog2))) {
+                            if (__any_sync(0xffffffffu, !(mt * sl <= m + margin))) {
                                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                                 for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
@@ -919,13 +925,13 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             // running maximum it takes its place, unless it may lie more than 2^60 above the
                             // true one (sums would be too small): in tiles with hidden columns their
                             // products are left out first, and a bias so steep within 64 columns
-                            // takes the scores themselves.
+                            // takes the scores themselves (as does a maximum that is followed closely).
                             off = slope * static_cast<float>(kbase - p);
                             const float top0 = slope > 0.f ? fmaf(63.f, slope, off) : off;
                             const float top1 = slope > 0.f ? fminf(fmaf(127.f, slope, off), 0.f) : fmaf(64.f, slope, off);
                             auto bound = [&]() { return fmaxf(fmaf(mc[0], sl, top0), fmaf(mc[1], sl, top1)); };
                             mt = bound();
-                            if (!whole && __any_sync(0xffffffffu, !(mt <= m + kRescaleLog2))) {
+                            if (!whole && __any_sync(0xffffffffu, !(mt <= m + margin))) {
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -935,7 +941,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                 }
                                 mt = bound();
                             }
-                            if (__any_sync(0xffffffffu, fabsf(slope) * 63.f > 60.f && !(mt <= m + kRescaleLog2))) {
+                            if (__any_sync(0xffffffffu, (close || fabsf(slope) * 63.f > 60.f) && !(mt <= m + margin))) {
                                 mt = -INFINITY;
                                 uint64_t tb = 0;
 #pragma unroll
@@ -950,7 +956,7 @@ sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         } else if (!FIXED || fresh) {
                             // the maximum over all columns bounds that over the visible ones: only where it
                             // would move the running one (or is no number) is the latter needed
-                            if (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + kRescaleLog2))) {
+                            if (!whole && __any_sync(0xffffffffu, !(log2_of(mt) <= m + margin))) {
                                 float m4[4] = {kHidden, kHidden, kHidden, kHidden};
 #pragma unroll
                                 for (int i = 0; i < 128; ++i) m4[i & 3] = greater(m4[i & 3], x[i]);
@@ -1235,7 +1241,7 @@ cudaError_t launch_sink_fwd(const SinkShape& s, const void* q, const void* k, co
                             : encode_bf16_3d(m, p, kvcols, s.L, s.B, s.kv_stride, (uint64_t)s.kv_stride * s.L, 128, 1, s.d == 128));
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (s.softcap > 0.f && a.cap_log2 <= 75.f) return launch_shape<kScoreCapFixed>(s, a, tq, tk, tv, st, launches);
+    if (s.softcap > 0.f && a.cap_log2 <= 75.f && a.s.TM > 1) return launch_shape<kScoreCapFixed>(s, a, tq, tk, tv, st, launches);
     if (s.softcap > 0.f) return launch_shape<kScoreCap>(s, a, tq, tk, tv, st, launches);
     if (s.slopes) return launch_shape<kScoreBias>(s, a, tq, tk, tv, st, launches);
     return launch_shape<kScorePlain>(s, a, tq, tk, tv, st, launches);
